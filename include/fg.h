@@ -347,9 +347,124 @@ fg_status fg_decode_block_step_graphed(fg_graph_cache* cache, const fg_layer* la
                                        int64_t b, int64_t pos, const fg_kv* kvs, void* y, void* ws,
                                        size_t ws_bytes, cudaStream_t stream);
 
+/* ---- paged 4-bit cache ------------------------------------------------------
+ * [BG] Concat and [S5] KV in 4-bit groups along the hidden dimension, for
+ * sequences of different lengths that grow, fork and end at different times
+ * (the notes' block has one length for all).  A cache is a pool of pages per
+ * layer and one page table for all layers.
+ *
+ * fg_page_pool: K and V of one layer, 4-bit groups only, page by page:
+ *   {k,v}_codes uint8 [pages][heads][page_size][head_dim/2],
+ *   {k,v}_mins, {k,v}_scales fp32 [pages][heads][page_size][head_dim/64],
+ * all 16-byte aligned.  page_size (tokens) is 16, 32, 64, 128 or 256,
+ * head_dim 64 or 128; `heads` are the K/V heads; dtype is the activations'. */
+typedef struct {
+  uint8_t* k_codes;
+  uint8_t* v_codes;
+  float* k_mins;
+  float* k_scales;
+  float* v_mins;
+  float* v_scales;
+  int64_t pages;
+  int32_t page_size, heads, head_dim;
+  fg_dtype dtype;
+} fg_page_pool;
+
+/* The page table, device memory owned by the caller: row i of `table`
+ * [seqs][stride] lists the pages of sequence i, entry j holding its tokens
+ * j*page_size .. ; lens [seqs] are the tokens of each sequence; refs [pages]
+ * counts the rows' entries that name a page (0: the page is free).  Entries
+ * past ceil(lens[i]/page_size) mean nothing.  A new table has lens and refs 0.
+ * stride * page_size is at most 2^30. */
+typedef struct {
+  int32_t* table;
+  int32_t* lens;
+  int32_t* refs;
+  int64_t seqs, stride, pages;
+  int32_t page_size;
+} fg_page_table;
+
+/* The paged calls read lengths, tables and lists on the device, so a step can
+ * be captured into a graph.  What only the device can see wrong is never
+ * followed out of a buffer: the entry is left out, the rest of the call is
+ * done, and fg_sync_status reports FG_ERR_CAPACITY (no free page, a table row
+ * too short, or a needed page missing) or FG_ERR_ARG (offsets, lengths or list
+ * entries out of range).
+ * A batch is ragged: `cu` (device int32 [seqs+1], not decreasing, within 0 ..
+ * ntok) gives each sequence of the table its rows cu[i] .. cu[i+1]-1 of the
+ * packed activations, none for a sequence that takes no part.  lens counts
+ * those tokens already: row t of n stands at position lens[i] - n + t.
+ * Calls that touch one table or workspace run in stream order; two calls at
+ * once need workspaces of their own. */
+
+/* Grow every sequence by its rows of `cu` (the values alone matter, not where
+ * they start): lens[i] += n, and entries of the row are filled with free pages,
+ * lowest numbered first, sequence by sequence.  A page that cannot be had is
+ * entered as -1 (its tokens are then not stored, see fg_paged_append), and the
+ * length grows all the same.  The last, partly filled page of a growing
+ * sequence must be its own (refs 1), as fg_pages_fork leaves it. */
+size_t fg_pages_workspace_bytes(const fg_page_table* t, int64_t n);   /* n: forks in a call, or 0 */
+fg_status fg_pages_reserve(const fg_page_table* t, const int32_t* cu, void* ws, size_t ws_bytes,
+                           cudaStream_t stream);
+
+/* Sequences dst[k] become copies of src[k] (device int32 [n]): full pages are
+ * shared (refs + 1), a partly filled last page is copied, in all l pools, into
+ * a free page, lowest numbered first, fork by fork.  dst rows must be empty
+ * (lens 0) and named once (the first of two counts); several forks may share a
+ * source.  A fork that cannot be made leaves dst as it was. */
+fg_status fg_pages_fork(const fg_page_table* t, const fg_page_pool* pools, int32_t l, const int32_t* src,
+                        const int32_t* dst, int64_t n, void* ws, size_t ws_bytes, cudaStream_t stream);
+
+/* End the sequences rows[0..n-1] (device int32): refs of their pages - 1,
+ * their entries -1, their lengths 0.  An empty row is left as it is, so a row
+ * may be named twice. */
+fg_status fg_pages_free(const fg_page_table* t, const int32_t* rows, int64_t n, cudaStream_t stream);
+
+/* Move the pages in use to the front of the pools: with m pages in use, those
+ * numbered m and above go, in ascending order, into the free pages below m, in
+ * ascending order; the others stay.  The data of all l pools, the entries of
+ * every row and refs follow.  Pages m .. pages-1 are free afterwards. */
+fg_status fg_pages_compact(const fg_page_table* t, const fg_page_pool* pools, int32_t l, void* ws,
+                           size_t ws_bytes, cudaStream_t stream);
+
+/* [BG] Concat into pages: quantize the rows of a ragged batch (k, v: device
+ * [ntok][ld], pool dtype, head h at columns h*head_dim; ld a multiple of 8,
+ * 16-byte aligned) into their positions' slots, with the fg_quantize_g64
+ * arithmetic.  k_restored, v_restored (both or neither; device [ntok][ldr])
+ * receive the rows as the cache restores them, fmaf(q, scale, min) rounded to
+ * the activations' type; they may be k and v themselves.  Rows without a slot
+ * are not stored and their restored rows are left as they are, as are rows
+ * outside cu[0] .. cu[seqs]. */
+fg_status fg_paged_append(const fg_page_pool* pool, const fg_page_table* t, const int32_t* cu, const void* k,
+                          const void* v, int64_t ld, int64_t ntok, void* k_restored, void* v_restored,
+                          int64_t ldr, cudaStream_t stream);
+
+/* [BG] causal attention of the rows of a ragged batch over the pages:
+ * q: device [ntok][ldq], q_heads heads of head_dim (a multiple of the pool's
+ * heads; query head h reads K/V head h / (q_heads / heads)); out: device
+ * [ntok][ldo], same columns; ldq, ldo multiples of 8, 16-byte aligned.  The
+ * row at position p sees the tokens j <= p with j > p - window or j < sinks
+ * (window 0: all j <= p).  Scores are scaled by 1/sqrt(head_dim); a row that
+ * sees nothing gives 0.  Attention reads the values the codes stand for:
+ * sequences of at most 16 rows per K/V head (rows times query heads per K/V
+ * head: decode steps) use them unrounded; longer chunks of fp16 round them to
+ * fp16, the tensor cores' operand; fp32 computes in fp32.  A group whose scale
+ * is not finite makes that group's columns NaN for the rows that see it, and
+ * for no other.  A missing page's tokens are not seen.
+ * max_q bounds the rows of one sequence; longer ones are refused on the device.
+ * Rows outside cu[0] .. cu[seqs] are left as they are.  ws: device, 256-byte
+ * aligned, >= fg_paged_attention_workspace_bytes. */
+size_t fg_paged_attention_workspace_bytes(const fg_page_pool* pool, const fg_page_table* t, int32_t q_heads,
+                                          int64_t ntok, int64_t max_q);
+fg_status fg_paged_attention(const fg_page_pool* pool, const fg_page_table* t, const int32_t* cu, const void* q,
+                             int64_t ldq, int32_t q_heads, int64_t ntok, int64_t max_q, int64_t window,
+                             int64_t sinks, void* out, int64_t ldo, void* ws, size_t ws_bytes,
+                             cudaStream_t stream);
+
 /* Synchronize `stream`, then report (and clear) the device error word that
- * kernels raise when a bounded wait runs out: FG_ERR_DEVICE_TIMEOUT, or
- * FG_ERR_CUDA if the synchronization itself failed. */
+ * kernels raise: FG_ERR_DEVICE_TIMEOUT when a bounded wait ran out, else
+ * FG_ERR_ARG or FG_ERR_CAPACITY for what a paged call found wrong on the
+ * device (above), or FG_ERR_CUDA if the synchronization itself failed. */
 #define FG_WAIT_LIMIT_DEFAULT (1u << 24)
 
 /* Failure handling: the number of polls every bounded wait of the library's

@@ -545,3 +545,233 @@ def topk_keep(tokens: int, percent: int = 10) -> int:
     """The page's sparse setting: the top `percent` per cent of the tokens,
     rounded up, at least one."""
     return max(1, (int(tokens) * int(percent) + 99) // 100)
+
+
+# ---- paged 4-bit cache -----------------------------------------------------------
+
+class fg_page_pool(ctypes.Structure):
+    _fields_ = [("k_codes", ctypes.c_void_p), ("v_codes", ctypes.c_void_p),
+                ("k_mins", ctypes.c_void_p), ("k_scales", ctypes.c_void_p),
+                ("v_mins", ctypes.c_void_p), ("v_scales", ctypes.c_void_p),
+                ("pages", ctypes.c_int64), ("page_size", ctypes.c_int32), ("heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("dtype", ctypes.c_int)]
+
+
+class fg_page_table(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("lens", ctypes.c_void_p), ("refs", ctypes.c_void_p),
+                ("seqs", ctypes.c_int64), ("stride", ctypes.c_int64), ("pages", ctypes.c_int64),
+                ("page_size", ctypes.c_int32)]
+
+
+_POOL = ctypes.POINTER(fg_page_pool)
+_TAB = ctypes.POINTER(fg_page_table)
+_I32 = ctypes.c_int32
+_sig("fg_pages_workspace_bytes", _SZ, _TAB, _I64)
+_sig("fg_pages_reserve", _INT, _TAB, _P, _P, _SZ, _P)
+_sig("fg_pages_fork", _INT, _TAB, _POOL, _I32, _P, _P, _I64, _P, _SZ, _P)
+_sig("fg_pages_free", _INT, _TAB, _P, _I64, _P)
+_sig("fg_pages_compact", _INT, _TAB, _POOL, _I32, _P, _SZ, _P)
+_sig("fg_paged_append", _INT, _POOL, _TAB, _P, _P, _P, _I64, _I64, _P, _P, _I64, _P)
+_sig("fg_paged_attention_workspace_bytes", _SZ, _POOL, _TAB, _I32, _I64, _I64)
+_sig("fg_paged_attention", _INT, _POOL, _TAB, _P, _P, _I64, _I32, _I64, _I64, _I64, _I64, _P, _I64, _P, _SZ, _P)
+
+
+def _dense(t: torch.Tensor, dtype, shape, device, name: str) -> torch.Tensor:
+    """t itself, when it is a contiguous tensor of this type, shape and device."""
+    if t.dtype != dtype or t.device != device or not t.is_contiguous() or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: expected a contiguous {dtype} tensor {tuple(shape)} on {device}, got {t.dtype} "
+                         f"{tuple(t.shape)} on {t.device}")
+    return t
+
+
+class PagePool:
+    """K and V pages of one layer, [pages][heads][page_size][head_dim] in
+    4-bit groups, on `device`."""
+
+    def __init__(self, pages, page_size, heads, head_dim, dtype=torch.float16, device="cuda"):
+        c = torch.zeros((pages, heads, page_size, head_dim // 2), dtype=torch.uint8, device=device)
+        m = torch.zeros((pages, heads, page_size, head_dim // GROUP), dtype=torch.float32, device=device)
+        self._hold(c, m, torch.zeros_like(m), torch.zeros_like(c), torch.zeros_like(m), torch.zeros_like(m), dtype)
+
+    @staticmethod
+    def of(k_codes, k_mins, k_scales, v_codes, v_mins, v_scales, dtype=torch.float16) -> "PagePool":
+        """The pool whose arrays are these tensors (kept, not copied)."""
+        p = PagePool.__new__(PagePool)
+        p._hold(k_codes, k_mins, k_scales, v_codes, v_mins, v_scales, dtype)
+        return p
+
+    def _hold(self, k_codes, k_mins, k_scales, v_codes, v_mins, v_scales, dtype):
+        if dtype not in (torch.float16, torch.float32):
+            raise TypeError(f"activations must be float16 or float32, got {dtype}")
+        if k_codes.dim() != 4:
+            raise ValueError("codes are [pages][heads][page_size][head_dim/2]")
+        self.pages, self.heads, self.page_size = (int(x) for x in k_codes.shape[:3])
+        self.head_dim = 2 * int(k_codes.shape[3])
+        self.dtype, self.device = dtype, k_codes.device
+        cs = (self.pages, self.heads, self.page_size, self.head_dim // 2)
+        ms = cs[:3] + (self.head_dim // GROUP,)
+        self.k_codes = _dense(k_codes, torch.uint8, cs, self.device, "k_codes")
+        self.v_codes = _dense(v_codes, torch.uint8, cs, self.device, "v_codes")
+        self.k_mins = _dense(k_mins, torch.float32, ms, self.device, "k_mins")
+        self.k_scales = _dense(k_scales, torch.float32, ms, self.device, "k_scales")
+        self.v_mins = _dense(v_mins, torch.float32, ms, self.device, "v_mins")
+        self.v_scales = _dense(v_scales, torch.float32, ms, self.device, "v_scales")
+        self._s = fg_page_pool(_ptr(self.k_codes), _ptr(self.v_codes), _ptr(self.k_mins), _ptr(self.k_scales),
+                               _ptr(self.v_mins), _ptr(self.v_scales), self.pages, self.page_size, self.heads,
+                               self.head_dim, FG_F16 if dtype == torch.float16 else FG_F32)
+        self._ref = ctypes.byref(self._s)
+
+    @property
+    def struct(self) -> fg_page_pool:
+        return self._s
+
+    def nbytes(self) -> int:
+        ts = [self.k_codes, self.v_codes, self.k_mins, self.k_scales, self.v_mins, self.v_scales]
+        return sum(t.numel() * t.element_size() for t in ts)
+
+
+class PagePools:
+    """Marshalled array of the layers' pools, for the calls that move pages."""
+
+    def __init__(self, pools: list):
+        self.pools = list(pools)
+        self.arr = (fg_page_pool * len(self.pools))(*(p.struct for p in self.pools))
+
+
+class PageTable:
+    """The page table of all layers: `table` int32 [seqs][stride], `lens` int32
+    [seqs], `refs` int32 [pages] (fg_page_table; kept, not copied)."""
+
+    def __init__(self, table: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor, page_size: int):
+        if table.dim() != 2 or refs.dim() != 1:
+            raise ValueError("table is [seqs][stride], refs [pages]")
+        self.device = table.device
+        self.table = _dense(table, torch.int32, table.shape, self.device, "table")
+        self.lens = _dense(lens, torch.int32, (table.shape[0],), self.device, "lens")
+        self.refs = _dense(refs, torch.int32, refs.shape, self.device, "refs")
+        self.seqs, self.stride = int(table.shape[0]), int(table.shape[1])
+        self.pages, self.page_size = int(refs.shape[0]), int(page_size)
+        self._s = fg_page_table(_ptr(table), _ptr(lens), _ptr(refs), self.seqs, self.stride, self.pages, self.page_size)
+        self._ref = ctypes.byref(self._s)
+
+    @staticmethod
+    def empty(seqs: int, stride: int, pages: int, page_size: int, device="cuda") -> "PageTable":
+        """A table of empty sequences, every page free."""
+        return PageTable(torch.full((seqs, stride), -1, dtype=torch.int32, device=device),
+                         torch.zeros(seqs, dtype=torch.int32, device=device),
+                         torch.zeros(pages, dtype=torch.int32, device=device), page_size)
+
+    @property
+    def struct(self) -> fg_page_table:
+        return self._s
+
+
+def _on(tab: "PageTable", stream) -> int:
+    """The stream of a paged call; its buffers must be on the current device."""
+    if tab.device.type == "cuda" and tab.device.index != torch.cuda.current_device():
+        raise ValueError(f"the page table is on {tab.device}, the current device is {torch.cuda.current_device()}")
+    return _stream(stream)
+
+
+def _paged_ws(nbytes: int, tab: "PageTable", stream) -> torch.Tensor:
+    """A workspace of one call, not reused before the call's stream is done with it."""
+    ws = workspace(nbytes, tab.device)
+    if stream is not None:
+        st = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream), device=tab.device)
+        ws.record_stream(st)
+    return ws
+
+
+def _ints(t: torch.Tensor, n, tab: "PageTable", name: str) -> int:
+    return _dense(t, torch.int32, (t.numel() if n is None else n,), tab.device, name).data_ptr()
+
+
+def _rows(t: torch.Tensor, pool: "PagePool", n, cols: int, name: str) -> torch.Tensor:
+    """t, when it is [n][cols] rows of the pool's type and device with unit column stride."""
+    if (t.dim() != 2 or t.dtype != pool.dtype or t.device != pool.device or t.shape[1] != cols
+            or (n is not None and t.shape[0] != n) or (cols > 1 and t.stride(1) != 1)):
+        raise ValueError(f"{name}: expected {pool.dtype} rows [{'n' if n is None else n}][{cols}] on {pool.device}, got "
+                         f"{t.dtype} {tuple(t.shape)} strides {t.stride()} on {t.device}")
+    return t
+
+
+def _ld(t: torch.Tensor) -> int:
+    """Row stride (a single row's own is any)."""
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+
+
+def fg_pages_workspace_bytes(tab: PageTable, n: int = 0) -> int:
+    """Workspace of fg_pages_reserve, fg_pages_compact (n = 0) and of fg_pages_fork of n sequences."""
+    return _lib.fg_pages_workspace_bytes(tab._ref, int(n))
+
+
+def fg_pages_reserve(tab: PageTable, cu: torch.Tensor, ws: torch.Tensor | None = None, stream=None) -> None:
+    """lens += the rows of cu (int32 [seqs+1]), with pages for them."""
+    if ws is None:
+        ws = _paged_ws(fg_pages_workspace_bytes(tab), tab, stream)
+    _check(_lib.fg_pages_reserve(tab._ref, _ints(cu, tab.seqs + 1, tab, "cu"), _ptr(ws), ws.numel(), _on(tab, stream)),
+           "fg_pages_reserve")
+
+
+def fg_pages_free(tab: PageTable, rows: torch.Tensor, stream=None) -> None:
+    """Ends the sequences rows (int32)."""
+    _check(_lib.fg_pages_free(tab._ref, _ints(rows, None, tab, "rows"), rows.numel(), _on(tab, stream)), "fg_pages_free")
+
+
+def fg_pages_fork(tab: PageTable, pools: PagePools, src: torch.Tensor, dst: torch.Tensor,
+                  ws: torch.Tensor | None = None, stream=None) -> None:
+    """Sequences dst (int32 [n], empty) become copies of src: full pages shared, a partly filled one copied."""
+    n = src.numel()
+    if ws is None:
+        ws = _paged_ws(fg_pages_workspace_bytes(tab, n), tab, stream)
+    _check(_lib.fg_pages_fork(tab._ref, pools.arr, len(pools.pools), _ints(src, n, tab, "src"),
+                              _ints(dst, n, tab, "dst"), n, _ptr(ws), ws.numel(), _on(tab, stream)), "fg_pages_fork")
+
+
+def fg_pages_compact(tab: PageTable, pools: PagePools, ws: torch.Tensor | None = None, stream=None) -> None:
+    """Moves the pages in use to the front of the pools."""
+    if ws is None:
+        ws = _paged_ws(fg_pages_workspace_bytes(tab), tab, stream)
+    _check(_lib.fg_pages_compact(tab._ref, pools.arr, len(pools.pools), _ptr(ws), ws.numel(), _on(tab, stream)),
+           "fg_pages_compact")
+
+
+def fg_paged_append(pool: PagePool, tab: PageTable, cu: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                    k_restored: torch.Tensor | None = None, v_restored: torch.Tensor | None = None,
+                    stream=None) -> None:
+    """Quantizes the ragged batch's K and V rows [ntok][heads*head_dim] into the pages; the restored tensors, when
+    given, receive the rows as the cache restores them."""
+    h1 = pool.heads * pool.head_dim
+    n = k.shape[0]
+    _rows(k, pool, None, h1, "k")
+    _rows(v, pool, n, h1, "v")
+    if n > 1 and v.stride(0) != k.stride(0):
+        raise ValueError("k and v need one row stride")
+    ldr = 0
+    if k_restored is not None and v_restored is not None:
+        _rows(k_restored, pool, n, h1, "k_restored")
+        _rows(v_restored, pool, n, h1, "v_restored")
+        ldr = _ld(k_restored)
+        if n > 1 and v_restored.stride(0) != k_restored.stride(0):
+            raise ValueError("k_restored and v_restored need one row stride")
+    _check(_lib.fg_paged_append(pool._ref, tab._ref, _ints(cu, tab.seqs + 1, tab, "cu"), _ptr(k), _ptr(v), _ld(k), n,
+                                _ptr(k_restored), _ptr(v_restored), ldr, _on(tab, stream)), "fg_paged_append")
+
+
+def fg_paged_attention_workspace_bytes(pool: PagePool, tab: PageTable, q_heads: int, ntok: int, max_q: int) -> int:
+    return _lib.fg_paged_attention_workspace_bytes(pool._ref, tab._ref, int(q_heads), int(ntok), int(max_q))
+
+
+def fg_paged_attention(pool: PagePool, tab: PageTable, cu: torch.Tensor, q: torch.Tensor, q_heads: int,
+                       out: torch.Tensor, max_q: int, window: int = 0, sinks: int = 0,
+                       ws: torch.Tensor | None = None, stream=None) -> None:
+    """out rows = causal attention of the ragged batch's rows q [ntok][q_heads*head_dim] over their sequences' pages
+    (window > 0: the last `window` tokens and the first `sinks`)."""
+    n = q.shape[0]
+    _rows(q, pool, None, q_heads * pool.head_dim, "q")
+    _rows(out, pool, n, q_heads * pool.head_dim, "out")
+    if ws is None:
+        ws = _paged_ws(fg_paged_attention_workspace_bytes(pool, tab, q_heads, n, max_q), tab, stream)
+    _check(_lib.fg_paged_attention(pool._ref, tab._ref, _ints(cu, tab.seqs + 1, tab, "cu"), _ptr(q), _ld(q),
+                                   int(q_heads), n, int(max_q), int(window), int(sinks), _ptr(out), _ld(out), _ptr(ws),
+                                   ws.numel(), _on(tab, stream)), "fg_paged_attention")

@@ -63,7 +63,7 @@ namespace {
 const char* const kClassNames[KC_COUNT] = {
     "quantize_g64", "dequant_g64", "kv_store_q4", "gemm_simt", "gemm_tc",
     "gemm_splitk_reduce", "attn_decode", "attn_decode_combine", "attn_prefill", "gemm_q4_decode",
-    "pack_weight", "attn_decode_topk"};
+    "pack_weight", "attn_decode_topk", "attn_paged", "attn_paged_plan", "pages_plan", "pages_copy"};
 
 // Launches of the same class that follow one another on a stream form one
 // timed run (one event pair): events between them would break the overlap
@@ -233,7 +233,9 @@ fg_status fg_sync_status(cudaStream_t stream) {
   if (v != 0) {
     unsigned int zero = 0;
     cudaMemcpy(w, &zero, sizeof(zero), cudaMemcpyHostToDevice);
-    return fg::fail(FG_ERR_DEVICE_TIMEOUT, "device error word 0x%x", v);
+    if (v & ~(fg::DEV_ERR_BATCH | fg::DEV_ERR_PAGE)) return fg::fail(FG_ERR_DEVICE_TIMEOUT, "device error word 0x%x", v);
+    if (v & fg::DEV_ERR_BATCH) return fg::fail(FG_ERR_ARG, "paged cache: offsets, lengths or list entries out of range");
+    return fg::fail(FG_ERR_CAPACITY, "paged cache: no free page, a table row too short, or a page missing");
   }
   return FG_OK;
 }

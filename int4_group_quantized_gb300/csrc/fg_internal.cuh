@@ -29,7 +29,11 @@ int num_sms();
 // that run bounded waits OR an error code into it.
 unsigned int* device_error_word();
 
-enum DeviceError : unsigned int { DEV_ERR_WAIT_TIMEOUT = 1u };
+enum DeviceError : unsigned int {
+  DEV_ERR_WAIT_TIMEOUT = 1u,
+  DEV_ERR_PAGE = 2u,    // a paged call: no free page, a row too short, a page missing
+  DEV_ERR_BATCH = 4u    // a paged call: offsets, lengths or list entries out of range
+};
 // Polls a bounded wait makes before it gives up (fg_set_wait_limit), passed
 // to every kernel that waits.  Waits for work that is already in flight (a
 // copy issued, an MMA committed) use kDrainLimit instead: a CTA never leaves
@@ -54,6 +58,10 @@ enum KernelClass : int {
   KC_GEMM_Q4DEC,
   KC_PACK,
   KC_ATTN_TOPK,
+  KC_ATTN_PAGED,
+  KC_ATTN_PAGED_PLAN,
+  KC_PAGES_PLAN,
+  KC_PAGES_COPY,
   KC_COUNT
 };
 constexpr int kProfilePhases = 4;
