@@ -5,26 +5,16 @@
 // A first form: one warp per (row, query head), its lanes along the head
 // dimension, one key at a time with a running maximum and sum.
 #include <math.h>
+#include <string.h>
 
-#include "paged.cuh"
+#include <algorithm>
+
+#include "paged_attn.cuh"
+#include "tc_ptx.cuh"
 
 namespace fg {
 namespace paged {
 namespace {
-
-template <typename T>
-struct AttnArgs {
-  Pool pool;
-  Table tab;
-  Batch batch;
-  const T* q;
-  T* out;
-  int64_t ldq, ldo;
-  int q_heads, group;   // query heads, and query heads per K/V head
-  int max_q;
-  int64_t window, sinks;
-  float scale;
-};
 
 __device__ __forceinline__ float to_f(float x) { return x; }
 __device__ __forceinline__ float to_f(__half x) { return __half2float(x); }
@@ -41,17 +31,18 @@ __global__ void __launch_bounds__(128) attn_rows_kernel(const AttnArgs<T> a) {
     for (int i = threadIdx.x; i < a.tab.seqs; i += blockDim.x) seq_of(a.tab, a.batch, i);
   const int64_t r64 = w / a.q_heads;
   if (r64 >= a.batch.ntok) return;
-  const int r = static_cast<int>(r64), qh = static_cast<int>(w % a.q_heads), h = qh / a.group;
+  const int r = static_cast<int>(r64), qh = static_cast<int>(w % a.q_heads), h = qh / a.shape.group;
   const int i = seq_of_row(a.batch.cu, a.tab.seqs, r);
   if (i >= a.tab.seqs) return;
   const Seq s = seq_of(a.tab, a.batch, i);
   if (r < s.row0 || r >= s.row0 + s.n) return;
-  if (s.n > a.max_q) {
+  if (s.n > a.shape.max_q) {
     atomicOr(a.batch.err, DEV_ERR_BATCH);
     return;
   }
   const int64_t pos = static_cast<int64_t>(s.len) - s.n + (r - s.row0);
-  const int64_t lo = a.window > 0 && pos - a.window + 1 > 0 ? pos - a.window + 1 : 0;
+  if (static_cast<int64_t>(s.n) * a.shape.group <= a.shape.skip) return;   // taken by the step kernel
+  const int64_t lo = a.shape.window > 0 && pos - a.shape.window + 1 > 0 ? pos - a.shape.window + 1 : 0;
   float q[E], o[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) {
@@ -61,7 +52,7 @@ __global__ void __launch_bounds__(128) attn_rows_kernel(const AttnArgs<T> a) {
   float m = -INFINITY, l = 0.0f;
   const int g = lane * E / 64;
   for (int64_t j = 0; j <= pos && j < s.keys; ++j) {
-    if (j < lo && j >= a.sinks) {
+    if (j < lo && j >= a.shape.sinks) {
       j = lo - 1;
       continue;
     }
@@ -94,10 +85,232 @@ __global__ void __launch_bounds__(128) attn_rows_kernel(const AttnArgs<T> a) {
   for (int e = 0; e < E; ++e) put(a.out + r * a.ldo + qh * D + lane * E + e, l != 0.0f ? o[e] / l : 0.0f);
 }
 
+// ---- the plan -------------------------------------------------------------------
+// One CTA: the tiles of every sequence, class by class, as prefix sums, and
+// the size of a share.  A warp takes a run of sequences, a lane one of them; a
+// long chunk's units are counted by the warp's lanes together.
+constexpr int kPlanThreads = 1024;
+
+struct PlanArgs {
+  Table tab;
+  Batch batch;
+  AttnShape shape;
+  int heads;
+  ClassPlan step, tile;   // a class with no workers is not used
+};
+
+template <int RU, int KTL>
+__device__ __forceinline__ int64_t units_cost(const Seq& s, const AttnShape& sh, int u0, int stride) {
+  const int64_t all = static_cast<int64_t>(s.n) * sh.group;
+  const int units = static_cast<int>((all + RU - 1) / RU);
+  int64_t c = 0;
+  for (int u = u0; u < units; u += stride) {
+    const Unit x = unit_of<RU>(s, sh.group, u);
+    c += span_of<KTL>(x.p0, x.p1, s.keys, sh.window, sh.sinks).n;
+  }
+  return c;
+}
+
+template <int TRU, int TKTL, int TSPLIT_MIN>
+__global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
+  __shared__ int64_t warp_sum[2][32];
+  __shared__ int warp_max[2][32];
+  tc::griddep_launch();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int nwarps = blockDim.x >> 5;
+  const int seqs = a.tab.seqs, per = (seqs + nwarps - 1) / nwarps;
+  const int begin = min(seqs, warp * per), end = min(seqs, begin + per);
+  int64_t sum[2] = {0, 0};
+  int longest[2] = {0, 0};
+  for (int pass = 0; pass < 2; ++pass) {
+    int64_t at[2] = {0, 0};
+    if (pass == 1) {
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        if (lane == 0) {
+          warp_sum[c][warp] = sum[c];
+          warp_max[c][warp] = longest[c];
+        }
+      }
+      __syncthreads();
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        int64_t v = lane < nwarps ? warp_sum[c][lane] : 0, inc = v;
+        int mx = lane < nwarps ? warp_max[c][lane] : 0;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int64_t up = __shfl_up_sync(0xffffffffu, inc, o);
+          if (lane >= o) inc += up;
+          mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        }
+        const int64_t total = __shfl_sync(0xffffffffu, inc, 31);
+        at[c] = __shfl_sync(0xffffffffu, inc - v, warp);
+        const ClassPlan& p = c ? a.tile : a.step;
+        if (threadIdx.x == 0 && p.workers > 0) {
+          int64_t share = (total + p.workers - 1) / p.workers;
+          const int64_t least = (mx + kMaxSplits - 1) / kMaxSplits;
+          share = share > least ? share : least;
+          const int64_t few = c ? TSPLIT_MIN : 2;
+          p.head[0] = total;
+          p.head[1] = share > few ? share : few;
+          p.pre[seqs] = total;
+        }
+      }
+    }
+    for (int i0 = begin; i0 < end; i0 += 32) {
+      const int i = i0 + lane;
+      int64_t cost[2] = {0, 0};
+      bool tall = false;
+      Seq s{0, 0, 0, 0};
+      if (i < end) {
+        s = seq_of(a.tab, a.batch, i);
+        if (s.n > a.shape.max_q) {
+          atomicOr(a.batch.err, DEV_ERR_BATCH);
+          s.n = 0;
+        }
+        const int64_t rows = static_cast<int64_t>(s.n) * a.shape.group;
+        if (rows > 0 && a.step.workers > 0 && rows <= kStepRows) {
+          const int base = s.len - s.n;
+          const Span sp = span_of<5>(base, s.len - 1, s.keys, a.shape.window, a.shape.sinks);
+          cost[0] = static_cast<int64_t>(sp.n) * a.heads;
+          longest[0] = max(longest[0], sp.n);
+        } else if (rows > 0 && a.tile.workers > 0) {
+          tall = true;
+          // the last unit sees the most tiles
+          const Unit x = unit_of<TRU>(s, a.shape.group, static_cast<int>((rows - 1) / TRU));
+          longest[1] = max(longest[1], span_of<TKTL>(x.p0, x.p1, s.keys, a.shape.window, a.shape.sinks).n + 1);
+        }
+      }
+      uint32_t todo = __ballot_sync(0xffffffffu, tall);
+      while (todo) {
+        const int src = __ffs(todo) - 1;
+        todo &= todo - 1;
+        Seq t;
+        t.row0 = 0;
+        t.n = __shfl_sync(0xffffffffu, s.n, src);
+        t.len = __shfl_sync(0xffffffffu, s.len, src);
+        t.keys = __shfl_sync(0xffffffffu, s.keys, src);
+        int64_t c = units_cost<TRU, TKTL>(t, a.shape, lane, 32);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) c += __shfl_xor_sync(0xffffffffu, c, o);
+        if (lane == src) cost[1] = c * a.heads;
+      }
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        int64_t inc = cost[c];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int64_t up = __shfl_up_sync(0xffffffffu, inc, o);
+          if (lane >= o) inc += up;
+        }
+        const ClassPlan& p = c ? a.tile : a.step;
+        if (pass == 1 && i < end && p.workers > 0) p.pre[i] = at[c] + inc - cost[c];
+        const int64_t all = __shfl_sync(0xffffffffu, inc, 31);
+        at[c] += all;
+        if (pass == 0) sum[c] += all;
+      }
+    }
+    if (pass == 0)
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) longest[c] = max(longest[c], __shfl_xor_sync(0xffffffffu, longest[c], o));
+  }
+}
+
+// ---- joining the partials of items that cross shares ------------------------------
+// Block w joins the item that begins in share w and ends later: the partials
+// lie in slot 1 of w and slot 0 of the shares after it, and are summed in that
+// order (the same bits every time).
+template <typename T, int D, int RU>
+__global__ void join_kernel(const AttnArgs<T> a, const ClassPlan pl) {
+  tc::griddep_launch();
+  tc::griddep_wait();
+  const int w = blockIdx.x;
+  const int4 rec = pl.rec[w];
+  if (rec.x < 0) return;
+  const Seq s = seq_of(a.tab, a.batch, rec.x);
+  const Unit x = unit_of<RU>(s, a.shape.group, rec.z);
+  const int d = threadIdx.x % D;
+  for (int n = threadIdx.x / D; n < x.rows; n += blockDim.x / D) {
+    auto at = [&](int k) { return ((k == w ? static_cast<int64_t>(w) * 2 + 1 : static_cast<int64_t>(k) * 2)) * pl.rows + n; };
+    float m = -INFINITY;
+#pragma unroll 8
+    for (int k = w; k <= rec.w; ++k) m = fmaxf(m, pl.stat[at(k)].x);
+    const float base = m == -INFINITY ? 0.0f : m;
+    float l = 0.0f, o = 0.0f;
+#pragma unroll 8
+    for (int k = w; k <= rec.w; ++k) {
+      const float2 st = pl.stat[at(k)];
+      const float f = exp2f(st.x - base);
+      l += f * st.y;
+      o += f * pl.part[at(k) * D + d];
+    }
+    const int row = x.r0 + n, t = row / a.shape.group;
+    put(a.out + static_cast<int64_t>(s.row0 + t) * a.ldo +
+            static_cast<int64_t>(rec.y * a.shape.group + row - t * a.shape.group) * D + d,
+        l == 0.0f ? 0.0f : o / l);
+  }
+}
+
+template <typename T, int D, int RU>
+fg_status join(const AttnArgs<T>& a, const ClassPlan& pl, cudaStream_t st) {
+  cudaLaunchAttribute pdl[1];
+  pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  pdl[0].val.programmaticStreamSerializationAllowed = 1;
+  Trace tr(KC_ATTN_COMBINE, st);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(pl.workers));
+  cfg.blockDim = dim3(D * std::min(pl.rows, 512 / D));
+  cfg.stream = st;
+  cfg.attrs = pdl;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, join_kernel<T, D, RU>, a, pl) != cudaSuccess) return check_launch("join_kernel (launch)");
+  return check_launch("join_kernel");
+}
+
+// ---- workspace ------------------------------------------------------------------------
+constexpr int kMaxSms = 160;   // a workspace fits this many SMs; launches use no more
+inline size_t up(size_t x) { return (x + 255) / 256 * 256; }
+
+struct Layout {
+  ClassPlan step, tile;
+  size_t bytes;
+};
+void carve_class(ClassPlan& c, char*& p, int64_t seqs, int head_dim, int workers, int most, int rows) {
+  c.workers = workers;
+  c.rows = rows;
+  if (workers == 0) return;
+  c.head = reinterpret_cast<int64_t*>(p);
+  p += 256;
+  c.pre = reinterpret_cast<int64_t*>(p);
+  p += up(8 * static_cast<size_t>(seqs + 1));
+  c.rec = reinterpret_cast<int4*>(p);
+  p += up(16 * static_cast<size_t>(most));
+  c.stat = reinterpret_cast<float2*>(p);
+  p += up(16 * static_cast<size_t>(most) * rows);
+  c.part = reinterpret_cast<float*>(p);
+  p += up(8 * static_cast<size_t>(most) * rows * head_dim);
+}
+// The classes that a call of at most max_q rows a sequence can need.
+Layout layout_of(const fg_page_pool& pool, const fg_page_table& t, int32_t q_heads, int64_t max_q, void* ws, int sms) {
+  Layout l;
+  const int64_t group = q_heads / pool.heads, most = max_q * group;
+  char* p = static_cast<char*>(ws);
+  memset(&l.step, 0, sizeof(l.step));
+  memset(&l.tile, 0, sizeof(l.tile));
+  if (pool.dtype == FG_F16 && group <= kStepRows) {
+    const int rows = most <= 8 ? 8 : kStepRows;
+    carve_class(l.step, p, t.seqs, pool.head_dim, step_workers(rows, sms), step_workers(rows, kMaxSms), rows);
+  }
+  l.bytes = static_cast<size_t>(p - static_cast<char*>(ws)) + 256;
+  return l;
+}
+
 template <typename T>
 fg_status launch_attn(const fg_page_pool& pool, const fg_page_table& t, const int32_t* cu, const void* q, int64_t ldq,
                       int32_t q_heads, int64_t ntok, int64_t max_q, int64_t window, int64_t sinks, void* out,
-                      int64_t ldo, unsigned int* err, cudaStream_t st) {
+                      int64_t ldo, void* ws, unsigned int* err, cudaStream_t st) {
   AttnArgs<T> a;
   a.pool = pool_of(pool);
   a.tab = table_of(t);
@@ -107,11 +320,32 @@ fg_status launch_attn(const fg_page_pool& pool, const fg_page_table& t, const in
   a.ldq = ldq;
   a.ldo = ldo;
   a.q_heads = q_heads;
-  a.group = q_heads / pool.heads;
-  a.max_q = static_cast<int>(max_q);
-  a.window = window;
-  a.sinks = sinks;
-  a.scale = static_cast<float>(1.0 / sqrt(static_cast<double>(pool.head_dim)));
+  const double scale = 1.0 / sqrt(static_cast<double>(pool.head_dim));
+  a.scale = static_cast<float>(scale);
+  a.scale_log2 = static_cast<float>(scale * 1.4426950408889634074);
+  a.shape.group = q_heads / pool.heads;
+  a.shape.max_q = static_cast<int>(std::min<int64_t>(max_q, ntok));
+  // positions are below 2^31: a wider window hides nothing
+  a.shape.window = window > (int64_t(1) << 30) ? 0 : static_cast<int>(window);
+  a.shape.sinks = static_cast<int>(std::min<int64_t>(sinks, int64_t(1) << 30));
+  const Layout l = layout_of(pool, t, q_heads, max_q, ws, std::min(num_sms(), kMaxSms));
+  const bool tall = max_q * a.shape.group > kStepRows || l.step.workers == 0;
+  a.shape.skip = l.step.workers > 0 ? kStepRows : 0;
+  if (l.step.workers > 0) {
+    PlanArgs p{a.tab, a.batch, a.shape, pool.heads, l.step, l.tile};
+    {
+      Trace tr(KC_ATTN_PAGED_PLAN, st);
+      const unsigned threads = static_cast<unsigned>(std::min<int64_t>(1024, (t.seqs + 31) / 32 * 32));
+      plan_kernel<256, 7, 1><<<1, threads, 0, st>>>(p);
+      FG_TRY(check_launch("plan_kernel"));
+    }
+    if constexpr (sizeof(T) == 2) {
+      FG_TRY(paged_attention_step(a, l.step, pool.head_dim, st));
+      if (pool.head_dim == 128) FG_TRY((join<T, 128, kStepRows>(a, l.step, st)));
+      else FG_TRY((join<T, 64, kStepRows>(a, l.step, st)));
+    }
+  }
+  if (!tall) return FG_OK;
   const int64_t warps = ntok * q_heads;
   const unsigned grid = static_cast<unsigned>((warps + 3) / 4);
   Trace tr(KC_ATTN_PAGED, st);
@@ -141,7 +375,7 @@ extern "C" {
 size_t fg_paged_attention_workspace_bytes(const fg_page_pool* pool, const fg_page_table* t, int32_t q_heads,
                                           int64_t ntok, int64_t max_q) {
   if (check_attn(pool, t, q_heads, ntok, max_q) != FG_OK) return 0;
-  return 256;
+  return layout_of(*pool, *t, q_heads, max_q, nullptr, kMaxSms).bytes;
 }
 
 fg_status fg_paged_attention(const fg_page_pool* pool, const fg_page_table* t, const int32_t* cu, const void* q,
@@ -161,8 +395,8 @@ fg_status fg_paged_attention(const fg_page_pool* pool, const fg_page_table* t, c
   unsigned int* err = device_error_word();
   if (!err) return fail(FG_ERR_CUDA, "device error word");
   if (pool->dtype == FG_F16)
-    return launch_attn<__half>(*pool, *t, cu, q, ldq, q_heads, ntok, max_q, window, sinks, out, ldo, err, stream);
-  return launch_attn<float>(*pool, *t, cu, q, ldq, q_heads, ntok, max_q, window, sinks, out, ldo, err, stream);
+    return launch_attn<__half>(*pool, *t, cu, q, ldq, q_heads, ntok, max_q, window, sinks, out, ldo, ws, err, stream);
+  return launch_attn<float>(*pool, *t, cu, q, ldq, q_heads, ntok, max_q, window, sinks, out, ldo, ws, err, stream);
 }
 
 }  // extern "C"

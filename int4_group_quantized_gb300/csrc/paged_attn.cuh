@@ -1,0 +1,28 @@
+// Internal interface of the paged attention kernels.
+#pragma once
+
+#include "paged_sched.cuh"
+
+namespace fg {
+namespace paged {
+
+template <typename T>
+struct AttnArgs {
+  Pool pool;
+  Table tab;
+  Batch batch;
+  const T* q;
+  T* out;
+  int64_t ldq, ldo;
+  int q_heads;
+  AttnShape shape;
+  float scale;        // 1 / sqrt(head_dim)
+  float scale_log2;   // times log2(e)
+};
+
+// Sequences of at most kStepRows rows per K/V head (fp16).
+int step_workers(int rows, int sms);
+fg_status paged_attention_step(const AttnArgs<__half>& a, const ClassPlan& pl, int head_dim, cudaStream_t st);
+
+}  // namespace paged
+}  // namespace fg

@@ -1,0 +1,90 @@
+// How the paged attention's work is dealt out.
+//
+// An item is one unit of rows of one sequence (RU rows, the query heads of a
+// K/V head side by side: row t * group + g) against the keys it sees, for one
+// K/V head; its cost is a number of key tiles (KT keys).  All items in a line,
+// sequence by sequence, head by head, unit by unit, make T tiles, and worker w
+// takes tiles [w * per, (w + 1) * per): equal work whatever the lengths are,
+// and neighbouring workers read the same head's keys.  An item inside one
+// worker's share is finished there; one that crosses shares leaves a partial
+// (sums, maximum and normaliser) with each, joined in order afterwards.  A
+// worker's first segment goes to its slot 0 when it began before, its last to
+// slot 1 when it ends later, so two slots a worker are enough.
+#pragma once
+
+#include <stdint.h>
+
+#include "paged.cuh"
+
+namespace fg {
+namespace paged {
+
+// Sequences with at most this many rows (rows times group) are steps: the
+// warp-level kernel takes them; longer ones go to the tile kernels.
+constexpr int kStepRows = 16;
+constexpr int kMaxSplits = 128;   // shares an item may cross (the join reads them one after another)
+
+struct AttnShape {
+  int group;            // query heads per K/V head
+  int max_q;
+  int window, sinks;    // window 0: none; both at most 2^30
+  int skip;             // sequences of at most this many rows are another kernel's
+};
+
+// What a class of items shares: header and prefix sums written by the plan.
+struct ClassPlan {
+  int64_t* head;        // [0] tiles in all, [1] tiles of a share
+  int64_t* pre;         // [seqs + 1] tiles before sequence i
+  int4* rec;            // [workers] the item that begins in a share and ends later: (sequence or -1, head, unit, last share)
+  float* part;          // [workers][2][rows][D] sums
+  float2* stat;         // [workers][2][rows] (maximum, normaliser)
+  int rows;             // rows of a slot
+  int workers;
+};
+
+// Key tiles that the rows at positions p0 .. p1 see: the first ns, then those
+// from t0 on; n in all, at least one (a unit that sees nothing still writes its
+// zeros).
+struct Span {
+  int ns, t0, n;
+  __device__ __forceinline__ int tile(int x) const { return x < ns ? x : t0 + x - ns; }
+};
+template <int KTL>
+__device__ __forceinline__ Span span_of(int p0, int p1, int keys, int window, int sinks) {
+  const int last = p1 < keys - 1 ? p1 : keys - 1;
+  Span s{0, 0, 1};
+  if (last < 0) return s;
+  int lo = window > 0 && p0 >= window ? p0 - window + 1 : 0;
+  lo = lo < last ? lo : last;
+  const int t1 = last >> KTL, t0 = lo >> KTL;
+  const int se = sinks < last + 1 ? sinks : last + 1;
+  const int ns = (se + (1 << KTL) - 1) >> KTL;
+  if (window == 0 || ns >= t0) {
+    s.n = t1 + 1;
+  } else {
+    s.ns = ns;
+    s.t0 = t0;
+    s.n = ns + t1 - t0 + 1;
+  }
+  return s;
+}
+
+// Unit u of a sequence: its rows and their positions.
+struct Unit {
+  int r0, rows;         // rows r0 .. r0 + rows - 1 of the sequence's n * group
+  int p0, p1;
+};
+template <int RU>
+__device__ __forceinline__ Unit unit_of(const Seq& s, int group, int u) {
+  Unit x;
+  const int64_t all = static_cast<int64_t>(s.n) * group;
+  x.r0 = u * RU;
+  x.rows = static_cast<int>(all - x.r0 < RU ? all - x.r0 : RU);
+  const int base = s.len - s.n;
+  x.p0 = base + x.r0 / group;
+  x.p1 = base + (x.r0 + x.rows - 1) / group;
+  return x;
+}
+
+}  // namespace paged
+}  // namespace fg
