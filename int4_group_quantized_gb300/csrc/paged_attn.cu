@@ -220,36 +220,92 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
 
 // ---- joining the partials of items that cross shares ------------------------------
 // Block w joins the item that begins in share w and ends later: the partials
-// lie in slot 1 of w and slot 0 of the shares after it, and are summed in that
-// order (the same bits every time).
+// lie in slot 1 of w and slot 0 of the shares after it.  The factors of all
+// (share, row) first, then the sums: a warp per row and part of the shares,
+// four columns a lane, the parts added in order (the same bits every time).
+constexpr int kJoinWarps = 8;
+
 template <typename T, int D, int RU>
-__global__ void join_kernel(const AttnArgs<T> a, const ClassPlan pl) {
+__global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const AttnArgs<T> a, const ClassPlan pl) {
+  constexpr int kRows = RU <= 16 ? RU : 16;   // rows at once
+  constexpr int kCols = D / 4;                // lanes of a row
+  __shared__ float fac[(kMaxSplits + 2) * kRows];
+  __shared__ float norm[kRows];
+  __shared__ float4 sums[kJoinWarps][32];
   tc::griddep_launch();
   tc::griddep_wait();
-  const int w = blockIdx.x;
+  const int w = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int4 rec = pl.rec[w];
   if (rec.x < 0) return;
   const Seq s = seq_of(a.tab, a.batch, rec.x);
   const Unit x = unit_of<RU>(s, a.shape.group, rec.z);
-  const int d = threadIdx.x % D;
-  for (int n = threadIdx.x / D; n < x.rows; n += blockDim.x / D) {
-    auto at = [&](int k) { return ((k == w ? static_cast<int64_t>(w) * 2 + 1 : static_cast<int64_t>(k) * 2)) * pl.rows + n; };
-    float m = -INFINITY;
-#pragma unroll 8
-    for (int k = w; k <= rec.w; ++k) m = fmaxf(m, pl.stat[at(k)].x);
-    const float base = m == -INFINITY ? 0.0f : m;
-    float l = 0.0f, o = 0.0f;
-#pragma unroll 8
-    for (int k = w; k <= rec.w; ++k) {
-      const float2 st = pl.stat[at(k)];
-      const float f = exp2f(st.x - base);
-      l += f * st.y;
-      o += f * pl.part[at(k) * D + d];
+  const int shares = rec.w - w + 1;
+  auto slot = [&](int k, int n) { return (static_cast<int64_t>(w + k) * 2 + (k == 0 ? 1 : 0)) * pl.rows + n; };
+  for (int n0 = 0; n0 < x.rows; n0 += kRows) {
+    const int rows = min(kRows, x.rows - n0);
+    for (int n = warp; n < rows; n += kJoinWarps) {
+      float m = -INFINITY;
+      for (int k = lane; k < shares; k += 32) m = fmaxf(m, pl.stat[slot(k, n0 + n)].x);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+      const float base = m == -INFINITY ? 0.0f : m;
+      float l = 0.0f;
+      for (int k = lane; k < shares; k += 32) {
+        const float2 st = pl.stat[slot(k, n0 + n)];
+        const float f = exp2f(st.x - base);
+        fac[k * kRows + n] = f;
+        l += f * st.y;
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+      if (lane == 0) norm[n] = l == 0.0f ? 0.0f : 1.0f / l;
     }
-    const int row = x.r0 + n, t = row / a.shape.group;
-    put(a.out + static_cast<int64_t>(s.row0 + t) * a.ldo +
-            static_cast<int64_t>(rec.y * a.shape.group + row - t * a.shape.group) * D + d,
-        l == 0.0f ? 0.0f : o / l);
+    __syncthreads();
+    // (row, part) pairs over half warps (D = 64) or warps (D = 128)
+    constexpr int kTeams = kJoinWarps * 32 / kCols;
+    const int team = threadIdx.x / kCols, col = threadIdx.x % kCols;
+    int parts = 1;
+    while (parts * 2 * rows <= kTeams && parts * 2 <= shares) parts *= 2;
+    for (int r0 = 0; r0 < rows; r0 += kTeams / parts) {
+      const int n = r0 + team / parts, part = team % parts;
+      float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (n < rows) {
+#pragma unroll 8
+        for (int k = part; k < shares; k += parts) {
+          const float4 v = *reinterpret_cast<const float4*>(pl.part + slot(k, n0 + n) * D + 4 * col);
+          const float f = fac[k * kRows + n];
+          o.x = fmaf(f, v.x, o.x);
+          o.y = fmaf(f, v.y, o.y);
+          o.z = fmaf(f, v.z, o.z);
+          o.w = fmaf(f, v.w, o.w);
+        }
+      }
+      if (parts > 1) {
+        sums[warp][lane] = o;
+        __syncthreads();
+        if (part == 0)
+          for (int q = 1; q < parts; ++q) {
+            const int tid = threadIdx.x + q * kCols;
+            const float4 v = sums[tid >> 5][tid & 31];
+            o.x += v.x;
+            o.y += v.y;
+            o.z += v.z;
+            o.w += v.w;
+          }
+        __syncthreads();
+      }
+      if (n < rows && part == 0) {
+        const float f = norm[n];
+        const int row = x.r0 + n0 + n, t = row / a.shape.group;
+        T* dst = a.out + static_cast<int64_t>(s.row0 + t) * a.ldo +
+                 static_cast<int64_t>(rec.y * a.shape.group + row - t * a.shape.group) * D + 4 * col;
+        put(dst, o.x * f);
+        put(dst + 1, o.y * f);
+        put(dst + 2, o.z * f);
+        put(dst + 3, o.w * f);
+      }
+    }
+    __syncthreads();
   }
 }
 
@@ -261,7 +317,7 @@ fg_status join(const AttnArgs<T>& a, const ClassPlan& pl, cudaStream_t st) {
   Trace tr(KC_ATTN_COMBINE, st);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(pl.workers));
-  cfg.blockDim = dim3(D * std::min(pl.rows, 512 / D));
+  cfg.blockDim = dim3(32 * kJoinWarps);
   cfg.stream = st;
   cfg.attrs = pdl;
   cfg.numAttrs = 1;

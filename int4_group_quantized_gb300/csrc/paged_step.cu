@@ -5,15 +5,16 @@
 // The path is bound by the cache's bytes, so every byte is read once for all
 // rows of a K/V head (8 rows are one N = 8 block of the warp-level MMA) and
 // codes are multiplied as they are:
-//   scores   s = sum_g scale_g (q . c)_g + min_g (sum q)_g: lop3 makes a
-//            nibble the exact fp16 1024 + c (or 1024 + 16c, against q / 16),
-//            and the bias 1024 sum q leaves in fp32;
+//   scores   s = sum_g scale_g (q . c)_g + min_g (sum q)_g: a masked nibble
+//            is the subnormal fp16 c * 2^-24 (or 16 c * 2^-24, against q /
+//            16), which the MMA multiplies exactly: no bias to take out;
 //   values   o = sum_t (p_t scale_t) (c_t - 8) + sum_t p_t (min_t + 8
-//            scale_t): centred, because a bias of 1024 in a sum over thousands
-//            of tokens would cost its low bits (the MMA truncates).  The
-//            weight p * scale is rounded to fp16 for the MMA after scaling by
-//            a power of two near 1 / max scale, so that small activations
-//            keep their bits.
+//            scale_t), tile by tile: a tile's MMAs begin from -8 sum w, which
+//            centres the code, because the MMA truncates and a positive sum
+//            over thousands of tokens would lose its low bits.  The weight w =
+//            p * scale is rounded to fp16 for the MMA after scaling by a power
+//            of two near 1 / max scale, so that small activations keep their
+//            bits; sum w is an MMA against ones, of the rounded weights.
 // A warp is a worker (see paged_sched.cuh) and walks tiles of 32 tokens of its
 // share: its own ring of stages in shared memory, filled by asynchronous
 // copies kStages - 1 tiles ahead across items, page numbers another tile
@@ -34,21 +35,19 @@ namespace fg {
 namespace paged {
 namespace {
 
-using attn::lop_mask_or;
 using attn::mma16816;
 using attn::pack_h2;
 using attn::unpack_h2;
 using attn::kHiNib;
 using attn::kLoNib;
-using attn::kMagic;
 
 constexpr int kTileLog2 = 5;
 constexpr int kTile = 1 << kTileLog2;   // tokens of a tile
 constexpr int kWarps = 4;               // warps of a CTA
 template <int NB>
-constexpr int kCtasPerSm = NB == 1 ? 4 : 3;
+constexpr int kCtasPerSm = 3;
 template <int D, int NB>
-constexpr int kStepStages = D == 128 ? (NB == 1 ? 2 : 3) : 4;
+constexpr int kStepStages = D == 128 ? 3 : 4;
 constexpr float kGrow = 8.0f;           // log2 growth of a maximum that forces a rescale
 
 template <int D>
@@ -57,9 +56,12 @@ struct Stage {
   static constexpr int NG = D / 64;
   static constexpr int kMeta = kTile * NG * 4;     // one (min or scale) array
   static constexpr int kV = kTile * C, kKs = 2 * kTile * C, kKm = kKs + kMeta, kVs = kKm + kMeta, kVm = kVs + kMeta;
-  static constexpr int kInfo = kVm + kMeta;        // which halves are present
-  static constexpr int kBytes = kInfo + 16;
+  static constexpr int kInfo = kVm + kMeta;        // (first token, flags, head, sequence), (row0, n, len, keys)
+  static constexpr int kBytes = kInfo + 32;
 };
+// Flags of a tile: the halves that are there, every row sees all of it, the
+// item's first and last tile, the share's last.
+enum : int { kHalf0 = 1, kHalf1 = 2, kWhole = 4, kFirst = 8, kLast = 16, kEnd = 32 };
 // Where the 16-byte piece pc of row t lies: pieces swizzled so that rows 0, 4,
 // 1, 5 (and 2, 6, 3, 7), and rows 0 .. 3 (and 4 .. 7), use all banks.
 template <int D>
@@ -68,6 +70,9 @@ __device__ __forceinline__ int piece_at(int t, int pc) {
   return (t ^ (((t >> 2) & 1) << 1)) * 32 + (pc << 4);
 }
 
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
   uint32_t r;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
@@ -78,28 +83,64 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-__device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
-  uint32_t r;
-  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+__device__ __forceinline__ float max_nan(float a, float b) {   // NaN if either is
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
+// Two fp32 at once (the queries 2 tig and 2 tig + 1 of a lane).
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 r;
+  asm("{ .reg .b64 x, y, z; mov.b64 x, {%2, %3}; mov.b64 y, {%4, %5}; mov.b64 z, {%6, %7};\n"
+      "fma.rn.f32x2 x, x, y, z; mov.b64 {%0, %1}, x; }"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
   return r;
 }
-constexpr uint32_t kOne2 = 0x3C003C00u, kNeg1032 = 0xE408E408u, kSixteenth2 = 0x2C002C00u, kNeg72 = 0xD480D480u;
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 r;
+  asm("{ .reg .b64 x, y; mov.b64 x, {%2, %3}; mov.b64 y, {%4, %5};\n"
+      "mul.rn.f32x2 x, x, y; mov.b64 {%0, %1}, x; }"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 r;
+  asm("{ .reg .b64 x, y; mov.b64 x, {%2, %3}; mov.b64 y, {%4, %5};\n"
+      "add.rn.f32x2 x, x, y; mov.b64 {%0, %1}, x; }"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+constexpr uint32_t kOnes = 0x3C003C00u;   // fp16 (1, 1)
+constexpr float k2p24 = 16777216.0f;      // a code's bits as a subnormal fp16 are c * 2^-24
+// D = A B + C with C = (c0, c1, c2, c3)
+__device__ __forceinline__ void mma_from(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1, float c0, float c1, float c2, float c3) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%10,%11,%12,%13};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
+}
 
 // One query row as this lane's B fragments of each 64-group (dims 16 tig ..
 // 16 tig + 15 of the group, in the order the code words give them: (0, 4),
-// (1, 5) / 16 | (2, 6), (3, 7) / 16), the sum of the fragments' entries (the
-// bias's factor) and of the query itself, over this lane's dims.
+// (1, 5) / 16 | (2, 6), (3, 7) / 16), and the sum of the query over this lane's
+// dims.
 template <int NG>
 struct QFrag {
   uint32_t b[NG][4][2];
-  float esum[NG], qsum[NG];
+  float qsum[NG];
 };
 template <int NG>
 __device__ __forceinline__ void load_q(QFrag<NG>& f, const __half* qrow, int tig) {
 #pragma unroll
   for (int g = 0; g < NG; ++g) {
     const uint4* src = reinterpret_cast<const uint4*>(qrow + 64 * g + 16 * tig);
-    f.esum[g] = f.qsum[g] = 0.0f;
+    f.qsum[g] = 0.0f;
 #pragma unroll
     for (int w = 0; w < 2; ++w) {
       const uint4 raw = src[w];
@@ -111,17 +152,27 @@ __device__ __forceinline__ void load_q(QFrag<NG>& f, const __half* qrow, int tig
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const float2 x = unpack_h2(f.b[g][2 * w + e][0]), y = unpack_h2(f.b[g][2 * w + e][1]);
-        f.esum[g] += (x.x + x.y) + (y.x + y.y);
         f.qsum[g] += (x.x + x.y) + 16.0f * (y.x + y.y);
       }
     }
   }
 }
 
+// (scale or min) of a row's groups from a stage's array.
+template <int NG>
+__device__ __forceinline__ void read_meta(const uint8_t* arr, int t, float (&v)[NG]) {
+  if (NG == 2) {
+    const float2 x = *reinterpret_cast<const float2*>(arr + 8 * t);
+    v[0] = x.x;
+    v[NG - 1] = x.y;
+  } else {
+    v[0] = *reinterpret_cast<const float*>(arr + 4 * t);
+  }
+}
+
 // A place in the line of tiles: the item and the tile in it.
 struct Cursor {
-  int64_t left;          // tiles of the share still to come
-  int64_t seq_left;      // tiles of the sequence still to come
+  int left;              // tiles of the share still to come
   int i, h, x;           // sequence, head, tile of the item
   Seq s;
   Span span;
@@ -162,123 +213,147 @@ __global__ void __launch_bounds__(32 * kWarps, kCtasPerSm<NB>) step_kernel(const
       else hi = mid;
     }
     rd.i = lo;
-    rd.seq_left = pl.pre[lo + 1] - o0;
-    rd.left = total - o0 < per ? total - o0 : per;
+    rd.left = static_cast<int>(total - o0 < per ? total - o0 : per);
     enter(rd);
     const int64_t in = o0 - pl.pre[lo];
     rd.h = static_cast<int>(in / rd.span.n);
     rd.x = static_cast<int>(in - static_cast<int64_t>(rd.h) * rd.span.n);
   }
+  // moves on by a tile; true where a new item begins
   auto advance = [&](Cursor& c) {
     --c.left;
-    --c.seq_left;
-    if (++c.x == c.span.n) {
-      c.x = 0;
-      ++c.h;
-      if (c.seq_left == 0 && c.left > 0) {
-        do {
-          ++c.i;
-          c.seq_left = pl.pre[c.i + 1] - pl.pre[c.i];
-        } while (c.seq_left == 0);
-        c.h = 0;
-        enter(c);
-      }
+    if (++c.x < c.span.n) return false;
+    c.x = 0;
+    if (++c.h == heads && c.left > 0) {
+      do ++c.i;
+      while (pl.pre[c.i + 1] == pl.pre[c.i]);
+      c.h = 0;
+      enter(c);
     }
+    return true;
   };
-  Cursor cs = rd;                 // the tile to be computed next
-
-  // pages of the two halves of the tile at rd (-1: none, or nothing of it is seen)
-  int pg0 = -1, pg1 = -1;
+  // ---- copying ------------------------------------------------------------------
+  // A lane's pieces lie at the same places of every half tile: 16-byte pieces
+  // lane and lane + 32 of the 16 rows' codes, and piece lane % (4 NG) of the
+  // (scale or min) array lane / (4 NG).
+  const int psl = a.pool.ps_log2, psm = (1 << psl) - 1;
+  const uint32_t page_codes = static_cast<uint32_t>(heads) * static_cast<uint32_t>(St::C) << psl;   // bytes of a page
+  const uint32_t page_meta = static_cast<uint32_t>(heads) * static_cast<uint32_t>(4 * NG) << psl;
+  const bool meta_lane = lane < 16 * NG;
+  const int arr = lane / (4 * NG), mpc = lane % (4 * NG);
+  const char* const meta0 = reinterpret_cast<const char*>(arr == 0   ? a.pool.scales[0]
+                                                          : arr == 1 ? a.pool.mins[0]
+                                                          : arr == 2 ? a.pool.scales[1]
+                                                                     : a.pool.mins[1]) +
+                            16 * mpc;
+  const int meta_at = St::kKs + arr * St::kMeta + 16 * mpc;
+  const int32_t* row = nullptr;      // of the item at rd: its table row, and its head's places in a page
+  uint32_t head_codes = 0, head_meta = 0;
+  int last = 0, lo_key = 0;
+  int whole_hi = 0, whole_lo = 0, sink_hi = 0;   // a tile at t0 is seen whole iff t0 <= whole_hi and (t0 >= whole_lo or t0 <= sink_hi)
+  auto enter_item = [&]() {
+    row = a.tab.table + rd.i * a.tab.stride;
+    head_codes = (static_cast<uint32_t>(rd.h) * St::C << psl) + 16 * lane;
+    head_meta = static_cast<uint32_t>(rd.h) * (4 * NG) << psl;
+    last = min(rd.s.len, rd.s.keys) - 1;
+    lo_key = a.shape.window > 0 ? rd.s.len - rd.s.n - a.shape.window + 1 : 0;
+    whole_hi = min(rd.s.len - rd.s.n, rd.s.keys - 1) - (kTile - 1);
+    whole_lo = a.shape.window > 0 ? rd.s.len - a.shape.window : 0;
+    sink_hi = a.shape.sinks - kTile;
+  };
+  // page of the 16 tokens from t on (-1: none, or nothing of them is seen)
+  auto page_at = [&](int t) {
+    if (t > last || (t + 15 < lo_key && t >= a.shape.sinks)) return -1;
+    const int page = row[t >> psl];   // t <= last < keys: the row reaches that far
+    if (static_cast<uint32_t>(page) < static_cast<uint32_t>(a.tab.pages)) return page;
+    if (lane == 0) atomicOr(a.batch.err, DEV_ERR_PAGE);
+    return -1;
+  };
+  int pg[2] = {-1, -1};              // of the two halves of the tile at rd
+  int t_rd = 0;                      // its first token
   auto look_up = [&]() {
-    if (rd.left <= 0) return;
-    const int t0 = rd.span.tile(rd.x) << kTileLog2;
-    const int last = rd.s.len - 1 < rd.s.keys - 1 ? rd.s.len - 1 : rd.s.keys - 1;
-    const int lo = a.shape.window > 0 ? rd.s.len - rd.s.n - a.shape.window + 1 : 0;
-    auto half = [&](int t) {
-      if (t > last || (t + 15 < lo && t >= a.shape.sinks)) return -1;
-      const int page = page_of(a.tab, rd.i, t);
-      if (page < 0 && lane == 0) atomicOr(a.batch.err, DEV_ERR_PAGE);
-      return page;
-    };
-    pg0 = half(t0);
-    pg1 = half(t0 + 16);
+    t_rd = rd.span.tile(rd.x) << kTileLog2;
+    pg[0] = page_at(t_rd);
+    pg[1] = page_at(t_rd + 16);
   };
-  // copies the tile at rd into stage st, and moves rd on
-  auto issue = [&](int st) {
+  const uint32_t ring_u32 = tc::smem_u32(ring);
+  // one half's codes and (min, scale) into stage s
+  const int to0 = piece_at<D>(lane / (St::C / 16), lane % (St::C / 16)), to1 = D == 128 ? piece_at<D>(8 + lane / 4, lane % 4) : 0;
+  auto copy_half = [&](uint32_t s, int hf) {
+    const uint32_t in = static_cast<uint32_t>((t_rd + 16 * hf) & psm), page = static_cast<uint32_t>(pg[hf]);
+    const uint64_t at = static_cast<uint64_t>(page) * page_codes + (head_codes + in * St::C);
+    const uint8_t* kc = a.pool.codes[0] + at;
+    const uint8_t* vc = a.pool.codes[1] + at;
+    const uint32_t to = s + 16 * hf * St::C;
+    cp16(to + to0, kc);
+    cp16(to + St::kV + to0, vc);
+    if (D == 128) {
+      cp16(to + to1, kc + 512);
+      cp16(to + St::kV + to1, vc + 512);
+    }
+    if (meta_lane)
+      cp16(s + meta_at + hf * (64 * NG), meta0 + (static_cast<uint64_t>(page) * page_meta + (head_meta + in * (4 * NG))));
+  };
+  // copies the tile at rd into the stage at offset st, and moves rd on
+  auto issue = [&](uint32_t st) {
     if (rd.left > 0) {
-      uint8_t* s = ring + st * St::kBytes;
-      const int t0 = rd.span.tile(rd.x) << kTileLog2;
-#pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        const int page = hf ? pg1 : pg0;
-        if (page >= 0) {
-          const int64_t slot = slot_of(a.pool, page, rd.h, t0 + 16 * hf);
-          const uint8_t* kc = a.pool.codes[0] + slot * St::C + 16 * lane;
-          const uint8_t* vc = a.pool.codes[1] + slot * St::C + 16 * lane;
-#pragma unroll
-          for (int u = 0; u < D / 64; ++u) {   // 16 rows of C bytes: D / 64 pieces a lane
-            const int pc = lane + 32 * u, row = 16 * hf + pc / (St::C / 16), at = piece_at<D>(row, pc % (St::C / 16));
-            tc::cp_async16(s + at, kc + 512 * u);
-            tc::cp_async16(s + St::kV + at, vc + 512 * u);
-          }
-          // (min, scale): 16 * NG floats of each array, 4 * NG pieces
-          if (lane < 16 * NG) {
-            const int arr = lane / (4 * NG), pc = lane % (4 * NG);
-            const float* from = arr == 0 ? a.pool.scales[0] : arr == 1 ? a.pool.mins[0] : arr == 2 ? a.pool.scales[1] : a.pool.mins[1];
-            tc::cp_async16(s + St::kKs + arr * St::kMeta + hf * (64 * NG) + 16 * pc, from + slot * NG + 4 * pc);
-          }
-        }
+      if (pg[0] >= 0) copy_half(ring_u32 + st, 0);
+      if (pg[1] >= 0) copy_half(ring_u32 + st, 1);
+      if (lane == 0) {
+        const int flags = (pg[0] >= 0 ? kHalf0 : 0) | (pg[1] >= 0 ? kHalf1 : 0) | (rd.x == 0 ? kFirst : 0) |
+                          (rd.x + 1 == rd.span.n ? kLast : 0) | (rd.left == 1 ? kEnd : 0) |
+                          ((pg[0] | pg[1]) >= 0 && t_rd <= whole_hi && (t_rd >= whole_lo || t_rd <= sink_hi) ? kWhole : 0);
+        uint8_t* s = ring + st;
+        *reinterpret_cast<int4*>(s + St::kInfo) = make_int4(t_rd, flags, rd.h, rd.i);
+        *reinterpret_cast<int4*>(s + St::kInfo + 16) = make_int4(rd.s.row0, rd.s.n, rd.s.len, rd.s.keys);
       }
-      if (lane == 0) *reinterpret_cast<int*>(s + St::kInfo) = (pg0 >= 0 ? 1 : 0) | (pg1 >= 0 ? 2 : 0);
-      advance(rd);
+      if (advance(rd) && rd.left > 0) enter_item();
+      if (rd.left > 0) look_up();
     }
     tc::cp_async_commit();
-    look_up();
   };
 
   // ---- the item's state --------------------------------------------------------
   uint32_t qb[NB][NG][4][2];                     // q as B fragments (query gq of each block of 8)
-  float bias[NB][NG][2], qsum[NB][NG][2];        // of queries 2 tig, 2 tig + 1
-  float m[NB][2], l[NB][2], cmn[NB][NG][2];
+  float2 qsum[NB][NG];                           // of queries 2 tig, 2 tig + 1
+  float m[NB][2];
+  float2 l[NB], cmn[NB][NG];
   float acc[NB][NT][4];
   float cap[NG], inv[NG];                        // weights carry the factor inv = 2 / cap
-  int rows = 0, pos0 = 0;
+  uint32_t nans = 0;                             // bit 4 nb + 2 e + g: the query sees a NaN value group
+  int rows = 0;
   const float kc2 = a.scale_log2;
 
   int pn[NB][2];                                 // positions of queries 2 tig, 2 tig + 1 (none: below every key)
 
-  auto begin_item = [&]() {
-    rows = cs.s.n * a.shape.group;
-    pos0 = cs.s.len - cs.s.n;
+  auto begin_item = [&](const uint8_t* s) {
+    const int h = reinterpret_cast<const int4*>(s + St::kInfo)->z;
+    const int4 q4 = *reinterpret_cast<const int4*>(s + St::kInfo + 16);   // row0, n, len, keys
+    rows = q4.y * a.shape.group;
+    const int pos0 = q4.z - q4.y;
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
       const int n = 8 * nb + gq;
       QFrag<NG> f;
       if (n < rows) {
         const int t = n / a.shape.group;
-        load_q<NG>(f, a.q + static_cast<int64_t>(cs.s.row0 + t) * a.ldq +
-                          static_cast<int64_t>(cs.h * a.shape.group + n - t * a.shape.group) * D, tig);
+        load_q<NG>(f, a.q + static_cast<int64_t>(q4.x + t) * a.ldq +
+                          static_cast<int64_t>(h * a.shape.group + n - t * a.shape.group) * D, tig);
       } else {
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
-          f.esum[g] = f.qsum[g] = 0.0f;
+          f.qsum[g] = 0.0f;
 #pragma unroll
           for (int e = 0; e < 4; ++e) f.b[g][e][0] = f.b[g][e][1] = 0u;
         }
       }
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
-        float b = f.esum[g], s = f.qsum[g];
-        b += __shfl_xor_sync(0xffffffffu, b, 1);
-        b += __shfl_xor_sync(0xffffffffu, b, 2);
-        s += __shfl_xor_sync(0xffffffffu, s, 1);
-        s += __shfl_xor_sync(0xffffffffu, s, 2);
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          bias[nb][g][e] = 1024.0f * __shfl_sync(0xffffffffu, b, 8 * tig + 4 * e);
-          qsum[nb][g][e] = __shfl_sync(0xffffffffu, s, 8 * tig + 4 * e);
-          cmn[nb][g][e] = 0.0f;
-        }
+        float sum = f.qsum[g];
+        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+        qsum[nb][g] = make_float2(__shfl_sync(0xffffffffu, sum, 8 * tig), __shfl_sync(0xffffffffu, sum, 8 * tig + 4));
+        cmn[nb][g] = both(0.0f);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           qb[nb][g][e][0] = f.b[g][e][0];
@@ -290,143 +365,160 @@ __global__ void __launch_bounds__(32 * kWarps, kCtasPerSm<NB>) step_kernel(const
         const int k = 8 * nb + 2 * tig + e;
         pn[nb][e] = k < rows ? pos0 + k / a.shape.group : -(1 << 30);
         m[nb][e] = -INFINITY;
-        l[nb][e] = 0.0f;
       }
+      l[nb] = both(0.0f);
 #pragma unroll
       for (int i = 0; i < NT; ++i) acc[nb][i][0] = acc[nb][i][1] = acc[nb][i][2] = acc[nb][i][3] = 0.0f;
     }
 #pragma unroll
     for (int g = 0; g < NG; ++g) cap[g] = inv[g] = 0.0f;
+    nans = 0;
   };
 
-  auto compute = [&](const uint8_t* s, int tile) {
-    const int t0 = tile << kTileLog2;
-    const int present = *reinterpret_cast<const int*>(s + St::kInfo);
-    const int pl1 = cs.s.len - 1;   // the last row's position
-    // every row sees the whole tile: inside all positions, stored, and inside the window or the sinks
-    const bool whole = present == 3 && t0 + kTile - 1 <= pos0 && t0 + kTile <= cs.s.keys &&
-                       (a.shape.window == 0 || t0 > pl1 - a.shape.window || t0 + kTile <= a.shape.sinks);
-    float ks[2][2][NG], vs[2][2][NG], vm[2][2][NG];   // [16-token half][row gq, gq + 8][group]
-    float sc[NB][2][2][2];                            // [block][half][row][query]
+  auto compute = [&](uint8_t* s, int t0, int flags) {
+    float2 sc[NB][2][2];                // [block][half][row]: scores, then weights, of this lane's two queries
     const int tok = (gq >> 1) + 4 * (gq & 1);
 #pragma unroll
     for (int hf = 0; hf < 2; ++hf) {
       uint2 kw[2][NG];
-      float km[2][NG];
+      float ks[2][NG], km[2][NG];
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        const int row = 16 * hf + 8 * r + tok;
+        const int t = 16 * hf + 8 * r + tok;
 #pragma unroll
-        for (int g = 0; g < NG; ++g) {
-          kw[r][g] = *reinterpret_cast<const uint2*>(s + piece_at<D>(row, 2 * g + (tig >> 1)) + 8 * (tig & 1));
-          ks[hf][r][g] = *reinterpret_cast<const float*>(s + St::kKs + 4 * (row * NG + g));
-          km[r][g] = *reinterpret_cast<const float*>(s + St::kKm + 4 * (row * NG + g));
-          vs[hf][r][g] = *reinterpret_cast<const float*>(s + St::kVs + 4 * (row * NG + g));
-          vm[hf][r][g] = *reinterpret_cast<const float*>(s + St::kVm + 4 * (row * NG + g));
-        }
+        for (int g = 0; g < NG; ++g)
+          kw[r][g] = *reinterpret_cast<const uint2*>(s + piece_at<D>(t, 2 * g + (tig >> 1)) + 8 * (tig & 1));
+        read_meta<NG>(s + St::kKs, t, ks[r]);
+        read_meta<NG>(s + St::kKm, t, km[r]);
       }
-#pragma unroll
-      for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-        for (int r = 0; r < 2; ++r) sc[nb][hf][r][0] = sc[nb][hf][r][1] = 0.0f;
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
         float d[NB][4];
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) d[nb][0] = d[nb][1] = d[nb][2] = d[nb][3] = 0.0f;
-#pragma unroll
         for (int ww = 0; ww < 2; ++ww) {
           const uint32_t x0 = ww ? kw[0][g].y : kw[0][g].x, x1 = ww ? kw[1][g].y : kw[1][g].x;
           const uint32_t y0 = x0 >> 8, y1 = x1 >> 8;
-          const uint32_t a0 = lop_mask_or(x0, kLoNib, kMagic), a1 = lop_mask_or(x1, kLoNib, kMagic);
-          const uint32_t a2 = lop_mask_or(x0, kHiNib, kMagic), a3 = lop_mask_or(x1, kHiNib, kMagic);
-          const uint32_t b0 = lop_mask_or(y0, kLoNib, kMagic), b1 = lop_mask_or(y1, kLoNib, kMagic);
-          const uint32_t b2 = lop_mask_or(y0, kHiNib, kMagic), b3 = lop_mask_or(y1, kHiNib, kMagic);
+          const uint32_t a0 = (x0 & kLoNib), a1 = (x1 & kLoNib);
+          const uint32_t a2 = (x0 & kHiNib), a3 = (x1 & kHiNib);
+          const uint32_t b0 = (y0 & kLoNib), b1 = (y1 & kLoNib);
+          const uint32_t b2 = (y0 & kHiNib), b3 = (y1 & kHiNib);
 #pragma unroll
           for (int nb = 0; nb < NB; ++nb) {
-            mma16816(d[nb], a0, a1, a2, a3, qb[nb][g][2 * ww][0], qb[nb][g][2 * ww][1]);
+            if (ww == 0)
+              mma_from(d[nb], a0, a1, a2, a3, qb[nb][g][0][0], qb[nb][g][0][1], 0.0f, 0.0f, 0.0f, 0.0f);
+            else
+              mma16816(d[nb], a0, a1, a2, a3, qb[nb][g][2][0], qb[nb][g][2][1]);
             mma16816(d[nb], b0, b1, b2, b3, qb[nb][g][2 * ww + 1][0], qb[nb][g][2 * ww + 1][1]);
           }
         }
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-          for (int r = 0; r < 2; ++r)
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-              sc[nb][hf][r][e] = fmaf(ks[hf][r][g], d[nb][2 * r + e] - bias[nb][g][e],
-                                      fmaf(km[r][g], qsum[nb][g][e], sc[nb][hf][r][e]));
+          for (int r = 0; r < 2; ++r) {
+            const float2 base = g == 0 ? mul2(both(km[r][0]), qsum[nb][0]) : fma2(both(km[r][g]), qsum[nb][g], sc[nb][hf][r]);
+            sc[nb][hf][r] = fma2(both(ks[r][g] * k2p24), make_float2(d[nb][2 * r], d[nb][2 * r + 1]), base);
+          }
       }
     }
+    // scale or minimum of this lane's value token of half hf, row r
+    auto value_meta = [&](uint8_t* arr, int hf, int r, int g) {
+      return reinterpret_cast<float*>(arr) + (16 * hf + 8 * r + tok) * NG + g;
+    };
     uint32_t seen = 0xffffffffu;   // bit 8 nb + 4 hf + 2 r + e: the query sees the token
-    if (!whole) {                  // a row or a token at the edge
+    if (!(flags & kWhole)) {       // a row or a token at the edge
       seen = 0;
+      const int keys = reinterpret_cast<const int4*>(s + St::kInfo + 16)->w;
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf)
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
           const int j = t0 + 16 * hf + 8 * r + tok;
-          const bool here = ((present >> hf) & 1) && j < cs.s.keys;
-          bool any = false;
+          const bool here = ((flags >> hf) & 1) && j < keys;
 #pragma unroll
           for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               const int p = pn[nb][e];
               const bool see = here && j <= p && (a.shape.window == 0 || j > p - a.shape.window || j < a.shape.sinks);
-              if (!see) sc[nb][hf][r][e] = -INFINITY;
+              if (!see) (e ? sc[nb][hf][r].y : sc[nb][hf][r].x) = -INFINITY;
               seen |= (see ? 1u : 0u) << (8 * nb + 4 * hf + 2 * r + e);
-              any |= see;
             }
-          // scale and minimum of a token that no query of this lane sees may be anything
-          if (!any)
+          // what was not copied may be anything: its values count as zeros
+          if (!here && tig == 0)
 #pragma unroll
-            for (int g = 0; g < NG; ++g) vs[hf][r][g] = vm[hf][r][g] = 0.0f;
+            for (int g = 0; g < NG; ++g) *value_meta(s + St::kVs, hf, r, g) = *value_meta(s + St::kVm, hf, r, g) = 0.0f;
         }
+      __syncwarp();
     }
-    // the weights' factor: a power of two that keeps max scale * factor in [1, 2)
+    // The weights' factor: a power of two that keeps max scale * factor in [1,
+    // 2).  A group whose scale is not finite stands for NaN: it is noted for
+    // the queries that see it and leaves the sums.
+    float vs_all[2][2][NG];
+#pragma unroll
+    for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+      for (int r = 0; r < 2; ++r) read_meta<NG>(s + St::kVs, 16 * hf + 8 * r + tok, vs_all[hf][r]);
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
-      float mx = 0.0f;
+      float vs[2][2];
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf)
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          if (!(vs[hf][r][g] < INFINITY)) vs[hf][r][g] = __uint_as_float(0x7fffffffu);   // such a group is NaN
-          mx = fmaxf(mx, vs[hf][r][g]);
-        }
-      if (__any_sync(0xffffffffu, mx >= cap[g])) {
+        for (int r = 0; r < 2; ++r) vs[hf][r] = vs_all[hf][r][g];
+      if (__any_sync(0xffffffffu, !(max_nan(max_nan(vs[0][0], vs[0][1]), max_nan(vs[1][0], vs[1][1])) < cap[g]))) {
+        float mx = 0.0f;
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            uint32_t mine = 0;   // this lane's queries that see the token
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) mine |= ((seen >> (8 * nb + 4 * hf + 2 * r)) & 3u) << (2 * nb);
+            if (!(vs[hf][r] < INFINITY)) {   // its values count as zeros from here on
+              vs[hf][r] = 0.0f;
+              if (tig == 0) *value_meta(s + St::kVs, hf, r, g) = *value_meta(s + St::kVm, hf, r, g) = 0.0f;
+#pragma unroll
+              for (int k = 0; k < 2 * NB; ++k)
+                if ((mine >> k) & 1u) nans |= 1u << (2 * k + g);
+            }
+            mx = fmaxf(mx, vs[hf][r]);
+          }
+        __syncwarp();
         const uint32_t bits = __reduce_max_sync(0xffffffffu, __float_as_uint(mx));
-        const int e = static_cast<int>(bits >> 23) > 1 ? static_cast<int>(bits >> 23) : 1;   // biased exponent
-        const float ncap = e >= 253 ? 1.7e38f : __uint_as_float(static_cast<uint32_t>(e + 1) << 23);
-        const float ninv = __uint_as_float(static_cast<uint32_t>(254 - (e >= 253 ? 253 : e)) << 23);
-        if (inv[g] != 0.0f) {
-          const float f = ninv / inv[g];
+        const uint32_t e = min(max(bits >> 23, 1u), 253u);   // biased exponent
+        const float ncap = __uint_as_float((e + 1) << 23), ninv = __uint_as_float((254u - e) << 23);
+        if (ncap > cap[g]) {
+          if (inv[g] != 0.0f) {
+            const float f = ninv / inv[g];
 #pragma unroll
-          for (int nb = 0; nb < NB; ++nb)
+            for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-            for (int i = 4 * g; i < 4 * g + 4; ++i)
+              for (int i = 4 * g; i < 4 * g + 4; ++i)
 #pragma unroll
-              for (int e4 = 0; e4 < 4; ++e4) acc[nb][i][e4] *= f;
+                for (int e4 = 0; e4 < 4; ++e4) acc[nb][i][e4] *= f;
+          }
+          cap[g] = ncap;
+          inv[g] = ninv;
         }
-        cap[g] = ncap;
-        inv[g] = ninv;
       }
     }
     // maxima: of this lane's tokens, then over the lanes of a query
     bool grow = false;
     float nm[NB][2];
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb)
+    for (int nb = 0; nb < NB; ++nb) {
+      float x = fmaxf(fmaxf(sc[nb][0][0].x, sc[nb][0][1].x), fmaxf(sc[nb][1][0].x, sc[nb][1][1].x));
+      float y = fmaxf(fmaxf(sc[nb][0][0].y, sc[nb][0][1].y), fmaxf(sc[nb][1][0].y, sc[nb][1][1].y));
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float x = fmaxf(fmaxf(sc[nb][0][0][e], sc[nb][0][1][e]), fmaxf(sc[nb][1][0][e], sc[nb][1][1][e]));
-        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
-        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
-        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-        nm[nb][e] = x;
-        grow |= (x - m[nb][e]) * kc2 > kGrow;   // -inf - -inf: no
+      for (int o = 4; o < 32; o <<= 1) {
+        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+        y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, o));
       }
+      nm[nb][0] = x;
+      nm[nb][1] = y;
+      grow |= (x - m[nb][0]) * kc2 > kGrow;   // -inf - -inf: no
+      grow |= (y - m[nb][1]) * kc2 > kGrow;
+    }
     if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
@@ -436,10 +528,11 @@ __global__ void __launch_bounds__(32 * kWarps, kCtasPerSm<NB>) step_kernel(const
           const float x = fmaxf(m[nb][e], nm[nb][e]);
           al[e] = x == -INFINITY ? 1.0f : ex2((m[nb][e] - x) * kc2);
           m[nb][e] = x;
-          l[nb][e] *= al[e];
-#pragma unroll
-          for (int g = 0; g < NG; ++g) cmn[nb][g][e] *= al[e];
         }
+        const float2 f = make_float2(al[0], al[1]);
+        l[nb] = mul2(l[nb], f);
+#pragma unroll
+        for (int g = 0; g < NG; ++g) cmn[nb][g] = mul2(cmn[nb][g], f);
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
           acc[nb][i][0] *= al[0];
@@ -449,94 +542,130 @@ __global__ void __launch_bounds__(32 * kWarps, kCtasPerSm<NB>) step_kernel(const
         }
       }
     }
-    // weights, and the values' products
+    // weights
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
-      const float mc0 = m[nb][0] == -INFINITY ? 0.0f : m[nb][0] * kc2, mc1 = m[nb][1] == -INFINITY ? 0.0f : m[nb][1] * kc2;
+      const float2 neg = make_float2(m[nb][0] == -INFINITY ? 0.0f : -m[nb][0] * kc2, m[nb][1] == -INFINITY ? 0.0f : -m[nb][1] * kc2);
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf)
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          sc[nb][hf][r][0] = ex2(fmaf(sc[nb][hf][r][0], kc2, -mc0));
-          sc[nb][hf][r][1] = ex2(fmaf(sc[nb][hf][r][1], kc2, -mc1));
-          l[nb][0] += sc[nb][hf][r][0];
-          l[nb][1] += sc[nb][hf][r][1];
+          const float2 x = fma2(sc[nb][hf][r], both(kc2), neg);
+          sc[nb][hf][r] = make_float2(ex2(x.x), ex2(x.y));
+          l[nb] = add2(l[nb], sc[nb][hf][r]);
         }
     }
+    float vf[2][2][NG], mid[2][2][NG];   // factor of p in the weights, value of the centre code
 #pragma unroll
     for (int hf = 0; hf < 2; ++hf)
 #pragma unroll
-      for (int g = 0; g < NG; ++g) {
-        uint32_t vb[NB][2];
+      for (int r = 0; r < 2; ++r) {
+        read_meta<NG>(s + St::kVs, 16 * hf + 8 * r + tok, vf[hf][r]);
+        read_meta<NG>(s + St::kVm, 16 * hf + 8 * r + tok, mid[hf][r]);
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const float f = vs[hf][r][g] * inv[g], mid = fmaf(8.0f, vs[hf][r][g], vm[hf][r][g]);
-#pragma unroll
-          for (int nb = 0; nb < NB; ++nb) {
-            float w0 = sc[nb][hf][r][0] * f, w1 = sc[nb][hf][r][1] * f;
-            float c0 = sc[nb][hf][r][0] * mid, c1 = sc[nb][hf][r][1] * mid;
-            if (!whole) {   // a NaN group reaches only the queries that see it
-              const int bit = 8 * nb + 4 * hf + 2 * r;
-              w0 = (seen >> bit) & 1u ? w0 : 0.0f;
-              c0 = (seen >> bit) & 1u ? c0 : 0.0f;
-              w1 = (seen >> (bit + 1)) & 1u ? w1 : 0.0f;
-              c1 = (seen >> (bit + 1)) & 1u ? c1 : 0.0f;
-            }
-            cmn[nb][g][0] += c0;
-            cmn[nb][g][1] += c1;
-            vb[nb][r] = movmatrix_trans(pack_h2(w0, w1));
-          }
-        }
-        uint32_t vw[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int row = 16 * hf + 4 * k + tig;
-          vw[k] = *reinterpret_cast<const uint32_t*>(s + St::kV + piece_at<D>(row, 2 * g + (gq >> 2)) + 4 * (gq & 3));
-        }
-#pragma unroll
-        for (int ii = 0; ii < 4; ++ii) {
-          const uint32_t sel = static_cast<uint32_t>(ii) | (static_cast<uint32_t>(ii + 4) << 8);
-          const uint32_t x01 = __byte_perm(vw[0], vw[1], sel), x89 = __byte_perm(vw[2], vw[3], sel);
-          const uint32_t a0 = hfma2(lop_mask_or(x01, kLoNib, kMagic), kOne2, kNeg1032);
-          const uint32_t a1 = hfma2(lop_mask_or(x01, kHiNib, kMagic), kSixteenth2, kNeg72);
-          const uint32_t a2 = hfma2(lop_mask_or(x89, kLoNib, kMagic), kOne2, kNeg1032);
-          const uint32_t a3 = hfma2(lop_mask_or(x89, kHiNib, kMagic), kSixteenth2, kNeg72);
-#pragma unroll
-          for (int nb = 0; nb < NB; ++nb) mma16816(acc[nb][4 * g + ii], a0, a1, a2, a3, vb[nb][0], vb[nb][1]);
+        for (int g = 0; g < NG; ++g) {
+          mid[hf][r][g] = fmaf(8.0f, vf[hf][r][g], mid[hf][r][g]);
+          vf[hf][r][g] *= inv[g];
         }
       }
+    // the values' products, group by group: the two halves' weights as B
+    // fragments, their sums, then the codes
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+      constexpr float lo = -8.0f / k2p24, hi = -128.0f / k2p24;
+      uint32_t vb[NB][2][2];
+      float ps[NB][4];
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) {
+            const float2 wt = mul2(sc[nb][hf][r], both(vf[hf][r][g]));
+            cmn[nb][g] = fma2(sc[nb][hf][r], both(mid[hf][r][g]), cmn[nb][g]);
+            vb[nb][hf][r] = movmatrix_trans(pack_h2(wt.x, wt.y));
+          }
+        }
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+          if (hf == 0) mma_from(ps[nb], kOnes, kOnes, kOnes, kOnes, vb[nb][0][0], vb[nb][0][1], 0.0f, 0.0f, 0.0f, 0.0f);
+          else mma16816(ps[nb], kOnes, kOnes, kOnes, kOnes, vb[nb][1][0], vb[nb][1][1]);
+        }
+      }
+      uint32_t vw[2][4];
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          vw[hf][k] = *reinterpret_cast<const uint32_t*>(s + St::kV + piece_at<D>(16 * hf + 4 * k + tig, 2 * g + (gq >> 2)) + 4 * (gq & 3));
+#pragma unroll
+      for (int ii = 0; ii < 4; ++ii) {
+        const uint32_t sel = static_cast<uint32_t>(ii) | (static_cast<uint32_t>(ii + 4) << 8);
+        float d[NB][4];
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          const uint32_t x01 = __byte_perm(vw[hf][0], vw[hf][1], sel), x89 = __byte_perm(vw[hf][2], vw[hf][3], sel);
+          const uint32_t a0 = x01 & kLoNib, a1 = x01 & kHiNib;
+          const uint32_t a2 = x89 & kLoNib, a3 = x89 & kHiNib;
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) {
+            if (hf == 0)
+              mma_from(d[nb], a0, a1, a2, a3, vb[nb][0][0], vb[nb][0][1], lo * ps[nb][0], lo * ps[nb][1], hi * ps[nb][0],
+                       hi * ps[nb][1]);
+            else
+              mma16816(d[nb], a0, a1, a2, a3, vb[nb][1][0], vb[nb][1][1]);
+          }
+        }
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+          float (&o)[4] = acc[nb][4 * g + ii];
+          const float2 u = add2(make_float2(o[0], o[1]), make_float2(d[nb][0], d[nb][1]));
+          const float2 v = add2(make_float2(o[2], o[3]), make_float2(d[nb][2], d[nb][3]));
+          o[0] = u.x;
+          o[1] = u.y;
+          o[2] = v.x;
+          o[3] = v.y;
+        }
+      }
+    }
   };
   // the item's rows, finished (one share) or as this share's partial
-  auto end_item = [&](bool from_start, bool to_end) {
+  auto end_item = [&](const uint8_t* s, bool from_start, bool to_end) {
+    const int h = reinterpret_cast<const int4*>(s + St::kInfo)->z, row0 = reinterpret_cast<const int4*>(s + St::kInfo + 16)->x;
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) nans |= __shfl_xor_sync(0xffffffffu, nans, o);
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
+        float lsum = e ? l[nb].y : l[nb].x, cm[NG];
+#pragma unroll
+        for (int g = 0; g < NG; ++g) cm[g] = e ? cmn[nb][g].y : cmn[nb][g].x;
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) {
-          l[nb][e] += __shfl_xor_sync(0xffffffffu, l[nb][e], o);
+          lsum += __shfl_xor_sync(0xffffffffu, lsum, o);
 #pragma unroll
-          for (int g = 0; g < NG; ++g) cmn[nb][g][e] += __shfl_xor_sync(0xffffffffu, cmn[nb][g][e], o);
+          for (int g = 0; g < NG; ++g) cm[g] += __shfl_xor_sync(0xffffffffu, cm[g], o);
         }
         const int n = 8 * nb + 2 * tig + e;
         if (n >= rows) continue;
-        const float lsum = l[nb][e];
         const bool whole = from_start && to_end;
         const float f = !whole ? 1.0f : lsum == 0.0f ? 0.0f : 1.0f / lsum;
         float v[NG][8];
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
-          const float un = inv[g] != 0.0f ? 1.0f / inv[g] : 0.0f;
+          const float un = inv[g] != 0.0f ? k2p24 / inv[g] : 0.0f;   // powers of two
+          if ((nans >> (4 * nb + 2 * e + g)) & 1u) cm[g] = __uint_as_float(0x7fffffffu);
 #pragma unroll
           for (int ii = 0; ii < 4; ++ii) {
-            v[g][2 * ii] = fmaf(acc[nb][4 * g + ii][e], un, cmn[nb][g][e]) * f;
-            v[g][2 * ii + 1] = fmaf(acc[nb][4 * g + ii][2 + e], un, cmn[nb][g][e]) * f;
+            v[g][2 * ii] = fmaf(acc[nb][4 * g + ii][e], un, cm[g]) * f;
+            v[g][2 * ii + 1] = fmaf(acc[nb][4 * g + ii][2 + e], 0.0625f * un, cm[g]) * f;
           }
         }
         if (whole) {
           const int t = n / a.shape.group;
-          __half* dst = a.out + static_cast<int64_t>(cs.s.row0 + t) * a.ldo +
-                        static_cast<int64_t>(cs.h * a.shape.group + n - t * a.shape.group) * D + 8 * gq;
+          __half* dst = a.out + static_cast<int64_t>(row0 + t) * a.ldo +
+                        static_cast<int64_t>(h * a.shape.group + n - t * a.shape.group) * D + 8 * gq;
 #pragma unroll
           for (int g = 0; g < NG; ++g)
             *reinterpret_cast<uint4*>(dst + 64 * g) = make_uint4(pack_h2(v[g][0], v[g][1]), pack_h2(v[g][2], v[g][3]),
@@ -555,33 +684,37 @@ __global__ void __launch_bounds__(32 * kWarps, kCtasPerSm<NB>) step_kernel(const
   };
 
   // ---- the share ------------------------------------------------------------------
+  enter_item();
   look_up();
 #pragma unroll
-  for (int st = 0; st < kStages - 1; ++st) issue(st);
+  for (int st = 0; st < kStages - 1; ++st) issue(st * St::kBytes);
   int4 rec = make_int4(-1, 0, 0, 0);
-  bool from_start = cs.x == 0;
-  begin_item();
-  for (int j = 0; cs.left > 0; ++j) {
-    issue((j + kStages - 1) % kStages);   // that stage was read in the round before, which ended in a warp barrier
+  bool fresh = true, from_start = false;
+  uint32_t st_rd = (kStages - 1) * St::kBytes, st_cs = 0;
+  while (true) {
+    issue(st_rd);                         // that stage was read in the round before, which ended in a warp barrier
+    st_rd = st_rd == (kStages - 1) * St::kBytes ? 0 : st_rd + St::kBytes;
     tc::cp_async_wait<kStages - 1>();     // this lane's copies of the tile have landed
     __syncwarp();                         // and every lane's
-    compute(ring + (j % kStages) * St::kBytes, cs.span.tile(cs.x));
-    __syncwarp();
-    const bool to_end = cs.x + 1 == cs.span.n;
-    if (to_end || cs.left == 1) {
-      end_item(from_start, to_end);
-      if (from_start && !to_end) {
-        const int64_t start = pl.pre[cs.i] + static_cast<int64_t>(cs.h) * cs.span.n;
-        rec = make_int4(cs.i, cs.h, 0, static_cast<int>((start + cs.span.n - 1) / per));
-      }
-      advance(cs);
-      if (cs.left > 0) {
-        from_start = true;
-        begin_item();
-      }
-    } else {
-      advance(cs);
+    uint8_t* s = ring + st_cs;
+    st_cs = st_cs == (kStages - 1) * St::kBytes ? 0 : st_cs + St::kBytes;
+    const int4 info = *reinterpret_cast<const int4*>(s + St::kInfo);
+    if (fresh) {
+      from_start = info.y & kFirst;
+      begin_item(s);
     }
+    compute(s, info.x, info.y);
+    fresh = info.y & (kLast | kEnd);
+    if (fresh) {
+      const bool to_end = info.y & kLast;
+      end_item(s, from_start, to_end);
+      if (from_start && !to_end) {
+        const int64_t cost = (pl.pre[info.w + 1] - pl.pre[info.w]) / heads;   // of the item
+        rec = make_int4(info.w, info.z, 0, static_cast<int>((pl.pre[info.w] + (info.z + 1) * cost - 1) / per));
+      }
+    }
+    __syncwarp();
+    if (info.y & kEnd) break;
   }
   if (lane == 0) pl.rec[w] = rec;
 }
