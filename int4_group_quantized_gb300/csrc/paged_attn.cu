@@ -41,7 +41,6 @@ __global__ void __launch_bounds__(128) attn_rows_kernel(const AttnArgs<T> a) {
     return;
   }
   const int64_t pos = static_cast<int64_t>(s.len) - s.n + (r - s.row0);
-  if (static_cast<int64_t>(s.n) * a.shape.group <= a.shape.skip) return;   // taken by the step kernel
   const int64_t lo = a.shape.window > 0 && pos - a.shape.window + 1 > 0 ? pos - a.shape.window + 1 : 0;
   float q[E], o[E];
 #pragma unroll
@@ -176,9 +175,9 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
           longest[0] = max(longest[0], sp.n);
         } else if (rows > 0 && a.tile.workers > 0) {
           tall = true;
-          // the last unit sees the most tiles
+          // the last unit sees the most tiles, but for a few where it is short and a window cuts them all
           const Unit x = unit_of<TRU>(s, a.shape.group, static_cast<int>((rows - 1) / TRU));
-          longest[1] = max(longest[1], span_of<TKTL>(x.p0, x.p1, s.keys, a.shape.window, a.shape.sinks).n + 1);
+          longest[1] = max(longest[1], span_of<TKTL>(x.p0, x.p1, s.keys, a.shape.window, a.shape.sinks).n + 4);
         }
       }
       uint32_t todo = __ballot_sync(0xffffffffu, tall);
@@ -219,7 +218,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
 }
 
 // ---- joining the partials of items that cross shares ------------------------------
-// Block w joins the item that begins in share w and ends later: the partials
+// Block (w, y) joins rows 16 y .. of the item that begins in share w and ends later: the partials
 // lie in slot 1 of w and slot 0 of the shares after it.  The factors of all
 // (share, row) first, then the sums: a warp per row and part of the shares,
 // four columns a lane, the parts added in order (the same bits every time).
@@ -241,7 +240,8 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const AttnArgs<T>
   const Unit x = unit_of<RU>(s, a.shape.group, rec.z);
   const int shares = rec.w - w + 1;
   auto slot = [&](int k, int n) { return (static_cast<int64_t>(w + k) * 2 + (k == 0 ? 1 : 0)) * pl.rows + n; };
-  for (int n0 = 0; n0 < x.rows; n0 += kRows) {
+  const int n0 = blockIdx.y * kRows;
+  if (n0 < x.rows) {
     const int rows = min(kRows, x.rows - n0);
     for (int n = warp; n < rows; n += kJoinWarps) {
       float m = -INFINITY;
@@ -305,7 +305,6 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const AttnArgs<T>
         put(dst + 3, o.w * f);
       }
     }
-    __syncthreads();
   }
 }
 
@@ -316,7 +315,7 @@ fg_status join(const AttnArgs<T>& a, const ClassPlan& pl, cudaStream_t st) {
   pdl[0].val.programmaticStreamSerializationAllowed = 1;
   Trace tr(KC_ATTN_COMBINE, st);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(pl.workers));
+  cfg.gridDim = dim3(static_cast<unsigned>(pl.workers), static_cast<unsigned>((pl.rows + 15) / 16));
   cfg.blockDim = dim3(32 * kJoinWarps);
   cfg.stream = st;
   cfg.attrs = pdl;
@@ -359,6 +358,8 @@ Layout layout_of(const fg_page_pool& pool, const fg_page_table& t, int32_t q_hea
     const int rows = most <= 8 ? 8 : kStepRows;
     carve_class(l.step, p, t.seqs, pool.head_dim, step_workers(rows, sms), step_workers(rows, kMaxSms), rows);
   }
+  if (pool.dtype == FG_F16 && most > (l.step.workers ? kStepRows : 0))
+    carve_class(l.tile, p, t.seqs, pool.head_dim, sms, kMaxSms, kTileRows);
   l.bytes = static_cast<size_t>(p - static_cast<char*>(ws)) + 256;
   return l;
 }
@@ -385,29 +386,32 @@ fg_status launch_attn(const fg_page_pool& pool, const fg_page_table& t, const in
   a.shape.window = window > (int64_t(1) << 30) ? 0 : static_cast<int>(window);
   a.shape.sinks = static_cast<int>(std::min<int64_t>(sinks, int64_t(1) << 30));
   const Layout l = layout_of(pool, t, q_heads, max_q, ws, std::min(num_sms(), kMaxSms));
-  const bool tall = max_q * a.shape.group > kStepRows || l.step.workers == 0;
-  a.shape.skip = l.step.workers > 0 ? kStepRows : 0;
-  if (l.step.workers > 0) {
+  if constexpr (sizeof(T) == 2) {
     PlanArgs p{a.tab, a.batch, a.shape, pool.heads, l.step, l.tile};
     {
       Trace tr(KC_ATTN_PAGED_PLAN, st);
-      const unsigned threads = static_cast<unsigned>(std::min<int64_t>(1024, (t.seqs + 31) / 32 * 32));
-      plan_kernel<256, 7, 1><<<1, threads, 0, st>>>(p);
+      const unsigned threads = static_cast<unsigned>(std::min<int64_t>(kPlanThreads, (t.seqs + 31) / 32 * 32));
+      plan_kernel<kTileRows, 7, 1><<<1, threads, 0, st>>>(p);
       FG_TRY(check_launch("plan_kernel"));
     }
-    if constexpr (sizeof(T) == 2) {
+    const bool wide = pool.head_dim == 128;
+    if (l.step.workers > 0) {
       FG_TRY(paged_attention_step(a, l.step, pool.head_dim, st));
-      if (pool.head_dim == 128) FG_TRY((join<T, 128, kStepRows>(a, l.step, st)));
-      else FG_TRY((join<T, 64, kStepRows>(a, l.step, st)));
+      FG_TRY((wide ? join<T, 128, kStepRows>(a, l.step, st) : join<T, 64, kStepRows>(a, l.step, st)));
     }
+    if (l.tile.workers > 0) {
+      FG_TRY(paged_attention_tile(a, l.tile, pool.head_dim, st));
+      FG_TRY((wide ? join<T, 128, kTileRows>(a, l.tile, st) : join<T, 64, kTileRows>(a, l.tile, st)));
+    }
+    return FG_OK;
+  } else {
+    const int64_t warps = ntok * q_heads;
+    const unsigned grid = static_cast<unsigned>((warps + 3) / 4);
+    Trace tr(KC_ATTN_PAGED, st);
+    if (pool.head_dim == 128) attn_rows_kernel<T, 128><<<grid, 128, 0, st>>>(a);
+    else attn_rows_kernel<T, 64><<<grid, 128, 0, st>>>(a);
+    return check_launch("attn_rows_kernel");
   }
-  if (!tall) return FG_OK;
-  const int64_t warps = ntok * q_heads;
-  const unsigned grid = static_cast<unsigned>((warps + 3) / 4);
-  Trace tr(KC_ATTN_PAGED, st);
-  if (pool.head_dim == 128) attn_rows_kernel<T, 128><<<grid, 128, 0, st>>>(a);
-  else attn_rows_kernel<T, 64><<<grid, 128, 0, st>>>(a);
-  return check_launch("attn_rows_kernel");
 }
 
 fg_status check_attn(const fg_page_pool* pool, const fg_page_table* t, int32_t q_heads, int64_t ntok, int64_t max_q) {

@@ -24,5 +24,10 @@ struct AttnArgs {
 int step_workers(int rows, int sms);
 fg_status paged_attention_step(const AttnArgs<__half>& a, const ClassPlan& pl, int head_dim, cudaStream_t st);
 
+
+// Longer chunks (fp16) on tcgen05, units of kTileRows rows and tiles of 128 keys; one worker an SM.
+constexpr int kTileRows = 256;
+fg_status paged_attention_tile(const AttnArgs<__half>& a, const ClassPlan& pl, int head_dim, cudaStream_t st);
+
 }  // namespace paged
 }  // namespace fg

@@ -28,7 +28,6 @@ struct AttnShape {
   int group;            // query heads per K/V head
   int max_q;
   int window, sinks;    // window 0: none; both at most 2^30
-  int skip;             // sequences of at most this many rows are another kernel's
 };
 
 // What a class of items shares: header and prefix sums written by the plan.

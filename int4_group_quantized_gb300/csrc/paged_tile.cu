@@ -1,0 +1,621 @@
+// Paged attention of chunks on tcgen05 (FlexGen notes, "背景知识": Softmax(x_Q
+// x_K^T / sqrt(h1)) x_V per head, causal; "5. 近似方法": K and V stored in
+// 4-bit groups of 64 and converted back to FP16), fp16 activations, sequences
+// of more than 16 rows per K/V head.
+//
+// A unit is 256 rows (token t, query head g of the K/V head's group: row t *
+// group + g), so that every restored K/V tile of 128 keys feeds two MMA tiles
+// of 128 rows; one persistent CTA per SM walks its share of the line of tiles
+// (paged_sched.cuh).  Roles:
+//   * four warps restore: a thread owns one key of the tile, takes its K and V
+//     codes (loaded into registers a tile ahead, the page number another tile
+//     ahead) through fp16(fmaf(q, scale, min)) -- exact fp32 codes by
+//     mixed-precision adds, one paired fp32 FMA, one rounding -- into the
+//     128-byte-swizzled rows the MMA reads (K: K-major panels, V: MN-major
+//     blocks; the same bytes).  A pair of a code word's halves holds dims (0,
+//     4), (1, 5), (2, 6), (3, 7); Q is laid out in the same order and O is
+//     taken apart in it;
+//   * two groups of four softmax warps (one row a thread) keep the running
+//     maximum and sum in base 2, write P (fp16) into tensor memory as the
+//     second MMA's A operand, rescale O there only when a row's maximum grew
+//     by more than 2^8, and finish or hand on a share's rows;
+//   * one thread issues S = Q K^T (M = N = 128) and O += P V for both groups in
+//     turn, so that one group's softmax runs under the other's MMAs.
+// Tensor memory: S of each group, O of each group, and P: in the columns of its
+// S at head_dim 128 (S of the next tile is issued after the P V that reads it,
+// in the order of one thread's MMAs of one shape), in columns of its own at 64.
+//
+// Rows see a key by position alone, so masks are words of bits per row, made
+// only for tiles at an edge.  A V group that restores to NaN enters the product
+// as zeros and is remembered for the rows that see it (0 * NaN would reach all).
+// Every wait is bounded; on timeout the CTA raises the device error word, lets
+// its MMAs finish and frees its tensor memory.
+#include <math.h>
+
+#include <algorithm>
+
+#include "paged_attn.cuh"
+#include "q4_dev.cuh"
+#include "tc_ptx.cuh"
+
+namespace fg {
+namespace paged {
+namespace {
+
+using namespace tc;
+
+constexpr int kKeysLog2 = 7;
+constexpr int kKeys = 1 << kKeysLog2;
+constexpr int kRows = kTileRows;
+constexpr int kSoftWarps = 8;      // warps 0..3: rows 0..127, warps 4..7: rows 128..255
+constexpr int kRestoreWarps = 4;   // warps 8..11
+constexpr int kMmaWarp = 12;
+constexpr int kThreads = 13 * 32;
+constexpr float kRescale = 8.0f;
+
+template <int D>
+struct Smem {
+  static constexpr int kPanels = D / 64;
+  static constexpr int kPanel = 128 * 128;              // 128 rows of 128 bytes
+  static constexpr int kQ = kPanels * kPanel;           // one group's
+  static constexpr int kK = kPanels * kPanel;
+  static constexpr int kStage = 2 * kK;                 // K, then V
+  static constexpr int kFlags = 3 * 16;                 // per stage: absent keys, NaN value groups 0 and 1 (128 bits each)
+  static constexpr int kBytes = 1024 + 2 * kQ + 2 * kStage + 2 * kFlags + 256;
+  static_assert(kBytes <= 232448, "shared memory of one CTA");
+};
+
+// A share's walk over its segments: parts of one unit's key tiles.
+struct Walk {
+  int left;              // tiles of the share still to come
+  int i, h, u, x;        // sequence, head, unit, tile of the unit
+  int units;
+  Seq s;
+  Unit un;
+  Span sp;
+  int x1;                // the current segment: tiles x .. x1 - 1
+};
+__device__ __forceinline__ void walk_unit(Walk& k, const AttnArgs<__half>& a) {
+  k.un = unit_of<kRows>(k.s, a.shape.group, k.u);
+  k.sp = span_of<kKeysLog2>(k.un.p0, k.un.p1, k.s.keys, a.shape.window, a.shape.sinks);
+}
+__device__ __forceinline__ void walk_seq(Walk& k, const AttnArgs<__half>& a) {
+  k.s = seq_of(a.tab, a.batch, k.i);
+  k.units = static_cast<int>((static_cast<int64_t>(k.s.n) * a.shape.group + kRows - 1) / kRows);
+  k.u = 0;
+}
+// Share w's first segment (left = 0: none).
+__device__ __forceinline__ void walk_begin(Walk& k, const AttnArgs<__half>& a, const ClassPlan& pl, int w) {
+  const int64_t total = pl.head[0], per = pl.head[1], o0 = w * per;
+  k.left = 0;
+  if (o0 >= total) return;
+  int lo = 0, hi = a.tab.seqs;   // pre[lo] <= o0 < pre[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (pl.pre[mid] <= o0) lo = mid;
+    else hi = mid;
+  }
+  k.i = lo;
+  k.left = static_cast<int>(total - o0 < per ? total - o0 : per);
+  walk_seq(k, a);
+  const int64_t cost = (pl.pre[lo + 1] - pl.pre[lo]) / a.pool.heads, in = o0 - pl.pre[lo];
+  k.h = static_cast<int>(in / cost);
+  int64_t rest = in - k.h * cost;
+  walk_unit(k, a);
+  while (rest >= k.sp.n) {
+    rest -= k.sp.n;
+    ++k.u;
+    walk_unit(k, a);
+  }
+  k.x = static_cast<int>(rest);
+  k.x1 = k.x + (k.left < k.sp.n - k.x ? k.left : k.sp.n - k.x);
+}
+// On to the next segment.
+__device__ __forceinline__ void walk_next(Walk& k, const AttnArgs<__half>& a, const ClassPlan& pl) {
+  k.left -= k.x1 - k.x;
+  if (k.left == 0) return;
+  if (++k.u == k.units) {
+    k.u = 0;
+    if (++k.h == a.pool.heads) {
+      do ++k.i;
+      while (pl.pre[k.i + 1] == pl.pre[k.i]);
+      k.h = 0;
+      walk_seq(k, a);
+    }
+  }
+  walk_unit(k, a);
+  k.x = 0;
+  k.x1 = k.left < k.sp.n ? k.left : k.sp.n;
+}
+
+__device__ __forceinline__ float ex2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float2 add_f32x2(float2 a, float2 b) {
+  float2 r;
+  asm("{ .reg .b64 x, y; mov.b64 x, {%2, %3}; mov.b64 y, {%4, %5};\n"
+      "add.rn.f32x2 x, x, y; mov.b64 {%0, %1}, x; }"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+// Bits c of a word with c < n, for any n.
+__device__ __forceinline__ uint32_t bits_below(int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; }
+
+// 64 codes (32 bytes) of one group through fp16(fmaf(q, scale, min)) into row
+// r of a swizzled panel.
+__device__ __forceinline__ void restore_group(const uint4& lo, const uint4& hi, float scale, float mn, uint8_t* prow, int r) {
+  const float2 s2 = make_float2(scale, scale), m2 = make_float2(mn, mn);
+  const uint32_t words[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+  for (int c = 0; c < 8; ++c) {
+    const uint32_t x = words[c], y = x >> 8;
+    uint4 o;
+    o.x = q4::cvt_f16x2(q4::fma_f32x2(q4::nib_pair_f32(q4::lop_mask_or(x, 0x000F000Fu, q4::kMagic)), s2, m2));
+    o.y = q4::cvt_f16x2(q4::fma_f32x2(q4::nib16_pair_f32(q4::lop_mask_or(x, 0x00F000F0u, q4::kMagic)), s2, m2));
+    o.z = q4::cvt_f16x2(q4::fma_f32x2(q4::nib_pair_f32(q4::lop_mask_or(y, 0x000F000Fu, q4::kMagic)), s2, m2));
+    o.w = q4::cvt_f16x2(q4::fma_f32x2(q4::nib16_pair_f32(q4::lop_mask_or(y, 0x00F000F0u, q4::kMagic)), s2, m2));
+    *reinterpret_cast<uint4*>(prow + ((c ^ (r & 7)) << 4)) = o;
+  }
+}
+
+// One key's row of K or V as it is stored.
+template <int NG>
+struct Raw {
+  uint4 code[2 * NG];
+  float scale[NG], mn[NG];
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) tile_kernel(const AttnArgs<__half> a, const ClassPlan pl, uint32_t wait_limit) {
+  using S = Smem<D>;
+  constexpr int NG = D / 64;
+  constexpr uint32_t kIdescS = idesc_f16(128, 128, 0, 0);   // A = Q (K-major), B = K (K-major)
+  constexpr uint32_t kIdescO = idesc_f16(128, D, 0, 1);     // A = P (tensor memory), B = V (MN-major)
+  constexpr uint32_t kO = 256;                              // S: 0 and 128; O: 256 and 256 + D
+  constexpr uint32_t kP = D == 128 ? 0 : 384, kPStep = D == 128 ? 128 : 64;
+  constexpr uint32_t kTmemCols = 512;
+
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sQ = sm;
+  uint8_t* sKV = sQ + 2 * S::kQ;
+  uint32_t* sFlags = reinterpret_cast<uint32_t*>(sKV + 2 * S::kStage);   // [stage][absent, nan 0, nan 1][4]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sKV + 2 * S::kStage + 2 * S::kFlags);
+  uint64_t* qfull = bars;         // [group] Q of the segment is in place
+  uint64_t* kfull = bars + 2;     // [stage]
+  uint64_t* kfree = bars + 4;
+  uint64_t* vfull = bars + 6;
+  uint64_t* vfree = bars + 8;
+  uint64_t* sfull = bars + 10;    // [group] S of the tile is in tensor memory
+  uint64_t* pfull = bars + 12;    // [group] P of the tile is
+  uint64_t* odone = bars + 14;    // [group] the segment's last P V has completed
+  uint64_t* done = bars + 16;     // every MMA has
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 17);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int w = blockIdx.x;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&qfull[i], 4);
+      mbar_init(&kfull[i], kRestoreWarps);
+      mbar_init(&vfull[i], kRestoreWarps);
+      mbar_init(&kfree[i], 1);
+      mbar_init(&vfree[i], 1);
+      mbar_init(&sfull[i], 1);
+      mbar_init(&pfull[i], 4);
+      mbar_init(&odone[i], 1);
+    }
+    mbar_init(done, 1);
+    *abort_flag = 0;
+    mbar_fence_init();
+  }
+  if (warp == kMmaWarp) tmem_alloc(tmem_slot, kTmemCols);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  griddep_launch();
+  griddep_wait();   // the plan, and what ran before it
+
+  Walk k;
+  walk_begin(k, a, pl, w);
+
+  if (warp >= kSoftWarps && warp < kSoftWarps + kRestoreWarps) {
+    // ---- restoring warps: key r of every tile -------------------------------------
+    const int r = threadIdx.x - 32 * kSoftWarps;
+    const int quarter = warp - kSoftWarps;
+    uint8_t* const base = sKV + r * 128;
+    const int cap = a.tab.pages;
+    // the key of tile x: its page (-1: none) and whether a row of the unit sees it
+    auto page_for = [&](const Walk& t, int x) {
+      const int j = (t.sp.tile(x) << kKeysLog2) + r;
+      const int last = min(t.un.p1, t.s.keys - 1);
+      const int lo = a.shape.window > 0 && t.un.p0 >= a.shape.window ? t.un.p0 - a.shape.window + 1 : 0;
+      if (j > last || (j < lo && j >= a.shape.sinks)) return -1;   // no row sees it
+      const int page = a.tab.table[t.i * a.tab.stride + (j >> a.pool.ps_log2)];
+      if (static_cast<uint32_t>(page) < static_cast<uint32_t>(cap)) return page;
+      atomicOr(a.batch.err, DEV_ERR_PAGE);
+      return -2;
+    };
+    auto load = [&](Raw<NG>& v, int which, int page, const Walk& t, int x) {
+      if (page >= 0) {
+        const int j = (t.sp.tile(x) << kKeysLog2) + r;
+        const int64_t slot = slot_of(a.pool, page, t.h, j);
+        const uint4* c = reinterpret_cast<const uint4*>((which ? a.pool.codes[1] : a.pool.codes[0]) + slot * (D / 2));
+        const float* sc = (which ? a.pool.scales[1] : a.pool.scales[0]) + slot * NG;
+        const float* mn = (which ? a.pool.mins[1] : a.pool.mins[0]) + slot * NG;
+#pragma unroll
+        for (int e = 0; e < 2 * NG; ++e) v.code[e] = c[e];
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+          v.scale[g] = sc[g];
+          v.mn[g] = mn[g];
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 2 * NG; ++e) v.code[e] = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+        for (int g = 0; g < NG; ++g) v.scale[g] = v.mn[g] = 0.0f;
+      }
+    };
+    Raw<NG> kr, vr;
+    int page = -1, next_page = -1;
+    Walk nx = k;   // the tile after the current one
+    int nxx = k.x;
+    auto step_next = [&]() {   // nx, nxx move one tile on
+      if (nx.left == 0) return;
+      if (++nxx == nx.x1) {
+        walk_next(nx, a, pl);
+        nxx = nx.x;
+      }
+    };
+    if (k.left > 0) {
+      page = page_for(k, k.x);
+      load(kr, 0, page, k, k.x);
+      load(vr, 1, page, k, k.x);
+      step_next();
+      if (nx.left > 0) next_page = page_for(nx, nxx);
+    }
+    bool ok = true;
+    for (int g = 0; k.left > 0 && ok; ++g) {
+      const int st = g & 1;
+      const uint32_t par = ((g >> 1) & 1) ^ 1;
+      ok = mbar_wait(&kfree[st], par, wait_limit, abort_flag);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      uint8_t* kp = base + st * S::kStage;
+#pragma unroll
+      for (int q = 0; q < NG; ++q) restore_group(kr.code[2 * q], kr.code[2 * q + 1], kr.scale[q], kr.mn[q], kp + q * S::kPanel, r);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&kfull[st]);
+      if (nx.left > 0) load(kr, 0, next_page, nx, nxx);
+      ok = mbar_wait(&vfree[st], par, wait_limit, abort_flag);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      const uint32_t absent = __ballot_sync(0xffffffffu, page == -2);
+      if (lane == 0) sFlags[st * 12 + quarter] = absent;
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        bool bad = false;
+        if (q < NG) {
+          bad = !(fabsf(vr.scale[q]) < INFINITY);
+          if (bad) vr.scale[q] = vr.mn[q] = 0.0f;
+        }
+        const uint32_t m = __ballot_sync(0xffffffffu, bad);
+        if (lane == 0) sFlags[st * 12 + 4 * (q + 1) + quarter] = m;
+      }
+#pragma unroll
+      for (int q = 0; q < NG; ++q)
+        restore_group(vr.code[2 * q], vr.code[2 * q + 1], vr.scale[q], vr.mn[q], kp + S::kK + q * S::kPanel, r);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&vfull[st]);
+      if (nx.left > 0) load(vr, 1, next_page, nx, nxx);
+      // on: the next tile becomes the current one
+      page = next_page;
+      k.left = nx.left;
+      step_next();
+      if (nx.left > 0) next_page = page_for(nx, nxx);
+    }
+  } else if (warp == kMmaWarp) {
+    // ---- MMA issuer --------------------------------------------------------------------
+    if (lane == 0) {
+      const uint32_t q_addr = smem_u32(sQ), kv_addr = smem_u32(sKV);
+      auto issue_s = [&](int grp, int g) {
+        const uint32_t qa = q_addr + grp * S::kQ, ka = kv_addr + (g & 1) * S::kStage;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = (kk / 4) * S::kPanel + (kk % 4) * 32;
+          mma_f16(tmem + 128 * grp, smem_desc_sw128(qa + off, 16, 1024), smem_desc_sw128(ka + off, 16, 1024), kIdescS, kk > 0 ? 1u : 0u);
+        }
+        mma_commit(&sfull[grp]);
+      };
+      auto issue_o = [&](int grp, int g, bool first) {
+        const uint32_t va = kv_addr + (g & 1) * S::kStage + S::kK;
+#pragma unroll
+        for (int kk = 0; kk < kKeys / 16; ++kk)
+          mma_f16_ts(tmem + kO + D * grp, tmem + kP + kPStep * grp + 8 * kk, smem_desc_sw128(va + kk * 2048, S::kPanel, 1024), kIdescO,
+                     (!first || kk > 0) ? 1u : 0u);
+      };
+      bool ok = true;
+      int g = 0, gb = 0, n = 0, nb = 0;   // tiles and segments, of group 1 too
+      auto wait = [&](uint64_t* bar, int phase) {
+        if (ok) ok = mbar_wait(bar, phase & 1, wait_limit, abort_flag);
+        return ok;
+      };
+      while (k.left > 0 && ok) {
+        const bool two = k.un.rows > 128;
+        if (!wait(&qfull[0], n) || !wait(&kfull[g & 1], g >> 1)) break;
+        tc_fence_after();
+        issue_s(0, g);
+        if (two) {
+          if (!wait(&qfull[1], nb)) break;
+          tc_fence_after();
+          issue_s(1, g);
+        }
+        mma_commit(&kfree[g & 1]);
+        for (int x = k.x; x < k.x1 && ok; ++x, ++g) {
+          const bool first = x == k.x, last = x + 1 == k.x1;
+          if (!wait(&pfull[0], g) || !wait(&vfull[g & 1], g >> 1)) break;
+          tc_fence_after();
+          issue_o(0, g, first);
+          if (last) {
+            mma_commit(&odone[0]);
+          } else {
+            if (!wait(&kfull[(g + 1) & 1], (g + 1) >> 1)) break;
+            tc_fence_after();
+            issue_s(0, g + 1);
+          }
+          if (two) {
+            if (!wait(&pfull[1], gb)) break;
+            tc_fence_after();
+            issue_o(1, g, first);
+            if (last) mma_commit(&odone[1]);
+            else issue_s(1, g + 1);
+            ++gb;
+          }
+          mma_commit(&vfree[g & 1]);
+          if (!last) mma_commit(&kfree[(g + 1) & 1]);
+        }
+        ++n;
+        nb += two;
+        walk_next(k, a, pl);
+      }
+      mma_commit(done);
+      if (!ok) atomicOr(a.batch.err, DEV_ERR_WAIT_TIMEOUT);
+    }
+    __syncwarp();
+  } else {
+    // ---- softmax warps: row r of group grp -------------------------------------------------
+    const int grp = warp >> 2, quarter = warp & 3;
+    const int rr = 32 * quarter + lane, r = 128 * grp + rr;
+    const uint32_t trow = tmem + (static_cast<uint32_t>(32 * quarter) << 16);
+    const uint32_t ts = trow + 128 * grp, to = trow + kO + D * grp, tp = trow + kP + kPStep * grp;
+    bool ok = true;
+    int4 rec = make_int4(-1, 0, 0, 0);
+    int g0 = 0;            // the CTA's tiles before the segment
+    int cnt = 0, seg = 0;  // this group's tiles and segments
+    while (k.left > 0 && ok) {
+      const int tiles = k.x1 - k.x;
+      if (grp == 1 && k.un.rows <= 128) {
+        g0 += tiles;
+        walk_next(k, a, pl);
+        continue;
+      }
+      const bool from_start = k.x == 0, to_end = k.x1 == k.sp.n;
+      const bool on = r < k.un.rows;
+      const int row = k.un.r0 + (on ? r : 0), t = row / a.shape.group;
+      const int head = k.h * a.shape.group + row - t * a.shape.group;
+      const int p = k.s.len - k.s.n + t;   // the row's position
+      // Q, with every 8 dims in the order (0, 4), (1, 5), (2, 6), (3, 7)
+      {
+        const uint4* src = reinterpret_cast<const uint4*>(a.q + static_cast<int64_t>(k.s.row0 + t) * a.ldq + static_cast<int64_t>(head) * D);
+        uint8_t* qrow = sQ + grp * S::kQ + rr * 128;
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c) {
+          const uint4 v = on ? src[c] : make_uint4(0u, 0u, 0u, 0u);
+          const uint4 o = make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632), __byte_perm(v.y, v.w, 0x5410),
+                                     __byte_perm(v.y, v.w, 0x7632));
+          *reinterpret_cast<uint4*>(qrow + (c >> 3) * S::kPanel + (((c & 7) ^ (rr & 7)) << 4)) = o;
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&qfull[grp]);
+      }
+      float m = -INFINITY;
+      float2 l2 = make_float2(0.0f, 0.0f);
+      uint32_t nans = 0;
+      for (int x = 0; x < tiles; ++x, ++cnt) {
+        // tcgen05.ld/st are warp-collective: every branch around them is taken by the whole warp
+        ok = mbar_wait(&sfull[grp], cnt & 1, wait_limit, abort_flag);
+        const int st = (g0 + x) & 1;
+        if (ok) ok = mbar_wait(&vfull[st], ((g0 + x) >> 1) & 1, wait_limit, abort_flag);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
+        const int t0 = k.sp.tile(k.x + x) << kKeysLog2;
+        const uint4 ab = *reinterpret_cast<const uint4*>(sFlags + st * 12);
+        const uint4 n0 = *reinterpret_cast<const uint4*>(sFlags + st * 12 + 4), n1 = *reinterpret_cast<const uint4*>(sFlags + st * 12 + 8);
+        const bool odd = (ab.x | ab.y | ab.z | ab.w | n0.x | n0.y | n0.z | n0.w | n1.x | n1.y | n1.z | n1.w) != 0;
+        // every row of the unit sees all of the tile
+        const bool whole = !odd && t0 + kKeys - 1 <= k.un.p0 && t0 + kKeys <= k.s.keys &&
+                           (a.shape.window == 0 || t0 > k.un.p1 - a.shape.window || t0 + kKeys <= a.shape.sinks);
+        uint32_t see[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
+        if (!whole) {
+          const int hi = min(p, k.s.keys - 1) - t0 + 1;                               // columns below it are not later than the row
+          const int lo = a.shape.window > 0 && p >= a.shape.window ? p - a.shape.window + 1 - t0 : 0;   // columns below it lie behind the window
+          const int sk = a.shape.sinks - t0;
+          const uint32_t abs4[4] = {ab.x, ab.y, ab.z, ab.w};
+          const uint32_t n04[4] = {n0.x, n0.y, n0.z, n0.w}, n14[4] = {n1.x, n1.y, n1.z, n1.w};
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            see[c] = bits_below(hi - 32 * c) & (~bits_below(lo - 32 * c) | bits_below(sk - 32 * c)) & ~abs4[c];
+            nans |= ((see[c] & n04[c]) ? 1u : 0u) | ((see[c] & n14[c]) ? 2u : 0u);
+          }
+        }
+        // the row's maximum
+        float mx = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t u[32];
+          tmem_ld_32x32b_x32(ts + 32 * c, u);
+          tmem_ld_wait();
+          if (!whole) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (!((see[c] >> e) & 1u)) u[e] = 0xff800000u;
+          }
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) mx = fmaxf(mx, fmaxf(__uint_as_float(u[e]), __uint_as_float(u[e + 1])));
+        }
+        mx *= a.scale_log2;
+        if (x == 0) {
+          m = mx;
+        } else {
+          const bool grow = mx > m + kRescale;
+          if (__any_sync(0xffffffffu, grow)) {
+            const float alpha = grow ? ex2_approx(m - mx) : 1.0f;
+            if (grow) {
+              l2.x *= alpha;
+              l2.y *= alpha;
+              m = mx;
+            }
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t u[32];
+              tmem_ld_32x32b_x32(to + 32 * c, u);
+              tmem_ld_wait();
+#pragma unroll
+              for (int e = 0; e < 32; ++e) u[e] = __float_as_uint(__uint_as_float(u[e]) * alpha);
+              tmem_st_32x32b_x32(to + 32 * c, u);
+            }
+          }
+        }
+        const float negm = m == -INFINITY ? 0.0f : -m;
+        const float2 sc2 = make_float2(a.scale_log2, a.scale_log2), nm2 = make_float2(negm, negm);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t u[32], pk[16];
+          tmem_ld_32x32b_x32(ts + 32 * c, u);
+          tmem_ld_wait();
+          if (!whole) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (!((see[c] >> e) & 1u)) u[e] = 0xff800000u;
+          }
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            float2 v = q4::fma_f32x2(make_float2(__uint_as_float(u[2 * e]), __uint_as_float(u[2 * e + 1])), sc2, nm2);
+            v = make_float2(ex2_approx(v.x), ex2_approx(v.y));
+            l2 = add_f32x2(l2, v);
+            pk[e] = q4::cvt_f16x2(v);
+          }
+          tmem_st_32x32b_x16(tp + 16 * c, pk);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&pfull[grp]);
+      }
+      if (!ok) break;
+      ok = mbar_wait(&odone[grp], seg & 1, wait_limit, abort_flag);
+      ok = __all_sync(0xffffffffu, ok && !*abort_flag);
+      if (!ok) break;
+      tc_fence_after();
+      // ---- the segment's rows: finished, or this share's partial ------------------------
+      const bool whole = from_start && to_end;
+      const float l = l2.x + l2.y;
+      const float f = !whole ? 1.0f : l == 0.0f ? 0.0f : 1.0f / l;
+      const int64_t slot = (static_cast<int64_t>(w) * 2 + (from_start ? 1 : 0)) * kRows + r;
+      __half* dst = a.out + static_cast<int64_t>(k.s.row0 + t) * a.ldo + static_cast<int64_t>(head) * D;
+#pragma unroll 1
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t u[32];
+        tmem_ld_32x32b_x32(to + 32 * c, u);
+        tmem_ld_wait();
+        if (!on) continue;   // no collective follows in the round
+        const bool nan = (nans >> (c >> 1)) & 1u;
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {   // 8 columns: dims 0..7 lie at 0, 2, 4, 6, 1, 3, 5, 7
+          float v[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            v[e] = __uint_as_float(u[8 * b + (e < 4 ? 2 * e : 2 * e - 7)]) * f;
+            if (nan) v[e] = __uint_as_float(0x7fffffffu);
+          }
+          if (whole) {
+            *reinterpret_cast<uint4*>(dst + 32 * c + 8 * b) =
+                make_uint4(q4::cvt_f16x2(make_float2(v[0], v[1])), q4::cvt_f16x2(make_float2(v[2], v[3])),
+                           q4::cvt_f16x2(make_float2(v[4], v[5])), q4::cvt_f16x2(make_float2(v[6], v[7])));
+          } else {
+            float4* part = reinterpret_cast<float4*>(pl.part + slot * D + 32 * c + 8 * b);
+            part[0] = make_float4(v[0], v[1], v[2], v[3]);
+            part[1] = make_float4(v[4], v[5], v[6], v[7]);
+          }
+        }
+      }
+      if (!whole && on) pl.stat[slot] = make_float2(m, l);
+      if (from_start && !to_end) {
+        // the item's first tile in the line: the share's first tiles, then those of the segments before it
+        const int64_t per = pl.head[1], start = w * per + g0;
+        rec = make_int4(k.i, k.h, k.u, static_cast<int>((start + k.sp.n - 1) / per));
+      }
+      ++seg;
+      g0 += tiles;
+      walk_next(k, a, pl);
+    }
+    if (threadIdx.x == 0) pl.rec[w] = rec;
+  }
+  // ---- teardown: every MMA done, then the tensor memory is freed ------------------------------
+  if (warp == kMmaWarp && lane == 0) {
+    volatile int dummy = 0;
+    mbar_wait(done, 0, kDrainLimit, &dummy);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+template <int D>
+fg_status launch(const AttnArgs<__half>& a, const ClassPlan& pl, cudaStream_t st) {
+  using S = Smem<D>;
+  static bool set[64] = {false};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev >= 0 && dev < 64 && !set[dev]) {
+    if (cudaFuncSetAttribute(tile_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kBytes) != cudaSuccess)
+      return check_launch("tile_kernel smem attribute");
+    set[dev] = true;
+  }
+  cudaLaunchAttribute pdl[1];
+  pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  pdl[0].val.programmaticStreamSerializationAllowed = 1;
+  Trace tr(KC_ATTN_PAGED, st);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(pl.workers));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = S::kBytes;
+  cfg.stream = st;
+  cfg.attrs = pdl;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, tile_kernel<D>, a, pl, wait_limit()) != cudaSuccess) return check_launch("tile_kernel (launch)");
+  return check_launch("tile_kernel");
+}
+
+}  // namespace
+
+fg_status paged_attention_tile(const AttnArgs<__half>& a, const ClassPlan& pl, int head_dim, cudaStream_t st) {
+  return head_dim == 128 ? launch<128>(a, pl, st) : launch<64>(a, pl, st);
+}
+
+}  // namespace paged
+}  // namespace fg
