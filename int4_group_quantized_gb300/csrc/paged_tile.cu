@@ -7,18 +7,19 @@
 // group + g), so that every restored K/V tile of 128 keys feeds two MMA tiles
 // of 128 rows; one persistent CTA per SM walks its share of the line of tiles
 // (paged_sched.cuh).  Roles:
-//   * four warps restore: a thread owns one key of the tile, takes its K and V
-//     codes (loaded into registers a tile ahead, the page number another tile
-//     ahead) through fp16(fmaf(q, scale, min)) -- exact fp32 codes by
-//     mixed-precision adds, one paired fp32 FMA, one rounding -- into the
-//     128-byte-swizzled rows the MMA reads (K: K-major panels, V: MN-major
+//   * seven warps restore: a tile is eight tasks (K or V of 32 keys, a key a
+//     lane), dealt round the warps in order.  A task's codes are loaded into
+//     registers a task ahead, its page number two; they go through
+//     fp16(fmaf(q, scale, min)) -- a masked nibble is the subnormal fp16 c *
+//     2^-24, exact in fp32, then one paired fp32 FMA and one rounding -- into
+//     the 128-byte-swizzled rows the MMA reads (K: K-major panels, V: MN-major
 //     blocks; the same bytes).  A pair of a code word's halves holds dims (0,
 //     4), (1, 5), (2, 6), (3, 7); Q is laid out in the same order and O is
 //     taken apart in it;
-//   * two groups of four softmax warps (one row a thread) keep the running
-//     maximum and sum in base 2, write P (fp16) into tensor memory as the
-//     second MMA's A operand, rescale O there only when a row's maximum grew
-//     by more than 2^8, and finish or hand on a share's rows;
+//   * two groups of four softmax warps (one row a thread) keep a maximum and
+//     the sum in base 2, write P (fp16) into tensor memory as the second MMA's
+//     A operand, look for a new maximum (and rescale O there) only when the
+//     known one no longer serves, and finish or hand on a share's rows;
 //   * one thread issues S = Q K^T (M = N = 128) and O += P V for both groups in
 //     turn, so that one group's softmax runs under the other's MMAs.
 // Tensor memory: S of each group, O of each group, and P: in the columns of its
@@ -48,10 +49,10 @@ constexpr int kKeysLog2 = 7;
 constexpr int kKeys = 1 << kKeysLog2;
 constexpr int kRows = kTileRows;
 constexpr int kSoftWarps = 8;      // warps 0..3: rows 0..127, warps 4..7: rows 128..255
-constexpr int kRestoreWarps = 4;   // warps 8..11
-constexpr int kMmaWarp = 12;
-constexpr int kThreads = 13 * 32;
-constexpr float kRescale = 8.0f;
+constexpr int kRestoreWarps = 7;   // warps 8..14
+constexpr int kMmaWarp = 15;
+constexpr int kThreads = 16 * 32;
+constexpr float kMostSum = 16384.0f;   // a tile's row sum up to which its weights stand as fp16
 
 template <int D>
 struct Smem {
@@ -141,22 +142,75 @@ __device__ __forceinline__ float2 add_f32x2(float2 a, float2 b) {
       : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
   return r;
 }
+// Waits for this thread's tensor-memory loads; the registers named are not
+// read before it.
+__device__ __forceinline__ void tmem_arrived(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
+                 "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+               :
+               : "memory");
+  asm volatile(""
+               : "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                 "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+               :
+               : "memory");
+}
+__device__ __forceinline__ void tmem_arrived(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
+                 "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+               :
+               : "memory");
+}
+// 16 consecutive columns (tmem_arrived before they are read).
+__device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+        "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
 // Bits c of a word with c < n, for any n.
 __device__ __forceinline__ uint32_t bits_below(int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; }
 
+// The MMAs with their descriptors as a running low word (the start address
+// field; offsets inside the CTA's allocation never carry out of it) and one
+// high word: a couple of instructions an MMA for the issuing thread.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t hi, uint32_t idesc, bool acc) {
+  asm volatile(
+      "{ .reg .pred p; .reg .b64 x, y; setp.ne.b32 p, %5, 0; mov.b64 x, {%1, %3}; mov.b64 y, {%2, %3};\n"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %4, p; }" ::"r"(d),
+      "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "r"(acc ? 1u : 0u)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a_tmem, uint32_t b_lo, uint32_t b_hi, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{ .reg .pred p; .reg .b64 y; setp.ne.b32 p, %5, 0; mov.b64 y, {%2, %3};\n"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %4, p; }" ::"r"(d),
+      "r"(a_tmem), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(acc)
+      : "memory");
+}
+
+__device__ __forceinline__ float2 halves(uint32_t h) {   // fp16x2 in fp32
+  float2 r;
+  asm("{ .reg .f16 a, b; mov.b32 {a, b}, %2; cvt.f32.f16 %0, a; cvt.f32.f16 %1, b; }" : "=f"(r.x), "=f"(r.y) : "r"(h));
+  return r;
+}
 // 64 codes (32 bytes) of one group through fp16(fmaf(q, scale, min)) into row
 // r of a swizzled panel.
 __device__ __forceinline__ void restore_group(const uint4& lo, const uint4& hi, float scale, float mn, uint8_t* prow, int r) {
-  const float2 s2 = make_float2(scale, scale), m2 = make_float2(mn, mn);
+  // a masked nibble is c * 2^-24 or 16 c * 2^-24; scaling by powers of two is exact
+  const float2 lo2 = make_float2(scale * 16777216.0f, scale * 16777216.0f), hi2 = make_float2(scale * 1048576.0f, scale * 1048576.0f);
+  const float2 m2 = make_float2(mn, mn);
   const uint32_t words[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
 #pragma unroll
   for (int c = 0; c < 8; ++c) {
     const uint32_t x = words[c], y = x >> 8;
-    uint4 o;
-    o.x = q4::cvt_f16x2(q4::fma_f32x2(q4::nib_pair_f32(q4::lop_mask_or(x, 0x000F000Fu, q4::kMagic)), s2, m2));
-    o.y = q4::cvt_f16x2(q4::fma_f32x2(q4::nib16_pair_f32(q4::lop_mask_or(x, 0x00F000F0u, q4::kMagic)), s2, m2));
-    o.z = q4::cvt_f16x2(q4::fma_f32x2(q4::nib_pair_f32(q4::lop_mask_or(y, 0x000F000Fu, q4::kMagic)), s2, m2));
-    o.w = q4::cvt_f16x2(q4::fma_f32x2(q4::nib16_pair_f32(q4::lop_mask_or(y, 0x00F000F0u, q4::kMagic)), s2, m2));
+    const uint4 o = make_uint4(q4::cvt_f16x2(q4::fma_f32x2(halves(x & 0x000F000Fu), lo2, m2)),
+                               q4::cvt_f16x2(q4::fma_f32x2(halves(x & 0x00F000F0u), hi2, m2)),
+                               q4::cvt_f16x2(q4::fma_f32x2(halves(y & 0x000F000Fu), lo2, m2)),
+                               q4::cvt_f16x2(q4::fma_f32x2(halves(y & 0x00F000F0u), hi2, m2)));
     *reinterpret_cast<uint4*>(prow + ((c ^ (r & 7)) << 4)) = o;
   }
 }
@@ -166,6 +220,7 @@ template <int NG>
 struct Raw {
   uint4 code[2 * NG];
   float scale[NG], mn[NG];
+  bool absent;           // the table has no page for it
 };
 
 template <int D>
@@ -202,8 +257,8 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const AttnArgs<__half
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&qfull[i], 4);
-      mbar_init(&kfull[i], kRestoreWarps);
-      mbar_init(&vfull[i], kRestoreWarps);
+      mbar_init(&kfull[i], 4);
+      mbar_init(&vfull[i], 4);
       mbar_init(&kfree[i], 1);
       mbar_init(&vfree[i], 1);
       mbar_init(&sfull[i], 1);
@@ -226,26 +281,33 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const AttnArgs<__half
   walk_begin(k, a, pl, w);
 
   if (warp >= kSoftWarps && warp < kSoftWarps + kRestoreWarps) {
-    // ---- restoring warps: key r of every tile -------------------------------------
-    const int r = threadIdx.x - 32 * kSoftWarps;
-    const int quarter = warp - kSoftWarps;
-    uint8_t* const base = sKV + r * 128;
-    const int cap = a.tab.pages;
-    // the key of tile x: its page (-1: none) and whether a row of the unit sees it
-    auto page_for = [&](const Walk& t, int x) {
-      const int j = (t.sp.tile(x) << kKeysLog2) + r;
-      const int last = min(t.un.p1, t.s.keys - 1);
-      const int lo = a.shape.window > 0 && t.un.p0 >= a.shape.window ? t.un.p0 - a.shape.window + 1 : 0;
-      if (j > last || (j < lo && j >= a.shape.sinks)) return -1;   // no row sees it
-      const int page = a.tab.table[t.i * a.tab.stride + (j >> a.pool.ps_log2)];
-      if (static_cast<uint32_t>(page) < static_cast<uint32_t>(cap)) return page;
-      atomicOr(a.batch.err, DEV_ERR_PAGE);
-      return -2;
+    // ---- restoring warps: task n is K (n % 8 < 4) or V of 32 keys of tile n / 8 ------------
+    const int tasks = 8 * k.left;
+    int n = warp - kSoftWarps;
+    Walk nx = k;             // at the tile of task `seen`, the next to be looked up
+    int nxx = k.left > 0 ? k.x : 0, seen = n;
+    // the lane's key of task `seen`: the table's entry (not looked at before the load below) and its place in a page (-1: no
+    // row of the unit sees the key)
+    auto look_up = [&](int& page, int& off) {
+      page = off = -1;
+      if (seen >= tasks) return;
+      const int j = (nx.sp.tile(nxx) << kKeysLog2) + 32 * (seen & 3) + lane;
+      const int last = min(nx.un.p1, nx.s.keys - 1);
+      const int lo = a.shape.window > 0 && nx.un.p0 >= a.shape.window ? nx.un.p0 - a.shape.window + 1 : 0;
+      if (j <= last && (j >= lo || j < a.shape.sinks)) {
+        page = a.tab.table[nx.i * a.tab.stride + (j >> a.pool.ps_log2)];
+        off = (nx.h << a.pool.ps_log2) + (j & ((1 << a.pool.ps_log2) - 1));
+      }
+      // on by 7 tasks: a tile further, unless the task was a tile's first
+      if ((seen & 7) != 0 && ++nxx == nx.x1) {
+        walk_next(nx, a, pl);
+        nxx = nx.x;
+      }
+      seen += kRestoreWarps;
     };
-    auto load = [&](Raw<NG>& v, int which, int page, const Walk& t, int x) {
-      if (page >= 0) {
-        const int j = (t.sp.tile(x) << kKeysLog2) + r;
-        const int64_t slot = slot_of(a.pool, page, t.h, j);
+    auto load = [&](Raw<NG>& v, int which, int page, int off) {
+      if (off >= 0 && static_cast<uint32_t>(page) < static_cast<uint32_t>(a.tab.pages)) {
+        const int64_t slot = (static_cast<int64_t>(page) * a.pool.heads << a.pool.ps_log2) + off;
         const uint4* c = reinterpret_cast<const uint4*>((which ? a.pool.codes[1] : a.pool.codes[0]) + slot * (D / 2));
         const float* sc = (which ? a.pool.scales[1] : a.pool.scales[0]) + slot * NG;
         const float* mn = (which ? a.pool.mins[1] : a.pool.mins[0]) + slot * NG;
@@ -256,92 +318,79 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const AttnArgs<__half
           v.scale[g] = sc[g];
           v.mn[g] = mn[g];
         }
+        v.absent = false;
       } else {
 #pragma unroll
         for (int e = 0; e < 2 * NG; ++e) v.code[e] = make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
         for (int g = 0; g < NG; ++g) v.scale[g] = v.mn[g] = 0.0f;
+        v.absent = off >= 0;
+        if (v.absent) atomicOr(a.batch.err, DEV_ERR_PAGE);
       }
     };
-    Raw<NG> kr, vr;
-    int page = -1, next_page = -1;
-    Walk nx = k;   // the tile after the current one
-    int nxx = k.x;
-    auto step_next = [&]() {   // nx, nxx move one tile on
-      if (nx.left == 0) return;
-      if (++nxx == nx.x1) {
-        walk_next(nx, a, pl);
-        nxx = nx.x;
-      }
-    };
-    if (k.left > 0) {
-      page = page_for(k, k.x);
-      load(kr, 0, page, k, k.x);
-      load(vr, 1, page, k, k.x);
-      step_next();
-      if (nx.left > 0) next_page = page_for(nx, nxx);
-    }
-    bool ok = true;
-    for (int g = 0; k.left > 0 && ok; ++g) {
-      const int st = g & 1;
-      const uint32_t par = ((g >> 1) & 1) ^ 1;
-      ok = mbar_wait(&kfree[st], par, wait_limit, abort_flag);
+    auto restore = [&](Raw<NG>& v) {   // task n
+      const int g = n >> 3, st = g & 1, quarter = n & 3, r = 32 * quarter + lane;
+      const bool value = n & 4;
+      bool ok = mbar_wait(value ? &vfree[st] : &kfree[st], ((g >> 1) & 1) ^ 1, wait_limit, abort_flag);
       ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
-      uint8_t* kp = base + st * S::kStage;
+      if (!ok) return false;
+      if (value) {
+        const uint32_t absent = __ballot_sync(0xffffffffu, v.absent);
+        if (lane == 0) sFlags[st * 12 + quarter] = absent;
 #pragma unroll
-      for (int q = 0; q < NG; ++q) restore_group(kr.code[2 * q], kr.code[2 * q + 1], kr.scale[q], kr.mn[q], kp + q * S::kPanel, r);
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&kfull[st]);
-      if (nx.left > 0) load(kr, 0, next_page, nx, nxx);
-      ok = mbar_wait(&vfree[st], par, wait_limit, abort_flag);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
-      const uint32_t absent = __ballot_sync(0xffffffffu, page == -2);
-      if (lane == 0) sFlags[st * 12 + quarter] = absent;
-#pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        bool bad = false;
-        if (q < NG) {
-          bad = !(fabsf(vr.scale[q]) < INFINITY);
-          if (bad) vr.scale[q] = vr.mn[q] = 0.0f;
+        for (int q = 0; q < 2; ++q) {
+          bool bad = false;
+          if (q < NG) {
+            bad = !(fabsf(v.scale[q]) < INFINITY);
+            if (bad) v.scale[q] = v.mn[q] = 0.0f;
+          }
+          const uint32_t m = __ballot_sync(0xffffffffu, bad);
+          if (lane == 0) sFlags[st * 12 + 4 * (q + 1) + quarter] = m;
         }
-        const uint32_t m = __ballot_sync(0xffffffffu, bad);
-        if (lane == 0) sFlags[st * 12 + 4 * (q + 1) + quarter] = m;
       }
+      uint8_t* p = sKV + st * S::kStage + (value ? S::kK : 0) + r * 128;
 #pragma unroll
-      for (int q = 0; q < NG; ++q)
-        restore_group(vr.code[2 * q], vr.code[2 * q + 1], vr.scale[q], vr.mn[q], kp + S::kK + q * S::kPanel, r);
+      for (int q = 0; q < NG; ++q) restore_group(v.code[2 * q], v.code[2 * q + 1], v.scale[q], v.mn[q], p + q * S::kPanel, r);
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&vfull[st]);
-      if (nx.left > 0) load(vr, 1, next_page, nx, nxx);
-      // on: the next tile becomes the current one
-      page = next_page;
-      k.left = nx.left;
-      step_next();
-      if (nx.left > 0) next_page = page_for(nx, nxx);
+      if (lane == 0) mbar_arrive(value ? &vfull[st] : &kfull[st]);
+      return true;
+    };
+    Raw<NG> r0, r1;
+    int page, off;
+    look_up(page, off);
+    load(r0, (n >> 2) & 1, page, off);
+    look_up(page, off);
+    // task n from one buffer while the next one's codes come into the other
+    auto turn = [&](Raw<NG>& now, Raw<NG>& then) {
+      load(then, ((n + kRestoreWarps) >> 2) & 1, page, off);
+      look_up(page, off);
+      const bool ok = restore(now);
+      n += kRestoreWarps;
+      return ok;
+    };
+    while (n < tasks && turn(r0, r1) && n < tasks && turn(r1, r0)) {
     }
   } else if (warp == kMmaWarp) {
     // ---- MMA issuer --------------------------------------------------------------------
     if (lane == 0) {
-      const uint32_t q_addr = smem_u32(sQ), kv_addr = smem_u32(sKV);
+      const uint64_t kd = smem_desc_sw128(smem_u32(sKV), 16, 1024), vd = smem_desc_sw128(smem_u32(sKV) + S::kK, S::kPanel, 1024);
+      const uint32_t q_lo = static_cast<uint32_t>(smem_desc_sw128(smem_u32(sQ), 16, 1024)), k_lo = static_cast<uint32_t>(kd);
+      const uint32_t k_hi = static_cast<uint32_t>(kd >> 32), v_lo = static_cast<uint32_t>(vd), v_hi = static_cast<uint32_t>(vd >> 32);
       auto issue_s = [&](int grp, int g) {
-        const uint32_t qa = q_addr + grp * S::kQ, ka = kv_addr + (g & 1) * S::kStage;
+        const uint32_t qa = q_lo + grp * (S::kQ >> 4), ka = k_lo + (g & 1) * (S::kStage >> 4);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = (kk / 4) * S::kPanel + (kk % 4) * 32;
-          mma_f16(tmem + 128 * grp, smem_desc_sw128(qa + off, 16, 1024), smem_desc_sw128(ka + off, 16, 1024), kIdescS, kk > 0 ? 1u : 0u);
+          const uint32_t off = ((kk / 4) * S::kPanel + (kk % 4) * 32) >> 4;
+          mma_ss(tmem + 128 * grp, qa + off, ka + off, k_hi, kIdescS, kk > 0);
         }
         mma_commit(&sfull[grp]);
       };
       auto issue_o = [&](int grp, int g, bool first) {
-        const uint32_t va = kv_addr + (g & 1) * S::kStage + S::kK;
+        const uint32_t va = v_lo + (g & 1) * (S::kStage >> 4), pa = tmem + kP + kPStep * grp;
 #pragma unroll
         for (int kk = 0; kk < kKeys / 16; ++kk)
-          mma_f16_ts(tmem + kO + D * grp, tmem + kP + kPStep * grp + 8 * kk, smem_desc_sw128(va + kk * 2048, S::kPanel, 1024), kIdescO,
-                     (!first || kk > 0) ? 1u : 0u);
+          mma_ts(tmem + kO + D * grp, pa + 8 * kk, va + kk * (2048 >> 4), v_hi, kIdescO, (!first || kk > 0) ? 1u : 0u);
       };
       bool ok = true;
       int g = 0, gb = 0, n = 0, nb = 0;   // tiles and segments, of group 1 too
@@ -459,65 +508,91 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const AttnArgs<__half
             nans |= ((see[c] & n04[c]) ? 1u : 0u) | ((see[c] & n14[c]) ? 2u : 0u);
           }
         }
-        // the row's maximum
-        float mx = -INFINITY;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t u[32];
-          tmem_ld_32x32b_x32(ts + 32 * c, u);
-          tmem_ld_wait();
-          if (!whole) {
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (!((see[c] >> e) & 1u)) u[e] = 0xff800000u;
-          }
-#pragma unroll
-          for (int e = 0; e < 32; e += 2) mx = fmaxf(mx, fmaxf(__uint_as_float(u[e]), __uint_as_float(u[e + 1])));
-        }
-        mx *= a.scale_log2;
-        if (x == 0) {
-          m = mx;
-        } else {
-          const bool grow = mx > m + kRescale;
-          if (__any_sync(0xffffffffu, grow)) {
-            const float alpha = grow ? ex2_approx(m - mx) : 1.0f;
-            if (grow) {
-              l2.x *= alpha;
-              l2.y *= alpha;
-              m = mx;
-            }
+        if (!whole) {   // what the row does not see becomes -inf, in place
 #pragma unroll 1
-            for (int c = 0; c < D / 32; ++c) {
-              uint32_t u[32];
-              tmem_ld_32x32b_x32(to + 32 * c, u);
-              tmem_ld_wait();
-#pragma unroll
-              for (int e = 0; e < 32; ++e) u[e] = __float_as_uint(__uint_as_float(u[e]) * alpha);
-              tmem_st_32x32b_x32(to + 32 * c, u);
-            }
-          }
-        }
-        const float negm = m == -INFINITY ? 0.0f : -m;
-        const float2 sc2 = make_float2(a.scale_log2, a.scale_log2), nm2 = make_float2(negm, negm);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t u[32], pk[16];
-          tmem_ld_32x32b_x32(ts + 32 * c, u);
-          tmem_ld_wait();
-          if (!whole) {
+          for (int c = 0; c < 4; ++c) {
+            uint32_t u[32];
+            tmem_ld_32x32b_x32(ts + 32 * c, u);
+            tmem_arrived(u);
+            const uint32_t word = c == 0 ? see[0] : c == 1 ? see[1] : c == 2 ? see[2] : see[3];
 #pragma unroll
             for (int e = 0; e < 32; ++e)
-              if (!((see[c] >> e) & 1u)) u[e] = 0xff800000u;
+              if (!((word >> e) & 1u)) u[e] = 0xff800000u;
+            tmem_st_32x32b_x32(ts + 32 * c, u);
           }
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            float2 v = q4::fma_f32x2(make_float2(__uint_as_float(u[2 * e]), __uint_as_float(u[2 * e + 1])), sc2, nm2);
-            v = make_float2(ex2_approx(v.x), ex2_approx(v.y));
-            l2 = add_f32x2(l2, v);
-            pk[e] = q4::cvt_f16x2(v);
-          }
-          tmem_st_32x32b_x16(tp + 16 * c, pk);
+          tmem_st_wait();
         }
+        // P = 2^(s - m) for the maximum m known so far.  A segment's first tile finds m; a later one takes it as it is and
+        // looks at the row's sum only: while that stays below 2^14 no weight has left fp16, and a larger maximum changes
+        // nothing but the scale of sums that are divided in the end.  Otherwise (or with no key seen before) the tile finds
+        // its maximum, the sums are rescaled, and the weights are formed again.
+        uint32_t pk[64];
+        float2 lt;
+        bool find = x == 0;
+        while (true) {
+          if (find) {
+            float mx = -INFINITY;
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              uint32_t u[32];
+              tmem_ld_32x32b_x32(ts + 32 * c, u);
+              tmem_arrived(u);
+              float m4[4] = {mx, mx, mx, mx};
+#pragma unroll
+              for (int e = 0; e < 32; e += 8)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) m4[q] = fmaxf(m4[q], fmaxf(__uint_as_float(u[e + 2 * q]), __uint_as_float(u[e + 2 * q + 1])));
+              mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+            }
+            mx = fmaxf(m, mx * a.scale_log2);
+            if (x > 0) {
+              const float alpha = mx == -INFINITY ? 1.0f : ex2_approx(m - mx);
+              l2 = make_float2(l2.x * alpha, l2.y * alpha);
+#pragma unroll 1
+              for (int c = 0; c < D / 16; ++c) {
+                uint32_t u[16];
+                tmem_ld_32x32b_x16(to + 16 * c, u);
+                tmem_arrived(u);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) u[e] = __float_as_uint(__uint_as_float(u[e]) * alpha);
+                tmem_st_32x32b_x16(to + 16 * c, u);
+              }
+            }
+            m = mx;
+          }
+          const float negm = m == -INFINITY ? 0.0f : -m;
+          const float2 sc2 = make_float2(a.scale_log2, a.scale_log2), nm2 = make_float2(negm, negm);
+          lt = make_float2(0.0f, 0.0f);
+          float2 lb = lt;
+          uint32_t ua[16], ub[16];
+          auto weigh = [&](const uint32_t (&u)[16], int c) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              float2 v = q4::fma_f32x2(make_float2(__uint_as_float(u[2 * e]), __uint_as_float(u[2 * e + 1])), sc2, nm2);
+              v = make_float2(ex2_approx(v.x), ex2_approx(v.y));
+              if (e & 1) lb = add_f32x2(lb, v);
+              else lt = add_f32x2(lt, v);
+              pk[8 * c + e] = q4::cvt_f16x2(v);
+            }
+          };
+          tmem_ld_32x32b_x16(ts, ua);
+#pragma unroll
+          for (int c = 0; c < 8; c += 2) {   // a load runs under the chunk before it
+            tmem_arrived(ua);
+            tmem_ld_32x32b_x16(ts + 16 * c + 16, ub);
+            weigh(ua, c);
+            tmem_arrived(ub);
+            if (c < 6) tmem_ld_32x32b_x16(ts + 16 * c + 32, ua);
+            weigh(ub, c + 1);
+          }
+          lt = add_f32x2(lt, lb);
+          const bool again = !find && __any_sync(0xffffffffu, m == -INFINITY || !(lt.x + lt.y <= kMostSum));
+          if (!again) break;
+          find = true;
+        }
+        l2 = add_f32x2(l2, lt);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_st_32x32b_x16(tp + 16 * c, *reinterpret_cast<const uint32_t(*)[16]>(pk + 16 * c));
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
@@ -538,7 +613,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const AttnArgs<__half
       for (int c = 0; c < D / 32; ++c) {
         uint32_t u[32];
         tmem_ld_32x32b_x32(to + 32 * c, u);
-        tmem_ld_wait();
+        tmem_arrived(u);
         if (!on) continue;   // no collective follows in the round
         const bool nan = (nans >> (c >> 1)) & 1u;
 #pragma unroll
