@@ -61,8 +61,8 @@ struct Smem {
   static constexpr int kQ = kPanels * kPanel;           // one group's
   static constexpr int kK = kPanels * kPanel;
   static constexpr int kStage = 2 * kK;                 // K, then V
-  static constexpr int kFlags = 3 * 16;                 // per stage: absent keys, NaN value groups 0 and 1 (128 bits each)
-  static constexpr int kBytes = 1024 + 2 * kQ + 2 * kStage + 2 * kFlags + 256;
+  static constexpr int kFlags = 3 * 16;                 // of a tile: absent keys, NaN value groups 0 and 1 (128 bits each)
+  static constexpr int kBytes = 1024 + 2 * kQ + 2 * kStage + 4 * kFlags + 256;
   static_assert(kBytes <= 232448, "shared memory of one CTA");
 };
 
@@ -220,8 +220,20 @@ template <int NG>
 struct Raw {
   uint4 code[2 * NG];
   float scale[NG], mn[NG];
+  float vscale[NG];      // of its value, with K
   bool absent;           // the table has no page for it
 };
+template <int NG>
+__device__ __forceinline__ void load_meta(float (&v)[NG], const float* base, uint64_t at) {
+  const char* p = reinterpret_cast<const char*>(base) + at;
+  if (NG == 2) {
+    const float2 x = *reinterpret_cast<const float2*>(p);
+    v[0] = x.x;
+    v[NG - 1] = x.y;
+  } else {
+    v[0] = *reinterpret_cast<const float*>(p);
+  }
+}
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const AttnArgs<__half> a, const ClassPlan pl, uint32_t wait_limit) {
@@ -237,8 +249,8 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const AttnArgs<__half
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sQ = sm;
   uint8_t* sKV = sQ + 2 * S::kQ;
-  uint32_t* sFlags = reinterpret_cast<uint32_t*>(sKV + 2 * S::kStage);   // [stage][absent, nan 0, nan 1][4]
-  uint64_t* bars = reinterpret_cast<uint64_t*>(sKV + 2 * S::kStage + 2 * S::kFlags);
+  uint32_t* sFlags = reinterpret_cast<uint32_t*>(sKV + 2 * S::kStage);   // [tile % 4][absent, nan 0, nan 1][4]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sKV + 2 * S::kStage + 4 * S::kFlags);
   uint64_t* qfull = bars;         // [group] Q of the segment is in place
   uint64_t* kfull = bars + 2;     // [stage]
   uint64_t* kfree = bars + 4;
@@ -261,7 +273,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const AttnArgs<__half
       mbar_init(&vfull[i], 4);
       mbar_init(&kfree[i], 1);
       mbar_init(&vfree[i], 1);
-      mbar_init(&sfull[i], 1);
+      mbar_init(&sfull[i], 2);   // the commit, and the issuer itself: it has seen K's barrier, and so the tile's flags
       mbar_init(&pfull[i], 4);
       mbar_init(&odone[i], 1);
     }
@@ -286,46 +298,58 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const AttnArgs<__half
     int n = warp - kSoftWarps;
     Walk nx = k;             // at the tile of task `seen`, the next to be looked up
     int nxx = k.left > 0 ? k.x : 0, seen = n;
-    // the lane's key of task `seen`: the table's entry (not looked at before the load below) and its place in a page (-1: no
+    const int psl = a.pool.ps_log2, psm = (1 << psl) - 1;
+    const uint32_t page_codes = static_cast<uint32_t>(a.pool.heads) * (D / 2) << psl;   // bytes of a page in a codes array
+    const uint32_t page_meta = static_cast<uint32_t>(a.pool.heads) * (4 * NG) << psl;   // and in a (min or scale) array
+    // the segment's table row, its head's first row in a page, and the keys that its rows see
+    const int32_t* row = nullptr;
+    int head_row = 0, last = -1, lo = 0;
+    auto enter = [&]() {
+      row = a.tab.table + nx.i * a.tab.stride;
+      head_row = nx.h << psl;
+      last = min(nx.un.p1, nx.s.keys - 1);
+      lo = a.shape.window > 0 && nx.un.p0 >= a.shape.window ? nx.un.p0 - a.shape.window + 1 : 0;
+    };
+    if (tasks > 0) enter();
+    // the lane's key of task `seen`: the table's entry (not looked at before the load below) and its row in a page (-1: no
     // row of the unit sees the key)
     auto look_up = [&](int& page, int& off) {
       page = off = -1;
       if (seen >= tasks) return;
       const int j = (nx.sp.tile(nxx) << kKeysLog2) + 32 * (seen & 3) + lane;
-      const int last = min(nx.un.p1, nx.s.keys - 1);
-      const int lo = a.shape.window > 0 && nx.un.p0 >= a.shape.window ? nx.un.p0 - a.shape.window + 1 : 0;
       if (j <= last && (j >= lo || j < a.shape.sinks)) {
-        page = a.tab.table[nx.i * a.tab.stride + (j >> a.pool.ps_log2)];
-        off = (nx.h << a.pool.ps_log2) + (j & ((1 << a.pool.ps_log2) - 1));
+        page = row[j >> psl];
+        off = head_row + (j & psm);
       }
       // on by 7 tasks: a tile further, unless the task was a tile's first
       if ((seen & 7) != 0 && ++nxx == nx.x1) {
         walk_next(nx, a, pl);
         nxx = nx.x;
+        if (nx.left > 0) enter();
       }
       seen += kRestoreWarps;
     };
-    auto load = [&](Raw<NG>& v, int which, int page, int off) {
+    // K's task loads the scales of V too: it writes the tile's flags
+    auto load = [&](Raw<NG>& v, bool value, int page, int off) {
+#pragma unroll
+      for (int g = 0; g < NG; ++g) v.scale[g] = v.mn[g] = v.vscale[g] = 0.0f;
+      v.absent = false;
       if (off >= 0 && static_cast<uint32_t>(page) < static_cast<uint32_t>(a.tab.pages)) {
-        const int64_t slot = (static_cast<int64_t>(page) * a.pool.heads << a.pool.ps_log2) + off;
-        const uint4* c = reinterpret_cast<const uint4*>((which ? a.pool.codes[1] : a.pool.codes[0]) + slot * (D / 2));
-        const float* sc = (which ? a.pool.scales[1] : a.pool.scales[0]) + slot * NG;
-        const float* mn = (which ? a.pool.mins[1] : a.pool.mins[0]) + slot * NG;
+        const uint64_t at = static_cast<uint64_t>(static_cast<uint32_t>(page)) * page_codes + static_cast<uint32_t>(off) * (D / 2);
+        const uint64_t am = static_cast<uint64_t>(static_cast<uint32_t>(page)) * page_meta + static_cast<uint32_t>(off) * (4 * NG);
+        const uint4* c = reinterpret_cast<const uint4*>((value ? a.pool.codes[1] : a.pool.codes[0]) + at);
 #pragma unroll
         for (int e = 0; e < 2 * NG; ++e) v.code[e] = c[e];
-#pragma unroll
-        for (int g = 0; g < NG; ++g) {
-          v.scale[g] = sc[g];
-          v.mn[g] = mn[g];
-        }
-        v.absent = false;
+        load_meta(v.scale, value ? a.pool.scales[1] : a.pool.scales[0], am);
+        load_meta(v.mn, value ? a.pool.mins[1] : a.pool.mins[0], am);
+        if (!value) load_meta(v.vscale, a.pool.scales[1], am);
       } else {
 #pragma unroll
         for (int e = 0; e < 2 * NG; ++e) v.code[e] = make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-        for (int g = 0; g < NG; ++g) v.scale[g] = v.mn[g] = 0.0f;
-        v.absent = off >= 0;
-        if (v.absent) atomicOr(a.batch.err, DEV_ERR_PAGE);
+        if (off >= 0) {
+          v.absent = true;
+          atomicOr(a.batch.err, DEV_ERR_PAGE);
+        }
       }
     };
     auto restore = [&](Raw<NG>& v) {   // task n
@@ -335,17 +359,19 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const AttnArgs<__half
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) return false;
       if (value) {
-        const uint32_t absent = __ballot_sync(0xffffffffu, v.absent);
-        if (lane == 0) sFlags[st * 12 + quarter] = absent;
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          bool bad = false;
-          if (q < NG) {
-            bad = !(fabsf(v.scale[q]) < INFINITY);
-            if (bad) v.scale[q] = v.mn[q] = 0.0f;
-          }
-          const uint32_t m = __ballot_sync(0xffffffffu, bad);
-          if (lane == 0) sFlags[st * 12 + 4 * (q + 1) + quarter] = m;
+        for (int q = 0; q < NG; ++q)
+          if (!(fabsf(v.scale[q]) < INFINITY)) v.scale[q] = v.mn[q] = 0.0f;   // such a group is NaN: see its flag
+      } else {
+        // A slot of the ring is free: S of tile g - 2 is complete, so every softmax warp is past tile g - 4.
+        uint32_t* f = sFlags + (g & 3) * 12 + quarter;
+        const uint32_t absent = __ballot_sync(0xffffffffu, v.absent);
+        const uint32_t nan0 = __ballot_sync(0xffffffffu, !(fabsf(v.vscale[0]) < INFINITY));
+        const uint32_t nan1 = __ballot_sync(0xffffffffu, !(fabsf(v.vscale[NG - 1]) < INFINITY));
+        if (lane == 0) {
+          f[0] = absent;
+          f[4] = nan0;
+          f[8] = NG == 2 ? nan1 : 0u;
         }
       }
       uint8_t* p = sKV + st * S::kStage + (value ? S::kK : 0) + r * 128;
@@ -359,11 +385,11 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const AttnArgs<__half
     Raw<NG> r0, r1;
     int page, off;
     look_up(page, off);
-    load(r0, (n >> 2) & 1, page, off);
+    load(r0, n & 4, page, off);
     look_up(page, off);
     // task n from one buffer while the next one's codes come into the other
     auto turn = [&](Raw<NG>& now, Raw<NG>& then) {
-      load(then, ((n + kRestoreWarps) >> 2) & 1, page, off);
+      load(then, (n + kRestoreWarps) & 4, page, off);
       look_up(page, off);
       const bool ok = restore(now);
       n += kRestoreWarps;
@@ -384,6 +410,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const AttnArgs<__half
           const uint32_t off = ((kk / 4) * S::kPanel + (kk % 4) * 32) >> 4;
           mma_ss(tmem + 128 * grp, qa + off, ka + off, k_hi, kIdescS, kk > 0);
         }
+        mbar_arrive(&sfull[grp]);
         mma_commit(&sfull[grp]);
       };
       auto issue_o = [&](int grp, int g, bool first) {
@@ -477,24 +504,24 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const AttnArgs<__half
         __syncwarp();
         if (lane == 0) mbar_arrive(&qfull[grp]);
       }
+      const int whole_hi = min(k.un.p0, k.s.keys - 1) - (kKeys - 1), sink_hi = a.shape.sinks - kKeys;
+      const int whole_lo = a.shape.window > 0 ? k.un.p1 - a.shape.window + 1 : 0;
       float m = -INFINITY;
       float2 l2 = make_float2(0.0f, 0.0f);
       uint32_t nans = 0;
       for (int x = 0; x < tiles; ++x, ++cnt) {
         // tcgen05.ld/st are warp-collective: every branch around them is taken by the whole warp
         ok = mbar_wait(&sfull[grp], cnt & 1, wait_limit, abort_flag);
-        const int st = (g0 + x) & 1;
-        if (ok) ok = mbar_wait(&vfull[st], ((g0 + x) >> 1) & 1, wait_limit, abort_flag);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
         const int t0 = k.sp.tile(k.x + x) << kKeysLog2;
-        const uint4 ab = *reinterpret_cast<const uint4*>(sFlags + st * 12);
-        const uint4 n0 = *reinterpret_cast<const uint4*>(sFlags + st * 12 + 4), n1 = *reinterpret_cast<const uint4*>(sFlags + st * 12 + 8);
+        const uint32_t* flags = sFlags + ((g0 + x) & 3) * 12;
+        const uint4 ab = *reinterpret_cast<const uint4*>(flags);
+        const uint4 n0 = *reinterpret_cast<const uint4*>(flags + 4), n1 = *reinterpret_cast<const uint4*>(flags + 8);
         const bool odd = (ab.x | ab.y | ab.z | ab.w | n0.x | n0.y | n0.z | n0.w | n1.x | n1.y | n1.z | n1.w) != 0;
         // every row of the unit sees all of the tile
-        const bool whole = !odd && t0 + kKeys - 1 <= k.un.p0 && t0 + kKeys <= k.s.keys &&
-                           (a.shape.window == 0 || t0 > k.un.p1 - a.shape.window || t0 + kKeys <= a.shape.sinks);
+        const bool whole = !odd && t0 <= whole_hi && (t0 >= whole_lo || t0 <= sink_hi);
         uint32_t see[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
         if (!whole) {
           const int hi = min(p, k.s.keys - 1) - t0 + 1;                               // columns below it are not later than the row
