@@ -61,7 +61,7 @@ struct Smem {
   static constexpr int kQ = kPanels * kPanel;           // one group's
   static constexpr int kK = kPanels * kPanel;
   static constexpr int kStage = 2 * kK;                 // K, then V
-  static constexpr int kFlags = 3 * 16;                 // of a tile: absent keys, NaN value groups 0 and 1 (128 bits each)
+  static constexpr int kFlags = 4 * 16;                 // of a tile: whether any is set, absent keys, NaN value groups 0 and 1
   static constexpr int kBytes = 1024 + 2 * kQ + 2 * kStage + 4 * kFlags + 256;
   static_assert(kBytes <= 232448, "shared memory of one CTA");
 };
@@ -249,7 +249,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const AttnArgs<__half
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sQ = sm;
   uint8_t* sKV = sQ + 2 * S::kQ;
-  uint32_t* sFlags = reinterpret_cast<uint32_t*>(sKV + 2 * S::kStage);   // [tile % 4][absent, nan 0, nan 1][4]
+  uint32_t* sFlags = reinterpret_cast<uint32_t*>(sKV + 2 * S::kStage);   // [tile % 4][any, absent, nan 0, nan 1][4]
   uint64_t* bars = reinterpret_cast<uint64_t*>(sKV + 2 * S::kStage + 4 * S::kFlags);
   uint64_t* qfull = bars;         // [group] Q of the segment is in place
   uint64_t* kfull = bars + 2;     // [stage]
@@ -364,14 +364,15 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const AttnArgs<__half
           if (!(fabsf(v.scale[q]) < INFINITY)) v.scale[q] = v.mn[q] = 0.0f;   // such a group is NaN: see its flag
       } else {
         // A slot of the ring is free: S of tile g - 2 is complete, so every softmax warp is past tile g - 4.
-        uint32_t* f = sFlags + (g & 3) * 12 + quarter;
+        uint32_t* f = sFlags + (g & 3) * 16 + quarter;
         const uint32_t absent = __ballot_sync(0xffffffffu, v.absent);
         const uint32_t nan0 = __ballot_sync(0xffffffffu, !(fabsf(v.vscale[0]) < INFINITY));
         const uint32_t nan1 = __ballot_sync(0xffffffffu, !(fabsf(v.vscale[NG - 1]) < INFINITY));
         if (lane == 0) {
-          f[0] = absent;
-          f[4] = nan0;
-          f[8] = NG == 2 ? nan1 : 0u;
+          f[0] = absent | nan0 | nan1;
+          f[4] = absent;
+          f[8] = nan0;
+          f[12] = NG == 2 ? nan1 : 0u;
         }
       }
       uint8_t* p = sKV + st * S::kStage + (value ? S::kK : 0) + r * 128;
@@ -382,20 +383,15 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const AttnArgs<__half
       if (lane == 0) mbar_arrive(value ? &vfull[st] : &kfull[st]);
       return true;
     };
-    Raw<NG> r0, r1;
+    Raw<NG> v;
     int page, off;
     look_up(page, off);
-    load(r0, n & 4, page, off);
+    load(v, n & 4, page, off);
     look_up(page, off);
-    // task n from one buffer while the next one's codes come into the other
-    auto turn = [&](Raw<NG>& now, Raw<NG>& then) {
-      load(then, (n + kRestoreWarps) & 4, page, off);
-      look_up(page, off);
-      const bool ok = restore(now);
+    while (n < tasks && restore(v)) {
       n += kRestoreWarps;
-      return ok;
-    };
-    while (n < tasks && turn(r0, r1) && n < tasks && turn(r1, r0)) {
+      load(v, n & 4, page, off);   // on its way while the warp waits for the task's place
+      look_up(page, off);
     }
   } else if (warp == kMmaWarp) {
     // ---- MMA issuer --------------------------------------------------------------------
@@ -516,10 +512,9 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const AttnArgs<__half
         if (!ok) break;
         tc_fence_after();
         const int t0 = k.sp.tile(k.x + x) << kKeysLog2;
-        const uint32_t* flags = sFlags + ((g0 + x) & 3) * 12;
-        const uint4 ab = *reinterpret_cast<const uint4*>(flags);
-        const uint4 n0 = *reinterpret_cast<const uint4*>(flags + 4), n1 = *reinterpret_cast<const uint4*>(flags + 8);
-        const bool odd = (ab.x | ab.y | ab.z | ab.w | n0.x | n0.y | n0.z | n0.w | n1.x | n1.y | n1.z | n1.w) != 0;
+        const uint32_t* flags = sFlags + ((g0 + x) & 3) * 16;
+        const uint4 any = *reinterpret_cast<const uint4*>(flags);
+        const bool odd = (any.x | any.y | any.z | any.w) != 0;
         // every row of the unit sees all of the tile
         const bool whole = !odd && t0 <= whole_hi && (t0 >= whole_lo || t0 <= sink_hi);
         uint32_t see[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
@@ -527,12 +522,10 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const AttnArgs<__half
           const int hi = min(p, k.s.keys - 1) - t0 + 1;                               // columns below it are not later than the row
           const int lo = a.shape.window > 0 && p >= a.shape.window ? p - a.shape.window + 1 - t0 : 0;   // columns below it lie behind the window
           const int sk = a.shape.sinks - t0;
-          const uint32_t abs4[4] = {ab.x, ab.y, ab.z, ab.w};
-          const uint32_t n04[4] = {n0.x, n0.y, n0.z, n0.w}, n14[4] = {n1.x, n1.y, n1.z, n1.w};
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            see[c] = bits_below(hi - 32 * c) & (~bits_below(lo - 32 * c) | bits_below(sk - 32 * c)) & ~abs4[c];
-            nans |= ((see[c] & n04[c]) ? 1u : 0u) | ((see[c] & n14[c]) ? 2u : 0u);
+            see[c] = bits_below(hi - 32 * c) & (~bits_below(lo - 32 * c) | bits_below(sk - 32 * c)) & ~flags[4 + c];
+            nans |= ((see[c] & flags[8 + c]) ? 1u : 0u) | ((see[c] & flags[12 + c]) ? 2u : 0u);
           }
         }
         if (!whole) {   // what the row does not see becomes -inf, in place
