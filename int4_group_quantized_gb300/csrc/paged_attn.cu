@@ -2,8 +2,9 @@
 // notes, "背景知识": Softmax(x_Q x_K^T / sqrt(h1)) x_V per head, causal; "5.
 // 近似方法": K and V stored in 4-bit groups of 64).
 //
-// A first form: one warp per (row, query head), its lanes along the head
-// dimension, one key at a time with a running maximum and sum.
+// Here: the plan that deals the work out, the joining of partials, the
+// workspace and the entry point.  The kernels: paged_step.cu (fp16, sequences
+// of few rows), paged_tile.cu (fp16, longer chunks), paged_f32.cu.
 #include <math.h>
 #include <string.h>
 
@@ -16,73 +17,8 @@ namespace fg {
 namespace paged {
 namespace {
 
-__device__ __forceinline__ float to_f(float x) { return x; }
-__device__ __forceinline__ float to_f(__half x) { return __half2float(x); }
 __device__ __forceinline__ void put(float* p, float x) { *p = x; }
 __device__ __forceinline__ void put(__half* p, float x) { *p = __float2half_rn(x); }
-
-template <typename T, int D>
-__global__ void __launch_bounds__(128) attn_rows_kernel(const AttnArgs<T> a) {
-  constexpr int E = D / 32;   // dims of a lane
-  constexpr int NG = D / 64;
-  const int lane = threadIdx.x & 31;
-  const int64_t w = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-  if (blockIdx.x == 0)   // what no row would notice: offsets that run backwards
-    for (int i = threadIdx.x; i < a.tab.seqs; i += blockDim.x) seq_of(a.tab, a.batch, i);
-  const int64_t r64 = w / a.q_heads;
-  if (r64 >= a.batch.ntok) return;
-  const int r = static_cast<int>(r64), qh = static_cast<int>(w % a.q_heads), h = qh / a.shape.group;
-  const int i = seq_of_row(a.batch.cu, a.tab.seqs, r);
-  if (i >= a.tab.seqs) return;
-  const Seq s = seq_of(a.tab, a.batch, i);
-  if (r < s.row0 || r >= s.row0 + s.n) return;
-  if (s.n > a.shape.max_q) {
-    atomicOr(a.batch.err, DEV_ERR_BATCH);
-    return;
-  }
-  const int64_t pos = static_cast<int64_t>(s.len) - s.n + (r - s.row0);
-  const int64_t lo = a.shape.window > 0 && pos - a.shape.window + 1 > 0 ? pos - a.shape.window + 1 : 0;
-  float q[E], o[E];
-#pragma unroll
-  for (int e = 0; e < E; ++e) {
-    q[e] = to_f(a.q[r * a.ldq + qh * D + lane * E + e]) * a.scale;
-    o[e] = 0.0f;
-  }
-  float m = -INFINITY, l = 0.0f;
-  const int g = lane * E / 64;
-  for (int64_t j = 0; j <= pos && j < s.keys; ++j) {
-    if (j < lo && j >= a.shape.sinks) {
-      j = lo - 1;
-      continue;
-    }
-    const int page = page_of(a.tab, i, static_cast<int>(j));
-    if (page < 0) {
-      if (lane == 0) atomicOr(a.batch.err, DEV_ERR_PAGE);
-      continue;
-    }
-    const int64_t sl = slot_of(a.pool, page, h, static_cast<int>(j));
-    auto value = [&](int which, int e) {
-      const int c = lane * E + e;
-      const int byte = a.pool.codes[which][sl * (D / 2) + c / 2];
-      return fmaf(static_cast<float>((byte >> (4 * (c & 1))) & 15), a.pool.scales[which][sl * NG + g],
-                  a.pool.mins[which][sl * NG + g]);
-    };
-    float x = 0.0f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) x += q[e] * value(0, e);
-#pragma unroll
-    for (int f = 16; f > 0; f >>= 1) x += __shfl_xor_sync(0xffffffffu, x, f);
-    const float nm = fmaxf(m, x);
-    const float base = nm == -INFINITY ? 0.0f : nm;
-    const float alpha = expf(m - base), p = expf(x - base);
-    l = l * alpha + p;
-#pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = o[e] * alpha + p * value(1, e);
-    m = nm;
-  }
-#pragma unroll
-  for (int e = 0; e < E; ++e) put(a.out + r * a.ldo + qh * D + lane * E + e, l != 0.0f ? o[e] / l : 0.0f);
-}
 
 // ---- the plan -------------------------------------------------------------------
 // One CTA: the tiles of every sequence, class by class, as prefix sums, and
@@ -110,7 +46,7 @@ __device__ __forceinline__ int64_t units_cost(const Seq& s, const AttnShape& sh,
   return c;
 }
 
-template <int TRU, int TKTL, int TSPLIT_MIN>
+template <int TRU, int TKTL>
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
   __shared__ int64_t warp_sum[2][32];
   __shared__ int warp_max[2][32];
@@ -149,7 +85,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
           int64_t share = (total + p.workers - 1) / p.workers;
           const int64_t least = (mx + kMaxSplits - 1) / kMaxSplits;
           share = share > least ? share : least;
-          const int64_t few = c ? TSPLIT_MIN : 2;
+          const int64_t few = c ? 1 : 2;   // a step's share: at least 64 tokens
           p.head[0] = total;
           p.head[1] = share > few ? share : few;
           p.pre[seqs] = total;
@@ -358,7 +294,9 @@ Layout layout_of(const fg_page_pool& pool, const fg_page_table& t, int32_t q_hea
     const int rows = most <= 8 ? 8 : kStepRows;
     carve_class(l.step, p, t.seqs, pool.head_dim, step_workers(rows, sms), step_workers(rows, kMaxSms), rows);
   }
-  if (pool.dtype == FG_F16 && most > (l.step.workers ? kStepRows : 0))
+  if (pool.dtype == FG_F32)
+    carve_class(l.tile, p, t.seqs, pool.head_dim, f32_workers(pool.head_dim, sms), f32_workers(pool.head_dim, kMaxSms), kF32Rows);
+  else if (most > (l.step.workers ? kStepRows : 0))
     carve_class(l.tile, p, t.seqs, pool.head_dim, sms, kMaxSms, kTileRows);
   l.bytes = static_cast<size_t>(p - static_cast<char*>(ws)) + 256;
   return l;
@@ -386,15 +324,17 @@ fg_status launch_attn(const fg_page_pool& pool, const fg_page_table& t, const in
   a.shape.window = window > (int64_t(1) << 30) ? 0 : static_cast<int>(window);
   a.shape.sinks = static_cast<int>(std::min<int64_t>(sinks, int64_t(1) << 30));
   const Layout l = layout_of(pool, t, q_heads, max_q, ws, std::min(num_sms(), kMaxSms));
-  if constexpr (sizeof(T) == 2) {
+  constexpr bool half = sizeof(T) == 2;
+  const bool wide = pool.head_dim == 128;
+  {
     PlanArgs p{a.tab, a.batch, a.shape, pool.heads, l.step, l.tile};
-    {
-      Trace tr(KC_ATTN_PAGED_PLAN, st);
-      const unsigned threads = static_cast<unsigned>(std::min<int64_t>(kPlanThreads, (t.seqs + 31) / 32 * 32));
-      plan_kernel<kTileRows, 7, 1><<<1, threads, 0, st>>>(p);
-      FG_TRY(check_launch("plan_kernel"));
-    }
-    const bool wide = pool.head_dim == 128;
+    Trace tr(KC_ATTN_PAGED_PLAN, st);
+    const unsigned threads = static_cast<unsigned>(std::min<int64_t>(kPlanThreads, (t.seqs + 31) / 32 * 32));
+    if (half) plan_kernel<kTileRows, 7><<<1, threads, 0, st>>>(p);
+    else plan_kernel<kF32Rows, kF32KeysLog2><<<1, threads, 0, st>>>(p);
+    FG_TRY(check_launch("plan_kernel"));
+  }
+  if constexpr (half) {
     if (l.step.workers > 0) {
       FG_TRY(paged_attention_step(a, l.step, pool.head_dim, st));
       FG_TRY((wide ? join<T, 128, kStepRows>(a, l.step, st) : join<T, 64, kStepRows>(a, l.step, st)));
@@ -403,15 +343,11 @@ fg_status launch_attn(const fg_page_pool& pool, const fg_page_table& t, const in
       FG_TRY(paged_attention_tile(a, l.tile, pool.head_dim, st));
       FG_TRY((wide ? join<T, 128, kTileRows>(a, l.tile, st) : join<T, 64, kTileRows>(a, l.tile, st)));
     }
-    return FG_OK;
   } else {
-    const int64_t warps = ntok * q_heads;
-    const unsigned grid = static_cast<unsigned>((warps + 3) / 4);
-    Trace tr(KC_ATTN_PAGED, st);
-    if (pool.head_dim == 128) attn_rows_kernel<T, 128><<<grid, 128, 0, st>>>(a);
-    else attn_rows_kernel<T, 64><<<grid, 128, 0, st>>>(a);
-    return check_launch("attn_rows_kernel");
+    FG_TRY(paged_attention_f32(a, l.tile, pool.head_dim, st));
+    FG_TRY((wide ? join<T, 128, kF32Rows>(a, l.tile, st) : join<T, 64, kF32Rows>(a, l.tile, st)));
   }
+  return FG_OK;
 }
 
 fg_status check_attn(const fg_page_pool* pool, const fg_page_table* t, int32_t q_heads, int64_t ntok, int64_t max_q) {

@@ -29,5 +29,11 @@ fg_status paged_attention_step(const AttnArgs<__half>& a, const ClassPlan& pl, i
 constexpr int kTileRows = 256;
 fg_status paged_attention_tile(const AttnArgs<__half>& a, const ClassPlan& pl, int head_dim, cudaStream_t st);
 
+
+// fp32 activations, every sequence: units of kF32Rows rows, tiles of 64 keys.
+constexpr int kF32Rows = 16, kF32KeysLog2 = 6;
+int f32_workers(int head_dim, int sms);
+fg_status paged_attention_f32(const AttnArgs<float>& a, const ClassPlan& pl, int head_dim, cudaStream_t st);
+
 }  // namespace paged
 }  // namespace fg
