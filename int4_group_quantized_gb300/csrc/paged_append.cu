@@ -4,21 +4,14 @@
 // sequence's pages, and on request comes back as the cache restores it.
 #include "codec_dev.cuh"
 #include "paged.cuh"
+#include "q4_dev.cuh"
 
 namespace fg {
 namespace paged {
 namespace {
 
-__device__ __forceinline__ void load8(const __half* p, float (&v)[8]) {
-  const uint4 raw = *reinterpret_cast<const uint4*>(p);
-  const __half2* h = reinterpret_cast<const __half2*>(&raw);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 f = __half22float2(h[i]);
-    v[2 * i] = f.x;
-    v[2 * i + 1] = f.y;
-  }
-}
+using q4::fma_f32x2;
+
 __device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
   const float4 a = *reinterpret_cast<const float4*>(p);
   const float4 b = *reinterpret_cast<const float4*>(p + 4);
@@ -47,30 +40,149 @@ struct AppendArgs {
   int64_t ld, ldr;
 };
 
-// A warp owns one (K or V, head) and a run of 16 batch rows, 8 lanes to a
-// 64-group.
-constexpr int kRun = 16;
+// ---- one 64-group over 8 lanes, 8 values a lane --------------------------------
+// Smallest and largest of the non-NaN values of a group, in the codec's order
+// (-0 < +0; both NaN for a group of NaN), on all of its 8 lanes.
+//
+// fp16: the type's own minimum skips NaN and puts -0 below +0, and the largest
+// is the negated minimum of the negated values, so both travel in one word.
+struct Half8 {
+  uint4 raw;
+  __device__ __forceinline__ void load(const __half* p) { raw = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void clear() { raw = make_uint4(0u, 0u, 0u, 0u); }
+  __device__ __forceinline__ float get(int e) const {
+    const uint32_t w = (e >> 1) == 0 ? raw.x : (e >> 1) == 1 ? raw.y : (e >> 1) == 2 ? raw.z : raw.w;
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
+    return (e & 1) ? f.y : f.x;
+  }
+  __device__ __forceinline__ void bounds(float& mn, float& mx) const {
+    const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+    uint32_t lo = min2(min2(w[0], w[1]), min2(w[2], w[3]));
+    uint32_t hi = min2(min2(w[0] ^ kSigns, w[1] ^ kSigns), min2(w[2] ^ kSigns, w[3] ^ kSigns));
+    uint32_t both = min2(__byte_perm(lo, hi, 0x5410), __byte_perm(lo, hi, 0x7632));   // (min, -max)
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) both = min2(both, __shfl_xor_sync(0xffffffffu, both, o));
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&both));
+    mn = f.x;
+    mx = -f.y;
+  }
+  static constexpr uint32_t kSigns = 0x80008000u;
+  static __device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("min.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+  }
+};
+// fp32: through the codec's order-preserving keys.
+struct Float8 {
+  float v[8];
+  __device__ __forceinline__ void load(const float* p) { load8(p, v); }
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = 0.0f;
+  }
+  __device__ __forceinline__ float get(int e) const { return v[e]; }
+  __device__ __forceinline__ void bounds(float& mn, float& mx) const {
+    uint32_t lo = 0xffffffffu, hi = 0u;
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (!isnan(v[e])) {
+        const uint32_t key = codec::order_key(v[e]);
+        lo = min(lo, key);
+        hi = max(hi, key);
+      }
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) {
+      lo = min(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+      hi = max(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+    }
+    codec::group_bounds(lo, hi, mn, mx);
+  }
+};
+template <typename T>
+struct Vec8 {
+  using type = Float8;
+};
+template <>
+struct Vec8<__half> {
+  using type = Half8;
+};
+
+__device__ __forceinline__ float2 add_f32x2(float2 a, float2 b) {
+  float2 r;
+  asm("{ .reg .b64 x, y; mov.b64 x, {%2, %3}; mov.b64 y, {%4, %5};\n"
+      "add.rn.f32x2 x, x, y; mov.b64 {%0, %1}, x; }"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+__device__ __forceinline__ float2 mul_f32x2(float2 a, float2 b) {
+  float2 r;
+  asm("{ .reg .b64 x, y; mov.b64 x, {%2, %3}; mov.b64 y, {%4, %5};\n"
+      "mul.rn.f32x2 x, x, y; mov.b64 {%0, %1}, x; }"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+
+// The codes of 8 values as floats, by the codec's short form (code_fast in
+// codec_dev.cuh: one product by 15 / r, rounded by adding 1.5 * 2^23), two at a
+// time; q[e] holds values e and e + 4.  Returns how near the nearest value
+// comes to a rounding boundary, as |u - rint(u)| (1/2 on it).
+__device__ __forceinline__ float codes_fast(const float2 (&v)[4], float mn, float c15, float2 (&q)[4]) {
+  const float2 nmn = make_float2(-mn, -mn), c2 = make_float2(c15, c15);
+  const float2 up = make_float2(codec::kRound, codec::kRound), down = make_float2(-codec::kRound, -codec::kRound);
+  float far = 0.0f;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    float2 u = mul_f32x2(add_f32x2(v[e], nmn), c2);
+    u = make_float2(fmaxf(u.x, 0.0f), fmaxf(u.y, 0.0f));   // NaN counts as 0; no value exceeds 15 (1 + 2^-23)
+    q[e] = add_f32x2(add_f32x2(u, up), down);
+    const float2 t = add_f32x2(u, make_float2(-q[e].x, -q[e].y));
+    far = fmaxf(far, fmaxf(fabsf(t.x), fabsf(t.y)));
+  }
+  return far;
+}
+// 8 codes (q[e] = codes e, e + 4) as a word, low nibble first: sums of multiples
+// of 16^e below 2^16, exact in fp32.
+__device__ __forceinline__ uint32_t pack_codes(const float2 (&q)[4]) {
+  const float2 k16 = make_float2(16.0f, 16.0f);
+  float2 s = q[3];
+#pragma unroll
+  for (int e = 2; e >= 0; --e) s = fma_f32x2(s, k16, q[e]);
+  s = add_f32x2(s, make_float2(8388608.0f, 8388608.0f));   // 2^23: the sum in the low mantissa bits
+  return __byte_perm(__float_as_uint(s.x), __float_as_uint(s.y), 0x5410);
+}
+
+// A warp takes a run of rows (8 batches of 4 groups: 16 rows of two groups a
+// head, 32 rows of one) and some of the 2 * heads (K or V, head) slices.  The
+// run's slots are found once; a slice's rows are loaded together; after the
+// batches' minima and maxima every lane holds one of the 32 groups and takes
+// its two divisions (the literal form spent two per lane and batch); then the
+// batches are coded with their group's numbers from that lane.
+template <int NG>
+constexpr int kRun = 32 / NG;
+constexpr int kBatches = 8;
 
 template <typename T, int NG>
-__global__ void __launch_bounds__(256) append_kernel(const AppendArgs<T> a) {
+__global__ void __launch_bounds__(256) append_kernel(const AppendArgs<T> a, int slices) {
   constexpr int D = 64 * NG;
-  constexpr int kTpi = 4 / NG;   // rows per warp-wide batch
+  constexpr uint32_t kNone = 0xffffffffu;
   const int lane = threadIdx.x & 31;
-  const int part = lane & 7, gi = (lane >> 3) % NG, tb = lane / (8 * NG);
-  const int64_t runs = (a.batch.ntok + kRun - 1) / kRun;
-  const int64_t items = 2 * runs * a.pool.heads;
+  const int part = lane & 7, gi = (lane >> 3) % NG, rb = (lane >> 3) / NG;   // row of a batch
+  const int heads = a.pool.heads, psl = a.pool.ps_log2;
+  const int64_t runs = (a.batch.ntok + kRun<NG> - 1) / kRun<NG>;
+  const int chunks = (2 * heads + slices - 1) / slices;
   const int64_t warp = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
   const int64_t nwarps = (static_cast<int64_t>(gridDim.x) * blockDim.x) >> 5;
   if (blockIdx.x == 0)   // what no row would notice: offsets that run backwards
     for (int i = threadIdx.x; i < a.tab.seqs; i += blockDim.x) seq_of(a.tab, a.batch, i);
-  for (int64_t it = warp; it < items; it += nwarps) {
-    const int64_t run = it % runs;
-    const int h = static_cast<int>((it / runs) % a.pool.heads);
-    const int which = static_cast<int>(it / (runs * a.pool.heads));
-    // lane r < 16 finds the slot of row r of the run
-    int64_t slot = -1;
-    const int64_t row0 = run * kRun;
-    if (lane < kRun && row0 + lane < a.batch.ntok) {
+  for (int64_t it = warp; it < runs * chunks; it += nwarps) {
+    const int64_t row0 = it / chunks * kRun<NG>;
+    const int s0 = static_cast<int>(it % chunks) * slices, s1 = min(2 * heads, s0 + slices);
+    // lane r finds the token of the pool that row r of the run goes to
+    uint32_t token = kNone;
+    if (lane < kRun<NG> && row0 + lane < a.batch.ntok) {
       const int r = static_cast<int>(row0 + lane);
       const int i = seq_of_row(a.batch.cu, a.tab.seqs, r);
       if (i < a.tab.seqs) {
@@ -82,40 +194,79 @@ __global__ void __launch_bounds__(256) append_kernel(const AppendArgs<T> a) {
           } else {
             const int page = page_of(a.tab, i, pos);
             if (page < 0) atomicOr(a.batch.err, DEV_ERR_PAGE);
-            else slot = slot_of(a.pool, page, h, pos);
+            else token = (static_cast<uint32_t>(page) << psl) + (pos & ((1 << psl) - 1));
           }
         }
       }
     }
-    const T* src = (which ? a.src[1] : a.src[0]) + h * D + gi * 64 + part * 8;
-    T* res = which ? a.restored[1] : a.restored[0];
-    uint8_t* codes = which ? a.pool.codes[1] : a.pool.codes[0];
-    float* mins = which ? a.pool.mins[1] : a.pool.mins[0];
-    float* scales = which ? a.pool.scales[1] : a.pool.scales[0];
+    for (int sl = s0; sl < s1; ++sl) {
+      const bool value = sl >= heads;
+      const int h = value ? sl - heads : sl;
+      const int col = h * D + gi * 64 + part * 8;
+      const T* src = (value ? a.src[1] : a.src[0]) + row0 * a.ld + col;
+      typename Vec8<T>::type x[kBatches];
 #pragma unroll
-    for (int t0 = 0; t0 < kRun; t0 += kTpi) {
-      const int t = t0 + tb;
-      const int64_t sl = __shfl_sync(0xffffffffu, slot, t);
-      float v[8];
-      if (sl >= 0) {
-        load8(src + (row0 + t) * a.ld, v);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = 0.0f;
+      for (int b = 0; b < kBatches; ++b) {
+        const int t = b * (4 / NG) + rb;
+        if (__shfl_sync(0xffffffffu, token, t) != kNone) x[b].load(src + t * a.ld);
+        else x[b].clear();
       }
-      float mn, sc;
-      const uint32_t packed = codec::quantize_group8(v, mn, sc);
-      if (sl >= 0) {
-        *reinterpret_cast<uint32_t*>(codes + sl * (D / 2) + gi * 32 + part * 4) = packed;
-        if (part == 0) {
-          mins[sl * NG + gi] = mn;
-          scales[sl * NG + gi] = sc;
-        }
-        if (res != nullptr) {
-          float r[8];
+      // lane 8 g + b keeps group g of batch b
+      float mn = 0.0f, mx = 0.0f;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) r[e] = __fmaf_rn(codec::code_float((packed >> (4 * e)) & 15u), sc, mn);
-          store8(res + (row0 + t) * a.ldr + h * D + gi * 64 + part * 8, r);
+      for (int b = 0; b < kBatches; ++b) {
+        float lo, hi;
+        x[b].bounds(lo, hi);
+        if (part == b) {
+          mn = lo;
+          mx = hi;
+        }
+      }
+      if (isnan(mn)) mn = mx = __uint_as_float(0x7fffffffu);   // the codec's NaN
+      const float r = __fsub_rn(mx, mn), c15 = __fdiv_rn(15.0f, r), scale = __fdiv_rn(r, 15.0f);
+      const bool fast = r > 0.0f && r < INFINITY && c15 < INFINITY;
+      const uint32_t fasts = __ballot_sync(0xffffffffu, fast);
+      uint8_t* codes = value ? a.pool.codes[1] : a.pool.codes[0];
+      // row of the pool's arrays that a token's slice of head h lies in
+      auto slot = [&](uint32_t tok) {
+        return ((static_cast<int64_t>(tok >> psl) * heads + h) << psl) + (tok & ((1u << psl) - 1));
+      };
+      {
+        const uint32_t tok = __shfl_sync(0xffffffffu, token, part * (4 / NG) + rb);
+        if (tok != kNone) {
+          const int64_t at = slot(tok) * NG + gi;
+          (value ? a.pool.mins[1] : a.pool.mins[0])[at] = mn;
+          (value ? a.pool.scales[1] : a.pool.scales[0])[at] = scale;
+        }
+      }
+      T* res = value ? a.restored[1] : a.restored[0];
+#pragma unroll
+      for (int b = 0; b < kBatches; ++b) {
+        const int from = (lane & 24) + b, t = b * (4 / NG) + rb;
+        const float bmn = __shfl_sync(0xffffffffu, mn, from), bc = __shfl_sync(0xffffffffu, c15, from), br = __shfl_sync(0xffffffffu, r, from);
+        const uint32_t tok = __shfl_sync(0xffffffffu, token, t);
+        float2 v[4], q[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = make_float2(x[b].get(e), x[b].get(e + 4));
+        const float far = codes_fast(v, bmn, bc, q);
+        const bool near = far > 0.5f - 1e-5f;
+        if (near || !((fasts >> from) & 1u)) {   // rare: within 1e-5 of a boundary, or a range that has no finite 15 / r
+#pragma unroll
+          for (int e = 0; e < 4; ++e) q[e] = make_float2(codec::code_exact(v[e].x, bmn, br), codec::code_exact(v[e].y, bmn, br));
+        }
+        if (tok != kNone)
+          *reinterpret_cast<uint32_t*>(codes + slot(tok) * (D / 2) + gi * 32 + part * 4) = pack_codes(q);
+        if (res != nullptr) {
+          const float bs = __shfl_sync(0xffffffffu, scale, from);
+          const float2 s2 = make_float2(bs, bs), m2 = make_float2(bmn, bmn);
+          float o[8];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 y = fma_f32x2(q[e], s2, m2);
+            o[e] = y.x;
+            o[e + 4] = y.y;
+          }
+          if (tok != kNone) store8(res + (row0 + t) * a.ldr + col, o);
         }
       }
     }
@@ -136,12 +287,17 @@ fg_status launch_append(const fg_page_pool& pool, const fg_page_table& t, const 
   a.restored[1] = static_cast<T*>(vr);
   a.ld = ld;
   a.ldr = ldr;
-  const int64_t items = 2 * ((ntok + kRun - 1) / kRun) * pool.heads;
-  const int64_t want = (items + 7) / 8, cap = static_cast<int64_t>(num_sms()) * 8;
+  // as many slices a warp as leave every SM its 16 warps, so that a run's slots are looked up no oftener than need be
+  const int run = pool.head_dim == 128 ? kRun<2> : kRun<1>;
+  const int64_t runs = (ntok + run - 1) / run, warps = static_cast<int64_t>(num_sms()) * 16;
+  const int64_t fit = runs * 2 * pool.heads / warps;
+  const int slices = static_cast<int>(fit < 1 ? 1 : fit > 8 ? 8 : fit);
+  const int64_t items = runs * ((2 * pool.heads + slices - 1) / slices);
+  const int64_t want = (items + 7) / 8, cap = static_cast<int64_t>(num_sms()) * 16;
   const unsigned grid = static_cast<unsigned>(want < cap ? want : cap);
   Trace tr(KC_KV_STORE, st);
-  if (pool.head_dim == 128) append_kernel<T, 2><<<grid, 256, 0, st>>>(a);
-  else append_kernel<T, 1><<<grid, 256, 0, st>>>(a);
+  if (pool.head_dim == 128) append_kernel<T, 2><<<grid, 256, 0, st>>>(a, slices);
+  else append_kernel<T, 1><<<grid, 256, 0, st>>>(a, slices);
   return check_launch("append_kernel");
 }
 
@@ -157,6 +313,7 @@ extern "C" fg_status fg_paged_append(const fg_page_pool* pool, const fg_page_tab
                                      void* v_restored, int64_t ldr, cudaStream_t stream) {
   FG_TRY(check_pool_table(pool, t));
   if (ntok < 0) return fail(FG_ERR_ARG, "negative row count");
+  if (pool->pages * pool->page_size >= UINT32_MAX) return fail(FG_ERR_UNSUPPORTED, "a pool of 2^32 tokens or more");
   if (ntok > INT32_MAX - 256) return fail(FG_ERR_UNSUPPORTED, "more than 2^31 rows");
   if (ntok == 0 || t->seqs == 0) return FG_OK;
   if (!cu || !k || !v) return fail(FG_ERR_ARG, "null pointer");
