@@ -646,6 +646,7 @@ class PageTable:
         if table.dim() != 2 or refs.dim() != 1:
             raise ValueError("table is [seqs][stride], refs [pages]")
         self.device = table.device
+        self.index = table.device.index if table.device.type == "cuda" else None
         self.table = _dense(table, torch.int32, table.shape, self.device, "table")
         self.lens = _dense(lens, torch.int32, (table.shape[0],), self.device, "lens")
         self.refs = _dense(refs, torch.int32, refs.shape, self.device, "refs")
@@ -668,9 +669,10 @@ class PageTable:
 
 def _on(tab: "PageTable", stream) -> int:
     """The stream of a paged call; its buffers must be on the current device."""
-    if tab.device.type == "cuda" and tab.device.index != torch.cuda.current_device():
+    i = tab.index
+    if i is not None and i != torch._C._cuda_getDevice():
         raise ValueError(f"the page table is on {tab.device}, the current device is {torch.cuda.current_device()}")
-    return _stream(stream)
+    return torch._C._cuda_getCurrentRawStream(i) if stream is None and i is not None else _stream(stream)
 
 
 def _paged_ws(nbytes: int, tab: "PageTable", stream) -> torch.Tensor:
@@ -682,22 +684,22 @@ def _paged_ws(nbytes: int, tab: "PageTable", stream) -> torch.Tensor:
     return ws
 
 
-def _ints(t: torch.Tensor, n, tab: "PageTable", name: str) -> int:
-    return _dense(t, torch.int32, (t.numel() if n is None else n,), tab.device, name).data_ptr()
+def _ints(t: torch.Tensor, n: int, tab: "PageTable", name: str) -> int:
+    if t.dtype is not torch.int32 or t.numel() != n or not t.is_contiguous() or t.device != tab.device:
+        raise ValueError(f"{name}: expected {n} contiguous int32 on {tab.device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
 
 
-def _rows(t: torch.Tensor, pool: "PagePool", n, cols: int, name: str) -> torch.Tensor:
-    """t, when it is [n][cols] rows of the pool's type and device with unit column stride."""
-    if (t.dim() != 2 or t.dtype != pool.dtype or t.device != pool.device or t.shape[1] != cols
-            or (n is not None and t.shape[0] != n) or (cols > 1 and t.stride(1) != 1)):
-        raise ValueError(f"{name}: expected {pool.dtype} rows [{'n' if n is None else n}][{cols}] on {pool.device}, got "
-                         f"{t.dtype} {tuple(t.shape)} strides {t.stride()} on {t.device}")
-    return t
-
-
-def _ld(t: torch.Tensor) -> int:
-    """Row stride (a single row's own is any)."""
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+def _rows(t: torch.Tensor, pool: "PagePool", n: int, cols: int, name: str) -> int:
+    """Row stride of t, when it is [n][cols] rows of the pool's type and device with unit column stride."""
+    shape = t.shape
+    if len(shape) != 2 or shape[0] != n or shape[1] != cols or t.dtype is not pool.dtype or t.device != pool.device:
+        raise ValueError(f"{name}: expected {pool.dtype} rows [{n}][{cols}] on {pool.device}, got {t.dtype} {tuple(shape)} "
+                         f"on {t.device}")
+    ld, unit = t.stride()
+    if unit != 1 and cols > 1:
+        raise ValueError(f"{name}: columns must be adjacent, strides are {t.stride()}")
+    return ld if n > 1 else max(ld, cols)   # a single row's own stride is any
 
 
 def fg_pages_workspace_bytes(tab: PageTable, n: int = 0) -> int:
@@ -715,7 +717,7 @@ def fg_pages_reserve(tab: PageTable, cu: torch.Tensor, ws: torch.Tensor | None =
 
 def fg_pages_free(tab: PageTable, rows: torch.Tensor, stream=None) -> None:
     """Ends the sequences rows (int32)."""
-    _check(_lib.fg_pages_free(tab._ref, _ints(rows, None, tab, "rows"), rows.numel(), _on(tab, stream)), "fg_pages_free")
+    _check(_lib.fg_pages_free(tab._ref, _ints(rows, rows.numel(), tab, "rows"), rows.numel(), _on(tab, stream)), "fg_pages_free")
 
 
 def fg_pages_fork(tab: PageTable, pools: PagePools, src: torch.Tensor, dst: torch.Tensor,
@@ -743,18 +745,14 @@ def fg_paged_append(pool: PagePool, tab: PageTable, cu: torch.Tensor, k: torch.T
     given, receive the rows as the cache restores them."""
     h1 = pool.heads * pool.head_dim
     n = k.shape[0]
-    _rows(k, pool, None, h1, "k")
-    _rows(v, pool, n, h1, "v")
-    if n > 1 and v.stride(0) != k.stride(0):
+    ld, ldr = _rows(k, pool, n, h1, "k"), 0
+    if _rows(v, pool, n, h1, "v") != ld:
         raise ValueError("k and v need one row stride")
-    ldr = 0
     if k_restored is not None and v_restored is not None:
-        _rows(k_restored, pool, n, h1, "k_restored")
-        _rows(v_restored, pool, n, h1, "v_restored")
-        ldr = _ld(k_restored)
-        if n > 1 and v_restored.stride(0) != k_restored.stride(0):
+        ldr = _rows(k_restored, pool, n, h1, "k_restored")
+        if _rows(v_restored, pool, n, h1, "v_restored") != ldr:
             raise ValueError("k_restored and v_restored need one row stride")
-    _check(_lib.fg_paged_append(pool._ref, tab._ref, _ints(cu, tab.seqs + 1, tab, "cu"), _ptr(k), _ptr(v), _ld(k), n,
+    _check(_lib.fg_paged_append(pool._ref, tab._ref, _ints(cu, tab.seqs + 1, tab, "cu"), k.data_ptr(), v.data_ptr(), ld, n,
                                 _ptr(k_restored), _ptr(v_restored), ldr, _on(tab, stream)), "fg_paged_append")
 
 
@@ -768,10 +766,10 @@ def fg_paged_attention(pool: PagePool, tab: PageTable, cu: torch.Tensor, q: torc
     """out rows = causal attention of the ragged batch's rows q [ntok][q_heads*head_dim] over their sequences' pages
     (window > 0: the last `window` tokens and the first `sinks`)."""
     n = q.shape[0]
-    _rows(q, pool, None, q_heads * pool.head_dim, "q")
-    _rows(out, pool, n, q_heads * pool.head_dim, "out")
+    ldq = _rows(q, pool, n, q_heads * pool.head_dim, "q")
+    ldo = _rows(out, pool, n, q_heads * pool.head_dim, "out")
     if ws is None:
         ws = _paged_ws(fg_paged_attention_workspace_bytes(pool, tab, q_heads, n, max_q), tab, stream)
-    _check(_lib.fg_paged_attention(pool._ref, tab._ref, _ints(cu, tab.seqs + 1, tab, "cu"), _ptr(q), _ld(q),
-                                   int(q_heads), n, int(max_q), int(window), int(sinks), _ptr(out), _ld(out), _ptr(ws),
-                                   ws.numel(), _on(tab, stream)), "fg_paged_attention")
+    _check(_lib.fg_paged_attention(pool._ref, tab._ref, _ints(cu, tab.seqs + 1, tab, "cu"), q.data_ptr(), ldq, q_heads, n,
+                                   max_q, window, sinks, out.data_ptr(), ldo, ws.data_ptr(), ws.numel(), _on(tab, stream)),
+           "fg_paged_attention")

@@ -125,23 +125,31 @@ __device__ __forceinline__ float2 mul_f32x2(float2 a, float2 b) {
   return r;
 }
 
+__device__ __forceinline__ float max_nan(float a, float b) {   // NaN if either is
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
+
 // The codes of 8 values as floats, by the codec's short form (code_fast in
-// codec_dev.cuh: one product by 15 / r, rounded by adding 1.5 * 2^23), two at a
-// time; q[e] holds values e and e + 4.  Returns how near the nearest value
-// comes to a rounding boundary, as |u - rint(u)| (1/2 on it).
-__device__ __forceinline__ float codes_fast(const float2 (&v)[4], float mn, float c15, float2 (&q)[4]) {
-  const float2 nmn = make_float2(-mn, -mn), c2 = make_float2(c15, c15);
+// codec_dev.cuh: one product by c15 = 15 / r, rounded by adding 1.5 * 2^23), two
+// at a time; q[e] holds values e and e + 4.  Returns whether they stand: every
+// |u - rint(u)| stays 1e-5 below a rounding boundary.  What the short form is
+// not made for gives a NaN there and does not stand either: a NaN value, a
+// range of 0 or one too small for a finite c15 (u is infinite or NaN), an
+// infinite value (c15 = 0).  No u exceeds 15 (1 + 2^-23), so no code does.
+__device__ __forceinline__ bool codes_fast(const float2 (&v)[4], float mn, float c15, float2 (&q)[4]) {
+  const float2 nmn = make_float2(-mn, -mn), c2 = make_float2(c15, c15), neg = make_float2(-1.0f, -1.0f);
   const float2 up = make_float2(codec::kRound, codec::kRound), down = make_float2(-codec::kRound, -codec::kRound);
   float far = 0.0f;
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
-    float2 u = mul_f32x2(add_f32x2(v[e], nmn), c2);
-    u = make_float2(fmaxf(u.x, 0.0f), fmaxf(u.y, 0.0f));   // NaN counts as 0; no value exceeds 15 (1 + 2^-23)
+    const float2 u = mul_f32x2(add_f32x2(v[e], nmn), c2);
     q[e] = add_f32x2(add_f32x2(u, up), down);
-    const float2 t = add_f32x2(u, make_float2(-q[e].x, -q[e].y));
-    far = fmaxf(far, fmaxf(fabsf(t.x), fabsf(t.y)));
+    const float2 t = fma_f32x2(q[e], neg, u);
+    far = max_nan(far, max_nan(fabsf(t.x), fabsf(t.y)));
   }
-  return far;
+  return far <= 0.5f - 1e-5f;
 }
 // 8 codes (q[e] = codes e, e + 4) as a word, low nibble first: sums of multiples
 // of 16^e below 2^16, exact in fp32.
@@ -152,6 +160,15 @@ __device__ __forceinline__ uint32_t pack_codes(const float2 (&q)[4]) {
   for (int e = 2; e >= 0; --e) s = fma_f32x2(s, k16, q[e]);
   s = add_f32x2(s, make_float2(8388608.0f, 8388608.0f));   // 2^23: the sum in the low mantissa bits
   return __byte_perm(__float_as_uint(s.x), __float_as_uint(s.y), 0x5410);
+}
+
+// The literal codes of 8 values, packed: out of the way of the common path.
+template <class X>
+__device__ __noinline__ uint32_t exact_word(X x, float mn, float r) {
+  uint32_t word = 0;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) word |= static_cast<uint32_t>(codec::code_exact(x.get(e), mn, r)) << (4 * e);
+  return word;
 }
 
 // A warp takes a run of rows (8 batches of 4 groups: 16 rows of two groups a
@@ -165,7 +182,7 @@ constexpr int kRun = 32 / NG;
 constexpr int kBatches = 8;
 
 template <typename T, int NG>
-__global__ void __launch_bounds__(256) append_kernel(const AppendArgs<T> a, int slices) {
+__global__ void __launch_bounds__(256, 2) append_kernel(const AppendArgs<T> a, int slices) {
   constexpr int D = 64 * NG;
   constexpr uint32_t kNone = 0xffffffffu;
   const int lane = threadIdx.x & 31;
@@ -199,6 +216,10 @@ __global__ void __launch_bounds__(256) append_kernel(const AppendArgs<T> a, int 
         }
       }
     }
+    uint32_t tok[kBatches];   // of this lane's row in each batch
+#pragma unroll
+    for (int b = 0; b < kBatches; ++b) tok[b] = __shfl_sync(0xffffffffu, token, b * (4 / NG) + rb);
+    const uint32_t mine = __shfl_sync(0xffffffffu, token, part * (4 / NG) + rb);
     for (int sl = s0; sl < s1; ++sl) {
       const bool value = sl >= heads;
       const int h = value ? sl - heads : sl;
@@ -208,7 +229,7 @@ __global__ void __launch_bounds__(256) append_kernel(const AppendArgs<T> a, int 
 #pragma unroll
       for (int b = 0; b < kBatches; ++b) {
         const int t = b * (4 / NG) + rb;
-        if (__shfl_sync(0xffffffffu, token, t) != kNone) x[b].load(src + t * a.ld);
+        if (tok[b] != kNone) x[b].load(src + t * a.ld);
         else x[b].clear();
       }
       // lane 8 g + b keeps group g of batch b
@@ -224,38 +245,32 @@ __global__ void __launch_bounds__(256) append_kernel(const AppendArgs<T> a, int 
       }
       if (isnan(mn)) mn = mx = __uint_as_float(0x7fffffffu);   // the codec's NaN
       const float r = __fsub_rn(mx, mn), c15 = __fdiv_rn(15.0f, r), scale = __fdiv_rn(r, 15.0f);
-      const bool fast = r > 0.0f && r < INFINITY && c15 < INFINITY;
-      const uint32_t fasts = __ballot_sync(0xffffffffu, fast);
       uint8_t* codes = value ? a.pool.codes[1] : a.pool.codes[0];
-      // row of the pool's arrays that a token's slice of head h lies in
-      auto slot = [&](uint32_t tok) {
-        return ((static_cast<int64_t>(tok >> psl) * heads + h) << psl) + (tok & ((1u << psl) - 1));
-      };
-      {
-        const uint32_t tok = __shfl_sync(0xffffffffu, token, part * (4 / NG) + rb);
-        if (tok != kNone) {
-          const int64_t at = slot(tok) * NG + gi;
-          (value ? a.pool.mins[1] : a.pool.mins[0])[at] = mn;
-          (value ? a.pool.scales[1] : a.pool.scales[0])[at] = scale;
-        }
+      // row of the pool's arrays that a token's slice of head h is
+      auto slot = [&](uint32_t k) { return ((static_cast<int64_t>(k >> psl) * heads + h) << psl) + (k & ((1u << psl) - 1)); };
+      if (mine != kNone) {
+        const int64_t at = slot(mine) * NG + gi;
+        (value ? a.pool.mins[1] : a.pool.mins[0])[at] = mn;
+        (value ? a.pool.scales[1] : a.pool.scales[0])[at] = scale;
       }
       T* res = value ? a.restored[1] : a.restored[0];
 #pragma unroll
       for (int b = 0; b < kBatches; ++b) {
         const int from = (lane & 24) + b, t = b * (4 / NG) + rb;
-        const float bmn = __shfl_sync(0xffffffffu, mn, from), bc = __shfl_sync(0xffffffffu, c15, from), br = __shfl_sync(0xffffffffu, r, from);
-        const uint32_t tok = __shfl_sync(0xffffffffu, token, t);
+        const float bmn = __shfl_sync(0xffffffffu, mn, from), bc = __shfl_sync(0xffffffffu, c15, from);
         float2 v[4], q[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[e] = make_float2(x[b].get(e), x[b].get(e + 4));
-        const float far = codes_fast(v, bmn, bc, q);
-        const bool near = far > 0.5f - 1e-5f;
-        if (near || !((fasts >> from) & 1u)) {   // rare: within 1e-5 of a boundary, or a range that has no finite 15 / r
+        const bool stands = codes_fast(v, bmn, bc, q);
+        if (__any_sync(0xffffffffu, !stands)) {   // rare
+          const float br = __shfl_sync(0xffffffffu, r, from);
+          const uint32_t word = exact_word(x[b], bmn, br);
+          if (!stands)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) q[e] = make_float2(codec::code_exact(v[e].x, bmn, br), codec::code_exact(v[e].y, bmn, br));
+            for (int e = 0; e < 4; ++e)
+              q[e] = make_float2(codec::code_float((word >> (4 * e)) & 15u), codec::code_float((word >> (4 * e + 16)) & 15u));
         }
-        if (tok != kNone)
-          *reinterpret_cast<uint32_t*>(codes + slot(tok) * (D / 2) + gi * 32 + part * 4) = pack_codes(q);
+        if (tok[b] != kNone) *reinterpret_cast<uint32_t*>(codes + slot(tok[b]) * (D / 2) + gi * 32 + part * 4) = pack_codes(q);
         if (res != nullptr) {
           const float bs = __shfl_sync(0xffffffffu, scale, from);
           const float2 s2 = make_float2(bs, bs), m2 = make_float2(bmn, bmn);
@@ -266,7 +281,7 @@ __global__ void __launch_bounds__(256) append_kernel(const AppendArgs<T> a, int 
             o[e] = y.x;
             o[e + 4] = y.y;
           }
-          if (tok != kNone) store8(res + (row0 + t) * a.ldr + col, o);
+          if (tok[b] != kNone) store8(res + (row0 + t) * a.ldr + col, o);
         }
       }
     }

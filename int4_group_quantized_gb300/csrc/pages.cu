@@ -11,6 +11,7 @@
 #include <algorithm>
 
 #include "paged.cuh"
+#include "tc_ptx.cuh"
 
 namespace fg {
 namespace paged {
@@ -278,6 +279,7 @@ __global__ void free_kernel(const Table t, const int32_t* rows, int n, unsigned 
 __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(const Table t, const int32_t* src, const int32_t* dst,
                                                                  int n, Plan p, unsigned int* err) {
   __shared__ int slots[kPlanWarps];
+  tc::griddep_launch();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int part_mask = (1 << t.ps_log2) - 1;
   auto in_range = [&](int x) { return x >= 0 && x < t.seqs; };
@@ -354,6 +356,7 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(const Table t, 
 // ---- compaction ---------------------------------------------------------------------------
 __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(const Table t, Plan p) {
   __shared__ int slots[kPlanWarps];
+  tc::griddep_launch();
   const int32_t* refs = t.refs;
   const int live = list_where(t.pages, [&](int x) { return refs[x] > 0; }, nullptr, 0, slots);
   const int moves = list_where(t.pages - live, [&](int x) { return refs[live + x] > 0; }, p.src, t.pages, slots);
@@ -370,11 +373,26 @@ __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(const Table 
   }
 }
 
+// ---- the pages' data ------------------------------------------------------------------------
+constexpr int kCopyLayers = 64;   // pools per launch (48 bytes of pointers each)
+constexpr int kCopyUnits = 1024;  // 16-byte units of a piece
+struct CopyArgs {
+  void* base[kCopyLayers][6];
+  const int* head;
+  const int* src;
+  const int* dst;
+  int layers;
+  int pages;
+  int codes16, meta16;     // 16-byte units of a page in a codes / (min or scale) array
+  int codes_n, meta_n;     // pieces of them
+  Table tab;               // compaction: the table whose entries follow the moves (seqs 0: none)
+};
+
 // The table after the moves: an entry at or past the pages in use was moved;
 // its place among the (ascending) sources is found by bisection.
-__global__ void compact_table_kernel(const Table t, const Plan p) {
-  const int moves = p.head[0], live = p.head[1];
-  if (moves == 0) return;
+__device__ __forceinline__ void move_entries(const CopyArgs& a, int moves) {
+  const Table& t = a.tab;
+  const int live = a.head[1];
   const int64_t n = t.seqs * t.stride;
   for (int64_t x = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; x < n;
        x += static_cast<int64_t>(gridDim.x) * blockDim.x) {
@@ -387,45 +405,63 @@ __global__ void compact_table_kernel(const Table t, const Plan p) {
     int lo = 0, hi = moves;   // src[lo] <= page < src[hi]
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if (p.src[mid] <= page) lo = mid;
+      if (a.src[mid] <= page) lo = mid;
       else hi = mid;
     }
-    if (p.src[lo] == page) t.table[x] = p.dst[lo];
+    if (a.src[lo] == page) t.table[x] = a.dst[lo];
   }
 }
 
-// ---- the pages' data ------------------------------------------------------------------------
-constexpr int kCopyLayers = 64;   // pools per launch (48 bytes of pointers each)
-struct CopyArgs {
-  void* base[kCopyLayers][6];
-  const int* head;
-  const int* src;
-  const int* dst;
-  int layers;
-  int pages;
-  int codes16, meta16;   // 16-byte units of a page in a codes / (min or scale) array
-};
-
-// A CTA takes (move, layer, array) items: whole contiguous blocks of a page.
+// Pieces of at most 16 KB of (move, layer, array), dealt over the CTAs; a
+// thread holds four units of a piece at once.  A source is never a
+// destination, so the order does not matter.
 __global__ void __launch_bounds__(256) copy_pages_kernel(const __grid_constant__ CopyArgs a) {
-  const int moves = *a.head;
-  const int64_t items = static_cast<int64_t>(moves) * a.layers * 6;
+  tc::griddep_launch();
+  tc::griddep_wait();
+  const int moves = a.head[0];
+  if (moves == 0) return;
+  if (a.tab.seqs > 0) move_entries(a, moves);
+  const int per = 2 * a.codes_n + 4 * a.meta_n;   // pieces of a page of a layer
+  const int64_t items = static_cast<int64_t>(moves) * a.layers * per;
   for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
-    const int arr = static_cast<int>(it % 6);
-    const int64_t ml = it / 6;
-    const int l = static_cast<int>(ml % a.layers), m = static_cast<int>(ml / a.layers);
+    const int64_t ml = it / per;
+    int c = static_cast<int>(it - ml * per);
+    const int m = static_cast<int>(ml / a.layers), l = static_cast<int>(ml - static_cast<int64_t>(m) * a.layers);
     const int s = a.src[m], d = a.dst[m];
     if (s < 0 || s >= a.pages || d < 0 || d >= a.pages) continue;
-    const int n = arr < 2 ? a.codes16 : a.meta16;
+    int arr, n;
+    if (c < 2 * a.codes_n) {
+      arr = c / a.codes_n;
+      c -= arr * a.codes_n;
+      n = a.codes16;
+    } else {
+      c -= 2 * a.codes_n;
+      arr = c / a.meta_n;
+      c -= arr * a.meta_n;
+      arr += 2;
+      n = a.meta16;
+    }
     const uint4* from = static_cast<const uint4*>(a.base[l][arr]) + static_cast<int64_t>(s) * n;
     uint4* to = static_cast<uint4*>(a.base[l][arr]) + static_cast<int64_t>(d) * n;
-    for (int x = threadIdx.x; x < n; x += 256) to[x] = from[x];
+    uint4 v[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int x = c * kCopyUnits + u * 256 + threadIdx.x;
+      if (x < n) v[u] = from[x];
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int x = c * kCopyUnits + u * 256 + threadIdx.x;
+      if (x < n) to[x] = v[u];
+    }
   }
 }
 
-fg_status copy_pages(const fg_page_pool* pools, int l, const Plan& p, cudaStream_t st) {
-  for (int l0 = 0; l0 < l; l0 += kCopyLayers) {
-    CopyArgs a;
+// Copies the plan's pages in all pools, and (tab given) moves the table's
+// entries; launched so that it may be scheduled while the plan still runs.
+fg_status copy_pages(const fg_page_pool* pools, int l, const Plan& p, const fg_page_table* tab, cudaStream_t st) {
+  for (int l0 = 0; l0 < l || l0 == 0; l0 += kCopyLayers) {
+    CopyArgs a = {};
     a.layers = std::min(kCopyLayers, l - l0);
     for (int i = 0; i < a.layers; ++i) {
       const fg_page_pool& q = pools[l0 + i];
@@ -439,12 +475,27 @@ fg_status copy_pages(const fg_page_pool* pools, int l, const Plan& p, cudaStream
     a.head = p.head;
     a.src = p.src;
     a.dst = p.dst;
-    a.pages = static_cast<int>(pools[0].pages);
-    const int64_t rows = static_cast<int64_t>(pools[0].heads) * pools[0].page_size;
-    a.codes16 = static_cast<int>(rows * pools[0].head_dim / 32);
-    a.meta16 = static_cast<int>(rows * pools[0].head_dim / 256);
+    if (l > 0) {
+      a.pages = static_cast<int>(pools[0].pages);
+      const int64_t rows = static_cast<int64_t>(pools[0].heads) * pools[0].page_size;
+      a.codes16 = static_cast<int>(rows * pools[0].head_dim / 32);
+      a.meta16 = static_cast<int>(rows * pools[0].head_dim / 256);
+      a.codes_n = (a.codes16 + kCopyUnits - 1) / kCopyUnits;
+      a.meta_n = (a.meta16 + kCopyUnits - 1) / kCopyUnits;
+    }
+    if (tab && l0 == 0) a.tab = table_of(*tab);
+    if (a.layers == 0 && a.tab.seqs == 0) break;
+    cudaLaunchAttribute pdl[1];
+    pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    pdl[0].val.programmaticStreamSerializationAllowed = 1;
     Trace tr(KC_PAGES_COPY, st);
-    copy_pages_kernel<<<num_sms() * 8, 256, 0, st>>>(a);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(num_sms() * 8));
+    cfg.blockDim = dim3(256);
+    cfg.stream = st;
+    cfg.attrs = pdl;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, copy_pages_kernel, a) != cudaSuccess) return check_launch("copy_pages_kernel (launch)");
     FG_TRY(check_launch("copy_pages_kernel"));
   }
   return FG_OK;
@@ -527,7 +578,7 @@ fg_status fg_pages_fork(const fg_page_table* t, const fg_page_pool* pools, int32
     fork_plan_kernel<<<1, kPlanThreads, 0, stream>>>(table_of(*t), src, dst, static_cast<int>(n), p, err);
     FG_TRY(check_launch("fork_plan_kernel"));
   }
-  return copy_pages(pools, l, p, stream);
+  return copy_pages(pools, l, p, nullptr, stream);
 }
 
 fg_status fg_pages_compact(const fg_page_table* t, const fg_page_pool* pools, int32_t l, void* ws, size_t ws_bytes,
@@ -541,14 +592,7 @@ fg_status fg_pages_compact(const fg_page_table* t, const fg_page_pool* pools, in
     compact_plan_kernel<<<1, kPlanThreads, 0, stream>>>(table_of(*t), p);
     FG_TRY(check_launch("compact_plan_kernel"));
   }
-  if (t->seqs > 0) {
-    Trace tr(KC_PAGES_PLAN, stream);
-    const int64_t n = t->seqs * t->stride;
-    const unsigned grid = static_cast<unsigned>(std::min<int64_t>((n + 255) / 256, num_sms() * 8));
-    compact_table_kernel<<<grid, 256, 0, stream>>>(table_of(*t), p);
-    FG_TRY(check_launch("compact_table_kernel"));
-  }
-  return copy_pages(pools, l, p, stream);
+  return copy_pages(pools, l, p, t, stream);
 }
 
 }  // extern "C"
