@@ -17,12 +17,16 @@
 //            bits; sum w is an MMA against ones, of the rounded weights.
 // A warp is a worker (see paged_sched.cuh) and walks tiles of 32 tokens of its
 // share: its own ring of stages in shared memory, filled by asynchronous
-// copies kStages - 1 tiles ahead across items, page numbers another tile
-// ahead; no CTA barrier.  Rows of a stage lie so that both the score reads
-// (8 bytes of token s(g)) and the value reads (4 bytes of 4 tokens side by
-// side) fall on 32 different banks: token row m of an MMA is token s(m) =
-// m/2 + 4 (m%2), which makes the transposed weights' token pairs (tig, tig +
-// 4), and 16-byte pieces are swizzled by the row.
+// copies kStages - 1 tiles ahead across items; no CTA barrier.  Where the next
+// 32 tiles lie (item, pages, edges) the lanes look up together, a tile each:
+// one tile after another that took a third of the instructions.  (A warp that
+// filled all rings by bulk copies, six a tile, measured slower: 178 us against
+// 124 for a step over 8 sequences of 30 to 65 thousand tokens.)  Rows of a
+// stage lie so that both the score reads (8 bytes of token s(g)) and the value
+// reads (4 bytes of 4 tokens side by side) fall on 32 different banks: token
+// row m of an MMA is token s(m) = m/2 + 4 (m%2), which makes the transposed
+// weights' token pairs (tig, tig + 4), and 16-byte pieces are swizzled by the
+// row.
 #include <math.h>
 
 #include <algorithm>
@@ -48,7 +52,7 @@ template <int NB>
 constexpr int kCtasPerSm = 3;
 template <int D, int NB>
 constexpr int kStepStages = D == 128 ? 3 : 4;
-constexpr float kGrow = 8.0f;           // log2 growth of a maximum that forces a rescale
+constexpr float kMostSum = 4096.0f;     // a lane's tile sum up to which its weights stand as fp16 (times 2 at most)
 
 template <int D>
 struct Stage {
@@ -56,8 +60,8 @@ struct Stage {
   static constexpr int NG = D / 64;
   static constexpr int kMeta = kTile * NG * 4;     // one (min or scale) array
   static constexpr int kV = kTile * C, kKs = 2 * kTile * C, kKm = kKs + kMeta, kVs = kKm + kMeta, kVm = kVs + kMeta;
-  static constexpr int kInfo = kVm + kMeta;        // (first token, flags, head, sequence), (row0, n, len, keys)
-  static constexpr int kBytes = kInfo + 32;
+  static constexpr int kInfo = kVm + kMeta;        // (first token, flags, head, sequence)
+  static constexpr int kBytes = kInfo + 16;
 };
 // Flags of a tile: the halves that are there, every row sees all of it, the
 // item's first and last tile, the share's last.
@@ -170,14 +174,6 @@ __device__ __forceinline__ void read_meta(const uint8_t* arr, int t, float (&v)[
   }
 }
 
-// A place in the line of tiles: the item and the tile in it.
-struct Cursor {
-  int left;              // tiles of the share still to come
-  int i, h, x;           // sequence, head, tile of the item
-  Seq s;
-  Span span;
-};
-
 template <int D, int NB>
 __global__ void __launch_bounds__(32 * kWarps, kCtasPerSm<NB>) step_kernel(const AttnArgs<__half> a, const ClassPlan pl) {
   constexpr int NG = D / 64, NT = D / 16;
@@ -199,12 +195,11 @@ __global__ void __launch_bounds__(32 * kWarps, kCtasPerSm<NB>) step_kernel(const
   }
   const int heads = a.pool.heads;
 
-  auto enter = [&](Cursor& c) {   // c.i, c.seq_left set: the sequence's shape
-    c.s = seq_of(a.tab, a.batch, c.i);
-    const int base = c.s.len - c.s.n;
-    c.span = span_of<kTileLog2>(base, c.s.len - 1, c.s.keys, a.shape.window, a.shape.sinks);
-  };
-  Cursor rd;                      // the tile to be copied next
+  const int mine = static_cast<int>(total - o0 < per ? total - o0 : per);   // tiles of the share
+
+  // ---- looking up: a lane finds one of the next 32 tiles ----------------------------
+  const int psl = a.pool.ps_log2, psm = (1 << psl) - 1;
+  int t_i = 0, t_h = 0, t_key = 0, t_flags = 0, t_pg0 = -1, t_pg1 = -1;
   {
     int lo = 0, hi = a.tab.seqs;     // pre[lo] <= o0 < pre[hi]
     while (hi - lo > 1) {
@@ -212,31 +207,41 @@ __global__ void __launch_bounds__(32 * kWarps, kCtasPerSm<NB>) step_kernel(const
       if (pl.pre[mid] <= o0) lo = mid;
       else hi = mid;
     }
-    rd.i = lo;
-    rd.left = static_cast<int>(total - o0 < per ? total - o0 : per);
-    enter(rd);
-    const int64_t in = o0 - pl.pre[lo];
-    rd.h = static_cast<int>(in / rd.span.n);
-    rd.x = static_cast<int>(in - static_cast<int64_t>(rd.h) * rd.span.n);
+    t_i = lo;
   }
-  // moves on by a tile; true where a new item begins
-  auto advance = [&](Cursor& c) {
-    --c.left;
-    if (++c.x < c.span.n) return false;
-    c.x = 0;
-    if (++c.h == heads && c.left > 0) {
-      do ++c.i;
-      while (pl.pre[c.i + 1] == pl.pre[c.i]);
-      c.h = 0;
-      enter(c);
-    }
-    return true;
+  auto look_up = [&](int k) {        // tile k + lane of the share
+    k += lane;
+    t_pg0 = t_pg1 = -1;
+    if (k >= mine) return;
+    const int64_t o = o0 + k;
+    while (pl.pre[t_i + 1] <= o) ++t_i;
+    const Seq s = seq_of(a.tab, a.batch, t_i);
+    const Span sp = span_of<kTileLog2>(s.len - s.n, s.len - 1, s.keys, a.shape.window, a.shape.sinks);
+    const int64_t in = o - pl.pre[t_i];
+    t_h = in <= INT32_MAX ? static_cast<int>(in) / sp.n : static_cast<int>(in / sp.n);
+    const int x = static_cast<int>(in - static_cast<int64_t>(t_h) * sp.n);
+    t_key = sp.tile(x) << kTileLog2;
+    const int last = min(s.len, s.keys) - 1, lo_key = a.shape.window > 0 ? s.len - s.n - a.shape.window + 1 : 0;
+    // page of the 16 tokens from t on (-1: none, or nothing of them is seen)
+    auto page_at = [&](int t) {
+      if (t > last || (t + 15 < lo_key && t >= a.shape.sinks)) return -1;
+      const int page = a.tab.table[t_i * a.tab.stride + (t >> psl)];   // t <= last < keys: the row reaches that far
+      if (static_cast<uint32_t>(page) < static_cast<uint32_t>(a.tab.pages)) return page;
+      atomicOr(a.batch.err, DEV_ERR_PAGE);
+      return -1;
+    };
+    t_pg0 = page_at(t_key);
+    t_pg1 = psl >= kTileLog2 && t_key + 16 <= last && t_pg0 >= 0 ? t_pg0 : page_at(t_key + 16);
+    // a row sees all of the tile: inside all rows' positions, stored, and inside the window or the sinks
+    const bool whole = t_pg0 >= 0 && t_pg1 >= 0 && t_key + kTile - 1 <= min(s.len - s.n, s.keys - 1) &&
+                       (a.shape.window == 0 || t_key >= s.len - a.shape.window || t_key + kTile <= a.shape.sinks);
+    t_flags = (t_pg0 >= 0 ? kHalf0 : 0) | (t_pg1 >= 0 ? kHalf1 : 0) | (whole ? kWhole : 0) | (x == 0 ? kFirst : 0) |
+              (x + 1 == sp.n ? kLast : 0) | (k + 1 == mine ? kEnd : 0);
   };
   // ---- copying ------------------------------------------------------------------
   // A lane's pieces lie at the same places of every half tile: 16-byte pieces
   // lane and lane + 32 of the 16 rows' codes, and piece lane % (4 NG) of the
   // (scale or min) array lane / (4 NG).
-  const int psl = a.pool.ps_log2, psm = (1 << psl) - 1;
   const uint32_t page_codes = static_cast<uint32_t>(heads) * static_cast<uint32_t>(St::C) << psl;   // bytes of a page
   const uint32_t page_meta = static_cast<uint32_t>(heads) * static_cast<uint32_t>(4 * NG) << psl;
   const bool meta_lane = lane < 16 * NG;
@@ -247,41 +252,11 @@ __global__ void __launch_bounds__(32 * kWarps, kCtasPerSm<NB>) step_kernel(const
                                                                      : a.pool.mins[1]) +
                             16 * mpc;
   const int meta_at = St::kKs + arr * St::kMeta + 16 * mpc;
-  const int32_t* row = nullptr;      // of the item at rd: its table row, and its head's places in a page
-  uint32_t head_codes = 0, head_meta = 0;
-  int last = 0, lo_key = 0;
-  int whole_hi = 0, whole_lo = 0, sink_hi = 0;   // a tile at t0 is seen whole iff t0 <= whole_hi and (t0 >= whole_lo or t0 <= sink_hi)
-  auto enter_item = [&]() {
-    row = a.tab.table + rd.i * a.tab.stride;
-    head_codes = (static_cast<uint32_t>(rd.h) * St::C << psl) + 16 * lane;
-    head_meta = static_cast<uint32_t>(rd.h) * (4 * NG) << psl;
-    last = min(rd.s.len, rd.s.keys) - 1;
-    lo_key = a.shape.window > 0 ? rd.s.len - rd.s.n - a.shape.window + 1 : 0;
-    whole_hi = min(rd.s.len - rd.s.n, rd.s.keys - 1) - (kTile - 1);
-    whole_lo = a.shape.window > 0 ? rd.s.len - a.shape.window : 0;
-    sink_hi = a.shape.sinks - kTile;
-  };
-  // page of the 16 tokens from t on (-1: none, or nothing of them is seen)
-  auto page_at = [&](int t) {
-    if (t > last || (t + 15 < lo_key && t >= a.shape.sinks)) return -1;
-    const int page = row[t >> psl];   // t <= last < keys: the row reaches that far
-    if (static_cast<uint32_t>(page) < static_cast<uint32_t>(a.tab.pages)) return page;
-    if (lane == 0) atomicOr(a.batch.err, DEV_ERR_PAGE);
-    return -1;
-  };
-  int pg[2] = {-1, -1};              // of the two halves of the tile at rd
-  int t_rd = 0;                      // its first token
-  auto look_up = [&]() {
-    t_rd = rd.span.tile(rd.x) << kTileLog2;
-    pg[0] = page_at(t_rd);
-    pg[1] = page_at(t_rd + 16);
-  };
   const uint32_t ring_u32 = tc::smem_u32(ring);
-  // one half's codes and (min, scale) into stage s
   const int to0 = piece_at<D>(lane / (St::C / 16), lane % (St::C / 16)), to1 = D == 128 ? piece_at<D>(8 + lane / 4, lane % 4) : 0;
-  auto copy_half = [&](uint32_t s, int hf) {
-    const uint32_t in = static_cast<uint32_t>((t_rd + 16 * hf) & psm), page = static_cast<uint32_t>(pg[hf]);
-    const uint64_t at = static_cast<uint64_t>(page) * page_codes + (head_codes + in * St::C);
+  // one half's codes and (min, scale) into stage s
+  auto copy_half = [&](uint32_t s, int hf, int page, uint32_t row) {   // row: of the page's arrays
+    const uint64_t at = static_cast<uint64_t>(static_cast<uint32_t>(page)) * page_codes + (row * St::C + 16 * lane);
     const uint8_t* kc = a.pool.codes[0] + at;
     const uint8_t* vc = a.pool.codes[1] + at;
     const uint32_t to = s + 16 * hf * St::C;
@@ -292,23 +267,21 @@ __global__ void __launch_bounds__(32 * kWarps, kCtasPerSm<NB>) step_kernel(const
       cp16(to + St::kV + to1, vc + 512);
     }
     if (meta_lane)
-      cp16(s + meta_at + hf * (64 * NG), meta0 + (static_cast<uint64_t>(page) * page_meta + (head_meta + in * (4 * NG))));
+      cp16(s + meta_at + hf * (64 * NG), meta0 + (static_cast<uint64_t>(static_cast<uint32_t>(page)) * page_meta + row * (4 * NG)));
   };
-  // copies the tile at rd into the stage at offset st, and moves rd on
+  // copies the share's next tile into the stage at offset st
+  int next = 0;
   auto issue = [&](uint32_t st) {
-    if (rd.left > 0) {
-      if (pg[0] >= 0) copy_half(ring_u32 + st, 0);
-      if (pg[1] >= 0) copy_half(ring_u32 + st, 1);
-      if (lane == 0) {
-        const int flags = (pg[0] >= 0 ? kHalf0 : 0) | (pg[1] >= 0 ? kHalf1 : 0) | (rd.x == 0 ? kFirst : 0) |
-                          (rd.x + 1 == rd.span.n ? kLast : 0) | (rd.left == 1 ? kEnd : 0) |
-                          ((pg[0] | pg[1]) >= 0 && t_rd <= whole_hi && (t_rd >= whole_lo || t_rd <= sink_hi) ? kWhole : 0);
-        uint8_t* s = ring + st;
-        *reinterpret_cast<int4*>(s + St::kInfo) = make_int4(t_rd, flags, rd.h, rd.i);
-        *reinterpret_cast<int4*>(s + St::kInfo + 16) = make_int4(rd.s.row0, rd.s.n, rd.s.len, rd.s.keys);
-      }
-      if (advance(rd) && rd.left > 0) enter_item();
-      if (rd.left > 0) look_up();
+    if (next < mine) {
+      const int from = next & 31;
+      if (from == 0) look_up(next);
+      const int key = __shfl_sync(0xffffffffu, t_key, from), h = __shfl_sync(0xffffffffu, t_h, from);
+      const int pg0 = __shfl_sync(0xffffffffu, t_pg0, from), pg1 = __shfl_sync(0xffffffffu, t_pg1, from);
+      const uint32_t row = (static_cast<uint32_t>(h) << psl);
+      if (pg0 >= 0) copy_half(ring_u32 + st, 0, pg0, row + (key & psm));
+      if (pg1 >= 0) copy_half(ring_u32 + st, 1, pg1, row + ((key + 16) & psm));
+      if (lane == from) *reinterpret_cast<int4*>(ring + st + St::kInfo) = make_int4(t_key, t_flags, t_h, t_i);
+      ++next;
     }
     tc::cp_async_commit();
   };
@@ -321,23 +294,26 @@ __global__ void __launch_bounds__(32 * kWarps, kCtasPerSm<NB>) step_kernel(const
   float acc[NB][NT][4];
   float cap[NG], inv[NG];                        // weights carry the factor inv = 2 / cap
   uint32_t nans = 0;                             // bit 4 nb + 2 e + g: the query sees a NaN value group
-  int rows = 0;
+  int rows = 0, row0 = 0, keys = 0;
   const float kc2 = a.scale_log2;
 
   int pn[NB][2];                                 // positions of queries 2 tig, 2 tig + 1 (none: below every key)
 
   auto begin_item = [&](const uint8_t* s) {
-    const int h = reinterpret_cast<const int4*>(s + St::kInfo)->z;
-    const int4 q4 = *reinterpret_cast<const int4*>(s + St::kInfo + 16);   // row0, n, len, keys
-    rows = q4.y * a.shape.group;
-    const int pos0 = q4.z - q4.y;
+    const int4 info = *reinterpret_cast<const int4*>(s + St::kInfo);
+    const int h = info.z;
+    const Seq sq = seq_of(a.tab, a.batch, info.w);
+    rows = sq.n * a.shape.group;
+    row0 = sq.row0;
+    keys = sq.keys;
+    const int pos0 = sq.len - sq.n;
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
       const int n = 8 * nb + gq;
       QFrag<NG> f;
       if (n < rows) {
         const int t = n / a.shape.group;
-        load_q<NG>(f, a.q + static_cast<int64_t>(q4.x + t) * a.ldq +
+        load_q<NG>(f, a.q + static_cast<int64_t>(row0 + t) * a.ldq +
                           static_cast<int64_t>(h * a.shape.group + n - t * a.shape.group) * D, tig);
       } else {
 #pragma unroll
@@ -427,7 +403,6 @@ __global__ void __launch_bounds__(32 * kWarps, kCtasPerSm<NB>) step_kernel(const
     uint32_t seen = 0xffffffffu;   // bit 8 nb + 4 hf + 2 r + e: the query sees the token
     if (!(flags & kWhole)) {       // a row or a token at the edge
       seen = 0;
-      const int keys = reinterpret_cast<const int4*>(s + St::kInfo + 16)->w;
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf)
 #pragma unroll
@@ -502,33 +477,48 @@ __global__ void __launch_bounds__(32 * kWarps, kCtasPerSm<NB>) step_kernel(const
         }
       }
     }
-    // maxima: of this lane's tokens, then over the lanes of a query
-    bool grow = false;
-    float nm[NB][2];
-#pragma unroll
-    for (int nb = 0; nb < NB; ++nb) {
-      float x = fmaxf(fmaxf(sc[nb][0][0].x, sc[nb][0][1].x), fmaxf(sc[nb][1][0].x, sc[nb][1][1].x));
-      float y = fmaxf(fmaxf(sc[nb][0][0].y, sc[nb][0][1].y), fmaxf(sc[nb][1][0].y, sc[nb][1][1].y));
-#pragma unroll
-      for (int o = 4; o < 32; o <<= 1) {
-        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
-        y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, o));
-      }
-      nm[nb][0] = x;
-      nm[nb][1] = y;
-      grow |= (x - m[nb][0]) * kc2 > kGrow;   // -inf - -inf: no
-      grow |= (y - m[nb][1]) * kc2 > kGrow;
-    }
-    if (__any_sync(0xffffffffu, grow)) {
+    // Weights for the maximum known so far; it serves while no lane's sum of a query grows past 2^12 (a larger maximum would
+    // only change the scale of sums that are divided in the end).  Before the first key is seen it is -inf, and the sum
+    // infinite or NaN: then, as later where it must, the tile's maximum is found over the lanes of a query and the sums are
+    // rescaled.
+    float2 pw[NB][2][2], lt[NB];
+    auto weigh = [&](bool found) {
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
+        float2 neg = make_float2(-m[nb][0] * kc2, -m[nb][1] * kc2);
+        if (found) neg = make_float2(m[nb][0] == -INFINITY ? 0.0f : neg.x, m[nb][1] == -INFINITY ? 0.0f : neg.y);   // no key: weights 0
+        lt[nb] = both(0.0f);
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const float2 x = fma2(sc[nb][hf][r], both(kc2), neg);
+            pw[nb][hf][r] = make_float2(ex2(x.x), ex2(x.y));
+            lt[nb] = add2(lt[nb], pw[nb][hf][r]);
+          }
+      }
+    };
+    weigh(false);
+    bool serves = true;
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) serves = serves && lt[nb].x <= kMostSum && lt[nb].y <= kMostSum;
+    if (__any_sync(0xffffffffu, !serves)) {
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) {
+        float x = fmaxf(fmaxf(sc[nb][0][0].x, sc[nb][0][1].x), fmaxf(sc[nb][1][0].x, sc[nb][1][1].x));
+        float y = fmaxf(fmaxf(sc[nb][0][0].y, sc[nb][0][1].y), fmaxf(sc[nb][1][0].y, sc[nb][1][1].y));
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) {
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+          y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, o));
+        }
+        // only the queries whose sums ask for it: a row's bits do not depend on its neighbours
+        const uint32_t mine = 0x11111111u << tig;
+        const bool ask0 = __ballot_sync(0xffffffffu, !(lt[nb].x <= kMostSum)) & mine, ask1 = __ballot_sync(0xffffffffu, !(lt[nb].y <= kMostSum)) & mine;
+        const float nm[2] = {ask0 ? fmaxf(m[nb][0], x) : m[nb][0], ask1 ? fmaxf(m[nb][1], y) : m[nb][1]};
         float al[2];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float x = fmaxf(m[nb][e], nm[nb][e]);
-          al[e] = x == -INFINITY ? 1.0f : ex2((m[nb][e] - x) * kc2);
-          m[nb][e] = x;
-        }
+        for (int e = 0; e < 2; ++e) al[e] = nm[e] == -INFINITY ? 1.0f : ex2((m[nb][e] - nm[e]) * kc2);
         const float2 f = make_float2(al[0], al[1]);
         l[nb] = mul2(l[nb], f);
 #pragma unroll
@@ -540,21 +530,13 @@ __global__ void __launch_bounds__(32 * kWarps, kCtasPerSm<NB>) step_kernel(const
           acc[nb][i][2] *= al[0];
           acc[nb][i][3] *= al[1];
         }
+        m[nb][0] = nm[0];
+        m[nb][1] = nm[1];
       }
+      weigh(true);
     }
-    // weights
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb) {
-      const float2 neg = make_float2(m[nb][0] == -INFINITY ? 0.0f : -m[nb][0] * kc2, m[nb][1] == -INFINITY ? 0.0f : -m[nb][1] * kc2);
-#pragma unroll
-      for (int hf = 0; hf < 2; ++hf)
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const float2 x = fma2(sc[nb][hf][r], both(kc2), neg);
-          sc[nb][hf][r] = make_float2(ex2(x.x), ex2(x.y));
-          l[nb] = add2(l[nb], sc[nb][hf][r]);
-        }
-    }
+    for (int nb = 0; nb < NB; ++nb) l[nb] = add2(l[nb], lt[nb]);
     float vf[2][2][NG], mid[2][2][NG];   // factor of p in the weights, value of the centre code
 #pragma unroll
     for (int hf = 0; hf < 2; ++hf)
@@ -581,8 +563,8 @@ __global__ void __launch_bounds__(32 * kWarps, kCtasPerSm<NB>) step_kernel(const
         for (int r = 0; r < 2; ++r) {
 #pragma unroll
           for (int nb = 0; nb < NB; ++nb) {
-            const float2 wt = mul2(sc[nb][hf][r], both(vf[hf][r][g]));
-            cmn[nb][g] = fma2(sc[nb][hf][r], both(mid[hf][r][g]), cmn[nb][g]);
+            const float2 wt = mul2(pw[nb][hf][r], both(vf[hf][r][g]));
+            cmn[nb][g] = fma2(pw[nb][hf][r], both(mid[hf][r][g]), cmn[nb][g]);
             vb[nb][hf][r] = movmatrix_trans(pack_h2(wt.x, wt.y));
           }
         }
@@ -631,7 +613,7 @@ __global__ void __launch_bounds__(32 * kWarps, kCtasPerSm<NB>) step_kernel(const
   };
   // the item's rows, finished (one share) or as this share's partial
   auto end_item = [&](const uint8_t* s, bool from_start, bool to_end) {
-    const int h = reinterpret_cast<const int4*>(s + St::kInfo)->z, row0 = reinterpret_cast<const int4*>(s + St::kInfo + 16)->x;
+    const int h = reinterpret_cast<const int4*>(s + St::kInfo)->z;
 #pragma unroll
     for (int o = 4; o < 32; o <<= 1) nans |= __shfl_xor_sync(0xffffffffu, nans, o);
 #pragma unroll
@@ -684,8 +666,6 @@ __global__ void __launch_bounds__(32 * kWarps, kCtasPerSm<NB>) step_kernel(const
   };
 
   // ---- the share ------------------------------------------------------------------
-  enter_item();
-  look_up();
 #pragma unroll
   for (int st = 0; st < kStages - 1; ++st) issue(st * St::kBytes);
   int4 rec = make_int4(-1, 0, 0, 0);

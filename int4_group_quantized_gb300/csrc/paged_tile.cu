@@ -547,7 +547,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const AttnArgs<__half
         // nothing but the scale of sums that are divided in the end.  Otherwise (or with no key seen before) the tile finds
         // its maximum, the sums are rescaled, and the weights are formed again.
         uint32_t pk[64];
-        float2 lt;
+        float2 lt = make_float2(0.0f, 0.0f);
         bool find = x == 0;
         while (true) {
           if (find) {
@@ -564,7 +564,8 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const AttnArgs<__half
                 for (int q = 0; q < 4; ++q) m4[q] = fmaxf(m4[q], fmaxf(__uint_as_float(u[e + 2 * q]), __uint_as_float(u[e + 2 * q + 1])));
               mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
             }
-            mx = fmaxf(m, mx * a.scale_log2);
+            // only for a row that asks: its bits do not depend on its neighbours
+            mx = x == 0 || m == -INFINITY || !(lt.x + lt.y <= kMostSum) ? fmaxf(m, mx * a.scale_log2) : m;
             if (x > 0) {
               const float alpha = mx == -INFINITY ? 1.0f : ex2_approx(m - mx);
               l2 = make_float2(l2.x * alpha, l2.y * alpha);
