@@ -82,12 +82,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
         at[c] = __shfl_sync(0xffffffffu, inc - v, warp);
         const ClassPlan& p = c ? a.tile : a.step;
         if (threadIdx.x == 0 && p.workers > 0) {
-          int64_t share = (total + p.workers - 1) / p.workers;
-          const int64_t least = (mx + kMaxSplits - 1) / kMaxSplits;
-          share = share > least ? share : least;
-          const int64_t few = c ? 1 : 2;   // a step's share: at least 64 tokens
           p.head[0] = total;
-          p.head[1] = share > few ? share : few;
+          p.head[1] = share_of(total, mx, p.workers, c ? 1 : kStepFew);
           p.pre[seqs] = total;
         }
       }
@@ -105,10 +101,9 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
         }
         const int64_t rows = static_cast<int64_t>(s.n) * a.shape.group;
         if (rows > 0 && a.step.workers > 0 && rows <= kStepRows) {
-          const int base = s.len - s.n;
-          const Span sp = span_of<5>(base, s.len - 1, s.keys, a.shape.window, a.shape.sinks);
-          cost[0] = static_cast<int64_t>(sp.n) * a.heads;
-          longest[0] = max(longest[0], sp.n);
+          const int tiles = step_tiles(s, a.shape);
+          cost[0] = static_cast<int64_t>(tiles) * a.heads;
+          longest[0] = max(longest[0], tiles);
         } else if (rows > 0 && a.tile.workers > 0) {
           tall = true;
           // the last unit sees the most tiles, but for a few where it is short and a window cuts them all
@@ -326,7 +321,8 @@ fg_status launch_attn(const fg_page_pool& pool, const fg_page_table& t, const in
   const Layout l = layout_of(pool, t, q_heads, max_q, ws, std::min(num_sms(), kMaxSms));
   constexpr bool half = sizeof(T) == 2;
   const bool wide = pool.head_dim == 128;
-  {
+  const bool own_plan = half && l.tile.workers == 0 && t.seqs <= kOwnPlan;
+  if (!own_plan) {
     PlanArgs p{a.tab, a.batch, a.shape, pool.heads, l.step, l.tile};
     Trace tr(KC_ATTN_PAGED_PLAN, st);
     const unsigned threads = static_cast<unsigned>(std::min<int64_t>(kPlanThreads, (t.seqs + 31) / 32 * 32));
@@ -336,7 +332,7 @@ fg_status launch_attn(const fg_page_pool& pool, const fg_page_table& t, const in
   }
   if constexpr (half) {
     if (l.step.workers > 0) {
-      FG_TRY(paged_attention_step(a, l.step, pool.head_dim, st));
+      FG_TRY(paged_attention_step(a, l.step, pool.head_dim, own_plan, st));
       FG_TRY((wide ? join<T, 128, kStepRows>(a, l.step, st) : join<T, 64, kStepRows>(a, l.step, st)));
     }
     if (l.tile.workers > 0) {

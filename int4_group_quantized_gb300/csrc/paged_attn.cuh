@@ -22,7 +22,7 @@ struct AttnArgs {
 
 // Sequences of at most kStepRows rows per K/V head (fp16).
 int step_workers(int rows, int sms);
-fg_status paged_attention_step(const AttnArgs<__half>& a, const ClassPlan& pl, int head_dim, cudaStream_t st);
+fg_status paged_attention_step(const AttnArgs<__half>& a, const ClassPlan& pl, int head_dim, bool own_plan, cudaStream_t st);
 
 
 // Longer chunks (fp16) on tcgen05, units of kTileRows rows and tiles of 128 keys; one worker an SM.

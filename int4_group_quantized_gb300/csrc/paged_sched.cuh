@@ -85,5 +85,23 @@ __device__ __forceinline__ Unit unit_of(const Seq& s, int group, int u) {
   return x;
 }
 
+// Tiles of a step (a sequence of at most kStepRows rows) for one K/V head.
+constexpr int kStepTileLog2 = 5;
+__device__ __forceinline__ int step_tiles(const Seq& s, const AttnShape& sh) {
+  return span_of<kStepTileLog2>(s.len - s.n, s.len - 1, s.keys, sh.window, sh.sinks).n;
+}
+// Tiles of a share: equal shares, but no item over more than kMaxSplits of
+// them, and at least `few`.
+__device__ __forceinline__ int64_t share_of(int64_t total, int longest, int workers, int few) {
+  const int64_t a = (total + workers - 1) / workers, b = (longest + kMaxSplits - 1) / kMaxSplits;
+  const int64_t c = a > b ? a : b;
+  return c > few ? c : few;
+}
+// A step's share: at least 64 tokens.  Calls of steps alone over at most
+// kOwnPlan sequences make their plan in every CTA (a scan of one warp) instead
+// of a launch of its own.
+constexpr int kStepFew = 2;
+constexpr int kOwnPlan = 128;
+
 }  // namespace paged
 }  // namespace fg

@@ -45,7 +45,7 @@ using attn::unpack_h2;
 using attn::kHiNib;
 using attn::kLoNib;
 
-constexpr int kTileLog2 = 5;
+constexpr int kTileLog2 = kStepTileLog2;
 constexpr int kTile = 1 << kTileLog2;   // tokens of a tile
 constexpr int kWarps = 4;               // warps of a CTA
 template <int NB>
@@ -175,7 +175,7 @@ __device__ __forceinline__ void read_meta(const uint8_t* arr, int t, float (&v)[
 }
 
 template <int D, int NB>
-__global__ void __launch_bounds__(32 * kWarps, kCtasPerSm<NB>) step_kernel(const AttnArgs<__half> a, const ClassPlan pl) {
+__global__ void __launch_bounds__(32 * kWarps, kCtasPerSm<NB>) step_kernel(const AttnArgs<__half> a, const ClassPlan pl, const bool own_plan) {
   constexpr int NG = D / 64, NT = D / 16;
   using St = Stage<D>;
   constexpr int kStages = kStepStages<D, NB>;
@@ -187,7 +187,50 @@ __global__ void __launch_bounds__(32 * kWarps, kCtasPerSm<NB>) step_kernel(const
 
   tc::griddep_launch();
   tc::griddep_wait();
-  const int64_t total = pl.head[0], per = pl.head[1];
+  __shared__ int64_t own_pre[kOwnPlan + 1];
+  __shared__ int64_t own_head[2];
+  const int64_t* pre = pl.pre;
+  int64_t total, per;
+  if (own_plan) {
+    if (warp == 0) {
+      int64_t at = 0;
+      int longest = 0;
+      for (int i0 = 0; i0 < a.tab.seqs; i0 += 32) {
+        const int i = i0 + lane;
+        int tiles = 0;
+        if (i < a.tab.seqs) {
+          const Seq s = seq_of(a.tab, a.batch, i);
+          if (s.n > a.shape.max_q) {
+            if (blockIdx.x == 0) atomicOr(a.batch.err, DEV_ERR_BATCH);
+          } else if (s.n > 0) {
+            tiles = step_tiles(s, a.shape);
+          }
+        }
+        int64_t inc = static_cast<int64_t>(tiles) * a.pool.heads;
+        const int64_t cost = inc;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int64_t up = __shfl_up_sync(0xffffffffu, inc, o);
+          if (lane >= o) inc += up;
+        }
+        if (i < a.tab.seqs) own_pre[i] = at + inc - cost;
+        at += __shfl_sync(0xffffffffu, inc, 31);
+        longest = max(longest, static_cast<int>(__reduce_max_sync(0xffffffffu, static_cast<unsigned>(tiles))));
+      }
+      if (lane == 0) {
+        own_pre[a.tab.seqs] = at;
+        own_head[0] = at;
+        own_head[1] = share_of(at, longest, pl.workers, kStepFew);
+      }
+    }
+    __syncthreads();
+    pre = own_pre;
+    total = own_head[0];
+    per = own_head[1];
+  } else {
+    total = pl.head[0];
+    per = pl.head[1];
+  }
   const int64_t o0 = w * per;
   if (o0 >= total) {
     if (lane == 0) pl.rec[w] = make_int4(-1, 0, 0, 0);
@@ -204,7 +247,7 @@ __global__ void __launch_bounds__(32 * kWarps, kCtasPerSm<NB>) step_kernel(const
     int lo = 0, hi = a.tab.seqs;     // pre[lo] <= o0 < pre[hi]
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if (pl.pre[mid] <= o0) lo = mid;
+      if (pre[mid] <= o0) lo = mid;
       else hi = mid;
     }
     t_i = lo;
@@ -214,10 +257,10 @@ __global__ void __launch_bounds__(32 * kWarps, kCtasPerSm<NB>) step_kernel(const
     t_pg0 = t_pg1 = -1;
     if (k >= mine) return;
     const int64_t o = o0 + k;
-    while (pl.pre[t_i + 1] <= o) ++t_i;
+    while (pre[t_i + 1] <= o) ++t_i;
     const Seq s = seq_of(a.tab, a.batch, t_i);
     const Span sp = span_of<kTileLog2>(s.len - s.n, s.len - 1, s.keys, a.shape.window, a.shape.sinks);
-    const int64_t in = o - pl.pre[t_i];
+    const int64_t in = o - pre[t_i];
     t_h = in <= INT32_MAX ? static_cast<int>(in) / sp.n : static_cast<int>(in / sp.n);
     const int x = static_cast<int>(in - static_cast<int64_t>(t_h) * sp.n);
     t_key = sp.tile(x) << kTileLog2;
@@ -689,8 +732,8 @@ __global__ void __launch_bounds__(32 * kWarps, kCtasPerSm<NB>) step_kernel(const
       const bool to_end = info.y & kLast;
       end_item(s, from_start, to_end);
       if (from_start && !to_end) {
-        const int64_t cost = (pl.pre[info.w + 1] - pl.pre[info.w]) / heads;   // of the item
-        rec = make_int4(info.w, info.z, 0, static_cast<int>((pl.pre[info.w] + (info.z + 1) * cost - 1) / per));
+        const int64_t cost = (pre[info.w + 1] - pre[info.w]) / heads;   // of the item
+        rec = make_int4(info.w, info.z, 0, static_cast<int>((pre[info.w] + (info.z + 1) * cost - 1) / per));
       }
     }
     __syncwarp();
@@ -705,7 +748,7 @@ constexpr int step_smem() {
 }
 
 template <int D, int NB>
-fg_status launch(const AttnArgs<__half>& a, const ClassPlan& pl, cudaStream_t st) {
+fg_status launch(const AttnArgs<__half>& a, const ClassPlan& pl, bool own_plan, cudaStream_t st) {
   constexpr int bytes = step_smem<D, NB>();
   static bool set[64] = {false};
   int dev = 0;
@@ -725,8 +768,8 @@ fg_status launch(const AttnArgs<__half>& a, const ClassPlan& pl, cudaStream_t st
   cfg.dynamicSmemBytes = bytes;
   cfg.stream = st;
   cfg.attrs = pdl;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, step_kernel<D, NB>, a, pl) != cudaSuccess) return check_launch("step_kernel (launch)");
+  cfg.numAttrs = own_plan ? 0 : 1;   // a plan of its own: the first launch of the call, which waits for what ran before
+  if (cudaLaunchKernelEx(&cfg, step_kernel<D, NB>, a, pl, own_plan) != cudaSuccess) return check_launch("step_kernel (launch)");
   return check_launch("step_kernel");
 }
 
@@ -734,9 +777,9 @@ fg_status launch(const AttnArgs<__half>& a, const ClassPlan& pl, cudaStream_t st
 
 int step_workers(int rows, int sms) { return sms * (rows <= 8 ? kCtasPerSm<1> : kCtasPerSm<2>) * kWarps; }
 
-fg_status paged_attention_step(const AttnArgs<__half>& a, const ClassPlan& pl, int head_dim, cudaStream_t st) {
-  if (head_dim == 128) return pl.rows <= 8 ? launch<128, 1>(a, pl, st) : launch<128, 2>(a, pl, st);
-  return pl.rows <= 8 ? launch<64, 1>(a, pl, st) : launch<64, 2>(a, pl, st);
+fg_status paged_attention_step(const AttnArgs<__half>& a, const ClassPlan& pl, int head_dim, bool own_plan, cudaStream_t st) {
+  if (head_dim == 128) return pl.rows <= 8 ? launch<128, 1>(a, pl, own_plan, st) : launch<128, 2>(a, pl, own_plan, st);
+  return pl.rows <= 8 ? launch<64, 1>(a, pl, own_plan, st) : launch<64, 2>(a, pl, own_plan, st);
 }
 
 }  // namespace paged
