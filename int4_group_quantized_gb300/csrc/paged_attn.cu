@@ -17,8 +17,11 @@ namespace fg {
 namespace paged {
 namespace {
 
-__device__ __forceinline__ void put(float* p, float x) { *p = x; }
-__device__ __forceinline__ void put(__half* p, float x) { *p = __float2half_rn(x); }
+__device__ __forceinline__ void put4(float* p, const float4& v) { *reinterpret_cast<float4*>(p) = v; }
+__device__ __forceinline__ void put4(__half* p, const float4& v) {
+  const __half2 a = __floats2half2_rn(v.x, v.y), b = __floats2half2_rn(v.z, v.w);
+  *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+}
 
 // ---- the plan -------------------------------------------------------------------
 // One CTA: the tiles of every sequence, class by class, as prefix sums, and
@@ -33,18 +36,6 @@ struct PlanArgs {
   int heads;
   ClassPlan step, tile;   // a class with no workers is not used
 };
-
-template <int RU, int KTL>
-__device__ __forceinline__ int64_t units_cost(const Seq& s, const AttnShape& sh, int u0, int stride) {
-  const int64_t all = static_cast<int64_t>(s.n) * sh.group;
-  const int units = static_cast<int>((all + RU - 1) / RU);
-  int64_t c = 0;
-  for (int u = u0; u < units; u += stride) {
-    const Unit x = unit_of<RU>(s, sh.group, u);
-    c += span_of<KTL>(x.p0, x.p1, s.keys, sh.window, sh.sinks).n;
-  }
-  return c;
-}
 
 template <int TRU, int TKTL>
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
@@ -106,9 +97,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
           longest[0] = max(longest[0], tiles);
         } else if (rows > 0 && a.tile.workers > 0) {
           tall = true;
-          // the last unit sees the most tiles, but for a few where it is short and a window cuts them all
-          const Unit x = unit_of<TRU>(s, a.shape.group, static_cast<int>((rows - 1) / TRU));
-          longest[1] = max(longest[1], span_of<TKTL>(x.p0, x.p1, s.keys, a.shape.window, a.shape.sinks).n + 4);
+          longest[1] = max(longest[1], longest_unit<TRU, TKTL>(s, a.shape));
         }
       }
       uint32_t todo = __ballot_sync(0xffffffffu, tall);
@@ -120,7 +109,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
         t.n = __shfl_sync(0xffffffffu, s.n, src);
         t.len = __shfl_sync(0xffffffffu, s.len, src);
         t.keys = __shfl_sync(0xffffffffu, s.keys, src);
-        int64_t c = units_cost<TRU, TKTL>(t, a.shape, lane, 32);
+        int64_t c = units_tiles<TRU, TKTL>(t, a.shape, lane, 32);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) c += __shfl_xor_sync(0xffffffffu, c, o);
         if (lane == src) cost[1] = c * a.heads;
@@ -149,30 +138,71 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
 }
 
 // ---- joining the partials of items that cross shares ------------------------------
-// Block (w, y) joins rows 16 y .. of the item that begins in share w and ends later: the partials
-// lie in slot 1 of w and slot 0 of the shares after it.  The factors of all
-// (share, row) first, then the sums: a warp per row and part of the shares,
-// four columns a lane, the parts added in order (the same bits every time).
+// A block joins 16 rows of the item that begins in share w and ends later: the partials
+// lie in slot 1 of w and slot 0 of the shares after it.  Up to four shares are
+// loaded at once, four columns a lane.  Of more the factors of all (share, row)
+// first, then the sums: a warp per row and part of the shares, the parts added
+// in order (the same bits every time).
 constexpr int kJoinWarps = 8;
+constexpr int kJoinRows = 16;
 
 template <typename T, int D, int RU>
-__global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const AttnArgs<T> a, const ClassPlan pl) {
-  constexpr int kRows = RU <= 16 ? RU : 16;   // rows at once
+__device__ __forceinline__ void join_rows(const AttnArgs<T>& a, const ClassPlan& pl, int w, int n0) {
+  constexpr int kRows = kJoinRows;
   constexpr int kCols = D / 4;                // lanes of a row
   __shared__ float fac[(kMaxSplits + 2) * kRows];
   __shared__ float norm[kRows];
   __shared__ float4 sums[kJoinWarps][32];
-  tc::griddep_launch();
-  tc::griddep_wait();
-  const int w = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int4 rec = pl.rec[w];
   if (rec.x < 0) return;
   const Seq s = seq_of(a.tab, a.batch, rec.x);
   const Unit x = unit_of<RU>(s, a.shape.group, rec.z);
   const int shares = rec.w - w + 1;
   auto slot = [&](int k, int n) { return (static_cast<int64_t>(w + k) * 2 + (k == 0 ? 1 : 0)) * pl.rows + n; };
-  const int n0 = blockIdx.y * kRows;
-  if (n0 < x.rows) {
+  auto write = [&](int n, int col, const float4& o, float f) {   // four columns of row n0 + n
+    const int row = x.r0 + n0 + n, t = row / a.shape.group;
+    T* dst = a.out + static_cast<int64_t>(s.row0 + t) * a.ldo +
+             static_cast<int64_t>(rec.y * a.shape.group + row - t * a.shape.group) * D + 4 * col;
+    put4(dst, make_float4(o.x * f, o.y * f, o.z * f, o.w * f));
+  };
+  if (n0 >= x.rows) return;
+  constexpr int kFew = 4;
+  if (shares <= kFew) {   // the usual case: everything is loaded at once
+    constexpr int kAtOnce = kJoinWarps * 32 / kCols;   // rows
+    const int col = threadIdx.x % kCols;
+#pragma unroll
+    for (int r = 0; r < kRows; r += kAtOnce) {
+      const int n = r + threadIdx.x / kCols;
+      if (n0 + n >= x.rows) continue;
+      float2 st[kFew];
+      float4 v[kFew];
+#pragma unroll
+      for (int k = 0; k < kFew; ++k) {
+        st[k] = make_float2(-INFINITY, 0.0f);
+        v[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (k < shares) {
+          st[k] = pl.stat[slot(k, n0 + n)];
+          v[k] = *reinterpret_cast<const float4*>(pl.part + slot(k, n0 + n) * D + 4 * col);
+        }
+      }
+      const float m = fmaxf(fmaxf(st[0].x, st[1].x), fmaxf(st[2].x, st[3].x)), base = m == -INFINITY ? 0.0f : m;
+      float l = 0.0f;
+      float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+      for (int k = 0; k < kFew; ++k) {
+        const float f = exp2f(st[k].x - base);
+        l += f * st[k].y;
+        o.x = fmaf(f, v[k].x, o.x);
+        o.y = fmaf(f, v[k].y, o.y);
+        o.z = fmaf(f, v[k].z, o.z);
+        o.w = fmaf(f, v[k].w, o.w);
+      }
+      write(n, col, o, l == 0.0f ? 0.0f : 1.0f / l);
+    }
+    return;
+  }
+  {
     const int rows = min(kRows, x.rows - n0);
     for (int n = warp; n < rows; n += kJoinWarps) {
       float m = -INFINITY;
@@ -225,33 +255,39 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const AttnArgs<T>
           }
         __syncthreads();
       }
-      if (n < rows && part == 0) {
-        const float f = norm[n];
-        const int row = x.r0 + n0 + n, t = row / a.shape.group;
-        T* dst = a.out + static_cast<int64_t>(s.row0 + t) * a.ldo +
-                 static_cast<int64_t>(rec.y * a.shape.group + row - t * a.shape.group) * D + 4 * col;
-        put(dst, o.x * f);
-        put(dst + 1, o.y * f);
-        put(dst + 2, o.z * f);
-        put(dst + 3, o.w * f);
-      }
+      if (n < rows && part == 0) write(n, col, o, norm[n]);
     }
   }
 }
 
+// Blocks 0 .. step.workers - 1: the steps' shares; then 16 rows of each of the
+// chunks' shares.
 template <typename T, int D, int RU>
-fg_status join(const AttnArgs<T>& a, const ClassPlan& pl, cudaStream_t st) {
+__global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const AttnArgs<T> a, const ClassPlan step, const ClassPlan tile) {
+  tc::griddep_launch();
+  tc::griddep_wait();
+  const int b = static_cast<int>(blockIdx.x) - step.workers;
+  if (b < 0) {
+    join_rows<T, D, kStepRows>(a, step, blockIdx.x, 0);
+  } else {
+    constexpr int kParts = RU / kJoinRows;
+    join_rows<T, D, RU>(a, tile, b / kParts, b % kParts * kJoinRows);
+  }
+}
+
+template <typename T, int D, int RU>
+fg_status join(const AttnArgs<T>& a, const ClassPlan& step, const ClassPlan& tile, cudaStream_t st) {
   cudaLaunchAttribute pdl[1];
   pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   pdl[0].val.programmaticStreamSerializationAllowed = 1;
   Trace tr(KC_ATTN_COMBINE, st);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(pl.workers), static_cast<unsigned>((pl.rows + 15) / 16));
+  cfg.gridDim = dim3(static_cast<unsigned>(step.workers + tile.workers * (RU / kJoinRows)));
   cfg.blockDim = dim3(32 * kJoinWarps);
   cfg.stream = st;
   cfg.attrs = pdl;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, join_kernel<T, D, RU>, a, pl) != cudaSuccess) return check_launch("join_kernel (launch)");
+  if (cudaLaunchKernelEx(&cfg, join_kernel<T, D, RU>, a, step, tile) != cudaSuccess) return check_launch("join_kernel (launch)");
   return check_launch("join_kernel");
 }
 
@@ -321,7 +357,7 @@ fg_status launch_attn(const fg_page_pool& pool, const fg_page_table& t, const in
   const Layout l = layout_of(pool, t, q_heads, max_q, ws, std::min(num_sms(), kMaxSms));
   constexpr bool half = sizeof(T) == 2;
   const bool wide = pool.head_dim == 128;
-  const bool own_plan = half && l.tile.workers == 0 && t.seqs <= kOwnPlan;
+  const bool own_plan = t.seqs <= kOwnPlan;
   if (!own_plan) {
     PlanArgs p{a.tab, a.batch, a.shape, pool.heads, l.step, l.tile};
     Trace tr(KC_ATTN_PAGED_PLAN, st);
@@ -331,19 +367,13 @@ fg_status launch_attn(const fg_page_pool& pool, const fg_page_table& t, const in
     FG_TRY(check_launch("plan_kernel"));
   }
   if constexpr (half) {
-    if (l.step.workers > 0) {
-      FG_TRY(paged_attention_step(a, l.step, pool.head_dim, own_plan, st));
-      FG_TRY((wide ? join<T, 128, kStepRows>(a, l.step, st) : join<T, 64, kStepRows>(a, l.step, st)));
-    }
-    if (l.tile.workers > 0) {
-      FG_TRY(paged_attention_tile(a, l.tile, pool.head_dim, st));
-      FG_TRY((wide ? join<T, 128, kTileRows>(a, l.tile, st) : join<T, 64, kTileRows>(a, l.tile, st)));
-    }
+    if (l.step.workers > 0) FG_TRY(paged_attention_step(a, l.step, pool.head_dim, own_plan, st));
+    if (l.tile.workers > 0) FG_TRY(paged_attention_tile(a, l.tile, pool.head_dim, own_plan, l.step.workers == 0, st));
+    return wide ? join<T, 128, kTileRows>(a, l.step, l.tile, st) : join<T, 64, kTileRows>(a, l.step, l.tile, st);
   } else {
-    FG_TRY(paged_attention_f32(a, l.tile, pool.head_dim, st));
-    FG_TRY((wide ? join<T, 128, kF32Rows>(a, l.tile, st) : join<T, 64, kF32Rows>(a, l.tile, st)));
+    FG_TRY(paged_attention_f32(a, l.tile, pool.head_dim, own_plan, st));
+    return wide ? join<T, 128, kF32Rows>(a, l.step, l.tile, st) : join<T, 64, kF32Rows>(a, l.step, l.tile, st);
   }
-  return FG_OK;
 }
 
 fg_status check_attn(const fg_page_pool* pool, const fg_page_table* t, int32_t q_heads, int64_t ntok, int64_t max_q) {

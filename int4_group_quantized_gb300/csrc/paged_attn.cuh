@@ -20,6 +20,7 @@ struct AttnArgs {
   float scale_log2;   // times log2(e)
 };
 
+// own_plan: no plan was made (paged_sched.cuh, make_line).
 // Sequences of at most kStepRows rows per K/V head (fp16).
 int step_workers(int rows, int sms);
 fg_status paged_attention_step(const AttnArgs<__half>& a, const ClassPlan& pl, int head_dim, bool own_plan, cudaStream_t st);
@@ -27,13 +28,14 @@ fg_status paged_attention_step(const AttnArgs<__half>& a, const ClassPlan& pl, i
 
 // Longer chunks (fp16) on tcgen05, units of kTileRows rows and tiles of 128 keys; one worker an SM.
 constexpr int kTileRows = 256;
-fg_status paged_attention_tile(const AttnArgs<__half>& a, const ClassPlan& pl, int head_dim, cudaStream_t st);
+// `every`: the call has no step class.
+fg_status paged_attention_tile(const AttnArgs<__half>& a, const ClassPlan& pl, int head_dim, bool own_plan, bool every, cudaStream_t st);
 
 
 // fp32 activations, every sequence: units of kF32Rows rows, tiles of 64 keys.
 constexpr int kF32Rows = 16, kF32KeysLog2 = 6;
 int f32_workers(int head_dim, int sms);
-fg_status paged_attention_f32(const AttnArgs<float>& a, const ClassPlan& pl, int head_dim, cudaStream_t st);
+fg_status paged_attention_f32(const AttnArgs<float>& a, const ClassPlan& pl, int head_dim, bool own_plan, cudaStream_t st);
 
 }  // namespace paged
 }  // namespace fg

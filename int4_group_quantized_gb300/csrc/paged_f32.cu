@@ -36,7 +36,7 @@ struct Smem {
 };
 
 template <int D>
-__global__ void __launch_bounds__(kThreads) f32_kernel(const AttnArgs<float> a, const ClassPlan pl) {
+__global__ void __launch_bounds__(kThreads) f32_kernel(const AttnArgs<float> a, const ClassPlan pl, const bool own_plan) {
   constexpr int NG = D / 64, CW = D / 16;     // output columns of a thread: 4 (cx + 16 i), i < D / 64
   extern __shared__ __align__(16) uint8_t raw[];
   Smem<D>& sm = *reinterpret_cast<Smem<D>*>(raw);
@@ -46,7 +46,10 @@ __global__ void __launch_bounds__(kThreads) f32_kernel(const AttnArgs<float> a, 
 
   tc::griddep_launch();
   tc::griddep_wait();
-  const int64_t total = pl.head[0], per = pl.head[1], o0 = w * per;
+  __shared__ OwnPlan own;
+  const Line line = own_plan ? make_line<false, kRows, kKeysLog2>(own, a.tab, a.batch, a.shape, a.pool.heads, pl.workers, true)
+                             : Line{pl.pre, pl.head[0], pl.head[1]};
+  const int64_t total = line.total, per = line.per, o0 = w * per;
   if (o0 >= total) {
     if (tid == 0) pl.rec[w] = make_int4(-1, 0, 0, 0);
     return;
@@ -69,13 +72,13 @@ __global__ void __launch_bounds__(kThreads) f32_kernel(const AttnArgs<float> a, 
     int lo = 0, hi = a.tab.seqs;
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if (pl.pre[mid] <= o0) lo = mid;
+      if (line.pre[mid] <= o0) lo = mid;
       else hi = mid;
     }
     i = lo;
     left = static_cast<int>(total - o0 < per ? total - o0 : per);
     enter_seq();
-    const int64_t cost = (pl.pre[lo + 1] - pl.pre[lo]) / a.pool.heads, in = o0 - pl.pre[lo];
+    const int64_t cost = (line.pre[lo + 1] - line.pre[lo]) / a.pool.heads, in = o0 - line.pre[lo];
     h = static_cast<int>(in / cost);
     int64_t rest = in - h * cost;
     enter_unit();
@@ -296,7 +299,7 @@ __global__ void __launch_bounds__(kThreads) f32_kernel(const AttnArgs<float> a, 
       u = 0;
       if (++h == a.pool.heads) {
         do ++i;
-        while (pl.pre[i + 1] == pl.pre[i]);
+        while (line.pre[i + 1] == line.pre[i]);
         h = 0;
         enter_seq();
       }
@@ -308,7 +311,7 @@ __global__ void __launch_bounds__(kThreads) f32_kernel(const AttnArgs<float> a, 
 }
 
 template <int D>
-fg_status launch(const AttnArgs<float>& a, const ClassPlan& pl, cudaStream_t st) {
+fg_status launch(const AttnArgs<float>& a, const ClassPlan& pl, bool own_plan, cudaStream_t st) {
   constexpr int bytes = sizeof(Smem<D>);
   static bool set[64] = {false};
   int dev = 0;
@@ -328,8 +331,8 @@ fg_status launch(const AttnArgs<float>& a, const ClassPlan& pl, cudaStream_t st)
   cfg.dynamicSmemBytes = bytes;
   cfg.stream = st;
   cfg.attrs = pdl;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, f32_kernel<D>, a, pl) != cudaSuccess) return check_launch("f32_kernel (launch)");
+  cfg.numAttrs = own_plan ? 0 : 1;   // with a plan of its own the call's first launch: it waits for all that ran before
+  if (cudaLaunchKernelEx(&cfg, f32_kernel<D>, a, pl, own_plan) != cudaSuccess) return check_launch("f32_kernel (launch)");
   return check_launch("f32_kernel");
 }
 
@@ -338,8 +341,8 @@ fg_status launch(const AttnArgs<float>& a, const ClassPlan& pl, cudaStream_t st)
 // CTAs that fit an SM's shared memory (44 and 81 KB each)
 int f32_workers(int head_dim, int sms) { return sms * (head_dim == 128 ? 2 : 4); }
 
-fg_status paged_attention_f32(const AttnArgs<float>& a, const ClassPlan& pl, int head_dim, cudaStream_t st) {
-  return head_dim == 128 ? launch<128>(a, pl, st) : launch<64>(a, pl, st);
+fg_status paged_attention_f32(const AttnArgs<float>& a, const ClassPlan& pl, int head_dim, bool own_plan, cudaStream_t st) {
+  return head_dim == 128 ? launch<128>(a, pl, own_plan, st) : launch<64>(a, pl, own_plan, st);
 }
 
 }  // namespace paged

@@ -97,11 +97,105 @@ __device__ __forceinline__ int64_t share_of(int64_t total, int longest, int work
   const int64_t c = a > b ? a : b;
   return c > few ? c : few;
 }
-// A step's share: at least 64 tokens.  Calls of steps alone over at most
-// kOwnPlan sequences make their plan in every CTA (a scan of one warp) instead
-// of a launch of its own.
-constexpr int kStepFew = 2;
+constexpr int kStepFew = 2;   // a step's share: at least 64 tokens
+
+// Tiles of a sequence's units for one K/V head, every `stride`-th from u0 on.
+template <int RU, int KTL>
+__device__ __forceinline__ int64_t units_tiles(const Seq& s, const AttnShape& sh, int u0, int stride) {
+  const int64_t all = static_cast<int64_t>(s.n) * sh.group;
+  const int units = static_cast<int>((all + RU - 1) / RU);
+  int64_t c = 0;
+  for (int u = u0; u < units; u += stride) {
+    const Unit x = unit_of<RU>(s, sh.group, u);
+    c += span_of<KTL>(x.p0, x.p1, s.keys, sh.window, sh.sinks).n;
+  }
+  return c;
+}
+// The most tiles that a unit of the sequence may see: the last one's, but for a
+// few where it is short and a window cuts them all.
+template <int RU, int KTL>
+__device__ __forceinline__ int longest_unit(const Seq& s, const AttnShape& sh) {
+  const Unit x = unit_of<RU>(s, sh.group, static_cast<int>((static_cast<int64_t>(s.n) * sh.group - 1) / RU));
+  return span_of<KTL>(x.p0, x.p1, s.keys, sh.window, sh.sinks).n + 4;
+}
+
+// Where a kernel reads its class's line.
+struct Line {
+  const int64_t* pre;
+  int64_t total, per;
+};
+// Calls over at most kOwnPlan sequences make the line in every CTA, by all its
+// warps, instead of by a launch before: step (at most kStepRows rows) or tile
+// class of a call that has both, or all sequences (`every`).
 constexpr int kOwnPlan = 128;
+struct OwnPlan {
+  int64_t pre[kOwnPlan + 1];
+  int64_t per;
+  int longest;
+};
+template <bool STEP, int RU, int KTL>
+__device__ __forceinline__ Line make_line(OwnPlan& o, const Table& t, const Batch& b, const AttnShape& sh, int heads, int workers,
+                                          bool every) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+  if (threadIdx.x == 0) o.longest = 0;
+  __syncthreads();
+  for (int i0 = 32 * warp; i0 < t.seqs; i0 += 32 * nw) {   // a lane a sequence
+    const int i = i0 + lane;
+    Seq s{0, 0, 0, 0};
+    if (i < t.seqs) {
+      s = seq_of(t, b, i);
+      if (s.n > sh.max_q) {
+        if (blockIdx.x == 0) atomicOr(b.err, DEV_ERR_BATCH);
+        s.n = 0;
+      }
+    }
+    const bool step = static_cast<int64_t>(s.n) * sh.group <= kStepRows;
+    const bool on = s.n > 0 && (every || step == STEP);
+    int64_t mine = 0;
+    if (STEP) {
+      if (on) mine = step_tiles(s, sh);
+      if (on) atomicMax(&o.longest, static_cast<int>(mine));
+    } else {
+      if (on) atomicMax(&o.longest, longest_unit<RU, KTL>(s, sh));
+      uint32_t todo = __ballot_sync(0xffffffffu, on);
+      while (todo) {                                       // a chunk's units: the lanes together
+        const int src = __ffs(todo) - 1;
+        todo &= todo - 1;
+        Seq c{0, 0, 0, 0};
+        c.n = __shfl_sync(0xffffffffu, s.n, src);
+        c.len = __shfl_sync(0xffffffffu, s.len, src);
+        c.keys = __shfl_sync(0xffffffffu, s.keys, src);
+        int64_t tiles = units_tiles<RU, KTL>(c, sh, lane, 32);
+#pragma unroll
+        for (int f = 16; f > 0; f >>= 1) tiles += __shfl_xor_sync(0xffffffffu, tiles, f);
+        if (lane == src) mine = tiles;
+      }
+    }
+    if (i < t.seqs) o.pre[i] = mine * heads;
+  }
+  __syncthreads();
+  if (warp == 0) {
+    int64_t at = 0;
+    for (int i0 = 0; i0 < t.seqs; i0 += 32) {
+      const int i = i0 + lane;
+      const int64_t c = i < t.seqs ? o.pre[i] : 0;
+      int64_t inc = c;
+#pragma unroll
+      for (int f = 1; f < 32; f <<= 1) {
+        const int64_t up = __shfl_up_sync(0xffffffffu, inc, f);
+        if (lane >= f) inc += up;
+      }
+      if (i < t.seqs) o.pre[i] = at + inc - c;
+      at += __shfl_sync(0xffffffffu, inc, 31);
+    }
+    if (lane == 0) {
+      o.pre[t.seqs] = at;
+      o.per = share_of(at, o.longest, workers, STEP ? kStepFew : 1);
+    }
+  }
+  __syncthreads();
+  return Line{o.pre, o.pre[t.seqs], o.per};
+}
 
 }  // namespace paged
 }  // namespace fg

@@ -187,50 +187,11 @@ __global__ void __launch_bounds__(32 * kWarps, kCtasPerSm<NB>) step_kernel(const
 
   tc::griddep_launch();
   tc::griddep_wait();
-  __shared__ int64_t own_pre[kOwnPlan + 1];
-  __shared__ int64_t own_head[2];
-  const int64_t* pre = pl.pre;
-  int64_t total, per;
-  if (own_plan) {
-    if (warp == 0) {
-      int64_t at = 0;
-      int longest = 0;
-      for (int i0 = 0; i0 < a.tab.seqs; i0 += 32) {
-        const int i = i0 + lane;
-        int tiles = 0;
-        if (i < a.tab.seqs) {
-          const Seq s = seq_of(a.tab, a.batch, i);
-          if (s.n > a.shape.max_q) {
-            if (blockIdx.x == 0) atomicOr(a.batch.err, DEV_ERR_BATCH);
-          } else if (s.n > 0) {
-            tiles = step_tiles(s, a.shape);
-          }
-        }
-        int64_t inc = static_cast<int64_t>(tiles) * a.pool.heads;
-        const int64_t cost = inc;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int64_t up = __shfl_up_sync(0xffffffffu, inc, o);
-          if (lane >= o) inc += up;
-        }
-        if (i < a.tab.seqs) own_pre[i] = at + inc - cost;
-        at += __shfl_sync(0xffffffffu, inc, 31);
-        longest = max(longest, static_cast<int>(__reduce_max_sync(0xffffffffu, static_cast<unsigned>(tiles))));
-      }
-      if (lane == 0) {
-        own_pre[a.tab.seqs] = at;
-        own_head[0] = at;
-        own_head[1] = share_of(at, longest, pl.workers, kStepFew);
-      }
-    }
-    __syncthreads();
-    pre = own_pre;
-    total = own_head[0];
-    per = own_head[1];
-  } else {
-    total = pl.head[0];
-    per = pl.head[1];
-  }
+  __shared__ OwnPlan own;
+  const Line line = own_plan ? make_line<true, kStepRows, kTileLog2>(own, a.tab, a.batch, a.shape, a.pool.heads, pl.workers, false)
+                             : Line{pl.pre, pl.head[0], pl.head[1]};
+  const int64_t* const pre = line.pre;
+  const int64_t total = line.total, per = line.per;
   const int64_t o0 = w * per;
   if (o0 >= total) {
     if (lane == 0) pl.rec[w] = make_int4(-1, 0, 0, 0);
@@ -768,7 +729,7 @@ fg_status launch(const AttnArgs<__half>& a, const ClassPlan& pl, bool own_plan, 
   cfg.dynamicSmemBytes = bytes;
   cfg.stream = st;
   cfg.attrs = pdl;
-  cfg.numAttrs = own_plan ? 0 : 1;   // a plan of its own: the first launch of the call, which waits for what ran before
+  cfg.numAttrs = own_plan ? 0 : 1;   // with a plan of its own the call's first launch: it waits for all that ran before
   if (cudaLaunchKernelEx(&cfg, step_kernel<D, NB>, a, pl, own_plan) != cudaSuccess) return check_launch("step_kernel (launch)");
   return check_launch("step_kernel");
 }

@@ -86,8 +86,8 @@ __device__ __forceinline__ void walk_seq(Walk& k, const AttnArgs<__half>& a) {
   k.u = 0;
 }
 // Share w's first segment (left = 0: none).
-__device__ __forceinline__ void walk_begin(Walk& k, const AttnArgs<__half>& a, const ClassPlan& pl, int w) {
-  const int64_t total = pl.head[0], per = pl.head[1], o0 = w * per;
+__device__ __forceinline__ void walk_begin(Walk& k, const AttnArgs<__half>& a, const Line& pl, int w) {
+  const int64_t total = pl.total, per = pl.per, o0 = w * per;
   k.left = 0;
   if (o0 >= total) return;
   int lo = 0, hi = a.tab.seqs;   // pre[lo] <= o0 < pre[hi]
@@ -112,7 +112,7 @@ __device__ __forceinline__ void walk_begin(Walk& k, const AttnArgs<__half>& a, c
   k.x1 = k.x + (k.left < k.sp.n - k.x ? k.left : k.sp.n - k.x);
 }
 // On to the next segment.
-__device__ __forceinline__ void walk_next(Walk& k, const AttnArgs<__half>& a, const ClassPlan& pl) {
+__device__ __forceinline__ void walk_next(Walk& k, const AttnArgs<__half>& a, const Line& pl) {
   k.left -= k.x1 - k.x;
   if (k.left == 0) return;
   if (++k.u == k.units) {
@@ -236,7 +236,7 @@ __device__ __forceinline__ void load_meta(float (&v)[NG], const float* base, uin
 }
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, 1) tile_kernel(const AttnArgs<__half> a, const ClassPlan pl, uint32_t wait_limit) {
+__global__ void __launch_bounds__(kThreads, 1) tile_kernel(const AttnArgs<__half> a, const ClassPlan pl, uint32_t wait_limit, const bool own_plan, const bool every) {
   using S = Smem<D>;
   constexpr int NG = D / 64;
   constexpr uint32_t kIdescS = idesc_f16(128, 128, 0, 0);   // A = Q (K-major), B = K (K-major)
@@ -287,10 +287,20 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const AttnArgs<__half
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   griddep_launch();
-  griddep_wait();   // the plan, and what ran before it
+  // With a plan of its own the kernel follows the step kernel, which began when all before the call was complete: nothing
+  // of it is needed here, and the wait is left to the end (so that what follows this kernel follows that one too).
+  __shared__ OwnPlan own;
+  if (!own_plan) griddep_wait();
+  __shared__ Line line;   // not in registers: it is read between segments only
+  {
+    const Line x = own_plan ? make_line<false, kRows, kKeysLog2>(own, a.tab, a.batch, a.shape, a.pool.heads, pl.workers, every)
+                            : Line{pl.pre, pl.head[0], pl.head[1]};
+    if (threadIdx.x == 0) line = x;
+    __syncthreads();
+  }
 
   Walk k;
-  walk_begin(k, a, pl, w);
+  walk_begin(k, a, line, w);
 
   if (warp >= kSoftWarps && warp < kSoftWarps + kRestoreWarps) {
     // ---- restoring warps: task n is K (n % 8 < 4) or V of 32 keys of tile n / 8 ------------
@@ -323,7 +333,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const AttnArgs<__half
       }
       // on by 7 tasks: a tile further, unless the task was a tile's first
       if ((seen & 7) != 0 && ++nxx == nx.x1) {
-        walk_next(nx, a, pl);
+        walk_next(nx, a, line);
         nxx = nx.x;
         if (nx.left > 0) enter();
       }
@@ -457,7 +467,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const AttnArgs<__half
         }
         ++n;
         nb += two;
-        walk_next(k, a, pl);
+        walk_next(k, a, line);
       }
       mma_commit(done);
       if (!ok) atomicOr(a.batch.err, DEV_ERR_WAIT_TIMEOUT);
@@ -477,7 +487,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const AttnArgs<__half
       const int tiles = k.x1 - k.x;
       if (grp == 1 && k.un.rows <= 128) {
         g0 += tiles;
-        walk_next(k, a, pl);
+        walk_next(k, a, line);
         continue;
       }
       const bool from_start = k.x == 0, to_end = k.x1 == k.sp.n;
@@ -659,12 +669,12 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const AttnArgs<__half
       if (!whole && on) pl.stat[slot] = make_float2(m, l);
       if (from_start && !to_end) {
         // the item's first tile in the line: the share's first tiles, then those of the segments before it
-        const int64_t per = pl.head[1], start = w * per + g0;
+        const int64_t per = line.per, start = w * per + g0;
         rec = make_int4(k.i, k.h, k.u, static_cast<int>((start + k.sp.n - 1) / per));
       }
       ++seg;
       g0 += tiles;
-      walk_next(k, a, pl);
+      walk_next(k, a, line);
     }
     if (threadIdx.x == 0) pl.rec[w] = rec;
   }
@@ -679,10 +689,11 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const AttnArgs<__half
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
   }
+  if (own_plan) griddep_wait();
 }
 
 template <int D>
-fg_status launch(const AttnArgs<__half>& a, const ClassPlan& pl, cudaStream_t st) {
+fg_status launch(const AttnArgs<__half>& a, const ClassPlan& pl, bool own_plan, bool every, cudaStream_t st) {
   using S = Smem<D>;
   static bool set[64] = {false};
   int dev = 0;
@@ -702,15 +713,15 @@ fg_status launch(const AttnArgs<__half>& a, const ClassPlan& pl, cudaStream_t st
   cfg.dynamicSmemBytes = S::kBytes;
   cfg.stream = st;
   cfg.attrs = pdl;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, tile_kernel<D>, a, pl, wait_limit()) != cudaSuccess) return check_launch("tile_kernel (launch)");
+  cfg.numAttrs = own_plan && every ? 0 : 1;   // then the call's first launch: it waits for all that ran before
+  if (cudaLaunchKernelEx(&cfg, tile_kernel<D>, a, pl, wait_limit(), own_plan, every) != cudaSuccess) return check_launch("tile_kernel (launch)");
   return check_launch("tile_kernel");
 }
 
 }  // namespace
 
-fg_status paged_attention_tile(const AttnArgs<__half>& a, const ClassPlan& pl, int head_dim, cudaStream_t st) {
-  return head_dim == 128 ? launch<128>(a, pl, st) : launch<64>(a, pl, st);
+fg_status paged_attention_tile(const AttnArgs<__half>& a, const ClassPlan& pl, int head_dim, bool own_plan, bool every, cudaStream_t st) {
+  return head_dim == 128 ? launch<128>(a, pl, own_plan, every, st) : launch<64>(a, pl, own_plan, every, st);
 }
 
 }  // namespace paged
