@@ -14,7 +14,12 @@
 //            over thousands of tokens would lose its low bits.  The weight w =
 //            p * scale is rounded to fp16 for the MMA after scaling by a power
 //            of two near 1 / max scale, so that small activations keep their
-//            bits; sum w is an MMA against ones, of the rounded weights.
+//            bits; sum w is an MMA against ones, of the rounded weights.  Where
+//            rows leave half the MMA's columns free (1 to 4; up to 8 when a
+//            call has sequences of more than 8), those carry the rounding's
+//            remainders: the result is then as exact as fp32 sums of unrounded
+//            weights (2.1e-4 of its size off, the fp16 result's own rounding;
+//            otherwise 3.1 to 3.6e-4).
 // A warp is a worker (see paged_sched.cuh) and walks tiles of 32 tokens of its
 // share: its own ring of stages in shared memory, filled by asynchronous
 // copies kStages - 1 tiles ahead across items; no CTA barrier.  Where the next
@@ -52,7 +57,7 @@ template <int NB>
 constexpr int kCtasPerSm = 3;
 template <int D, int NB>
 constexpr int kStepStages = D == 128 ? 3 : 4;
-constexpr float kMostSum = 4096.0f;     // a lane's tile sum up to which its weights stand as fp16 (times 2 at most)
+constexpr float kMostSum = 4096.0f;     // a lane's tile sum up to which its weights, times 8 at most, stand as fp16
 
 template <int D>
 struct Stage {
@@ -296,9 +301,13 @@ __global__ void __launch_bounds__(32 * kWarps, kCtasPerSm<NB>) step_kernel(const
   float m[NB][2];
   float2 l[NB], cmn[NB][NG];
   float acc[NB][NT][4];
-  float cap[NG], inv[NG];                        // weights carry the factor inv = 2 / cap
+  float cap[NG], inv[NG];                        // weights carry the factor inv = 8 / cap
   uint32_t nans = 0;                             // bit 4 nb + 2 e + g: the query sees a NaN value group
   int rows = 0, row0 = 0, keys = 0;
+  // Up to four rows (eight with two blocks of columns) leave half of the MMAs' columns free: columns 4 .. 7 (the second
+  // block) take the same queries again and carry what the rounding of the weights to fp16 left over, so that the two add
+  // up to the weights in full.
+  bool split = false;
   const float kc2 = a.scale_log2;
 
   int pn[NB][2];                                 // positions of queries 2 tig, 2 tig + 1 (none: below every key)
@@ -308,12 +317,13 @@ __global__ void __launch_bounds__(32 * kWarps, kCtasPerSm<NB>) step_kernel(const
     const int h = info.z;
     const Seq sq = seq_of(a.tab, a.batch, info.w);
     rows = sq.n * a.shape.group;
+    split = rows <= 4 * NB;
     row0 = sq.row0;
     keys = sq.keys;
     const int pos0 = sq.len - sq.n;
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
-      const int n = 8 * nb + gq;
+      const int n = !split ? 8 * nb + gq : NB == 1 ? gq & 3 : gq;
       QFrag<NG> f;
       if (n < rows) {
         const int t = n / a.shape.group;
@@ -342,7 +352,7 @@ __global__ void __launch_bounds__(32 * kWarps, kCtasPerSm<NB>) step_kernel(const
       }
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const int k = 8 * nb + 2 * tig + e;
+        const int k = !split ? 8 * nb + 2 * tig + e : NB == 1 ? (2 * tig + e) & 3 : 2 * tig + e;
         pn[nb][e] = k < rows ? pos0 + k / a.shape.group : -(1 << 30);
         m[nb][e] = -INFINITY;
       }
@@ -429,8 +439,8 @@ __global__ void __launch_bounds__(32 * kWarps, kCtasPerSm<NB>) step_kernel(const
         }
       __syncwarp();
     }
-    // The weights' factor: a power of two that keeps max scale * factor in [1,
-    // 2).  A group whose scale is not finite stands for NaN: it is noted for
+    // The weights' factor: a power of two that keeps max scale * factor in [4,
+    // 8).  A group whose scale is not finite stands for NaN: it is noted for
     // the queries that see it and leaves the sums.
     float vs_all[2][2][NG];
 #pragma unroll
@@ -464,8 +474,8 @@ __global__ void __launch_bounds__(32 * kWarps, kCtasPerSm<NB>) step_kernel(const
           }
         __syncwarp();
         const uint32_t bits = __reduce_max_sync(0xffffffffu, __float_as_uint(mx));
-        const uint32_t e = min(max(bits >> 23, 1u), 253u);   // biased exponent
-        const float ncap = __uint_as_float((e + 1) << 23), ninv = __uint_as_float((254u - e) << 23);
+        const uint32_t e = min(max(bits >> 23, 4u), 253u);   // biased exponent
+        const float ncap = __uint_as_float((e + 1) << 23), ninv = 4.0f * __uint_as_float((254u - min(e, 251u)) << 23);
         if (ncap > cap[g]) {
           if (inv[g] != 0.0f) {
             const float f = ninv / inv[g];
@@ -567,7 +577,11 @@ __global__ void __launch_bounds__(32 * kWarps, kCtasPerSm<NB>) step_kernel(const
         for (int r = 0; r < 2; ++r) {
 #pragma unroll
           for (int nb = 0; nb < NB; ++nb) {
-            const float2 wt = mul2(pw[nb][hf][r], both(vf[hf][r][g]));
+            float2 wt = mul2(pw[nb][hf][r], both(vf[hf][r][g]));
+            if (split && (NB == 1 ? tig >= 2 : nb == 1)) {
+              const float2 hi = unpack_h2(pack_h2(wt.x, wt.y));
+              wt = make_float2(wt.x - hi.x, wt.y - hi.y);
+            }
             cmn[nb][g] = fma2(pw[nb][hf][r], both(mid[hf][r][g]), cmn[nb][g]);
             vb[nb][hf][r] = movmatrix_trans(pack_h2(wt.x, wt.y));
           }
@@ -620,6 +634,12 @@ __global__ void __launch_bounds__(32 * kWarps, kCtasPerSm<NB>) step_kernel(const
     const int h = reinterpret_cast<const int4*>(s + St::kInfo)->z;
 #pragma unroll
     for (int o = 4; o < 32; o <<= 1) nans |= __shfl_xor_sync(0xffffffffu, nans, o);
+    if (split) {   // the weights' remainders
+#pragma unroll
+      for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[0][i][e] += NB == 1 ? __shfl_xor_sync(0xffffffffu, acc[0][i][e], 2) : acc[NB - 1][i][e];
+    }
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb)
 #pragma unroll

@@ -809,3 +809,22 @@ def test_python_checks(fg):
         fg.PagePool.of(S.pool.k_codes, S.pool.k_mins.half(), S.pool.k_scales, S.pool.v_codes, S.pool.v_mins, S.pool.v_scales)
     with pytest.raises(ValueError):
         fg.PageTable(S.tab.table, S.tab.lens.long(), S.tab.refs, 16)
+
+
+def test_waits_that_run_out_are_reported(fg):
+    """With a wait limit of 0 the chunk kernel gives up at once, reports it, and the next call is right."""
+    S = Setup(fg, [500, 300], 2, 128, 64, torch.float16, 42)
+    cu = np.array([0, 400, 500])
+    q = _q(S, 500, 4)
+    want = _attend(fg, S, cu, q, 4)
+    fg.fg_sync_status()
+    old = fg.fg_set_wait_limit(0)
+    try:
+        _attend(fg, S, cu, q, 4)
+        with pytest.raises(fg.FGError) as e:
+            fg.fg_sync_status()
+        assert e.value.status == 7
+    finally:
+        fg.fg_set_wait_limit(old)
+    assert torch.equal(_attend(fg, S, cu, q, 4), want)
+    fg.fg_sync_status()
