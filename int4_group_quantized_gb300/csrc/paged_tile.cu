@@ -197,6 +197,14 @@ __device__ __forceinline__ float2 halves(uint32_t h) {   // fp16x2 in fp32
   asm("{ .reg .f16 a, b; mov.b32 {a, b}, %2; cvt.f32.f16 %0, a; cvt.f32.f16 %1, b; }" : "=f"(r.x), "=f"(r.y) : "r"(h));
   return r;
 }
+__device__ __forceinline__ uint32_t mbar_test(uint64_t* bar, uint32_t parity) {   // without waiting
+  uint32_t over;
+  asm volatile("{ .reg .pred p; mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
+               : "=r"(over)
+               : "r"(smem_u32(bar)), "r"(parity)
+               : "memory");
+  return over;
+}
 // 64 codes (32 bytes) of one group through fp16(fmaf(q, scale, min)) into row
 // r of a swizzled panel.
 __device__ __forceinline__ void restore_group(const uint4& lo, const uint4& hi, float scale, float mn, uint8_t* prow, int r) {
@@ -253,9 +261,10 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const AttnArgs<__half
   uint64_t* bars = reinterpret_cast<uint64_t*>(sKV + 2 * S::kStage + 4 * S::kFlags);
   uint64_t* qfull = bars;         // [group] Q of the segment is in place
   uint64_t* kfull = bars + 2;     // [stage]
-  uint64_t* kfree = bars + 4;
-  uint64_t* vfull = bars + 6;
-  uint64_t* vfree = bars + 8;
+  uint64_t* vfull = bars + 4;
+  // Release c (barrier c % 2) says that S of tile c and P V of tile c - 1 have read their operands: K's place of tile c and
+  // V's of tile c - 1 are free.
+  uint64_t* freed = bars + 6;
   uint64_t* sfull = bars + 10;    // [group] S of the tile is in tensor memory
   uint64_t* pfull = bars + 12;    // [group] P of the tile is
   uint64_t* odone = bars + 14;    // [group] the segment's last P V has completed
@@ -271,8 +280,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const AttnArgs<__half
       mbar_init(&qfull[i], 4);
       mbar_init(&kfull[i], 4);
       mbar_init(&vfull[i], 4);
-      mbar_init(&kfree[i], 1);
-      mbar_init(&vfree[i], 1);
+      mbar_init(&freed[i], 1);
       mbar_init(&sfull[i], 2);   // the commit, and the issuer itself: it has seen K's barrier, and so the tile's flags
       mbar_init(&pfull[i], 4);
       mbar_init(&odone[i], 1);
@@ -365,7 +373,8 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const AttnArgs<__half
     auto restore = [&](Raw<NG>& v) {   // task n
       const int g = n >> 3, st = g & 1, quarter = n & 3, r = 32 * quarter + lane;
       const bool value = n & 4;
-      bool ok = mbar_wait(value ? &vfree[st] : &kfree[st], ((g >> 1) & 1) ^ 1, wait_limit, abort_flag);
+      const int c = value ? g - 1 : g - 2;   // the release that frees the place
+      bool ok = g < 2 || mbar_wait(&freed[c & 1], (c >> 1) & 1, wait_limit, abort_flag);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) return false;
       if (value) {
@@ -373,7 +382,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const AttnArgs<__half
         for (int q = 0; q < NG; ++q)
           if (!(fabsf(v.scale[q]) < INFINITY)) v.scale[q] = v.mn[q] = 0.0f;   // such a group is NaN: see its flag
       } else {
-        // A slot of the ring is free: S of tile g - 2 is complete, so every softmax warp is past tile g - 4.
+        // A slot of the ring of four is free: S of tile g - 2 is complete, so every softmax warp is past tile g - 4.
         uint32_t* f = sFlags + (g & 3) * 16 + quarter;
         const uint32_t absent = __ballot_sync(0xffffffffu, v.absent);
         const uint32_t nan0 = __ballot_sync(0xffffffffu, !(fabsf(v.vscale[0]) < INFINITY));
@@ -431,6 +440,10 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const AttnArgs<__half
         if (ok) ok = mbar_wait(bar, phase & 1, wait_limit, abort_flag);
         return ok;
       };
+      // A wait takes some 250 cycles even where it is over (the MMAs' operand reads fill shared memory) and an MMA is taken
+      // every 64, few of them ahead: so the next batch's barrier is looked at before a batch is issued, and waited for after
+      // it only where it was not over yet.
+      auto look = [&](uint64_t* bar, int phase) { return mbar_test(bar, phase & 1); };
       while (k.left > 0 && ok) {
         const bool two = k.un.rows > 128;
         if (!wait(&qfull[0], n) || !wait(&kfull[g & 1], g >> 1)) break;
@@ -441,29 +454,35 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const AttnArgs<__half
           tc_fence_after();
           issue_s(1, g);
         }
-        mma_commit(&kfree[g & 1]);
+        mma_commit(&freed[g & 1]);
+        if (!wait(&vfull[g & 1], g >> 1)) break;
         for (int x = k.x; x < k.x1 && ok; ++x, ++g) {
           const bool first = x == k.x, last = x + 1 == k.x1;
-          if (!wait(&pfull[0], g) || !wait(&vfull[g & 1], g >> 1)) break;
+          if (!wait(&pfull[0], g)) break;
           tc_fence_after();
+          const uint32_t k_in = last ? 1u : look(&kfull[(g + 1) & 1], (g + 1) >> 1);
           issue_o(0, g, first);
+          const uint32_t p_in = two ? look(&pfull[1], gb) : 1u;
           if (last) {
             mma_commit(&odone[0]);
           } else {
-            if (!wait(&kfull[(g + 1) & 1], (g + 1) >> 1)) break;
+            if (!k_in && !wait(&kfull[(g + 1) & 1], (g + 1) >> 1)) break;
             tc_fence_after();
             issue_s(0, g + 1);
           }
+          const uint32_t v_in = last ? 1u : look(&vfull[(g + 1) & 1], (g + 1) >> 1);
           if (two) {
-            if (!wait(&pfull[1], gb)) break;
+            if (!p_in && !wait(&pfull[1], gb)) break;
             tc_fence_after();
             issue_o(1, g, first);
             if (last) mma_commit(&odone[1]);
             else issue_s(1, g + 1);
             ++gb;
           }
-          mma_commit(&vfree[g & 1]);
-          if (!last) mma_commit(&kfree[(g + 1) & 1]);
+          if (!last) {
+            mma_commit(&freed[(g + 1) & 1]);
+            if (!v_in && !wait(&vfull[(g + 1) & 1], (g + 1) >> 1)) break;
+          }
         }
         ++n;
         nb += two;
