@@ -395,7 +395,9 @@ typedef struct {
  * packed activations, none for a sequence that takes no part.  lens counts
  * those tokens already: row t of n stands at position lens[i] - n + t.
  * Calls that touch one table or workspace run in stream order; two calls at
- * once need workspaces of their own. */
+ * once need workspaces of their own.  The first call on a device looks up the
+ * library's error word and sets the kernels' shared-memory limits: make it
+ * before a capture. */
 
 /* Grow every sequence by its rows of `cu` (the values alone matter, not where
  * they start): lens[i] += n, and entries of the row are filled with free pages,
@@ -452,6 +454,8 @@ fg_status fg_paged_append(const fg_page_pool* pool, const fg_page_table* t, cons
  * is not finite makes that group's columns NaN for the rows that see it, and
  * for no other.  A missing page's tokens are not seen.
  * max_q bounds the rows of one sequence; longer ones are refused on the device.
+ * Results are the same bits every time for one max_q class (up to 8, up to 16,
+ * more rows per K/V head); out must not overlap q.
  * Rows outside cu[0] .. cu[seqs] are left as they are.  ws: device, 256-byte
  * aligned, >= fg_paged_attention_workspace_bytes. */
 size_t fg_paged_attention_workspace_bytes(const fg_page_pool* pool, const fg_page_table* t, int32_t q_heads,

@@ -57,6 +57,7 @@ __device__ __forceinline__ Seq seq_of(const Table& t, const Batch& b, int i) {
   s.len = ok ? len : 0;
   const int64_t cap = t.stride << t.ps_log2;
   s.keys = s.len > cap ? static_cast<int>(cap) : s.len;
+  if (s.n > 0 && s.len > cap) atomicOr(b.err, DEV_ERR_PAGE);
   return s;
 }
 

@@ -382,6 +382,10 @@ fg_status check_attn(const fg_page_pool* pool, const fg_page_table* t, int32_t q
   if (q_heads % pool->heads)
     return fail(FG_ERR_SHAPE, "q_heads %d is no multiple of the pool's %d heads", q_heads, pool->heads);
   if (ntok * q_heads > INT32_MAX - 1024) return fail(FG_ERR_UNSUPPORTED, "more than 2^31 (row, head) pairs");
+  // a worker counts its tiles in an int: units of at least 16 rows, tiles of at least 32 tokens, at least 64 workers
+  const double units = static_cast<double>(ntok) * (q_heads / pool->heads) / 16 + t->seqs;
+  const double tiles = static_cast<double>(t->stride) * t->page_size / 32 + 2;
+  if (units * tiles * pool->heads / 64 > 2e9) return fail(FG_ERR_UNSUPPORTED, "more than 2^31 tiles for a worker");
   return FG_OK;
 }
 

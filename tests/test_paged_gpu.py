@@ -828,3 +828,127 @@ def test_waits_that_run_out_are_reported(fg):
         fg.fg_set_wait_limit(old)
     assert torch.equal(_attend(fg, S, cu, q, 4), want)
     fg.fg_sync_status()
+
+
+@pytest.mark.parametrize("seqs", [129, 300, 1100])
+@pytest.mark.parametrize("kind", ["steps", "chunks", "f32"])
+def test_many_sequences(fg, seqs, kind):
+    """More sequences than a kernel plans for by itself; some take no part."""
+    rng = np.random.default_rng(seqs)
+    lens = rng.integers(1, 60, seqs)
+    n = np.where(rng.random(seqs) < 0.3, 0, 1)
+    if kind != "steps":
+        n = np.where(rng.random(seqs) < 0.2, rng.integers(1, 60, seqs), n)
+    n = np.minimum(n, lens)
+    dtype = torch.float32 if kind == "f32" else torch.float16
+    S = Setup(fg, lens, 1, 64, 16, dtype, seqs)
+    cu = np.concatenate(([0], np.cumsum(n)))
+    q = _q(S, int(cu[-1]), 2)
+    out = _attend(fg, S, cu, q, 2)
+    fg.fg_sync_status()
+    ref, tol = _expect(S, cu, q.cpu().numpy().astype(np.float64), 2, 0, 0, True)
+    if kind == "chunks":   # the bound of a chunk where a sequence is one, of a step elsewhere: the larger
+        tol = np.maximum(tol, _expect(S, cu, q.cpu().numpy().astype(np.float64), 2, 0, 0, False)[1])
+    _compare(S, out, ref, tol, cu)
+
+
+@pytest.mark.parametrize("n", [[1, 1, 1], [1, 13, 40]])
+@pytest.mark.parametrize("heads", [(20, 1), (40, 2), (33, 1)])
+def test_more_query_heads_than_a_step_takes(fg, n, heads):
+    qh, h = heads
+    S = Setup(fg, [300, 13, 129], h, 128, 32, torch.float16, 50)
+    cu = np.concatenate(([0], np.cumsum(n)))
+    q = _q(S, int(cu[-1]), qh)
+    out = _attend(fg, S, cu, q, qh, window=90, sinks=2)
+    fg.fg_sync_status()
+    ref, tol = _expect(S, cu, q.cpu().numpy().astype(np.float64), qh, 90, 2, False)
+    _compare(S, out, ref, tol, cu, 3 * U)
+
+
+@pytest.mark.parametrize("n", [[1, 1], [30, 40]])
+@pytest.mark.parametrize("dtype", [torch.float16, torch.float32])
+def test_a_row_too_short_for_its_length(fg, n, dtype):
+    """Tokens past the table row's end are not seen, and reported."""
+    S = Setup(fg, [64, 50], 1, 64, 16, dtype, 51, spare=0)
+    S.lens = np.array([90, 50])
+    S.upload(fg)
+    cu = np.concatenate(([0], np.cumsum(n)))
+    q = _q(S, int(cu[-1]), 2)
+    out = _attend(fg, S, cu, q, 2)
+    with pytest.raises(fg.FGError) as e:
+        fg.fg_sync_status()
+    assert e.value.status == 4
+    ref, tol = _expect(S, cu, q.cpu().numpy().astype(np.float64), 2, 0, 0, max(n) == 1)
+    _compare(S, out, ref, tol, cu)
+
+
+def test_two_calls_at_once(fg):
+    """Two streams, two workspaces, the same pool."""
+    S = Setup(fg, [3000, 900, 1500], 4, 128, 64, torch.float16, 52)
+    jobs = []
+    for n in ([1, 1, 1], [300, 40, 200], [200, 1, 3]):
+        cu = np.concatenate(([0], np.cumsum(n)))
+        q = _q(S, int(cu[-1]), 8)
+        jobs.append((_i32(cu), q, max(n), _attend(fg, S, cu, q, 8), torch.zeros_like(q), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for cu, q, mq, _, out, st in jobs:
+            fg.fg_paged_attention(S.pool, S.tab, cu, q, 8, out, mq, stream=st)
+    torch.cuda.synchronize()
+    fg.fg_sync_status()
+    for *_, want, out, _ in jobs:
+        assert torch.equal(out, want)
+
+
+def test_two_graphs_share_a_workspace(fg):
+    S = Setup(fg, [700, 400], 2, 64, 32, torch.float16, 53)
+    ws = fg.workspace(fg.fg_paged_attention_workspace_bytes(S.pool, S.tab, 4, 300, 200))
+    graphs = []
+    for n in ([1, 1], [200, 100]):
+        cu = np.concatenate(([0], np.cumsum(n)))
+        q = _q(S, int(cu[-1]), 4)
+        want, c, out = _attend(fg, S, cu, q, 4, max_q=200), _i32(cu), torch.zeros_like(q)
+        g = torch.cuda.CUDAGraph()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(g):
+            fg.fg_paged_attention(S.pool, S.tab, c, q, 4, out, 200, ws=ws)
+        graphs.append((g, out, want, c, q))
+    for _ in range(3):
+        for g, out, want, _, _ in graphs:
+            out.zero_()
+            g.replay()
+        torch.cuda.synchronize()
+        for _, out, want, _, _ in graphs:
+            assert torch.equal(out, want)
+    fg.fg_sync_status()
+
+
+def test_offsets_past_32_bits(fg):
+    """Pages more than 4 GB into the arrays: appended, copied and attended."""
+    heads, d, ps, pages = 8, 128, 256, 36000                  # 4.7 GB of codes each for K and V
+    pool = fg.PagePool(pages, ps, heads, d)
+    assert pool.k_codes.numel() > 2 ** 32
+    tab = fg.PageTable.empty(4, 4, pages, ps)
+    tab.refs[:pages - 6] = 1                                  # only the last pages are free
+    rng = np.random.default_rng(60)
+    n = [300, 0, 40, 0]
+    cu = np.concatenate(([0], np.cumsum(n)))
+    x = {w: rng.normal(size=(340, heads * d)).astype(np.float16) for w in "kv"}
+    fg.fg_pages_reserve(tab, _i32(cu))
+    fg.fg_paged_append(pool, tab, _i32(cu), *(torch.as_tensor(x[w], device="cuda") for w in "kv"))
+    fg.fg_pages_fork(tab, fg.PagePools([pool]), _i32([0, 2]), _i32([1, 3]))
+    fg.fg_sync_status()
+    assert tab.table[0, :2].tolist() == [pages - 6, pages - 5] and tab.table[1, 1].item() == pages - 3
+    q = torch.as_tensor(rng.normal(size=(42, heads * d)), device="cuda").half()
+    for m in ([1, 1, 1, 1], [1, 20, 1, 20]):
+        c = np.concatenate(([0], np.cumsum(m)))
+        out = torch.zeros_like(q)
+        fg.fg_paged_attention(pool, tab, _i32(c), q, heads, out, max(m))
+        fg.fg_sync_status()
+        for i, (src, length) in enumerate(((0, 300), (0, 300), (2, 40), (2, 40))):
+            k, v = (op.restore(*codec.quantize_g64(x[w][cu[src]:cu[src + 1]].reshape(-1, heads, d))) for w in "kv")
+            for h in (0, heads - 1):
+                qq = q[c[i]:c[i + 1], h * d:(h + 1) * d].double().cpu().numpy()
+                ref, mag, work = op.attention(qq, k[:, h], v[:, h], np.arange(length - m[i], length))
+                got = out[c[i]:c[i + 1], h * d:(h + 1) * d].double().cpu().numpy()
+                assert (np.abs(got - ref) <= U * (np.abs(ref) + 4 * mag * (1 + work[:, None]) + 4)).all()
