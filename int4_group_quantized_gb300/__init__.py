@@ -607,7 +607,7 @@ class PagePool:
             raise ValueError("codes are [pages][heads][page_size][head_dim/2]")
         self.pages, self.heads, self.page_size = (int(x) for x in k_codes.shape[:3])
         self.head_dim = 2 * int(k_codes.shape[3])
-        self.dtype, self.device = dtype, k_codes.device
+        self.dtype, self.device, self.index = dtype, k_codes.device, k_codes.get_device()
         cs = (self.pages, self.heads, self.page_size, self.head_dim // 2)
         ms = cs[:3] + (self.head_dim // GROUP,)
         self.k_codes = _dense(k_codes, torch.uint8, cs, self.device, "k_codes")
@@ -646,7 +646,7 @@ class PageTable:
         if table.dim() != 2 or refs.dim() != 1:
             raise ValueError("table is [seqs][stride], refs [pages]")
         self.device = table.device
-        self.index = table.device.index if table.device.type == "cuda" else None
+        self.index = table.get_device()   # -1: not on a GPU
         self.table = _dense(table, torch.int32, table.shape, self.device, "table")
         self.lens = _dense(lens, torch.int32, (table.shape[0],), self.device, "lens")
         self.refs = _dense(refs, torch.int32, refs.shape, self.device, "refs")
@@ -670,9 +670,9 @@ class PageTable:
 def _on(tab: "PageTable", stream) -> int:
     """The stream of a paged call; its buffers must be on the current device."""
     i = tab.index
-    if i is not None and i != torch._C._cuda_getDevice():
+    if i < 0 or i != torch._C._cuda_getDevice():
         raise ValueError(f"the page table is on {tab.device}, the current device is {torch.cuda.current_device()}")
-    return torch._C._cuda_getCurrentRawStream(i) if stream is None and i is not None else _stream(stream)
+    return torch._C._cuda_getCurrentRawStream(i) if stream is None else _stream(stream)
 
 
 def _paged_ws(nbytes: int, tab: "PageTable", stream) -> torch.Tensor:
@@ -685,7 +685,7 @@ def _paged_ws(nbytes: int, tab: "PageTable", stream) -> torch.Tensor:
 
 
 def _ints(t: torch.Tensor, n: int, tab: "PageTable", name: str) -> int:
-    if t.dtype is not torch.int32 or t.numel() != n or not t.is_contiguous() or t.device != tab.device:
+    if t.dtype is not torch.int32 or t.numel() != n or not t.is_contiguous() or t.get_device() != tab.index:
         raise ValueError(f"{name}: expected {n} contiguous int32 on {tab.device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
     return t.data_ptr()
 
@@ -693,7 +693,7 @@ def _ints(t: torch.Tensor, n: int, tab: "PageTable", name: str) -> int:
 def _rows(t: torch.Tensor, pool: "PagePool", n: int, cols: int, name: str) -> int:
     """Row stride of t, when it is [n][cols] rows of the pool's type and device with unit column stride."""
     shape = t.shape
-    if len(shape) != 2 or shape[0] != n or shape[1] != cols or t.dtype is not pool.dtype or t.device != pool.device:
+    if len(shape) != 2 or shape[0] != n or shape[1] != cols or t.dtype is not pool.dtype or t.get_device() != pool.index:
         raise ValueError(f"{name}: expected {pool.dtype} rows [{n}][{cols}] on {pool.device}, got {t.dtype} {tuple(shape)} "
                          f"on {t.device}")
     ld, unit = t.stride()

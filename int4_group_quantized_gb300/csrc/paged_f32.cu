@@ -13,6 +13,7 @@
 #include <math.h>
 
 #include "paged_attn.cuh"
+#include "q4_dev.cuh"
 #include "tc_ptx.cuh"
 
 namespace fg {
@@ -191,10 +192,11 @@ __global__ void __launch_bounds__(kThreads) f32_kernel(const AttnArgs<float> a, 
       if (x + 1 < x1) load(x + 1);
       // scores
       float sc[2][4];
+      float2 s2[2][4];   // even and odd dims
 #pragma unroll
       for (int r = 0; r < 2; ++r)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) sc[r][c] = 0.0f;
+        for (int c = 0; c < 4; ++c) s2[r][c] = make_float2(0.0f, 0.0f);
 #pragma unroll 4
       for (int d = 0; d < D; d += 4) {
         float4 q[2], k[4];
@@ -206,12 +208,14 @@ __global__ void __launch_bounds__(kThreads) f32_kernel(const AttnArgs<float> a, 
         for (int r = 0; r < 2; ++r)
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            sc[r][c] = fmaf(q[r].x, k[c].x, sc[r][c]);
-            sc[r][c] = fmaf(q[r].y, k[c].y, sc[r][c]);
-            sc[r][c] = fmaf(q[r].z, k[c].z, sc[r][c]);
-            sc[r][c] = fmaf(q[r].w, k[c].w, sc[r][c]);
+            s2[r][c] = q4::fma_f32x2(make_float2(q[r].x, q[r].y), make_float2(k[c].x, k[c].y), s2[r][c]);
+            s2[r][c] = q4::fma_f32x2(make_float2(q[r].z, q[r].w), make_float2(k[c].z, k[c].w), s2[r][c]);
           }
       }
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) sc[r][c] = s2[r][c].x + s2[r][c].y;
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         float mx = -INFINITY;

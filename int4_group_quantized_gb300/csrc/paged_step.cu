@@ -57,7 +57,7 @@ template <int NB>
 constexpr int kCtasPerSm = 3;
 template <int D, int NB>
 constexpr int kStepStages = D == 128 ? 3 : 4;
-constexpr float kMostSum = 4096.0f;     // a lane's tile sum up to which its weights, times 8 at most, stand as fp16
+constexpr float kGrow = 12.0f;          // how far (in powers of two) a score may lie above the maximum: its weight, times 8 at most, stands as fp16
 
 template <int D>
 struct Stage {
@@ -491,32 +491,20 @@ __global__ void __launch_bounds__(32 * kWarps, kCtasPerSm<NB>) step_kernel(const
         }
       }
     }
-    // Weights for the maximum known so far; it serves while no lane's sum of a query grows past 2^12 (a larger maximum would
-    // only change the scale of sums that are divided in the end).  Before the first key is seen it is -inf, and the sum
-    // infinite or NaN: then, as later where it must, the tile's maximum is found over the lanes of a query and the sums are
-    // rescaled.
-    float2 pw[NB][2][2], lt[NB];
-    auto weigh = [&](bool found) {
+    // The maximum known so far serves while no score of a query lies more than 2^12 above it (a larger one would only change
+    // the scale of sums that are divided in the end).  Otherwise, and before a key was seen, the tile's maximum is found
+    // over the lanes of a query and the sums are rescaled.
+    bool asks[NB][2];
+    bool ask = false;
 #pragma unroll
-      for (int nb = 0; nb < NB; ++nb) {
-        float2 neg = make_float2(-m[nb][0] * kc2, -m[nb][1] * kc2);
-        if (found) neg = make_float2(m[nb][0] == -INFINITY ? 0.0f : neg.x, m[nb][1] == -INFINITY ? 0.0f : neg.y);   // no key: weights 0
-        lt[nb] = both(0.0f);
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf)
-#pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            const float2 x = fma2(sc[nb][hf][r], both(kc2), neg);
-            pw[nb][hf][r] = make_float2(ex2(x.x), ex2(x.y));
-            lt[nb] = add2(lt[nb], pw[nb][hf][r]);
-          }
-      }
-    };
-    weigh(false);
-    bool serves = true;
-#pragma unroll
-    for (int nb = 0; nb < NB; ++nb) serves = serves && lt[nb].x <= kMostSum && lt[nb].y <= kMostSum;
-    if (__any_sync(0xffffffffu, !serves)) {
+    for (int nb = 0; nb < NB; ++nb) {
+      const float x = fmaxf(fmaxf(sc[nb][0][0].x, sc[nb][0][1].x), fmaxf(sc[nb][1][0].x, sc[nb][1][1].x));
+      const float y = fmaxf(fmaxf(sc[nb][0][0].y, sc[nb][0][1].y), fmaxf(sc[nb][1][0].y, sc[nb][1][1].y));
+      asks[nb][0] = (x - m[nb][0]) * kc2 > kGrow;   // -inf - -inf: no
+      asks[nb][1] = (y - m[nb][1]) * kc2 > kGrow;
+      ask = ask || asks[nb][0] || asks[nb][1];
+    }
+    if (__any_sync(0xffffffffu, ask)) {
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
         float x = fmaxf(fmaxf(sc[nb][0][0].x, sc[nb][0][1].x), fmaxf(sc[nb][1][0].x, sc[nb][1][1].x));
@@ -528,7 +516,7 @@ __global__ void __launch_bounds__(32 * kWarps, kCtasPerSm<NB>) step_kernel(const
         }
         // only the queries whose sums ask for it: a row's bits do not depend on its neighbours
         const uint32_t mine = 0x11111111u << tig;
-        const bool ask0 = __ballot_sync(0xffffffffu, !(lt[nb].x <= kMostSum)) & mine, ask1 = __ballot_sync(0xffffffffu, !(lt[nb].y <= kMostSum)) & mine;
+        const bool ask0 = __ballot_sync(0xffffffffu, asks[nb][0]) & mine, ask1 = __ballot_sync(0xffffffffu, asks[nb][1]) & mine;
         const float nm[2] = {ask0 ? fmaxf(m[nb][0], x) : m[nb][0], ask1 ? fmaxf(m[nb][1], y) : m[nb][1]};
         float al[2];
 #pragma unroll
@@ -547,10 +535,19 @@ __global__ void __launch_bounds__(32 * kWarps, kCtasPerSm<NB>) step_kernel(const
         m[nb][0] = nm[0];
         m[nb][1] = nm[1];
       }
-      weigh(true);
     }
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb) l[nb] = add2(l[nb], lt[nb]);
+    for (int nb = 0; nb < NB; ++nb) {
+      const float2 neg = make_float2(m[nb][0] == -INFINITY ? 0.0f : -m[nb][0] * kc2, m[nb][1] == -INFINITY ? 0.0f : -m[nb][1] * kc2);
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const float2 x = fma2(sc[nb][hf][r], both(kc2), neg);
+          sc[nb][hf][r] = make_float2(ex2(x.x), ex2(x.y));   // scores become weights
+          l[nb] = add2(l[nb], sc[nb][hf][r]);
+        }
+    }
     float vf[2][2][NG], mid[2][2][NG];   // factor of p in the weights, value of the centre code
 #pragma unroll
     for (int hf = 0; hf < 2; ++hf)
@@ -577,12 +574,12 @@ __global__ void __launch_bounds__(32 * kWarps, kCtasPerSm<NB>) step_kernel(const
         for (int r = 0; r < 2; ++r) {
 #pragma unroll
           for (int nb = 0; nb < NB; ++nb) {
-            float2 wt = mul2(pw[nb][hf][r], both(vf[hf][r][g]));
+            float2 wt = mul2(sc[nb][hf][r], both(vf[hf][r][g]));
             if (split && (NB == 1 ? tig >= 2 : nb == 1)) {
               const float2 hi = unpack_h2(pack_h2(wt.x, wt.y));
               wt = make_float2(wt.x - hi.x, wt.y - hi.y);
             }
-            cmn[nb][g] = fma2(pw[nb][hf][r], both(mid[hf][r][g]), cmn[nb][g]);
+            cmn[nb][g] = fma2(sc[nb][hf][r], both(mid[hf][r][g]), cmn[nb][g]);
             vb[nb][hf][r] = movmatrix_trans(pack_h2(wt.x, wt.y));
           }
         }
