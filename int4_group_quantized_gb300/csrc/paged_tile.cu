@@ -328,7 +328,21 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const AttnArgs<__half
       last = min(nx.un.p1, nx.s.keys - 1);
       lo = a.shape.window > 0 && nx.un.p0 >= a.shape.window ? nx.un.p0 - a.shape.window + 1 : 0;
     };
-    if (tasks > 0) enter();
+    // The segment's rows of Q on their way into L2, by one warp, two tiles before the softmax warps read them.
+    auto fetch_q = [&]() {
+      if (warp != kSoftWarps) return;
+      const int base = nx.h * a.shape.group;
+      for (int r = lane; r < nx.un.rows; r += 32) {
+        const int row_ = nx.un.r0 + r, t = row_ / a.shape.group;
+        const __half* p = a.q + static_cast<int64_t>(nx.s.row0 + t) * a.ldq + static_cast<int64_t>(base + row_ - t * a.shape.group) * D;
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
+        if (D == 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(p + 64));
+      }
+    };
+    if (tasks > 0) {
+      enter();
+      fetch_q();
+    }
     // the lane's key of task `seen`: the table's entry (not looked at before the load below) and its row in a page (-1: no
     // row of the unit sees the key)
     auto look_up = [&](int& page, int& off) {
@@ -343,7 +357,10 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const AttnArgs<__half
       if ((seen & 7) != 0 && ++nxx == nx.x1) {
         walk_next(nx, a, line);
         nxx = nx.x;
-        if (nx.left > 0) enter();
+        if (nx.left > 0) {
+          enter();
+          fetch_q();
+        }
       }
       seen += kRestoreWarps;
     };
@@ -518,12 +535,17 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const AttnArgs<__half
       {
         const uint4* src = reinterpret_cast<const uint4*>(a.q + static_cast<int64_t>(k.s.row0 + t) * a.ldq + static_cast<int64_t>(head) * D);
         uint8_t* qrow = sQ + grp * S::kQ + rr * 128;
+        // (loops here and below: code that runs once a segment is fetched anew each time, and straight code costs its length)
+#pragma unroll 1
+        for (int c = 0; c < D / 8; c += 4) {
+          uint4 v[4];
 #pragma unroll
-        for (int c = 0; c < D / 8; ++c) {
-          const uint4 v = on ? src[c] : make_uint4(0u, 0u, 0u, 0u);
-          const uint4 o = make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632), __byte_perm(v.y, v.w, 0x5410),
-                                     __byte_perm(v.y, v.w, 0x7632));
-          *reinterpret_cast<uint4*>(qrow + (c >> 3) * S::kPanel + (((c & 7) ^ (rr & 7)) << 4)) = o;
+          for (int e = 0; e < 4; ++e) v[e] = on ? src[c + e] : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            *reinterpret_cast<uint4*>(qrow + (c >> 3) * S::kPanel + ((((c & 7) + e) ^ (rr & 7)) << 4)) =
+                make_uint4(__byte_perm(v[e].x, v[e].z, 0x5410), __byte_perm(v[e].x, v[e].z, 0x7632), __byte_perm(v[e].y, v[e].w, 0x5410),
+                           __byte_perm(v[e].y, v[e].w, 0x7632));
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -660,29 +682,25 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const AttnArgs<__half
       const int64_t slot = (static_cast<int64_t>(w) * 2 + (from_start ? 1 : 0)) * kRows + r;
       __half* dst = a.out + static_cast<int64_t>(k.s.row0 + t) * a.ldo + static_cast<int64_t>(head) * D;
 #pragma unroll 1
-      for (int c = 0; c < D / 32; ++c) {
-        uint32_t u[32];
-        tmem_ld_32x32b_x32(to + 32 * c, u);
+      for (int c = 0; c < D / 16; ++c) {
+        uint32_t u[16];
+        tmem_ld_32x32b_x16(to + 16 * c, u);
         tmem_arrived(u);
         if (!on) continue;   // no collective follows in the round
-        const bool nan = (nans >> (c >> 1)) & 1u;
+        const float fc = (nans >> (c >> 2)) & 1u ? __uint_as_float(0x7fffffffu) : f;   // a NaN group's columns
+        float v[16];         // of 8 columns dims 0..7 lie at 0, 2, 4, 6, 1, 3, 5, 7
 #pragma unroll
-        for (int b = 0; b < 4; ++b) {   // 8 columns: dims 0..7 lie at 0, 2, 4, 6, 1, 3, 5, 7
-          float v[8];
+        for (int e = 0; e < 16; ++e) v[e] = __uint_as_float(u[(e & 8) + ((e & 7) < 4 ? 2 * (e & 7) : 2 * (e & 7) - 7)]) * fc;
+        if (whole) {
+          uint32_t h[8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            v[e] = __uint_as_float(u[8 * b + (e < 4 ? 2 * e : 2 * e - 7)]) * f;
-            if (nan) v[e] = __uint_as_float(0x7fffffffu);
-          }
-          if (whole) {
-            *reinterpret_cast<uint4*>(dst + 32 * c + 8 * b) =
-                make_uint4(q4::cvt_f16x2(make_float2(v[0], v[1])), q4::cvt_f16x2(make_float2(v[2], v[3])),
-                           q4::cvt_f16x2(make_float2(v[4], v[5])), q4::cvt_f16x2(make_float2(v[6], v[7])));
-          } else {
-            float4* part = reinterpret_cast<float4*>(pl.part + slot * D + 32 * c + 8 * b);
-            part[0] = make_float4(v[0], v[1], v[2], v[3]);
-            part[1] = make_float4(v[4], v[5], v[6], v[7]);
-          }
+          for (int e = 0; e < 8; ++e) h[e] = q4::cvt_f16x2(make_float2(v[2 * e], v[2 * e + 1]));
+          *reinterpret_cast<uint4*>(dst + 16 * c) = make_uint4(h[0], h[1], h[2], h[3]);
+          *reinterpret_cast<uint4*>(dst + 16 * c + 8) = make_uint4(h[4], h[5], h[6], h[7]);
+        } else {
+          float4* part = reinterpret_cast<float4*>(pl.part + slot * D + 16 * c);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) part[e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
         }
       }
       if (!whole && on) pl.stat[slot] = make_float2(m, l);
