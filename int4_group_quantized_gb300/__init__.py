@@ -635,6 +635,9 @@ class PagePools:
 
     def __init__(self, pools: list):
         self.pools = list(pools)
+        if any(p.index != self.pools[0].index for p in self.pools):
+            raise ValueError("pools on several devices")
+        self.device, self.index = (self.pools[0].device, self.pools[0].index) if self.pools else (None, None)
         self.arr = (fg_page_pool * len(self.pools))(*(p.struct for p in self.pools))
 
 
@@ -675,13 +678,25 @@ def _on(tab: "PageTable", stream) -> int:
     return torch._C._cuda_getCurrentRawStream(i) if stream is None else _stream(stream)
 
 
-def _paged_ws(nbytes: int, tab: "PageTable", stream) -> torch.Tensor:
-    """A workspace of one call, not reused before the call's stream is done with it."""
-    ws = workspace(nbytes, tab.device)
-    if stream is not None:
-        st = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream), device=tab.device)
-        ws.record_stream(st)
-    return ws
+def _paged_ws(ws, nbytes: int, tab: "PageTable", stream) -> torch.Tensor:
+    """The caller's workspace, or one of this call: allocated on the call's stream, so that the allocator hands its
+    memory to nothing that could run beside the call."""
+    if ws is not None:
+        if ws.get_device() != tab.index or not ws.is_contiguous():
+            raise ValueError(f"workspace: expected a contiguous tensor on {tab.device}, it is on {ws.device}")
+        return ws
+    if stream is None or tab.index < 0:
+        return workspace(nbytes, tab.device)
+    st = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream), device=tab.device)
+    with torch.cuda.stream(st):
+        return workspace(nbytes, tab.device)
+
+
+def _beside(pool, tab: "PageTable"):
+    """The pool (or pools), when it lies on the table's device."""
+    if pool.index != tab.index and pool.index is not None:
+        raise ValueError(f"the pages are on {pool.device}, their table is on {tab.device}")
+    return pool
 
 
 def _ints(t: torch.Tensor, n: int, tab: "PageTable", name: str) -> int:
@@ -709,8 +724,7 @@ def fg_pages_workspace_bytes(tab: PageTable, n: int = 0) -> int:
 
 def fg_pages_reserve(tab: PageTable, cu: torch.Tensor, ws: torch.Tensor | None = None, stream=None) -> None:
     """lens += the rows of cu (int32 [seqs+1]), with pages for them."""
-    if ws is None:
-        ws = _paged_ws(fg_pages_workspace_bytes(tab), tab, stream)
+    ws = _paged_ws(ws, fg_pages_workspace_bytes(tab) if ws is None else 0, tab, stream)
     _check(_lib.fg_pages_reserve(tab._ref, _ints(cu, tab.seqs + 1, tab, "cu"), _ptr(ws), ws.numel(), _on(tab, stream)),
            "fg_pages_reserve")
 
@@ -724,17 +738,15 @@ def fg_pages_fork(tab: PageTable, pools: PagePools, src: torch.Tensor, dst: torc
                   ws: torch.Tensor | None = None, stream=None) -> None:
     """Sequences dst (int32 [n], empty) become copies of src: full pages shared, a partly filled one copied."""
     n = src.numel()
-    if ws is None:
-        ws = _paged_ws(fg_pages_workspace_bytes(tab, n), tab, stream)
-    _check(_lib.fg_pages_fork(tab._ref, pools.arr, len(pools.pools), _ints(src, n, tab, "src"),
+    ws = _paged_ws(ws, fg_pages_workspace_bytes(tab, n) if ws is None else 0, tab, stream)
+    _check(_lib.fg_pages_fork(tab._ref, _beside(pools, tab).arr, len(pools.pools), _ints(src, n, tab, "src"),
                               _ints(dst, n, tab, "dst"), n, _ptr(ws), ws.numel(), _on(tab, stream)), "fg_pages_fork")
 
 
 def fg_pages_compact(tab: PageTable, pools: PagePools, ws: torch.Tensor | None = None, stream=None) -> None:
     """Moves the pages in use to the front of the pools."""
-    if ws is None:
-        ws = _paged_ws(fg_pages_workspace_bytes(tab), tab, stream)
-    _check(_lib.fg_pages_compact(tab._ref, pools.arr, len(pools.pools), _ptr(ws), ws.numel(), _on(tab, stream)),
+    ws = _paged_ws(ws, fg_pages_workspace_bytes(tab) if ws is None else 0, tab, stream)
+    _check(_lib.fg_pages_compact(tab._ref, _beside(pools, tab).arr, len(pools.pools), _ptr(ws), ws.numel(), _on(tab, stream)),
            "fg_pages_compact")
 
 
@@ -752,7 +764,7 @@ def fg_paged_append(pool: PagePool, tab: PageTable, cu: torch.Tensor, k: torch.T
         ldr = _rows(k_restored, pool, n, h1, "k_restored")
         if _rows(v_restored, pool, n, h1, "v_restored") != ldr:
             raise ValueError("k_restored and v_restored need one row stride")
-    _check(_lib.fg_paged_append(pool._ref, tab._ref, _ints(cu, tab.seqs + 1, tab, "cu"), k.data_ptr(), v.data_ptr(), ld, n,
+    _check(_lib.fg_paged_append(_beside(pool, tab)._ref, tab._ref, _ints(cu, tab.seqs + 1, tab, "cu"), k.data_ptr(), v.data_ptr(), ld, n,
                                 _ptr(k_restored), _ptr(v_restored), ldr, _on(tab, stream)), "fg_paged_append")
 
 
@@ -768,8 +780,7 @@ def fg_paged_attention(pool: PagePool, tab: PageTable, cu: torch.Tensor, q: torc
     n = q.shape[0]
     ldq = _rows(q, pool, n, q_heads * pool.head_dim, "q")
     ldo = _rows(out, pool, n, q_heads * pool.head_dim, "out")
-    if ws is None:
-        ws = _paged_ws(fg_paged_attention_workspace_bytes(pool, tab, q_heads, n, max_q), tab, stream)
-    _check(_lib.fg_paged_attention(pool._ref, tab._ref, _ints(cu, tab.seqs + 1, tab, "cu"), q.data_ptr(), ldq, q_heads, n,
+    ws = _paged_ws(ws, fg_paged_attention_workspace_bytes(pool, tab, q_heads, n, max_q) if ws is None else 0, tab, stream)
+    _check(_lib.fg_paged_attention(_beside(pool, tab)._ref, tab._ref, _ints(cu, tab.seqs + 1, tab, "cu"), q.data_ptr(), ldq, q_heads, n,
                                    max_q, window, sinks, out.data_ptr(), ldo, ws.data_ptr(), ws.numel(), _on(tab, stream)),
            "fg_paged_attention")

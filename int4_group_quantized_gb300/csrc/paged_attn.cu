@@ -317,7 +317,7 @@ void carve_class(ClassPlan& c, char*& p, int64_t seqs, int head_dim, int workers
 // The classes that a call of at most max_q rows a sequence can need.
 Layout layout_of(const fg_page_pool& pool, const fg_page_table& t, int32_t q_heads, int64_t max_q, void* ws, int sms) {
   Layout l;
-  const int64_t group = q_heads / pool.heads, most = max_q * group;
+  const int64_t group = q_heads / pool.heads, most = std::min<int64_t>(max_q, INT32_MAX) * group;
   char* p = static_cast<char*>(ws);
   memset(&l.step, 0, sizeof(l.step));
   memset(&l.tile, 0, sizeof(l.tile));
@@ -381,7 +381,7 @@ fg_status check_attn(const fg_page_pool* pool, const fg_page_table* t, int32_t q
   if (q_heads <= 0 || ntok < 0 || max_q < 0) return fail(FG_ERR_ARG, "attention sizes");
   if (q_heads % pool->heads)
     return fail(FG_ERR_SHAPE, "q_heads %d is no multiple of the pool's %d heads", q_heads, pool->heads);
-  if (ntok * q_heads > INT32_MAX - 1024) return fail(FG_ERR_UNSUPPORTED, "more than 2^31 (row, head) pairs");
+  if (ntok > INT32_MAX || ntok * q_heads > INT32_MAX - 1024) return fail(FG_ERR_UNSUPPORTED, "more than 2^31 (row, head) pairs");
   // a worker counts its tiles in an int: units of at least 16 rows, tiles of at least 32 tokens, at least 64 workers
   const double units = static_cast<double>(ntok) * (q_heads / pool->heads) / 16 + t->seqs;
   const double tiles = static_cast<double>(t->stride) * t->page_size / 32 + 2;

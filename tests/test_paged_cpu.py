@@ -146,6 +146,38 @@ def test_page_call_arguments(fg):
     assert L.fg_pages_compact(_br(tab), _br(pool), 1, P, 100, None) == 5
 
 
+def test_a_bound_past_32_bits_is_no_bound(fg):
+    """max_q times the group must not wrap round: the layout is that of the largest bound, with the chunks' class."""
+    pool, tab = _pool(fg), _tab(fg)
+    need = fg.lib.fg_paged_attention_workspace_bytes
+    small, large = need(_br(pool), _br(tab), 4, 64, 2), need(_br(pool), _br(tab), 4, 64, 1 << 20)
+    assert 0 < small < large
+    for mq in ((1 << 31) - 1, 1 << 62, (1 << 63) - 1):
+        assert need(_br(pool), _br(tab), 4, 64, mq) == large
+    for n in (1 << 62, (1 << 63) - 1):
+        assert need(_br(pool), _br(tab), 4, n, 2) == 0
+        assert _attn(fg, pool, tab, ntok=n) == 8
+
+
+def test_python_keeps_a_call_on_one_device(fg):
+    class At:
+        def __init__(self, index):
+            self.index, self.device = index, f"device {index}"
+    assert fg._beside(At(0), At(0)).index == 0
+    for pool, tab in ((At(-1), At(0)), (At(1), At(0)), (At(0), At(1))):
+        with pytest.raises(ValueError):
+            fg._beside(pool, tab)
+    ws = fg.workspace(64, "cpu")
+    with pytest.raises(ValueError):
+        fg._paged_ws(ws, 64, At(0), None)
+    assert fg._beside(fg.PagePools([]), At(0)).index is None      # no pools: the table alone moves
+    layers = [At(0), At(1)]
+    for p in layers:
+        p.struct = _pool(fg)
+    with pytest.raises(ValueError):
+        fg.PagePools(layers)
+
+
 # ---- the oracle -----------------------------------------------------------------
 
 def _check_invariants(pg, pages):

@@ -793,6 +793,20 @@ def test_on_another_stream(fg):
         assert torch.equal(out, want)
 
 
+def test_a_calls_own_workspace_belongs_to_its_stream(fg):
+    """A workspace freed by a call on one stream may still be in use there: a call on another stream has other memory."""
+    S = Setup(fg, [300], 2, 64, 16, torch.float16, 42)
+    side, n = torch.cuda.Stream(), 1 << 20
+    here = fg._paged_ws(None, n, S.tab, None)
+    at = here.data_ptr()
+    del here
+    for st in (side, side.cuda_stream):
+        there = fg._paged_ws(None, n, S.tab, st)
+        assert there.data_ptr() != at
+    again = fg._paged_ws(None, n, S.tab, None)
+    assert again.data_ptr() == at
+
+
 def test_python_checks(fg):
     S = Setup(fg, [30], 2, 64, 16, torch.float16, 41)
     q = torch.zeros((1, 128), dtype=torch.float16, device="cuda")
