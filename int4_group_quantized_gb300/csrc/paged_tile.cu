@@ -62,8 +62,9 @@ struct Smem {
   static constexpr int kK = kPanels * kPanel;
   static constexpr int kStage = 2 * kK;                 // K, then V
   static constexpr int kFlags = 4 * 16;                 // of a tile: whether any is set, absent keys, NaN value groups 0 and 1
-  static constexpr int kBytes = 1024 + 2 * kQ + 2 * kStage + 4 * kFlags + 256;
-  static_assert(kBytes <= 232448, "shared memory of one CTA");
+  static constexpr int kOut = 32 * 128;                 // a softmax warp's rows on their way out, 128 bytes of each
+  static constexpr int kBytes = 1024 + 2 * kQ + 2 * kStage + kSoftWarps * kOut + 4 * kFlags + 256;
+  static_assert(kBytes + sizeof(OwnPlan) + sizeof(Line) + 64 <= 232448, "shared memory of one CTA");
 };
 
 // A share's walk over its segments: parts of one unit's key tiles.
@@ -163,6 +164,10 @@ __device__ __forceinline__ void tmem_arrived(uint32_t (&r)[16]) {
                :
                : "memory");
 }
+// 16 bytes into shared memory, zeros where not `there` (then the address is not read).
+__device__ __forceinline__ void cp16_zfill(uint32_t to, const void* from, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(there ? 16u : 0u) : "memory");
+}
 // 16 consecutive columns (tmem_arrived before they are read).
 __device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
@@ -257,8 +262,9 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const AttnArgs<__half
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sQ = sm;
   uint8_t* sKV = sQ + 2 * S::kQ;
-  uint32_t* sFlags = reinterpret_cast<uint32_t*>(sKV + 2 * S::kStage);   // [tile % 4][any, absent, nan 0, nan 1][4]
-  uint64_t* bars = reinterpret_cast<uint64_t*>(sKV + 2 * S::kStage + 4 * S::kFlags);
+  uint8_t* sOut = sKV + 2 * S::kStage;
+  uint32_t* sFlags = reinterpret_cast<uint32_t*>(sOut + kSoftWarps * S::kOut);   // [tile % 4][any, absent, nan 0, nan 1][4]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sOut + kSoftWarps * S::kOut + 4 * S::kFlags);
   uint64_t* qfull = bars;         // [group] Q of the segment is in place
   uint64_t* kfull = bars + 2;     // [stage]
   uint64_t* vfull = bars + 4;
@@ -515,47 +521,118 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const AttnArgs<__half
     const int rr = 32 * quarter + lane, r = 128 * grp + rr;
     const uint32_t trow = tmem + (static_cast<uint32_t>(32 * quarter) << 16);
     const uint32_t ts = trow + 128 * grp, to = trow + kO + D * grp, tp = trow + kP + kPStep * grp;
+    // A warp brings its 32 rows of Q into shared memory a row over kPieces lanes, 16 bytes each.
+    constexpr int kPieces = D / 8, kAtOnce = 32 / kPieces;
+    const int pc = lane % kPieces, row_w = r - lane;
+    uint8_t* const qt = sQ + grp * S::kQ + 32 * quarter * 128;
+    auto piece = [&](int n) { return reinterpret_cast<uint4*>(qt + (pc >> 3) * S::kPanel + n * 128 + (((pc & 7) ^ (n & 7)) << 4)); };
+    // where the lane's row begins in rows ld apart
+    auto place = [&](int64_t ld) {
+      const int row = k.un.r0 + (r < k.un.rows ? r : 0), tok = row / a.shape.group;
+      return (k.s.row0 + tok) * ld + static_cast<int64_t>(k.h * a.shape.group + row - tok * a.shape.group) * D;
+    };
+    uint8_t* const stage = sOut + warp * S::kOut;
     bool ok = true;
     int4 rec = make_int4(-1, 0, 0, 0);
     int g0 = 0;            // the CTA's tiles before the segment
     int cnt = 0, seg = 0;  // this group's tiles and segments
-    while (k.left > 0 && ok) {
-      const int tiles = k.x1 - k.x;
-      if (grp == 1 && k.un.rows <= 128) {
-        g0 += tiles;
+    // the segment that ends: its rows, sums, and where they go
+    bool whole_item = false, from_start = false;
+    int rows = -1;         // -1: none
+    int64_t dst = 0;
+    float m = -INFINITY;
+    float2 l2 = make_float2(0.0f, 0.0f);
+    uint32_t nans = 0;
+    while (true) {
+      // A round ends one segment and works on the next.  S of the last tile is complete, so Q's place is free: the next Q is
+      // on its way while the last P V runs, and its first S runs while O is written.
+      while (k.left > 0 && grp == 1 && k.un.rows <= 128) {
+        g0 += k.x1 - k.x;
         walk_next(k, a, line);
-        continue;
       }
-      const bool from_start = k.x == 0, to_end = k.x1 == k.sp.n;
-      const bool on = r < k.un.rows;
-      const int row = k.un.r0 + (on ? r : 0), t = row / a.shape.group;
-      const int head = k.h * a.shape.group + row - t * a.shape.group;
-      const int p = k.s.len - k.s.n + t;   // the row's position
-      // Q, with every 8 dims in the order (0, 4), (1, 5), (2, 6), (3, 7)
-      {
-        const uint4* src = reinterpret_cast<const uint4*>(a.q + static_cast<int64_t>(k.s.row0 + t) * a.ldq + static_cast<int64_t>(head) * D);
-        uint8_t* qrow = sQ + grp * S::kQ + rr * 128;
+      const bool more = k.left > 0;
+      if (more) {
+        const int64_t src = place(a.ldq);
         // (loops here and below: code that runs once a segment is fetched anew each time, and straight code costs its length)
-#pragma unroll 1
-        for (int c = 0; c < D / 8; c += 4) {
-          uint4 v[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) v[e] = on ? src[c + e] : make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            *reinterpret_cast<uint4*>(qrow + (c >> 3) * S::kPanel + ((((c & 7) + e) ^ (rr & 7)) << 4)) =
-                make_uint4(__byte_perm(v[e].x, v[e].z, 0x5410), __byte_perm(v[e].x, v[e].z, 0x7632), __byte_perm(v[e].y, v[e].w, 0x5410),
-                           __byte_perm(v[e].y, v[e].w, 0x7632));
+#pragma unroll 2
+        for (int i = 0; i < 32; i += kAtOnce) {
+          const int n = i + lane / kPieces;
+          const __half* from = a.q + __shfl_sync(0xffffffffu, src, n) + 8 * pc;
+          cp16_zfill(smem_u32(piece(n)), from, row_w + n < k.un.rows);
+        }
+        cp_async_commit();
+      }
+      if (rows >= 0) {
+        ok = mbar_wait(&odone[grp], seg & 1, wait_limit, abort_flag);
+        ok = __all_sync(0xffffffffu, ok && !*abort_flag);
+        if (!ok) break;
+        ++seg;
+        tc_fence_after();
+      }
+      if (more) {   // Q has every 8 dims in the order (0, 4), (1, 5), (2, 6), (3, 7): a lane's own pieces
+        cp_async_wait<0>();
+#pragma unroll 2
+        for (int i = 0; i < 32; i += kAtOnce) {
+          uint4* q = piece(i + lane / kPieces);
+          const uint4 v = *q;
+          *q = make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632), __byte_perm(v.y, v.w, 0x5410),
+                          __byte_perm(v.y, v.w, 0x7632));
         }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&qfull[grp]);
       }
+      if (rows >= 0) {
+        // ---- the segment's rows: finished, or this share's partial ------------------------
+        const float l = l2.x + l2.y;
+        const float f = !whole_item ? 1.0f : l == 0.0f ? 0.0f : 1.0f / l;
+        const int64_t slot = (static_cast<int64_t>(w) * 2 + (from_start ? 1 : 0)) * kRows + row_w;   // of the warp's first row
+#pragma unroll 1
+        for (int c = 0; c < D / 16; ++c) {
+          uint32_t u[16];
+          tmem_ld_32x32b_x16(to + 16 * c, u);
+          tmem_arrived(u);
+          const float fc = (nans >> (c >> 2)) & 1u ? __uint_as_float(0x7fffffffu) : f;   // a NaN group's columns
+          float v[16];         // of 8 columns dims 0..7 lie at 0, 2, 4, 6, 1, 3, 5, 7
+#pragma unroll
+          for (int e = 0; e < 16; ++e) v[e] = __uint_as_float(u[(e & 8) + ((e & 7) < 4 ? 2 * (e & 7) : 2 * (e & 7) - 7)]) * fc;
+          if (whole_item) {
+            if (r >= rows) continue;   // no collective follows in the round
+            uint32_t h[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) h[e] = q4::cvt_f16x2(make_float2(v[2 * e], v[2 * e + 1]));
+            uint4* out = reinterpret_cast<uint4*>(a.out + dst + 16 * c);
+            out[0] = make_uint4(h[0], h[1], h[2], h[3]);
+            out[1] = make_uint4(h[4], h[5], h[6], h[7]);
+            continue;
+          }
+          // A partial's 32 columns go through shared memory and leave eight lanes a row: a row a lane took a line of the L1
+          // per lane and store (8500 cycles for the partial, 6500 this way).
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            *reinterpret_cast<uint4*>(stage + lane * 128 + (((4 * (c & 1) + e) ^ (lane & 7)) << 4)) =
+                make_uint4(__float_as_uint(v[4 * e]), __float_as_uint(v[4 * e + 1]), __float_as_uint(v[4 * e + 2]), __float_as_uint(v[4 * e + 3]));
+          if (!(c & 1)) continue;
+          __syncwarp();
+#pragma unroll 4
+          for (int i = 0; i < 32; i += 4) {
+            const int n = i + (lane >> 3);
+            const uint4 x = *reinterpret_cast<const uint4*>(stage + n * 128 + (((lane & 7) ^ (n & 7)) << 4));
+            if (row_w + n < rows) *reinterpret_cast<uint4*>(pl.part + (slot + n) * D + 16 * (c - 1) + 4 * (lane & 7)) = x;
+          }
+          __syncwarp();
+        }
+        if (!whole_item && r < rows) pl.stat[slot + lane] = make_float2(m, l);
+      }
+      if (!more) break;
+      const int tiles = k.x1 - k.x;
+      const bool on = r < k.un.rows;
+      const int p = k.s.len - k.s.n + (k.un.r0 + (on ? r : 0)) / a.shape.group;   // the row's position
       const int whole_hi = min(k.un.p0, k.s.keys - 1) - (kKeys - 1), sink_hi = a.shape.sinks - kKeys;
       const int whole_lo = a.shape.window > 0 ? k.un.p1 - a.shape.window + 1 : 0;
-      float m = -INFINITY;
-      float2 l2 = make_float2(0.0f, 0.0f);
-      uint32_t nans = 0;
+      m = -INFINITY;
+      l2 = make_float2(0.0f, 0.0f);
+      nans = 0;
       for (int x = 0; x < tiles; ++x, ++cnt) {
         // tcgen05.ld/st are warp-collective: every branch around them is taken by the whole warp
         ok = mbar_wait(&sfull[grp], cnt & 1, wait_limit, abort_flag);
@@ -671,45 +748,15 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const AttnArgs<__half
         if (lane == 0) mbar_arrive(&pfull[grp]);
       }
       if (!ok) break;
-      ok = mbar_wait(&odone[grp], seg & 1, wait_limit, abort_flag);
-      ok = __all_sync(0xffffffffu, ok && !*abort_flag);
-      if (!ok) break;
-      tc_fence_after();
-      // ---- the segment's rows: finished, or this share's partial ------------------------
-      const bool whole = from_start && to_end;
-      const float l = l2.x + l2.y;
-      const float f = !whole ? 1.0f : l == 0.0f ? 0.0f : 1.0f / l;
-      const int64_t slot = (static_cast<int64_t>(w) * 2 + (from_start ? 1 : 0)) * kRows + r;
-      __half* dst = a.out + static_cast<int64_t>(k.s.row0 + t) * a.ldo + static_cast<int64_t>(head) * D;
-#pragma unroll 1
-      for (int c = 0; c < D / 16; ++c) {
-        uint32_t u[16];
-        tmem_ld_32x32b_x16(to + 16 * c, u);
-        tmem_arrived(u);
-        if (!on) continue;   // no collective follows in the round
-        const float fc = (nans >> (c >> 2)) & 1u ? __uint_as_float(0x7fffffffu) : f;   // a NaN group's columns
-        float v[16];         // of 8 columns dims 0..7 lie at 0, 2, 4, 6, 1, 3, 5, 7
-#pragma unroll
-        for (int e = 0; e < 16; ++e) v[e] = __uint_as_float(u[(e & 8) + ((e & 7) < 4 ? 2 * (e & 7) : 2 * (e & 7) - 7)]) * fc;
-        if (whole) {
-          uint32_t h[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) h[e] = q4::cvt_f16x2(make_float2(v[2 * e], v[2 * e + 1]));
-          *reinterpret_cast<uint4*>(dst + 16 * c) = make_uint4(h[0], h[1], h[2], h[3]);
-          *reinterpret_cast<uint4*>(dst + 16 * c + 8) = make_uint4(h[4], h[5], h[6], h[7]);
-        } else {
-          float4* part = reinterpret_cast<float4*>(pl.part + slot * D + 16 * c);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) part[e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
-        }
-      }
-      if (!whole && on) pl.stat[slot] = make_float2(m, l);
-      if (from_start && !to_end) {
+      from_start = k.x == 0;
+      whole_item = from_start && k.x1 == k.sp.n;
+      rows = k.un.rows;
+      dst = place(a.ldo);
+      if (from_start && !whole_item) {
         // the item's first tile in the line: the share's first tiles, then those of the segments before it
         const int64_t per = line.per, start = w * per + g0;
         rec = make_int4(k.i, k.h, k.u, static_cast<int>((start + k.sp.n - 1) / per));
       }
-      ++seg;
       g0 += tiles;
       walk_next(k, a, line);
     }
