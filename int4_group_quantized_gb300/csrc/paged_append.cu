@@ -5,6 +5,7 @@
 #include "codec_dev.cuh"
 #include "paged.cuh"
 #include "q4_dev.cuh"
+#include "tc_ptx.cuh"
 
 namespace fg {
 namespace paged {
@@ -30,6 +31,11 @@ __device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
   *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
 }
 
+// 16 bytes into shared memory, zeros where not `there` (then the address is not read).
+__device__ __forceinline__ void cp16_zfill(uint32_t to, const void* from, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(there ? 16u : 0u) : "memory");
+}
+
 template <typename T>
 struct AppendArgs {
   Pool pool;
@@ -48,8 +54,6 @@ struct AppendArgs {
 // is the negated minimum of the negated values, so both travel in one word.
 struct Half8 {
   uint4 raw;
-  __device__ __forceinline__ void load(const __half* p) { raw = *reinterpret_cast<const uint4*>(p); }
-  __device__ __forceinline__ void clear() { raw = make_uint4(0u, 0u, 0u, 0u); }
   __device__ __forceinline__ float get(int e) const {
     const uint32_t w = (e >> 1) == 0 ? raw.x : (e >> 1) == 1 ? raw.y : (e >> 1) == 2 ? raw.z : raw.w;
     const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
@@ -173,21 +177,35 @@ __device__ __noinline__ uint32_t exact_word(X x, float mn, float r) {
 
 // A warp takes a run of rows (8 batches of 4 groups: 16 rows of two groups a
 // head, 32 rows of one) and some of the 2 * heads (K or V, head) slices.  The
-// run's slots are found once; a slice's rows are loaded together; after the
-// batches' minima and maxima every lane holds one of the 32 groups and takes
-// its two divisions (the literal form spent two per lane and batch); then the
-// batches are coded with their group's numbers from that lane.
+// run's slots are found once; after the batches' minima and maxima every lane
+// holds one of the 32 groups and takes its two divisions (the literal form
+// spent two per lane and batch); then the batches are coded with their group's
+// numbers from that lane.  The bytes are the floor (fp16: 2 read, 0.625 written
+// and 2 more where the restored rows are wanted); half the instructions that
+// could issue do.  fp16 rows therefore come by asynchronous copies a slice
+// ahead, 4 KB a warp and slice: 24 thousand rows of 32 heads of 128 with
+// restored rows 162.7 us (4.5 TB/s) where loads into registers took 178; two
+// slices ahead 161.6, three blocks an SM (80 registers, spills) 196.
 template <int NG>
 constexpr int kRun = 32 / NG;
 constexpr int kBatches = 8;
 
+constexpr int kAppendWarps = 8;
+template <typename T>
+constexpr bool kRing = sizeof(T) == 2;
+template <typename T>
+constexpr int kRingBytes = kRing<T> ? kAppendWarps * 2 * kBatches * 32 * 16 : 0;
+
 template <typename T, int NG>
-__global__ void __launch_bounds__(256, 2) append_kernel(const AppendArgs<T> a, int slices) {
+__global__ void __launch_bounds__(32 * kAppendWarps, 2) append_kernel(const AppendArgs<T> a, int slices) {
   constexpr int D = 64 * NG;
   constexpr uint32_t kNone = 0xffffffffu;
   const int lane = threadIdx.x & 31;
   const int part = lane & 7, gi = (lane >> 3) % NG, rb = (lane >> 3) / NG;   // row of a batch
   const int heads = a.pool.heads, psl = a.pool.ps_log2;
+  extern __shared__ __align__(16) uint8_t ring_mem[];
+  uint4* const ring = reinterpret_cast<uint4*>(ring_mem) + (threadIdx.x >> 5) * (2 * kBatches * 32) + lane;
+  using X = typename Vec8<T>::type;
   const int64_t runs = (a.batch.ntok + kRun<NG> - 1) / kRun<NG>;
   const int chunks = (2 * heads + slices - 1) / slices;
   const int64_t warp = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
@@ -220,24 +238,45 @@ __global__ void __launch_bounds__(256, 2) append_kernel(const AppendArgs<T> a, i
 #pragma unroll
     for (int b = 0; b < kBatches; ++b) tok[b] = __shfl_sync(0xffffffffu, token, b * (4 / NG) + rb);
     const uint32_t mine = __shfl_sync(0xffffffffu, token, part * (4 / NG) + rb);
+    auto source = [&](int sl) {   // the lane's values of the run's first row
+      return (sl >= heads ? a.src[1] : a.src[0]) + row0 * a.ld + (sl >= heads ? sl - heads : sl) * D + gi * 64 + part * 8;
+    };
+    auto fetch = [&](int sl) {
+      if (sl < s1) {
+        const T* src = source(sl);
+#pragma unroll
+        for (int b = 0; b < kBatches; ++b)
+          cp16_zfill(tc::smem_u32(ring + ((sl & 1) * kBatches + b) * 32), tok[b] != kNone ? src + (b * (4 / NG) + rb) * a.ld : src, tok[b] != kNone);
+      }
+      tc::cp_async_commit();
+    };
+    if constexpr (kRing<T>) fetch(s0);
     for (int sl = s0; sl < s1; ++sl) {
       const bool value = sl >= heads;
       const int h = value ? sl - heads : sl;
       const int col = h * D + gi * 64 + part * 8;
-      const T* src = (value ? a.src[1] : a.src[0]) + row0 * a.ld + col;
-      typename Vec8<T>::type x[kBatches];
+      X held[kRing<T> ? 1 : kBatches];
+      if constexpr (kRing<T>) {
+        fetch(sl + 1);
+        tc::cp_async_wait<1>();   // a lane reads what it copied itself
+      } else {
+        const T* src = source(sl);
 #pragma unroll
-      for (int b = 0; b < kBatches; ++b) {
-        const int t = b * (4 / NG) + rb;
-        if (tok[b] != kNone) x[b].load(src + t * a.ld);
-        else x[b].clear();
+        for (int b = 0; b < kBatches; ++b) {
+          if (tok[b] != kNone) held[b].load(src + (b * (4 / NG) + rb) * a.ld);
+          else held[b].clear();
+        }
       }
+      auto batch = [&](int b) {
+        if constexpr (kRing<T>) return X{ring[((sl & 1) * kBatches + b) * 32]};
+        else return held[b];
+      };
       // lane 8 g + b keeps group g of batch b
       float mn = 0.0f, mx = 0.0f;
 #pragma unroll
       for (int b = 0; b < kBatches; ++b) {
         float lo, hi;
-        x[b].bounds(lo, hi);
+        batch(b).bounds(lo, hi);
         if (part == b) {
           mn = lo;
           mx = hi;
@@ -258,13 +297,14 @@ __global__ void __launch_bounds__(256, 2) append_kernel(const AppendArgs<T> a, i
       for (int b = 0; b < kBatches; ++b) {
         const int from = (lane & 24) + b, t = b * (4 / NG) + rb;
         const float bmn = __shfl_sync(0xffffffffu, mn, from), bc = __shfl_sync(0xffffffffu, c15, from);
+        const X x = batch(b);
         float2 v[4], q[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = make_float2(x[b].get(e), x[b].get(e + 4));
+        for (int e = 0; e < 4; ++e) v[e] = make_float2(x.get(e), x.get(e + 4));
         const bool stands = codes_fast(v, bmn, bc, q);
         if (__any_sync(0xffffffffu, !stands)) {   // rare
           const float br = __shfl_sync(0xffffffffu, r, from);
-          const uint32_t word = exact_word(x[b], bmn, br);
+          const uint32_t word = exact_word(x, bmn, br);
           if (!stands)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
@@ -288,6 +328,20 @@ __global__ void __launch_bounds__(256, 2) append_kernel(const AppendArgs<T> a, i
   }
 }
 
+template <typename T, int NG>
+fg_status launch_run(const AppendArgs<T>& a, int slices, unsigned grid, cudaStream_t st) {
+  static bool set[64] = {false};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (kRingBytes<T> > 48 * 1024 && dev >= 0 && dev < 64 && !set[dev]) {
+    if (cudaFuncSetAttribute(append_kernel<T, NG>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes<T>) != cudaSuccess)
+      return check_launch("append_kernel smem attribute");
+    set[dev] = true;
+  }
+  append_kernel<T, NG><<<grid, 32 * kAppendWarps, kRingBytes<T>, st>>>(a, slices);
+  return check_launch("append_kernel");
+}
+
 template <typename T>
 fg_status launch_append(const fg_page_pool& pool, const fg_page_table& t, const int32_t* cu, const void* k,
                         const void* v, int64_t ld, int64_t ntok, void* kr, void* vr, int64_t ldr, unsigned int* err,
@@ -302,7 +356,8 @@ fg_status launch_append(const fg_page_pool& pool, const fg_page_table& t, const 
   a.restored[1] = static_cast<T*>(vr);
   a.ld = ld;
   a.ldr = ldr;
-  // as many slices a warp as leave every SM its 16 warps, so that a run's slots are looked up no oftener than need be
+  // as many slices a warp as leave every SM its 16 warps, so that a run's slots are looked up no oftener than need be; at
+  // most 8 (4 to 8: 162 us for the rows above; 10, whose last warps run alone: 177; 16: 208)
   const int run = pool.head_dim == 128 ? kRun<2> : kRun<1>;
   const int64_t runs = (ntok + run - 1) / run, warps = static_cast<int64_t>(num_sms()) * 16;
   const int64_t fit = runs * 2 * pool.heads / warps;
@@ -311,9 +366,8 @@ fg_status launch_append(const fg_page_pool& pool, const fg_page_table& t, const 
   const int64_t want = (items + 7) / 8, cap = static_cast<int64_t>(num_sms()) * 16;
   const unsigned grid = static_cast<unsigned>(want < cap ? want : cap);
   Trace tr(KC_KV_STORE, st);
-  if (pool.head_dim == 128) append_kernel<T, 2><<<grid, 256, 0, st>>>(a, slices);
-  else append_kernel<T, 1><<<grid, 256, 0, st>>>(a, slices);
-  return check_launch("append_kernel");
+  if (pool.head_dim == 128) return launch_run<T, 2>(a, slices, grid, st);
+  return launch_run<T, 1>(a, slices, grid, st);
 }
 
 }  // namespace
