@@ -367,8 +367,9 @@ fg_status launch_attn(const fg_page_pool& pool, const fg_page_table& t, const in
     FG_TRY(check_launch("plan_kernel"));
   }
   if constexpr (half) {
-    if (l.step.workers > 0) FG_TRY(paged_attention_step(a, l.step, pool.head_dim, own_plan, st));
+    // the chunks first: the steps' small CTAs then fill the SMs as the chunks' shares end
     if (l.tile.workers > 0) FG_TRY(paged_attention_tile(a, l.tile, pool.head_dim, own_plan, l.step.workers == 0, st));
+    if (l.step.workers > 0) FG_TRY(paged_attention_step(a, l.step, pool.head_dim, own_plan, l.tile.workers > 0, st));
     return wide ? join<T, 128, kTileRows>(a, l.step, l.tile, st) : join<T, 64, kTileRows>(a, l.step, l.tile, st);
   } else {
     FG_TRY(paged_attention_f32(a, l.tile, pool.head_dim, own_plan, st));

@@ -23,14 +23,13 @@ struct AttnArgs {
 // own_plan: no plan was made (paged_sched.cuh, make_line).
 // Sequences of at most kStepRows rows per K/V head (fp16).
 int step_workers(int rows, int sms);
-fg_status paged_attention_step(const AttnArgs<__half>& a, const ClassPlan& pl, int head_dim, bool own_plan, cudaStream_t st);
-
+// `after`: launched after the chunks' kernel.
+fg_status paged_attention_step(const AttnArgs<__half>& a, const ClassPlan& pl, int head_dim, bool own_plan, bool after, cudaStream_t st);
 
 // Longer chunks (fp16) on tcgen05, units of kTileRows rows and tiles of 128 keys; one worker an SM.
 constexpr int kTileRows = 256;
 // `every`: the call has no step class.
 fg_status paged_attention_tile(const AttnArgs<__half>& a, const ClassPlan& pl, int head_dim, bool own_plan, bool every, cudaStream_t st);
-
 
 // fp32 activations, every sequence: units of kF32Rows rows, tiles of 64 keys.
 constexpr int kF32Rows = 16, kF32KeysLog2 = 6;

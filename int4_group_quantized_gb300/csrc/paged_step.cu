@@ -180,7 +180,7 @@ __device__ __forceinline__ void read_meta(const uint8_t* arr, int t, float (&v)[
 }
 
 template <int D, int NB>
-__global__ void __launch_bounds__(32 * kWarps, kCtasPerSm<NB>) step_kernel(const AttnArgs<__half> a, const ClassPlan pl, const bool own_plan) {
+__global__ void __launch_bounds__(32 * kWarps, kCtasPerSm<NB>) step_kernel(const AttnArgs<__half> a, const ClassPlan pl, const bool own_plan, const bool after) {
   constexpr int NG = D / 64, NT = D / 16;
   using St = Stage<D>;
   constexpr int kStages = kStepStages<D, NB>;
@@ -191,7 +191,10 @@ __global__ void __launch_bounds__(32 * kWarps, kCtasPerSm<NB>) step_kernel(const
   const int w = blockIdx.x * kWarps + warp;
 
   tc::griddep_launch();
-  tc::griddep_wait();
+  // After the chunks' kernel with a plan of its own nothing of that kernel is needed here: the CTAs fill the SMs that it
+  // leaves, and the wait is left to the end (so that what follows this kernel follows that one too).
+  const bool late = own_plan && after;
+  if (!late) tc::griddep_wait();
   __shared__ OwnPlan own;
   const Line line = own_plan ? make_line<true, kStepRows, kTileLog2>(own, a.tab, a.batch, a.shape, a.pool.heads, pl.workers, false)
                              : Line{pl.pre, pl.head[0], pl.head[1]};
@@ -200,6 +203,7 @@ __global__ void __launch_bounds__(32 * kWarps, kCtasPerSm<NB>) step_kernel(const
   const int64_t o0 = w * per;
   if (o0 >= total) {
     if (lane == 0) pl.rec[w] = make_int4(-1, 0, 0, 0);
+    if (late) tc::griddep_wait();
     return;
   }
   const int heads = a.pool.heads;
@@ -718,6 +722,7 @@ __global__ void __launch_bounds__(32 * kWarps, kCtasPerSm<NB>) step_kernel(const
     if (info.y & kEnd) break;
   }
   if (lane == 0) pl.rec[w] = rec;
+  if (late) tc::griddep_wait();
 }
 
 template <int D, int NB>
@@ -726,7 +731,7 @@ constexpr int step_smem() {
 }
 
 template <int D, int NB>
-fg_status launch(const AttnArgs<__half>& a, const ClassPlan& pl, bool own_plan, cudaStream_t st) {
+fg_status launch(const AttnArgs<__half>& a, const ClassPlan& pl, bool own_plan, bool after, cudaStream_t st) {
   constexpr int bytes = step_smem<D, NB>();
   static bool set[64] = {false};
   int dev = 0;
@@ -746,8 +751,8 @@ fg_status launch(const AttnArgs<__half>& a, const ClassPlan& pl, bool own_plan, 
   cfg.dynamicSmemBytes = bytes;
   cfg.stream = st;
   cfg.attrs = pdl;
-  cfg.numAttrs = own_plan ? 0 : 1;   // with a plan of its own the call's first launch: it waits for all that ran before
-  if (cudaLaunchKernelEx(&cfg, step_kernel<D, NB>, a, pl, own_plan) != cudaSuccess) return check_launch("step_kernel (launch)");
+  cfg.numAttrs = own_plan && !after ? 0 : 1;   // then the call's first launch: it waits for all that ran before
+  if (cudaLaunchKernelEx(&cfg, step_kernel<D, NB>, a, pl, own_plan, after) != cudaSuccess) return check_launch("step_kernel (launch)");
   return check_launch("step_kernel");
 }
 
@@ -755,9 +760,9 @@ fg_status launch(const AttnArgs<__half>& a, const ClassPlan& pl, bool own_plan, 
 
 int step_workers(int rows, int sms) { return sms * (rows <= 8 ? kCtasPerSm<1> : kCtasPerSm<2>) * kWarps; }
 
-fg_status paged_attention_step(const AttnArgs<__half>& a, const ClassPlan& pl, int head_dim, bool own_plan, cudaStream_t st) {
-  if (head_dim == 128) return pl.rows <= 8 ? launch<128, 1>(a, pl, own_plan, st) : launch<128, 2>(a, pl, own_plan, st);
-  return pl.rows <= 8 ? launch<64, 1>(a, pl, own_plan, st) : launch<64, 2>(a, pl, own_plan, st);
+fg_status paged_attention_step(const AttnArgs<__half>& a, const ClassPlan& pl, int head_dim, bool own_plan, bool after, cudaStream_t st) {
+  if (head_dim == 128) return pl.rows <= 8 ? launch<128, 1>(a, pl, own_plan, after, st) : launch<128, 2>(a, pl, own_plan, after, st);
+  return pl.rows <= 8 ? launch<64, 1>(a, pl, own_plan, after, st) : launch<64, 2>(a, pl, own_plan, after, st);
 }
 
 }  // namespace paged

@@ -301,10 +301,8 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const AttnArgs<__half
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   griddep_launch();
-  // With a plan of its own the kernel follows the step kernel, which began when all before the call was complete: nothing
-  // of it is needed here, and the wait is left to the end (so that what follows this kernel follows that one too).
+  griddep_wait();
   __shared__ OwnPlan own;
-  if (!own_plan) griddep_wait();
   __shared__ Line line;   // not in registers: it is read between segments only
   {
     const Line x = own_plan ? make_line<false, kRows, kKeysLog2>(own, a.tab, a.batch, a.shape, a.pool.heads, pl.workers, every)
@@ -773,7 +771,6 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const AttnArgs<__half
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
   }
-  if (own_plan) griddep_wait();
 }
 
 template <int D>
@@ -797,7 +794,7 @@ fg_status launch(const AttnArgs<__half>& a, const ClassPlan& pl, bool own_plan, 
   cfg.dynamicSmemBytes = S::kBytes;
   cfg.stream = st;
   cfg.attrs = pdl;
-  cfg.numAttrs = own_plan && every ? 0 : 1;   // then the call's first launch: it waits for all that ran before
+  cfg.numAttrs = own_plan ? 0 : 1;   // with a plan of its own the call's first launch: it waits for all that ran before
   if (cudaLaunchKernelEx(&cfg, tile_kernel<D>, a, pl, wait_limit(), own_plan, every) != cudaSuccess) return check_launch("tile_kernel (launch)");
   return check_launch("tile_kernel");
 }
