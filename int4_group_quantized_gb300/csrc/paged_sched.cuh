@@ -139,8 +139,8 @@ __device__ __forceinline__ Line make_line(OwnPlan& o, const Table& t, const Batc
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
   if (threadIdx.x == 0) o.longest = 0;
   __syncthreads();
-  for (int i0 = 32 * warp; i0 < t.seqs; i0 += 32 * nw) {   // a lane a sequence
-    const int i = i0 + lane;
+  for (int i0 = warp; i0 < t.seqs; i0 += 32 * nw) {   // a lane a sequence, the warps in turn (a warp counts its chunks one by one)
+    const int i = i0 + nw * lane;
     Seq s{0, 0, 0, 0};
     if (i < t.seqs) {
       s = seq_of(t, b, i);

@@ -100,15 +100,31 @@ __device__ __forceinline__ void walk_begin(Walk& k, const AttnArgs<__half>& a, c
   k.i = lo;
   k.left = static_cast<int>(total - o0 < per ? total - o0 : per);
   walk_seq(k, a);
-  const int64_t cost = (pl.pre[lo + 1] - pl.pre[lo]) / a.pool.heads, in = o0 - pl.pre[lo];
-  k.h = static_cast<int>(in / cost);
+  const int64_t all = pl.pre[lo + 1] - pl.pre[lo], in = o0 - pl.pre[lo];   // (32-bit divisions where they do: the short ones)
+  const int64_t cost = all <= INT32_MAX ? static_cast<int>(all) / a.pool.heads : all / a.pool.heads;
+  k.h = all <= INT32_MAX ? static_cast<int>(in) / static_cast<int>(cost) : static_cast<int>(in / cost);
   int64_t rest = in - k.h * cost;
-  walk_unit(k, a);
-  while (rest >= k.sp.n) {
-    rest -= k.sp.n;
-    ++k.u;
-    walk_unit(k, a);
+  const int lane = threadIdx.x & 31;
+  for (;; k.u += 32) {   // a unit a lane
+    const Unit un = unit_of<kRows>(k.s, a.shape.group, min(k.u + lane, k.units - 1));
+    const int n = k.u + lane < k.units ? span_of<kKeysLog2>(un.p0, un.p1, k.s.keys, a.shape.window, a.shape.sinks).n : 0;
+    int64_t inc = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t up = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += up;
+    }
+    const uint32_t past = __ballot_sync(0xffffffffu, rest < inc);
+    if (past) {
+      const int at = __ffs(past) - 1;
+      k.u += at;
+      rest -= __shfl_sync(0xffffffffu, inc - n, at);
+      break;
+    }
+    rest -= __shfl_sync(0xffffffffu, inc, 31);
+    if (k.u + 32 >= k.units) break;   // not reached: the share begins inside the item
   }
+  walk_unit(k, a);
   k.x = static_cast<int>(rest);
   k.x1 = k.x + (k.left < k.sp.n - k.x ? k.left : k.sp.n - k.x);
 }
