@@ -79,8 +79,9 @@ __global__ void __launch_bounds__(kThreads) f32_kernel(const AttnArgs<float> a, 
     i = lo;
     left = static_cast<int>(total - o0 < per ? total - o0 : per);
     enter_seq();
-    const int64_t cost = (line.pre[lo + 1] - line.pre[lo]) / a.pool.heads, in = o0 - line.pre[lo];
-    h = static_cast<int>(in / cost);
+    const int64_t all = line.pre[lo + 1] - line.pre[lo], in = o0 - line.pre[lo];   // (32-bit divisions where they do: the short ones)
+    const int64_t cost = all <= INT32_MAX ? static_cast<int>(all) / a.pool.heads : all / a.pool.heads;
+    h = all <= INT32_MAX ? static_cast<int>(in) / static_cast<int>(cost) : static_cast<int>(in / cost);
     int64_t rest = in - h * cost;
     enter_unit();
     while (rest >= sp.n) {
@@ -168,6 +169,7 @@ __global__ void __launch_bounds__(kThreads) f32_kernel(const AttnArgs<float> a, 
     const int x0 = x;
     const bool from_start = x0 == 0, to_end = x1 == sp.n;
     // Q of the unit's rows; a thread's two rows
+    load(x);           // on its way under Q
     __syncthreads();   // the rows before are done with
     for (int e = tid; e < kRows * D / 4; e += kThreads) {
       const int r = e / (D / 4), c = e % (D / 4), row = un.r0 + (r < un.rows ? r : 0), t = row / a.shape.group;
@@ -184,7 +186,6 @@ __global__ void __launch_bounds__(kThreads) f32_kernel(const AttnArgs<float> a, 
 #pragma unroll
       for (int c = 0; c < CW; ++c) o[r][c] = 0.0f;
     }
-    load(x);
     for (; x < x1; ++x) {
       const int t0 = sp.tile(x) << kKeysLog2;
       restore();
