@@ -10,6 +10,9 @@
 // the rows it reads lie four banks apart), the running maximum and sum over the
 // half warp, the weights through shared memory, and 2 x D/16 outputs a thread.
 // Bound by the FMAs' operands: ten shared-memory wavefronts for 32 FMAs a warp.
+// 3 sequences of 300 to 777 tokens, 5 to 67 rows, 12 heads of 64: 23.9 us by
+// graph replay, two tiles a CTA of 8 to 10 thousand cycles each; the rest is
+// launch, plan and the first loads (9000 cycles) and the join.
 #include <math.h>
 
 #include "paged_attn.cuh"

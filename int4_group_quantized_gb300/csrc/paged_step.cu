@@ -32,6 +32,16 @@
 // row m of an MMA is token s(m) = m/2 + 4 (m%2), which makes the transposed
 // weights' token pairs (tig, tig + 4), and 16-byte pieces are swizzled by the
 // row.
+//
+// Measured, a call replayed from a graph (plan in the kernel, join after it):
+// 64 sequences of 300 to 900 tokens, 32 heads of 128, one row each 54 us (3.6
+// TB/s); 8 sequences of 30 to 65 thousand tokens, 8 K/V heads of 128 with 8
+// query heads each 107 us (4.7 TB/s; the copies alone, without the sums, 95);
+// 4 sequences of 100 to 300 tokens, 12 heads of 64 10.7 us, of which the two
+// launches are most.  What bounds a long step: bytes in flight first (12 warps
+// of three stages an SM: 63% of the DRAM's rate), then the integer pipe that
+// masks the nibbles (46%); four warps of three CTAs and three stages were the
+// best of what fits (8 warps x 5 stages 120 us, 11 x 4 122).
 #include <math.h>
 
 #include <algorithm>
@@ -191,10 +201,10 @@ __global__ void __launch_bounds__(32 * kWarps, kCtasPerSm<NB>) step_kernel(const
   const int w = blockIdx.x * kWarps + warp;
 
   tc::griddep_launch();
-  // After the chunks' kernel with a plan of its own nothing of that kernel is needed here: the CTAs fill the SMs that it
-  // leaves, and the wait is left to the end (so that what follows this kernel follows that one too).
-  const bool late = own_plan && after;
-  if (!late) tc::griddep_wait();
+  // After the chunks' kernel, which lets this one begin when all before it is complete, nothing of that kernel is needed
+  // here: the CTAs fill the SMs that it leaves, and the wait is left to the end (so that what follows this kernel follows
+  // that one too).
+  if (!after) tc::griddep_wait();
   __shared__ OwnPlan own;
   const Line line = own_plan ? make_line<true, kStepRows, kTileLog2>(own, a.tab, a.batch, a.shape, a.pool.heads, pl.workers, false)
                              : Line{pl.pre, pl.head[0], pl.head[1]};
@@ -203,7 +213,7 @@ __global__ void __launch_bounds__(32 * kWarps, kCtasPerSm<NB>) step_kernel(const
   const int64_t o0 = w * per;
   if (o0 >= total) {
     if (lane == 0) pl.rec[w] = make_int4(-1, 0, 0, 0);
-    if (late) tc::griddep_wait();
+    if (after) tc::griddep_wait();
     return;
   }
   const int heads = a.pool.heads;
@@ -722,7 +732,7 @@ __global__ void __launch_bounds__(32 * kWarps, kCtasPerSm<NB>) step_kernel(const
     if (info.y & kEnd) break;
   }
   if (lane == 0) pl.rec[w] = rec;
-  if (late) tc::griddep_wait();
+  if (after) tc::griddep_wait();
 }
 
 template <int D, int NB>

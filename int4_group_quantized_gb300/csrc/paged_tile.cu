@@ -31,6 +31,17 @@
 // as zeros and is remembered for the rows that see it (0 * NaN would reach all).
 // Every wait is bounded; on timeout the CTA raises the device error word, lets
 // its MMAs finish and frees its tensor memory.
+//
+// Measured: a chunk of 2048 rows over 16384 tokens, 32 heads of 128, 451 to 458
+// us (1.13 PFLOP/s, 59% of what a large bf16 library product reaches); a mixed
+// batch of 12 sequences (1 to 600 rows, 32 query heads on 8, a window of 1000
+// with 4 sinks) 115 to 119 us; 64 chunks of 20 rows over 300 to 600 tokens, 8
+// heads, 64 us.  A tile takes 3400 cycles where its four MMA batches take 2200:
+// the protocol with its MMAs alone, no softmax and no restoring, takes 362 us
+// of the chunk's 458.  A segment costs 10000 cycles more (walk, Q, first S,
+// first softmax, O), a launch 25000 before its first P V.  Other splits when a
+// tile took a quarter longer: 24 softmax and restoring warps of 80 registers
+// 715 us against 588, two issuing warps 562 against 470.
 #include <math.h>
 
 #include <algorithm>
@@ -316,8 +327,8 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const AttnArgs<__half
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  griddep_launch();
   griddep_wait();
+  griddep_launch();   // not before: the steps' kernel begins with the plan and all before it complete
   __shared__ OwnPlan own;
   __shared__ Line line;   // not in registers: it is read between segments only
   {
@@ -620,8 +631,9 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const AttnArgs<__half
             out[1] = make_uint4(h[4], h[5], h[6], h[7]);
             continue;
           }
-          // A partial's 32 columns go through shared memory and leave eight lanes a row: a row a lane took a line of the L1
-          // per lane and store (8500 cycles for the partial, 6500 this way).
+          // A partial's 32 columns go through shared memory and leave eight lanes a row: a row a lane takes a line of the L1
+          // per lane and store (8500 cycles for the partial, 6500 to 7900 this way; whole rows, half the bytes and no
+          // second pass, are faster straight out).
 #pragma unroll
           for (int e = 0; e < 4; ++e)
             *reinterpret_cast<uint4*>(stage + lane * 128 + (((4 * (c & 1) + e) ^ (lane & 7)) << 4)) =

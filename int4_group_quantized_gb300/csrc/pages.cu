@@ -414,7 +414,10 @@ __device__ __forceinline__ void move_entries(const CopyArgs& a, int moves) {
 
 // Pieces of at most 16 KB of (move, layer, array), dealt over the CTAs; a
 // thread holds four units of a piece at once.  A source is never a
-// destination, so the order does not matter.
+// destination, so the order does not matter.  Bound by the memory: 48 forks
+// with a partly filled page in 8 layers (236 MB) 41 us by graph replay with
+// their plan and the growth after it (5.8 TB/s), a compaction of 415 MB 72 us
+// with the frees before it (5.8 TB/s); one unit in flight took 46 and 85.
 __global__ void __launch_bounds__(256) copy_pages_kernel(const __grid_constant__ CopyArgs a) {
   tc::griddep_launch();
   tc::griddep_wait();
