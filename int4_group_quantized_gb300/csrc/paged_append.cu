@@ -204,6 +204,7 @@ __global__ void __launch_bounds__(32 * kAppendWarps, 2) append_kernel(const Appe
   const int part = lane & 7, gi = (lane >> 3) % NG, rb = (lane >> 3) / NG;   // row of a batch
   const int heads = a.pool.heads, psl = a.pool.ps_log2;
   extern __shared__ __align__(16) uint8_t ring_mem[];
+  tc::griddep_wait();
   uint4* const ring = reinterpret_cast<uint4*>(ring_mem) + (threadIdx.x >> 5) * (2 * kBatches * 32) + lane;
   using X = typename Vec8<T>::type;
   const int64_t runs = (a.batch.ntok + kRun<NG> - 1) / kRun<NG>;
@@ -338,8 +339,7 @@ fg_status launch_run(const AppendArgs<T>& a, int slices, unsigned grid, cudaStre
       return check_launch("append_kernel smem attribute");
     set[dev] = true;
   }
-  append_kernel<T, NG><<<grid, 32 * kAppendWarps, kRingBytes<T>, st>>>(a, slices);
-  return check_launch("append_kernel");
+  return paged::launch("append_kernel", true, append_kernel<T, NG>, grid, 32 * kAppendWarps, kRingBytes<T>, st, a, slices);
 }
 
 template <typename T>

@@ -44,6 +44,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
   __shared__ int64_t warp_sum[2][32];
   __shared__ int warp_max[2][32];
   tc::griddep_launch();
+  tc::griddep_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int nwarps = blockDim.x >> 5;
   const int seqs = a.tab.seqs, per = (seqs + nwarps - 1) / nwarps;
@@ -286,18 +287,9 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const AttnArgs<T>
 
 template <typename T, int D, int RU>
 fg_status join(const AttnArgs<T>& a, const ClassPlan& step, const ClassPlan& tile, cudaStream_t st) {
-  cudaLaunchAttribute pdl[1];
-  pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  pdl[0].val.programmaticStreamSerializationAllowed = 1;
   Trace tr(KC_ATTN_COMBINE, st);
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(step.workers + tile.workers * (RU / kJoinRows)));
-  cfg.blockDim = dim3(32 * kJoinWarps);
-  cfg.stream = st;
-  cfg.attrs = pdl;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, join_kernel<T, D, RU>, a, step, tile) != cudaSuccess) return check_launch("join_kernel (launch)");
-  return check_launch("join_kernel");
+  return paged::launch("join_kernel", true, join_kernel<T, D, RU>, static_cast<unsigned>(step.workers + tile.workers * (RU / kJoinRows)),
+                      32 * kJoinWarps, 0, st, a, step, tile);
 }
 
 // ---- workspace ------------------------------------------------------------------------
@@ -374,9 +366,7 @@ fg_status launch_attn(const fg_page_pool& pool, const fg_page_table& t, const in
     // for steps alone a lane a sequence (129: 33.1 us, 34.5 with all)
     const unsigned lanes = static_cast<unsigned>(std::min<int64_t>(kPlanThreads, (t.seqs + 31) / 32 * 32));
     const unsigned threads = l.tile.workers > 0 ? kPlanThreads : lanes;
-    if (half) plan_kernel<kTileRows, 7><<<1, threads, 0, st>>>(p);
-    else plan_kernel<kF32Rows, kF32KeysLog2><<<1, threads, 0, st>>>(p);
-    FG_TRY(check_launch("plan_kernel"));
+    FG_TRY(paged::launch("plan_kernel", true, half ? plan_kernel<kTileRows, 7> : plan_kernel<kF32Rows, kF32KeysLog2>, 1, threads, 0, st, p));
   }
   if constexpr (half) {
     // the chunks first: the steps' small CTAs then fill the SMs as the chunks' shares end

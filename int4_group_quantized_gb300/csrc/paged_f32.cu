@@ -329,19 +329,8 @@ fg_status launch(const AttnArgs<float>& a, const ClassPlan& pl, bool own_plan, c
       return check_launch("f32_kernel smem attribute");
     set[dev] = true;
   }
-  cudaLaunchAttribute pdl[1];
-  pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  pdl[0].val.programmaticStreamSerializationAllowed = 1;
   Trace tr(KC_ATTN_PAGED, st);
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(pl.workers));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = bytes;
-  cfg.stream = st;
-  cfg.attrs = pdl;
-  cfg.numAttrs = own_plan ? 0 : 1;   // with a plan of its own the call's first launch: it waits for all that ran before
-  if (cudaLaunchKernelEx(&cfg, f32_kernel<D>, a, pl, own_plan) != cudaSuccess) return check_launch("f32_kernel (launch)");
-  return check_launch("f32_kernel");
+  return paged::launch("f32_kernel", true, f32_kernel<D>, static_cast<unsigned>(pl.workers), kThreads, bytes, st, a, pl, own_plan);
 }
 
 }  // namespace

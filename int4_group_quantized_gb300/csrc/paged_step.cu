@@ -751,19 +751,8 @@ fg_status launch(const AttnArgs<__half>& a, const ClassPlan& pl, bool own_plan, 
       return check_launch("step_kernel smem attribute");
     set[dev] = true;
   }
-  cudaLaunchAttribute pdl[1];
-  pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  pdl[0].val.programmaticStreamSerializationAllowed = 1;
   Trace tr(KC_ATTN_PAGED, st);
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(pl.workers / kWarps));
-  cfg.blockDim = dim3(32 * kWarps);
-  cfg.dynamicSmemBytes = bytes;
-  cfg.stream = st;
-  cfg.attrs = pdl;
-  cfg.numAttrs = own_plan && !after ? 0 : 1;   // then the call's first launch: it waits for all that ran before
-  if (cudaLaunchKernelEx(&cfg, step_kernel<D, NB>, a, pl, own_plan, after) != cudaSuccess) return check_launch("step_kernel (launch)");
-  return check_launch("step_kernel");
+  return paged::launch("step_kernel", true, step_kernel<D, NB>, static_cast<unsigned>(pl.workers / kWarps), 32 * kWarps, bytes, st, a, pl, own_plan, after);
 }
 
 }  // namespace

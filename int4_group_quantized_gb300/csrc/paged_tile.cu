@@ -812,19 +812,10 @@ fg_status launch(const AttnArgs<__half>& a, const ClassPlan& pl, bool own_plan, 
       return check_launch("tile_kernel smem attribute");
     set[dev] = true;
   }
-  cudaLaunchAttribute pdl[1];
-  pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  pdl[0].val.programmaticStreamSerializationAllowed = 1;
   Trace tr(KC_ATTN_PAGED, st);
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(pl.workers));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = S::kBytes;
-  cfg.stream = st;
-  cfg.attrs = pdl;
-  cfg.numAttrs = own_plan ? 0 : 1;   // with a plan of its own the call's first launch: it waits for all that ran before
-  if (cudaLaunchKernelEx(&cfg, tile_kernel<D>, a, pl, wait_limit(), own_plan, every) != cudaSuccess) return check_launch("tile_kernel (launch)");
-  return check_launch("tile_kernel");
+  // Not early as a call's first launch: the CTAs then take the SMs in order, so that neighbours in the line share a head's
+  // keys in L2 (a chunk of 2048 rows 452 us, 457 early).
+  return paged::launch("tile_kernel", !own_plan, tile_kernel<D>, static_cast<unsigned>(pl.workers), kThreads, S::kBytes, st, a, pl, wait_limit(), own_plan, every);
 }
 
 }  // namespace

@@ -202,6 +202,7 @@ __device__ __forceinline__ Growth growth_of(const Table& t, const int32_t* cu, i
 __global__ void __launch_bounds__(kPlanThreads) reserve_kernel(const Table t, const int32_t* cu, Plan p,
                                                                unsigned int* err) {
   __shared__ int slots[kPlanWarps];
+  tc::griddep_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int begin, end;
   warp_share(t.seqs, warp, begin, end);
@@ -250,6 +251,7 @@ __global__ void __launch_bounds__(kPlanThreads) reserve_kernel(const Table t, co
 // One warp per named row; the exchange of the length decides which of two
 // mentions of a row ends it.
 __global__ void free_kernel(const Table t, const int32_t* rows, int n, unsigned int* err) {
+  tc::griddep_wait();
   const int lane = threadIdx.x & 31;
   const int k = (blockIdx.x * blockDim.x + threadIdx.x) >> 5;
   if (k >= n) return;
@@ -280,6 +282,7 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(const Table t, 
                                                                  int n, Plan p, unsigned int* err) {
   __shared__ int slots[kPlanWarps];
   tc::griddep_launch();
+  tc::griddep_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int part_mask = (1 << t.ps_log2) - 1;
   auto in_range = [&](int x) { return x >= 0 && x < t.seqs; };
@@ -357,6 +360,7 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(const Table t, 
 __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(const Table t, Plan p) {
   __shared__ int slots[kPlanWarps];
   tc::griddep_launch();
+  tc::griddep_wait();
   const int32_t* refs = t.refs;
   const int live = list_where(t.pages, [&](int x) { return refs[x] > 0; }, nullptr, 0, slots);
   const int moves = list_where(t.pages - live, [&](int x) { return refs[live + x] > 0; }, p.src, t.pages, slots);
@@ -461,7 +465,7 @@ __global__ void __launch_bounds__(256) copy_pages_kernel(const __grid_constant__
 }
 
 // Copies the plan's pages in all pools, and (tab given) moves the table's
-// entries; launched so that it may be scheduled while the plan still runs.
+// entries.
 fg_status copy_pages(const fg_page_pool* pools, int l, const Plan& p, const fg_page_table* tab, cudaStream_t st) {
   for (int l0 = 0; l0 < l || l0 == 0; l0 += kCopyLayers) {
     CopyArgs a = {};
@@ -488,18 +492,8 @@ fg_status copy_pages(const fg_page_pool* pools, int l, const Plan& p, const fg_p
     }
     if (tab && l0 == 0) a.tab = table_of(*tab);
     if (a.layers == 0 && a.tab.seqs == 0) break;
-    cudaLaunchAttribute pdl[1];
-    pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    pdl[0].val.programmaticStreamSerializationAllowed = 1;
     Trace tr(KC_PAGES_COPY, st);
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(num_sms() * 8));
-    cfg.blockDim = dim3(256);
-    cfg.stream = st;
-    cfg.attrs = pdl;
-    cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, copy_pages_kernel, a) != cudaSuccess) return check_launch("copy_pages_kernel (launch)");
-    FG_TRY(check_launch("copy_pages_kernel"));
+    FG_TRY(paged::launch("copy_pages_kernel", true, copy_pages_kernel, static_cast<unsigned>(num_sms() * 8), 256, 0, st, a));
   }
   return FG_OK;
 }
@@ -545,8 +539,7 @@ fg_status fg_pages_reserve(const fg_page_table* t, const int32_t* cu, void* ws, 
   unsigned int* err = device_error_word();
   if (!err) return fail(FG_ERR_CUDA, "device error word");
   Trace tr(KC_PAGES_PLAN, stream);
-  reserve_kernel<<<1, kPlanThreads, 0, stream>>>(table_of(*t), cu, plan_of(*t, ws), err);
-  return check_launch("reserve_kernel");
+  return paged::launch("reserve_kernel", true, reserve_kernel, 1, kPlanThreads, 0, stream, table_of(*t), cu, plan_of(*t, ws), err);
 }
 
 fg_status fg_pages_free(const fg_page_table* t, const int32_t* rows, int64_t n, cudaStream_t stream) {
@@ -559,8 +552,8 @@ fg_status fg_pages_free(const fg_page_table* t, const int32_t* rows, int64_t n, 
   unsigned int* err = device_error_word();
   if (!err) return fail(FG_ERR_CUDA, "device error word");
   Trace tr(KC_PAGES_PLAN, stream);
-  free_kernel<<<static_cast<unsigned>((n + 3) / 4), 128, 0, stream>>>(table_of(*t), rows, static_cast<int>(n), err);
-  return check_launch("free_kernel");
+  return paged::launch("free_kernel", true, free_kernel, static_cast<unsigned>((n + 3) / 4), 128, 0, stream, table_of(*t), rows,
+                      static_cast<int>(n), err);
 }
 
 fg_status fg_pages_fork(const fg_page_table* t, const fg_page_pool* pools, int32_t l, const int32_t* src,
@@ -578,8 +571,8 @@ fg_status fg_pages_fork(const fg_page_table* t, const fg_page_pool* pools, int32
   const Plan p = plan_of(*t, ws);
   {
     Trace tr(KC_PAGES_PLAN, stream);
-    fork_plan_kernel<<<1, kPlanThreads, 0, stream>>>(table_of(*t), src, dst, static_cast<int>(n), p, err);
-    FG_TRY(check_launch("fork_plan_kernel"));
+    FG_TRY(paged::launch("fork_plan_kernel", true, fork_plan_kernel, 1, kPlanThreads, 0, stream, table_of(*t), src, dst,
+                        static_cast<int>(n), p, err));
   }
   return copy_pages(pools, l, p, nullptr, stream);
 }
@@ -592,8 +585,7 @@ fg_status fg_pages_compact(const fg_page_table* t, const fg_page_pool* pools, in
   const Plan p = plan_of(*t, ws);
   {
     Trace tr(KC_PAGES_PLAN, stream);
-    compact_plan_kernel<<<1, kPlanThreads, 0, stream>>>(table_of(*t), p);
-    FG_TRY(check_launch("compact_plan_kernel"));
+    FG_TRY(paged::launch("compact_plan_kernel", true, compact_plan_kernel, 1, kPlanThreads, 0, stream, table_of(*t), p));
   }
   return copy_pages(pools, l, p, t, stream);
 }
