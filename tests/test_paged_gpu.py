@@ -914,6 +914,53 @@ def test_two_calls_at_once(fg):
         assert torch.equal(out, want)
 
 
+@pytest.mark.parametrize("seqs,dtype", [(20, torch.float16), (150, torch.float16), (20, torch.float32), (150, torch.float32)])
+def test_calls_one_after_another(fg, seqs, dtype):
+    """Every call's kernels may be set up while the call before still runs: the results are those of calls that each wait
+    for the one before."""
+    heads, qh, d, ps, pages, turns = 2, 4, 128, 16, 3000, 5
+    rng = np.random.default_rng(54)
+    lengths = np.array([0, 1, 1, 2, 20, 70])
+    jobs = []
+    for _ in range(turns):
+        n = lengths[rng.integers(len(lengths), size=seqs)]
+        n[seqs - 2:] = 0                                      # forked into and freed
+        cu = np.concatenate(([0], np.cumsum(n)))
+        x = [torch.as_tensor(rng.normal(size=(int(cu[-1]), w * d)), device="cuda").to(dtype) for w in (heads, heads, qh)]
+        jobs.append((_i32(cu), *x, _i32(rng.integers(0, seqs - 2, size=2)), int(n.max())))
+    dst = _i32([seqs - 2, seqs - 1])
+    most = max(q.shape[0] for *_, q, _, _ in jobs)
+    results = []
+    for wait in (True, False):
+        after = torch.cuda.synchronize if wait else (lambda: None)
+        pool, tab = fg.PagePool(pages, ps, heads, d, dtype), fg.PageTable.empty(seqs, 64, pages, ps)
+        pools = fg.PagePools([pool])
+        ws = fg.workspace(max(fg.fg_pages_workspace_bytes(tab, 2), fg.fg_paged_attention_workspace_bytes(pool, tab, qh, most, 70)))
+        outs = []
+        torch.cuda.synchronize()
+        for cu, k, v, q, src, _ in jobs:
+            out = [torch.zeros_like(q) for _ in range(3)]
+            kr, vr = torch.zeros_like(k), torch.zeros_like(v)
+            for call in (lambda: fg.fg_pages_reserve(tab, cu, ws),
+                         lambda: fg.fg_paged_append(pool, tab, cu, k, v, kr, vr),
+                         lambda: fg.fg_paged_attention(pool, tab, cu, q, qh, out[0], 70, ws=ws),
+                         lambda: fg.fg_paged_attention(pool, tab, cu, out[0], qh, out[1], 70, window=40, sinks=3, ws=ws),
+                         lambda: fg.fg_pages_fork(tab, pools, src, dst, ws),
+                         lambda: fg.fg_pages_free(tab, src[:1]),
+                         lambda: fg.fg_pages_compact(tab, pools, ws),
+                         lambda: fg.fg_paged_attention(pool, tab, cu, out[1], qh, out[2], 70, ws=ws),
+                         lambda: fg.fg_pages_free(tab, dst)):
+                call()
+                after()
+            outs += out + [kr, vr, tab.table.clone(), tab.lens.clone(), tab.refs.clone()]
+        torch.cuda.synchronize()
+        fg.fg_sync_status()
+        results.append(outs)
+    for a, b in zip(*results):
+        assert torch.equal(a, b)
+    assert all(bool(t.isfinite().all()) for t in results[0])
+
+
 def test_two_graphs_share_a_workspace(fg):
     S = Setup(fg, [700, 400], 2, 64, 32, torch.float16, 53)
     ws = fg.workspace(fg.fg_paged_attention_workspace_bytes(S.pool, S.tab, 4, 300, 200))
