@@ -40,10 +40,11 @@
 // the protocol with its MMAs alone, no softmax and no restoring, takes 362 us
 // of the chunk's 458; with every exponential replaced by a multiply-add it takes
 // as long, without the restoring's arithmetic 424: a group's S, softmax and P V
-// follow one another, and so do their barriers (250 cycles each).  A segment costs 10000 cycles more (walk, Q, first S,
-// first softmax, O), a launch 25000 before its first P V.  Other splits when a
-// tile took a quarter longer: 24 softmax and restoring warps of 80 registers
-// 715 us against 588, two issuing warps 562 against 470.
+// follow one another, and so do their barriers (250 cycles each).  A segment
+// costs 10000 cycles more (walk, Q, first S, first softmax, O), a launch 25000
+// before its first P V.  Other splits when a tile took a quarter longer: 24
+// softmax and restoring warps of 80 registers 715 us against 588, two issuing
+// warps 562 against 470.
 #include <math.h>
 
 #include <algorithm>

@@ -10,7 +10,8 @@ sqrt(d):
     normaliser);
   * steps (at most 16 rows per K/V head): the weight p * scale is rounded to
     fp16 and multiplies c - 8, |c - 8| <= 8: u * 8 * max scale; scores are sums
-    of (1024 + c) q in fp32: d 2^-23 * 1039 * sum |q| * scale / sqrt(d);
+    of c q in fp32, allowed d 2^-23 * 1039 * sum |q| * scale / sqrt(d), what
+    sums of (1024 + c) q would need;
   * chunks of fp16: K and V rounded to fp16 (2 u work on the weights, u mag),
     P rounded to fp16 (u mag, and 2^-25 of the largest weight where P is
     subnormal).
