@@ -19,8 +19,9 @@
 //            call has sequences of more than 8), those carry the rounding's
 //            remainders: the result is then as exact as fp32 sums of unrounded
 //            weights (2.1e-4 of its size off, the fp16 result's own rounding;
-//            otherwise 3.1 to 3.6e-4; a second block of columns for 5 to 8
-//            rows alone would double the long step below, 229 us).
+//            otherwise 3.1 to 3.6e-4: for 5 to 8 rows a second MMA beside
+//            each, with the remainders, gave 2.5e-4 and took 125 us for the
+//            107 of the long step below).
 // A warp is a worker (see paged_sched.cuh) and walks tiles of 32 tokens of its
 // share: its own ring of stages in shared memory, filled by asynchronous
 // copies kStages - 1 tiles ahead across items; no CTA barrier.  Where the next
