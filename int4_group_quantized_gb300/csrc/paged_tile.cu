@@ -616,38 +616,36 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const AttnArgs<__half
         const float f = !whole_item ? 1.0f : l == 0.0f ? 0.0f : 1.0f / l;
         const int64_t slot = (static_cast<int64_t>(w) * 2 + (from_start ? 1 : 0)) * kRows + row_w;   // of the warp's first row
 #pragma unroll 1
-        for (int c = 0; c < D / 16; ++c) {
-          uint32_t u[16];
-          tmem_ld_32x32b_x16(to + 16 * c, u);
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t u[32];
+          tmem_ld_32x32b_x32(to + 32 * c, u);
           tmem_arrived(u);
-          const float fc = (nans >> (c >> 2)) & 1u ? __uint_as_float(0x7fffffffu) : f;   // a NaN group's columns
-          float v[16];         // of 8 columns dims 0..7 lie at 0, 2, 4, 6, 1, 3, 5, 7
+          const float fc = (nans >> (c >> 1)) & 1u ? __uint_as_float(0x7fffffffu) : f;   // a NaN group's columns
+          float v[32];         // of 8 columns dims 0..7 lie at 0, 2, 4, 6, 1, 3, 5, 7
 #pragma unroll
-          for (int e = 0; e < 16; ++e) v[e] = __uint_as_float(u[(e & 8) + ((e & 7) < 4 ? 2 * (e & 7) : 2 * (e & 7) - 7)]) * fc;
+          for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(u[(e & 24) + ((e & 7) < 4 ? 2 * (e & 7) : 2 * (e & 7) - 7)]) * fc;
           if (whole_item) {
             if (r >= rows) continue;   // no collective follows in the round
-            uint32_t h[8];
+            uint4* out = reinterpret_cast<uint4*>(a.out + dst + 32 * c);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) h[e] = q4::cvt_f16x2(make_float2(v[2 * e], v[2 * e + 1]));
-            uint4* out = reinterpret_cast<uint4*>(a.out + dst + 16 * c);
-            out[0] = make_uint4(h[0], h[1], h[2], h[3]);
-            out[1] = make_uint4(h[4], h[5], h[6], h[7]);
+            for (int e = 0; e < 32; e += 8)
+              out[e / 8] = make_uint4(q4::cvt_f16x2(make_float2(v[e], v[e + 1])), q4::cvt_f16x2(make_float2(v[e + 2], v[e + 3])),
+                                      q4::cvt_f16x2(make_float2(v[e + 4], v[e + 5])), q4::cvt_f16x2(make_float2(v[e + 6], v[e + 7])));
             continue;
           }
           // A partial's 32 columns go through shared memory and leave eight lanes a row: a row a lane takes a line of the L1
           // per lane and store (8500 cycles for the partial, 6500 to 7900 this way; whole rows, half the bytes and no
           // second pass, are faster straight out).
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            *reinterpret_cast<uint4*>(stage + lane * 128 + (((4 * (c & 1) + e) ^ (lane & 7)) << 4)) =
+          for (int e = 0; e < 8; ++e)
+            *reinterpret_cast<uint4*>(stage + lane * 128 + ((e ^ (lane & 7)) << 4)) =
                 make_uint4(__float_as_uint(v[4 * e]), __float_as_uint(v[4 * e + 1]), __float_as_uint(v[4 * e + 2]), __float_as_uint(v[4 * e + 3]));
-          if (!(c & 1)) continue;
           __syncwarp();
 #pragma unroll 4
           for (int i = 0; i < 32; i += 4) {
             const int n = i + (lane >> 3);
             const uint4 x = *reinterpret_cast<const uint4*>(stage + n * 128 + (((lane & 7) ^ (n & 7)) << 4));
-            if (row_w + n < rows) *reinterpret_cast<uint4*>(pl.part + (slot + n) * D + 16 * (c - 1) + 4 * (lane & 7)) = x;
+            if (row_w + n < rows) *reinterpret_cast<uint4*>(pl.part + (slot + n) * D + 32 * c + 4 * (lane & 7)) = x;
           }
           __syncwarp();
         }
