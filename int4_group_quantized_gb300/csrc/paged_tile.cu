@@ -32,13 +32,13 @@
 // Every wait is bounded; on timeout the CTA raises the device error word, lets
 // its MMAs finish and frees its tensor memory.
 //
-// Measured: a chunk of 2048 rows over 16384 tokens, 32 heads of 128, 451 to 458
-// us (1.13 PFLOP/s, 59% of what a large bf16 library product reaches); a mixed
+// Measured: a chunk of 2048 rows over 16384 tokens, 32 heads of 128, 447 to 455
+// us (1.14 PFLOP/s, 60% of what a large bf16 library product reaches); a mixed
 // batch of 12 sequences (1 to 600 rows, 32 query heads on 8, a window of 1000
 // with 4 sinks) 115 to 119 us; 64 chunks of 20 rows over 300 to 600 tokens, 8
-// heads, 64 us.  A tile takes 3400 cycles where its four MMA batches take 2200:
+// heads, 63 us.  A tile takes 3400 cycles where its four MMA batches take 2200:
 // the protocol with its MMAs alone, no softmax and no restoring, takes 362 us
-// of the chunk's 458; with every exponential replaced by a multiply-add it takes
+// of the chunk's 450; with every exponential replaced by a multiply-add it takes
 // as long, without the restoring's arithmetic 424: a group's S, softmax and P V
 // follow one another, and so do their barriers (250 cycles each).  A segment
 // costs 10000 cycles more (walk, Q, first S, first softmax, O), a launch 25000
