@@ -714,7 +714,7 @@ def _rows(t: torch.Tensor, pool: "PagePool", n: int, cols: int, name: str) -> in
     ld, unit = t.stride()
     if unit != 1 and cols > 1:
         raise ValueError(f"{name}: columns must be adjacent, strides are {t.stride()}")
-    return ld if n > 1 else max(ld, cols)   # a single row's own stride is any
+    return ld if n > 1 else cols   # a single row's own stride is any
 
 
 def fg_pages_workspace_bytes(tab: PageTable, n: int = 0) -> int:

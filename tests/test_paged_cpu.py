@@ -178,6 +178,18 @@ def test_python_keeps_a_call_on_one_device(fg):
         fg.PagePools(layers)
 
 
+def test_python_row_strides(fg):
+    import torch
+    pool = fg.PagePool(2, 16, 2, 64, device="cpu")
+    rows = torch.zeros((3, 136), dtype=torch.float16)
+    assert fg._rows(rows[:, :128], pool, 3, 128, "q") == 136
+    for stride in (0, 1, 130, 136):                    # a single row has no next one
+        assert fg._rows(torch.as_strided(rows, (1, 128), (stride, 1)), pool, 1, 128, "q") == 128
+    for bad in (torch.as_strided(rows, (1, 64), (136, 2)), rows[:, :128].float(), rows[:, :64], rows[0, :128]):
+        with pytest.raises(ValueError):
+            fg._rows(bad, pool, 1 if bad.shape[0] == 1 else 3, bad.shape[-1] if bad.dim() == 2 and bad.shape[0] == 1 else 128, "q")
+
+
 # ---- the oracle -----------------------------------------------------------------
 
 def _check_invariants(pg, pages):
