@@ -143,3 +143,71 @@ def attention(q, k, v, pos, window=0, sinks=0, present=None):
         mag = p @ np.where(fin, np.abs(v), 0.0)
         work = np.where(see, np.abs(q) @ np.abs(np.where(np.isfinite(k), k, 0.0)).T / np.sqrt(d), 0.0)
     return out, mag, work.max(axis=1, initial=0.0)
+
+
+# ---- how far a kernel's rows may be off ------------------------------------------
+
+HALF = 2.0 ** -11   # half a step of fp16, relative; of its subnormals 2^-25
+F32 = 2.0 ** -23    # a truncated fp32 sum, relative
+
+
+def attention_bound(q, k, v, pos, window=0, sinks=0, present=None, kind="step"):
+    """The rows' output (attention above) and what an element of it may be off, for K and V given as (codes, mins,
+    scales) of a head's tokens.  Every term is taken over the tokens that a row sees, with their weights p_j:
+
+      * the result's rounding: half a step;
+      * sums in fp32: (n + d + 16) steps of what is summed.  A score off by e moves the output by at most
+        (exp(2 e) - 1) sum p |v|;
+      * step: scores are sums of q c, c <= 15, times the scale, and of the minimum times sum q.  The weight w = p scale
+        is rounded to fp16 and multiplies c - 8.  Its power of two keeps the largest w of the row and group at 2^4 or
+        more, so a small w is off by 2^-25 / 2^4 of the largest;
+      * chunk: K, V and P are rounded to fp16.  The largest P of a row is 2^8 or more, so a small one is off by 2^-33 of
+        the largest;
+      * f32: no rounding but fp32's own."""
+    kv, vv = restore(*k), restore(*v)
+    out, mag, work = attention(q, kv, vv, pos, window, sinks, present)
+    n, d = kv.shape
+    groups = d // 64
+    see = visible(pos, n, window, sinks)
+    if present is not None:
+        see &= np.asarray(present)[None]
+    with np.errstate(all="ignore"):
+        fin = lambda x: np.where(np.isfinite(x), x, 0.0)   # what is not finite gives NaN rows or groups: no bound there
+        s = np.where(see, q @ fin(kv).T / np.sqrt(d), -np.inf)
+        p = np.exp(s - np.max(s, axis=1, keepdims=True, initial=-1e300))
+        p = np.where(see, p, 0.0)
+        p /= np.maximum(p.sum(axis=1, keepdims=True), 1e-300)
+        qg = np.abs(fin(q)).reshape(len(q), groups, 64).sum(2)
+        terms = np.where(see, qg @ (15 * np.abs(fin(k[2])) + np.abs(fin(k[1]))).astype(np.float64).T / np.sqrt(d), 0.0).max(axis=1, initial=0.0)
+    wide = lambda x: np.repeat(x, 64, axis=1)              # a value a group, for each of its dims
+    vmin, vscale = np.abs(fin(v[1])).astype(np.float64), np.abs(fin(v[2])).astype(np.float64)
+    steps = (n + d + 16) * F32
+    work, terms = work[:, None], terms[:, None]
+    if kind == "f32":
+        tol = 2.0 ** -24 * np.abs(out) + steps * mag + np.expm1(2 * steps * work) * mag
+    elif kind == "step":
+        big = (p[:, :, None] * vscale[None]).max(axis=1, initial=0.0)
+        tol = HALF * np.abs(out) + 2.0 ** -25 + steps * wide(p @ (vmin + 15 * vscale)) + np.expm1(2 * (d + 16) * F32 * terms) * mag
+        tol = tol + wide(HALF * 8 * (p @ vscale) + n * 2.0 ** -26 * big)
+    else:
+        tiny = 2.0 ** -25 * np.abs(fin(q)).sum(1, keepdims=True) / np.sqrt(d)     # K's subnormals, in the scores
+        tol = HALF * (np.abs(out) + 2 * mag) + 2.0 ** -24 + steps * mag + np.expm1(2 * ((HALF + steps) * work + tiny)) * mag
+        tol = tol + n * 2.0 ** -33 * p.max(axis=1, initial=0.0)[:, None] * np.abs(fin(vv)).max(axis=0, initial=0.0)[None]
+    return out, tol
+
+
+def off_by_too_much(got, ref, tol, rms=None):
+    """Why `got` is not `ref` within `tol`, and within `rms` in the mean (relative, and half a step of fp16's
+    subnormals); None where it is."""
+    if not np.array_equal(np.isnan(got), np.isnan(ref)):
+        return "NaN where there should be none, or none where there should be"
+    f = ~np.isnan(ref)
+    err = np.abs(got[f] - ref[f])
+    worst = (err - tol[f]).max(initial=-1.0)
+    if worst > 0:
+        return f"error {err.max():.3g} above its bound by {worst:.3g}"
+    if rms is not None and f.any():
+        e, w = np.sqrt(np.mean(err ** 2)), np.sqrt(np.mean(ref[f] ** 2))
+        if e > rms * w + 2.0 ** -25:
+            return f"rms error {e / w:.3g} > {rms:.3g}"
+    return None

@@ -1,0 +1,142 @@
+"""The paged attention against the oracle in 64 bits with bounds taken over the tokens that each row sees
+(oracle/paged.py, attention_bound; tests/test_paged_bounds_cpu.py shows what they refuse), and in the mean: the roundings
+are independent, each at most u / sqrt(3) of the row's size (times 8 / 4.3 for the centred codes), u = 2^-11, so the root
+mean square error of a step is below 2 u, of a chunk below 3 u."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import codec, paged as op
+from test_paged_gpu import CHUNK, STEP, Setup, _attend, _i32, _ids, _q
+
+pytestmark = pytest.mark.gpu
+U = op.HALF
+KINDS = {"step": 2 * U, "chunk": 3 * U, "f32": None}
+
+
+@pytest.fixture(scope="module")
+def fg():
+    import int4_group_quantized_gb300 as fg
+    return fg
+
+
+def _kind(S, n, q_heads):
+    """How the library takes a sequence of n rows."""
+    return "f32" if S.dtype == torch.float32 else "step" if n * (q_heads // S.heads) <= 16 else "chunk"
+
+
+def _hold(S, out, cu, q, q_heads, window=0, sinks=0, mean=True, rows_mean=None):
+    """Every sequence and K/V head within its bound; `mean` (and rows_mean, a factor, row by row): in the mean as well."""
+    r, d = q_heads // S.heads, S.d
+    got, q = out.cpu().numpy().astype(np.float64), q.cpu().numpy().astype(np.float64)
+    live = np.zeros(len(got), bool)
+    live[int(cu[0]):int(cu[-1])] = True
+    assert (got[~live] == 7.0).all(), "a row outside the batch was written"
+    parts = {}
+    for i in range(len(S.lens)):
+        a, e, length = int(cu[i]), int(cu[i + 1]), int(S.lens[i])
+        if a == e:
+            continue
+        kind = _kind(S, e - a, q_heads)
+        j = np.arange(length)
+        col = np.minimum(j // S.ps, S.table.shape[1] - 1)
+        page = np.where(j // S.ps < S.table.shape[1], S.table[i, col], -1)
+        ok = (page >= 0) & (page < S.pages)
+        page = np.where(ok, page, 0)
+        pos = np.repeat(np.arange(length - (e - a), length), r)
+        for h in range(S.heads):
+            k, v = ([x[page, h, j % S.ps] for x in S.arr[w]] for w in "kv")
+            sl = np.s_[a:e, h * r * d:(h + 1) * r * d]
+            o = got[sl].reshape(-1, d)
+            ref, tol = op.attention_bound(q[sl].reshape(-1, d), k, v, pos, window, sinks, ok, kind)
+            why = op.off_by_too_much(o, ref, tol)
+            assert why is None, f"sequence {i}, head {h}: {why}"
+            if rows_mean is not None and KINDS[kind]:
+                for x, w in zip(o, ref):
+                    why = op.off_by_too_much(x, w, np.inf + 0 * x, rows_mean * KINDS[kind])
+                    assert why is None, f"sequence {i}, head {h}, a row: {why}"
+            parts.setdefault(kind, []).append((o, ref))
+    for kind, p in parts.items():
+        if mean and KINDS[kind]:
+            o, ref = (np.concatenate([x[n].reshape(-1) for x in p]) for n in (0, 1))
+            why = op.off_by_too_much(o, ref, np.full(o.shape, np.inf), KINDS[kind])
+            assert why is None, f"{kind}: {why}"
+
+
+def _run(fg, S, n, q_heads, window=0, sinks=0, q=None, status=None, **kw):
+    cu = np.concatenate(([0], np.cumsum(n)))
+    q = _q(S, int(cu[-1]), q_heads) if q is None else q
+    out = _attend(fg, S, cu, q, q_heads, window, sinks)
+    if status is None:
+        fg.fg_sync_status()
+    else:
+        with pytest.raises(fg.FGError) as e:
+            fg.fg_sync_status()
+        assert e.value.status == status
+    _hold(S, out, cu, q, q_heads, window, sinks, **kw)
+    return out
+
+
+@pytest.mark.parametrize("case", STEP + CHUNK, ids=_ids)
+@pytest.mark.parametrize("dtype", [torch.float16, torch.float32])
+def test_every_row_within_its_bound(fg, case, dtype):
+    lens, n, qh, h, d, ps, window, sinks = case
+    _run(fg, Setup(fg, lens, h, d, ps, dtype, 11), n, qh, window, sinks)
+
+
+@pytest.mark.parametrize("n", [[1, 2], [7, 5], [40, 90]])
+@pytest.mark.parametrize("scale", [1e-6, 1e-3, 30.0])
+def test_rows_of_any_size(fg, scale, n):
+    _run(fg, Setup(fg, [400, 300], 2, 128, 32, torch.float16, 14, scale=scale), n, 4, mean=scale < 1)
+
+
+@pytest.mark.parametrize("seqs", [129, 1100])
+@pytest.mark.parametrize("most", [1, 59])
+@pytest.mark.parametrize("dtype", [torch.float16, torch.float32])
+def test_many_sequences(fg, seqs, most, dtype):
+    rng = np.random.default_rng(seqs)
+    lens = rng.integers(1, 60, seqs)
+    n = np.minimum(lens, np.where(rng.random(seqs) < 0.3, 0, np.where(rng.random(seqs) < 0.8, 1, rng.integers(1, most + 1, seqs))))
+    _run(fg, Setup(fg, lens, 1, 64, 16, dtype, seqs), n, 2)
+
+
+@pytest.mark.parametrize("n", [[1, 1, 1], [30, 20, 10]])
+@pytest.mark.parametrize("dtype", [torch.float16, torch.float32])
+def test_missing_pages(fg, n, dtype):
+    S = Setup(fg, [200, 100, 90], 2, 64, 16, dtype, 17, extra=4)
+    S.table[0, 3], S.table[1, 0], S.table[2, 2] = -1, S.pages, 2 ** 30
+    S.upload(fg)
+    _run(fg, S, n, 4, status=4)
+
+
+@pytest.mark.parametrize("n", [[1, 1], [30, 40]])
+@pytest.mark.parametrize("dtype", [torch.float16, torch.float32])
+def test_a_table_row_too_short(fg, n, dtype):
+    S = Setup(fg, [64, 50], 1, 64, 16, dtype, 51, spare=0)
+    S.lens = np.array([90, 50])
+    S.upload(fg)
+    _run(fg, S, n, 2, status=4)
+
+
+@pytest.mark.parametrize("n", [6, 40])
+@pytest.mark.parametrize("dtype", [torch.float16, torch.float32])
+def test_more_rows_than_tokens(fg, n, dtype):
+    _run(fg, Setup(fg, [4, 30], 1, 64, 16, dtype, 18), [n, 1], 2)
+
+
+@pytest.mark.parametrize("n", [[1, 1, 1], [4, 3, 8], [20, 150, 33]])
+@pytest.mark.parametrize("dtype", [torch.float16, torch.float32])
+def test_nan_groups_leave_the_other_rows_exact(fg, n, dtype):
+    lens = [150, 300, 64]
+    S = Setup(fg, lens, 2, 128, 32, dtype, 15)
+    for w in "kv":
+        for i, length in enumerate(lens):
+            last = S.table[i, (length - 1) // 32]
+            for x in S.arr[w][1:]:
+                x[last, :, (length - 1) % 32 + 1:] = np.nan
+        S.arr[w][1][S.refs == 0] = np.inf
+        S.arr[w][2][S.refs == 0] = np.nan
+    for w, i, h, t, g in (("v", 1, 0, 10, 1), ("v", 1, 1, 295, 0), ("v", 1, 0, 298, 0), ("k", 2, 1, 62, 1), ("k", 0, 0, 20, 0)):
+        S.arr[w][2][S.table[i, t // 32], h, t % 32, g] = np.nan
+    S.upload(fg)
+    _run(fg, S, n, 2, 100, 3)
