@@ -609,6 +609,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const AttnArgs<__half
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&qfull[grp]);
+        __syncwarp();   // collective loads follow
       }
       if (rows >= 0) {
         // ---- the segment's rows: finished, or this share's partial ------------------------
@@ -625,12 +626,14 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const AttnArgs<__half
 #pragma unroll
           for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(u[(e & 24) + ((e & 7) < 4 ? 2 * (e & 7) : 2 * (e & 7) - 7)]) * fc;
           if (whole_item) {
-            if (r >= rows) continue;   // no collective follows in the round
-            uint4* out = reinterpret_cast<uint4*>(a.out + dst + 32 * c);
+            if (r < rows) {
+              uint4* out = reinterpret_cast<uint4*>(a.out + dst + 32 * c);
 #pragma unroll
-            for (int e = 0; e < 32; e += 8)
-              out[e / 8] = make_uint4(q4::cvt_f16x2(make_float2(v[e], v[e + 1])), q4::cvt_f16x2(make_float2(v[e + 2], v[e + 3])),
-                                      q4::cvt_f16x2(make_float2(v[e + 4], v[e + 5])), q4::cvt_f16x2(make_float2(v[e + 6], v[e + 7])));
+              for (int e = 0; e < 32; e += 8)
+                out[e / 8] = make_uint4(q4::cvt_f16x2(make_float2(v[e], v[e + 1])), q4::cvt_f16x2(make_float2(v[e + 2], v[e + 3])),
+                                        q4::cvt_f16x2(make_float2(v[e + 4], v[e + 5])), q4::cvt_f16x2(make_float2(v[e + 6], v[e + 7])));
+            }
+            __syncwarp();   // the next round begins with a collective load
             continue;
           }
           // A partial's 32 columns go through shared memory and leave eight lanes a row: a row a lane takes a line of the L1
