@@ -13,8 +13,9 @@
 //            centres the code, because the MMA truncates and a positive sum
 //            over thousands of tokens would lose its low bits.  The weight w =
 //            p * scale is rounded to fp16 for the MMA after scaling by a power
-//            of two near 1 / max scale, so that small activations keep their
-//            bits; sum w is an MMA against ones, of the rounded weights.  Where
+//            of two that fits the largest weight of the query, so that small
+//            activations keep their bits; sum w is an MMA against ones, of the
+//            rounded weights.  Where
 //            rows leave half the MMA's columns free (1 to 4; up to 8 when a
 //            call has sequences of more than 8), those carry the rounding's
 //            remainders: the result is then as exact as fp32 sums of unrounded
@@ -69,7 +70,14 @@ template <int NB>
 constexpr int kCtasPerSm = 3;
 template <int D, int NB>
 constexpr int kStepStages = D == 128 ? 3 : 4;
-constexpr float kGrow = 12.0f;          // how far (in powers of two) a score may lie above the maximum: its weight, times 8 at most, stands as fp16
+constexpr float kGrow = 12.0f;          // how far (in powers of two) a score may lie above the maximum
+// The weights w = p * scale travel as fp16 times a power of two, one per query and group: found when the sum of a lane's
+// four would pass kMostW, so that the largest lies in [2^5, 2^6), and raised with the maximum of the scores.  What is small
+// beside the largest weight of its row alone may lose bits (below 2^-19 of it), whatever the scales of tokens that the
+// row does not see or gives no weight.
+constexpr float kMostW = 32768.0f;
+constexpr int kTargetW = 5;
+constexpr float kMostInv = 1.329227995784916e36f;   // 2^120: of a row without weights
 
 template <int D>
 struct Stage {
@@ -104,10 +112,10 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-__device__ __forceinline__ float max_nan(float a, float b) {   // NaN if either is
-  float y;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
-  return y;
+__device__ __forceinline__ uint32_t add_h2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
 }
 // Two fp32 at once (the queries 2 tig and 2 tig + 1 of a lane).
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
@@ -135,6 +143,16 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   return r;
 }
 __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+__device__ __forceinline__ float reciprocal2(float x) { return __uint_as_float(0x7f000000u - __float_as_uint(x)); }   // of 2^k
+// Whether one of two fp16 is above kMostW, or NaN.
+__device__ __forceinline__ bool past(uint32_t h) {
+  return !__hble2(*reinterpret_cast<const __half2*>(&h), __floats2half2_rn(kMostW, kMostW));
+}
+// The factor that takes the weight `most` > 0 into [2^kTargetW, 2 * 2^kTargetW).
+__device__ __forceinline__ float factor_for(float most) {
+  const int e = min(static_cast<int>(__float_as_uint(most) >> 23), 253);
+  return __uint_as_float(static_cast<uint32_t>(min(254 + kTargetW - e, 247)) << 23);
+}
 constexpr uint32_t kOnes = 0x3C003C00u;   // fp16 (1, 1)
 constexpr float k2p24 = 16777216.0f;      // a code's bits as a subnormal fp16 are c * 2^-24
 // D = A B + C with C = (c0, c1, c2, c3)
@@ -317,7 +335,7 @@ __global__ void __launch_bounds__(32 * kWarps, kCtasPerSm<NB>) step_kernel(const
   float m[NB][2];
   float2 l[NB], cmn[NB][NG];
   float acc[NB][NT][4];
-  float cap[NG], inv[NG];                        // weights carry the factor inv = 8 / cap
+  float2 inv[NB][NG];                            // the weights' factor
   uint32_t nans = 0;                             // bit 4 nb + 2 e + g: the query sees a NaN value group
   int rows = 0, row0 = 0, keys = 0;
   // Up to four rows (eight with two blocks of columns) leave half of the MMAs' columns free: columns 4 .. 7 (the second
@@ -360,6 +378,7 @@ __global__ void __launch_bounds__(32 * kWarps, kCtasPerSm<NB>) step_kernel(const
         sum += __shfl_xor_sync(0xffffffffu, sum, 2);
         qsum[nb][g] = make_float2(__shfl_sync(0xffffffffu, sum, 8 * tig), __shfl_sync(0xffffffffu, sum, 8 * tig + 4));
         cmn[nb][g] = both(0.0f);
+        inv[nb][g] = both(kMostInv);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           qb[nb][g][e][0] = f.b[g][e][0];
@@ -376,8 +395,6 @@ __global__ void __launch_bounds__(32 * kWarps, kCtasPerSm<NB>) step_kernel(const
 #pragma unroll
       for (int i = 0; i < NT; ++i) acc[nb][i][0] = acc[nb][i][1] = acc[nb][i][2] = acc[nb][i][3] = 0.0f;
     }
-#pragma unroll
-    for (int g = 0; g < NG; ++g) cap[g] = inv[g] = 0.0f;
     nans = 0;
   };
 
@@ -455,58 +472,6 @@ __global__ void __launch_bounds__(32 * kWarps, kCtasPerSm<NB>) step_kernel(const
         }
       __syncwarp();
     }
-    // The weights' factor: a power of two that keeps max scale * factor in [4,
-    // 8).  A group whose scale is not finite stands for NaN: it is noted for
-    // the queries that see it and leaves the sums.
-    float vs_all[2][2][NG];
-#pragma unroll
-    for (int hf = 0; hf < 2; ++hf)
-#pragma unroll
-      for (int r = 0; r < 2; ++r) read_meta<NG>(s + St::kVs, 16 * hf + 8 * r + tok, vs_all[hf][r]);
-#pragma unroll
-    for (int g = 0; g < NG; ++g) {
-      float vs[2][2];
-#pragma unroll
-      for (int hf = 0; hf < 2; ++hf)
-#pragma unroll
-        for (int r = 0; r < 2; ++r) vs[hf][r] = vs_all[hf][r][g];
-      if (__any_sync(0xffffffffu, !(max_nan(max_nan(vs[0][0], vs[0][1]), max_nan(vs[1][0], vs[1][1])) < cap[g]))) {
-        float mx = 0.0f;
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf)
-#pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            uint32_t mine = 0;   // this lane's queries that see the token
-#pragma unroll
-            for (int nb = 0; nb < NB; ++nb) mine |= ((seen >> (8 * nb + 4 * hf + 2 * r)) & 3u) << (2 * nb);
-            if (!(vs[hf][r] < INFINITY)) {   // its values count as zeros from here on
-              vs[hf][r] = 0.0f;
-              if (tig == 0) *value_meta(s + St::kVs, hf, r, g) = *value_meta(s + St::kVm, hf, r, g) = 0.0f;
-#pragma unroll
-              for (int k = 0; k < 2 * NB; ++k)
-                if ((mine >> k) & 1u) nans |= 1u << (2 * k + g);
-            }
-            mx = fmaxf(mx, vs[hf][r]);
-          }
-        __syncwarp();
-        const uint32_t bits = __reduce_max_sync(0xffffffffu, __float_as_uint(mx));
-        const uint32_t e = min(max(bits >> 23, 4u), 253u);   // biased exponent
-        const float ncap = __uint_as_float((e + 1) << 23), ninv = 4.0f * __uint_as_float((254u - min(e, 251u)) << 23);
-        if (ncap > cap[g]) {
-          if (inv[g] != 0.0f) {
-            const float f = ninv / inv[g];
-#pragma unroll
-            for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-              for (int i = 4 * g; i < 4 * g + 4; ++i)
-#pragma unroll
-                for (int e4 = 0; e4 < 4; ++e4) acc[nb][i][e4] *= f;
-          }
-          cap[g] = ncap;
-          inv[g] = ninv;
-        }
-      }
-    }
     // The maximum known so far serves while no score of a query lies more than 2^12 above it (a larger one would only change
     // the scale of sums that are divided in the end).  Otherwise, and before a key was seen, the tile's maximum is found
     // over the lanes of a query and the sums are rescaled.
@@ -534,19 +499,28 @@ __global__ void __launch_bounds__(32 * kWarps, kCtasPerSm<NB>) step_kernel(const
         const uint32_t mine = 0x11111111u << tig;
         const bool ask0 = __ballot_sync(0xffffffffu, asks[nb][0]) & mine, ask1 = __ballot_sync(0xffffffffu, asks[nb][1]) & mine;
         const float nm[2] = {ask0 ? fmaxf(m[nb][0], x) : m[nb][0], ask1 ? fmaxf(m[nb][1], y) : m[nb][1]};
-        float al[2];
+        float al[2], grown[2];            // the power of two by which the weights' factor grows with the maximum
 #pragma unroll
-        for (int e = 0; e < 2; ++e) al[e] = nm[e] == -INFINITY ? 1.0f : ex2((m[nb][e] - nm[e]) * kc2);
+        for (int e = 0; e < 2; ++e) {
+          const float up = (nm[e] - m[nb][e]) * kc2;
+          al[e] = nm[e] == -INFINITY ? 1.0f : ex2(-up);
+          grown[e] = nm[e] == -INFINITY ? 1.0f : __uint_as_float(static_cast<uint32_t>(127 + static_cast<int>(fminf(up, 126.0f))) << 23);
+        }
         const float2 f = make_float2(al[0], al[1]);
         l[nb] = mul2(l[nb], f);
 #pragma unroll
-        for (int g = 0; g < NG; ++g) cmn[nb][g] = mul2(cmn[nb][g], f);
+        for (int g = 0; g < NG; ++g) {
+          cmn[nb][g] = mul2(cmn[nb][g], f);
+          const float ni[2] = {fminf(inv[nb][g].x * grown[0], kMostInv), fminf(inv[nb][g].y * grown[1], kMostInv)};
+          const float fx = al[0] * (ni[0] * reciprocal2(inv[nb][g].x)), fy = al[1] * (ni[1] * reciprocal2(inv[nb][g].y));
+          inv[nb][g] = make_float2(ni[0], ni[1]);
 #pragma unroll
-        for (int i = 0; i < NT; ++i) {
-          acc[nb][i][0] *= al[0];
-          acc[nb][i][1] *= al[1];
-          acc[nb][i][2] *= al[0];
-          acc[nb][i][3] *= al[1];
+          for (int i = 4 * g; i < 4 * g + 4; ++i) {
+            acc[nb][i][0] *= fx;
+            acc[nb][i][1] *= fy;
+            acc[nb][i][2] *= fx;
+            acc[nb][i][3] *= fy;
+          }
         }
         m[nb][0] = nm[0];
         m[nb][1] = nm[1];
@@ -564,18 +538,15 @@ __global__ void __launch_bounds__(32 * kWarps, kCtasPerSm<NB>) step_kernel(const
           l[nb] = add2(l[nb], sc[nb][hf][r]);
         }
     }
-    float vf[2][2][NG], mid[2][2][NG];   // factor of p in the weights, value of the centre code
+    float vs[2][2][NG], mid[2][2][NG];   // scales, and values of the centre code
 #pragma unroll
     for (int hf = 0; hf < 2; ++hf)
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        read_meta<NG>(s + St::kVs, 16 * hf + 8 * r + tok, vf[hf][r]);
+        read_meta<NG>(s + St::kVs, 16 * hf + 8 * r + tok, vs[hf][r]);
         read_meta<NG>(s + St::kVm, 16 * hf + 8 * r + tok, mid[hf][r]);
 #pragma unroll
-        for (int g = 0; g < NG; ++g) {
-          mid[hf][r][g] = fmaf(8.0f, vf[hf][r][g], mid[hf][r][g]);
-          vf[hf][r][g] *= inv[g];
-        }
+        for (int g = 0; g < NG; ++g) mid[hf][r][g] = fmaf(8.0f, vs[hf][r][g], mid[hf][r][g]);
       }
     // the values' products, group by group: the two halves' weights as B
     // fragments, their sums, then the codes
@@ -584,19 +555,81 @@ __global__ void __launch_bounds__(32 * kWarps, kCtasPerSm<NB>) step_kernel(const
       constexpr float lo = -8.0f / k2p24, hi = -128.0f / k2p24;
       uint32_t vb[NB][2][2];
       float ps[NB][4];
+      auto weight = [&](int nb, int hf, int r) { return mul2(mul2(sc[nb][hf][r], both(vs[hf][r][g])), inv[nb][g]); };
+      auto weigh = [&]() {              // whether a lane's weights pass the bound (or are NaN)
+        bool over = false;
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              const float2 wt = weight(nb, hf, r);
+              vb[nb][hf][r] = pack_h2(wt.x, wt.y);
+            }
+          over = over || past(add_h2(add_h2(vb[nb][0][0], vb[nb][0][1]), add_h2(vb[nb][1][0], vb[nb][1][1])));
+        }
+        return over;
+      };
+      if (__any_sync(0xffffffffu, weigh())) {
+        // A group whose scale is not finite stands for NaN: it is noted for the queries that see it and leaves the sums.
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+          for (int r = 0; r < 2; ++r)
+            if (!(fabsf(vs[hf][r][g]) < INFINITY)) {
+              vs[hf][r][g] = mid[hf][r][g] = 0.0f;
+#pragma unroll
+              for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                  if ((seen >> (8 * nb + 4 * hf + 2 * r + e)) & 1u) nans |= 1u << (4 * nb + 2 * e + g);
+            }
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+          float2 most = both(0.0f), sum = both(0.0f);
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              const float2 t = mul2(sc[nb][hf][r], both(vs[hf][r][g]));
+              most = make_float2(fmaxf(most.x, t.x), fmaxf(most.y, t.y));
+              sum = add2(sum, t);
+            }
+#pragma unroll
+          for (int o = 4; o < 32; o <<= 1) {
+            most.x = fmaxf(most.x, __shfl_xor_sync(0xffffffffu, most.x, o));
+            most.y = fmaxf(most.y, __shfl_xor_sync(0xffffffffu, most.y, o));
+          }
+          // only the queries whose own weights ask for it; a little below the bound, since fp16 sums are rounded
+          const uint32_t mine = 0x11111111u << tig;
+          const bool ask0 = __ballot_sync(0xffffffffu, sum.x * inv[nb][g].x > 0.9f * kMostW) & mine;
+          const bool ask1 = __ballot_sync(0xffffffffu, sum.y * inv[nb][g].y > 0.9f * kMostW) & mine;
+          const float2 ni = make_float2(ask0 ? factor_for(most.x) : inv[nb][g].x, ask1 ? factor_for(most.y) : inv[nb][g].y);
+          const float fx = ni.x * reciprocal2(inv[nb][g].x), fy = ni.y * reciprocal2(inv[nb][g].y);
+          inv[nb][g] = ni;
+#pragma unroll
+          for (int i = 4 * g; i < 4 * g + 4; ++i) {
+            acc[nb][i][0] *= fx;
+            acc[nb][i][1] *= fy;
+            acc[nb][i][2] *= fx;
+            acc[nb][i][3] *= fy;
+          }
+        }
+        weigh();
+      }
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf) {
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
 #pragma unroll
           for (int nb = 0; nb < NB; ++nb) {
-            float2 wt = mul2(sc[nb][hf][r], both(vf[hf][r][g]));
             if (split && (NB == 1 ? tig >= 2 : nb == 1)) {
-              const float2 hi = unpack_h2(pack_h2(wt.x, wt.y));
-              wt = make_float2(wt.x - hi.x, wt.y - hi.y);
+              const float2 wt = weight(nb, hf, r), hi = unpack_h2(vb[nb][hf][r]);
+              vb[nb][hf][r] = pack_h2(wt.x - hi.x, wt.y - hi.y);
             }
             cmn[nb][g] = fma2(sc[nb][hf][r], both(mid[hf][r][g]), cmn[nb][g]);
-            vb[nb][hf][r] = movmatrix_trans(pack_h2(wt.x, wt.y));
+            vb[nb][hf][r] = movmatrix_trans(vb[nb][hf][r]);
           }
         }
 #pragma unroll
@@ -673,7 +706,8 @@ __global__ void __launch_bounds__(32 * kWarps, kCtasPerSm<NB>) step_kernel(const
         float v[NG][8];
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
-          const float un = inv[g] != 0.0f ? k2p24 / inv[g] : 0.0f;   // powers of two
+          // 2^24 / inv
+          const float un = __uint_as_float(min(278u - (__float_as_uint(e ? inv[nb][g].y : inv[nb][g].x) >> 23), 254u) << 23);
           if ((nans >> (4 * nb + 2 * e + g)) & 1u) cm[g] = __uint_as_float(0x7fffffffu);
 #pragma unroll
           for (int ii = 0; ii < 4; ++ii) {

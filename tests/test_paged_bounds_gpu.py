@@ -140,3 +140,89 @@ def test_nan_groups_leave_the_other_rows_exact(fg, n, dtype):
         S.arr[w][2][S.table[i, t // 32], h, t % 32, g] = np.nan
     S.upload(fg)
     _run(fg, S, n, 2, 100, 3)
+
+
+# ---- values whose sizes differ ------------------------------------------------------
+
+def _towards(S, n, q_heads, spread=0.05):
+    """Query rows that all point the same way, per K/V head, and that direction as unit vectors."""
+    d, r = S.d, q_heads // S.heads
+    u = S.rng.normal(size=(S.heads, d))
+    u /= np.linalg.norm(u, axis=1, keepdims=True)
+    x = np.repeat(u * np.sqrt(d), r, axis=0)[None] + spread * S.rng.normal(size=(n, q_heads, d))
+    return torch.as_tensor(x.reshape(n, -1), device="cuda").to(S.dtype), u
+
+
+def _put(S, w, i, t, rows):
+    """Token t of sequence i becomes `rows` [heads][d]."""
+    for a, new in zip(S.arr[w], codec.quantize_g64(np.asarray(rows).astype(np.float16))):
+        a[S.table[i, t // S.ps], :, t % S.ps] = new
+
+
+SHAPES = [(1, 2, 2), (1, 8, 1), (1, 16, 1), (3, 2, 2), (7, 1, 1), (9, 1, 1)]   # rows, query heads, K/V heads: steps
+
+
+@pytest.mark.parametrize("n,qh,h", SHAPES + [(40, 2, 2)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_hidden_tokens_do_not_cost_accuracy(fg, n, qh, h, d):
+    """Values far larger than the rest, behind the window's edge: rows that do not see them are as exact as without."""
+    S = Setup(fg, [1000], h, d, 32, torch.float16, 71)
+    S.arr["v"] = list(codec.quantize_g64((0.01 * S.rng.normal(size=(S.pages, h, 32, d))).astype(np.float16)))
+    first = 1000 - n - 190 + 1                                 # the first token that any row sees
+    for t in (first - 1, first - 3):
+        _put(S, "v", 0, t, 6e4 * np.sign(S.rng.normal(size=(h, d))))
+    S.upload(fg)
+    _run(fg, S, [n], qh, window=190, rows_mean=2)
+
+
+@pytest.mark.parametrize("n,qh,h", [s for s in SHAPES if s[0] > 1] + [(40, 2, 2)])
+def test_a_later_rows_token_does_not_cost_the_earlier_rows(fg, n, qh, h):
+    S = Setup(fg, [1000], h, 128, 32, torch.float16, 72)
+    S.arr["v"] = list(codec.quantize_g64((0.01 * S.rng.normal(size=(S.pages, h, 32, 128))).astype(np.float16)))
+    _put(S, "v", 0, 999, 6e4 * np.sign(S.rng.normal(size=(h, 128))))
+    S.upload(fg)
+    _run(fg, S, [n], qh, rows_mean=2)
+
+
+@pytest.mark.parametrize("n,qh,h", SHAPES + [(40, 2, 2)])
+@pytest.mark.parametrize("at", [3, 500, 990])
+def test_large_values_of_no_weight_do_not_cost_accuracy(fg, n, qh, h, at):
+    """A token that all rows see and none weighs (its score 50 below the others'), with values far larger."""
+    S = Setup(fg, [1000], h, 128, 32, torch.float16, 73)
+    S.arr["v"] = list(codec.quantize_g64((0.01 * S.rng.normal(size=(S.pages, h, 32, 128))).astype(np.float16)))
+    q, u = _towards(S, n, qh)
+    _put(S, "k", 0, at, -50 * u)
+    _put(S, "v", 0, at, 6e4 * np.sign(S.rng.normal(size=(h, 128))))
+    S.upload(fg)
+    _run(fg, S, [n], qh, q=q, rows_mean=2)
+
+
+@pytest.mark.parametrize("n,qh,h", SHAPES)
+def test_large_values_that_lose_their_weight(fg, n, qh, h):
+    """Large values lead until later tokens, whose scores lie 40 above, leave them no weight.  (Steps alone: a chunk rounds
+    K, and scores of 50 are then 0.4 * 50 * sqrt(3 / d) u = 3 u off in the mean.)"""
+    S = Setup(fg, [1000], h, 128, 32, torch.float16, 74)
+    S.arr["v"] = list(codec.quantize_g64((0.01 * S.rng.normal(size=(S.pages, h, 32, 128))).astype(np.float16)))
+    q, u = _towards(S, n, qh)
+    x = S.rng.normal(size=(1000, h, 128)) * 0.5
+    x[200:] += 40 * u
+    x[600:] += 10 * u
+    for t in range(1000):
+        _put(S, "k", 0, t, x[t])
+    _put(S, "v", 0, 5, 6e4 * np.sign(S.rng.normal(size=(h, 128))))
+    S.upload(fg)
+    _run(fg, S, [n], qh, q=q, rows_mean=2)
+
+
+@pytest.mark.parametrize("n", [[2, 9], [8, 16], [1, 300], [5, 70]])
+def test_values_of_two_sizes_in_one_call(fg, n):
+    """The same beside sequences of other numbers of rows."""
+    S = Setup(fg, [1000, 700], 2, 128, 32, torch.float16, 78)
+    S.arr["v"] = list(codec.quantize_g64((0.01 * S.rng.normal(size=(S.pages, 2, 32, 128))).astype(np.float16)))
+    q, u = _towards(S, sum(n), 2)
+    for i, length in enumerate((1000, 700)):
+        for t in (40, length // 2):
+            _put(S, "k", i, t, -50 * u)
+            _put(S, "v", i, t, 6e4 * np.sign(S.rng.normal(size=(2, 128))))
+    S.upload(fg)
+    _run(fg, S, n, 2, q=q, rows_mean=2)
