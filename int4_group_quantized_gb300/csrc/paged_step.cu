@@ -168,29 +168,50 @@ __device__ __forceinline__ void mma_from(float (&d)[4], uint32_t a0, uint32_t a1
 // One query row as this lane's B fragments of each 64-group (dims 16 tig ..
 // 16 tig + 15 of the group, in the order the code words give them: (0, 4),
 // (1, 5) / 16 | (2, 6), (3, 7) / 16), and the sum of the query over this lane's
-// dims.
+// dims.  The row is multiplied by the power of two that takes its largest
+// element into [2^10, 2^11): a sixteenth of an element then loses bits only
+// below 2^-20 of the largest, however small the row is.  undo takes that back.
 template <int NG>
 struct QFrag {
   uint32_t b[NG][4][2];
   float qsum[NG];
+  float undo;
 };
 template <int NG>
-__device__ __forceinline__ void load_q(QFrag<NG>& f, const __half* qrow, int tig) {
+__device__ __forceinline__ void load_q(QFrag<NG>& f, const __half* qrow, int tig, bool there) {
+  uint4 raw[NG][2];
+  uint32_t most = 0;                // of |q| as fp16 bits, two at once
+#pragma unroll
+  for (int g = 0; g < NG; ++g)
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+      raw[g][w] = there ? reinterpret_cast<const uint4*>(qrow + 64 * g + 16 * tig)[w] : make_uint4(0u, 0u, 0u, 0u);
+      const uint32_t x[4] = {raw[g][w].x, raw[g][w].y, raw[g][w].z, raw[g][w].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) most = __vmaxu2(most, x[e] & 0x7fff7fffu);
+    }
+  most = max(most >> 16, most & 0xffffu);
+  most = max(most, __shfl_xor_sync(0xffffffffu, most, 1));
+  most = max(most, __shfl_xor_sync(0xffffffffu, most, 2));
+  // the exponent of the largest (zeros, infinities and NaN stay as they are)
+  const uint32_t e = most == 0 || most >= 0x7c00u ? 127u + 10u : __float_as_uint(__half2float(__ushort_as_half(static_cast<unsigned short>(most)))) >> 23;
+  const float up = __uint_as_float((264u - e) << 23);
+  f.undo = __uint_as_float((e - 10u) << 23);
 #pragma unroll
   for (int g = 0; g < NG; ++g) {
-    const uint4* src = reinterpret_cast<const uint4*>(qrow + 64 * g + 16 * tig);
     f.qsum[g] = 0.0f;
 #pragma unroll
     for (int w = 0; w < 2; ++w) {
-      const uint4 raw = src[w];
-      const float2 d01 = unpack_h2(raw.x), d23 = unpack_h2(raw.y), d45 = unpack_h2(raw.z), d67 = unpack_h2(raw.w);
-      f.b[g][2 * w][0] = pack_h2(d01.x, d45.x);
-      f.b[g][2 * w][1] = pack_h2(d01.y * 0.0625f, d45.y * 0.0625f);
-      f.b[g][2 * w + 1][0] = pack_h2(d23.x, d67.x);
-      f.b[g][2 * w + 1][1] = pack_h2(d23.y * 0.0625f, d67.y * 0.0625f);
+      const float2 up2 = both(up), up16 = both(up * 0.0625f);
+      const float2 d01 = unpack_h2(raw[g][w].x), d23 = unpack_h2(raw[g][w].y), d45 = unpack_h2(raw[g][w].z), d67 = unpack_h2(raw[g][w].w);
+      auto pair = [](float a, float b, float2 by) { const float2 p = mul2(make_float2(a, b), by); return pack_h2(p.x, p.y); };
+      f.b[g][2 * w][0] = pair(d01.x, d45.x, up2);
+      f.b[g][2 * w][1] = pair(d01.y, d45.y, up16);
+      f.b[g][2 * w + 1][0] = pair(d23.x, d67.x, up2);
+      f.b[g][2 * w + 1][1] = pair(d23.y, d67.y, up16);
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const float2 x = unpack_h2(f.b[g][2 * w + e][0]), y = unpack_h2(f.b[g][2 * w + e][1]);
+      for (int h = 0; h < 2; ++h) {
+        const float2 x = unpack_h2(f.b[g][2 * w + h][0]), y = unpack_h2(f.b[g][2 * w + h][1]);
         f.qsum[g] += (x.x + x.y) + 16.0f * (y.x + y.y);
       }
     }
@@ -342,7 +363,7 @@ __global__ void __launch_bounds__(32 * kWarps, kCtasPerSm<NB>) step_kernel(const
   // block) take the same queries again and carry what the rounding of the weights to fp16 left over, so that the two add
   // up to the weights in full.
   bool split = false;
-  const float kc2 = a.scale_log2;
+  float2 kc2[NB];                                // takes scores of queries 2 tig, 2 tig + 1 to base 2
 
   int pn[NB][2];                                 // positions of queries 2 tig, 2 tig + 1 (none: below every key)
 
@@ -359,18 +380,10 @@ __global__ void __launch_bounds__(32 * kWarps, kCtasPerSm<NB>) step_kernel(const
     for (int nb = 0; nb < NB; ++nb) {
       const int n = !split ? 8 * nb + gq : NB == 1 ? gq & 3 : gq;
       QFrag<NG> f;
-      if (n < rows) {
-        const int t = n / a.shape.group;
-        load_q<NG>(f, a.q + static_cast<int64_t>(row0 + t) * a.ldq +
-                          static_cast<int64_t>(h * a.shape.group + n - t * a.shape.group) * D, tig);
-      } else {
-#pragma unroll
-        for (int g = 0; g < NG; ++g) {
-          f.qsum[g] = 0.0f;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) f.b[g][e][0] = f.b[g][e][1] = 0u;
-        }
-      }
+      const int t = n / a.shape.group;
+      load_q<NG>(f, a.q + static_cast<int64_t>(row0 + t) * a.ldq + static_cast<int64_t>(h * a.shape.group + n - t * a.shape.group) * D,
+                 tig, n < rows);
+      kc2[nb] = make_float2(a.scale_log2 * __shfl_sync(0xffffffffu, f.undo, 8 * tig), a.scale_log2 * __shfl_sync(0xffffffffu, f.undo, 8 * tig + 4));
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
         float sum = f.qsum[g];
@@ -481,8 +494,8 @@ __global__ void __launch_bounds__(32 * kWarps, kCtasPerSm<NB>) step_kernel(const
     for (int nb = 0; nb < NB; ++nb) {
       const float x = fmaxf(fmaxf(sc[nb][0][0].x, sc[nb][0][1].x), fmaxf(sc[nb][1][0].x, sc[nb][1][1].x));
       const float y = fmaxf(fmaxf(sc[nb][0][0].y, sc[nb][0][1].y), fmaxf(sc[nb][1][0].y, sc[nb][1][1].y));
-      asks[nb][0] = (x - m[nb][0]) * kc2 > kGrow;   // -inf - -inf: no
-      asks[nb][1] = (y - m[nb][1]) * kc2 > kGrow;
+      asks[nb][0] = (x - m[nb][0]) * kc2[nb].x > kGrow;   // -inf - -inf: no
+      asks[nb][1] = (y - m[nb][1]) * kc2[nb].y > kGrow;
       ask = ask || asks[nb][0] || asks[nb][1];
     }
     if (__any_sync(0xffffffffu, ask)) {
@@ -502,7 +515,7 @@ __global__ void __launch_bounds__(32 * kWarps, kCtasPerSm<NB>) step_kernel(const
         float al[2], grown[2];            // the power of two by which the weights' factor grows with the maximum
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const float up = (nm[e] - m[nb][e]) * kc2;
+          const float up = (nm[e] - m[nb][e]) * (e ? kc2[nb].y : kc2[nb].x);
           al[e] = nm[e] == -INFINITY ? 1.0f : ex2(-up);
           grown[e] = nm[e] == -INFINITY ? 1.0f : __uint_as_float(static_cast<uint32_t>(127 + static_cast<int>(fminf(up, 126.0f))) << 23);
         }
@@ -528,12 +541,12 @@ __global__ void __launch_bounds__(32 * kWarps, kCtasPerSm<NB>) step_kernel(const
     }
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
-      const float2 neg = make_float2(m[nb][0] == -INFINITY ? 0.0f : -m[nb][0] * kc2, m[nb][1] == -INFINITY ? 0.0f : -m[nb][1] * kc2);
+      const float2 neg = make_float2(m[nb][0] == -INFINITY ? 0.0f : -m[nb][0] * kc2[nb].x, m[nb][1] == -INFINITY ? 0.0f : -m[nb][1] * kc2[nb].y);
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf)
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          const float2 x = fma2(sc[nb][hf][r], both(kc2), neg);
+          const float2 x = fma2(sc[nb][hf][r], kc2[nb], neg);
           sc[nb][hf][r] = make_float2(ex2(x.x), ex2(x.y));   // scores become weights
           l[nb] = add2(l[nb], sc[nb][hf][r]);
         }
@@ -731,7 +744,7 @@ __global__ void __launch_bounds__(32 * kWarps, kCtasPerSm<NB>) step_kernel(const
             *reinterpret_cast<float4*>(dst + 64 * g) = make_float4(v[g][0], v[g][1], v[g][2], v[g][3]);
             *reinterpret_cast<float4*>(dst + 64 * g + 4) = make_float4(v[g][4], v[g][5], v[g][6], v[g][7]);
           }
-          if (gq == 0) pl.stat[slot] = make_float2(m[nb][e] * kc2, lsum);
+          if (gq == 0) pl.stat[slot] = make_float2(m[nb][e] * (e ? kc2[nb].y : kc2[nb].x), lsum);
         }
       }
   };

@@ -226,3 +226,15 @@ def test_values_of_two_sizes_in_one_call(fg, n):
             _put(S, "v", i, t, 6e4 * np.sign(S.rng.normal(size=(2, 128))))
     S.upload(fg)
     _run(fg, S, n, 2, q=q, rows_mean=2)
+
+
+@pytest.mark.parametrize("n,qh,h", SHAPES)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("size", [1e-4, 2e-6])
+def test_small_queries(fg, n, qh, h, d, size):
+    """Queries near fp16's smallest numbers against keys near its largest: every bit of q counts."""
+    S = Setup(fg, [300], h, d, 32, torch.float16, 76)
+    S.arr["k"] = list(codec.quantize_g64((1.3e4 * S.rng.normal(size=(S.pages, h, 32, d))).clip(-6e4, 6e4).astype(np.float16)))
+    S.upload(fg)
+    q = _q(S, n, qh, size)
+    _run(fg, S, [n], qh, q=q, rows_mean=2)
