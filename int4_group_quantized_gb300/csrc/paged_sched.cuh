@@ -22,10 +22,10 @@ namespace paged {
 // Sequences with at most this many rows (rows times group) are steps: the
 // warp-level kernel takes them (a warp holds 8 or 16 rows); longer ones go to
 // the tile kernels, whose units are 256 rows.  At 16 rows (8 K/V heads of 128, 4
-// tokens of 4 query heads each): 32 sequences of 4000 tokens 98 us as steps,
-// 122 to 125 as chunks (head_dim 64: 41 and 103); the chunks' kernel is ahead
-// only where there is little to share out: 4 sequences of 500 tokens 22.3 and
-// 20.2 us, one of 30000 76.7 and 53.5.
+// tokens of 4 query heads each): 32 sequences of 4000 tokens 67 us as steps,
+// 122 to 125 as chunks (head_dim 64: 44 and 103), 4 sequences of 500 tokens 15.9
+// and 20.2 us; the chunks' kernel is ahead only for one long sequence (30000
+// tokens 62.7 and 53.5).
 constexpr int kStepRows = 16;
 constexpr int kMaxSplits = 128;   // shares an item may cross (the join reads them one after another)
 

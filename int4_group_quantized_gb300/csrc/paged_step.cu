@@ -66,8 +66,10 @@ using attn::kLoNib;
 constexpr int kTileLog2 = kStepTileLog2;
 constexpr int kTile = 1 << kTileLog2;   // tokens of a tile
 constexpr int kWarps = 4;               // warps of a CTA
+// CTAs an SM.  Two blocks of columns take 255 registers at head_dim 128; in the 168 of three CTAs they spilled 668 bytes:
+// the 16 rows below 67 us for 108 (head_dim 64: 44 for 59), a call of 63 single tokens and a chunk of 512 355 for 549.
 template <int NB>
-constexpr int kCtasPerSm = 3;
+constexpr int kCtasPerSm = NB == 2 ? 2 : 3;
 template <int D, int NB>
 constexpr int kStepStages = D == 128 ? 3 : 4;
 constexpr float kGrow = 12.0f;          // how far (in powers of two) a score may lie above the maximum
