@@ -66,7 +66,13 @@ constexpr int kSoftWarps = 8;      // warps 0..3: rows 0..127, warps 4..7: rows 
 constexpr int kRestoreWarps = 7;   // warps 8..14
 constexpr int kMmaWarp = 15;
 constexpr int kThreads = 16 * 32;
-constexpr float kMostSum = 16384.0f;   // a tile's row sum up to which its weights stand as fp16
+// Weights P = 2^(s - m) with m kLift below the largest score known when m was found: the largest weight of a row is 2^4
+// or more, so that small ones keep their bits down to 2^-18 of it, and thousands of 2^-26 beside one large weight still add
+// up (without the lift they were rounded to zero).  A higher lift leaves less room above a first tile's maximum, and more
+// tiles look for theirs: the mixed batch below 118.0 us with 3 or 4, 118.4 with 5, 124.6 with 6, 140 with 8 (the chunk 457
+// to 458 with any).
+constexpr float kLift = 4.0f;
+constexpr float kMostSum = 60000.0f;   // a tile's row sum up to which its weights stand as fp16; where m is the tile's own, at most 128 * 2^4
 
 template <int D>
 struct Smem {
@@ -700,8 +706,8 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const AttnArgs<__half
           }
           tmem_st_wait();
         }
-        // P = 2^(s - m) for the maximum m known so far.  A segment's first tile finds m; a later one takes it as it is and
-        // looks at the row's sum only: while that stays below 2^14 no weight has left fp16, and a larger maximum changes
+        // P = 2^(s - m) for the m known so far.  A segment's first tile finds m; a later one takes it as it is and
+        // looks at the row's sum only: while that stays below kMostSum no weight has left fp16, and a larger maximum changes
         // nothing but the scale of sums that are divided in the end.  Otherwise (or with no key seen before) the tile finds
         // its maximum, the sums are rescaled, and the weights are formed again.
         uint32_t pk[64];
@@ -723,7 +729,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const AttnArgs<__half
               mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
             }
             // only for a row that asks: its bits do not depend on its neighbours
-            mx = x == 0 || m == -INFINITY || !(lt.x + lt.y <= kMostSum) ? fmaxf(m, mx * a.scale_log2) : m;
+            mx = x == 0 || m == -INFINITY || !(lt.x + lt.y <= kMostSum) ? fmaxf(m, fmaf(mx, a.scale_log2, -kLift)) : m;
             if (x > 0) {
               const float alpha = mx == -INFINITY ? 1.0f : ex2_approx(m - mx);
               l2 = make_float2(l2.x * alpha, l2.y * alpha);

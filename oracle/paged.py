@@ -161,8 +161,8 @@ def attention_bound(q, k, v, pos, window=0, sinks=0, present=None, kind="step"):
       * step: scores are sums of q c, c <= 15, times the scale, and of the minimum times sum q.  The weight w = p scale
         is rounded to fp16 and multiplies c - 8.  Its power of two keeps the largest w of the row and group at 2^4 or
         more, so a small w is off by 2^-25 / 2^4 of the largest;
-      * chunk: K, V and P are rounded to fp16.  The largest P of a row is 2^8 or more, so a small one is off by 2^-33 of
-        the largest;
+      * chunk: K, V and P are rounded to fp16.  The largest P of a row is 2^4 or more, so a small one is off by 2^-25 /
+        2^4 of the largest;
       * f32: no rounding but fp32's own."""
     kv, vv = restore(*k), restore(*v)
     out, mag, work = attention(q, kv, vv, pos, window, sinks, present)
@@ -192,7 +192,7 @@ def attention_bound(q, k, v, pos, window=0, sinks=0, present=None, kind="step"):
     else:
         tiny = 2.0 ** -25 * np.abs(fin(q)).sum(1, keepdims=True) / np.sqrt(d)     # K's subnormals, in the scores
         tol = HALF * (np.abs(out) + 2 * mag) + 2.0 ** -24 + steps * mag + np.expm1(2 * ((HALF + steps) * work + tiny)) * mag
-        tol = tol + n * 2.0 ** -33 * p.max(axis=1, initial=0.0)[:, None] * np.abs(fin(vv)).max(axis=0, initial=0.0)[None]
+        tol = tol + n * 2.0 ** -29 * p.max(axis=1, initial=0.0)[:, None] * np.abs(fin(vv)).max(axis=0, initial=0.0)[None]
     return out, tol
 
 

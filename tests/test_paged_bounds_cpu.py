@@ -25,7 +25,7 @@ def _rounded(q, k, v, pos, window, sinks, kind):
     p = np.exp(s - s.max(axis=1, keepdims=True))
     total = p.sum(axis=1, keepdims=True)
     if kind == "chunk":
-        o = (p * 256).astype(np.float16).astype(np.float64) @ vv / 256
+        o = (p * 16).astype(np.float16).astype(np.float64) @ vv / 16
     else:
         codes = codec.unpack_codes(v[0]).reshape(len(vv), -1, 64).astype(np.float64)
         o = np.zeros((len(q), codes.shape[1], 64))

@@ -238,3 +238,17 @@ def test_small_queries(fg, n, qh, h, d, size):
     S.upload(fg)
     q = _q(S, n, qh, size)
     _run(fg, S, [n], qh, q=q, rows_mean=2)
+
+
+@pytest.mark.parametrize("n,qh,h", SHAPES + [(40, 2, 2), (300, 1, 1)])
+def test_many_small_weights_beside_a_large_one(fg, n, qh, h):
+    """A first token whose score lies 18 above the others' and whose values are zero: the output is the sum of thousands of
+    weights of 2^-26."""
+    S = Setup(fg, [4000], h, 128, 64, torch.float16, 75)
+    S.arr["v"] = list(codec.quantize_g64((60 * (1 + 0.5 * S.rng.normal(size=(S.pages, h, 64, 128)))).astype(np.float16)))
+    S.arr["k"] = list(codec.quantize_g64((0.3 * S.rng.normal(size=(S.pages, h, 64, 128))).astype(np.float16)))
+    q, u = _towards(S, n, qh)
+    _put(S, "k", 0, 0, 18 * u)
+    _put(S, "v", 0, 0, np.zeros((h, 128)))
+    S.upload(fg)
+    _run(fg, S, [n], qh, q=q, rows_mean=2)
