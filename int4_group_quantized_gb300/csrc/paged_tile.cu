@@ -546,7 +546,6 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const AttnArgs<__half
         walk_next(k, a, line);
       }
       mma_commit(done);
-      if (!ok) atomicOr(a.batch.err, DEV_ERR_WAIT_TIMEOUT);
     }
     __syncwarp();
   } else {
@@ -597,7 +596,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const AttnArgs<__half
         cp_async_commit();
       }
       if (rows >= 0) {
-        ok = mbar_wait(&odone[grp], seg & 1, wait_limit, abort_flag);
+        ok = mbar_wait(&odone[grp], seg & 1, kDrainLimit, abort_flag);   // of an MMA that the issuer is at: it gives up, or this comes
         ok = __all_sync(0xffffffffu, ok && !*abort_flag);
         if (!ok) break;
         ++seg;
@@ -796,15 +795,17 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const AttnArgs<__half
       g0 += tiles;
       walk_next(k, a, line);
     }
+    cp_async_wait<0>();   // none is left in flight where a wait ran out
     if (threadIdx.x == 0) pl.rec[w] = rec;
   }
   // ---- teardown: every MMA done, then the tensor memory is freed ------------------------------
   if (warp == kMmaWarp && lane == 0) {
-    volatile int dummy = 0;
-    mbar_wait(done, 0, kDrainLimit, &dummy);
+    volatile int dummy = 0;   // not the flag: a CTA that gave up waits for its MMAs all the same
+    if (!mbar_wait(done, 0, kDrainLimit, &dummy)) *abort_flag = 1;
   }
   tc_fence_before();
   __syncthreads();
+  if (threadIdx.x == 0 && *abort_flag) atomicOr(a.batch.err, DEV_ERR_WAIT_TIMEOUT);   // whichever warp's wait ran out
   if (warp == kMmaWarp) {
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);

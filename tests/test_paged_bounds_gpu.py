@@ -252,3 +252,33 @@ def test_many_small_weights_beside_a_large_one(fg, n, qh, h):
     _put(S, "v", 0, 0, np.zeros((h, 128)))
     S.upload(fg)
     _run(fg, S, [n], qh, q=q, rows_mean=2)
+
+
+# ---- waits --------------------------------------------------------------------------
+
+def test_a_wait_that_runs_out_is_never_silent(fg):
+    """Whatever the limit, a call either reports a wait that ran out or is right."""
+    S = Setup(fg, [700, 300], 2, 128, 64, torch.float16, 77)
+    cu = np.array([0, 600, 700])
+    q = _q(S, 700, 4)
+    want = _attend(fg, S, cu, q, 4)
+    fg.fg_sync_status()
+    seen = set()
+    old = fg.fg_set_wait_limit(0)
+    try:
+        for limit in sorted({int(1.17 ** k) for k in range(75)}):
+            fg.fg_set_wait_limit(limit)
+            for _ in range(4):
+                out = _attend(fg, S, cu, q, 4)
+                try:
+                    fg.fg_sync_status()
+                    assert torch.equal(out, want), f"limit {limit}: wrong, and no status"
+                    seen.add(True)
+                except fg.FGError as e:
+                    assert e.status == 7
+                    seen.add(False)
+    finally:
+        fg.fg_set_wait_limit(old)
+    assert torch.equal(_attend(fg, S, cu, q, 4), want)
+    fg.fg_sync_status()
+    assert seen == {True, False}
