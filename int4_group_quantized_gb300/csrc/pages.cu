@@ -277,7 +277,8 @@ __global__ void free_kernel(const Table t, const int32_t* rows, int n, unsigned 
 // ---- forking ---------------------------------------------------------------------------
 // p.row[dst] = the first fork that names it; p.fork[k] = the source's length,
 // -1 for a fork that is refused.  The copied page of fork k is entry k' of
-// (src, dst), k' counting the forks with a partly filled page before it.
+// (src, dst), k' counting the forks with a page to copy before it: a source
+// whose partly filled page is missing is refused first and takes none.
 __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(const Table t, const int32_t* src, const int32_t* dst,
                                                                  int n, Plan p, unsigned int* err) {
   __shared__ int slots[kPlanWarps];
@@ -299,10 +300,18 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(const Table t, 
     const int a = src[k], b = dst[k];
     const bool ok = in_range(a) && in_range(b) && a != b && p.row[b] == k && t.lens[b] == 0 && t.lens[a] >= 0 &&
                     pages_for(t.lens[a], t.ps_log2) <= t.stride;
-    const int len = ok ? t.lens[a] : -1;
-    p.fork[k] = len;
+    int len = ok ? t.lens[a] : -1;
     if (!ok) atomicOr(err, DEV_ERR_BATCH);
-    mine += (ok && (len & part_mask)) ? 1 : 0;
+    if (ok && (len & part_mask)) {
+      const int page = t.table[a * t.stride + (len >> t.ps_log2)];
+      if (page >= 0 && page < t.pages) {
+        ++mine;
+      } else {
+        atomicOr(err, DEV_ERR_PAGE);
+        len = -1;
+      }
+    }
+    p.fork[k] = len;
   }
   mine = __reduce_add_sync(0xffffffffu, mine);
   int need;
@@ -325,9 +334,9 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(const Table t, 
       bool ok = true;
       if (part) {
         page = from[full];
-        ok = page >= 0 && page < t.pages && kk < nfree && kk < limit;
+        ok = kk < nfree && kk < limit;
         fresh = ok ? p.dst[kk] : -1;
-        if (kk < limit) p.src[kk] = ok ? page : -1;   // -1: nothing to copy
+        if (ok) p.src[kk] = page;
       }
       if (!ok) {
         p.fork[k] = -1;

@@ -282,3 +282,26 @@ def test_a_wait_that_runs_out_is_never_silent(fg):
     assert torch.equal(_attend(fg, S, cu, q, 4), want)
     fg.fg_sync_status()
     assert seen == {True, False}
+
+
+# ---- forks --------------------------------------------------------------------------
+
+def test_a_fork_that_cannot_be_made_takes_no_page(fg):
+    """A source whose last page is missing is refused; the free pages go to the forks that can be made, lowest first."""
+    ps = 16
+    table = np.full((9, 2), -1)
+    table[0, 0], table[1, 0], table[2, :2] = 5, -1, [1, -1]     # sources: whole; no page; a full page and no second
+    lens = np.array([7, 9, 20, 0, 0, 0, 0, 0, 0])
+    refs = np.zeros(8, int)
+    refs[[5, 1, 0, 2, 7]] = 1                                   # free: 3, 4, 6
+    tab = fg.PageTable(_i32(table), _i32(lens), _i32(refs), ps)
+    pool = fg.PagePool(8, ps, 1, 64)
+    pool.k_codes.copy_(torch.arange(8, device="cuda", dtype=torch.uint8).view(8, 1, 1, 1).expand_as(pool.k_codes))
+    fg.fg_pages_fork(tab, fg.PagePools([pool]), _i32([1, 0, 2, 0, 0, 0]), _i32([3, 4, 5, 6, 7, 8]))
+    with pytest.raises(fg.FGError) as e:
+        fg.fg_sync_status()
+    assert e.value.status == 4
+    assert tab.table[:, 0].tolist() == [5, -1, 1, -1, 3, -1, 4, 6, -1]
+    assert tab.lens.tolist() == [7, 9, 20, 0, 7, 0, 7, 7, 0]
+    assert tab.refs.tolist() == [1, 1, 1, 1, 1, 1, 1, 1]
+    assert pool.k_codes[:, 0, 0, 0].tolist() == [0, 1, 2, 5, 5, 5, 5, 7]
