@@ -369,9 +369,12 @@ fg_status launch_attn(const fg_page_pool& pool, const fg_page_table& t, const in
     FG_TRY(paged::launch("plan_kernel", true, half ? plan_kernel<kTileRows, 7> : plan_kernel<kF32Rows, kF32KeysLog2>, 1, threads, 0, st, p));
   }
   if constexpr (half) {
-    // the chunks first: the steps' small CTAs then fill the SMs as the chunks' shares end
+    // One after the other: a kernel reads nothing before those before it are complete.  (Steps that were set up beside the
+    // chunks' last shares and read the plan and the lengths without that wait: 63 single tokens beside a chunk of 512 rows
+    // 355 us for 362, with shared heads 141.5 for 142.5, 100 beside 28 chunks of 20 rows 83.7 for 81; chunks first and the
+    // steps behind them 372, 157 and 95.)
+    if (l.step.workers > 0) FG_TRY(paged_attention_step(a, l.step, pool.head_dim, own_plan, st));
     if (l.tile.workers > 0) FG_TRY(paged_attention_tile(a, l.tile, pool.head_dim, own_plan, l.step.workers == 0, st));
-    if (l.step.workers > 0) FG_TRY(paged_attention_step(a, l.step, pool.head_dim, own_plan, l.tile.workers > 0, st));
     return wide ? join<T, 128, kTileRows>(a, l.step, l.tile, st) : join<T, 64, kTileRows>(a, l.step, l.tile, st);
   } else {
     FG_TRY(paged_attention_f32(a, l.tile, pool.head_dim, own_plan, st));

@@ -23,8 +23,7 @@ struct AttnArgs {
 // own_plan: no plan was made (paged_sched.cuh, make_line).
 // Sequences of at most kStepRows rows per K/V head (fp16).
 int step_workers(int rows, int sms);
-// `after`: launched after the chunks' kernel.
-fg_status paged_attention_step(const AttnArgs<__half>& a, const ClassPlan& pl, int head_dim, bool own_plan, bool after, cudaStream_t st);
+fg_status paged_attention_step(const AttnArgs<__half>& a, const ClassPlan& pl, int head_dim, bool own_plan, cudaStream_t st);
 
 // Longer chunks (fp16) on tcgen05, units of kTileRows rows and tiles of 128 keys; one worker an SM.
 constexpr int kTileRows = 256;

@@ -233,7 +233,7 @@ __device__ __forceinline__ void read_meta(const uint8_t* arr, int t, float (&v)[
 }
 
 template <int D, int NB>
-__global__ void __launch_bounds__(32 * kWarps, kCtasPerSm<NB>) step_kernel(const AttnArgs<__half> a, const ClassPlan pl, const bool own_plan, const bool after) {
+__global__ void __launch_bounds__(32 * kWarps, kCtasPerSm<NB>) step_kernel(const AttnArgs<__half> a, const ClassPlan pl, const bool own_plan) {
   constexpr int NG = D / 64, NT = D / 16;
   using St = Stage<D>;
   constexpr int kStages = kStepStages<D, NB>;
@@ -244,10 +244,7 @@ __global__ void __launch_bounds__(32 * kWarps, kCtasPerSm<NB>) step_kernel(const
   const int w = blockIdx.x * kWarps + warp;
 
   tc::griddep_launch();
-  // After the chunks' kernel, which lets this one begin when all before it is complete, nothing of that kernel is needed
-  // here: the CTAs fill the SMs that it leaves, and the wait is left to the end (so that what follows this kernel follows
-  // that one too).
-  if (!after) tc::griddep_wait();
+  tc::griddep_wait();
   __shared__ OwnPlan own;
   const Line line = own_plan ? make_line<true, kStepRows, kTileLog2>(own, a.tab, a.batch, a.shape, a.pool.heads, pl.workers, false)
                              : Line{pl.pre, pl.head[0], pl.head[1]};
@@ -256,7 +253,6 @@ __global__ void __launch_bounds__(32 * kWarps, kCtasPerSm<NB>) step_kernel(const
   const int64_t o0 = w * per;
   if (o0 >= total) {
     if (lane == 0) pl.rec[w] = make_int4(-1, 0, 0, 0);
-    if (after) tc::griddep_wait();
     return;
   }
   const int heads = a.pool.heads;
@@ -783,7 +779,6 @@ __global__ void __launch_bounds__(32 * kWarps, kCtasPerSm<NB>) step_kernel(const
     if (info.y & kEnd) break;
   }
   if (lane == 0) pl.rec[w] = rec;
-  if (after) tc::griddep_wait();
 }
 
 template <int D, int NB>
@@ -792,7 +787,7 @@ constexpr int step_smem() {
 }
 
 template <int D, int NB>
-fg_status launch(const AttnArgs<__half>& a, const ClassPlan& pl, bool own_plan, bool after, cudaStream_t st) {
+fg_status launch(const AttnArgs<__half>& a, const ClassPlan& pl, bool own_plan, cudaStream_t st) {
   constexpr int bytes = step_smem<D, NB>();
   static bool set[64] = {false};
   int dev = 0;
@@ -803,16 +798,16 @@ fg_status launch(const AttnArgs<__half>& a, const ClassPlan& pl, bool own_plan, 
     set[dev] = true;
   }
   Trace tr(KC_ATTN_PAGED, st);
-  return paged::launch("step_kernel", true, step_kernel<D, NB>, static_cast<unsigned>(pl.workers / kWarps), 32 * kWarps, bytes, st, a, pl, own_plan, after);
+  return paged::launch("step_kernel", true, step_kernel<D, NB>, static_cast<unsigned>(pl.workers / kWarps), 32 * kWarps, bytes, st, a, pl, own_plan);
 }
 
 }  // namespace
 
 int step_workers(int rows, int sms) { return sms * (rows <= 8 ? kCtasPerSm<1> : kCtasPerSm<2>) * kWarps; }
 
-fg_status paged_attention_step(const AttnArgs<__half>& a, const ClassPlan& pl, int head_dim, bool own_plan, bool after, cudaStream_t st) {
-  if (head_dim == 128) return pl.rows <= 8 ? launch<128, 1>(a, pl, own_plan, after, st) : launch<128, 2>(a, pl, own_plan, after, st);
-  return pl.rows <= 8 ? launch<64, 1>(a, pl, own_plan, after, st) : launch<64, 2>(a, pl, own_plan, after, st);
+fg_status paged_attention_step(const AttnArgs<__half>& a, const ClassPlan& pl, int head_dim, bool own_plan, cudaStream_t st) {
+  if (head_dim == 128) return pl.rows <= 8 ? launch<128, 1>(a, pl, own_plan, st) : launch<128, 2>(a, pl, own_plan, st);
+  return pl.rows <= 8 ? launch<64, 1>(a, pl, own_plan, st) : launch<64, 2>(a, pl, own_plan, st);
 }
 
 }  // namespace paged

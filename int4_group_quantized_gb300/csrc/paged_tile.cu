@@ -336,8 +336,8 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const AttnArgs<__half
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  griddep_launch();
   griddep_wait();
-  griddep_launch();   // not before: the steps' kernel begins with the plan and all before it complete
   __shared__ OwnPlan own;
   __shared__ Line line;   // not in registers: it is read between segments only
   {
@@ -824,9 +824,10 @@ fg_status launch(const AttnArgs<__half>& a, const ClassPlan& pl, bool own_plan, 
     set[dev] = true;
   }
   Trace tr(KC_ATTN_PAGED, st);
-  // Not early as a call's first launch: the CTAs then take the SMs in order, so that neighbours in the line share a head's
-  // keys in L2 (a chunk of 2048 rows 452 us, 457 early).
-  return paged::launch("tile_kernel", !own_plan, tile_kernel<D>, static_cast<unsigned>(pl.workers), kThreads, S::kBytes, st, a, pl, wait_limit(), own_plan, every);
+  // Early behind the plan alone.  As a call's first launch or behind the steps the CTAs then would not take the SMs in
+  // order, so that neighbours in the line share a head's keys in L2 (a chunk of 2048 rows 459 us, 464 early; 63 single
+  // tokens beside a chunk of 512 362 and 367).
+  return paged::launch("tile_kernel", every && !own_plan, tile_kernel<D>, static_cast<unsigned>(pl.workers), kThreads, S::kBytes, st, a, pl, wait_limit(), own_plan, every);
 }
 
 }  // namespace
