@@ -413,7 +413,7 @@ fg_status fg_pages_reserve(const fg_page_table* t, const int32_t* cu, void* ws, 
  * shared (refs + 1), a partly filled last page is copied, in all l pools, into
  * a free page, lowest numbered first, fork by fork.  dst rows must be empty
  * (lens 0) and named once (the first of two counts); several forks may share a
- * source.  A fork that cannot be made leaves dst as it was. */
+ * source.  A fork that cannot be made leaves dst as it was and takes no page. */
 fg_status fg_pages_fork(const fg_page_table* t, const fg_page_pool* pools, int32_t l, const int32_t* src,
                         const int32_t* dst, int64_t n, void* ws, size_t ws_bytes, cudaStream_t stream);
 
@@ -447,17 +447,23 @@ fg_status fg_paged_append(const fg_page_pool* pool, const fg_page_table* t, cons
  * [ntok][ldo], same columns; ldq, ldo multiples of 8, 16-byte aligned.  The
  * row at position p sees the tokens j <= p with j > p - window or j < sinks
  * (window 0: all j <= p).  Scores are scaled by 1/sqrt(head_dim); a row that
- * sees nothing gives 0.  Attention reads the values the codes stand for:
- * sequences of at most 16 rows per K/V head (rows times query heads per K/V
- * head: decode steps) use them unrounded; longer chunks of fp16 round them to
- * fp16, the tensor cores' operand; fp32 computes in fp32.  A group whose scale
+ * sees nothing gives 0; so does a row before its sequence's first token (a
+ * chunk of more rows than lens[i]; fg_paged_append reports such rows, attention
+ * does not).  Attention reads the values the codes stand for: sequences of at
+ * most 16 rows per K/V head (rows times query heads per K/V head: decode steps)
+ * use them unrounded, and round a row's weights (softmax weight times scale) to
+ * fp16, with their remainders where there are at most 4 rows (8 when max_q
+ * allows more than 8); longer chunks of fp16 round values and weights to fp16,
+ * the tensor cores' operand; fp32 computes in fp32.  A group whose scale
  * is not finite makes that group's columns NaN for the rows that see it, and
  * for no other.  A missing page's tokens are not seen.
  * max_q bounds the rows of one sequence; longer ones are refused on the device.
  * Results are the same bits every time for one max_q class (up to 8, up to 16,
  * more rows per K/V head); out must not overlap q.
  * Rows outside cu[0] .. cu[seqs] are left as they are.  ws: device, 256-byte
- * aligned, >= fg_paged_attention_workspace_bytes. */
+ * aligned, >= fg_paged_attention_workspace_bytes: about 65 MB at head_dim 128
+ * where max_q allows chunks of fp16 (more than 16 rows per K/V head), 16 to 22 MB
+ * where it does not. */
 size_t fg_paged_attention_workspace_bytes(const fg_page_pool* pool, const fg_page_table* t, int32_t q_heads,
                                           int64_t ntok, int64_t max_q);
 fg_status fg_paged_attention(const fg_page_pool* pool, const fg_page_table* t, const int32_t* cu, const void* q,

@@ -41,10 +41,11 @@
 // TB/s); 8 sequences of 30 to 65 thousand tokens, 8 K/V heads of 128 with 8
 // query heads each 107 us (4.7 TB/s; the copies alone, without the sums, 95);
 // 4 sequences of 100 to 300 tokens, 12 heads of 64 10.7 us, of which the two
-// launches are most.  What bounds a long step: bytes in flight first (12 warps
-// of three stages an SM: 63% of the DRAM's rate), then the integer pipe that
-// masks the nibbles (46%); four warps of three CTAs and three stages were the
-// best of what fits (8 warps x 5 stages 120 us, 11 x 4 122).
+// launches are most.  What bounds a long step are fixed latencies at three warps
+// a scheduler (issue slots 56% used; a warp waits 16 of a tile's 3,200 cycles
+// for copies; DRAM at 64% of its rate), then the integer pipe that masks the
+// nibbles (45%); four warps of three CTAs and three stages were the best of the
+// shapes tried (8 warps x 5 stages 120 us, 11 x 4 122).
 #include <math.h>
 
 #include <algorithm>
@@ -67,7 +68,8 @@ constexpr int kTileLog2 = kStepTileLog2;
 constexpr int kTile = 1 << kTileLog2;   // tokens of a tile
 constexpr int kWarps = 4;               // warps of a CTA
 // CTAs an SM.  Two blocks of columns take 255 registers at head_dim 128; in the 168 of three CTAs they spilled 668 bytes:
-// the 16 rows below 67 us for 108 (head_dim 64: 44 for 59), a call of 63 single tokens and a chunk of 512 355 for 549.
+// 16 rows of 32 sequences of 4000 tokens 67 us for 108 (head_dim 64: 44 for 59), 63 single tokens beside a chunk of 512
+// rows 355 for 549.
 template <int NB>
 constexpr int kCtasPerSm = NB == 2 ? 2 : 3;
 template <int D, int NB>

@@ -32,11 +32,10 @@
 // Every wait is bounded; on timeout the CTA raises the device error word, lets
 // its MMAs finish and frees its tensor memory.
 //
-// Measured: a chunk of 2048 rows over 16384 tokens, 32 heads of 128, 447 to 455
-// us (1.14 PFLOP/s, 60% of what a large bf16 library product reaches); a mixed
-// batch of 12 sequences (1 to 600 rows, 32 query heads on 8, a window of 1000
-// with 4 sinks) 115 to 119 us; 64 chunks of 20 rows over 300 to 600 tokens, 8
-// heads, 63 us.  A tile takes 3400 cycles where its four MMA batches take 2200:
+// Measured: a chunk of 2048 rows over 16384 tokens, 32 heads of 128, 452 to 460
+// us (1.13 PFLOP/s, 59% of what a large bf16 library product reaches); a batch of
+// 12 chunks (7 to 554 rows, 32 query heads on 8, a window of 1000 with 4 sinks)
+// 118 to 119 us; 64 chunks of 20 rows over 300 to 600 tokens, 8 heads, 62 us.  A tile takes 3400 cycles where its four MMA batches take 2200:
 // the protocol with its MMAs alone, no softmax and no restoring, takes 362 us
 // of the chunk's 450; with every exponential replaced by a multiply-add it takes
 // as long, without the restoring's arithmetic 424: a group's S, softmax and P V
@@ -69,7 +68,7 @@ constexpr int kThreads = 16 * 32;
 // Weights P = 2^(s - m) with m kLift below the largest score known when m was found: the largest weight of a row is 2^4
 // or more, so that small ones keep their bits down to 2^-18 of it, and thousands of 2^-26 beside one large weight still add
 // up (without the lift they were rounded to zero).  A higher lift leaves less room above a first tile's maximum, and more
-// tiles look for theirs: the mixed batch below 118.0 us with 3 or 4, 118.4 with 5, 124.6 with 6, 140 with 8 (the chunk 457
+// tiles look for theirs: the 12 chunks above 118.0 us with 3 or 4, 118.4 with 5, 124.6 with 6, 140 with 8 (the chunk 457
 // to 458 with any).
 constexpr float kLift = 4.0f;
 constexpr float kMostSum = 60000.0f;   // a tile's row sum up to which its weights stand as fp16; where m is the tile's own, at most 128 * 2^4
