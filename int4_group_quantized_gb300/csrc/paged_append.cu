@@ -183,7 +183,7 @@ __device__ __noinline__ uint32_t exact_word(X x, float mn, float r) {
 // numbers from that lane.  The bytes are the floor (fp16: 2 read, 0.625 written
 // and 2 more where the restored rows are wanted); half the instructions that
 // could issue do.  fp16 rows therefore come by asynchronous copies a slice
-// ahead, 4 KB a warp and slice: 24 thousand rows of 32 heads of 128 with
+// ahead, 4 KB a warp and slice: 19 thousand rows of 32 heads of 128 with
 // restored rows 162.7 us (4.5 TB/s) where loads into registers took 178; two
 // slices ahead 161.6, three blocks an SM (80 registers, spills) 196.
 template <int NG>

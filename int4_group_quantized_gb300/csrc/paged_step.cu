@@ -15,9 +15,8 @@
 //            p * scale is rounded to fp16 for the MMA after scaling by a power
 //            of two that fits the largest weight of the query, so that small
 //            activations keep their bits; sum w is an MMA against ones, of the
-//            rounded weights.  Where
-//            rows leave half the MMA's columns free (1 to 4; up to 8 when a
-//            call has sequences of more than 8), those carry the rounding's
+//            rounded weights.  Where rows leave half the MMA's columns free (1
+//            to 4; up to 8 when max_q allows more than 8), those carry the rounding's
 //            remainders: the result is then as exact as fp32 sums of unrounded
 //            weights (2.1e-4 of its size off, the fp16 result's own rounding;
 //            otherwise 3.1 to 3.6e-4: for 5 to 8 rows a second MMA beside
