@@ -471,6 +471,127 @@ fg_status fg_paged_attention(const fg_page_pool* pool, const fg_page_table* t, c
                              int64_t sinks, void* out, int64_t ldo, void* ws, size_t ws_bytes,
                              cudaStream_t stream);
 
+/* Reading back what the cache holds, to go on in another form or elsewhere:
+ * row t of sequence i's rows in `cu` receives the token at position
+ * start[i] + t (start: device int32 [seqs]; NULL: the sequence's last rows,
+ * lens[i] - n + t) as the codes stand for it, fmaf(q, scale, min) rounded to
+ * the activations' type, head h at columns h*head_dim.  k, v: device [ntok][ld],
+ * ld a multiple of 8, 16-byte aligned; either may be NULL.  A row whose position
+ * is not below lens[i] (FG_ERR_ARG) or whose page is missing (FG_ERR_CAPACITY)
+ * is left as it is, as are rows outside cu[0] .. cu[seqs]. */
+fg_status fg_paged_read(const fg_page_pool* pool, const fg_page_table* t, const int32_t* cu, const int32_t* start,
+                        void* k, void* v, int64_t ld, int64_t ntok, cudaStream_t stream);
+
+/* ---- rotary positions ---------------------------------------------------------
+ * The notes' layer has no positions of its own; models that rotate queries and
+ * keys do it between the products and the cache.  Pair i of a head, at position
+ * p, turns by p * theta_i:
+ *   (a, b) -> (a c - b s, a s + b c),  c = scale cos(p theta_i), s = scale sin(p theta_i),
+ * c and s rounded to fp32 from about 36 correct bits, the products and their sum
+ * rounded one by one in fp32 (nothing is contracted), then once to the
+ * activations' type.  Only the first `rot` dims of a head are rotated:
+ *   FG_ROTARY_HALF:  pairs (i, i + rot/2);   FG_ROTARY_PAIRS: (2i, 2i + 1).
+ * turns: device uint64 [rot/2], theta_i / 2 pi as a fraction of 2^64: a position
+ * times it wraps exactly, so far positions lose nothing.  The rotation by -p is
+ * the gradient of the one by p: negative positions are allowed in fg_rotate. */
+typedef enum { FG_ROTARY_HALF = 0, FG_ROTARY_PAIRS = 1 } fg_rotary_layout;
+typedef struct {
+  const uint64_t* turns;
+  int32_t rot, layout;
+  float scale;
+} fg_rotary;
+
+/* The turns (host memory, rot/2 of them) and the scale for frequencies
+ * theta_i = base^(-2i/rot), stretched for contexts `factor` times as long:
+ *   PLAIN   theta_i;                          LINEAR  theta_i / factor;
+ *   BASE    base * factor^(rot/(rot-2)) in place of base (rot >= 4);
+ *   BANDS   by the turns t_i = context theta_i / 2 pi of the first context: a
+ *           share clamp((t_i - low)/(high - low), 0, 1) of theta_i, the rest
+ *           theta_i / factor;
+ *   RAMP    by the pair's number: with n(t) = rot ln(context / (2 pi t)) /
+ *           (2 ln base), a = max(0, floor n(high)), z = min(rot - 1, ceil n(low)),
+ *           a share clamp((i - a)/max(z - a, 0.001), 0, 1) of theta_i / factor,
+ *           the rest theta_i, and scale 0.1 ln(factor) + 1 (factor >= 1).
+ * The other kinds have scale 1 and read only the numbers they name (BANDS and
+ * RAMP: 0 < low < high).  rot even, 2 .. 65536; base > 1.  Host only. */
+typedef enum {
+  FG_ROTARY_PLAIN = 0, FG_ROTARY_LINEAR = 1, FG_ROTARY_BASE = 2, FG_ROTARY_BANDS = 3, FG_ROTARY_RAMP = 4
+} fg_rotary_scaling;
+fg_status fg_rotary_turns(int32_t rot, int32_t scaling, double base, double factor, double context, double low,
+                          double high, uint64_t* turns, float* scale);
+
+/* Rotates rows x (device [rows][ldx], `heads` heads of head_dim side by side) to
+ * the positions pos (device int32 [rows]) into out (device [rows][ldo]: x itself
+ * with ldo = ldx, or memory apart from it).  Any even rot <= head_dim; dims past
+ * rot are copied.  Rows that are 16-byte aligned with strides a multiple of 8,
+ * head_dim a multiple of 8 and rot of 16 (HALF) or 8 (PAIRS) move 16 bytes at a
+ * time, others two elements. */
+fg_status fg_rotate(const fg_rotary* r, const void* x, fg_dtype dt, int64_t rows, int64_t ldx, int32_t heads,
+                    int32_t head_dim, const int32_t* pos, void* out, int64_t ldo, cudaStream_t stream);
+
+/* The append of a model with rotary positions, in one launch: q's rows (device
+ * [ntok][ldq], q_heads heads) are rotated to their positions lens[i] - n + t into
+ * q_out (device [ntok][ldqo]; may be q itself), k's rows are rotated, rounded to the
+ * activations' type and stored as fg_paged_append stores them, v's as they are:
+ * the same bits as fg_rotate of q and k and fg_paged_append of the result.
+ * rot a multiple of 16, at most head_dim.  q may be NULL (then q_out is not
+ * read).  A row of q before its sequence's first token is left out with its k. */
+fg_status fg_paged_append_rotated(const fg_page_pool* pool, const fg_page_table* t, const int32_t* cu,
+                                  const fg_rotary* r, const void* q, int64_t ldq, int32_t q_heads, void* q_out,
+                                  int64_t ldqo, const void* k, const void* v, int64_t ld, int64_t ntok,
+                                  void* k_restored, void* v_restored, int64_t ldr, cudaStream_t stream);
+
+/* ---- shared prefixes ----------------------------------------------------------
+ * Forks begin with the same pages.  fg_pages_share finds which sequences of a
+ * batch do, and fg_paged_attention_shared then reads the pages of a group's common
+ * prefix once for all of its rows.
+ *
+ * fg_page_share: device int32, owned by the caller, for a batch of `seqs` sequences
+ * (the table's) and `ntok` rows; groups are numbered by their lowest sequence, the
+ * leader:
+ *   group  [seqs]      the group of a sequence, -1: none
+ *   tokens [seqs]      the leading tokens that its group shares (0: none), full pages
+ *   first  [seqs]      where its rows begin among its group's rows
+ *   leader [seqs]      the leader of a group, -1 past the last group
+ *   begin  [seqs + 1]  where a group's rows begin in `rows` (past the last: their number)
+ *   rows   [ntok]      rows of the batch, group by group, sequence by sequence, -1 past the last */
+typedef struct {
+  int32_t* group;
+  int32_t* tokens;
+  int32_t* first;
+  int32_t* leader;
+  int32_t* begin;
+  int32_t* rows;
+  int64_t seqs, ntok;
+} fg_page_share;
+
+/* Fills s.  A sequence takes part with the full pages that end before its rows of
+ * `cu`; its leader is the lowest-numbered sequence with the same first page.  A
+ * leader and those that have at least P leading entries in common with it form a
+ * group: P is the number that saves the most page reads, P times the followers
+ * that have so many, among numbers of at least min_tokens (>= 1) tokens; the larger
+ * of two that save the same.  Entries that name no page end a prefix.
+ * A share holds until the table's leading entries, the offsets cu or the set of
+ * sequences change: lengths may grow and pages be compacted meanwhile, so steps of an unchanged batch and
+ * all layers use one.  Up to 16384 sequences. */
+size_t fg_pages_share_workspace_bytes(const fg_page_table* t);
+fg_status fg_pages_share(const fg_page_table* t, const int32_t* cu, int64_t min_tokens, const fg_page_share* s, void* ws,
+                         size_t ws_bytes, cudaStream_t stream);
+
+/* fg_paged_attention (without a window) of a batch whose sequences share prefixes
+ * as s says: every group's shared tokens are read once for all its rows, each
+ * sequence's others as before, and the two are joined in fp32.  Results differ from
+ * fg_paged_attention's by roundings only and are the same bits every time for one
+ * max_q class and share.  A sequence whose rows do not all stand behind its
+ * group's tokens is computed by itself, and so is every sequence of an fp32 pool
+ * (fp32 sums on the CUDA cores: the rows' arithmetic, not the cache's bytes, is
+ * their cost).  ws: 256-byte aligned, >= fg_paged_attention_shared_workspace_bytes. */
+size_t fg_paged_attention_shared_workspace_bytes(const fg_page_pool* pool, const fg_page_table* t, int32_t q_heads,
+                                                 int64_t ntok, int64_t max_q);
+fg_status fg_paged_attention_shared(const fg_page_pool* pool, const fg_page_table* t, const int32_t* cu,
+                                    const fg_page_share* s, const void* q, int64_t ldq, int32_t q_heads, int64_t ntok,
+                                    int64_t max_q, void* out, int64_t ldo, void* ws, size_t ws_bytes, cudaStream_t stream);
+
 /* Synchronize `stream`, then report (and clear) the device error word that
  * kernels raise: FG_ERR_DEVICE_TIMEOUT when a bounded wait ran out, else
  * FG_ERR_ARG or FG_ERR_CAPACITY for what a paged call found wrong on the

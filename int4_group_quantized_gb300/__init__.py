@@ -784,3 +784,180 @@ def fg_paged_attention(pool: PagePool, tab: PageTable, cu: torch.Tensor, q: torc
     _check(_lib.fg_paged_attention(_beside(pool, tab)._ref, tab._ref, _ints(cu, tab.seqs + 1, tab, "cu"), q.data_ptr(), ldq, q_heads, n,
                                    max_q, window, sinks, out.data_ptr(), ldo, ws.data_ptr(), ws.numel(), _on(tab, stream)),
            "fg_paged_attention")
+
+
+_sig("fg_paged_read", _INT, _POOL, _TAB, _P, _P, _P, _P, _I64, _I64, _P)
+
+
+def fg_paged_read(pool: PagePool, tab: PageTable, cu: torch.Tensor, k: torch.Tensor | None = None, v: torch.Tensor | None = None,
+                  start: torch.Tensor | None = None, stream=None) -> None:
+    """Fills the ragged batch's rows k, v [ntok][heads*head_dim] (either may be left out) with the cached tokens at positions
+    start[i] .. (int32 [seqs]), or each sequence's last ones, as their codes stand for them."""
+    given = [(t, name) for t, name in ((k, "k"), (v, "v")) if t is not None]
+    if not given:
+        raise ValueError("neither k nor v is given")
+    n, h1 = given[0][0].shape[0], pool.heads * pool.head_dim
+    lds = [_rows(t, pool, n, h1, name) for t, name in given]
+    if lds[0] != lds[-1]:
+        raise ValueError("k and v need one row stride")
+    _check(_lib.fg_paged_read(_beside(pool, tab)._ref, tab._ref, _ints(cu, tab.seqs + 1, tab, "cu"),
+                              None if start is None else _ints(start, tab.seqs, tab, "start"), _ptr(k), _ptr(v), lds[0], n,
+                              _on(tab, stream)), "fg_paged_read")
+
+
+# ---- rotary positions --------------------------------------------------------------
+
+class fg_rotary(ctypes.Structure):
+    _fields_ = [("turns", ctypes.c_void_p), ("rot", ctypes.c_int32), ("layout", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+_ROT = ctypes.POINTER(fg_rotary)
+_F64 = ctypes.c_double
+FG_ROTARY_HALF, FG_ROTARY_PAIRS = 0, 1
+_LAYOUTS = {"half": FG_ROTARY_HALF, "pairs": FG_ROTARY_PAIRS}
+FG_ROTARY_PLAIN, FG_ROTARY_LINEAR, FG_ROTARY_BASE, FG_ROTARY_BANDS, FG_ROTARY_RAMP = range(5)
+_SCALINGS = {"plain": FG_ROTARY_PLAIN, "linear": FG_ROTARY_LINEAR, "base": FG_ROTARY_BASE, "bands": FG_ROTARY_BANDS,
+             "ramp": FG_ROTARY_RAMP}
+_sig("fg_rotary_turns", _INT, _I32, _I32, _F64, _F64, _F64, _F64, _F64, _P, ctypes.POINTER(ctypes.c_float))
+_sig("fg_rotate", _INT, _ROT, _P, _INT, _I64, _I64, _I32, _I32, _P, _P, _I64, _P)
+_sig("fg_paged_append_rotated", _INT, _POOL, _TAB, _P, _ROT, _P, _I64, _I32, _P, _I64, _P, _P, _I64, _I64, _P, _P, _I64, _P)
+
+
+def fg_rotary_turns(rot: int, scaling: int = FG_ROTARY_PLAIN, base: float = 10000.0, factor: float = 1.0, context: float = 0.0,
+                    low: float = 1.0, high: float = 32.0) -> tuple[torch.Tensor, float]:
+    """The turns of the rot/2 pairs, as the 64 bits of an int64 tensor on the CPU, and the scale of cosines and sines."""
+    turns = torch.empty(max(int(rot) // 2, 1), dtype=torch.int64)
+    scale = ctypes.c_float()
+    _check(_lib.fg_rotary_turns(int(rot), int(scaling), base, factor, context, low, high, turns.data_ptr(), ctypes.byref(scale)),
+           "fg_rotary_turns")
+    return turns, scale.value
+
+
+class Rotary:
+    """Rotary positions of the first `rot` dims of a head (fg_rotary): layout "half" or "pairs", scaling "plain", "linear",
+    "base", "bands" or "ramp" (fg_rotary_turns)."""
+
+    def __init__(self, rot: int, layout: str = "half", scaling: str = "plain", base: float = 10000.0, factor: float = 1.0,
+                 context: float = 0.0, low: float = 1.0, high: float = 32.0, device="cuda"):
+        if layout not in _LAYOUTS or scaling not in _SCALINGS:
+            raise ValueError(f"layout {layout!r} is one of {sorted(_LAYOUTS)}, scaling {scaling!r} one of {sorted(_SCALINGS)}")
+        turns, self.scale = fg_rotary_turns(rot, _SCALINGS[scaling], base, factor, context, low, high)
+        self.rot, self.layout = int(rot), layout
+        self.turns = turns.to(device)
+        self.device, self.index = self.turns.device, self.turns.get_device()
+        self._s = fg_rotary(_ptr(self.turns), self.rot, _LAYOUTS[layout], self.scale)
+        self._ref = ctypes.byref(self._s)
+
+    @property
+    def struct(self) -> fg_rotary:
+        return self._s
+
+
+def _rotary_on(rotary: "Rotary", index: int) -> "Rotary":
+    """The rotation, when it lies on that device, the current one."""
+    if rotary.index != index or index < 0 or index != torch._C._cuda_getDevice():
+        raise ValueError(f"the rotation is on {rotary.device}, the rows on device {index}, the current device is "
+                         f"{torch.cuda.current_device()}")
+    return rotary
+
+
+def fg_rotate(rotary: Rotary, x: torch.Tensor, pos: torch.Tensor, heads: int, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """out (x itself where None) = rows x [n][heads*head_dim] rotated to positions pos (int32 [n]); by -pos for gradients."""
+    out = x if out is None else out
+    if x.dim() != 2 or heads < 1 or x.shape[1] % heads:
+        raise ValueError(f"x: expected rows [n][heads*head_dim] of {heads} heads, got {tuple(x.shape)}")
+    n, cols = x.shape
+    if out.shape != x.shape or out.dtype is not x.dtype or out.device != x.device:
+        raise ValueError(f"out: expected {x.dtype} {tuple(x.shape)} on {x.device}, got {out.dtype} {tuple(out.shape)} on {out.device}")
+    if pos.dtype is not torch.int32 or tuple(pos.shape) != (n,) or not pos.is_contiguous() or pos.device != x.device:
+        raise ValueError(f"pos: expected {n} contiguous int32 on {x.device}, got {pos.dtype} {tuple(pos.shape)} on {pos.device}")
+    if cols > 1 and (x.stride(1) != 1 or out.stride(1) != 1):
+        raise ValueError("columns must be adjacent")
+    ldx, ldo = (x.stride(0), out.stride(0)) if n > 1 else (cols, cols)
+    i = x.get_device()
+    ref = _rotary_on(rotary, i)._ref
+    st = torch._C._cuda_getCurrentRawStream(i) if stream is None else _stream(stream)
+    _check(_lib.fg_rotate(ref, x.data_ptr(), _dt(x), n, ldx, heads, cols // heads, pos.data_ptr(), out.data_ptr(), ldo, st), "fg_rotate")
+    return out
+
+
+def fg_paged_append_rotated(pool: PagePool, tab: PageTable, cu: torch.Tensor, rotary: Rotary, q: torch.Tensor | None, q_heads: int,
+                            q_out: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, k_restored: torch.Tensor | None = None,
+                            v_restored: torch.Tensor | None = None, stream=None) -> None:
+    """fg_rotate of the ragged batch's queries (into q_out; q itself where None) and keys to their positions, and
+    fg_paged_append of the keys and values, in one launch."""
+    h1 = pool.heads * pool.head_dim
+    n = k.shape[0]
+    ld, ldr, ldq, ldqo = _rows(k, pool, n, h1, "k"), 0, 0, 0
+    if _rows(v, pool, n, h1, "v") != ld:
+        raise ValueError("k and v need one row stride")
+    if q is not None:
+        q_out = q if q_out is None else q_out
+        ldq, ldqo = _rows(q, pool, n, q_heads * pool.head_dim, "q"), _rows(q_out, pool, n, q_heads * pool.head_dim, "q_out")
+    if k_restored is not None and v_restored is not None:
+        ldr = _rows(k_restored, pool, n, h1, "k_restored")
+        if _rows(v_restored, pool, n, h1, "v_restored") != ldr:
+            raise ValueError("k_restored and v_restored need one row stride")
+    ref = _rotary_on(rotary, tab.index)._ref
+    _check(_lib.fg_paged_append_rotated(_beside(pool, tab)._ref, tab._ref, _ints(cu, tab.seqs + 1, tab, "cu"), ref, _ptr(q), ldq,
+                                        q_heads, _ptr(q_out), ldqo, k.data_ptr(), v.data_ptr(), ld, n, _ptr(k_restored),
+                                        _ptr(v_restored), ldr, _on(tab, stream)), "fg_paged_append_rotated")
+
+
+# ---- shared prefixes ---------------------------------------------------------------
+
+class fg_page_share(ctypes.Structure):
+    _fields_ = [("group", ctypes.c_void_p), ("tokens", ctypes.c_void_p), ("first", ctypes.c_void_p),
+                ("leader", ctypes.c_void_p), ("begin", ctypes.c_void_p), ("rows", ctypes.c_void_p),
+                ("seqs", ctypes.c_int64), ("ntok", ctypes.c_int64)]
+
+
+_SHARE = ctypes.POINTER(fg_page_share)
+_sig("fg_pages_share_workspace_bytes", _SZ, _TAB)
+_sig("fg_pages_share", _INT, _TAB, _P, _I64, _SHARE, _P, _SZ, _P)
+
+
+class PageShare:
+    """Which sequences share leading pages (fg_page_share): int32 tensors group, tokens, first, leader [seqs], begin [seqs+1]
+    and rows [ntok] (kept, not copied)."""
+
+    def __init__(self, group: torch.Tensor, tokens: torch.Tensor, first: torch.Tensor, leader: torch.Tensor, begin: torch.Tensor,
+                 rows: torch.Tensor):
+        if group.dim() != 1 or rows.dim() != 1:
+            raise ValueError("group is [seqs], rows [ntok]")
+        self.device, self.index = group.device, group.get_device()
+        self.seqs, self.ntok = int(group.shape[0]), int(rows.shape[0])
+        for name, t, n in (("group", group, self.seqs), ("tokens", tokens, self.seqs), ("first", first, self.seqs),
+                           ("leader", leader, self.seqs), ("begin", begin, self.seqs + 1), ("rows", rows, self.ntok)):
+            setattr(self, name, _dense(t, torch.int32, (n,), self.device, name))
+        self._s = fg_page_share(_ptr(group), _ptr(tokens), _ptr(first), _ptr(leader), _ptr(begin), _ptr(rows), self.seqs, self.ntok)
+        self._ref = ctypes.byref(self._s)
+
+    @staticmethod
+    def empty(tab: PageTable, ntok: int) -> "PageShare":
+        """A share of no groups, for a batch of ntok rows."""
+        def ints(n, fill):
+            return torch.full((n,), fill, dtype=torch.int32, device=tab.device)
+        return PageShare(ints(tab.seqs, -1), ints(tab.seqs, 0), ints(tab.seqs, 0), ints(tab.seqs, -1), ints(tab.seqs + 1, 0), ints(ntok, -1))
+
+    @property
+    def struct(self) -> fg_page_share:
+        return self._s
+
+
+def _share_on(share: "PageShare", tab: "PageTable") -> "PageShare":
+    if share.index != tab.index:
+        raise ValueError(f"the share is on {share.device}, the page table on {tab.device}")
+    return share
+
+
+def fg_pages_share_workspace_bytes(tab: PageTable) -> int:
+    return _lib.fg_pages_share_workspace_bytes(tab._ref)
+
+
+def fg_pages_share(tab: PageTable, cu: torch.Tensor, share: PageShare, min_tokens: int = 256, ws: torch.Tensor | None = None,
+                   stream=None) -> None:
+    """Fills share: the groups of sequences whose rows of cu stand behind at least min_tokens common leading tokens."""
+    ws = _paged_ws(ws, fg_pages_share_workspace_bytes(tab) if ws is None else 0, tab, stream)
+    _check(_lib.fg_pages_share(tab._ref, _ints(cu, tab.seqs + 1, tab, "cu"), int(min_tokens), _share_on(share, tab)._ref, _ptr(ws),
+                               ws.numel(), _on(tab, stream)), "fg_pages_share")

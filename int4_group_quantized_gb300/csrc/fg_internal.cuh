@@ -62,6 +62,8 @@ enum KernelClass : int {
   KC_ATTN_PAGED_PLAN,
   KC_PAGES_PLAN,
   KC_PAGES_COPY,
+  KC_ROTATE,
+  KC_PAGED_READ,
   KC_COUNT
 };
 constexpr int kProfilePhases = 4;
@@ -191,6 +193,9 @@ fg_status prefill_attention(const fg_kv& kv, const void* q, int64_t ldq, int64_t
                             void* out, int64_t ldo, cudaStream_t st);
 fg_status prefill_attention_simt(const fg_kv& kv, const void* q, int64_t ldq, int64_t b, int64_t s,
                                  void* out, int64_t ldo, cudaStream_t st);
+
+// ---- rotary positions ------------------------------------------------------
+fg_status check_rotary(const fg_rotary* r, int32_t head_dim);
 
 // ---- codec -----------------------------------------------------------------
 fg_status quantize_rows(const void* x, fg_dtype dt, int64_t rows, int64_t cols, uint8_t* codes,

@@ -110,6 +110,7 @@ fg_status launch(const char* what, bool early, void (*kernel)(P...), unsigned gr
 fg_status check_pool(const fg_page_pool* p);
 fg_status check_table(const fg_page_table* t);
 fg_status check_pool_table(const fg_page_pool* p, const fg_page_table* t);
+fg_status check_share(const fg_page_share* s, const fg_page_table* t, int64_t ntok);
 Pool pool_of(const fg_page_pool& p);
 Table table_of(const fg_page_table& t);
 

@@ -1,0 +1,265 @@
+// Rotary positions of rows: the frequencies (host) and the rotation.
+//
+// Bound by the rows' bytes, read and written once.  A block takes a few rows:
+// their cosines and sines go into shared memory once for all heads, a thread
+// then moves 16 bytes of each half (or 16 bytes of neighbouring pairs).
+#include <math.h>
+
+#include <algorithm>
+
+#include "fg_internal.cuh"
+#include "rotary.cuh"
+#include "tc_ptx.cuh"
+
+namespace fg {
+namespace {
+
+using namespace rotary;
+
+constexpr int kThreads = 256;
+constexpr int kMostRot = 65536;
+
+__device__ __forceinline__ void load8(const float* p, float2 (&v)[4]) {
+  const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+  v[0] = make_float2(a.x, a.y);
+  v[1] = make_float2(a.z, a.w);
+  v[2] = make_float2(b.x, b.y);
+  v[3] = make_float2(b.z, b.w);
+}
+__device__ __forceinline__ void load8(const __half* p, float2 (&v)[4]) {
+  const uint4 r = *reinterpret_cast<const uint4*>(p);
+  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) v[e] = __half22float2(*reinterpret_cast<const __half2*>(&w[e]));
+}
+__device__ __forceinline__ void store8(float* p, const float2 (&v)[4]) {
+  *reinterpret_cast<float4*>(p) = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
+  *reinterpret_cast<float4*>(p + 4) = make_float4(v[2].x, v[2].y, v[3].x, v[3].y);
+}
+__device__ __forceinline__ void store8(__half* p, const float2 (&v)[4]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const __half2 h = __float22half2_rn(v[e]);
+    w[e] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ float get(const float* p) { return *p; }
+__device__ __forceinline__ float get(const __half* p) { return __half2float(*p); }
+__device__ __forceinline__ void put(float* p, float v) { *p = v; }
+__device__ __forceinline__ void put(__half* p, float v) { *p = __float2half_rn(v); }
+
+template <typename T>
+struct RotateArgs {
+  const T* x;
+  T* out;
+  const int32_t* pos;
+  const uint64_t* turns;
+  int64_t rows, ldx, ldo;
+  int heads, d, rot;
+  float scale;
+  int part;        // heads of a block
+  bool copy;       // the dims past rot go to out
+};
+
+// 16 bytes at a time.  kRows rows and `part` heads a block; a head has rot / 16
+// pieces that turn (HALF: eight dims of each half; PAIRS: 16 dims side by side) and,
+// where out is other memory, (d - rot) / 8 that are copied.
+constexpr int kRows = 4;
+template <typename T, bool HALF>
+__global__ void __launch_bounds__(kThreads) rotate_kernel(const RotateArgs<T> a) {
+  extern __shared__ __align__(16) float cs[];   // [kRows][cosines, sines][rot / 2]
+  tc::griddep_launch();
+  tc::griddep_wait();
+  const int pairs = a.rot / 2;
+  const int parts = (a.heads + a.part - 1) / a.part;
+  const int64_t row0 = blockIdx.x / parts * static_cast<int64_t>(kRows);
+  const int h0 = static_cast<int>(blockIdx.x % parts) * a.part;
+  const int rows = static_cast<int>(a.rows - row0 < kRows ? a.rows - row0 : kRows), heads = min(a.part, a.heads - h0);
+  for (int i = threadIdx.x; i < rows * pairs; i += kThreads) {
+    const int r = i / pairs, p = i - r * pairs;
+    const float2 v = cos_sin(phase_of(a.pos[row0 + r], a.turns[p]), a.scale);
+    cs[2 * r * pairs + p] = v.x;
+    cs[(2 * r + 1) * pairs + p] = v.y;
+  }
+  __syncthreads();
+  const int turn = HALF ? a.rot / 16 : a.rot / 8, per = turn + (a.copy ? (a.d - a.rot) / 8 : 0);
+  const int items = rows * heads * per;
+#pragma unroll 2
+  for (int i = threadIdx.x; i < items; i += kThreads) {
+    const int rh = i / per, j = i - rh * per, r = rh / heads, h = h0 + rh - r * heads;
+    const T* x = a.x + (row0 + r) * a.ldx + static_cast<int64_t>(h) * a.d;
+    T* out = a.out + (row0 + r) * a.ldo + static_cast<int64_t>(h) * a.d;
+    float2 u[4], v[4];
+    if (j >= turn) {
+      const int at = a.rot + 8 * (j - turn);
+      load8(x + at, u);
+      store8(out + at, u);
+      continue;
+    }
+    const float* c = cs + 2 * r * pairs;
+    const float* s = c + pairs;
+    if (HALF) {
+      load8(x + 8 * j, u);
+      load8(x + pairs + 8 * j, v);
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        turn2(u[e], v[e], *reinterpret_cast<const float2*>(c + 8 * j + 2 * e), *reinterpret_cast<const float2*>(s + 8 * j + 2 * e));
+      store8(out + 8 * j, u);
+      store8(out + pairs + 8 * j, v);
+    } else {
+      load8(x + 8 * j, u);
+#pragma unroll
+      for (int e = 0; e < 4; e += 2) {
+        float2 p = make_float2(u[e].x, u[e + 1].x), q = make_float2(u[e].y, u[e + 1].y);
+        turn2(p, q, *reinterpret_cast<const float2*>(c + 4 * j + e), *reinterpret_cast<const float2*>(s + 4 * j + e));
+        u[e] = make_float2(p.x, q.x);
+        u[e + 1] = make_float2(p.y, q.y);
+      }
+      store8(out + 8 * j, u);
+    }
+  }
+}
+
+// Any strides and any even rot: a thread a pair, or an element past rot, of
+// one row and head.
+template <typename T, bool HALF>
+__global__ void __launch_bounds__(kThreads) rotate_any_kernel(const RotateArgs<T> a) {
+  tc::griddep_launch();
+  tc::griddep_wait();
+  const int pairs = a.rot / 2, per = pairs + (a.copy ? a.d - a.rot : 0);
+  const int64_t items = a.rows * per;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < items; i += static_cast<int64_t>(gridDim.x) * kThreads) {
+    const int64_t r = i / per;
+    const int j = static_cast<int>(i - r * per);
+    const T* x = a.x + r * a.ldx;
+    T* out = a.out + r * a.ldo;
+    if (j >= pairs) {
+      for (int h = 0; h < a.heads; ++h) out[static_cast<int64_t>(h) * a.d + a.rot + j - pairs] = x[static_cast<int64_t>(h) * a.d + a.rot + j - pairs];
+      continue;
+    }
+    const float2 v = cos_sin(phase_of(a.pos[r], a.turns[j]), a.scale);
+    for (int h = 0; h < a.heads; ++h) {
+      const int64_t p = static_cast<int64_t>(h) * a.d + (HALF ? j : 2 * j), q = p + (HALF ? pairs : 1);
+      float u = get(x + p), w = get(x + q);
+      turn1(u, w, v.x, v.y);
+      put(out + p, u);
+      put(out + q, w);
+    }
+  }
+}
+
+template <class... P, class... A>
+fg_status launch(const char* what, void (*kernel)(P...), unsigned grid, size_t smem, cudaStream_t st, A&&... args) {
+  cudaLaunchAttribute pdl[1];
+  pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  pdl[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = pdl;
+  cfg.numAttrs = 1;
+  Trace tr(KC_ROTATE, st);
+  cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+  return check_launch(what);
+}
+
+template <typename T>
+fg_status rotate(const fg_rotary& r, const void* x, int64_t rows, int64_t ldx, int32_t heads, int32_t d, const int32_t* pos, void* out,
+                 int64_t ldo, cudaStream_t st) {
+  RotateArgs<T> a{static_cast<const T*>(x), static_cast<T*>(out), pos, r.turns, rows, ldx, ldo, heads, d, r.rot, r.scale, heads, x != out && r.rot < d};
+  const bool half = r.layout == FG_ROTARY_HALF;
+  const size_t smem = static_cast<size_t>(kRows) * r.rot * sizeof(float);
+  const int64_t blocks = (rows + kRows - 1) / kRows, sms = num_sms();
+  if (d % 8 == 0 && r.rot % (half ? 16 : 8) == 0 && ldx % 8 == 0 && ldo % 8 == 0 && aligned(x, 16) && aligned(out, 16) && smem <= 48 * 1024 &&
+      static_cast<int64_t>(heads) * d <= (1 << 28)) {
+    // few rows: the heads of a block of rows go to as many blocks as give every SM two
+    const int64_t parts = std::min<int64_t>(heads, std::max<int64_t>(1, 2 * sms / blocks));
+    a.part = static_cast<int>((heads + parts - 1) / parts);
+    const int64_t grid = blocks * ((heads + a.part - 1) / a.part);
+    if (grid <= INT32_MAX)
+      return launch("rotate_kernel", half ? rotate_kernel<T, true> : rotate_kernel<T, false>, static_cast<unsigned>(grid), smem, st, a);
+  }
+  const int64_t items = rows * (r.rot / 2 + (a.copy ? d - r.rot : 0));
+  const int64_t grid = std::min<int64_t>((items + kThreads - 1) / kThreads, sms * 16);
+  return launch("rotate_any_kernel", half ? rotate_any_kernel<T, true> : rotate_any_kernel<T, false>, static_cast<unsigned>(grid), 0, st, a);
+}
+
+}  // namespace
+
+fg_status check_rotary(const fg_rotary* r, int32_t head_dim) {
+  if (!r) return fail(FG_ERR_ARG, "null rotation");
+  if (!r->turns) return fail(FG_ERR_ARG, "rotation: null turns");
+  if (!aligned(r->turns, 8)) return fail(FG_ERR_ALIGN, "rotation: turns need 8-byte alignment");
+  if (r->layout != FG_ROTARY_HALF && r->layout != FG_ROTARY_PAIRS) return fail(FG_ERR_ARG, "rotation: layout %d", r->layout);
+  if (r->rot < 2 || r->rot % 2 || r->rot > head_dim) return fail(FG_ERR_SHAPE, "rotation of %d of %d dims", r->rot, head_dim);
+  if (!(fabsf(r->scale) < INFINITY)) return fail(FG_ERR_ARG, "rotation: scale");
+  return FG_OK;
+}
+
+}  // namespace fg
+
+using namespace fg;
+
+extern "C" {
+
+fg_status fg_rotary_turns(int32_t rot, int32_t scaling, double base, double factor, double context, double low, double high,
+                          uint64_t* turns, float* scale) {
+  constexpr double kTau = 6.28318530717958647692;
+  if (!turns || !scale) return fail(FG_ERR_ARG, "null pointer");
+  if (scaling < FG_ROTARY_PLAIN || scaling > FG_ROTARY_RAMP) return fail(FG_ERR_ARG, "scaling %d", scaling);
+  if (rot < 2 || rot % 2 || rot > kMostRot) return fail(FG_ERR_SHAPE, "rotation of %d dims", rot);
+  if (!(base > 1.0 && base < INFINITY)) return fail(FG_ERR_ARG, "base %g", base);
+  const bool banded = scaling == FG_ROTARY_BANDS || scaling == FG_ROTARY_RAMP;
+  if (scaling != FG_ROTARY_PLAIN && !(factor > 0.0 && factor < INFINITY)) return fail(FG_ERR_ARG, "factor %g", factor);
+  if (scaling == FG_ROTARY_RAMP && factor < 1.0) return fail(FG_ERR_ARG, "factor %g below 1", factor);
+  if (scaling == FG_ROTARY_BASE && rot < 4) return fail(FG_ERR_SHAPE, "a rotation of two dims has no other base");
+  if (banded && !(context > 0.0 && context < INFINITY && low > 0.0 && low < high && high < INFINITY))
+    return fail(FG_ERR_ARG, "context %g, low %g, high %g", context, low, high);
+  double from = 0.0, to = 0.0;
+  if (scaling == FG_ROTARY_BASE) base *= pow(factor, static_cast<double>(rot) / (rot - 2));
+  if (scaling == FG_ROTARY_RAMP) {
+    auto pair_of = [&](double t) { return rot * log(context / (kTau * t)) / (2.0 * log(base)); };
+    from = std::max(0.0, floor(pair_of(high)));
+    to = std::min(rot - 1.0, ceil(pair_of(low)));
+  }
+  for (int i = 0; i < rot / 2; ++i) {
+    double f = pow(base, -2.0 * i / rot);
+    double share = 1.0;   // of f, the rest of f / factor
+    if (scaling == FG_ROTARY_LINEAR) share = 0.0;
+    if (scaling == FG_ROTARY_BANDS) share = std::min(1.0, std::max(0.0, (context * f / kTau - low) / (high - low)));
+    if (scaling == FG_ROTARY_RAMP) share = 1.0 - std::min(1.0, std::max(0.0, (i - from) / std::max(to - from, 0.001)));
+    if (share < 1.0) f = share * f + (1.0 - share) * (f / factor);
+    const double t = f / kTau, part = rint(ldexp(t - floor(t), 64));
+    turns[i] = part >= 18446744073709551616.0 ? 0 : static_cast<uint64_t>(part);
+  }
+  *scale = scaling == FG_ROTARY_RAMP ? static_cast<float>(0.1 * log(factor) + 1.0) : 1.0f;
+  return FG_OK;
+}
+
+fg_status fg_rotate(const fg_rotary* r, const void* x, fg_dtype dt, int64_t rows, int64_t ldx, int32_t heads, int32_t head_dim,
+                    const int32_t* pos, void* out, int64_t ldo, cudaStream_t stream) {
+  if (dt != FG_F16 && dt != FG_F32) return fail(FG_ERR_ARG, "dtype");
+  if (rows < 0 || heads < 0 || head_dim < 0) return fail(FG_ERR_ARG, "negative sizes");
+  if (head_dim > kMostRot || heads > 65535 || rows > (int64_t(1) << 40)) return fail(FG_ERR_UNSUPPORTED, "more than 65536 dims, 65535 heads or 2^40 rows");
+  FG_TRY(check_rotary(r, head_dim));
+  if (rows == 0 || heads == 0) return FG_OK;
+  if (!x || !out || !pos) return fail(FG_ERR_ARG, "null pointer");
+  const int64_t h1 = static_cast<int64_t>(heads) * head_dim;
+  if (rows > 1 && (ldx < h1 || ldo < h1)) return fail(FG_ERR_SHAPE, "row stride below heads * head_dim = %lld", (long long)h1);
+  if (!aligned(x, dtype_bytes(dt)) || !aligned(out, dtype_bytes(dt)) || !aligned(pos, 4)) return fail(FG_ERR_ALIGN, "rows or positions");
+  const char *xb = static_cast<const char*>(x), *ob = static_cast<const char*>(out);
+  const int64_t e = static_cast<int64_t>(dtype_bytes(dt)), xn = ((rows - 1) * ldx + h1) * e, on = ((rows - 1) * ldo + h1) * e;
+  // columns of one buffer's rows may lie side by side
+  const int64_t row = ldx * e, off = rows > 1 && ldx == ldo ? ((ob - xb) % row + row) % row : 0;
+  const bool beside = off >= h1 * e && row - off >= h1 * e;
+  if (x == out ? (rows > 1 && ldx != ldo) : (xb < ob + on && ob < xb + xn && !beside))
+    return fail(FG_ERR_ARG, "out is x itself, with its row stride, or memory apart from it");
+  if (dt == FG_F16) return rotate<__half>(*r, x, rows, ldx, heads, head_dim, pos, out, ldo, stream);
+  return rotate<float>(*r, x, rows, ldx, heads, head_dim, pos, out, ldo, stream);
+}
+
+}  // extern "C"

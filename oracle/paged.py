@@ -211,3 +211,51 @@ def off_by_too_much(got, ref, tol, rms=None):
         if e > rms * w + 2.0 ** -25:
             return f"rms error {e / w:.3g} > {rms:.3g}"
     return None
+
+
+# ---- shared prefixes ---------------------------------------------------------------
+
+def share(table, lens, cu, pages, ps, min_tokens):
+    """Groups of sequences that share leading pages: (group, tokens, first, leader, begin, rows), one sequence after another.
+    A sequence takes part with the full pages before its rows; its leader is the lowest one with the same first page; a
+    group shares the P >= min_tokens / ps that saves the most page reads, the larger of two that save the same."""
+    seqs, stride = table.shape
+    n = np.diff(cu)
+
+    def usable(i):
+        k = 0 if n[i] <= 0 else min(max(int(lens[i]) - int(n[i]), 0) // ps, stride)
+        for j in range(k):
+            if not 0 <= table[i, j] < pages:
+                return j
+        return k
+
+    use = [usable(i) for i in range(seqs)]
+    group, tokens, first = np.full(seqs, -1), np.zeros(seqs, int), np.zeros(seqs, int)
+    leaders, members = [], []
+    for lead in range(seqs):
+        if use[lead] == 0 or any(use[j] and table[j, 0] == table[lead, 0] for j in range(lead)):
+            continue
+        common = {}
+        for i in range(lead + 1, seqs):
+            if use[i] and table[i, 0] == table[lead, 0]:
+                c = 0
+                while c < min(use[i], use[lead]) and table[i, c] == table[lead, c]:
+                    c += 1
+                common[i] = c
+        best = (0, 0)
+        for p in set(common.values()):
+            if p * ps >= min_tokens:
+                best = max(best, (p * sum(c >= p for c in common.values()), p))
+        if best[0]:
+            leaders.append(lead)
+            members.append([lead] + [i for i, c in common.items() if c >= best[1]])
+            for i in members[-1]:
+                group[i], tokens[i] = len(leaders) - 1, best[1] * ps
+    begin, rows = [0], []
+    for m in members:
+        for i in m:
+            first[i] = len(rows) - begin[-1]
+            rows += range(int(cu[i]), int(cu[i + 1]))
+        begin.append(len(rows))
+    pad = lambda x, k, fill: np.array(list(x) + [fill] * (k - len(x)), dtype=int)
+    return group, tokens, first, pad(leaders, seqs, -1), pad(begin, seqs + 1, len(rows)), pad(rows, int(cu[-1]), -1)
