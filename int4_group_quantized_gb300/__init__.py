@@ -961,3 +961,24 @@ def fg_pages_share(tab: PageTable, cu: torch.Tensor, share: PageShare, min_token
     ws = _paged_ws(ws, fg_pages_share_workspace_bytes(tab) if ws is None else 0, tab, stream)
     _check(_lib.fg_pages_share(tab._ref, _ints(cu, tab.seqs + 1, tab, "cu"), int(min_tokens), _share_on(share, tab)._ref, _ptr(ws),
                                ws.numel(), _on(tab, stream)), "fg_pages_share")
+
+
+_sig("fg_paged_attention_shared_workspace_bytes", _SZ, _POOL, _TAB, _I32, _I64, _I64)
+_sig("fg_paged_attention_shared", _INT, _POOL, _TAB, _P, _SHARE, _P, _I64, _I32, _I64, _I64, _P, _I64, _P, _SZ, _P)
+
+
+def fg_paged_attention_shared_workspace_bytes(pool: PagePool, tab: PageTable, q_heads: int, ntok: int, max_q: int) -> int:
+    return _lib.fg_paged_attention_shared_workspace_bytes(pool._ref, tab._ref, int(q_heads), int(ntok), int(max_q))
+
+
+def fg_paged_attention_shared(pool: PagePool, tab: PageTable, cu: torch.Tensor, share: PageShare, q: torch.Tensor, q_heads: int,
+                              out: torch.Tensor, max_q: int, ws: torch.Tensor | None = None, stream=None) -> None:
+    """fg_paged_attention of the ragged batch (without a window), with the tokens that share's groups have in common read once
+    for all of a group's rows."""
+    n = q.shape[0]
+    ldq = _rows(q, pool, n, q_heads * pool.head_dim, "q")
+    ldo = _rows(out, pool, n, q_heads * pool.head_dim, "out")
+    ws = _paged_ws(ws, fg_paged_attention_shared_workspace_bytes(pool, tab, q_heads, n, max_q) if ws is None else 0, tab, stream)
+    _check(_lib.fg_paged_attention_shared(_beside(pool, tab)._ref, tab._ref, _ints(cu, tab.seqs + 1, tab, "cu"),
+                                          _share_on(share, tab)._ref, q.data_ptr(), ldq, q_heads, n, max_q, out.data_ptr(), ldo,
+                                          ws.data_ptr(), ws.numel(), _on(tab, stream)), "fg_paged_attention_shared")

@@ -25,6 +25,7 @@ struct Table {
   int32_t* refs;
   int seqs, pages, ps_log2;
   int64_t stride;
+  const int32_t* skip;  // leading tokens of a sequence that are attended to elsewhere (shared prefixes), or null
 };
 
 // A ragged batch: rows cu[i] .. cu[i+1]-1 belong to sequence i.
@@ -45,17 +46,23 @@ inline int log2_of(int ps) {
 // DEV_ERR_BATCH.
 struct Seq {
   int row0, n, len, keys;   // len as stored; keys = min(len, stride * ps)
+  int off;                  // first entry of its table row that counts
 };
+// SKIP: the sequence without its first t.skip[i] tokens (full pages, before its rows): lengths, positions and entries are
+// counted from there.
+template <bool SKIP = false>
 __device__ __forceinline__ Seq seq_of(const Table& t, const Batch& b, int i) {
   Seq s;
   const int a = b.cu[i], e = b.cu[i + 1];
   const int len = t.lens[i];
   const bool ok = a >= 0 && e >= a && e <= b.ntok && len >= 0;
   if (!ok) atomicOr(b.err, DEV_ERR_BATCH);
+  const int skip = SKIP && ok ? t.skip[i] : 0;
   s.row0 = ok ? a : 0;
   s.n = ok ? e - a : 0;
-  s.len = ok ? len : 0;
-  const int64_t cap = t.stride << t.ps_log2;
+  s.len = ok ? len - skip : 0;
+  s.off = skip >> t.ps_log2;
+  const int64_t cap = (t.stride << t.ps_log2) - skip;
   s.keys = s.len > cap ? static_cast<int>(cap) : s.len;
   if (s.n > 0 && s.len > cap) atomicOr(b.err, DEV_ERR_PAGE);
   return s;

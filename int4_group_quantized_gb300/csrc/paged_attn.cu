@@ -9,8 +9,10 @@
 #include <string.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "paged_attn.cuh"
+#include "paged_prefix.cuh"
 #include "tc_ptx.cuh"
 
 namespace fg {
@@ -39,7 +41,7 @@ struct PlanArgs {
   ClassPlan step, tile;   // a class with no workers is not used
 };
 
-template <int TRU, int TKTL>
+template <int TRU, int TKTL, bool SKIP>
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
   __shared__ int64_t warp_sum[2][32];
   __shared__ int warp_max[2][32];
@@ -86,7 +88,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
       const int i = i0 + lane;
       int64_t cost[2] = {0, 0};
       bool tall = false;
-      Seq s{0, 0, 0, 0};
+      Seq s{0, 0, 0, 0, 0};
       if (pass == 1 && i < end) {
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
@@ -95,7 +97,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
         }
       }
       if (pass == 0 && i < end) {
-        s = seq_of(a.tab, a.batch, i);
+        s = seq_of<SKIP>(a.tab, a.batch, i);
         if (s.n > a.shape.max_q) {
           atomicOr(a.batch.err, DEV_ERR_BATCH);
           s.n = 0;
@@ -114,8 +116,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
       while (todo) {
         const int src = __ffs(todo) - 1;
         todo &= todo - 1;
-        Seq t;
-        t.row0 = 0;
+        Seq t{0, 0, 0, 0, 0};
         t.n = __shfl_sync(0xffffffffu, s.n, src);
         t.len = __shfl_sync(0xffffffffu, s.len, src);
         t.keys = __shfl_sync(0xffffffffu, s.keys, src);
@@ -298,6 +299,8 @@ inline size_t up(size_t x) { return (x + 255) / 256 * 256; }
 
 struct Layout {
   ClassPlan step, tile;
+  Prefix prefix;     // of a call beside shared prefixes
+  int32_t* skip;
   size_t bytes;
 };
 void carve_class(ClassPlan& c, char*& p, int64_t seqs, int head_dim, int workers, int most, int rows) {
@@ -316,7 +319,7 @@ void carve_class(ClassPlan& c, char*& p, int64_t seqs, int head_dim, int workers
   p += up(8 * static_cast<size_t>(most) * rows * head_dim);
 }
 // The classes that a call of at most max_q rows a sequence can need.
-Layout layout_of(const fg_page_pool& pool, const fg_page_table& t, int32_t q_heads, int64_t max_q, void* ws, int sms) {
+Layout layout_of(const fg_page_pool& pool, const fg_page_table& t, int32_t q_heads, int64_t max_q, void* ws, int sms, int64_t shared_rows = -1) {
   Layout l;
   const int64_t group = q_heads / pool.heads, most = std::min<int64_t>(max_q, INT32_MAX) * group;
   char* p = static_cast<char*>(ws);
@@ -330,6 +333,22 @@ Layout layout_of(const fg_page_pool& pool, const fg_page_table& t, int32_t q_hea
     carve_class(l.tile, p, t.seqs, pool.head_dim, f32_workers(pool.head_dim, sms), f32_workers(pool.head_dim, kMaxSms), kF32Rows);
   else if (most > (l.step.workers ? kStepRows : 0))
     carve_class(l.tile, p, t.seqs, pool.head_dim, sms, kMaxSms, kTileRows);
+  memset(&l.prefix, 0, sizeof(l.prefix));
+  l.skip = nullptr;
+  if (shared_rows >= 0) {
+    const size_t pairs = static_cast<size_t>(shared_rows) * q_heads, d = pool.head_dim;
+    auto take = [&](auto*& x, size_t bytes) {
+      x = reinterpret_cast<std::remove_reference_t<decltype(x)>>(p);
+      p += up(bytes);
+    };
+    take(l.skip, 4 * static_cast<size_t>(t.seqs));
+    take(l.prefix.info, sizeof(PrefixGroup) * static_cast<size_t>(t.seqs));
+    take(l.prefix.per, 8);
+    take(l.prefix.home_stat, 8 * pairs);
+    take(l.prefix.extra_stat, 8 * static_cast<size_t>(kMaxSms) * kPrefixRows);
+    take(l.prefix.home, 4 * pairs * d);
+    take(l.prefix.extra, 4 * static_cast<size_t>(kMaxSms) * kPrefixRows * d);
+  }
   l.bytes = static_cast<size_t>(p - static_cast<char*>(ws)) + 256;
   return l;
 }
@@ -337,7 +356,7 @@ Layout layout_of(const fg_page_pool& pool, const fg_page_table& t, int32_t q_hea
 template <typename T>
 fg_status launch_attn(const fg_page_pool& pool, const fg_page_table& t, const int32_t* cu, const void* q, int64_t ldq,
                       int32_t q_heads, int64_t ntok, int64_t max_q, int64_t window, int64_t sinks, void* out,
-                      int64_t ldo, void* ws, unsigned int* err, cudaStream_t st) {
+                      int64_t ldo, void* ws, unsigned int* err, cudaStream_t st, const fg_page_share* share = nullptr) {
   AttnArgs<T> a;
   a.pool = pool_of(pool);
   a.tab = table_of(t);
@@ -355,8 +374,18 @@ fg_status launch_attn(const fg_page_pool& pool, const fg_page_table& t, const in
   // positions are below 2^31: a wider window hides nothing
   a.shape.window = window > (int64_t(1) << 30) ? 0 : static_cast<int>(window);
   a.shape.sinks = static_cast<int>(std::min<int64_t>(sinks, int64_t(1) << 30));
-  const Layout l = layout_of(pool, t, q_heads, max_q, ws, std::min(num_sms(), kMaxSms));
+  const Layout l = layout_of(pool, t, q_heads, max_q, ws, std::min(num_sms(), kMaxSms), share ? ntok : -1);
   constexpr bool half = sizeof(T) == 2;
+  a.prefix = l.prefix;
+  if constexpr (half) {
+    if (share) {
+      a.prefix.group = share->group;
+      a.prefix.first = share->first;
+      const PrefixArgs p{a, share->tokens, share->leader, share->begin, share->rows, l.skip, std::min(num_sms(), kMaxSms)};
+      FG_TRY(paged_prefix(p, pool.head_dim, st));
+      a.tab.skip = l.skip;
+    }
+  }
   const bool wide = pool.head_dim == 128;
   const bool own_plan = t.seqs <= kOwnPlan;
   if (!own_plan) {
@@ -366,7 +395,8 @@ fg_status launch_attn(const fg_page_pool& pool, const fg_page_table& t, const in
     // for steps alone a lane a sequence (129: 33.1 us, 34.5 with all)
     const unsigned lanes = static_cast<unsigned>(std::min<int64_t>(kPlanThreads, (t.seqs + 31) / 32 * 32));
     const unsigned threads = l.tile.workers > 0 ? kPlanThreads : lanes;
-    FG_TRY(paged::launch("plan_kernel", true, half ? plan_kernel<kTileRows, 7> : plan_kernel<kF32Rows, kF32KeysLog2>, 1, threads, 0, st, p));
+    const auto plan = !half ? plan_kernel<kF32Rows, kF32KeysLog2, false> : a.tab.skip ? plan_kernel<kTileRows, 7, true> : plan_kernel<kTileRows, 7, false>;
+    FG_TRY(paged::launch("plan_kernel", true, plan, 1, threads, 0, st, p));
   }
   if constexpr (half) {
     // One after the other: a kernel reads nothing before those before it are complete.  (Steps that were set up beside the
@@ -395,6 +425,15 @@ fg_status check_attn(const fg_page_pool* pool, const fg_page_table* t, int32_t q
   return FG_OK;
 }
 
+fg_status check_rows(const fg_page_pool* pool, const int32_t* cu, const void* q, int64_t ldq, int32_t q_heads, const void* out, int64_t ldo) {
+  if (!cu || !q || !out) return fail(FG_ERR_ARG, "null pointer");
+  const int64_t h1 = static_cast<int64_t>(q_heads) * pool->head_dim;
+  if (ldq < h1 || ldo < h1) return fail(FG_ERR_SHAPE, "row stride below q_heads * head_dim = %lld", (long long)h1);
+  if (!aligned(cu, 4) || !aligned(q, 16) || !aligned(out, 16) || ldq % 8 || ldo % 8)
+    return fail(FG_ERR_ALIGN, "q and out need 16-byte alignment and strides that are multiples of 8");
+  return FG_OK;
+}
+
 }  // namespace
 }  // namespace paged
 }  // namespace fg
@@ -416,11 +455,7 @@ fg_status fg_paged_attention(const fg_page_pool* pool, const fg_page_table* t, c
   FG_TRY(check_attn(pool, t, q_heads, ntok, max_q));
   if (window < 0 || sinks < 0) return fail(FG_ERR_ARG, "negative window or sinks");
   if (ntok == 0 || max_q == 0 || t->seqs == 0) return FG_OK;
-  if (!cu || !q || !out) return fail(FG_ERR_ARG, "null pointer");
-  const int64_t h1 = static_cast<int64_t>(q_heads) * pool->head_dim;
-  if (ldq < h1 || ldo < h1) return fail(FG_ERR_SHAPE, "row stride below q_heads * head_dim = %lld", (long long)h1);
-  if (!aligned(cu, 4) || !aligned(q, 16) || !aligned(out, 16) || ldq % 8 || ldo % 8)
-    return fail(FG_ERR_ALIGN, "q and out need 16-byte alignment and strides that are multiples of 8");
+  FG_TRY(check_rows(pool, cu, q, ldq, q_heads, out, ldo));
   const size_t need = fg_paged_attention_workspace_bytes(pool, t, q_heads, ntok, max_q);
   if (!ws || ws_bytes < need) return fail(FG_ERR_WORKSPACE, "paged attention needs %zu workspace bytes", need);
   if (!aligned(ws, 256)) return fail(FG_ERR_ALIGN, "workspace needs 256-byte alignment");
@@ -429,6 +464,30 @@ fg_status fg_paged_attention(const fg_page_pool* pool, const fg_page_table* t, c
   if (pool->dtype == FG_F16)
     return launch_attn<__half>(*pool, *t, cu, q, ldq, q_heads, ntok, max_q, window, sinks, out, ldo, ws, err, stream);
   return launch_attn<float>(*pool, *t, cu, q, ldq, q_heads, ntok, max_q, window, sinks, out, ldo, ws, err, stream);
+}
+
+size_t fg_paged_attention_shared_workspace_bytes(const fg_page_pool* pool, const fg_page_table* t, int32_t q_heads, int64_t ntok,
+                                                 int64_t max_q) {
+  if (check_attn(pool, t, q_heads, ntok, max_q) != FG_OK) return 0;
+  return layout_of(*pool, *t, q_heads, max_q, nullptr, kMaxSms, pool->dtype == FG_F16 ? ntok : -1).bytes;
+}
+
+fg_status fg_paged_attention_shared(const fg_page_pool* pool, const fg_page_table* t, const int32_t* cu, const fg_page_share* s,
+                                    const void* q, int64_t ldq, int32_t q_heads, int64_t ntok, int64_t max_q, void* out, int64_t ldo,
+                                    void* ws, size_t ws_bytes, cudaStream_t stream) {
+  FG_TRY(check_attn(pool, t, q_heads, ntok, max_q));
+  if (!s) return fail(FG_ERR_ARG, "null share");
+  if (ntok == 0 || max_q == 0 || t->seqs == 0) return FG_OK;
+  FG_TRY(check_share(s, t, ntok));
+  if (pool->dtype == FG_F32)   // the rows' arithmetic is the cost: every sequence by itself
+    return fg_paged_attention(pool, t, cu, q, ldq, q_heads, ntok, max_q, 0, 0, out, ldo, ws, ws_bytes, stream);
+  FG_TRY(check_rows(pool, cu, q, ldq, q_heads, out, ldo));
+  const size_t need = fg_paged_attention_shared_workspace_bytes(pool, t, q_heads, ntok, max_q);
+  if (!ws || ws_bytes < need) return fail(FG_ERR_WORKSPACE, "shared paged attention needs %zu workspace bytes", need);
+  if (!aligned(ws, 256)) return fail(FG_ERR_ALIGN, "workspace needs 256-byte alignment");
+  unsigned int* err = device_error_word();
+  if (!err) return fail(FG_ERR_CUDA, "device error word");
+  return launch_attn<__half>(*pool, *t, cu, q, ldq, q_heads, ntok, max_q, 0, 0, out, ldo, ws, err, stream, s);
 }
 
 }  // extern "C"

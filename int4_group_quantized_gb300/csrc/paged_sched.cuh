@@ -140,7 +140,7 @@ struct OwnPlan {
   int64_t per;
   int longest;
 };
-template <bool STEP, int RU, int KTL>
+template <bool STEP, int RU, int KTL, bool SKIP = false>
 __device__ __forceinline__ Line make_line(OwnPlan& o, const Table& t, const Batch& b, const AttnShape& sh, int heads, int workers,
                                           bool every) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
@@ -148,9 +148,9 @@ __device__ __forceinline__ Line make_line(OwnPlan& o, const Table& t, const Batc
   __syncthreads();
   for (int i0 = warp; i0 < t.seqs; i0 += 32 * nw) {   // a lane a sequence, the warps in turn (a warp counts its chunks one by one)
     const int i = i0 + nw * lane;
-    Seq s{0, 0, 0, 0};
+    Seq s{0, 0, 0, 0, 0};
     if (i < t.seqs) {
-      s = seq_of(t, b, i);
+      s = seq_of<SKIP>(t, b, i);
       if (s.n > sh.max_q) {
         if (blockIdx.x == 0) atomicOr(b.err, DEV_ERR_BATCH);
         s.n = 0;
@@ -168,7 +168,7 @@ __device__ __forceinline__ Line make_line(OwnPlan& o, const Table& t, const Batc
       while (todo) {                                       // a chunk's units: the lanes together
         const int src = __ffs(todo) - 1;
         todo &= todo - 1;
-        Seq c{0, 0, 0, 0};
+        Seq c{0, 0, 0, 0, 0};
         c.n = __shfl_sync(0xffffffffu, s.n, src);
         c.len = __shfl_sync(0xffffffffu, s.len, src);
         c.keys = __shfl_sync(0xffffffffu, s.keys, src);

@@ -233,7 +233,7 @@ __device__ __forceinline__ void read_meta(const uint8_t* arr, int t, float (&v)[
   }
 }
 
-template <int D, int NB>
+template <int D, int NB, bool SHARED>
 __global__ void __launch_bounds__(32 * kWarps, kCtasPerSm<NB>) step_kernel(const AttnArgs<__half> a, const ClassPlan pl, const bool own_plan) {
   constexpr int NG = D / 64, NT = D / 16;
   using St = Stage<D>;
@@ -247,7 +247,7 @@ __global__ void __launch_bounds__(32 * kWarps, kCtasPerSm<NB>) step_kernel(const
   tc::griddep_launch();
   tc::griddep_wait();
   __shared__ OwnPlan own;
-  const Line line = own_plan ? make_line<true, kStepRows, kTileLog2>(own, a.tab, a.batch, a.shape, a.pool.heads, pl.workers, false)
+  const Line line = own_plan ? make_line<true, kStepRows, kTileLog2, SHARED>(own, a.tab, a.batch, a.shape, a.pool.heads, pl.workers, false)
                              : Line{pl.pre, pl.head[0], pl.head[1]};
   const int64_t* const pre = line.pre;
   const int64_t total = line.total, per = line.per;
@@ -278,7 +278,7 @@ __global__ void __launch_bounds__(32 * kWarps, kCtasPerSm<NB>) step_kernel(const
     if (k >= mine) return;
     const int64_t o = o0 + k;
     while (pre[t_i + 1] <= o) ++t_i;
-    const Seq s = seq_of(a.tab, a.batch, t_i);
+    const Seq s = seq_of<SHARED>(a.tab, a.batch, t_i);
     const Span sp = span_of<kTileLog2>(s.len - s.n, s.len - 1, s.keys, a.shape.window, a.shape.sinks);
     const int64_t in = o - pre[t_i];
     t_h = in <= INT32_MAX ? static_cast<int>(in) / sp.n : static_cast<int>(in / sp.n);
@@ -288,7 +288,7 @@ __global__ void __launch_bounds__(32 * kWarps, kCtasPerSm<NB>) step_kernel(const
     // page of the 16 tokens from t on (-1: none, or nothing of them is seen)
     auto page_at = [&](int t) {
       if (t > last || (t + 15 < lo_key && t >= a.shape.sinks)) return -1;
-      const int page = a.tab.table[t_i * a.tab.stride + (t >> psl)];   // t <= last < keys: the row reaches that far
+      const int page = a.tab.table[t_i * a.tab.stride + s.off + (t >> psl)];   // t <= last < keys: the row reaches that far
       if (static_cast<uint32_t>(page) < static_cast<uint32_t>(a.tab.pages)) return page;
       atomicOr(a.batch.err, DEV_ERR_PAGE);
       return -1;
@@ -369,7 +369,7 @@ __global__ void __launch_bounds__(32 * kWarps, kCtasPerSm<NB>) step_kernel(const
   auto begin_item = [&](const uint8_t* s) {
     const int4 info = *reinterpret_cast<const int4*>(s + St::kInfo);
     const int h = info.z;
-    const Seq sq = seq_of(a.tab, a.batch, info.w);
+    const Seq sq = seq_of<SHARED>(a.tab, a.batch, info.w);
     rows = sq.n * a.shape.group;
     split = rows <= 4 * NB;
     row0 = sq.row0;
@@ -687,9 +687,38 @@ __global__ void __launch_bounds__(32 * kWarps, kCtasPerSm<NB>) step_kernel(const
       }
     }
   };
+  // the parts that row n's shared prefix left (paged_prefix.cu) come to its own sums, in order
+  auto join_prefix = [&](float (&v)[NG][8], float& most, float& sum, int seq, int h, int n) {
+    const int t = n / a.shape.group;
+    const PrefixParts pp = prefix_parts(a.prefix, seq, t, h, n - t * a.shape.group, a.shape.group, a.q_heads);
+    float2 st = a.prefix.home_stat[pp.home];
+    const float* x = a.prefix.home + pp.home * D;
+    for (int k = 0;; ++k) {
+      const float top = fmaxf(most, st.x), base = top == -INFINITY ? 0.0f : top;
+      const float fa = exp2f(most - base), fb = exp2f(st.x - base);
+      sum = sum * fa + st.y * fb;
+#pragma unroll
+      for (int g = 0; g < NG; ++g)
+#pragma unroll
+        for (int c = 0; c < 8; c += 4) {
+          const float4 y = *reinterpret_cast<const float4*>(x + 64 * g + 8 * gq + c);
+          v[g][c] = fmaf(y.x, fb, v[g][c] * fa);
+          v[g][c + 1] = fmaf(y.y, fb, v[g][c + 1] * fa);
+          v[g][c + 2] = fmaf(y.z, fb, v[g][c + 2] * fa);
+          v[g][c + 3] = fmaf(y.w, fb, v[g][c + 3] * fa);
+        }
+      most = top;
+      if (k == pp.count) break;
+      const int64_t at = static_cast<int64_t>(pp.w0 + k) * kPrefixRows + pp.row;
+      st = a.prefix.extra_stat[at];
+      x = a.prefix.extra + at * D;
+    }
+  };
   // the item's rows, finished (one share) or as this share's partial
   auto end_item = [&](const uint8_t* s, bool from_start, bool to_end) {
-    const int h = reinterpret_cast<const int4*>(s + St::kInfo)->z;
+    const int4 about = *reinterpret_cast<const int4*>(s + St::kInfo);
+    const int h = about.z, seq = about.w;
+    const bool prefixed = SHARED && a.tab.skip[seq] > 0;
 #pragma unroll
     for (int o = 4; o < 32; o <<= 1) nans |= __shfl_xor_sync(0xffffffffu, nans, o);
     if (split) {   // the weights' remainders
@@ -714,7 +743,7 @@ __global__ void __launch_bounds__(32 * kWarps, kCtasPerSm<NB>) step_kernel(const
         const int n = 8 * nb + 2 * tig + e;
         if (n >= rows) continue;
         const bool whole = from_start && to_end;
-        const float f = !whole ? 1.0f : lsum == 0.0f ? 0.0f : 1.0f / lsum;
+        float f = SHARED || !whole ? 1.0f : lsum == 0.0f ? 0.0f : 1.0f / lsum;
         float v[NG][8];
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
@@ -726,6 +755,15 @@ __global__ void __launch_bounds__(32 * kWarps, kCtasPerSm<NB>) step_kernel(const
             v[g][2 * ii] = fmaf(acc[nb][4 * g + ii][e], un, cm[g]) * f;
             v[g][2 * ii + 1] = fmaf(acc[nb][4 * g + ii][2 + e], 0.0625f * un, cm[g]) * f;
           }
+        }
+        float most = m[nb][e] * (e ? kc2[nb].y : kc2[nb].x);
+        if (SHARED) {
+          if (prefixed && from_start) join_prefix(v, most, lsum, seq, h, n);
+          f = !whole ? 1.0f : lsum == 0.0f ? 0.0f : 1.0f / lsum;
+#pragma unroll
+          for (int g = 0; g < NG; ++g)
+#pragma unroll
+            for (int c = 0; c < 8; ++c) v[g][c] *= f;
         }
         if (whole) {
           const int t = n / a.shape.group;
@@ -743,7 +781,7 @@ __global__ void __launch_bounds__(32 * kWarps, kCtasPerSm<NB>) step_kernel(const
             *reinterpret_cast<float4*>(dst + 64 * g) = make_float4(v[g][0], v[g][1], v[g][2], v[g][3]);
             *reinterpret_cast<float4*>(dst + 64 * g + 4) = make_float4(v[g][4], v[g][5], v[g][6], v[g][7]);
           }
-          if (gq == 0) pl.stat[slot] = make_float2(m[nb][e] * (e ? kc2[nb].y : kc2[nb].x), lsum);
+          if (gq == 0) pl.stat[slot] = make_float2(most, lsum);
         }
       }
   };
@@ -787,19 +825,24 @@ constexpr int step_smem() {
   return kWarps * kStepStages<D, NB> * Stage<D>::kBytes;
 }
 
-template <int D, int NB>
-fg_status launch(const AttnArgs<__half>& a, const ClassPlan& pl, bool own_plan, cudaStream_t st) {
+template <int D, int NB, bool SHARED>
+fg_status launch_kernel(const AttnArgs<__half>& a, const ClassPlan& pl, bool own_plan, cudaStream_t st) {
   constexpr int bytes = step_smem<D, NB>();
   static bool set[64] = {false};
   int dev = 0;
   cudaGetDevice(&dev);
   if (bytes > 48 * 1024 && dev >= 0 && dev < 64 && !set[dev]) {
-    if (cudaFuncSetAttribute(step_kernel<D, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
+    if (cudaFuncSetAttribute(step_kernel<D, NB, SHARED>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
       return check_launch("step_kernel smem attribute");
     set[dev] = true;
   }
   Trace tr(KC_ATTN_PAGED, st);
-  return paged::launch("step_kernel", true, step_kernel<D, NB>, static_cast<unsigned>(pl.workers / kWarps), 32 * kWarps, bytes, st, a, pl, own_plan);
+  return paged::launch("step_kernel", true, step_kernel<D, NB, SHARED>, static_cast<unsigned>(pl.workers / kWarps), 32 * kWarps, bytes, st, a, pl, own_plan);
+}
+
+template <int D, int NB>
+fg_status launch(const AttnArgs<__half>& a, const ClassPlan& pl, bool own_plan, cudaStream_t st) {
+  return a.tab.skip != nullptr ? launch_kernel<D, NB, true>(a, pl, own_plan, st) : launch_kernel<D, NB, false>(a, pl, own_plan, st);
 }
 
 }  // namespace

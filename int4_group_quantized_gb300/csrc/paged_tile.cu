@@ -100,12 +100,14 @@ __device__ __forceinline__ void walk_unit(Walk& k, const AttnArgs<__half>& a) {
   k.un = unit_of<kRows>(k.s, a.shape.group, k.u);
   k.sp = span_of<kKeysLog2>(k.un.p0, k.un.p1, k.s.keys, a.shape.window, a.shape.sinks);
 }
+template <bool SHARED>
 __device__ __forceinline__ void walk_seq(Walk& k, const AttnArgs<__half>& a) {
-  k.s = seq_of(a.tab, a.batch, k.i);
+  k.s = seq_of<SHARED>(a.tab, a.batch, k.i);
   k.units = static_cast<int>((static_cast<int64_t>(k.s.n) * a.shape.group + kRows - 1) / kRows);
   k.u = 0;
 }
 // Share w's first segment (left = 0: none).
+template <bool SHARED>
 __device__ __forceinline__ void walk_begin(Walk& k, const AttnArgs<__half>& a, const Line& pl, int w) {
   const int64_t total = pl.total, per = pl.per, o0 = w * per;
   k.left = 0;
@@ -118,7 +120,7 @@ __device__ __forceinline__ void walk_begin(Walk& k, const AttnArgs<__half>& a, c
   }
   k.i = lo;
   k.left = static_cast<int>(total - o0 < per ? total - o0 : per);
-  walk_seq(k, a);
+  walk_seq<SHARED>(k, a);
   const int64_t all = pl.pre[lo + 1] - pl.pre[lo], in = o0 - pl.pre[lo];   // (32-bit divisions where they do: the short ones)
   const int64_t cost = all <= INT32_MAX ? static_cast<int>(all) / a.pool.heads : all / a.pool.heads;
   k.h = all <= INT32_MAX ? static_cast<int>(in) / static_cast<int>(cost) : static_cast<int>(in / cost);
@@ -148,6 +150,7 @@ __device__ __forceinline__ void walk_begin(Walk& k, const AttnArgs<__half>& a, c
   k.x1 = k.x + (k.left < k.sp.n - k.x ? k.left : k.sp.n - k.x);
 }
 // On to the next segment.
+template <bool SHARED>
 __device__ __forceinline__ void walk_next(Walk& k, const AttnArgs<__half>& a, const Line& pl) {
   k.left -= k.x1 - k.x;
   if (k.left == 0) return;
@@ -157,7 +160,7 @@ __device__ __forceinline__ void walk_next(Walk& k, const AttnArgs<__half>& a, co
       do ++k.i;
       while (pl.pre[k.i + 1] == pl.pre[k.i]);
       k.h = 0;
-      walk_seq(k, a);
+      walk_seq<SHARED>(k, a);
     }
   }
   walk_unit(k, a);
@@ -283,7 +286,7 @@ __device__ __forceinline__ void load_meta(float (&v)[NG], const float* base, uin
   }
 }
 
-template <int D>
+template <int D, bool SHARED>
 __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const AttnArgs<__half> a, const ClassPlan pl, uint32_t wait_limit, const bool own_plan, const bool every) {
   using S = Smem<D>;
   constexpr int NG = D / 64;
@@ -340,14 +343,14 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const AttnArgs<__half
   __shared__ OwnPlan own;
   __shared__ Line line;   // not in registers: it is read between segments only
   {
-    const Line x = own_plan ? make_line<false, kRows, kKeysLog2>(own, a.tab, a.batch, a.shape, a.pool.heads, pl.workers, every)
+    const Line x = own_plan ? make_line<false, kRows, kKeysLog2, SHARED>(own, a.tab, a.batch, a.shape, a.pool.heads, pl.workers, every)
                             : Line{pl.pre, pl.head[0], pl.head[1]};
     if (threadIdx.x == 0) line = x;
     __syncthreads();
   }
 
   Walk k;
-  walk_begin(k, a, line, w);
+  walk_begin<SHARED>(k, a, line, w);
 
   if (warp >= kSoftWarps && warp < kSoftWarps + kRestoreWarps) {
     // ---- restoring warps: task n is K (n % 8 < 4) or V of 32 keys of tile n / 8 ------------
@@ -362,7 +365,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const AttnArgs<__half
     const int32_t* row = nullptr;
     int head_row = 0, last = -1, lo = 0;
     auto enter = [&]() {
-      row = a.tab.table + nx.i * a.tab.stride;
+      row = a.tab.table + nx.i * a.tab.stride + nx.s.off;
       head_row = nx.h << psl;
       last = min(nx.un.p1, nx.s.keys - 1);
       lo = a.shape.window > 0 && nx.un.p0 >= a.shape.window ? nx.un.p0 - a.shape.window + 1 : 0;
@@ -394,7 +397,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const AttnArgs<__half
       }
       // on by 7 tasks: a tile further, unless the task was a tile's first
       if ((seen & 7) != 0 && ++nxx == nx.x1) {
-        walk_next(nx, a, line);
+        walk_next<SHARED>(nx, a, line);
         nxx = nx.x;
         if (nx.left > 0) {
           enter();
@@ -542,7 +545,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const AttnArgs<__half
         }
         ++n;
         nb += two;
-        walk_next(k, a, line);
+        walk_next<SHARED>(k, a, line);
       }
       mma_commit(done);
     }
@@ -575,12 +578,13 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const AttnArgs<__half
     float m = -INFINITY;
     float2 l2 = make_float2(0.0f, 0.0f);
     uint32_t nans = 0;
+    PrefixParts pp{-1, 0, 0, 0};   // what the row's shared prefix left (paged_prefix.cu)
     while (true) {
       // A round ends one segment and works on the next.  S of the last tile is complete, so Q's place is free: the next Q is
       // on its way while the last P V runs, and its first S runs while O is written.
       while (k.left > 0 && grp == 1 && k.un.rows <= 128) {
         g0 += k.x1 - k.x;
-        walk_next(k, a, line);
+        walk_next<SHARED>(k, a, line);
       }
       const bool more = k.left > 0;
       if (more) {
@@ -617,7 +621,22 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const AttnArgs<__half
       }
       if (rows >= 0) {
         // ---- the segment's rows: finished, or this share's partial ------------------------
-        const float l = l2.x + l2.y;
+        float l = l2.x + l2.y;
+        // parts of a shared prefix: the largest maximum first, and the sum, then column by column
+        auto part_at = [&](int k) { return static_cast<int64_t>(pp.w0 + k - 1) * kPrefixRows + pp.row; };
+        float own = 1.0f, base = 0.0f;
+        if (SHARED && pp.home >= 0) {
+          float top = fmaxf(m, a.prefix.home_stat[pp.home].x);
+          for (int k = 1; k <= pp.count; ++k) top = fmaxf(top, a.prefix.extra_stat[part_at(k)].x);
+          base = top == -INFINITY ? 0.0f : top;
+          own = exp2f(m - base);
+          l *= own;
+          for (int k = 0; k <= pp.count; ++k) {
+            const float2 st = k == 0 ? a.prefix.home_stat[pp.home] : a.prefix.extra_stat[part_at(k)];
+            l = fmaf(st.y, exp2f(st.x - base), l);
+          }
+          m = top;
+        }
         const float f = !whole_item ? 1.0f : l == 0.0f ? 0.0f : 1.0f / l;
         const int64_t slot = (static_cast<int64_t>(w) * 2 + (from_start ? 1 : 0)) * kRows + row_w;   // of the warp's first row
 #pragma unroll 1
@@ -628,7 +647,24 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const AttnArgs<__half
           const float fc = (nans >> (c >> 1)) & 1u ? __uint_as_float(0x7fffffffu) : f;   // a NaN group's columns
           float v[32];         // of 8 columns dims 0..7 lie at 0, 2, 4, 6, 1, 3, 5, 7
 #pragma unroll
-          for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(u[(e & 24) + ((e & 7) < 4 ? 2 * (e & 7) : 2 * (e & 7) - 7)]) * fc;
+          for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(u[(e & 24) + ((e & 7) < 4 ? 2 * (e & 7) : 2 * (e & 7) - 7)]) * (SHARED ? fc * own : fc);
+          if (SHARED) {
+            if (pp.home >= 0)
+              for (int k = 0; k <= pp.count; ++k) {
+                const float2 st = k == 0 ? a.prefix.home_stat[pp.home] : a.prefix.extra_stat[part_at(k)];
+                const float* x = (k == 0 ? a.prefix.home + pp.home * D : a.prefix.extra + part_at(k) * D) + 32 * c;
+                const float fk = exp2f(st.x - base) * f;
+#pragma unroll
+                for (int e = 0; e < 32; e += 4) {
+                  const float4 y = *reinterpret_cast<const float4*>(x + e);
+                  v[e] = fmaf(y.x, fk, v[e]);
+                  v[e + 1] = fmaf(y.y, fk, v[e + 1]);
+                  v[e + 2] = fmaf(y.z, fk, v[e + 2]);
+                  v[e + 3] = fmaf(y.w, fk, v[e + 3]);
+                }
+              }
+            __syncwarp();   // collective loads follow
+          }
           if (whole_item) {
             if (r < rows) {
               uint4* out = reinterpret_cast<uint4*>(a.out + dst + 32 * c);
@@ -786,13 +822,21 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const AttnArgs<__half
       whole_item = from_start && k.x1 == k.sp.n;
       rows = k.un.rows;
       dst = place(a.ldo);
+      if (SHARED) {
+        pp.home = -1;
+        if (from_start && r < rows && a.tab.skip[k.i] > 0) {
+          const int row = k.un.r0 + r, t = row / a.shape.group;
+          pp = prefix_parts(a.prefix, k.i, t, k.h, row - t * a.shape.group, a.shape.group, a.q_heads);
+        }
+        __syncwarp();
+      }
       if (from_start && !whole_item) {
         // the item's first tile in the line: the share's first tiles, then those of the segments before it
         const int64_t per = line.per, start = w * per + g0;
         rec = make_int4(k.i, k.h, k.u, static_cast<int>((start + k.sp.n - 1) / per));
       }
       g0 += tiles;
-      walk_next(k, a, line);
+      walk_next<SHARED>(k, a, line);
     }
     cp_async_wait<0>();   // none is left in flight where a wait ran out
     if (threadIdx.x == 0) pl.rec[w] = rec;
@@ -811,14 +855,14 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const AttnArgs<__half
   }
 }
 
-template <int D>
-fg_status launch(const AttnArgs<__half>& a, const ClassPlan& pl, bool own_plan, bool every, cudaStream_t st) {
+template <int D, bool SHARED>
+fg_status launch_kernel(const AttnArgs<__half>& a, const ClassPlan& pl, bool own_plan, bool every, cudaStream_t st) {
   using S = Smem<D>;
   static bool set[64] = {false};
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev >= 0 && dev < 64 && !set[dev]) {
-    if (cudaFuncSetAttribute(tile_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kBytes) != cudaSuccess)
+    if (cudaFuncSetAttribute(tile_kernel<D, SHARED>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kBytes) != cudaSuccess)
       return check_launch("tile_kernel smem attribute");
     set[dev] = true;
   }
@@ -826,7 +870,12 @@ fg_status launch(const AttnArgs<__half>& a, const ClassPlan& pl, bool own_plan, 
   // Early behind the plan alone.  As a call's first launch or behind the steps the CTAs then would not take the SMs in
   // order, so that neighbours in the line share a head's keys in L2 (a chunk of 2048 rows 459 us, 464 early; 63 single
   // tokens beside a chunk of 512 362 and 367).
-  return paged::launch("tile_kernel", every && !own_plan, tile_kernel<D>, static_cast<unsigned>(pl.workers), kThreads, S::kBytes, st, a, pl, wait_limit(), own_plan, every);
+  return paged::launch("tile_kernel", every && !own_plan, tile_kernel<D, SHARED>, static_cast<unsigned>(pl.workers), kThreads, S::kBytes, st, a, pl, wait_limit(), own_plan, every);
+}
+
+template <int D>
+fg_status launch(const AttnArgs<__half>& a, const ClassPlan& pl, bool own_plan, bool every, cudaStream_t st) {
+  return a.tab.skip != nullptr ? launch_kernel<D, true>(a, pl, own_plan, every, st) : launch_kernel<D, false>(a, pl, own_plan, every, st);
 }
 
 }  // namespace

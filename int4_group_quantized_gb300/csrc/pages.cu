@@ -78,6 +78,7 @@ Table table_of(const fg_page_table& t) {
   a.pages = static_cast<int>(t.pages);
   a.ps_log2 = log2_of(t.page_size);
   a.stride = t.stride;
+  a.skip = nullptr;
   return a;
 }
 

@@ -173,3 +173,28 @@ def test_oracle_share_by_hand():
     # an entry that names no page ends the prefix: with two pages everyone is in
     t[5, 2] = 77
     assert op.share(t, lens, cu, 10, 16, 1)[0].tolist() == [0, 0, 0, -1, -1, 0]
+
+
+def test_shared_attention_arguments(fg):
+    pool, tab = _pool(fg), _tab(fg)
+
+    def attend(pool=pool, tab=tab, cu=P, s=None, q=P, ldq=256, qh=4, ntok=4, mq=2, out=P, ldo=256, ws=P, wsb=1 << 40):
+        s = _share(fg) if s is None else s
+        return fg.lib.fg_paged_attention_shared(_br(pool), _br(tab), cu, _br(s) if s else None, q, ldq, qh, ntok, mq, out, ldo, ws, wsb, None)
+
+    assert attend(s=False) == 1 and attend(s=_share(fg, seqs=4)) == 2 and attend(s=_share(fg, ntok=5)) == 2
+    for field in ("group", "tokens", "first", "leader", "begin", "rows"):
+        assert attend(s=_share(fg, **{field: None})) == 1
+        assert attend(s=_share(fg, **{field: P + 1})) == 3
+    assert attend(qh=3) == 2 and attend(qh=0) == 1 and attend(ntok=-1) == 1 and attend(mq=-1) == 1
+    assert attend(cu=None) == 1 and attend(q=None) == 1 and attend(out=None) == 1
+    assert attend(ldq=248) == 2 and attend(ldo=248) == 2 and attend(ldq=260) == 3 and attend(q=P + 2) == 3 and attend(cu=P + 1) == 3
+    need = fg.lib.fg_paged_attention_shared_workspace_bytes(_br(pool), _br(tab), 4, 4, 2)
+    assert need > fg.lib.fg_paged_attention_workspace_bytes(_br(pool), _br(tab), 4, 4, 2)
+    assert attend(ws=None) == 5 and attend(wsb=need - 1) == 5 and attend(ws=P + 16) == 3
+    assert attend(ntok=0, s=_share(fg, ntok=0)) == 0 and attend(mq=0) == 0
+    assert fg.lib.fg_paged_attention_shared_workspace_bytes(_br(_pool(fg, ps=32)), _br(tab), 4, 4, 2) == 0
+    f32 = _pool(fg, dtype=1)      # every sequence by itself, in that call's workspace
+    assert fg.lib.fg_paged_attention_shared_workspace_bytes(_br(f32), _br(tab), 4, 4, 2) == \
+        fg.lib.fg_paged_attention_workspace_bytes(_br(f32), _br(tab), 4, 4, 2)
+    assert attend(pool=f32, wsb=16) == 5

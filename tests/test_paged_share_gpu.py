@@ -94,3 +94,277 @@ def test_share_of_offsets_out_of_range(fg):
         with pytest.raises(fg.FGError, match="FG_ERR_ARG"):
             fg.fg_sync_status()
         assert (guard[:16] == -77).all() and (guard[20:] == -77).all()
+
+
+# ---- attention ---------------------------------------------------------------------
+#
+# A row's bound: the prefix is multiplied as chunks are (K, V and the weights rounded to fp16), a sequence's own tokens as
+# steps or as chunks; with the row's weights p_j over all of its tokens each part's terms (oracle/paged.py,
+# attention_bound) are sums over some of them, so the two kinds' sum bounds both.  The parts are joined in fp32: at most
+# 130 parts, a rounding of the sums (2^-24) and of a factor (2^-22 in all) each.
+
+class Forked:
+    """Sequences that share leading pages group by group, with rows of their own after that; values, keys and queries of
+    unlike sizes."""
+
+    def __init__(self, fg, groups, tails, n, heads, r, d, ps, seed, q_size=1.0, dtype=torch.float16):
+        # groups: of each sequence (group or -1); pages of a group: shared[g]
+        rng = np.random.default_rng(seed)
+        which, shared = groups
+        self.which = np.asarray(which)
+        lead = np.array([0 if g < 0 else shared[g] for g in which])
+        tails, n = np.asarray(tails), np.asarray(n)
+        own = -(-tails // ps)
+        pages = int(sum(shared) + own.sum()) + 2
+        perm = rng.permutation(pages)
+        start = np.concatenate(([0], np.cumsum(shared)))
+        self.table = np.full((len(which), int((lead + own).max()) + 1), -1)
+        at = int(sum(shared))
+        for i, g in enumerate(which):
+            if g >= 0:
+                self.table[i, :lead[i]] = perm[start[g]:start[g + 1]]
+            self.table[i, lead[i]:lead[i] + own[i]] = perm[at:at + own[i]]
+            at += own[i]
+        self.lens, self.n, self.ps, self.heads, self.r, self.d, self.pages, self.dtype = lead * ps + tails, n, ps, heads, r, d, pages, dtype
+        self.cu = np.concatenate(([0], np.cumsum(n)))
+        np_dt = np.float16 if dtype == torch.float16 else np.float32
+        self.arr = {}
+        for w in "kv":
+            x = rng.normal(size=(pages, heads, ps, d)) * (0.5 + rng.random((heads, 1, d))) * 2.0 ** rng.integers(-2, 2, (pages, heads, ps, 1))
+            self.arr[w] = list(op.codec.quantize_g64(x.astype(np_dt)))
+        self.q = (q_size * rng.normal(size=(int(self.cu[-1]), heads * r * d))).astype(np_dt)
+        self.upload(fg)
+
+    def upload(self, fg):
+        k, v = ([torch.as_tensor(a, device="cuda") for a in self.arr[w]] for w in "kv")
+        self.pool = fg.PagePool.of(*k, *v, self.dtype)
+        self.tab = fg.PageTable(_i32(self.table), _i32(self.lens), _i32(np.ones(self.pages)), self.ps)
+
+    def find(self, fg, least=1):
+        s = fg.PageShare.empty(self.tab, int(self.cu[-1]))
+        fg.fg_pages_share(self.tab, _i32(self.cu), s, least)
+        return s
+
+    def expect(self):
+        d, r = self.d, self.r
+        ref, tol = np.full(self.q.shape, np.nan), np.zeros(self.q.shape)
+        for i, length in enumerate(self.lens):
+            a, e = int(self.cu[i]), int(self.cu[i + 1])
+            if a == e:
+                continue
+            pos = np.repeat(np.arange(length - (e - a), length), r)
+            j = np.arange(length)
+            page = self.table[i, j // self.ps]
+            ok = (page >= 0) & (page < self.pages)
+            at = np.where(ok, page, 0), j % self.ps
+            for h in range(self.heads):
+                qq = self.q[a:e].reshape(e - a, -1, d)[:, h * r:(h + 1) * r].reshape(-1, d).astype(np.float64)
+                k, v = ([x[at[0], h, at[1]] for x in self.arr[w]] for w in "kv")
+                if self.dtype == torch.float32:
+                    out, t = op.attention_bound(qq, k, v, pos, present=ok, kind="f32")
+                else:
+                    out, t = op.attention_bound(qq, k, v, pos, present=ok, kind="step")
+                    _, t2 = op.attention_bound(qq, k, v, pos, present=ok, kind="chunk")
+                    with np.errstate(all="ignore"):
+                        t = t + t2 + 130 * 2.0 ** -22 * np.abs(out)
+                sl = np.s_[a:e, h * r * d:(h + 1) * r * d]
+                ref[sl], tol[sl] = out.reshape(e - a, -1), t.reshape(e - a, -1)
+        return ref, tol
+
+
+def _run(fg, F, share=None, max_q=None, **kw):
+    out = torch.full(F.q.shape, 7.0, dtype=F.dtype, device="cuda")
+    fg.fg_paged_attention_shared(F.pool, F.tab, _i32(F.cu), F.find(fg) if share is None else share, torch.as_tensor(F.q, device="cuda"),
+                                 F.heads * F.r, out, int(F.n.max()) if max_q is None else max_q, **kw)
+    return out
+
+
+def _hold(got, ref, tol, rms=3 * 2.0 ** -11):
+    why = op.off_by_too_much(got.double().cpu().numpy(), ref, tol, rms)
+    assert why is None, why
+
+
+def _sizes(b, lo, hi, seed):
+    return np.random.default_rng(seed).integers(lo, hi + 1, b)
+
+
+SHARED = {   # groups, tails, rows, heads, query heads a head, d, page size
+    "two sequences of a page": (([0, 0], [1]), [1, 5], [1, 1], 1, 1, 64, 16),
+    "a step": (([0] * 6, [19]), _sizes(6, 1, 60, 1), [1] * 6, 12, 1, 64, 16),
+    "a step of wide heads": (([0] * 5 + [-1], [5]), _sizes(6, 1, 60, 2), [1] * 6, 3, 1, 128, 64),
+    "130 followers, two units": (([0] * 130, [26]), _sizes(130, 1, 30, 3), [1] * 130, 2, 1, 128, 16),
+    "eight query heads, three groups": (([0, 1, 2, -1] * 5, [3, 9, 1]), _sizes(20, 1, 200, 4), [1] * 20, 2, 8, 128, 32),
+    "few rows, idle sequences": (([0, 0, 1, 1, 0, -1], [4, 7]), [9, 1, 30, 3, 5, 6], [2, 0, 3, 1, 4, 2], 3, 2, 64, 16),
+    "chunks": (([0, 1, 0, 1, -1, 0], [7, 2]), [60, 40, 5, 33, 70, 61], [60, 17, 5, 33, 70, 1], 2, 4, 128, 32),
+    "chunks beside steps": (([0] * 8, [10]), [1, 200, 1, 2, 90, 1, 1, 7], [1, 100, 1, 2, 90, 1, 1, 7], 2, 3, 64, 32),
+    "a long prefix over many shares": (([0] * 3, [200]), [3, 4, 5], [1] * 3, 1, 1, 64, 32),
+    "a long prefix of chunks": (([0] * 3, [33]), [150, 4, 64], [150, 4, 64], 1, 4, 128, 128),
+    "tokens that no tile divides": (([0] * 4 + [1] * 4, [9, 17]), _sizes(8, 1, 40, 5), [1] * 8, 2, 2, 128, 16),
+    "wide groups": (([0, 0, 0], [8]), [20, 30, 40], [3, 1, 2], 1, 20, 64, 64),
+    "300 sequences": (([0] * 120 + [-1] * 30 + [1] * 150, [4, 6]), _sizes(300, 1, 40, 6), [1] * 300, 1, 1, 64, 16),
+    "one row a unit more": (([0] * 129, [2]), [3] * 129, [1] * 129, 1, 1, 64, 64),
+}
+
+
+@pytest.mark.parametrize("name", SHARED)
+def test_shared_attention(fg, name):
+    groups, tails, n, heads, r, d, ps = SHARED[name]
+    F = Forked(fg, groups, tails, n, heads, r, d, ps, 11)
+    out = _run(fg, F)
+    fg.fg_sync_status()
+    _hold(out, *F.expect())
+    assert torch.equal(_run(fg, F), out)                     # the same bits again
+
+
+@pytest.mark.parametrize("size", [8.0, 40.0])
+def test_large_scores(fg, size):
+    """A later tile's scores may lie far above the first ones'."""
+    F = Forked(fg, ([0] * 5, [70]), [3, 40, 100, 7, 1], [1, 1, 3, 1, 1], 2, 2, 128, 16, 12, q_size=size)
+    out = _run(fg, F)
+    fg.fg_sync_status()
+    ref, tol = F.expect()
+    _hold(out, ref, tol, rms=None)
+
+
+def test_every_sequence_of_fp32_by_itself(fg):
+    F = Forked(fg, ([0, 0, 0, -1], [5]), [20, 30, 40, 7], [3, 1, 20, 7], 2, 2, 64, 16, 13, dtype=torch.float32)
+    out = _run(fg, F)
+    fg.fg_sync_status()
+    _hold(out, *F.expect(), rms=None)
+
+
+def test_nobody_shares(fg):
+    F = Forked(fg, ([-1] * 5, []), [40, 1, 30, 100, 17], [1, 1, 30, 2, 1], 2, 2, 64, 16, 14)
+    out, plain = _run(fg, F), torch.full(F.q.shape, 7.0, dtype=torch.float16, device="cuda")
+    fg.fg_paged_attention(F.pool, F.tab, _i32(F.cu), torch.as_tensor(F.q, device="cuda"), 4, plain, 30)
+    fg.fg_sync_status()
+    assert torch.equal(out, plain)                           # the same launches over the same lines
+    _hold(out, *F.expect())
+
+
+def test_rows_that_reach_into_the_prefix_go_alone(fg):
+    """A share made earlier: one sequence's rows now begin before its group's tokens end, another takes no part."""
+    F = Forked(fg, ([0] * 5, [6]), [40, 20, 50, 33, 2], [4] * 4 + [2], 2, 2, 64, 16, 15)
+    s = F.find(fg)
+    F.lens[1] = 6 * 16 + 3                                   # of 4 rows, one stands inside the prefix
+    F.upload(fg)
+    out = _run(fg, F, s)
+    fg.fg_sync_status()
+    _hold(out, *F.expect())
+    F.lens[1] = 4                                            # all of them, at the beginning
+    F.upload(fg)
+    out = _run(fg, F, s)
+    fg.fg_sync_status()
+    _hold(out, *F.expect())
+
+
+def test_pages_may_be_compacted_and_lengths_grow(fg):
+    F = Forked(fg, ([0, 0, 1, 1], [3, 4]), [5, 6, 7, 8], [1] * 4, 2, 1, 64, 16, 16)
+    s = F.find(fg)
+    perm = np.random.default_rng(17).permutation(F.pages)    # page p is now perm[p]
+    F.table = np.where(F.table >= 0, perm[F.table], -1)
+    F.arr = {w: [x[np.argsort(perm)] for x in F.arr[w]] for w in "kv"}
+    F.lens = F.lens + 3
+    F.upload(fg)
+    out = _run(fg, F, s)
+    fg.fg_sync_status()
+    _hold(out, *F.expect())
+
+
+def test_a_missing_page_of_the_prefix_is_not_seen(fg):
+    F = Forked(fg, ([0] * 4, [9]), [5, 6, 7, 80], [1, 1, 1, 70], 2, 2, 64, 16, 18)
+    s = F.find(fg)
+    F.table[:, 3] = -1
+    F.upload(fg)
+    out = _run(fg, F, s)
+    with pytest.raises(fg.FGError, match="FG_ERR_CAPACITY"):
+        fg.fg_sync_status()
+    _hold(out, *F.expect())
+    F.table[:, :9] = F.pages + 3                             # the whole prefix: rows see their own tokens
+    F.upload(fg)
+    out = _run(fg, F, s)
+    with pytest.raises(fg.FGError, match="FG_ERR_CAPACITY"):
+        fg.fg_sync_status()
+    _hold(out, *F.expect())
+
+
+@pytest.mark.parametrize("bad", [np.nan, np.inf, -np.inf])
+def test_what_is_not_finite_reaches_the_group_alone(fg, bad):
+    F = Forked(fg, ([0, 0, 1, 1, -1], [10, 9]), [5, 6, 7, 8, 90], [1, 1, 1, 20, 1], 1, 2, 128, 16, 19)
+    F.arr["v"][2][F.table[0, 4], 0, 7, 1] = bad              # dims 64 .. 127 of one value of group 0
+    F.upload(fg)
+    out = _run(fg, F)
+    fg.fg_sync_status()
+    ref, tol = F.expect()
+    assert np.isnan(ref[:2]).sum() == 2 * 2 * 64 and not np.isnan(ref[2:]).any()
+    _hold(out, ref, tol)
+    F.arr["k"][2][F.table[2, 2], 0, 3, 0] = bad              # a key of group 1's prefix: its rows' scores are NaN
+    F.upload(fg)
+    got = _run(fg, F).double().cpu().numpy()
+    fg.fg_sync_status()
+    assert np.isnan(got[2:-1]).all() and not np.isnan(got[-1]).any()
+
+
+def test_rows_behind_the_last_sequence_stay(fg):
+    F = Forked(fg, ([0, 0, 0], [9]), [5, 6, 40], [1, 1, 25], 2, 1, 64, 16, 20)
+    wide = torch.randn((F.cu[-1] + 3, 2 * 64 + 24), device="cuda").half()
+    wide[:F.cu[-1], :128] = torch.as_tensor(F.q, device="cuda")
+    out = torch.full_like(wide, 7.0)
+    share = fg.PageShare.empty(F.tab, int(F.cu[-1]) + 3)
+    fg.fg_pages_share(F.tab, _i32(F.cu), share, 1)
+    fg.fg_paged_attention_shared(F.pool, F.tab, _i32(F.cu), share, wide[:, :128], 2, out[:, :128], 25)
+    fg.fg_sync_status()
+    _hold(out[:F.cu[-1], :128], *F.expect())
+    assert (out[F.cu[-1]:] == 7.0).all() and (out[:, 128:] == 7.0).all()
+
+
+def test_a_share_of_nonsense_is_not_followed(fg):
+    """Numbers out of range are no groups: every sequence goes by itself."""
+    F = Forked(fg, ([0] * 4, [9]), [5, 6, 7, 80], [1, 1, 1, 70], 2, 2, 64, 16, 21)
+    good = F.find(fg)
+    ref = F.expect()
+    for field, values in (("group", [10 ** 9, -(10 ** 9), 77]), ("tokens", [17, -16, 10 ** 9, 2 ** 31 - 16]), ("first", [-1, 10 ** 9, 60]),
+                          ("leader", [-5, 10 ** 9, 4]), ("begin", [-1, 10 ** 9, -(10 ** 9), 74]), ("rows", [-1, 10 ** 9])):
+        for v in values:
+            s = fg.PageShare(*[getattr(good, f).clone() for f in FIELDS])
+            getattr(s, field).fill_(v)
+            out = _run(fg, F, s)
+            fg.fg_sync_status()
+            _hold(out, *ref)
+
+
+def test_graphs_streams_and_shared_workspaces(fg):
+    """Two captured graphs use one workspace in turn; a call on another stream gives the same bits."""
+    A = Forked(fg, ([0] * 5, [20]), [5, 6, 7, 80, 9], [1, 1, 1, 70, 2], 2, 2, 64, 16, 22)
+    B = Forked(fg, ([0, 0, 1, 1], [3, 40]), [5, 6, 7, 8], [1] * 4, 3, 1, 128, 32, 23)
+    need = max(fg.fg_paged_attention_shared_workspace_bytes(F.pool, F.tab, F.heads * F.r, len(F.q), int(F.n.max())) for F in (A, B))
+    ws = fg.workspace(need)
+    want, graphs = [], []
+    for F in (A, B):
+        F.out, F.dev_q, F.dev_cu, F.s = torch.empty(F.q.shape, dtype=torch.float16, device="cuda"), torch.as_tensor(F.q, device="cuda"), _i32(F.cu), F.find(fg)
+
+        def call(F=F, stream=None):
+            fg.fg_pages_share(F.tab, F.dev_cu, F.s, 1, ws=ws, stream=stream)
+            fg.fg_paged_attention_shared(F.pool, F.tab, F.dev_cu, F.s, F.dev_q, F.heads * F.r, F.out, int(F.n.max()), ws=ws, stream=stream)
+
+        call()
+        torch.cuda.synchronize()
+        want.append(F.out.clone())
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            call()
+        graphs.append(g)
+        F.out.zero_()
+        st = torch.cuda.Stream()
+        st.wait_stream(torch.cuda.current_stream())
+        call(stream=st)
+        st.synchronize()
+        assert torch.equal(F.out, want[-1])
+    for _ in range(5):
+        for F in (A, B):
+            F.out.zero_()
+        for g in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(F.out, w) for F, w in zip((A, B), want))
+    fg.fg_sync_status()
