@@ -95,15 +95,17 @@ __device__ __forceinline__ float2 cos_sin(uint64_t phase, float scale) {
 __device__ __forceinline__ uint64_t phase_of(int pos, uint64_t turns) { return static_cast<uint64_t>(static_cast<int64_t>(pos)) * turns; }
 
 // a c - b s and a s + b c of two pairs at once, each operation rounded by
-// itself (a paired product is not contracted with the sum after it).
+// itself.  (Both sums are differences taken by an FMA with -1: a paired product
+// with a paired sum after it came out contracted, in a quarter of the values.)
 __device__ __forceinline__ void turn2(float2& a, float2& b, float2 c, float2 s) {
   float2 x, y;
   asm("{ .reg .b64 a, b, c, s, n, p, q; mov.b64 a, {%4, %5}; mov.b64 b, {%6, %7}; mov.b64 c, {%8, %9}; mov.b64 s, {%10, %11};\n"
-      "mov.b64 n, {%12, %13};\n"
+      "mov.b64 n, {%12, %12};\n"
       "mul.rn.f32x2 p, a, c; mul.rn.f32x2 q, b, s; fma.rn.f32x2 p, q, n, p; mov.b64 {%0, %1}, p;\n"
-      "mul.rn.f32x2 p, a, s; mul.rn.f32x2 q, b, c; add.rn.f32x2 p, p, q; mov.b64 {%2, %3}, p; }"
+      "xor.b64 b, b, 0x8000000080000000;\n"
+      "mul.rn.f32x2 p, a, s; mul.rn.f32x2 q, b, c; fma.rn.f32x2 p, q, n, p; mov.b64 {%2, %3}, p; }"
       : "=f"(x.x), "=f"(x.y), "=f"(y.x), "=f"(y.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y), "f"(s.x), "f"(s.y), "f"(-1.0f), "f"(-1.0f));
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y), "f"(s.x), "f"(s.y), "f"(-1.0f));
   a = x;
   b = y;
 }

@@ -67,6 +67,26 @@ def test_rotate(fg, n, heads, d, rot, dt, layout):
     assert torch.equal(y, out)
 
 
+@pytest.mark.parametrize("layout", ["half", "pairs"])
+def test_sums_and_products_are_rounded_one_by_one(fg, layout):
+    """fp32 rows moved 16 bytes at a time and two elements at a time are the same bits, those of separate operations on
+    cosines and sines rounded to fp32 (which differ from fp64's rounded ones in 3.5e-5 of the angles)."""
+    n, d = 400, 128
+    rotary = fg.Rotary(d, layout)
+    gen = torch.Generator(device="cuda").manual_seed(8)
+    wide = torch.randn((n, d + 1), generator=gen, device="cuda")
+    pos = torch.randint(0, 5000, (n,), generator=gen, device="cuda", dtype=torch.int32)
+    x = wide[:, 1:].contiguous()
+    a, b = (fg.fg_rotate(rotary, t, pos, 1, torch.empty_like(x)) for t in (x, wide[:, 1:]))
+    assert torch.equal(a, b)
+    ang = torch.as_tensor(orot.angles(pos.tolist(), _turns(rotary)), device="cuda")
+    c, s = torch.cos(ang).float(), torch.sin(ang).float()
+    u, v = (x[:, :64], x[:, 64:]) if layout == "half" else (x[:, 0::2], x[:, 1::2])
+    y, z = u * c - v * s, u * s + v * c
+    want = torch.cat((y, z), 1) if layout == "half" else torch.stack((y, z), -1).reshape(n, d)
+    assert float((a != want).float().mean()) < 1e-3
+
+
 @pytest.mark.parametrize("dt", ["f16", "f32"])
 def test_far_positions_lose_nothing(fg, dt):
     rotary = fg.Rotary(64)
