@@ -300,6 +300,7 @@ inline size_t up(size_t x) { return (x + 255) / 256 * 256; }
 struct Layout {
   ClassPlan step, tile;
   Prefix prefix;     // of a call beside shared prefixes
+  ClassPlan tall;    // its groups of many rows
   int32_t* skip;
   size_t bytes;
 };
@@ -334,6 +335,7 @@ Layout layout_of(const fg_page_pool& pool, const fg_page_table& t, int32_t q_hea
   else if (most > (l.step.workers ? kStepRows : 0))
     carve_class(l.tile, p, t.seqs, pool.head_dim, sms, kMaxSms, kTileRows);
   memset(&l.prefix, 0, sizeof(l.prefix));
+  memset(&l.tall, 0, sizeof(l.tall));
   l.skip = nullptr;
   if (shared_rows >= 0) {
     const size_t pairs = static_cast<size_t>(shared_rows) * q_heads, d = pool.head_dim;
@@ -343,11 +345,17 @@ Layout layout_of(const fg_page_pool& pool, const fg_page_table& t, int32_t q_hea
     };
     take(l.skip, 4 * static_cast<size_t>(t.seqs));
     take(l.prefix.info, sizeof(PrefixGroup) * static_cast<size_t>(t.seqs));
-    take(l.prefix.per, 8);
+    const size_t extra = static_cast<size_t>(kMaxSms) * (kPrefixRows + (l.tile.workers ? kTileRows : 0));
+    if (l.tile.workers) {
+      l.tall.workers = l.tile.workers;
+      l.tall.rows = kTileRows;
+      take(l.tall.head, 256);
+      take(l.tall.pre, 8 * static_cast<size_t>(t.seqs + 1));
+    }
     take(l.prefix.home_stat, 8 * pairs);
-    take(l.prefix.extra_stat, 8 * static_cast<size_t>(kMaxSms) * kPrefixRows);
+    take(l.prefix.extra_stat, 8 * extra);
     take(l.prefix.home, 4 * pairs * d);
-    take(l.prefix.extra, 4 * static_cast<size_t>(kMaxSms) * kPrefixRows * d);
+    take(l.prefix.extra, 4 * extra * d);
   }
   l.bytes = static_cast<size_t>(p - static_cast<char*>(ws)) + 256;
   return l;
@@ -380,9 +388,13 @@ fg_status launch_attn(const fg_page_pool& pool, const fg_page_table& t, const in
   if constexpr (half) {
     if (share) {
       a.prefix.group = share->group;
+      a.prefix.tokens = share->tokens;
       a.prefix.first = share->first;
-      const PrefixArgs p{a, share->tokens, share->leader, share->begin, share->rows, l.skip, std::min(num_sms(), kMaxSms)};
-      FG_TRY(paged_prefix(p, pool.head_dim, st));
+      a.prefix.leader = share->leader;
+      a.prefix.begin = share->begin;
+      a.prefix.rows = share->rows;
+      FG_TRY(paged_prefix(PrefixArgs{a, l.skip, l.tall, std::min(num_sms(), kMaxSms)}, pool.head_dim, st));
+      if (l.tall.workers > 0) FG_TRY(paged_prefix_tile(a, l.tall, pool.head_dim, st));
       a.tab.skip = l.skip;
     }
   }

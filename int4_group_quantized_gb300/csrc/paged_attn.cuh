@@ -6,41 +6,61 @@
 namespace fg {
 namespace paged {
 
-// What the rows of a shared prefix's groups left behind (paged_prefix.cu): sums, maximum (base 2) and normaliser of every
-// row over its group's prefix, in parts.  Part 0 of a row is its home; the parts of later shares are theirs.
+// What the rows of a shared prefix's groups left behind (paged_prefix.cu, and paged_tile.cu for groups of many rows): sums,
+// maximum (base 2) and normaliser of every row over its group's prefix, in parts.  Part 0 of a row is its home; the parts of
+// later shares of the line are in the shares' own places.
 struct PrefixGroup {
-  int64_t base;         // tiles of the line before the group
+  int64_t base, per;    // tiles of its line before the group, and of a share of the line
   int tiles, rows, units;   // tiles of a unit, rows of a unit, units of a head
   int first_row;        // of the group in the share's list
+  int extra, stride;    // rows of `extra` before its line's places, and of a place
 };
 struct Prefix {
-  const int32_t *group, *first;   // of a sequence (fg_page_share)
+  const int32_t *group, *tokens, *first, *leader, *begin, *rows;   // fg_page_share
   PrefixGroup* info;              // [groups]
-  int64_t* per;                   // tiles of a worker's share
   float* home;                    // [ntok][q_heads][D], rows in the share's order
   float2* home_stat;              // [ntok][q_heads]
-  float* extra;                   // [workers][kPrefixRows][D], of the unit that a share goes on with
-  float2* extra_stat;             // [workers][kPrefixRows]
+  float* extra;                   // [workers][kPrefixRows][D], then [workers][kTileRows][D]: of the unit that a share goes on with
+  float2* extra_stat;
 };
-constexpr int kPrefixRows = 128;  // most rows of a unit
+constexpr int kPrefixRows = 128;  // most rows of a unit of paged_prefix.cu
 
 // Where one row's parts lie.
 struct PrefixParts {
   int64_t home;         // row of home
-  int w0, count;        // extra parts are those of the shares w0 .. w0 + count - 1
-  int row;              // in them
+  int extra, stride, count;   // part k = 1 .. count is row extra + (k - 1) * stride of extra
 };
 __device__ __forceinline__ PrefixParts prefix_parts(const Prefix& p, int seq, int t, int h, int gh, int group, int q_heads) {
   const PrefixGroup g = p.info[p.group[seq]];
   const int x = p.first[seq] + t, r = x * group + gh, u = r / g.rows;
-  const int64_t start = g.base + (static_cast<int64_t>(h) * g.units + u) * g.tiles, per = *p.per;
+  const int64_t start = g.base + (static_cast<int64_t>(h) * g.units + u) * g.tiles;
   PrefixParts o;
   o.home = static_cast<int64_t>(g.first_row + x) * q_heads + h * group + gh;
-  o.row = r - u * g.rows;
-  const int w = static_cast<int>(start / per);
-  o.w0 = w + 1;
-  o.count = static_cast<int>((start + g.tiles - 1) / per) - w;
+  const int w = static_cast<int>(start / g.per);
+  o.stride = g.stride;
+  o.extra = g.extra + (w + 1) * g.stride + r - u * g.rows;
+  o.count = static_cast<int>((start + g.tiles - 1) / g.per) - w;
   return o;
+}
+
+// Group g as the share has it; list = 0: none, or not one that can be followed.
+struct SharedGroup {
+  int leader, tokens, first, list;
+};
+__device__ __forceinline__ SharedGroup shared_group(const Prefix& p, const Table& t, const Batch& b, int g) {
+  SharedGroup s{p.leader[g], 0, p.begin[g], 0};
+  const int end = p.begin[g + 1];
+  if (s.leader < 0 || s.leader >= t.seqs) return s;
+  s.tokens = p.tokens[s.leader];
+  const bool ok = s.tokens > 0 && (s.tokens & ((1 << t.ps_log2) - 1)) == 0 && s.tokens <= (t.stride << t.ps_log2) && s.first >= 0 &&
+                  end > s.first && end <= b.ntok;
+  s.list = ok ? end - s.first : 0;
+  return s;
+}
+// Row x of the share's list as a row of the batch (row 0 in place of what is none: nobody reads its parts).
+__device__ __forceinline__ int listed_row(const Prefix& p, const Batch& b, int x) {
+  const int r = p.rows[x];
+  return r >= 0 && r < b.ntok ? r : 0;
 }
 
 template <typename T>
@@ -68,6 +88,8 @@ fg_status paged_attention_step(const AttnArgs<__half>& a, const ClassPlan& pl, i
 constexpr int kTileRows = 256;
 // `every`: the call has no step class.
 fg_status paged_attention_tile(const AttnArgs<__half>& a, const ClassPlan& pl, int head_dim, bool own_plan, bool every, cudaStream_t st);
+// The prefixes of the groups in pl's line (pl.head, pl.pre by group), by the same kernel.
+fg_status paged_prefix_tile(const AttnArgs<__half>& a, const ClassPlan& pl, int head_dim, cudaStream_t st);
 
 // fp32 activations, every sequence: units of kF32Rows rows, tiles of 64 keys.
 constexpr int kF32Rows = 16, kF32KeysLog2 = 6;

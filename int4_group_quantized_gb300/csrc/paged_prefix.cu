@@ -29,7 +29,7 @@ __global__ void __launch_bounds__(kPrefixRows) prefix_kernel(const PrefixArgs p)
   int64_t left = min(line.per, line.total - o0);
   int g = line.g;
   PrefixGroup at = line.at;
-  SharedGroup s = shared_group(p, g);
+  SharedGroup s = shared_group(a.prefix, a.tab, a.batch, g);
   int64_t in = o0 - at.base;
   int h = static_cast<int>(in / (static_cast<int64_t>(at.units) * at.tiles));
   in -= static_cast<int64_t>(h) * at.units * at.tiles;
@@ -38,9 +38,8 @@ __global__ void __launch_bounds__(kPrefixRows) prefix_kernel(const PrefixArgs p)
     const int x1 = static_cast<int>(min(static_cast<int64_t>(at.tiles), x0 + left));
     const int r = u * at.rows + tid;
     const bool on = tid < at.rows && r < s.list * group;
-    const int x = on ? r / group : 0, gh = on ? r - x * group : 0, row = on ? p.rows[s.first + x] : -1;
-    const bool real = on && row >= 0 && row < a.batch.ntok;
-    const __half* q = a.q + (real ? row : 0) * a.ldq + static_cast<int64_t>(h * group + gh) * D;
+    const int x = on ? r / group : 0, gh = on ? r - x * group : 0, row = on ? listed_row(a.prefix, a.batch, s.first + x) : 0;
+    const __half* q = a.q + row * a.ldq + static_cast<int64_t>(h * group + gh) * D;
     float o[D], m = -INFINITY, l = 0.0f;
 #pragma unroll 8
     for (int c = 0; c < D; ++c) o[c] = 0.0f;
@@ -60,7 +59,7 @@ __global__ void __launch_bounds__(kPrefixRows) prefix_kernel(const PrefixArgs p)
         }
       }
       __syncthreads();
-      if (!real) continue;
+      if (!on) continue;
       for (int j = 0; j < kKeys; ++j) {
         if (!there[j]) continue;
         float sum = 0.0f;
@@ -86,9 +85,10 @@ __global__ void __launch_bounds__(kPrefixRows) prefix_kernel(const PrefixArgs p)
       if (++h == a.pool.heads) {
         h = 0;
         const int64_t next = at.base + static_cast<int64_t>(a.pool.heads) * at.units * at.tiles;
-        do s = shared_group(p, ++g);
-        while (s.list == 0);
-        at = prefix_group(s, group, next);
+        do s = shared_group(a.prefix, a.tab, a.batch, ++g);
+        while (s.list == 0 || (p.tile.workers > 0 && s.list * group > kPrefixFew));
+        at = prefix_group(s, group, false);
+        at.base = next;
       }
     }
   }

@@ -709,7 +709,7 @@ __global__ void __launch_bounds__(32 * kWarps, kCtasPerSm<NB>) step_kernel(const
         }
       most = top;
       if (k == pp.count) break;
-      const int64_t at = static_cast<int64_t>(pp.w0 + k) * kPrefixRows + pp.row;
+      const int64_t at = pp.extra + static_cast<int64_t>(k) * pp.stride;
       st = a.prefix.extra_stat[at];
       x = a.prefix.extra + at * D;
     }

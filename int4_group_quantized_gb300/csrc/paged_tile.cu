@@ -87,9 +87,12 @@ struct Smem {
 };
 
 // A share's walk over its segments: parts of one unit's key tiles.
+// What a launch attends to: sequences alone, sequences behind their shared prefixes (Table::skip), or the prefixes: then an
+// "i" is a group, whose rows all stand behind its tokens, and its rows' parts are left for the sequences.
+enum : int { kAlone = 0, kBehind = 1, kPrefix = 2 };
 struct Walk {
   int left;              // tiles of the share still to come
-  int i, h, u, x;        // sequence, head, unit, tile of the unit
+  int i, h, u, x;        // sequence (or group), head, unit, tile of the unit
   int units;
   Seq s;
   Unit un;
@@ -100,14 +103,19 @@ __device__ __forceinline__ void walk_unit(Walk& k, const AttnArgs<__half>& a) {
   k.un = unit_of<kRows>(k.s, a.shape.group, k.u);
   k.sp = span_of<kKeysLog2>(k.un.p0, k.un.p1, k.s.keys, a.shape.window, a.shape.sinks);
 }
-template <bool SHARED>
+template <int MODE>
 __device__ __forceinline__ void walk_seq(Walk& k, const AttnArgs<__half>& a) {
-  k.s = seq_of<SHARED>(a.tab, a.batch, k.i);
+  if (MODE == kPrefix) {
+    const SharedGroup g = shared_group(a.prefix, a.tab, a.batch, k.i);
+    k.s = Seq{g.first, g.list, g.tokens + g.list, g.tokens, 0};
+  } else {
+    k.s = seq_of<MODE == kBehind>(a.tab, a.batch, k.i);
+  }
   k.units = static_cast<int>((static_cast<int64_t>(k.s.n) * a.shape.group + kRows - 1) / kRows);
   k.u = 0;
 }
 // Share w's first segment (left = 0: none).
-template <bool SHARED>
+template <int MODE>
 __device__ __forceinline__ void walk_begin(Walk& k, const AttnArgs<__half>& a, const Line& pl, int w) {
   const int64_t total = pl.total, per = pl.per, o0 = w * per;
   k.left = 0;
@@ -120,7 +128,7 @@ __device__ __forceinline__ void walk_begin(Walk& k, const AttnArgs<__half>& a, c
   }
   k.i = lo;
   k.left = static_cast<int>(total - o0 < per ? total - o0 : per);
-  walk_seq<SHARED>(k, a);
+  walk_seq<MODE>(k, a);
   const int64_t all = pl.pre[lo + 1] - pl.pre[lo], in = o0 - pl.pre[lo];   // (32-bit divisions where they do: the short ones)
   const int64_t cost = all <= INT32_MAX ? static_cast<int>(all) / a.pool.heads : all / a.pool.heads;
   k.h = all <= INT32_MAX ? static_cast<int>(in) / static_cast<int>(cost) : static_cast<int>(in / cost);
@@ -150,7 +158,7 @@ __device__ __forceinline__ void walk_begin(Walk& k, const AttnArgs<__half>& a, c
   k.x1 = k.x + (k.left < k.sp.n - k.x ? k.left : k.sp.n - k.x);
 }
 // On to the next segment.
-template <bool SHARED>
+template <int MODE>
 __device__ __forceinline__ void walk_next(Walk& k, const AttnArgs<__half>& a, const Line& pl) {
   k.left -= k.x1 - k.x;
   if (k.left == 0) return;
@@ -160,7 +168,7 @@ __device__ __forceinline__ void walk_next(Walk& k, const AttnArgs<__half>& a, co
       do ++k.i;
       while (pl.pre[k.i + 1] == pl.pre[k.i]);
       k.h = 0;
-      walk_seq<SHARED>(k, a);
+      walk_seq<MODE>(k, a);
     }
   }
   walk_unit(k, a);
@@ -286,7 +294,7 @@ __device__ __forceinline__ void load_meta(float (&v)[NG], const float* base, uin
   }
 }
 
-template <int D, bool SHARED>
+template <int D, int MODE>
 __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const AttnArgs<__half> a, const ClassPlan pl, uint32_t wait_limit, const bool own_plan, const bool every) {
   using S = Smem<D>;
   constexpr int NG = D / 64;
@@ -343,14 +351,14 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const AttnArgs<__half
   __shared__ OwnPlan own;
   __shared__ Line line;   // not in registers: it is read between segments only
   {
-    const Line x = own_plan ? make_line<false, kRows, kKeysLog2, SHARED>(own, a.tab, a.batch, a.shape, a.pool.heads, pl.workers, every)
+    const Line x = own_plan ? make_line<false, kRows, kKeysLog2, MODE == kBehind>(own, a.tab, a.batch, a.shape, a.pool.heads, pl.workers, every)
                             : Line{pl.pre, pl.head[0], pl.head[1]};
     if (threadIdx.x == 0) line = x;
     __syncthreads();
   }
 
   Walk k;
-  walk_begin<SHARED>(k, a, line, w);
+  walk_begin<MODE>(k, a, line, w);
 
   if (warp >= kSoftWarps && warp < kSoftWarps + kRestoreWarps) {
     // ---- restoring warps: task n is K (n % 8 < 4) or V of 32 keys of tile n / 8 ------------
@@ -365,7 +373,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const AttnArgs<__half
     const int32_t* row = nullptr;
     int head_row = 0, last = -1, lo = 0;
     auto enter = [&]() {
-      row = a.tab.table + nx.i * a.tab.stride + nx.s.off;
+      row = MODE == kPrefix ? a.tab.table + a.prefix.leader[nx.i] * a.tab.stride : a.tab.table + nx.i * a.tab.stride + nx.s.off;
       head_row = nx.h << psl;
       last = min(nx.un.p1, nx.s.keys - 1);
       lo = a.shape.window > 0 && nx.un.p0 >= a.shape.window ? nx.un.p0 - a.shape.window + 1 : 0;
@@ -376,7 +384,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const AttnArgs<__half
       const int base = nx.h * a.shape.group;
       for (int r = lane; r < nx.un.rows; r += 32) {
         const int row_ = nx.un.r0 + r, t = row_ / a.shape.group;
-        const __half* p = a.q + static_cast<int64_t>(nx.s.row0 + t) * a.ldq + static_cast<int64_t>(base + row_ - t * a.shape.group) * D;
+        const __half* p = a.q + static_cast<int64_t>(MODE == kPrefix ? listed_row(a.prefix, a.batch, nx.s.row0 + t) : nx.s.row0 + t) * a.ldq + static_cast<int64_t>(base + row_ - t * a.shape.group) * D;
         asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
         if (D == 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(p + 64));
       }
@@ -397,7 +405,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const AttnArgs<__half
       }
       // on by 7 tasks: a tile further, unless the task was a tile's first
       if ((seen & 7) != 0 && ++nxx == nx.x1) {
-        walk_next<SHARED>(nx, a, line);
+        walk_next<MODE>(nx, a, line);
         nxx = nx.x;
         if (nx.left > 0) {
           enter();
@@ -545,7 +553,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const AttnArgs<__half
         }
         ++n;
         nb += two;
-        walk_next<SHARED>(k, a, line);
+        walk_next<MODE>(k, a, line);
       }
       mma_commit(done);
     }
@@ -564,7 +572,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const AttnArgs<__half
     // where the lane's row begins in rows ld apart
     auto place = [&](int64_t ld) {
       const int row = k.un.r0 + (r < k.un.rows ? r : 0), tok = row / a.shape.group;
-      return (k.s.row0 + tok) * ld + static_cast<int64_t>(k.h * a.shape.group + row - tok * a.shape.group) * D;
+      return (MODE == kPrefix ? listed_row(a.prefix, a.batch, k.s.row0 + tok) : k.s.row0 + tok) * ld + static_cast<int64_t>(k.h * a.shape.group + row - tok * a.shape.group) * D;
     };
     uint8_t* const stage = sOut + warp * S::kOut;
     bool ok = true;
@@ -578,13 +586,13 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const AttnArgs<__half
     float m = -INFINITY;
     float2 l2 = make_float2(0.0f, 0.0f);
     uint32_t nans = 0;
-    PrefixParts pp{-1, 0, 0, 0};   // what the row's shared prefix left (paged_prefix.cu)
+    PrefixParts pp{-1, 0, 0, 0};   // kBehind: what the row's shared prefix left
     while (true) {
       // A round ends one segment and works on the next.  S of the last tile is complete, so Q's place is free: the next Q is
       // on its way while the last P V runs, and its first S runs while O is written.
       while (k.left > 0 && grp == 1 && k.un.rows <= 128) {
         g0 += k.x1 - k.x;
-        walk_next<SHARED>(k, a, line);
+        walk_next<MODE>(k, a, line);
       }
       const bool more = k.left > 0;
       if (more) {
@@ -623,9 +631,9 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const AttnArgs<__half
         // ---- the segment's rows: finished, or this share's partial ------------------------
         float l = l2.x + l2.y;
         // parts of a shared prefix: the largest maximum first, and the sum, then column by column
-        auto part_at = [&](int k) { return static_cast<int64_t>(pp.w0 + k - 1) * kPrefixRows + pp.row; };
+        auto part_at = [&](int k) { return pp.extra + static_cast<int64_t>(k - 1) * pp.stride; };
         float own = 1.0f, base = 0.0f;
-        if (SHARED && pp.home >= 0) {
+        if (MODE == kBehind && pp.home >= 0) {
           float top = fmaxf(m, a.prefix.home_stat[pp.home].x);
           for (int k = 1; k <= pp.count; ++k) top = fmaxf(top, a.prefix.extra_stat[part_at(k)].x);
           base = top == -INFINITY ? 0.0f : top;
@@ -639,6 +647,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const AttnArgs<__half
         }
         const float f = !whole_item ? 1.0f : l == 0.0f ? 0.0f : 1.0f / l;
         const int64_t slot = (static_cast<int64_t>(w) * 2 + (from_start ? 1 : 0)) * kRows + row_w;   // of the warp's first row
+        float* const parts = MODE != kPrefix ? pl.part + slot * D : from_start ? a.prefix.home : a.prefix.extra;   // kPrefix: dst is the lane's row
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
           uint32_t u[32];
@@ -647,8 +656,8 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const AttnArgs<__half
           const float fc = (nans >> (c >> 1)) & 1u ? __uint_as_float(0x7fffffffu) : f;   // a NaN group's columns
           float v[32];         // of 8 columns dims 0..7 lie at 0, 2, 4, 6, 1, 3, 5, 7
 #pragma unroll
-          for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(u[(e & 24) + ((e & 7) < 4 ? 2 * (e & 7) : 2 * (e & 7) - 7)]) * (SHARED ? fc * own : fc);
-          if (SHARED) {
+          for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(u[(e & 24) + ((e & 7) < 4 ? 2 * (e & 7) : 2 * (e & 7) - 7)]) * (MODE == kBehind ? fc * own : fc);
+          if (MODE == kBehind) {
             if (pp.home >= 0)
               for (int k = 0; k <= pp.count; ++k) {
                 const float2 st = k == 0 ? a.prefix.home_stat[pp.home] : a.prefix.extra_stat[part_at(k)];
@@ -688,11 +697,12 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const AttnArgs<__half
           for (int i = 0; i < 32; i += 4) {
             const int n = i + (lane >> 3);
             const uint4 x = *reinterpret_cast<const uint4*>(stage + n * 128 + (((lane & 7) ^ (n & 7)) << 4));
-            if (row_w + n < rows) *reinterpret_cast<uint4*>(pl.part + (slot + n) * D + 32 * c + 4 * (lane & 7)) = x;
+            const int64_t to = MODE == kPrefix ? __shfl_sync(0xffffffffu, dst, n) : n;
+            if (row_w + n < rows) *reinterpret_cast<uint4*>(parts + to * D + 32 * c + 4 * (lane & 7)) = x;
           }
           __syncwarp();
         }
-        if (!whole_item && r < rows) pl.stat[slot + lane] = make_float2(m, l);
+        if (!whole_item && r < rows) (MODE != kPrefix ? pl.stat + slot : from_start ? a.prefix.home_stat : a.prefix.extra_stat)[MODE == kPrefix ? dst : lane] = make_float2(m, l);
       }
       if (!more) break;
       const int tiles = k.x1 - k.x;
@@ -819,10 +829,16 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const AttnArgs<__half
       }
       if (!ok) break;
       from_start = k.x == 0;
-      whole_item = from_start && k.x1 == k.sp.n;
+      whole_item = MODE != kPrefix && from_start && k.x1 == k.sp.n;
       rows = k.un.rows;
-      dst = place(a.ldo);
-      if (SHARED) {
+      if (MODE == kPrefix) {
+        const int row = k.un.r0 + (r < rows ? r : 0), t = row / a.shape.group;
+        dst = from_start ? static_cast<int64_t>(k.s.row0 + t) * a.q_heads + k.h * a.shape.group + row - t * a.shape.group
+                         : a.prefix.info[k.i].extra + static_cast<int64_t>(w) * kRows + r;
+      } else {
+        dst = place(a.ldo);
+      }
+      if (MODE == kBehind) {
         pp.home = -1;
         if (from_start && r < rows && a.tab.skip[k.i] > 0) {
           const int row = k.un.r0 + r, t = row / a.shape.group;
@@ -830,16 +846,16 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const AttnArgs<__half
         }
         __syncwarp();
       }
-      if (from_start && !whole_item) {
+      if (MODE != kPrefix && from_start && !whole_item) {
         // the item's first tile in the line: the share's first tiles, then those of the segments before it
         const int64_t per = line.per, start = w * per + g0;
         rec = make_int4(k.i, k.h, k.u, static_cast<int>((start + k.sp.n - 1) / per));
       }
       g0 += tiles;
-      walk_next<SHARED>(k, a, line);
+      walk_next<MODE>(k, a, line);
     }
     cp_async_wait<0>();   // none is left in flight where a wait ran out
-    if (threadIdx.x == 0) pl.rec[w] = rec;
+    if (MODE != kPrefix && threadIdx.x == 0) pl.rec[w] = rec;
   }
   // ---- teardown: every MMA done, then the tensor memory is freed ------------------------------
   if (warp == kMmaWarp && lane == 0) {
@@ -855,14 +871,14 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const AttnArgs<__half
   }
 }
 
-template <int D, bool SHARED>
+template <int D, int MODE>
 fg_status launch_kernel(const AttnArgs<__half>& a, const ClassPlan& pl, bool own_plan, bool every, cudaStream_t st) {
   using S = Smem<D>;
   static bool set[64] = {false};
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev >= 0 && dev < 64 && !set[dev]) {
-    if (cudaFuncSetAttribute(tile_kernel<D, SHARED>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kBytes) != cudaSuccess)
+    if (cudaFuncSetAttribute(tile_kernel<D, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kBytes) != cudaSuccess)
       return check_launch("tile_kernel smem attribute");
     set[dev] = true;
   }
@@ -870,18 +886,22 @@ fg_status launch_kernel(const AttnArgs<__half>& a, const ClassPlan& pl, bool own
   // Early behind the plan alone.  As a call's first launch or behind the steps the CTAs then would not take the SMs in
   // order, so that neighbours in the line share a head's keys in L2 (a chunk of 2048 rows 459 us, 464 early; 63 single
   // tokens beside a chunk of 512 362 and 367).
-  return paged::launch("tile_kernel", every && !own_plan, tile_kernel<D, SHARED>, static_cast<unsigned>(pl.workers), kThreads, S::kBytes, st, a, pl, wait_limit(), own_plan, every);
+  return paged::launch("tile_kernel", every && !own_plan, tile_kernel<D, MODE>, static_cast<unsigned>(pl.workers), kThreads, S::kBytes, st, a, pl, wait_limit(), own_plan, every);
 }
 
 template <int D>
 fg_status launch(const AttnArgs<__half>& a, const ClassPlan& pl, bool own_plan, bool every, cudaStream_t st) {
-  return a.tab.skip != nullptr ? launch_kernel<D, true>(a, pl, own_plan, every, st) : launch_kernel<D, false>(a, pl, own_plan, every, st);
+  return a.tab.skip != nullptr ? launch_kernel<D, kBehind>(a, pl, own_plan, every, st) : launch_kernel<D, kAlone>(a, pl, own_plan, every, st);
 }
 
 }  // namespace
 
 fg_status paged_attention_tile(const AttnArgs<__half>& a, const ClassPlan& pl, int head_dim, bool own_plan, bool every, cudaStream_t st) {
   return head_dim == 128 ? launch<128>(a, pl, own_plan, every, st) : launch<64>(a, pl, own_plan, every, st);
+}
+
+fg_status paged_prefix_tile(const AttnArgs<__half>& a, const ClassPlan& pl, int head_dim, cudaStream_t st) {
+  return head_dim == 128 ? launch_kernel<128, kPrefix>(a, pl, false, true, st) : launch_kernel<64, kPrefix>(a, pl, false, true, st);
 }
 
 }  // namespace paged
