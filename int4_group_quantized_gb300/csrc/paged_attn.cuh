@@ -23,7 +23,7 @@ struct Prefix {
   float* extra;                   // [workers][kPrefixRows][D], then [workers][kTileRows][D]: of the unit that a share goes on with
   float2* extra_stat;
 };
-constexpr int kPrefixRows = 128;  // most rows of a unit of paged_prefix.cu
+constexpr int kPrefixRows = 64;   // most rows of a unit of paged_prefix.cu
 
 // Where one row's parts lie.
 struct PrefixParts {
