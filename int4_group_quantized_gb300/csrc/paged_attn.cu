@@ -345,6 +345,8 @@ Layout layout_of(const fg_page_pool& pool, const fg_page_table& t, int32_t q_hea
     };
     take(l.skip, 4 * static_cast<size_t>(t.seqs));
     take(l.prefix.info, sizeof(PrefixGroup) * static_cast<size_t>(t.seqs));
+    take(l.prefix.home_row, 4 * static_cast<size_t>(t.seqs));
+    take(l.prefix.planned, 4);
     const size_t extra = static_cast<size_t>(kMaxSms) * (kPrefixRows + (l.tile.workers ? kTileRows : 0));
     if (l.tile.workers) {
       l.tall.workers = l.tile.workers;
@@ -393,8 +395,10 @@ fg_status launch_attn(const fg_page_pool& pool, const fg_page_table& t, const in
       a.prefix.leader = share->leader;
       a.prefix.begin = share->begin;
       a.prefix.rows = share->rows;
-      FG_TRY(paged_prefix(PrefixArgs{a, l.skip, l.tall, std::min(num_sms(), kMaxSms)}, pool.head_dim, st));
+      const PrefixArgs p{a, l.skip, l.tall, std::min(num_sms(), kMaxSms)};
+      FG_TRY(paged_prefix(p, pool.head_dim, st));
       if (l.tall.workers > 0) FG_TRY(paged_prefix_tile(a, l.tall, pool.head_dim, st));
+      FG_TRY(paged_prefix_join(p, pool.head_dim, st));
       a.tab.skip = l.skip;
     }
   }

@@ -8,7 +8,7 @@ namespace paged {
 
 // What the rows of a shared prefix's groups left behind (paged_prefix.cu, and paged_tile.cu for groups of many rows): sums,
 // maximum (base 2) and normaliser of every row over its group's prefix, in parts.  Part 0 of a row is its home; the parts of
-// later shares of the line are in the shares' own places.
+// later shares of the line are in the shares' own places until they are joined there (paged_prefix_join).
 struct PrefixGroup {
   int64_t base, per;    // tiles of its line before the group, and of a share of the line
   int tiles, rows, units;   // tiles of a unit, rows of a unit, units of a head
@@ -17,7 +17,9 @@ struct PrefixGroup {
 };
 struct Prefix {
   const int32_t *group, *tokens, *first, *leader, *begin, *rows;   // fg_page_share
-  PrefixGroup* info;              // [groups]
+  PrefixGroup* info;              // [*planned], groups that are none with no units among them
+  int32_t* planned;
+  int32_t* home_row;              // [seqs] the home of a sequence's first row
   float* home;                    // [ntok][q_heads][D], rows in the share's order
   float2* home_stat;              // [ntok][q_heads]
   float* extra;                   // [workers][kPrefixRows][D], then [workers][kTileRows][D]: of the unit that a share goes on with
@@ -25,22 +27,9 @@ struct Prefix {
 };
 constexpr int kPrefixRows = 64;   // most rows of a unit of paged_prefix.cu
 
-// Where one row's parts lie.
-struct PrefixParts {
-  int64_t home;         // row of home
-  int extra, stride, count;   // part k = 1 .. count is row extra + (k - 1) * stride of extra
-};
-__device__ __forceinline__ PrefixParts prefix_parts(const Prefix& p, int seq, int t, int h, int gh, int group, int q_heads) {
-  const PrefixGroup g = p.info[p.group[seq]];
-  const int x = p.first[seq] + t, r = x * group + gh, u = r / g.rows;
-  const int64_t start = g.base + (static_cast<int64_t>(h) * g.units + u) * g.tiles;
-  PrefixParts o;
-  o.home = static_cast<int64_t>(g.first_row + x) * q_heads + h * group + gh;
-  const int w = static_cast<int>(start / g.per);
-  o.stride = g.stride;
-  o.extra = g.extra + (w + 1) * g.stride + r - u * g.rows;
-  o.count = static_cast<int>((start + g.tiles - 1) / g.per) - w;
-  return o;
+// The home of row t of a sequence (Table::skip of it > 0), query head hq.
+__device__ __forceinline__ int64_t prefix_home(const Prefix& p, int seq, int t, int hq, int q_heads) {
+  return static_cast<int64_t>(p.home_row[seq] + t) * q_heads + hq;
 }
 
 // Group g as the share has it; list = 0: none, or not one that can be followed.

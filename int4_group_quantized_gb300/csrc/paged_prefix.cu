@@ -42,9 +42,26 @@ constexpr int kKeys = 1 << kPrefixKeysLog2;
 constexpr int kSoftWarps = 8, kKeyWarps = 4, kValueWarps = 3;
 constexpr int kFirstKey = kSoftWarps, kFirstValue = kFirstKey + kKeyWarps, kMmaWarp = kFirstValue + kValueWarps;
 constexpr int kThreads = 32 * (kMmaWarp + 1);
-static_assert(kThreads == 512 && kPrefixRows == 64, "the layout below");
+static_assert(kPrefixRows == 64 && kFirstKey % 4 == 0 , "the layout below");
 constexpr float kLift = 4.0f;          // a row's largest weight is 2^4 or more when its maximum is found (paged_tile.cu)
 constexpr uint32_t kMostHalf = 0x7800u;   // 2^15 as fp16: weights up to it stand
+
+// mbar_wait with each poll asleep for up to kNap ns: a few of the CTA's warps work while most wait, and what those poll
+// takes issue slots from these (half of all instructions were polls).
+constexpr uint32_t kNap = 4000;
+__device__ __forceinline__ bool wait_on(uint64_t* bar, uint32_t parity, uint32_t limit, volatile int* abort) {
+  for (uint32_t i = 0; i < limit; ++i) {
+    uint32_t over;
+    asm volatile("{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3; selp.u32 %0, 1, 0, p; }"
+                 : "=r"(over)
+                 : "r"(smem_u32(bar)), "r"(parity), "r"(kNap)
+                 : "memory");
+    if (over) return true;
+    if ((i & 15u) == 15u && *abort) return false;
+  }
+  *abort = 1;
+  return false;
+}
 
 template <int D>
 struct Smem {
@@ -54,7 +71,8 @@ struct Smem {
   static constexpr int kQPanel = kPrefixRows * 128;
   static constexpr int kQ = D / 64 * kQPanel;
   static constexpr int kSums = kPrefixRows * 8;         // (sum q of group 0, 1) of two rows side by side
-  static constexpr int kBytes = 1024 + 2 * (kV + kP + kQ) + 2 * kSums + 4 * kPrefixRows * 2 + 4 * kPrefixRows * 4 + 256;
+  static constexpr int kMeta = kKeys * 16;              // K's scales and minima in units of the exponent
+  static constexpr int kBytes = 1024 + 2 * (kV + kP + kQ + kMeta) + 2 * kSums + 4 * kPrefixRows * 2 + 4 * kPrefixRows * 4 + 256;
 };
 
 // A share's walk over its segments: parts of one unit's key tiles.
@@ -112,6 +130,14 @@ __device__ __forceinline__ float2 halves(uint32_t h) {   // fp16x2 in fp32
   asm("{ .reg .f16 a, b; mov.b32 {a, b}, %2; cvt.f32.f16 %0, a; cvt.f32.f16 %1, b; }" : "=f"(r.x), "=f"(r.y) : "r"(h));
   return r;
 }
+__device__ __forceinline__ uint32_t mbar_test(uint64_t* bar, uint32_t parity) {   // without waiting
+  uint32_t over;
+  asm volatile("{ .reg .pred p; mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
+               : "=r"(over)
+               : "r"(smem_u32(bar)), "r"(parity)
+               : "memory");
+  return over;
+}
 __device__ __forceinline__ uint32_t max_h2(uint32_t a, uint32_t b) {   // NaN if either is
   uint32_t r;
   asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
@@ -135,6 +161,22 @@ __device__ __forceinline__ void arrived(uint32_t (&a)[8], uint32_t (&b)[8]) {
                  "+r"(b[2]), "+r"(b[3]), "+r"(b[4]), "+r"(b[5]), "+r"(b[6]), "+r"(b[7])
                :
                : "memory");
+}
+// Of eight values of every lane: lane i's (i < 8) is the sum or the maximum of value i over the lanes, in one order.
+template <bool MAX>
+__device__ __forceinline__ float fold8(float (&v)[8]) {
+  const int lane = threadIdx.x & 31;
+  auto join = [](float a, float b) { return MAX ? fmaxf(a, b) : a + b; };
+#pragma unroll
+  for (int o = 4; o > 0; o >>= 1)
+#pragma unroll
+    for (int i = 0; i < o; ++i) {
+      const bool up = lane & o;
+      v[i] = join(up ? v[i + o] : v[i], __shfl_xor_sync(0xffffffffu, up ? v[i] : v[i + o], o));
+    }
+#pragma unroll
+  for (int o = 8; o < 32; o <<= 1) v[0] = join(v[0], __shfl_xor_sync(0xffffffffu, v[0], o));
+  return v[0];
 }
 // Named barrier over a half's 128 threads; true where any of them says so.
 __device__ __forceinline__ bool bar_any(int id, bool pred) {
@@ -160,17 +202,17 @@ __device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_lo, uint32_t a_hi,
       "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(acc ? 1u : 0u)
       : "memory");
 }
-// 64 codes of one group through fp16(fmaf(q, scale, min)) into row r of a swizzled panel; every 8 dims in the order (0, 4),
-// (1, 5), (2, 6), (3, 7).
-__device__ __forceinline__ void restore_group(const uint4& lo, const uint4& hi, float scale, float mn, uint8_t* prow, int r) {
+// 32 codes of a group through fp16(fmaf(q, scale, min)) into row r of a swizzled panel, from its 16-byte piece c0 on; every 8
+// dims in the order (0, 4), (1, 5), (2, 6), (3, 7).
+__device__ __forceinline__ void restore_half(const uint4& code, float scale, float mn, uint8_t* prow, int r, int c0) {
   const float2 lo2 = both(scale * 16777216.0f), hi2 = both(scale * 1048576.0f), m2 = both(mn);
-  const uint32_t words[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+  const uint32_t words[4] = {code.x, code.y, code.z, code.w};
 #pragma unroll
-  for (int c = 0; c < 8; ++c) {
+  for (int c = 0; c < 4; ++c) {
     const uint32_t x = words[c], y = x >> 8;
     const uint4 o = make_uint4(q4::cvt_f16x2(q4::fma_f32x2(halves(x & 0x000F000Fu), lo2, m2)), q4::cvt_f16x2(q4::fma_f32x2(halves(x & 0x00F000F0u), hi2, m2)),
                                q4::cvt_f16x2(q4::fma_f32x2(halves(y & 0x000F000Fu), lo2, m2)), q4::cvt_f16x2(q4::fma_f32x2(halves(y & 0x00F000F0u), hi2, m2)));
-    *reinterpret_cast<uint4*>(prow + ((c ^ (r & 7)) << 4)) = o;
+    *reinterpret_cast<uint4*>(prow + (((c0 + c) ^ (r & 7)) << 4)) = o;
   }
 }
 template <int NG>
@@ -196,22 +238,23 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const PrefixArgs p,
   uint8_t* const sV = sm;
   uint8_t* const sP = sV + 2 * S::kV;
   uint8_t* const sQ = sP + 2 * S::kP;
-  float* const sSum = reinterpret_cast<float*>(sQ + 2 * S::kQ);            // [segment % 2][row / 2][group][row % 2]
+  float4* const sMeta = reinterpret_cast<float4*>(sQ + 2 * S::kQ);         // [stage][key] (scale, scale of group 1, minimum, minimum)
+  float* const sSum = reinterpret_cast<float*>(sMeta + 2 * kKeys);         // [segment % 2][row / 2][group][row % 2]
   float* const sNeg = sSum + 2 * S::kSums / 4;                             // [row] minus the maximum
-  uint32_t* const sTop = reinterpret_cast<uint32_t*>(sNeg + kPrefixRows);  // [row] a tile's largest score, as an ordered key
-  float* const sNorm = reinterpret_cast<float*>(sTop + kPrefixRows);       // [quarter][row]
+  float* const sShrink = sNeg + kPrefixRows;                               // [row] what a new maximum makes of sums
+  float* const sNorm = sShrink + kPrefixRows;                              // [quarter][row] maxima, and normalisers in the end
   uint64_t* const bars = reinterpret_cast<uint64_t*>(sNorm + 4 * kPrefixRows);
   uint64_t* const kfull = bars;        // [stage] K's codes of the tile are in tensor memory
-  uint64_t* const sfull = bars + 2;    // [stage] S^T of the tile is, and K's place is free
-  uint64_t* const sfree = bars + 4;    // [stage] the softmax warps have read it, and the rows' sums
+  uint64_t* const sfull = bars + 2;    // [stage] S^T of the tile is, K's place is free, and P V of the tile two before has completed
   uint64_t* const vfull = bars + 6;    // [stage] V of the tile is in shared memory
-  uint64_t* const pfull = bars + 8;    // [stage] P is
+  uint64_t* const pfull = bars + 8;    // [stage] P is, and S^T and the rows' sums have been read
   uint64_t* const pvdone = bars + 10;  // [stage] P V of the tile has completed
   uint64_t* const qfull = bars + 12;   // [segment % 2] Q of the segment is in shared memory
   uint64_t* const drained = bars + 14; // O of the segment has been read
   uint64_t* const done = bars + 15;    // every MMA has completed
   uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(bars + 16);
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  uint32_t* const sHere = tmem_slot + 2;                                   // [stage][quarter] keys of the tile that are there
   __shared__ PrefixLine line;
 
   const AttnArgs<__half>& a = p.a;
@@ -219,9 +262,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const PrefixArgs p,
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&kfull[i], kKeyWarps);
-      mbar_init(&sfull[i], 1);
-      mbar_init(&sfree[i], kSoftWarps);
-      mbar_init(&vfull[i], 4);
+      mbar_init(&sfull[i], 2);   // the commit, and the issuer itself: it has seen K's barrier and Q's, and so the scales and sums
+      mbar_init(&vfull[i], kValueWarps + NG);
       mbar_init(&pfull[i], kSoftWarps);
       mbar_init(&pvdone[i], 1);
       mbar_init(&qfull[i], kKeyWarps);
@@ -242,156 +284,180 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const PrefixArgs p,
   Walk k;
   walk_begin(k, p, line);
 
-  const int psl = a.pool.ps_log2, psm = (1 << psl) - 1;
-  // page number of a key's table entry (not looked at before `there`), and the key's place in a page of head h
-  auto entry = [&](const Walk& w, int j) { return j < w.s.tokens ? a.tab.table[w.s.leader * a.tab.stride + (j >> psl)] : -1; };
-  auto there = [&](int page) { return static_cast<uint32_t>(page) < static_cast<uint32_t>(a.tab.pages); };
-  auto slot = [&](int page, int h, int j) {
-    return ((static_cast<int64_t>(page) * a.pool.heads + h) << psl) + (j & psm);
-  };
-
-  if (warp >= kFirstKey && warp < kFirstValue) {
-    // ---- K's codes, a key a thread; a segment's Q before its first tile -------------------
-    const int quarter = warp & 3, r = 32 * quarter + lane;
-    int n = 0, seg = 0;
-    uint4 code[2 * NG];
-    auto load = [&](const Walk& w, int x, int page) {
-      const int j = (x << kPrefixKeysLog2) + r;
-      const bool on = j < w.s.tokens && there(page);
-      if (j < w.s.tokens && !on) atomicOr(a.batch.err, DEV_ERR_PAGE);
-      const uint4* c = reinterpret_cast<const uint4*>(a.pool.codes[0] + slot(on ? page : 0, w.h, on ? j : 0) * (D / 2));
-#pragma unroll
-      for (int e = 0; e < 2 * NG; ++e) code[e] = on ? c[e] : make_uint4(0u, 0u, 0u, 0u);
+  if (warp >= kFirstKey && warp < kMmaWarp) {
+    // ---- K's codes and V, a key a lane: warps 8 .. 11 a quarter of every tile's K each, 12 .. 14 quarters 0 .. 2 of V; V's last
+    // quarter, group by group, is the K warps' in turn, which have time for it.
+    const bool value = warp >= kFirstValue;
+    const int quarter = warp & 3, r = 32 * quarter + lane;   // (of 12 .. 14 the same)
+    const int tiles = static_cast<int>(k.left);
+    const int psl = a.pool.ps_log2, psm = (1 << psl) - 1;
+    const uint32_t page_codes = static_cast<uint32_t>(a.pool.heads) * (D / 2) << psl;   // bytes of a page in a codes array
+    const uint32_t page_meta = static_cast<uint32_t>(a.pool.heads) * (4 * NG) << psl;   // and in a (min or scale) array
+    const uint8_t* const codes = value ? a.pool.codes[1] : a.pool.codes[0];
+    const float* const scales = value ? a.pool.scales[1] : a.pool.scales[0];
+    const float* const mins = value ? a.pool.mins[1] : a.pool.mins[0];
+    // a key as it is stored; its row in a page (-1: no key of the prefix), and the table's entry: looked up a tile before it
+    // is loaded, loaded a tile before it is used.  x...: the same of a K warp's group of V
+    uint4 code[2 * NG], xcode[2];
+    float scale[NG], mn[NG], xscale = 0.0f, xmn = 0.0f;
+    bool there = false;
+    Walk w = k;              // of the tile that is looked up next
+    const int32_t* row = a.tab.table + w.s.leader * a.tab.stride;
+    int wx = k.x, seen = 0, loaded = 0, page = -1, off = -1, xpage = -1, xoff = -1;
+    auto extra = [&](int tile) { return !value && (NG == 2 ? (tile & 1) == (quarter >> 1) : (tile & 3) == quarter); };
+    const int xg = NG == 2 ? quarter & 1 : 0;
+    auto look_up = [&]() {
+      off = xoff = -1;
+      if (seen == tiles) return;
+      const int t0 = wx << kPrefixKeysLog2, j = t0 + r, xj = t0 + 96 + lane;
+      if (j < w.s.tokens) {
+        page = row[j >> psl];
+        off = (w.h << psl) + (j & psm);
+      }
+      if (extra(seen) && xj < w.s.tokens) {
+        xpage = row[xj >> psl];
+        xoff = (w.h << psl) + (xj & psm);
+      }
+      ++seen;
+      if (++wx == w.x1) {
+        walk_next(w, p);
+        wx = w.x;
+        row = a.tab.table + w.s.leader * a.tab.stride;
+      }
     };
+    auto is_page = [&](int e) { return static_cast<uint32_t>(e) < static_cast<uint32_t>(a.tab.pages); };
+    auto load = [&]() {
+      asm volatile("" : "+r"(page), "+r"(xpage));   // the entries are waited for here and not where they were asked for
+      there = off >= 0 && is_page(page);
+#pragma unroll
+      for (int e = 0; e < 2 * NG; ++e) code[e] = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+      for (int g = 0; g < NG; ++g) scale[g] = mn[g] = 0.0f;
+      if (there) {
+        const uint64_t at = static_cast<uint64_t>(static_cast<uint32_t>(page)) * page_codes + static_cast<uint32_t>(off) * (D / 2);
+        const uint64_t am = static_cast<uint64_t>(static_cast<uint32_t>(page)) * page_meta + static_cast<uint32_t>(off) * (4 * NG);
+        const uint4* c = reinterpret_cast<const uint4*>(codes + at);
+#pragma unroll
+        for (int e = 0; e < 2 * NG; ++e) code[e] = c[e];
+        load_meta(scale, scales, am);
+        load_meta(mn, mins, am);
+      } else if (off >= 0 && !value) {
+        atomicOr(a.batch.err, DEV_ERR_PAGE);
+      }
+      if (extra(loaded)) {
+        xcode[0] = xcode[1] = make_uint4(0u, 0u, 0u, 0u);
+        xscale = xmn = 0.0f;
+        if (xoff >= 0 && is_page(xpage)) {
+          const uint64_t at = static_cast<uint64_t>(static_cast<uint32_t>(xpage)) * page_codes + static_cast<uint32_t>(xoff) * (D / 2);
+          const uint64_t am = static_cast<uint64_t>(static_cast<uint32_t>(xpage)) * page_meta + static_cast<uint32_t>(xoff) * (4 * NG);
+          const uint4* c = reinterpret_cast<const uint4*>(a.pool.codes[1] + at) + 2 * xg;
+          xcode[0] = c[0];
+          xcode[1] = c[1];
+          xscale = reinterpret_cast<const float*>(reinterpret_cast<const char*>(a.pool.scales[1]) + am)[xg];
+          xmn = reinterpret_cast<const float*>(reinterpret_cast<const char*>(a.pool.mins[1]) + am)[xg];
+        }
+      }
+      ++loaded;
+    };
+    // a group whose scale is not finite is NaN for all rows: they all see the key
+    auto finite = [](float f) { return fabsf(f) < INFINITY ? f : __uint_as_float(0x7fffffffu); };
+    look_up();
+    load();
+    look_up();
     bool ok = true;
-    while (k.left > 0 && ok) {
-      // Q and the sums of this segment's place were last used two segments ago: by S of a tile two or more before this
-      // one, and by the softmax that followed it
-      if (n >= 2) ok = mbar_wait(&sfree[n & 1], ((n >> 1) - 1) & 1, wait_limit, abort_flag);
+    int seg = 0, x = k.x;
+    for (int n = 0; n < tiles; ++n) {
+      if (value) {
+        ok = n < 2 || wait_on(&pvdone[n & 1], ((n >> 1) - 1) & 1, wait_limit, abort_flag);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        uint8_t* const to = sV + (n & 1) * S::kV + r * 128;
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+          restore_half(code[2 * g], finite(scale[g]), mn[g], to + g * S::kPanel, r, 0);
+          restore_half(code[2 * g + 1], finite(scale[g]), mn[g], to + g * S::kPanel, r, 4);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&vfull[n & 1]);
+        load();      // behind the fence, which would wait for it
+        look_up();
+        continue;
+      }
+      // P of the tile two before is there: S has read its codes, the softmax its scales.  (And Q and the sums of the segment
+      // two before, whose place a new one takes: its last tile is no later.)
+      ok = n < 2 || wait_on(&pfull[n & 1], ((n >> 1) - 1) & 1, wait_limit, abort_flag);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
-      int page = entry(k, (k.x << kPrefixKeysLog2) + r);
-      load(k, k.x, page);
-      page = entry(k, ((k.x + 1) << kPrefixKeysLog2) + r);
-      {
+      if (x == k.x) {
         uint8_t* const q = sQ + (seg & 1) * S::kQ;
         float* const sum = sSum + (seg & 1) * (S::kSums / 4);
         constexpr int kPieces = D / 8;                    // 16 bytes each, a lane a piece
         const int pc = lane % kPieces, all = k.s.list * a.shape.group, r0 = k.u * k.at.rows;
-        for (int i = quarter * (32 / kPieces) + lane / kPieces; i < k.at.rows; i += kKeyWarps * (32 / kPieces)) {
-          const int row = r0 + i, x = row / a.shape.group;
+        for (int m = quarter * (32 / kPieces) + lane / kPieces; m < k.at.rows; m += kKeyWarps * (32 / kPieces)) {
+          const int row = r0 + m, lx = row / a.shape.group;
           const bool on = row < all;
-          const __half* from = a.q + static_cast<int64_t>(on ? listed_row(a.prefix, a.batch, k.s.first + x) : 0) * a.ldq +
-                               static_cast<int64_t>(k.h * a.shape.group + (on ? row - x * a.shape.group : 0)) * D + 8 * pc;
-          const uint4 v = on ? *reinterpret_cast<const uint4*>(from) : make_uint4(0u, 0u, 0u, 0u);
+          const __half* from = a.q + static_cast<int64_t>(on ? listed_row(a.prefix, a.batch, k.s.first + lx) : 0) * a.ldq +
+                               static_cast<int64_t>(k.h * a.shape.group + (on ? row - lx * a.shape.group : 0)) * D + 8 * pc;
+          const uint4 u = on ? *reinterpret_cast<const uint4*>(from) : make_uint4(0u, 0u, 0u, 0u);
           // every 8 dims in the codes' order
-          *reinterpret_cast<uint4*>(q + (pc >> 3) * S::kQPanel + i * 128 + (((pc & 7) ^ (i & 7)) << 4)) =
-              make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632), __byte_perm(v.y, v.w, 0x5410), __byte_perm(v.y, v.w, 0x7632));
-          const float2 f0 = halves(v.x), f1 = halves(v.y), f2 = halves(v.z), f3 = halves(v.w);
+          *reinterpret_cast<uint4*>(q + (pc >> 3) * S::kQPanel + m * 128 + (((pc & 7) ^ (m & 7)) << 4)) =
+              make_uint4(__byte_perm(u.x, u.z, 0x5410), __byte_perm(u.x, u.z, 0x7632), __byte_perm(u.y, u.w, 0x5410), __byte_perm(u.y, u.w, 0x7632));
+          const float2 f0 = halves(u.x), f1 = halves(u.y), f2 = halves(u.z), f3 = halves(u.w);
           float s = ((f0.x + f0.y) + (f1.x + f1.y)) + ((f2.x + f2.y) + (f3.x + f3.y));
 #pragma unroll
           for (int o = 1; o < 8; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);   // rows are a multiple of 16: every lane comes as often
-          if ((pc & 7) == 0) sum[(i >> 1) * 4 + (pc >> 3) * 2 + (i & 1)] = s;
+          if ((pc & 7) == 0) sum[(m >> 1) * 4 + (pc >> 3) * 2 + (m & 1)] = s;
         }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&qfull[seg & 1]);
       }
-      for (int x = k.x; x < k.x1; ++x, ++n) {
-        ok = n < 2 || mbar_wait(&sfull[n & 1], ((n >> 1) - 1) & 1, wait_limit, abort_flag);
+      tc_fence_after();
+      const uint32_t to = tmem + kCodes + 64 * (n & 1) + (static_cast<uint32_t>(32 * quarter) << 16);
+#pragma unroll
+      for (int e = 0; e < 2 * NG; ++e) {
+        uint32_t o[16];
+        const uint32_t c4[4] = {code[e].x, code[e].y, code[e].z, code[e].w};
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          o[4 * c] = c4[c] & 0x000F000Fu;
+          o[4 * c + 1] = (c4[c] >> 4) & 0x000F000Fu;
+          o[4 * c + 2] = (c4[c] >> 8) & 0x000F000Fu;
+          o[4 * c + 3] = (c4[c] >> 12) & 0x000F000Fu;
+        }
+        tmem_st_32x32b_x16(to + 16 * e, o);
+      }
+      // a code in the MMA is c * 2^-24; a scale that is not finite makes the key's scores NaN
+      const float unit = a.scale_log2 * 16777216.0f;
+      sMeta[(n & 1) * kKeys + r] = make_float4(finite(scale[0]) * unit, finite(scale[NG - 1]) * unit, mn[0] * a.scale_log2, mn[NG - 1] * a.scale_log2);
+      const uint32_t here = __ballot_sync(0xffffffffu, there);
+      if (lane == 0) sHere[4 * (n & 1) + quarter] = here;
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&kfull[n & 1]);
+      if (extra(n)) {
+        ok = n < 2 || wait_on(&pvdone[n & 1], ((n >> 1) - 1) & 1, wait_limit, abort_flag);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        tc_fence_after();
-        const uint32_t to = tmem + kCodes + 64 * (n & 1) + (static_cast<uint32_t>(32 * quarter) << 16);
-#pragma unroll
-        for (int g = 0; g < NG; ++g) {
-          uint32_t o[32];
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const uint32_t w[4] = {code[2 * g + e].x, code[2 * g + e].y, code[2 * g + e].z, code[2 * g + e].w};
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              o[16 * e + 4 * c] = w[c] & 0x000F000Fu;
-              o[16 * e + 4 * c + 1] = (w[c] >> 4) & 0x000F000Fu;
-              o[16 * e + 4 * c + 2] = (w[c] >> 8) & 0x000F000Fu;
-              o[16 * e + 4 * c + 3] = (w[c] >> 12) & 0x000F000Fu;
-            }
-          }
-          tmem_st_32x32b_x32(to + 32 * g, o);
+        uint8_t* const vto = sV + (n & 1) * S::kV + xg * S::kPanel + (96 + lane) * 128;
+#pragma unroll 1
+        for (int e = 0; e < 2; ++e) {
+          restore_half(xcode[0], finite(xscale), xmn, vto, lane, 4 * e);   // (row 96 + lane: the same swizzle)
+          xcode[0] = xcode[1];
         }
-        if (x + 1 < k.x1) {
-          load(k, x + 1, page);
-          page = entry(k, ((x + 2) << kPrefixKeysLog2) + r);
-        }
-        tmem_st_wait();
-        tc_fence_before();
+        fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&kfull[n & 1]);
+        if (lane == 0) mbar_arrive(&vfull[n & 1]);
       }
-      ++seg;
-      walk_next(k, p);
-    }
-  } else if (warp >= kFirstValue && warp < kMmaWarp) {
-    // ---- V, 32 keys a task, four tasks a tile, dealt round the warps ------------------------
-    Walk w = k;              // of the task that is loaded next
-    int x = k.x, at = 0, n = warp - kFirstValue;   // its tile, that tile's number, the task in hand
-    const int tasks = k.left > 0 ? static_cast<int>(4 * k.left) : 0;
-    auto go_to = [&](int tile) {   // the walk at the tile of that number
-      while (at < tile) {
-        ++at;
-        if (++x == w.x1) {
-          walk_next(w, p);
-          x = w.x;
-          if (w.left == 0) return;
-        }
+      load();      // behind the arrivals, which would wait for it
+      look_up();
+      if (++x == k.x1) {
+        ++seg;
+        walk_next(k, p);
+        x = k.x;
       }
-    };
-    uint4 code[2 * NG];
-    float scale[NG], mn[NG];
-    int page = -1, j = 0, h = 0;
-    bool in = false;
-    auto look_up = [&](int task) {   // the lane's key and its table entry
-      in = task < tasks;
-      if (!in) return;
-      go_to(task >> 2);
-      j = (x << kPrefixKeysLog2) + 32 * (task & 3) + lane;
-      h = w.h;
-      in = j < w.s.tokens;
-      page = entry(w, j);
-    };
-    auto load = [&]() {
-      const bool on = in && there(page);
-      const int64_t s = slot(on ? page : 0, h, on ? j : 0);
-      const uint4* c = reinterpret_cast<const uint4*>(a.pool.codes[1] + s * (D / 2));
-#pragma unroll
-      for (int e = 0; e < 2 * NG; ++e) code[e] = on ? c[e] : make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-      for (int g = 0; g < NG; ++g) scale[g] = mn[g] = 0.0f;
-      if (on) {
-        load_meta(scale, a.pool.scales[1], s * (4 * NG));
-        load_meta(mn, a.pool.mins[1], s * (4 * NG));
-      }
-    };
-    look_up(n);
-    load();
-    look_up(n + kValueWarps);
-    for (; n < tasks; n += kValueWarps) {
-      const int g = n >> 2, r = 32 * (n & 3) + lane;
-      bool ok = g < 2 || mbar_wait(&pvdone[g & 1], ((g >> 1) - 1) & 1, wait_limit, abort_flag);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
-      uint8_t* const to = sV + (g & 1) * S::kV + r * 128;
-#pragma unroll
-      for (int q = 0; q < NG; ++q) {
-        // a group whose scale is not finite is NaN for all rows: they all see the key
-        const float sc = fabsf(scale[q]) < INFINITY ? scale[q] : __uint_as_float(0x7fffffffu);
-        restore_group(code[2 * q], code[2 * q + 1], sc, mn[q], to + q * S::kPanel, r);
-      }
-      load();
-      look_up(n + 2 * kValueWarps);
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&vfull[g & 1]);
     }
   } else if (warp == kMmaWarp) {
     // ---- MMA issuer --------------------------------------------------------------------
@@ -402,19 +468,26 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const PrefixArgs p,
       int n = 0, seg = 0;
       bool ok = true, pending = false;
       auto wait = [&](uint64_t* bar, int phase) {
-        if (ok) ok = mbar_wait(bar, phase & 1, wait_limit, abort_flag);
+        if (ok) ok = wait_on(bar, phase & 1, wait_limit, abort_flag);
         return ok;
       };
+      // A wait takes some 250 cycles even where it is over, and a batch of MMAs 600 to issue: so barriers are looked at before
+      // a batch is issued, and waited for after it only where they were not over yet.
+      auto look = [&](uint64_t* bar, int phase) { return mbar_test(bar, phase & 1); };
+      uint32_t k_in = 0;
       // P V of tile g; first: of its segment, whose number is `of` and whose unit has `rows` rows
-      auto issue_o = [&](int g, bool first, int of, int rows) {
+      auto issue_o = [&](int g, bool first, int of, int rows, uint32_t v_in, uint32_t p_in) {
         if (first && of > 0 && !wait(drained, of - 1)) return;
-        if (!wait(&vfull[g & 1], g >> 1) || !wait(&pfull[g & 1], g >> 1)) return;
+        if (!v_in && !wait(&vfull[g & 1], g >> 1)) return;
+        if (!p_in && !wait(&pfull[g & 1], g >> 1)) return;
         tc_fence_after();
         const uint32_t idesc = idesc_f16(128, 0, 1, 1) + (static_cast<uint32_t>(rows >> 2) << 17);   // 2 rows columns
 #pragma unroll
-        for (int kk = 0; kk < kKeys / 16; ++kk)
+        for (int kk = 0; kk < kKeys / 16; ++kk) {
+          if (kk == kKeys / 16 - 2) k_in = look(&kfull[g & 1], (g + 2) >> 1);   // of tile g + 2, late in the batch
           mma_ss(tmem + kOut, v_lo + (g & 1) * (S::kV >> 4) + kk * (2048 >> 4), kDescHi, p_lo + (g & 1) * (S::kP >> 4) + kk * (2048 >> 4), kDescHi, idesc,
                  !first || kk > 0);
+        }
         mma_commit(&pvdone[g & 1]);
       };
       bool first = false;   // of the tile before this one
@@ -423,17 +496,20 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const PrefixArgs p,
         const uint32_t idesc = idesc_f16(128, 0, 0, 0) + (static_cast<uint32_t>(k.at.rows >> 3) << 17);
         if (!wait(&qfull[seg & 1], seg >> 1)) break;
         for (int x = k.x; x < k.x1; ++x, ++n) {
-          if (!wait(&kfull[n & 1], n >> 1)) break;
-          if (n >= 2 && !wait(&sfree[n & 1], (n >> 1) - 1)) break;
+          // S's place is free: P of the tile two before was waited for
+          if (!k_in && !wait(&kfull[n & 1], n >> 1)) break;
           tc_fence_after();
+          const uint32_t v_in = pending ? look(&vfull[(n - 1) & 1], (n - 1) >> 1) : 0u, p_in = pending ? look(&pfull[(n - 1) & 1], (n - 1) >> 1) : 0u;
 #pragma unroll
           for (int g = 0; g < NG; ++g)
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
               mma_ts(tmem + kScore + 128 * (n & 1) + 64 * g, tmem + kCodes + 64 * (n & 1) + 32 * g + 8 * kk,
                      q_lo + (((seg & 1) * S::kQ + g * S::kQPanel + 32 * kk) >> 4), kDescHi, idesc, kk > 0);
+          mbar_arrive(&sfull[n & 1]);
           mma_commit(&sfull[n & 1]);
-          if (pending) issue_o(n - 1, first, of, rows);
+          k_in = 0;
+          if (pending) issue_o(n - 1, first, of, rows, v_in, p_in);
           if (!ok) break;
           pending = true;
           first = x == k.x;
@@ -443,7 +519,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const PrefixArgs p,
         ++seg;
         walk_next(k, p);
       }
-      if (ok && pending) issue_o(n - 1, first, of, rows);
+      if (ok && pending) issue_o(n - 1, first, of, rows, 0u, 0u);
       mma_commit(done);
     }
     __syncwarp();
@@ -454,94 +530,70 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const PrefixArgs p,
     const int bar = 1 + half;
     int n = 0, seg = 0;
     bool ok = true;
-    // the key's scales and minima of K, in units of the exponent
-    float ks[NG], km[NG];
-    bool here = false;
-    auto load = [&](const Walk& w, int x, int page) {
-      const int j = (x << kPrefixKeysLog2) + r;
-      here = j < w.s.tokens && there(page);
-#pragma unroll
-      for (int g = 0; g < NG; ++g) ks[g] = km[g] = 0.0f;
-      if (here) {
-        const int64_t s = slot(page, w.h, j) * (4 * NG);
-        load_meta(ks, a.pool.scales[0], s);
-        load_meta(km, a.pool.mins[0], s);
-      }
-    };
     while (k.left > 0) {
       const int rows = k.at.rows / 2, chunks = rows / 8, first = half * rows;   // of this half
       const float* const sum = sSum + (seg & 1) * (S::kSums / 4) + first * 2;
       float2 l[16];        // the normaliser's part of this key and those 128 after it, of two rows each
 #pragma unroll
       for (int i = 0; i < 16; ++i) l[i] = both(0.0f);
-      int page = entry(k, (k.x << kPrefixKeysLog2) + r);
-      load(k, k.x, page);
-      page = entry(k, ((k.x + 1) << kPrefixKeysLog2) + r);
-      ok = mbar_wait(&qfull[seg & 1], (seg >> 1) & 1, wait_limit, abort_flag);   // the rows' sums
       bool gave_up = false;
       for (int x = k.x; x < k.x1; ++x, ++n) {
         const int st = n & 1;
         const uint32_t ts = tmem + kScore + 128 * st + lanes + first;
-        float2 s2[NG], m2[NG];
-#pragma unroll
-        for (int g = 0; g < NG; ++g) {
-          // a code in the MMA is c * 2^-24; a scale that is not finite makes the key's scores NaN
-          s2[g] = both(fabsf(ks[g]) < INFINITY ? ks[g] * (a.scale_log2 * 16777216.0f) : __uint_as_float(0x7fffffffu));
-          m2[g] = both(km[g] * a.scale_log2);
-        }
-        const bool on = here;
-        if (x + 1 < k.x1) {
-          load(k, x + 1, page);
-          page = entry(k, ((x + 2) << kPrefixKeysLog2) + r);
-        }
-        ok = ok && mbar_wait(&sfull[st], (n >> 1) & 1, wait_limit, abort_flag);
+        ok = wait_on(&sfull[st], (n >> 1) & 1, wait_limit, abort_flag);
         ok = __all_sync(0xffffffffu, ok);
         tc_fence_after();
+        const float4 meta = sMeta[st * kKeys + r];
+        const float2 s2[2] = {both(meta.x), both(meta.y)}, m2[2] = {both(meta.z), both(meta.w)};
+        const bool on = (sHere[4 * st + quarter] >> lane) & 1u;
         // scores of rows 8 c .. 8 c + 7 of the half, on top of from(row)
-        auto scores = [&](int c, float2 (&z)[4], auto from) {
-          uint32_t u[8], v[8];
+        auto fetch = [&](int c, uint32_t (&u)[8], uint32_t (&v)[8]) {
           tmem_ld8(ts + 8 * c, u);
           if (NG == 2) tmem_ld8(ts + 64 + 8 * c, v);
-          else
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = 0u;
-          arrived(u, v);
+        };
+        auto scores_of = [&](int c, const uint32_t (&u)[8], const uint32_t (&v)[8], float2 (&z)[4], auto from) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const float4 q = *reinterpret_cast<const float4*>(sum + 4 * (4 * c + e));
             float2 t = q4::fma_f32x2(m2[0], make_float2(q.x, q.y), from(8 * c + 2 * e));
-            if (NG == 2) t = q4::fma_f32x2(m2[NG - 1], make_float2(q.z, q.w), t);
+            if (NG == 2) t = q4::fma_f32x2(m2[1], make_float2(q.z, q.w), t);
             t = q4::fma_f32x2(s2[0], make_float2(__uint_as_float(u[2 * e]), __uint_as_float(u[2 * e + 1])), t);
-            if (NG == 2) t = q4::fma_f32x2(s2[NG - 1], make_float2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])), t);
+            if (NG == 2) t = q4::fma_f32x2(s2[1], make_float2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])), t);
             z[e] = t;
           }
+        };
+        auto scores = [&](int c, float2 (&z)[4], auto from) {
+          uint32_t u[8], v[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+          fetch(c, u, v);
+          arrived(u, v);
+          scores_of(c, u, v, z, from);
         };
         auto below = [&](int i) {   // minus the maximum of rows i, i + 1 of the half; a key that is not there weighs nothing
           const float2 m = *reinterpret_cast<const float2*>(sNeg + first + i);
           return on ? m : both(-INFINITY);
         };
-        // the tile's largest score of every row of the half, as ordered keys (two barriers around it)
+        // the tile's largest score of every row of the half: a row's 32 keys of the warp to one lane, the four warps through
+        // sNorm (a barrier after it)
         auto find = [&]() {
-          if (quarter == 0 && lane < rows) sTop[first + lane] = 0u;
-          bar_any(bar, false);
           if (ok)
 #pragma unroll 1
             for (int c = 0; c < chunks; ++c) {
               float2 z[4];
               scores(c, z, [](int) { return both(0.0f); });
+              float v[8];
 #pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                const float f = on ? (e & 1 ? z[e / 2].y : z[e / 2].x) : -INFINITY;
-                const uint32_t b = __float_as_uint(f), key = f != f ? 0u : b & 0x80000000u ? ~b : b | 0x80000000u;
-                const uint32_t top = __reduce_max_sync(0xffffffffu, key);
-                if (lane == e) atomicMax(sTop + first + 8 * c + e, top);
+              for (int e = 0; e < 4; ++e) {
+                v[2 * e] = on ? fmaxf(z[e].x, -INFINITY) : -INFINITY;    // a NaN is no maximum
+                v[2 * e + 1] = on ? fmaxf(z[e].y, -INFINITY) : -INFINITY;
               }
+              const float top = fold8<true>(v);
+              if (lane < 8) sNorm[quarter * kPrefixRows + first + 8 * c + lane] = top;
             }
           bar_any(bar, false);
         };
         auto top_of = [&](int i) {
-          const uint32_t key = sTop[first + i];
-          return key == 0u ? -INFINITY : __uint_as_float(key & 0x80000000u ? key & 0x7fffffffu : ~key);
+          const float* const c = sNorm + first + i;
+          return fmaxf(fmaxf(c[0], c[kPrefixRows]), fmaxf(c[2 * kPrefixRows], c[3 * kPrefixRows]));
         };
         // A row without a maximum has minus infinity's: +infinity, which takes the weights of any key that is there out of
         // fp16, so that a tile that has one finds it.
@@ -553,8 +605,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const PrefixArgs p,
           }
           bar_any(bar, false);
         }
-        if (ok && n >= 2) ok = mbar_wait(&pvdone[st], ((n >> 1) - 1) & 1, wait_limit, abort_flag);   // P's place is free
-        ok = __all_sync(0xffffffffu, ok);
         uint8_t* const sp = sP + st * S::kP + r * 128;
         const int lo_chunk = k.at.rows / 8;
         uint32_t most = 0u;   // of the weights, as fp16 pairs
@@ -604,15 +654,15 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const PrefixArgs p,
             const bool ask = top + old > 15.0f;
             const float neg = ask ? kLift - top : old;
             sNeg[first + lane] = neg;
-            reinterpret_cast<float*>(sTop)[first + lane] = !ask ? 1.0f : old == INFINITY ? 0.0f : ex2_approx(neg - old);
+            sShrink[first + lane] = !ask ? 1.0f : old == INFINITY ? 0.0f : ex2_approx(neg - old);
           }
           bar_any(bar, false);
-          const float* const shrink = reinterpret_cast<const float*>(sTop) + first;
+          const float* const shrink = sShrink + first;
 #pragma unroll
           for (int i = 0; i < 16; ++i)
             if (2 * i < rows) l[i] = make_float2(l[i].x * shrink[2 * i], l[i].y * shrink[2 * i + 1]);
           if (ok && x > k.x) {   // the segment's sums so far
-            ok = mbar_wait(&pvdone[st ^ 1], ((n - 1) >> 1) & 1, wait_limit, abort_flag);
+            ok = wait_on(&pvdone[st ^ 1], ((n - 1) >> 1) & 1, wait_limit, abort_flag);
             ok = __all_sync(0xffffffffu, ok);
             tc_fence_after();
             if (ok)
@@ -640,30 +690,25 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const PrefixArgs p,
         __syncwarp();
         if (lane == 0) {
           mbar_arrive(&pfull[st]);
-          mbar_arrive(&sfree[st]);
         }
       }
       if (gave_up) break;
       // ---- the segment's rows: their parts ------------------------------------------------
-      ok = mbar_wait(&pvdone[(n - 1) & 1], ((n - 1) >> 1) & 1, wait_limit, abort_flag);
+      ok = wait_on(&pvdone[(n - 1) & 1], ((n - 1) >> 1) & 1, wait_limit, abort_flag);
       ok = __all_sync(0xffffffffu, ok);
       tc_fence_after();
-      {   // the normaliser: a row's 32 keys of the warp to one lane, the four warps in order
-        float v[32];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          v[2 * i] = l[i].x;
-          v[2 * i + 1] = l[i].y;
-        }
+      for (int c = 0; c < 4; ++c)   // the normaliser: a row's 32 keys of the warp to one lane, the four warps in order
+        if (c < chunks) {
+          float v[8];
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1)
-#pragma unroll
-          for (int i = 0; i < o; ++i) {
-            const bool up = lane & o;
-            v[i] = (up ? v[i + o] : v[i]) + __shfl_xor_sync(0xffffffffu, up ? v[i] : v[i + o], o);
+          for (int e = 0; e < 4; ++e) {
+            v[2 * e] = l[4 * c + e].x;
+            v[2 * e + 1] = l[4 * c + e].y;
           }
-        if (lane < rows) sNorm[quarter * kPrefixRows + first + lane] = v[0];
-      }
+          const float all = fold8<false>(v);
+          if (lane < 8) sNorm[quarter * kPrefixRows + first + 8 * c + lane] = all;
+        }
       if (bar_any(bar, !ok)) break;
       // where row `first` + lane of the unit goes
       const int row = k.u * k.at.rows + first + lane;
@@ -713,6 +758,69 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const PrefixArgs p,
   }
 }
 
+// ---- joining: a row's parts to its home, in order ----------------------------------------------------
+constexpr int kJoinThreads = 256;
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const PrefixArgs p) {
+  constexpr int kCols = D / 4, kAtOnce = kJoinThreads / kCols, kFew = 4;
+  griddep_launch();
+  griddep_wait();
+  const AttnArgs<__half>& a = p.a;
+  const int col = threadIdx.x % kCols, group = a.shape.group;
+  const uint32_t mates = D == 128 ? 0xffffffffu : 0xffffu << (threadIdx.x & 16);   // a row's lanes
+  const int listed = a.prefix.begin[a.tab.seqs], planned = *a.prefix.planned;
+  const int64_t pairs = static_cast<int64_t>(listed < 0 || listed > a.batch.ntok ? 0 : listed) * a.q_heads;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kAtOnce + threadIdx.x / kCols; i < pairs; i += static_cast<int64_t>(gridDim.x) * kAtOnce) {
+    const int x = static_cast<int>(i / a.q_heads), hq = static_cast<int>(i - static_cast<int64_t>(x) * a.q_heads);
+    int g = -1;              // the last group that begins at x or before, found by the row's lanes together
+    for (int n = kCols; n == kCols;) {
+      const int c = g + 1 + col;
+      n = __popc(__ballot_sync(mates, c < planned && a.prefix.begin[c] <= x));
+      g += n;
+    }
+    if (g < 0 || shared_group(a.prefix, a.tab, a.batch, g).list == 0) continue;
+    const PrefixGroup at = a.prefix.info[g];
+    const int h = hq / group, r = (x - at.first_row) * group + hq - h * group, u = r / at.rows;
+    if (r < 0 || u >= at.units) continue;
+    const int64_t start = at.base + (static_cast<int64_t>(h) * at.units + u) * at.tiles;
+    const int w = static_cast<int>(start / at.per), count = static_cast<int>((start + at.tiles - 1) / at.per) - w;
+    if (count == 0) continue;
+    float* const home = a.prefix.home + i * D + 4 * col;
+    const int64_t extra = at.extra + static_cast<int64_t>(w + 1) * at.stride + r - u * at.rows;
+    float2 s = a.prefix.home_stat[i];
+    float4 o = *reinterpret_cast<const float4*>(home);
+    float m = s.x, l = s.y;
+    for (int k0 = 0; k0 < count; k0 += kFew) {
+      float2 st[kFew];
+      float4 v[kFew];
+#pragma unroll
+      for (int k = 0; k < kFew; ++k) {
+        st[k] = make_float2(-INFINITY, 0.0f);
+        v[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (k0 + k < count) {
+          const int64_t row = extra + static_cast<int64_t>(k0 + k) * at.stride;
+          st[k] = a.prefix.extra_stat[row];
+          v[k] = *reinterpret_cast<const float4*>(a.prefix.extra + row * D + 4 * col);
+        }
+      }
+      const float top = fmaxf(fmaxf(m, fmaxf(st[0].x, st[1].x)), fmaxf(st[2].x, st[3].x)), base = top == -INFINITY ? 0.0f : top;
+      const float f0 = exp2f(m - base);
+      l *= f0;
+      o = make_float4(o.x * f0, o.y * f0, o.z * f0, o.w * f0);
+#pragma unroll
+      for (int k = 0; k < kFew; ++k) {
+        const float f = exp2f(st[k].x - base);
+        l = fmaf(st[k].y, f, l);
+        o = make_float4(fmaf(v[k].x, f, o.x), fmaf(v[k].y, f, o.y), fmaf(v[k].z, f, o.z), fmaf(v[k].w, f, o.w));
+      }
+      m = top;
+    }
+    *reinterpret_cast<float4*>(home) = o;
+    __syncwarp(mates);       // all have read it
+    if (col == 0) a.prefix.home_stat[i] = make_float2(m, l);
+  }
+}
+
 template <int D>
 fg_status launch(const PrefixArgs& p, cudaStream_t st) {
   using S = Smem<D>;
@@ -729,6 +837,13 @@ fg_status launch(const PrefixArgs& p, cudaStream_t st) {
 }
 
 }  // namespace
+
+fg_status paged_prefix_join(const PrefixArgs& p, int head_dim, cudaStream_t st) {
+  const int64_t want = (static_cast<int64_t>(p.a.batch.ntok) * p.a.q_heads * (head_dim / 4) + kJoinThreads - 1) / kJoinThreads, cap = 8 * static_cast<int64_t>(p.workers);
+  Trace tr(KC_ATTN_COMBINE, st);
+  return paged::launch("prefix_join_kernel", true, head_dim == 128 ? prefix_join_kernel<128> : prefix_join_kernel<64>,
+                       static_cast<unsigned>(want < cap ? want : cap), kJoinThreads, 0, st, p);
+}
 
 fg_status paged_prefix(const PrefixArgs& p, int head_dim, cudaStream_t st) { return head_dim == 128 ? launch<128>(p, st) : launch<64>(p, st); }
 

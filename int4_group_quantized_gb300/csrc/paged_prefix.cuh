@@ -66,7 +66,13 @@ __device__ __forceinline__ void prefix_line(const PrefixArgs& p, PrefixLine& lin
   const AttnArgs<__half>& a = p.a;
   const Table& t = a.tab;
   const int group = a.shape.group, heads = a.pool.heads, lane = threadIdx.x & 31;
-  for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < t.seqs; i += gridDim.x * blockDim.x) p.skip[i] = shared_tokens(a, i);
+  // (the sequences one a CTA in turn, by its last threads: the plan does not wait for them)
+  if (threadIdx.x >= blockDim.x / 2)
+    for (int64_t i = blockIdx.x + static_cast<int64_t>(gridDim.x) * (threadIdx.x - blockDim.x / 2); i < t.seqs; i += static_cast<int64_t>(gridDim.x) * (blockDim.x / 2)) {
+      const int skip = shared_tokens(a, static_cast<int>(i));
+      p.skip[i] = skip;
+      if (skip > 0) a.prefix.home_row[i] = a.prefix.begin[a.prefix.group[i]] + a.prefix.first[i];
+    }
   if (threadIdx.x < 32) {
     int64_t per[2] = {1, 1};
     for (int pass = 0; pass < 2; ++pass) {
@@ -103,6 +109,7 @@ __device__ __forceinline__ void prefix_line(const PrefixArgs& p, PrefixLine& lin
 #pragma unroll
         for (int c = 0; c < 2; ++c) at[c] += __shfl_sync(0xffffffffu, inc[c], 31);
         const bool last = __any_sync(0xffffffffu, s.leader < 0) || g0 + 32 >= t.seqs;   // past the last group
+        if (last && pass == 1 && blockIdx.x == 0 && lane == 0) *a.prefix.planned = g0 + 32 < t.seqs ? g0 + 32 : t.seqs;
         if (last && pass == 1 && blockIdx.x == 0 && p.tile.workers > 0)
           for (int i = g0 + 32 + lane; i <= t.seqs; i += 32) p.tile.pre[i] = at[1];
         if (last) break;
@@ -125,6 +132,8 @@ __device__ __forceinline__ void prefix_line(const PrefixArgs& p, PrefixLine& lin
 }
 
 fg_status paged_prefix(const PrefixArgs& p, int head_dim, cudaStream_t st);
+// Behind it, and behind the chunks' kernel where that has groups: the parts of every row joined in its home.
+fg_status paged_prefix_join(const PrefixArgs& p, int head_dim, cudaStream_t st);
 
 }  // namespace paged
 }  // namespace fg

@@ -687,32 +687,24 @@ __global__ void __launch_bounds__(32 * kWarps, kCtasPerSm<NB>) step_kernel(const
       }
     }
   };
-  // the parts that row n's shared prefix left (paged_prefix.cu) come to its own sums, in order
-  auto join_prefix = [&](float (&v)[NG][8], float& most, float& sum, int seq, int h, int n) {
-    const int t = n / a.shape.group;
-    const PrefixParts pp = prefix_parts(a.prefix, seq, t, h, n - t * a.shape.group, a.shape.group, a.q_heads);
-    float2 st = a.prefix.home_stat[pp.home];
-    const float* x = a.prefix.home + pp.home * D;
-    for (int k = 0;; ++k) {
-      const float top = fmaxf(most, st.x), base = top == -INFINITY ? 0.0f : top;
-      const float fa = exp2f(most - base), fb = exp2f(st.x - base);
-      sum = sum * fa + st.y * fb;
+  // what row n's shared prefix left (paged_prefix.cu) comes to its own sums
+  auto join_prefix = [&](float (&v)[NG][8], float& most, float& sum, int64_t home) {
+    const float2 st = a.prefix.home_stat[home];
+    const float* x = a.prefix.home + home * D;
+    const float top = fmaxf(most, st.x), base = top == -INFINITY ? 0.0f : top;
+    const float fa = exp2f(most - base), fb = exp2f(st.x - base);
+    sum = sum * fa + st.y * fb;
 #pragma unroll
-      for (int g = 0; g < NG; ++g)
+    for (int g = 0; g < NG; ++g)
 #pragma unroll
-        for (int c = 0; c < 8; c += 4) {
-          const float4 y = *reinterpret_cast<const float4*>(x + 64 * g + 8 * gq + c);
-          v[g][c] = fmaf(y.x, fb, v[g][c] * fa);
-          v[g][c + 1] = fmaf(y.y, fb, v[g][c + 1] * fa);
-          v[g][c + 2] = fmaf(y.z, fb, v[g][c + 2] * fa);
-          v[g][c + 3] = fmaf(y.w, fb, v[g][c + 3] * fa);
-        }
-      most = top;
-      if (k == pp.count) break;
-      const int64_t at = pp.extra + static_cast<int64_t>(k) * pp.stride;
-      st = a.prefix.extra_stat[at];
-      x = a.prefix.extra + at * D;
-    }
+      for (int c = 0; c < 8; c += 4) {
+        const float4 y = *reinterpret_cast<const float4*>(x + 64 * g + 8 * gq + c);
+        v[g][c] = fmaf(y.x, fb, v[g][c] * fa);
+        v[g][c + 1] = fmaf(y.y, fb, v[g][c + 1] * fa);
+        v[g][c + 2] = fmaf(y.z, fb, v[g][c + 2] * fa);
+        v[g][c + 3] = fmaf(y.w, fb, v[g][c + 3] * fa);
+      }
+    most = top;
   };
   // the item's rows, finished (one share) or as this share's partial
   auto end_item = [&](const uint8_t* s, bool from_start, bool to_end) {
@@ -758,7 +750,10 @@ __global__ void __launch_bounds__(32 * kWarps, kCtasPerSm<NB>) step_kernel(const
         }
         float most = m[nb][e] * (e ? kc2[nb].y : kc2[nb].x);
         if (SHARED) {
-          if (prefixed && from_start) join_prefix(v, most, lsum, seq, h, n);
+          if (prefixed && from_start) {
+            const int t = n / a.shape.group;
+            join_prefix(v, most, lsum, prefix_home(a.prefix, seq, t, h * a.shape.group + n - t * a.shape.group, a.q_heads));
+          }
           f = !whole ? 1.0f : lsum == 0.0f ? 0.0f : 1.0f / lsum;
 #pragma unroll
           for (int g = 0; g < NG; ++g)

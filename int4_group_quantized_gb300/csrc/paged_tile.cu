@@ -586,7 +586,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const AttnArgs<__half
     float m = -INFINITY;
     float2 l2 = make_float2(0.0f, 0.0f);
     uint32_t nans = 0;
-    PrefixParts pp{-1, 0, 0, 0};   // kBehind: what the row's shared prefix left
+    int64_t home = -1;     // kBehind: where the row's shared prefix left its sums
     while (true) {
       // A round ends one segment and works on the next.  S of the last tile is complete, so Q's place is free: the next Q is
       // on its way while the last P V runs, and its first S runs while O is written.
@@ -630,19 +630,13 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const AttnArgs<__half
       if (rows >= 0) {
         // ---- the segment's rows: finished, or this share's partial ------------------------
         float l = l2.x + l2.y;
-        // parts of a shared prefix: the largest maximum first, and the sum, then column by column
-        auto part_at = [&](int k) { return pp.extra + static_cast<int64_t>(k - 1) * pp.stride; };
-        float own = 1.0f, base = 0.0f;
-        if (MODE == kBehind && pp.home >= 0) {
-          float top = fmaxf(m, a.prefix.home_stat[pp.home].x);
-          for (int k = 1; k <= pp.count; ++k) top = fmaxf(top, a.prefix.extra_stat[part_at(k)].x);
-          base = top == -INFINITY ? 0.0f : top;
+        float own = 1.0f, other = 0.0f;   // factors of its own sums and of its prefix's
+        if (MODE == kBehind && home >= 0) {
+          const float2 st = a.prefix.home_stat[home];
+          const float top = fmaxf(m, st.x), base = top == -INFINITY ? 0.0f : top;
           own = exp2f(m - base);
-          l *= own;
-          for (int k = 0; k <= pp.count; ++k) {
-            const float2 st = k == 0 ? a.prefix.home_stat[pp.home] : a.prefix.extra_stat[part_at(k)];
-            l = fmaf(st.y, exp2f(st.x - base), l);
-          }
+          other = exp2f(st.x - base);
+          l = l * own + st.y * other;
           m = top;
         }
         const float f = !whole_item ? 1.0f : l == 0.0f ? 0.0f : 1.0f / l;
@@ -658,20 +652,17 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const AttnArgs<__half
 #pragma unroll
           for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(u[(e & 24) + ((e & 7) < 4 ? 2 * (e & 7) : 2 * (e & 7) - 7)]) * (MODE == kBehind ? fc * own : fc);
           if (MODE == kBehind) {
-            if (pp.home >= 0)
-              for (int k = 0; k <= pp.count; ++k) {
-                const float2 st = k == 0 ? a.prefix.home_stat[pp.home] : a.prefix.extra_stat[part_at(k)];
-                const float* x = (k == 0 ? a.prefix.home + pp.home * D : a.prefix.extra + part_at(k) * D) + 32 * c;
-                const float fk = exp2f(st.x - base) * f;
+            if (home >= 0) {
+              const float* x = a.prefix.home + home * D + 32 * c;
 #pragma unroll
-                for (int e = 0; e < 32; e += 4) {
-                  const float4 y = *reinterpret_cast<const float4*>(x + e);
-                  v[e] = fmaf(y.x, fk, v[e]);
-                  v[e + 1] = fmaf(y.y, fk, v[e + 1]);
-                  v[e + 2] = fmaf(y.z, fk, v[e + 2]);
-                  v[e + 3] = fmaf(y.w, fk, v[e + 3]);
-                }
+              for (int e = 0; e < 32; e += 4) {
+                const float4 y = *reinterpret_cast<const float4*>(x + e);
+                v[e] = fmaf(y.x, other * f, v[e]);
+                v[e + 1] = fmaf(y.y, other * f, v[e + 1]);
+                v[e + 2] = fmaf(y.z, other * f, v[e + 2]);
+                v[e + 3] = fmaf(y.w, other * f, v[e + 3]);
               }
+            }
             __syncwarp();   // collective loads follow
           }
           if (whole_item) {
@@ -839,10 +830,10 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const AttnArgs<__half
         dst = place(a.ldo);
       }
       if (MODE == kBehind) {
-        pp.home = -1;
+        home = -1;
         if (from_start && r < rows && a.tab.skip[k.i] > 0) {
           const int row = k.un.r0 + r, t = row / a.shape.group;
-          pp = prefix_parts(a.prefix, k.i, t, k.h, row - t * a.shape.group, a.shape.group, a.q_heads);
+          home = prefix_home(a.prefix, k.i, t, k.h * a.shape.group + row - t * a.shape.group, a.q_heads);
         }
         __syncwarp();
       }
