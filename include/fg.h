@@ -585,12 +585,16 @@ fg_status fg_pages_share(const fg_page_table* t, const int32_t* cu, int64_t min_
  * max_q class and share.  A sequence whose rows do not all stand behind its
  * group's tokens is computed by itself, and so is every sequence of an fp32 pool
  * (fp32 sums on the CUDA cores: the rows' arithmetic, not the cache's bytes, is
- * their cost).  ws: 256-byte aligned, >= fg_paged_attention_shared_workspace_bytes. */
+ * their cost).  Sharing has launches of its own: where the groups save less than
+ * min_saved bytes of cache reads (tokens * (rows - 1) of every group; negative: 144
+ * MB) every sequence goes by itself.  ws: 256-byte aligned, >=
+ * fg_paged_attention_shared_workspace_bytes. */
 size_t fg_paged_attention_shared_workspace_bytes(const fg_page_pool* pool, const fg_page_table* t, int32_t q_heads,
                                                  int64_t ntok, int64_t max_q);
 fg_status fg_paged_attention_shared(const fg_page_pool* pool, const fg_page_table* t, const int32_t* cu,
                                     const fg_page_share* s, const void* q, int64_t ldq, int32_t q_heads, int64_t ntok,
-                                    int64_t max_q, void* out, int64_t ldo, void* ws, size_t ws_bytes, cudaStream_t stream);
+                                    int64_t max_q, int64_t min_saved, void* out, int64_t ldo, void* ws, size_t ws_bytes,
+                                    cudaStream_t stream);
 
 /* Synchronize `stream`, then report (and clear) the device error word that
  * kernels raise: FG_ERR_DEVICE_TIMEOUT when a bounded wait ran out, else

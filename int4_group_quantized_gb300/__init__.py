@@ -964,7 +964,7 @@ def fg_pages_share(tab: PageTable, cu: torch.Tensor, share: PageShare, min_token
 
 
 _sig("fg_paged_attention_shared_workspace_bytes", _SZ, _POOL, _TAB, _I32, _I64, _I64)
-_sig("fg_paged_attention_shared", _INT, _POOL, _TAB, _P, _SHARE, _P, _I64, _I32, _I64, _I64, _P, _I64, _P, _SZ, _P)
+_sig("fg_paged_attention_shared", _INT, _POOL, _TAB, _P, _SHARE, _P, _I64, _I32, _I64, _I64, _I64, _P, _I64, _P, _SZ, _P)
 
 
 def fg_paged_attention_shared_workspace_bytes(pool: PagePool, tab: PageTable, q_heads: int, ntok: int, max_q: int) -> int:
@@ -972,13 +972,13 @@ def fg_paged_attention_shared_workspace_bytes(pool: PagePool, tab: PageTable, q_
 
 
 def fg_paged_attention_shared(pool: PagePool, tab: PageTable, cu: torch.Tensor, share: PageShare, q: torch.Tensor, q_heads: int,
-                              out: torch.Tensor, max_q: int, ws: torch.Tensor | None = None, stream=None) -> None:
+                              out: torch.Tensor, max_q: int, min_saved: int = -1, ws: torch.Tensor | None = None, stream=None) -> None:
     """fg_paged_attention of the ragged batch (without a window), with the tokens that share's groups have in common read once
-    for all of a group's rows."""
+    for all of a group's rows, where that saves at least min_saved bytes of reads (-1: the library's own bound)."""
     n = q.shape[0]
     ldq = _rows(q, pool, n, q_heads * pool.head_dim, "q")
     ldo = _rows(out, pool, n, q_heads * pool.head_dim, "out")
     ws = _paged_ws(ws, fg_paged_attention_shared_workspace_bytes(pool, tab, q_heads, n, max_q) if ws is None else 0, tab, stream)
     _check(_lib.fg_paged_attention_shared(_beside(pool, tab)._ref, tab._ref, _ints(cu, tab.seqs + 1, tab, "cu"),
-                                          _share_on(share, tab)._ref, q.data_ptr(), ldq, q_heads, n, max_q, out.data_ptr(), ldo,
+                                          _share_on(share, tab)._ref, q.data_ptr(), ldq, q_heads, n, max_q, min_saved, out.data_ptr(), ldo,
                                           ws.data_ptr(), ws.numel(), _on(tab, stream)), "fg_paged_attention_shared")

@@ -293,6 +293,12 @@ fg_status join(const AttnArgs<T>& a, const ClassPlan& step, const ClassPlan& til
                       32 * kJoinWarps, 0, st, a, step, tile);
 }
 
+// Bytes of cache reads that groups have to save before a call shares: the prefixes' launches take 15 to 25 us whatever they
+// do.  One prefix for a step of 64 sequences, 32 heads of 128: 83 MB saved 42.0 us each by itself and 52.1 shared, 165 MB 56.8
+// and 52.3, 1.3 GB 258 and 73; 16 sequences, 32 on 8 heads: 79 MB 31.9 and 42.7, 157 MB 46.4 and 46.5, 629 MB 133 and 69; 4
+// sequences, 32 heads: 126 MB 44.9 and 55.4, 503 MB 133 and 122.
+constexpr int64_t kSharedSaves = int64_t(144) << 20;
+
 // ---- workspace ------------------------------------------------------------------------
 constexpr int kMaxSms = 160;   // a workspace fits this many SMs; launches use no more
 inline size_t up(size_t x) { return (x + 255) / 256 * 256; }
@@ -366,7 +372,7 @@ Layout layout_of(const fg_page_pool& pool, const fg_page_table& t, int32_t q_hea
 template <typename T>
 fg_status launch_attn(const fg_page_pool& pool, const fg_page_table& t, const int32_t* cu, const void* q, int64_t ldq,
                       int32_t q_heads, int64_t ntok, int64_t max_q, int64_t window, int64_t sinks, void* out,
-                      int64_t ldo, void* ws, unsigned int* err, cudaStream_t st, const fg_page_share* share = nullptr) {
+                      int64_t ldo, void* ws, unsigned int* err, cudaStream_t st, const fg_page_share* share = nullptr, int64_t min_saved = 0) {
   AttnArgs<T> a;
   a.pool = pool_of(pool);
   a.tab = table_of(t);
@@ -395,7 +401,7 @@ fg_status launch_attn(const fg_page_pool& pool, const fg_page_table& t, const in
       a.prefix.leader = share->leader;
       a.prefix.begin = share->begin;
       a.prefix.rows = share->rows;
-      const PrefixArgs p{a, l.skip, l.tall, std::min(num_sms(), kMaxSms)};
+      const PrefixArgs p{a, l.skip, l.tall, std::min(num_sms(), kMaxSms), min_saved};
       FG_TRY(paged_prefix(p, pool.head_dim, st));
       if (l.tall.workers > 0) FG_TRY(paged_prefix_tile(a, l.tall, pool.head_dim, st));
       FG_TRY(paged_prefix_join(p, pool.head_dim, st));
@@ -489,8 +495,8 @@ size_t fg_paged_attention_shared_workspace_bytes(const fg_page_pool* pool, const
 }
 
 fg_status fg_paged_attention_shared(const fg_page_pool* pool, const fg_page_table* t, const int32_t* cu, const fg_page_share* s,
-                                    const void* q, int64_t ldq, int32_t q_heads, int64_t ntok, int64_t max_q, void* out, int64_t ldo,
-                                    void* ws, size_t ws_bytes, cudaStream_t stream) {
+                                    const void* q, int64_t ldq, int32_t q_heads, int64_t ntok, int64_t max_q, int64_t min_saved, void* out,
+                                    int64_t ldo, void* ws, size_t ws_bytes, cudaStream_t stream) {
   FG_TRY(check_attn(pool, t, q_heads, ntok, max_q));
   if (!s) return fail(FG_ERR_ARG, "null share");
   if (ntok == 0 || max_q == 0 || t->seqs == 0) return FG_OK;
@@ -503,7 +509,12 @@ fg_status fg_paged_attention_shared(const fg_page_pool* pool, const fg_page_tabl
   if (!aligned(ws, 256)) return fail(FG_ERR_ALIGN, "workspace needs 256-byte alignment");
   unsigned int* err = device_error_word();
   if (!err) return fail(FG_ERR_CUDA, "device error word");
-  return launch_attn<__half>(*pool, *t, cu, q, ldq, q_heads, ntok, max_q, 0, 0, out, ldo, ws, err, stream, s);
+  // in tokens; K and V of one are 1.25 bytes an element
+  const int64_t token = static_cast<int64_t>(pool->heads) * pool->head_dim * 5 / 4;
+  const int64_t least = ((min_saved < 0 ? kSharedSaves : min_saved) + token - 1) / token;
+  // no group saves more than every row but one of all that a table row can name
+  const bool never = least > 0 && static_cast<double>(t->stride) * t->page_size * static_cast<double>(ntok) < static_cast<double>(least);
+  return launch_attn<__half>(*pool, *t, cu, q, ldq, q_heads, ntok, max_q, 0, 0, out, ldo, ws, err, stream, never ? nullptr : s, least);
 }
 
 }  // extern "C"

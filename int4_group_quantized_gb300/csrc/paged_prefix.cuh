@@ -22,6 +22,7 @@ struct PrefixArgs {
   int32_t* skip;          // [seqs] out: the tokens of a sequence that its group attends to
   ClassPlan tile;         // head and pre by group, out; no workers: one class
   int workers;
+  int64_t min_saved;      // tokens, times the rows that do not read them again, from which on groups are made
 };
 
 constexpr int kPrefixKeysLog2 = 7;
@@ -59,6 +60,7 @@ __device__ __forceinline__ int shared_tokens(const AttnArgs<__half>& a, int i) {
 // (written by the CTAs together), and where its own share begins.
 struct PrefixLine {
   int64_t total, per;
+  bool worth;            // the groups save enough
   int g;                 // the group that the share begins in
   PrefixGroup at;
 };
@@ -66,22 +68,19 @@ __device__ __forceinline__ void prefix_line(const PrefixArgs& p, PrefixLine& lin
   const AttnArgs<__half>& a = p.a;
   const Table& t = a.tab;
   const int group = a.shape.group, heads = a.pool.heads, lane = threadIdx.x & 31;
-  // (the sequences one a CTA in turn, by its last threads: the plan does not wait for them)
-  if (threadIdx.x >= blockDim.x / 2)
-    for (int64_t i = blockIdx.x + static_cast<int64_t>(gridDim.x) * (threadIdx.x - blockDim.x / 2); i < t.seqs; i += static_cast<int64_t>(gridDim.x) * (blockDim.x / 2)) {
-      const int skip = shared_tokens(a, static_cast<int>(i));
-      p.skip[i] = skip;
-      if (skip > 0) a.prefix.home_row[i] = a.prefix.begin[a.prefix.group[i]] + a.prefix.first[i];
-    }
+  bool worth = true;
   if (threadIdx.x < 32) {
     int64_t per[2] = {1, 1};
     for (int pass = 0; pass < 2; ++pass) {
+      int64_t saved = 0;                      // tokens that are not read again
       int64_t at[2] = {0, 0};                 // of the two classes' lines
       const int64_t o0 = blockIdx.x * per[0];
       for (int g0 = 0; g0 < t.seqs; g0 += 32) {
         const int g = g0 + lane;
         SharedGroup s{-1, 0, 0, 0};
         if (g < t.seqs) s = shared_group(a.prefix, t, a.batch, g);
+        saved += s.list > 0 ? static_cast<int64_t>(s.tokens) * (s.list - 1) : 0;
+        if (!worth) s.list = 0;
         const bool tall = p.tile.workers > 0 && static_cast<int64_t>(s.list) * group > kPrefixFew;
         PrefixGroup x = prefix_group(s, group, tall);
         const int64_t n = s.list > 0 ? static_cast<int64_t>(heads) * x.units * x.tiles : 0;
@@ -115,11 +114,16 @@ __device__ __forceinline__ void prefix_line(const PrefixArgs& p, PrefixLine& lin
         if (last) break;
       }
       if (pass == 0) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) saved += __shfl_xor_sync(0xffffffffu, saved, o);
+        worth = saved >= p.min_saved;
+        if (!worth) at[0] = at[1] = 0;
         per[0] = at[0] > p.workers ? (at[0] + p.workers - 1) / p.workers : 1;
         per[1] = p.tile.workers > 0 && at[1] > p.tile.workers ? (at[1] + p.tile.workers - 1) / p.tile.workers : 1;
         if (lane == 0) {
           line.total = at[0];
           line.per = per[0];
+          line.worth = worth;
           if (blockIdx.x == 0 && p.tile.workers > 0) {
             p.tile.head[0] = at[1];
             p.tile.head[1] = per[1];
@@ -129,6 +133,13 @@ __device__ __forceinline__ void prefix_line(const PrefixArgs& p, PrefixLine& lin
     }
   }
   __syncthreads();
+  // the sequences one a CTA in turn, by warps that are not in a hurry
+  if (threadIdx.x >= 128 && threadIdx.x < 256)
+    for (int64_t i = blockIdx.x + static_cast<int64_t>(gridDim.x) * (threadIdx.x - 128); i < t.seqs; i += static_cast<int64_t>(gridDim.x) * 128) {
+      const int skip = line.worth ? shared_tokens(a, static_cast<int>(i)) : 0;
+      p.skip[i] = skip;
+      if (skip > 0) a.prefix.home_row[i] = a.prefix.begin[a.prefix.group[i]] + a.prefix.first[i];
+    }
 }
 
 fg_status paged_prefix(const PrefixArgs& p, int head_dim, cudaStream_t st);

@@ -86,10 +86,84 @@ __device__ __forceinline__ Float8 from_lane(const Float8& x, int lane) {
 }
 __device__ __forceinline__ void put8(__half* p, const Half8& x) { *reinterpret_cast<uint4*>(p) = x.raw; }
 __device__ __forceinline__ void put8(float* p, const Float8& x) { store8(p, x.v); }
+__device__ __forceinline__ void get8(const __half* p, Half8& x) { x.raw = *reinterpret_cast<const uint4*>(p); }
+__device__ __forceinline__ void get8(const float* p, Float8& x) { x.load(p); }
+
+// Cosines and sines of eight pairs from p on (HALF), or of four (PAIRS).
+template <bool HALF>
+__device__ __forceinline__ void read_cs(const float* cs, int p, int P, float4 (&c)[2], float4 (&s)[2]) {
+#pragma unroll
+  for (int e = 0; e < (HALF ? 2 : 1); ++e) {
+    c[e] = *reinterpret_cast<const float4*>(cs + cs_at<HALF>(0, p + 4 * e, P));
+    s[e] = *reinterpret_cast<const float4*>(cs + cs_at<HALF>(1, p + 4 * e, P));
+  }
+}
+__device__ __forceinline__ void turn_half(float2 (&u)[4], float2 (&v)[4], const float4 (&c)[2], const float4 (&s)[2]) {
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    rotary::turn2(u[2 * e], v[2 * e], make_float2(c[e].x, c[e].y), make_float2(s[e].x, s[e].y));
+    rotary::turn2(u[2 * e + 1], v[2 * e + 1], make_float2(c[e].z, c[e].w), make_float2(s[e].z, s[e].w));
+  }
+}
+__device__ __forceinline__ void turn_pairs(float2 (&u)[4], const float4& c, const float4& s) {
+#pragma unroll
+  for (int e = 0; e < 4; e += 2) {
+    float2 p = make_float2(u[e].x, u[e + 1].x), q = make_float2(u[e].y, u[e + 1].y);
+    rotary::turn2(p, q, e ? make_float2(c.z, c.w) : make_float2(c.x, c.y), e ? make_float2(s.z, s.w) : make_float2(s.x, s.y));
+    u[e] = make_float2(p.x, q.x);
+    u[e + 1] = make_float2(p.y, q.y);
+  }
+}
+
+// A head's queries of a run, by a warp: a lane has a piece of a row (HALF: eight dims of each half), four (fp32: two) of them at a time.
+template <typename T, int NG, bool HALF>
+__device__ __forceinline__ void rotate_slice(const T* x, int64_t ldx, T* out, int64_t ldo, const float* cs, const int* pos, int rot, bool copy) {
+  using X = typename Vec8<T>::type;
+  constexpr int D = 64 * NG, R = kRun<NG>, kAhead = sizeof(T) == 2 ? 4 : 2;
+  const int lane = threadIdx.x & 31, P = rot / 2;
+  const int turn = HALF ? rot / 16 : rot / 8, per = turn + (copy ? (D - rot) / 8 : 0);
+  for (int i0 = lane; i0 < R * per; i0 += 32 * kAhead) {
+    X a[kAhead], b[kAhead];
+    int row[kAhead], j[kAhead];
+#pragma unroll
+    for (int e = 0; e < kAhead; ++e) {
+      const int i = i0 + 32 * e;
+      row[e] = i / per;
+      j[e] = i - row[e] * per;
+      if (i >= R * per || pos[row[e]] < 0) row[e] = -1;
+      if (row[e] >= 0) {
+        const T* from = x + row[e] * ldx + (j[e] < turn ? 8 * j[e] : rot + 8 * (j[e] - turn));
+        get8(from, a[e]);
+        if (HALF && j[e] < turn) get8(from + P, b[e]);
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < kAhead; ++e) {
+      if (row[e] < 0) continue;
+      T* to = out + row[e] * ldo + (j[e] < turn ? 8 * j[e] : rot + 8 * (j[e] - turn));
+      if (j[e] < turn) {
+        float2 u[4], v[4];
+        float4 c[2], s[2];
+        read_cs<HALF>(cs + row[e] * rot, HALF ? 8 * j[e] : 4 * j[e], P, c, s);
+        unpack(a[e], u);
+        if (HALF) {
+          unpack(b[e], v);
+          turn_half(u, v, c, s);
+          pack(b[e], v);
+          put8(to + P, b[e]);
+        } else {
+          turn_pairs(u, c[0], s[0]);
+        }
+        pack(a[e], u);
+      }
+      put8(to, a[e]);
+    }
+  }
+}
 
 // The lane's eight dims (chunk ck of the row's head) rotated; cs: the row's cosines and sines.
 template <bool HALF, class X>
-__device__ __forceinline__ void rotate8(X& x, const float* cs, int ck, int rot, int lane, int chunks) {
+__device__ __forceinline__ void rotate8(X& x, const float* cs, int ck, int rot, int lane) {
   const int P = rot / 2;
   float2 u[4], v[4];
   if (HALF) {
@@ -99,32 +173,17 @@ __device__ __forceinline__ void rotate8(X& x, const float* cs, int ck, int rot, 
     if (!on) return;
     unpack(second ? y : x, u);
     unpack(second ? x : y, v);
-    const int p = 8 * (second ? ck - far : ck);
     float4 c[2], s[2];
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      c[e] = *reinterpret_cast<const float4*>(cs + cs_at<true>(0, p + 4 * e, P));
-      s[e] = *reinterpret_cast<const float4*>(cs + cs_at<true>(1, p + 4 * e, P));
-    }
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      rotary::turn2(u[2 * e], v[2 * e], make_float2(c[e].x, c[e].y), make_float2(s[e].x, s[e].y));
-      rotary::turn2(u[2 * e + 1], v[2 * e + 1], make_float2(c[e].z, c[e].w), make_float2(s[e].z, s[e].w));
-    }
+    read_cs<true>(cs, 8 * (second ? ck - far : ck), P, c, s);
+    turn_half(u, v, c, s);
     if (second) pack(x, v);
     else pack(x, u);
   } else {
     if (8 * ck >= rot) return;
     unpack(x, u);
-    const float4 c = *reinterpret_cast<const float4*>(cs + cs_at<false>(0, 4 * ck, P));
-    const float4 s = *reinterpret_cast<const float4*>(cs + cs_at<false>(1, 4 * ck, P));
-#pragma unroll
-    for (int e = 0; e < 4; e += 2) {
-      float2 p = make_float2(u[e].x, u[e + 1].x), q = make_float2(u[e].y, u[e + 1].y);
-      rotary::turn2(p, q, e ? make_float2(c.z, c.w) : make_float2(c.x, c.y), e ? make_float2(s.z, s.w) : make_float2(s.x, s.y));
-      u[e] = make_float2(p.x, q.x);
-      u[e + 1] = make_float2(p.y, q.y);
-    }
+    float4 c[2], s[2];
+    read_cs<false>(cs, 4 * ck, P, c, s);
+    turn_pairs(u, c[0], s[0]);
     pack(x, u);
   }
 }
@@ -175,7 +234,7 @@ __global__ void __launch_bounds__(kThreads, 2) rotated_kernel(const RotatedArgs<
     };
     auto stride = [&](int sl) { return sl < heads ? a.ld[0] : sl < 2 * heads ? a.ld[1] : a.ld[2]; };
     auto fetch = [&](int sl, int slot) {
-      if (sl < s1) {
+      if (sl < s1 && kind_of(sl) != 2) {
         const T* src = source(sl);
         const int64_t ld = stride(sl);
 #pragma unroll
@@ -199,11 +258,17 @@ __global__ void __launch_bounds__(kThreads, 2) rotated_kernel(const RotatedArgs<
     __syncthreads();
     for (int sl = s0 + warp; sl < s1; sl += kWarps, slot ^= 1) {
       const int kind = kind_of(sl), h = sl - kind * heads;
+      if (kind == 2) {
+        rotate_slice<T, NG, HALF>(a.src[2] + row0 * a.ld[2] + static_cast<int64_t>(h) * D, a.ld[2], a.q_out + row0 * a.ldqo + static_cast<int64_t>(h) * D, a.ldqo,
+                                  cs, run_pos, a.rot, a.src[2] != a.q_out);
+        if constexpr (kRing<T>) fetch(sl + kWarps, slot ^ 1);   // a group of copies each round
+        continue;
+      }
       X held[kBatches];
       if constexpr (kRing<T>) {
         fetch(sl + kWarps, slot ^ 1);
         tc::cp_async_wait<1>();   // a lane reads what it copied itself
-        if (kind != 1)
+        if (kind == 0)
 #pragma unroll
           for (int b = 0; b < kBatches; ++b) held[b].raw = ring[(slot * kBatches + b) * 32];
       } else {
@@ -215,14 +280,9 @@ __global__ void __launch_bounds__(kThreads, 2) rotated_kernel(const RotatedArgs<
           else held[b].clear();
         }
       }
-      if (kind != 1)
+      if (kind == 0) {
 #pragma unroll
-        for (int b = 0; b < kBatches; ++b) rotate8<HALF>(held[b], cs + (b * (4 / NG) + rb) * a.rot, ck, a.rot, lane, 8 * NG);
-      if (kind == 2) {
-#pragma unroll
-        for (int b = 0; b < kBatches; ++b)
-          if ((there >> b) & 1u) put8(a.q_out + (row0 + b * (4 / NG) + rb) * a.ldqo + static_cast<int64_t>(h) * D + 8 * ck, held[b]);
-      } else if (kind == 0) {
+        for (int b = 0; b < kBatches; ++b) rotate8<HALF>(held[b], cs + (b * (4 / NG) + rb) * a.rot, ck, a.rot, lane);
         store_slice<T, NG>(a.pool, false, h, tok, mine, row0, a.restored[0], a.ldr, [&](int b) { return held[b]; });
       } else {
         auto batch = [&](int b) {

@@ -71,7 +71,7 @@ __global__ void __launch_bounds__(32 * kWarps) compare_kernel(const ShareArgs a)
     const int32_t* x = a.tab.table + i * a.tab.stride;
     const int32_t* y = a.tab.table + lead * a.tab.stride;
     common = end;
-    constexpr int kAhead = 8;
+    constexpr int kAhead = 16;
     for (int j0 = 0; j0 < end; j0 += 32 * kAhead) {   // the first entry that differs or is no page
       int at = end;
 #pragma unroll
@@ -120,93 +120,119 @@ __device__ __forceinline__ int cta_prefix(int v, int* slots, int& total) {
   return inc - v + (warp > 0 ? before : 0);
 }
 
+// SMALL: up to kSmall sequences, whose numbers then stay in shared memory (256 sequences: 9 us for 17).
+constexpr int kSmall = 1024;
+template <bool SMALL>
 __global__ void __launch_bounds__(kPickThreads) pick_kernel(const ShareArgs a) {
   __shared__ int slots[32];
   __shared__ int groups, listed;
+  __shared__ int32_t own[SMALL ? 8 * kSmall + 1 : 1];
+  __shared__ unsigned long long own_best[SMALL ? kSmall : 1];
   tc::griddep_launch();
   tc::griddep_wait();
   const int seqs = a.tab.seqs, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  int32_t* const lead = SMALL ? own : a.lead;
+  int32_t* const common = SMALL ? own + kSmall : a.common;
+  int32_t* const rows_of = SMALL ? own + 2 * kSmall : a.n;
+  int32_t* const pick = SMALL ? own + 3 * kSmall : a.pick;
+  int32_t* const number = SMALL ? own + 4 * kSmall : a.number;   // of a leader's group; then a group's rows
+  int32_t* const group = SMALL ? own + 5 * kSmall : a.group;
+  int32_t* const first = SMALL ? own + 6 * kSmall : a.first;
+  int32_t* const begin = SMALL ? own + 7 * kSmall : a.begin;     // [seqs + 1]
+  int32_t* const size = SMALL ? number : a.size;
+  unsigned long long* const best = SMALL ? own_best : a.best;
+  if (SMALL) {
+    if (tid < seqs) {
+      lead[tid] = a.lead[tid];
+      common[tid] = a.common[tid];
+      rows_of[tid] = a.n[tid];
+      best[tid] = 0;
+    }
+    __syncthreads();
+  }
   // The pages of a leader's group: c pages shared by the leader and every follower with c or more in common save c times
   // their number page reads; the most of these, the larger c (the fewer followers) of two.  A warp a follower.
   for (int i = warp; i < seqs; i += kPickThreads / 32) {
-    const int L = a.lead[i], c = a.common[i];
+    const int L = lead[i], c = common[i];
     if (L < 0 || L == i || c < a.min_pages) continue;
     int count = 0;
 #pragma unroll 4
-    for (int j = lane; j < seqs; j += 32) count += a.lead[j] == L && j != L && a.common[j] >= c ? 1 : 0;
+    for (int j = lane; j < seqs; j += 32) count += lead[j] == L && j != L && common[j] >= c ? 1 : 0;
     count = __reduce_add_sync(0xffffffffu, count);
-    if (lane == 0)
-      atomicMax(a.best + L, (static_cast<unsigned long long>(c) * count) * kMostSeqs + (kMostSeqs - 1 - count));
+    if (lane == 0) atomicMax(best + L, (static_cast<unsigned long long>(c) * count) * kMostSeqs + (kMostSeqs - 1 - count));
   }
+  if (tid == 0) groups = listed = 0;
   __syncthreads();
   for (int i = tid; i < seqs; i += kPickThreads) {
-    const unsigned long long key = __ldcg(a.best + i);   // atomics act in L2
-    a.pick[i] = key == 0 ? 0 : static_cast<int>(key / kMostSeqs / (kMostSeqs - 1 - key % kMostSeqs));
+    const unsigned long long key = SMALL ? best[i] : __ldcg(best + i);   // atomics act in L2
+    pick[i] = key == 0 ? 0 : static_cast<int>(key / kMostSeqs / (kMostSeqs - 1 - key % kMostSeqs));
   }
-  if (tid == 0) groups = 0;
   __syncthreads();
   // groups in the order of their leaders
   for (int i0 = 0; i0 < seqs; i0 += kPickThreads) {
     const int i = i0 + tid;
-    const bool head = i < seqs && a.pick[i] > 0;
+    const bool head = i < seqs && pick[i] > 0;
     int total;
     const int at = groups + cta_prefix(head ? 1 : 0, slots, total);
     if (head) {
-      a.number[i] = at;
+      number[i] = at;
       a.leader[at] = i;
     }
     __syncthreads();
     if (tid == 0) groups += total;
     __syncthreads();
   }
-  auto member = [&](int i) {
-    const int L = a.lead[i];
-    return L >= 0 && a.pick[L] > 0 && (L == i || a.common[i] >= a.pick[L]);
-  };
   for (int i = tid; i < seqs; i += kPickThreads) {
-    const bool in = member(i);
-    const int L = in ? a.lead[i] : i;
-    a.group[i] = in ? a.number[L] : -1;
-    a.tokens[i] = in ? a.pick[L] << a.tab.ps_log2 : 0;
-    a.first[i] = 0;
+    const int L = lead[i];
+    const bool in = L >= 0 && pick[L] > 0 && (L == i || common[i] >= pick[L]);
+    group[i] = in ? number[L] : -1;
+    if (SMALL) a.group[i] = in ? number[L] : -1;
+    a.tokens[i] = in ? pick[L] << a.tab.ps_log2 : 0;
+    first[i] = 0;
     if (i >= groups) a.leader[i] = -1;
   }
-  // a group's rows, and the rows of its members before each: a warp a group
   __syncthreads();
+  // a group's rows, and the rows of its members before each: a warp a group
   for (int g = warp; g < groups; g += kPickThreads / 32) {
     int at = 0;
-    for (int i0 = a.leader[g]; i0 < seqs; i0 += 32) {
+    for (int i0 = 0; i0 < seqs; i0 += 32) {
       const int i = i0 + lane;
-      const bool in = i < seqs && a.group[i] == g;
-      int inc = in ? a.n[i] : 0;
+      const bool in = i < seqs && group[i] == g;
+      if (!__any_sync(0xffffffffu, in)) continue;
+      int inc = in ? rows_of[i] : 0;
       const int n = inc;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int up = __shfl_up_sync(0xffffffffu, inc, o);
         if (lane >= o) inc += up;
       }
-      if (in) a.first[i] = at + inc - n;
+      if (in) first[i] = at + inc - n;
       at += __shfl_sync(0xffffffffu, inc, 31);
     }
-    if (lane == 0) a.size[g] = at;
+    if (lane == 0) size[g] = at;
   }
-  if (tid == 0) listed = 0;
   __syncthreads();
   for (int g0 = 0; g0 < groups; g0 += kPickThreads) {
     const int g = g0 + tid;
     int total;
-    const int at = listed + cta_prefix(g < groups ? a.size[g] : 0, slots, total);
-    if (g < groups) a.begin[g] = at;
+    const int at = listed + cta_prefix(g < groups ? size[g] : 0, slots, total);
+    if (g < groups) begin[g] = at;
     __syncthreads();
     if (tid == 0) listed += total;
     __syncthreads();
   }
-  for (int g = groups + tid; g <= seqs; g += kPickThreads) a.begin[g] = listed;
+  for (int g = groups + tid; g <= seqs; g += kPickThreads) begin[g] = listed;
   __syncthreads();
+  if (SMALL) {
+    for (int i = tid; i <= seqs; i += kPickThreads) {
+      a.begin[i] = begin[i];
+      if (i < seqs) a.first[i] = first[i];
+    }
+  }
   for (int i = warp; i < seqs; i += kPickThreads / 32) {
-    const int g = a.group[i];
+    const int g = group[i];
     if (g < 0) continue;
-    const int to = a.begin[g] + a.first[i], from = a.batch.cu[i], n = a.n[i];
+    const int to = begin[g] + first[i], from = a.batch.cu[i], n = rows_of[i];
     for (int r = lane; r < n; r += 32)
       if (static_cast<uint32_t>(to) + r < static_cast<uint32_t>(a.batch.ntok)) a.rows[to + r] = from + r;   // ranges that overlap (refused offsets) stay inside the array
   }
@@ -279,7 +305,7 @@ fg_status fg_pages_share(const fg_page_table* t, const int32_t* cu, int64_t min_
   Trace tr(KC_PAGES_PLAN, stream);
   FG_TRY(paged::launch("compare_kernel", true, compare_kernel, static_cast<unsigned>((t->seqs + kWarps - 1) / kWarps), 32 * kWarps, 0, stream, a));
   trace_extra_launch();
-  return paged::launch("pick_kernel", true, pick_kernel, 1, kPickThreads, 0, stream, a);
+  return paged::launch("pick_kernel", true, t->seqs <= kSmall ? pick_kernel<true> : pick_kernel<false>, 1, kPickThreads, 0, stream, a);
 }
 
 }  // extern "C"

@@ -64,8 +64,11 @@ struct RotateArgs {
 };
 
 // 16 bytes at a time.  kRows rows and `part` heads a block; a head has rot / 16
-// pieces that turn (HALF: eight dims of each half; PAIRS: 16 dims side by side) and,
-// where out is other memory, (d - rot) / 8 that are copied.
+// pieces that turn (HALF: eight dims of each half; PAIRS: rot / 8, eight dims side by side) and,
+// where out is other memory, (d - rot) / 8 that are copied.  A thread has one
+// piece of every (threads / pieces)-th head, in all rows at once: their loads are on
+// their way together, and nothing is divided in the loop (with a piece after another,
+// found by two divisions each, 20 thousand rows of 40 heads of 128 took 116 us).
 constexpr int kRows = 4;
 template <typename T, bool HALF>
 __global__ void __launch_bounds__(kThreads) rotate_kernel(const RotateArgs<T> a) {
@@ -76,7 +79,7 @@ __global__ void __launch_bounds__(kThreads) rotate_kernel(const RotateArgs<T> a)
   const int parts = (a.heads + a.part - 1) / a.part;
   const int64_t row0 = blockIdx.x / parts * static_cast<int64_t>(kRows);
   const int h0 = static_cast<int>(blockIdx.x % parts) * a.part;
-  const int rows = static_cast<int>(a.rows - row0 < kRows ? a.rows - row0 : kRows), heads = min(a.part, a.heads - h0);
+  const int rows = static_cast<int>(a.rows - row0 < kRows ? a.rows - row0 : kRows), h1 = min(a.heads, h0 + a.part);
   for (int i = threadIdx.x; i < rows * pairs; i += kThreads) {
     const int r = i / pairs, p = i - r * pairs;
     const float2 v = cos_sin(phase_of(a.pos[row0 + r], a.turns[p]), a.scale);
@@ -84,41 +87,43 @@ __global__ void __launch_bounds__(kThreads) rotate_kernel(const RotateArgs<T> a)
     cs[(2 * r + 1) * pairs + p] = v.y;
   }
   __syncthreads();
-  const int turn = HALF ? a.rot / 16 : a.rot / 8, per = turn + (a.copy ? (a.d - a.rot) / 8 : 0);
-  const int items = rows * heads * per;
-#pragma unroll 2
-  for (int i = threadIdx.x; i < items; i += kThreads) {
-    const int rh = i / per, j = i - rh * per, r = rh / heads, h = h0 + rh - r * heads;
-    const T* x = a.x + (row0 + r) * a.ldx + static_cast<int64_t>(h) * a.d;
-    T* out = a.out + (row0 + r) * a.ldo + static_cast<int64_t>(h) * a.d;
-    float2 u[4], v[4];
-    if (j >= turn) {
-      const int at = a.rot + 8 * (j - turn);
-      load8(x + at, u);
-      store8(out + at, u);
-      continue;
-    }
-    const float* c = cs + 2 * r * pairs;
-    const float* s = c + pairs;
-    if (HALF) {
-      load8(x + 8 * j, u);
-      load8(x + pairs + 8 * j, v);
+  const int turn = HALF ? a.rot / 16 : a.rot / 8, per = turn + (a.copy ? (a.d - a.rot) / 8 : 0), step = kThreads / per;
+  const int j = threadIdx.x % per, first = threadIdx.x / per;
+  if (first >= step) return;
+  const bool turns = j < turn, two = HALF && turns;
+  const int at = turns ? 8 * j : a.rot + 8 * (j - turn);
+  const T* x = a.x + row0 * a.ldx + at;
+  T* out = a.out + row0 * a.ldo + at;
+  for (int h = h0 + first; h < h1; h += step) {
+    const int64_t off = static_cast<int64_t>(h) * a.d;
+    float2 u[kRows][4], v[kRows][4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        turn2(u[e], v[e], *reinterpret_cast<const float2*>(c + 8 * j + 2 * e), *reinterpret_cast<const float2*>(s + 8 * j + 2 * e));
-      store8(out + 8 * j, u);
-      store8(out + pairs + 8 * j, v);
-    } else {
-      load8(x + 8 * j, u);
-#pragma unroll
-      for (int e = 0; e < 4; e += 2) {
-        float2 p = make_float2(u[e].x, u[e + 1].x), q = make_float2(u[e].y, u[e + 1].y);
-        turn2(p, q, *reinterpret_cast<const float2*>(c + 4 * j + e), *reinterpret_cast<const float2*>(s + 4 * j + e));
-        u[e] = make_float2(p.x, q.x);
-        u[e + 1] = make_float2(p.y, q.y);
+    for (int r = 0; r < kRows; ++r)
+      if (r < rows) {
+        load8(x + r * a.ldx + off, u[r]);
+        if (two) load8(x + r * a.ldx + off + pairs, v[r]);
       }
-      store8(out + 8 * j, u);
-    }
+#pragma unroll
+    for (int r = 0; r < kRows; ++r)
+      if (r < rows) {
+        const float* c = cs + 2 * r * pairs;
+        const float* s = c + pairs;
+        if (two) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            turn2(u[r][e], v[r][e], *reinterpret_cast<const float2*>(c + 8 * j + 2 * e), *reinterpret_cast<const float2*>(s + 8 * j + 2 * e));
+          store8(out + r * a.ldo + off + pairs, v[r]);
+        } else if (turns) {
+#pragma unroll
+          for (int e = 0; e < 4; e += 2) {
+            float2 p = make_float2(u[r][e].x, u[r][e + 1].x), q = make_float2(u[r][e].y, u[r][e + 1].y);
+            turn2(p, q, *reinterpret_cast<const float2*>(c + 4 * j + e), *reinterpret_cast<const float2*>(s + 4 * j + e));
+            u[r][e] = make_float2(p.x, q.x);
+            u[r][e + 1] = make_float2(p.y, q.y);
+          }
+        }
+        store8(out + r * a.ldo + off, u[r]);
+      }
   }
 }
 
@@ -174,7 +179,8 @@ fg_status rotate(const fg_rotary& r, const void* x, int64_t rows, int64_t ldx, i
   const bool half = r.layout == FG_ROTARY_HALF;
   const size_t smem = static_cast<size_t>(kRows) * r.rot * sizeof(float);
   const int64_t blocks = (rows + kRows - 1) / kRows, sms = num_sms();
-  if (d % 8 == 0 && r.rot % (half ? 16 : 8) == 0 && ldx % 8 == 0 && ldo % 8 == 0 && aligned(x, 16) && aligned(out, 16) && smem <= 48 * 1024 &&
+  const int per = (half ? r.rot / 16 : r.rot / 8) + (a.copy ? (d - r.rot) / 8 : 0);   // pieces of a head
+  if (d % 8 == 0 && per <= kThreads && r.rot % (half ? 16 : 8) == 0 && ldx % 8 == 0 && ldo % 8 == 0 && aligned(x, 16) && aligned(out, 16) && smem <= 48 * 1024 &&
       static_cast<int64_t>(heads) * d <= (1 << 28)) {
     // few rows: the heads of a block of rows go to as many blocks as give every SM two
     const int64_t parts = std::min<int64_t>(heads, std::max<int64_t>(1, 2 * sms / blocks));

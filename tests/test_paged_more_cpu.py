@@ -180,7 +180,7 @@ def test_shared_attention_arguments(fg):
 
     def attend(pool=pool, tab=tab, cu=P, s=None, q=P, ldq=256, qh=4, ntok=4, mq=2, out=P, ldo=256, ws=P, wsb=1 << 40):
         s = _share(fg) if s is None else s
-        return fg.lib.fg_paged_attention_shared(_br(pool), _br(tab), cu, _br(s) if s else None, q, ldq, qh, ntok, mq, out, ldo, ws, wsb, None)
+        return fg.lib.fg_paged_attention_shared(_br(pool), _br(tab), cu, _br(s) if s else None, q, ldq, qh, ntok, mq, 0, out, ldo, ws, wsb, None)
 
     assert attend(s=False) == 1 and attend(s=_share(fg, seqs=4)) == 2 and attend(s=_share(fg, ntok=5)) == 2
     for field in ("group", "tokens", "first", "leader", "begin", "rows"):

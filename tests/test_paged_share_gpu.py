@@ -172,10 +172,10 @@ class Forked:
         return ref, tol
 
 
-def _run(fg, F, share=None, max_q=None, **kw):
+def _run(fg, F, share=None, max_q=None, min_saved=0, **kw):
     out = torch.full(F.q.shape, 7.0, dtype=F.dtype, device="cuda")
     fg.fg_paged_attention_shared(F.pool, F.tab, _i32(F.cu), F.find(fg) if share is None else share, torch.as_tensor(F.q, device="cuda"),
-                                 F.heads * F.r, out, int(F.n.max()) if max_q is None else max_q, **kw)
+                                 F.heads * F.r, out, int(F.n.max()) if max_q is None else max_q, min_saved, **kw)
     return out
 
 
@@ -240,6 +240,22 @@ def test_nobody_shares(fg):
     fg.fg_sync_status()
     assert torch.equal(out, plain)                           # the same launches over the same lines
     _hold(out, *F.expect())
+
+
+def test_what_saves_too_little_is_not_shared(fg):
+    """Below min_saved the bits are those of fg_paged_attention; a table row too short for that much is refused sharing on the
+    host, a longer one on the device."""
+    F = Forked(fg, ([0] * 6 + [1] * 3, [9, 30]), [4, 1, 30, 100, 17, 5, 6, 7, 8], [1, 1, 30, 2, 1, 1, 1, 1, 1], 2, 2, 64, 16, 24)
+    plain = torch.full(F.q.shape, 7.0, dtype=torch.float16, device="cuda")
+    fg.fg_paged_attention(F.pool, F.tab, _i32(F.cu), torch.as_tensor(F.q, device="cuda"), 4, plain, 30)
+    token, listed = 2 * 64 * 5 // 4, [36, 3]
+    saved = token * (9 * 16 * (listed[0] - 1) + 30 * 16 * (listed[1] - 1))
+    ref = F.expect()
+    for least, same in ((saved + 1, True), (saved, False), (1 << 60, True), (-1, True)):
+        out = _run(fg, F, min_saved=least)
+        fg.fg_sync_status()
+        assert torch.equal(out, plain) == same, least
+        _hold(out, *ref)
 
 
 def test_rows_that_reach_into_the_prefix_go_alone(fg):
@@ -312,7 +328,7 @@ def test_rows_behind_the_last_sequence_stay(fg):
     out = torch.full_like(wide, 7.0)
     share = fg.PageShare.empty(F.tab, int(F.cu[-1]) + 3)
     fg.fg_pages_share(F.tab, _i32(F.cu), share, 1)
-    fg.fg_paged_attention_shared(F.pool, F.tab, _i32(F.cu), share, wide[:, :128], 2, out[:, :128], 25)
+    fg.fg_paged_attention_shared(F.pool, F.tab, _i32(F.cu), share, wide[:, :128], 2, out[:, :128], 25, 0)
     fg.fg_sync_status()
     _hold(out[:F.cu[-1], :128], *F.expect())
     assert (out[F.cu[-1]:] == 7.0).all() and (out[:, 128:] == 7.0).all()
@@ -345,7 +361,7 @@ def test_graphs_streams_and_shared_workspaces(fg):
 
         def call(F=F, stream=None):
             fg.fg_pages_share(F.tab, F.dev_cu, F.s, 1, ws=ws, stream=stream)
-            fg.fg_paged_attention_shared(F.pool, F.tab, F.dev_cu, F.s, F.dev_q, F.heads * F.r, F.out, int(F.n.max()), ws=ws, stream=stream)
+            fg.fg_paged_attention_shared(F.pool, F.tab, F.dev_cu, F.s, F.dev_q, F.heads * F.r, F.out, int(F.n.max()), 0, ws=ws, stream=stream)
 
         call()
         torch.cuda.synchronize()
