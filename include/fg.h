@@ -531,7 +531,7 @@ fg_status fg_rotate(const fg_rotary* r, const void* x, fg_dtype dt, int64_t rows
 
 /* The append of a model with rotary positions, in one launch: q's rows (device
  * [ntok][ldq], q_heads heads) are rotated to their positions lens[i] - n + t into
- * q_out (device [ntok][ldqo]; may be q itself), k's rows are rotated, rounded to the
+ * q_out (device [ntok][ldqo]: q itself with ldqo = ldq, or memory apart from it), k's rows are rotated, rounded to the
  * activations' type and stored as fg_paged_append stores them, v's as they are:
  * the same bits as fg_rotate of q and k and fg_paged_append of the result.
  * rot a multiple of 16, at most head_dim.  q may be NULL (then q_out is not
@@ -585,10 +585,15 @@ fg_status fg_pages_share(const fg_page_table* t, const int32_t* cu, int64_t min_
  * max_q class and share.  A sequence whose rows do not all stand behind its
  * group's tokens is computed by itself, and so is every sequence of an fp32 pool
  * (fp32 sums on the CUDA cores: the rows' arithmetic, not the cache's bytes, is
- * their cost).  Sharing has launches of its own: where the groups save less than
- * min_saved bytes of cache reads (tokens * (rows - 1) of every group; negative: 144
- * MB) every sequence goes by itself.  ws: 256-byte aligned, >=
- * fg_paged_attention_shared_workspace_bytes. */
+ * their cost).
+ * Sharing has launches of its own: where the groups save less than min_saved bytes
+ * of cache reads (0: share all the same; negative: 64 MB) every sequence goes by
+ * itself.  Counted are a sequence's reads of its group's tokens, once for up to 16
+ * rows of a K/V head, four times for each 256 of more (they take as long), less
+ * the group's own, once for each 64 of its rows (four times for each 256 in calls
+ * of more than 16 where they are more than 128), and 8 tokens for the parts of
+ * each of its rows.  (A row here: a row of the batch and a query head.)
+ * ws: 256-byte aligned, >= fg_paged_attention_shared_workspace_bytes. */
 size_t fg_paged_attention_shared_workspace_bytes(const fg_page_pool* pool, const fg_page_table* t, int32_t q_heads,
                                                  int64_t ntok, int64_t max_q);
 fg_status fg_paged_attention_shared(const fg_page_pool* pool, const fg_page_table* t, const int32_t* cu,

@@ -855,9 +855,10 @@ class Rotary:
 
 def _rotary_on(rotary: "Rotary", index: int) -> "Rotary":
     """The rotation, when it lies on that device, the current one."""
-    if rotary.index != index or index < 0 or index != torch._C._cuda_getDevice():
-        raise ValueError(f"the rotation is on {rotary.device}, the rows on device {index}, the current device is "
-                         f"{torch.cuda.current_device()}")
+    if index < 0 or rotary.index != index:
+        raise ValueError(f"the rotation is on {rotary.device}, the rows on {f'cuda:{index}' if index >= 0 else 'no device'}")
+    if index != torch._C._cuda_getDevice():
+        raise ValueError(f"the rotation is on {rotary.device}, the current device is cuda:{torch._C._cuda_getDevice()}")
     return rotary
 
 

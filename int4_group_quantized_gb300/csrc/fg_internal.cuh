@@ -196,6 +196,8 @@ fg_status prefill_attention_simt(const fg_kv& kv, const void* q, int64_t ldq, in
 
 // ---- rotary positions ------------------------------------------------------
 fg_status check_rotary(const fg_rotary* r, int32_t head_dim);
+// Rotated rows (cols columns) go to the rows themselves or to memory apart from them.
+fg_status check_apart(const void* x, int64_t ldx, const void* out, int64_t ldo, int64_t rows, int64_t cols, fg_dtype dt);
 
 // ---- codec -----------------------------------------------------------------
 fg_status quantize_rows(const void* x, fg_dtype dt, int64_t rows, int64_t cols, uint8_t* codes,

@@ -99,12 +99,12 @@ __device__ __forceinline__ int64_t slot_of(const Pool& p, int page, int h, int p
 // that one (griddepcontrol.wait) before it reads or writes anything.  Calls outside a graph gain the 2 us between kernels
 // (a small step's attention 10.8 us from 13.1, an append of a step 7.9 from 10.2).
 template <class... P, class... A>
-fg_status launch(const char* what, bool early, void (*kernel)(P...), unsigned grid, unsigned block, size_t smem, cudaStream_t st, A&&... args) {
+fg_status launch(const char* what, bool early, void (*kernel)(P...), dim3 grid, unsigned block, size_t smem, cudaStream_t st, A&&... args) {
   cudaLaunchAttribute pdl[1];
   pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   pdl[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
+  cfg.gridDim = grid;
   cfg.blockDim = dim3(block);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;

@@ -293,11 +293,14 @@ fg_status join(const AttnArgs<T>& a, const ClassPlan& step, const ClassPlan& til
                       32 * kJoinWarps, 0, st, a, step, tile);
 }
 
-// Bytes of cache reads that groups have to save before a call shares: the prefixes' launches take 15 to 25 us whatever they
-// do.  One prefix for a step of 64 sequences, 32 heads of 128: 83 MB saved 42.0 us each by itself and 52.1 shared, 165 MB 56.8
-// and 52.3, 1.3 GB 258 and 73; 16 sequences, 32 on 8 heads: 79 MB 31.9 and 42.7, 157 MB 46.4 and 46.5, 629 MB 133 and 69; 4
-// sequences, 32 heads: 126 MB 44.9 and 55.4, 503 MB 133 and 122.
-constexpr int64_t kSharedSaves = int64_t(144) << 20;
+// Bytes of cache reads that groups have to save before a call shares, as paged_prefix.cuh counts them.  Both sides in us, alone
+// (the launches that find it out among them: 8 for steps, 13 for chunks) and shared.  Steps over one prefix: 64 sequences, 32
+// heads of 128, 75 MB saved: 50 and 52, 157 MB: 65 and 52, 1.3 GB: 266 and 71; 16 sequences, 32 heads on 8, 39 MB: 32 and 39, 77
+// MB: 40 and 40, 157 MB: 54 and 43, 629 MB: 142 and 67.  Chunks, 16 sequences of 32 heads: 32 rows over 512 tokens, 126 MB: 99
+// and 105, over 2,048, 566 MB: 172 and 125; 128 rows over 2,048, 250 MB: 186 and 195, over 8,192, 1.3 GB: 479 and 360; 400 rows
+// over 2,048, 31 MB: 354 and 410 (their units of 256 rows are as full by themselves as in a group), over 8,192, 910 MB: 990 and
+// 917; ragged ones of 2 to 139 rows, 32 heads on 8, over two prefixes of 1,920 and 4,160, 69 MB: 194 and 163.
+constexpr int64_t kSharedSaves = int64_t(64) << 20;
 
 // ---- workspace ------------------------------------------------------------------------
 constexpr int kMaxSms = 160;   // a workspace fits this many SMs; launches use no more
@@ -511,9 +514,11 @@ fg_status fg_paged_attention_shared(const fg_page_pool* pool, const fg_page_tabl
   if (!err) return fail(FG_ERR_CUDA, "device error word");
   // in tokens; K and V of one are 1.25 bytes an element
   const int64_t token = static_cast<int64_t>(pool->heads) * pool->head_dim * 5 / 4;
-  const int64_t least = ((min_saved < 0 ? kSharedSaves : min_saved) + token - 1) / token;
-  // no group saves more than every row but one of all that a table row can name
-  const bool never = least > 0 && static_cast<double>(t->stride) * t->page_size * static_cast<double>(ntok) < static_cast<double>(least);
+  const int64_t bytes = min_saved < 0 ? kSharedSaves : min_saved, least = bytes / token + (bytes % token != 0);
+  // all sequences' reads of all that a table row can name are no less than what groups can save
+  const double group = static_cast<double>(q_heads / pool->heads), most = static_cast<double>(std::min<int64_t>(t->seqs, ntok));
+  const double reads = max_q * group <= kStepRows ? most : kChunkRead * (most + static_cast<double>(ntok) * group / kTileRows);
+  const bool never = least > 0 && static_cast<double>(t->stride) * t->page_size * reads < static_cast<double>(least);
   return launch_attn<__half>(*pool, *t, cu, q, ldq, q_heads, ntok, max_q, 0, 0, out, ldo, ws, err, stream, never ? nullptr : s, least);
 }
 

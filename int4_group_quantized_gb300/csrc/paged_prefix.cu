@@ -42,26 +42,9 @@ constexpr int kKeys = 1 << kPrefixKeysLog2;
 constexpr int kSoftWarps = 8, kKeyWarps = 4, kValueWarps = 3;
 constexpr int kFirstKey = kSoftWarps, kFirstValue = kFirstKey + kKeyWarps, kMmaWarp = kFirstValue + kValueWarps;
 constexpr int kThreads = 32 * (kMmaWarp + 1);
-static_assert(kPrefixRows == 64 && kFirstKey % 4 == 0 , "the layout below");
+static_assert(kPrefixRows == 64 && kThreads == 512 && kFirstKey % 4 == 0 && kFirstValue % 4 == 0, "the layout below");
 constexpr float kLift = 4.0f;          // a row's largest weight is 2^4 or more when its maximum is found (paged_tile.cu)
 constexpr uint32_t kMostHalf = 0x7800u;   // 2^15 as fp16: weights up to it stand
-
-// mbar_wait with each poll asleep for up to kNap ns: a few of the CTA's warps work while most wait, and what those poll
-// takes issue slots from these (half of all instructions were polls).
-constexpr uint32_t kNap = 4000;
-__device__ __forceinline__ bool wait_on(uint64_t* bar, uint32_t parity, uint32_t limit, volatile int* abort) {
-  for (uint32_t i = 0; i < limit; ++i) {
-    uint32_t over;
-    asm volatile("{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3; selp.u32 %0, 1, 0, p; }"
-                 : "=r"(over)
-                 : "r"(smem_u32(bar)), "r"(parity), "r"(kNap)
-                 : "memory");
-    if (over) return true;
-    if ((i & 15u) == 15u && *abort) return false;
-  }
-  *abort = 1;
-  return false;
-}
 
 template <int D>
 struct Smem {
@@ -271,6 +254,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const PrefixArgs p,
     mbar_init(drained, kSoftWarps);
     mbar_init(done, 1);
     *abort_flag = 0;
+    line.alone = 0;
     mbar_fence_init();
   }
   if (warp == kMmaWarp) tmem_alloc(tmem_slot, kTmemCols);
@@ -281,7 +265,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const PrefixArgs p,
   griddep_launch();
   griddep_wait();
   prefix_line(p, line);
-  Walk k;
+  Walk k = {};
   walk_begin(k, p, line);
 
   if (warp >= kFirstKey && warp < kMmaWarp) {
@@ -368,7 +352,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const PrefixArgs p,
     int seg = 0, x = k.x;
     for (int n = 0; n < tiles; ++n) {
       if (value) {
-        ok = n < 2 || wait_on(&pvdone[n & 1], ((n >> 1) - 1) & 1, wait_limit, abort_flag);
+        ok = n < 2 || mbar_wait(&pvdone[n & 1], ((n >> 1) - 1) & 1, wait_limit, abort_flag);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         uint8_t* const to = sV + (n & 1) * S::kV + r * 128;
@@ -386,7 +370,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const PrefixArgs p,
       }
       // P of the tile two before is there: S has read its codes, the softmax its scales.  (And Q and the sums of the segment
       // two before, whose place a new one takes: its last tile is no later.)
-      ok = n < 2 || wait_on(&pfull[n & 1], ((n >> 1) - 1) & 1, wait_limit, abort_flag);
+      ok = n < 2 || mbar_wait(&pfull[n & 1], ((n >> 1) - 1) & 1, wait_limit, abort_flag);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       if (x == k.x) {
@@ -438,7 +422,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const PrefixArgs p,
       __syncwarp();
       if (lane == 0) mbar_arrive(&kfull[n & 1]);
       if (extra(n)) {
-        ok = n < 2 || wait_on(&pvdone[n & 1], ((n >> 1) - 1) & 1, wait_limit, abort_flag);
+        ok = n < 2 || mbar_wait(&pvdone[n & 1], ((n >> 1) - 1) & 1, wait_limit, abort_flag);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         uint8_t* const vto = sV + (n & 1) * S::kV + xg * S::kPanel + (96 + lane) * 128;
@@ -468,7 +452,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const PrefixArgs p,
       int n = 0, seg = 0;
       bool ok = true, pending = false;
       auto wait = [&](uint64_t* bar, int phase) {
-        if (ok) ok = wait_on(bar, phase & 1, wait_limit, abort_flag);
+        if (ok) ok = mbar_wait(bar, phase & 1, wait_limit, abort_flag);
         return ok;
       };
       // A wait takes some 250 cycles even where it is over, and a batch of MMAs 600 to issue: so barriers are looked at before
@@ -540,7 +524,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const PrefixArgs p,
       for (int x = k.x; x < k.x1; ++x, ++n) {
         const int st = n & 1;
         const uint32_t ts = tmem + kScore + 128 * st + lanes + first;
-        ok = wait_on(&sfull[st], (n >> 1) & 1, wait_limit, abort_flag);
+        ok = mbar_wait(&sfull[st], (n >> 1) & 1, wait_limit, abort_flag);
         ok = __all_sync(0xffffffffu, ok);
         tc_fence_after();
         const float4 meta = sMeta[st * kKeys + r];
@@ -662,7 +646,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const PrefixArgs p,
           for (int i = 0; i < 16; ++i)
             if (2 * i < rows) l[i] = make_float2(l[i].x * shrink[2 * i], l[i].y * shrink[2 * i + 1]);
           if (ok && x > k.x) {   // the segment's sums so far
-            ok = wait_on(&pvdone[st ^ 1], ((n - 1) >> 1) & 1, wait_limit, abort_flag);
+            ok = mbar_wait(&pvdone[st ^ 1], ((n - 1) >> 1) & 1, wait_limit, abort_flag);
             ok = __all_sync(0xffffffffu, ok);
             tc_fence_after();
             if (ok)
@@ -694,7 +678,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const PrefixArgs p,
       }
       if (gave_up) break;
       // ---- the segment's rows: their parts ------------------------------------------------
-      ok = wait_on(&pvdone[(n - 1) & 1], ((n - 1) >> 1) & 1, wait_limit, abort_flag);
+      ok = mbar_wait(&pvdone[(n - 1) & 1], ((n - 1) >> 1) & 1, wait_limit, abort_flag);
       ok = __all_sync(0xffffffffu, ok);
       tc_fence_after();
 #pragma unroll
@@ -759,34 +743,44 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const PrefixArgs p,
 }
 
 // ---- joining: a row's parts to its home, in order ----------------------------------------------------
-constexpr int kJoinThreads = 256;
+// Only a unit that some worker goes on with has parts, so the blocks look at the workers: kSplit of them (blockIdx.y) take the
+// rows of the unit that worker blockIdx.x of its class (blockIdx.z) is the first to go on with, if any.  (Looking at all rows
+// of the list took 40 us for 6400 rows of 32 heads with nothing to join.)
+constexpr int kJoinThreads = 256, kSplit = 8;
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const PrefixArgs p) {
   constexpr int kCols = D / 4, kAtOnce = kJoinThreads / kCols, kFew = 4;
   griddep_launch();
   griddep_wait();
   const AttnArgs<__half>& a = p.a;
-  const int col = threadIdx.x % kCols, group = a.shape.group;
+  const int col = threadIdx.x % kCols, group = a.shape.group, lane = threadIdx.x & 31, worker = blockIdx.x;
   const uint32_t mates = D == 128 ? 0xffffffffu : 0xffffu << (threadIdx.x & 16);   // a row's lanes
-  const int listed = a.prefix.begin[a.tab.seqs], planned = *a.prefix.planned;
-  const int64_t pairs = static_cast<int64_t>(listed < 0 || listed > a.batch.ntok ? 0 : listed) * a.q_heads;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kAtOnce + threadIdx.x / kCols; i < pairs; i += static_cast<int64_t>(gridDim.x) * kAtOnce) {
-    const int x = static_cast<int>(i / a.q_heads), hq = static_cast<int>(i - static_cast<int64_t>(x) * a.q_heads);
-    int g = -1;              // the last group that begins at x or before, found by the row's lanes together
-    for (int n = kCols; n == kCols;) {
-      const int c = g + 1 + col;
-      n = __popc(__ballot_sync(mates, c < planned && a.prefix.begin[c] <= x));
-      g += n;
+  const int planned = *a.prefix.planned;
+  // the class's last group that begins before the worker's share does, found by every warp
+  const bool tall = blockIdx.z > 0;
+  int g = -1;
+  for (int g0 = 0; g0 < planned; g0 += 32) {
+    bool before = false;
+    if (g0 + lane < planned) {
+      const PrefixGroup& x = a.prefix.info[g0 + lane];
+      before = x.units > 0 && (x.extra > 0) == tall && x.base < worker * x.per;
     }
-    if (g < 0 || shared_group(a.prefix, a.tab, a.batch, g).list == 0) continue;
-    const PrefixGroup at = a.prefix.info[g];
-    const int h = hq / group, r = (x - at.first_row) * group + hq - h * group, u = r / at.rows;
-    if (r < 0 || u >= at.units) continue;
-    const int64_t start = at.base + (static_cast<int64_t>(h) * at.units + u) * at.tiles;
-    const int w = static_cast<int>(start / at.per), count = static_cast<int>((start + at.tiles - 1) / at.per) - w;
-    if (count == 0) continue;
+    const uint32_t found = __ballot_sync(0xffffffffu, before);
+    if (found) g = g0 + 31 - __clz(found);
+  }
+  if (g < 0) return;
+  const PrefixGroup at = a.prefix.info[g];
+  const int64_t in = worker * at.per - at.base, unit = (in - 1) / at.tiles, start = at.base + unit * at.tiles;   // of the tile before the share
+  const int h = static_cast<int>(unit / at.units), u = static_cast<int>(unit - static_cast<int64_t>(h) * at.units);
+  if (h >= a.pool.heads || start / at.per + 1 != worker) return;   // past the group, or not the first
+  const int count = static_cast<int>((start + at.tiles - 1) / at.per) - (worker - 1);
+  if (count == 0) return;            // the share begins with the next unit
+  const int rows = min(at.rows, shared_group(a.prefix, a.tab, a.batch, g).list * group - u * at.rows);
+  for (int rr = blockIdx.y * kAtOnce + threadIdx.x / kCols; rr < rows; rr += kSplit * kAtOnce) {
+    const int r = u * at.rows + rr, x = r / group;
+    const int64_t i = static_cast<int64_t>(at.first_row + x) * a.q_heads + h * group + r - x * group;
     float* const home = a.prefix.home + i * D + 4 * col;
-    const int64_t extra = at.extra + static_cast<int64_t>(w + 1) * at.stride + r - u * at.rows;
+    const int64_t extra = at.extra + static_cast<int64_t>(worker) * at.stride + rr;
     float2 s = a.prefix.home_stat[i];
     float4 o = *reinterpret_cast<const float4*>(home);
     float m = s.x, l = s.y;
@@ -839,10 +833,9 @@ fg_status launch(const PrefixArgs& p, cudaStream_t st) {
 }  // namespace
 
 fg_status paged_prefix_join(const PrefixArgs& p, int head_dim, cudaStream_t st) {
-  const int64_t want = (static_cast<int64_t>(p.a.batch.ntok) * p.a.q_heads * (head_dim / 4) + kJoinThreads - 1) / kJoinThreads, cap = 8 * static_cast<int64_t>(p.workers);
   Trace tr(KC_ATTN_COMBINE, st);
-  return paged::launch("prefix_join_kernel", true, head_dim == 128 ? prefix_join_kernel<128> : prefix_join_kernel<64>,
-                       static_cast<unsigned>(want < cap ? want : cap), kJoinThreads, 0, st, p);
+  const dim3 grid(static_cast<unsigned>(p.workers), kSplit, p.tile.workers > 0 ? 2 : 1);
+  return paged::launch("prefix_join_kernel", true, head_dim == 128 ? prefix_join_kernel<128> : prefix_join_kernel<64>, grid, kJoinThreads, 0, st, p);
 }
 
 fg_status paged_prefix(const PrefixArgs& p, int head_dim, cudaStream_t st) { return head_dim == 128 ? launch<128>(p, st) : launch<64>(p, st); }

@@ -378,6 +378,7 @@ extern "C" fg_status fg_paged_append_rotated(const fg_page_pool* pool, const fg_
   if (!aligned(cu, 4) || !aligned(k, 16) || !aligned(v, 16) || ld % 8 || !aligned(k_restored, 16) || !aligned(v_restored, 16) ||
       (k_restored && ldr % 8) || (hq > 0 && (!aligned(q, 16) || !aligned(q_out, 16) || ldq % 8 || ldqo % 8)))
     return fail(FG_ERR_ALIGN, "rows need 16-byte alignment and strides that are multiples of 8");
+  if (hq > 0) FG_TRY(check_apart(q, ldq, q_out, ldqo, ntok, hq, static_cast<fg_dtype>(pool->dtype)));
   unsigned int* err = device_error_word();
   if (!err) return fail(FG_ERR_CUDA, "device error word");
   if (pool->dtype == FG_F16)

@@ -206,6 +206,17 @@ fg_status check_rotary(const fg_rotary* r, int32_t head_dim) {
   return FG_OK;
 }
 
+fg_status check_apart(const void* x, int64_t ldx, const void* out, int64_t ldo, int64_t rows, int64_t cols, fg_dtype dt) {
+  const char *xb = static_cast<const char*>(x), *ob = static_cast<const char*>(out);
+  const int64_t e = static_cast<int64_t>(dtype_bytes(dt)), xn = ((rows - 1) * ldx + cols) * e, on = ((rows - 1) * ldo + cols) * e;
+  // columns of one buffer's rows may lie side by side
+  const int64_t row = ldx * e, off = rows > 1 && ldx == ldo ? ((ob - xb) % row + row) % row : 0;
+  const bool beside = off >= cols * e && row - off >= cols * e;
+  if (x == out ? (rows > 1 && ldx != ldo) : (xb < ob + on && ob < xb + xn && !beside))
+    return fail(FG_ERR_ARG, "rotated rows go to the rows themselves, with their stride, or to memory apart from them");
+  return FG_OK;
+}
+
 }  // namespace fg
 
 using namespace fg;
@@ -257,13 +268,7 @@ fg_status fg_rotate(const fg_rotary* r, const void* x, fg_dtype dt, int64_t rows
   const int64_t h1 = static_cast<int64_t>(heads) * head_dim;
   if (rows > 1 && (ldx < h1 || ldo < h1)) return fail(FG_ERR_SHAPE, "row stride below heads * head_dim = %lld", (long long)h1);
   if (!aligned(x, dtype_bytes(dt)) || !aligned(out, dtype_bytes(dt)) || !aligned(pos, 4)) return fail(FG_ERR_ALIGN, "rows or positions");
-  const char *xb = static_cast<const char*>(x), *ob = static_cast<const char*>(out);
-  const int64_t e = static_cast<int64_t>(dtype_bytes(dt)), xn = ((rows - 1) * ldx + h1) * e, on = ((rows - 1) * ldo + h1) * e;
-  // columns of one buffer's rows may lie side by side
-  const int64_t row = ldx * e, off = rows > 1 && ldx == ldo ? ((ob - xb) % row + row) % row : 0;
-  const bool beside = off >= h1 * e && row - off >= h1 * e;
-  if (x == out ? (rows > 1 && ldx != ldo) : (xb < ob + on && ob < xb + xn && !beside))
-    return fail(FG_ERR_ARG, "out is x itself, with its row stride, or memory apart from it");
+  FG_TRY(check_apart(x, ldx, out, ldo, rows, h1, dt));
   if (dt == FG_F16) return rotate<__half>(*r, x, rows, ldx, heads, head_dim, pos, out, ldo, stream);
   return rotate<float>(*r, x, rows, ldx, heads, head_dim, pos, out, ldo, stream);
 }

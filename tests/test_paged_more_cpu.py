@@ -119,6 +119,8 @@ def test_append_rotated_arguments(fg):
     assert app(ld=120) == 2 and app(ldq=248) == 2 and app(ldqo=248) == 2 and app(kr=P, vr=P, ldr=64) == 2
     assert app(ld=132) == 3 and app(ldq=260) == 3 and app(q=P + 8) == 3 and app(qo=P + 2) == 3 and app(k=P + 8) == 3 and app(cu=P + 1) == 3
     assert app(ntok=(1 << 31) - 1) == 8
+    # rotated queries: q itself with its stride, or memory apart from it
+    assert app(ldqo=264) == 1 and app(qo=P + 16) == 1 and app(qo=P + 256) == 1 and app(qo=P + 512, ldq=512, ldqo=264) == 1
 
 
 def test_read_arguments(fg):
@@ -198,3 +200,36 @@ def test_shared_attention_arguments(fg):
     assert fg.lib.fg_paged_attention_shared_workspace_bytes(_br(f32), _br(tab), 4, 4, 2) == \
         fg.lib.fg_paged_attention_workspace_bytes(_br(f32), _br(tab), 4, 4, 2)
     assert attend(pool=f32, wsb=16) == 5
+
+
+def test_python_checks(fg):
+    import torch
+
+    i32 = lambda *n: torch.zeros(n, dtype=torch.int32)
+    with pytest.raises(ValueError, match="layout"):
+        fg.Rotary(64, "sideways", device="cpu")
+    with pytest.raises(fg.FGError, match="FG_ERR_SHAPE"):
+        fg.Rotary(63, device="cpu")
+    rotary = fg.Rotary(64, device="cpu")
+    assert rotary.turns.dtype == torch.int64 and rotary.turns.numel() == 32 and rotary.scale == 1.0
+    x = torch.zeros((4, 128), dtype=torch.float16)
+    with pytest.raises(ValueError, match="heads"):
+        fg.fg_rotate(rotary, x, i32(4), 3)
+    with pytest.raises(ValueError, match="pos"):
+        fg.fg_rotate(rotary, x, i32(3), 2)
+    with pytest.raises(ValueError, match="pos"):
+        fg.fg_rotate(rotary, x, i32(4).long(), 2)
+    with pytest.raises(ValueError, match="out"):
+        fg.fg_rotate(rotary, x, i32(4), 2, x.float())
+    with pytest.raises(ValueError, match="adjacent"):
+        fg.fg_rotate(rotary, torch.zeros((4, 256), dtype=torch.float16)[:, ::2], i32(4), 2)
+    with pytest.raises(ValueError, match="no device"):
+        fg.fg_rotate(rotary, x, i32(4), 2)
+    with pytest.raises(ValueError, match="first"):
+        fg.PageShare(i32(3), i32(3), i32(2), i32(3), i32(4), i32(5))
+    with pytest.raises(ValueError, match="begin"):
+        fg.PageShare(i32(3), i32(3), i32(3), i32(3), i32(3), i32(5))
+    with pytest.raises(ValueError, match="rows"):
+        fg.PageShare(i32(3), i32(3), i32(3), i32(3), i32(4), torch.zeros(5))
+    s = fg.PageShare(i32(3), i32(3), i32(3), i32(3), i32(4), i32(5))
+    assert (s.seqs, s.ntok) == (3, 5)

@@ -248,8 +248,8 @@ def test_what_saves_too_little_is_not_shared(fg):
     F = Forked(fg, ([0] * 6 + [1] * 3, [9, 30]), [4, 1, 30, 100, 17, 5, 6, 7, 8], [1, 1, 30, 2, 1, 1, 1, 1, 1], 2, 2, 64, 16, 24)
     plain = torch.full(F.q.shape, 7.0, dtype=torch.float16, device="cuda")
     fg.fg_paged_attention(F.pool, F.tab, _i32(F.cu), torch.as_tensor(F.q, device="cuda"), 4, plain, 30)
-    token, listed = 2 * 64 * 5 // 4, [36, 3]
-    saved = token * (9 * 16 * (listed[0] - 1) + 30 * 16 * (listed[1] - 1))
+    # reads alone less those of the group (72 rows of a K/V head: two units; 6: one), the chunk's four, and the 39 rows' parts
+    saved = 2 * 64 * 5 // 4 * (9 * 16 * (5 + 4 - 2) + 30 * 16 * (3 - 1) - 8 * 2 * 39)
     ref = F.expect()
     for least, same in ((saved + 1, True), (saved, False), (1 << 60, True), (-1, True)):
         out = _run(fg, F, min_saved=least)
@@ -384,3 +384,179 @@ def test_graphs_streams_and_shared_workspaces(fg):
         torch.cuda.synchronize()
         assert all(torch.equal(F.out, w) for F, w in zip((A, B), want))
     fg.fg_sync_status()
+
+
+def test_waits_that_run_out(fg):
+    """With a limit of 0 every wait gives up at once: the error word says so, and the next call is right."""
+    F = Forked(fg, ([0] * 5 + [1] * 40, [40, 12]), [5] * 45, [1] * 5 + [2] * 40, 2, 4, 128, 16, 25)
+    want = _run(fg, F)
+    fg.fg_sync_status()
+    old = fg.fg_set_wait_limit(0)
+    try:
+        _run(fg, F)
+        with pytest.raises(fg.FGError) as e:
+            fg.fg_sync_status()
+        assert e.value.status == 7
+    finally:
+        fg.fg_set_wait_limit(old)
+    assert torch.equal(_run(fg, F), want)
+    fg.fg_sync_status()
+    _hold(want, *F.expect())
+
+
+def test_one_row_listed_twice_and_groups_that_overlap_stay_in_bounds(fg):
+    """Lists that contradict themselves: whoever's rows are not where the share says goes by itself."""
+    F = Forked(fg, ([0, 0, 0, 1, 1, 1], [6, 8]), [5, 6, 7, 8, 9, 1], [1] * 6, 2, 2, 64, 16, 26)
+    good = F.find(fg)
+    ref = F.expect()
+    s = fg.PageShare(*[getattr(good, f).clone() for f in FIELDS])
+    s.rows[1] = s.rows[0]                                    # sequence 1's place names sequence 0's row
+    _hold(_run(fg, F, s), *ref)
+    s = fg.PageShare(*[getattr(good, f).clone() for f in FIELDS])
+    s.begin[1] = 0                                           # group 0 has no rows, group 1 everyone's
+    s.first[:3] += 0
+    _hold(_run(fg, F, s)[3:], ref[0][3:], ref[1][3:])
+    fg.fg_sync_status()
+
+
+def test_a_gap_between_groups_ends_them(fg):
+    """Groups are numbered without gaps: those behind one are not made, and their sequences go by themselves."""
+    n = 40
+    F = Forked(fg, (np.repeat(np.arange(n), 2), [4] * n), [3] * (2 * n), [1] * (2 * n), 1, 2, 64, 16, 28)
+    good, ref = F.find(fg), F.expect()
+    assert int(good.leader[n - 1]) == 2 * n - 2
+    s = fg.PageShare(*[getattr(good, f).clone() for f in FIELDS])
+    s.leader[3] = -1
+    _hold(_run(fg, F, s), *ref)
+    every = _run(fg, F, good, min_saved=2 ** 63 - 1)         # never worth it
+    alone = torch.empty_like(every)
+    fg.fg_paged_attention(F.pool, F.tab, _i32(F.cu), torch.as_tensor(F.q, device="cuda"), F.heads * F.r, alone, 1)
+    fg.fg_sync_status()
+    assert torch.equal(every, alone)
+
+
+@pytest.mark.parametrize("n, pages, shares", [(1, 20, False), (1, 90, True), (7, 10, False), (20, 24, True), (150, 24, False)])
+def test_sharing_where_it_saves(fg, n, pages, shares):
+    """The library's own bound: 16 sequences over one prefix go by themselves, bit for bit, where that is cheaper."""
+    F = Forked(fg, ([0] * 16, [pages]), [n] * 16, [n] * 16, 16, 1, 128, 64, 29)
+    alone, both = torch.empty(F.q.shape, dtype=torch.float16, device="cuda"), _run(fg, F)
+    fg.fg_paged_attention(F.pool, F.tab, _i32(F.cu), torch.as_tensor(F.q, device="cuda"), 16, alone, n)
+    assert not torch.equal(alone, both)
+    assert torch.equal(_run(fg, F, min_saved=-1), both if shares else alone)
+    token = 16 * 128 * 5 // 4
+    rows = 16 * n
+    units = (16 if n <= 16 else 16 * 4) - (-(-rows // 64) if rows <= 128 else 4 * -(-rows // 256))
+    saved = (units * 64 * pages - 8 * rows) * token
+    assert (saved >= 64 << 20) == shares
+    if saved > 0:
+        assert torch.equal(_run(fg, F, min_saved=saved), both) and torch.equal(_run(fg, F, min_saved=saved + 1), alone)
+    else:
+        assert torch.equal(_run(fg, F, min_saved=1), alone)
+    fg.fg_sync_status()
+
+
+@pytest.mark.parametrize("captured", [False, True])
+def test_a_serving_run(fg, captured):
+    """A prompt, its children, and their steps: queries and keys rotated as they are appended, the prompt's pages found and read
+    once for all, every step's rows held to attention over what the cache then holds, which is read back besides."""
+    heads, r, d, ps, steps = 2, 2, 64, 16, 6
+    seqs, pages = 6, 120
+    gen = torch.Generator(device="cuda").manual_seed(31)
+    pool, tab = fg.PagePool(pages, ps, heads, d), fg.PageTable.empty(seqs, 40, pages, ps)
+    pools, rotary = fg.PagePools([pool]), fg.Rotary(d)
+
+    def rows(n):
+        return [torch.randn((n, k * d), generator=gen, device="cuda").half() for k in (heads * r, heads, heads)]
+
+    def hold(q, out, cu):
+        table, lens = tab.table.cpu().numpy(), tab.lens.cpu().numpy()
+        arr = [[t.cpu().numpy() for t in x] for x in ((pool.k_codes, pool.k_mins, pool.k_scales), (pool.v_codes, pool.v_mins, pool.v_scales))]
+        for i in range(seqs):
+            a, e = int(cu[i]), int(cu[i + 1])
+            if a == e:
+                continue
+            j = np.arange(lens[i])
+            pos = np.repeat(np.arange(lens[i] - (e - a), lens[i]), r)
+            for h in range(heads):
+                qq = q[a:e].double().cpu().numpy().reshape(e - a, -1, d)[:, h * r:(h + 1) * r].reshape(-1, d)
+                k, v = ([t[table[i, j // ps], h, j % ps] for t in x] for x in arr)
+                ref, t1 = op.attention_bound(qq, k, v, pos, kind="step")
+                _, t2 = op.attention_bound(qq, k, v, pos, kind="chunk")
+                got = out[a:e].double().cpu().numpy().reshape(e - a, -1, d)[:, h * r:(h + 1) * r].reshape(-1, d)
+                assert op.off_by_too_much(got, ref, t1 + t2 + 130 * 2.0 ** -22 * np.abs(ref)) is None
+
+    # the prompt: 100 rows of sequence 0, and another of 37 that shares nothing
+    cu = _i32([0, 100, 100, 100, 100, 137, 137])
+    fg.fg_pages_reserve(tab, cu)
+    q, k, v = rows(137)
+    fg.fg_paged_append_rotated(pool, tab, cu, rotary, q, heads * r, None, k, v)
+    share = fg.PageShare.empty(tab, 137)
+    fg.fg_pages_share(tab, cu, share, 1)
+    assert share.group.max() < 0
+    out = torch.empty_like(q)
+    fg.fg_paged_attention_shared(pool, tab, cu, share, q, heads * r, out, 100, 0)
+    fg.fg_sync_status()
+    hold(q, out, cu.tolist())
+    # three children; then steps of everyone but row 5
+    fg.fg_pages_fork(tab, pools, _i32([0, 0, 0]), _i32([1, 2, 3]))
+    cu = _i32([0, 1, 2, 3, 4, 5, 5])
+    q, k, v = rows(5)
+    turned, out = torch.empty_like(q), torch.empty_like(q)
+    share = fg.PageShare.empty(tab, 5)
+    kr, vr = torch.empty_like(k), torch.empty_like(v)
+    back = [torch.empty_like(k), torch.empty_like(v)]
+
+    def step():
+        fg.fg_pages_reserve(tab, cu)
+        fg.fg_paged_append_rotated(pool, tab, cu, rotary, q, heads * r, turned, k, v, kr, vr)
+        fg.fg_pages_share(tab, cu, share, 1)
+        fg.fg_paged_attention_shared(pool, tab, cu, share, turned, heads * r, out, 1, 0)
+        fg.fg_paged_read(pool, tab, cu, *back)
+
+    graph = None
+    for n in range(steps):
+        for t, new in zip((q, k, v), rows(5)):
+            t.copy_(new)
+        if captured and n == 1:
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph):
+                step()
+        if graph is None:
+            step()
+        else:
+            graph.replay()
+        fg.fg_sync_status()
+        assert tab.lens.tolist() == [101 + n] * 4 + [38 + n, 0]
+        assert share.group.tolist() == [0, 0, 0, 0, -1, -1] and share.tokens.tolist()[:4] == [96] * 4
+        hold(turned, out, cu.tolist())
+        assert torch.equal(back[0], kr) and torch.equal(back[1], vr)
+
+
+def test_pools_past_32_bits(fg):
+    """Codes of K past 4 GB: the last pages hold what a small pool's first ones do."""
+    heads, d, ps, big = 8, 128, 256, 34000
+    F = Forked(fg, ([0] * 3, [2]), [40, 300, 7], [1, 20, 1], heads, 1, d, ps, 27)
+    want = _run(fg, F)
+    pool = fg.PagePool(big, ps, heads, d)
+    assert pool.k_codes.numel() > 2 ** 32
+    for dst, src in zip((pool.k_codes, pool.k_mins, pool.k_scales, pool.v_codes, pool.v_mins, pool.v_scales),
+                        (F.pool.k_codes, F.pool.k_mins, F.pool.k_scales, F.pool.v_codes, F.pool.v_mins, F.pool.v_scales)):
+        dst[big - F.pages:] = src
+    table = np.where(F.table >= 0, F.table + big - F.pages, -1)
+    tab = fg.PageTable(_i32(table), _i32(F.lens), torch.ones(big, dtype=torch.int32, device="cuda"), ps)
+    small, F.pool, F.tab = (F.pool, F.tab), pool, tab
+    assert torch.equal(_run(fg, F), want)
+    n = np.array([100, 552, 0])
+    cu = _i32(np.concatenate(([0], np.cumsum(n))))
+    k, v, k2, v2 = (torch.empty((652, heads * d), dtype=torch.float16, device="cuda") for _ in range(4))
+    fg.fg_paged_read(small[0], small[1], cu, k, v)
+    fg.fg_paged_read(pool, tab, cu, k2, v2)
+    assert torch.equal(k, k2) and torch.equal(v, v2)
+    rotary = fg.Rotary(128, "pairs")
+    n = np.array([40, 300, 7])                               # rows behind the shared pages: one writer for each
+    cu = _i32(np.concatenate(([0], np.cumsum(n))))
+    k, v, k2, v2, *new = (torch.randn((347, heads * d), device="cuda").half() for _ in range(6))
+    fg.fg_paged_append_rotated(small[0], small[1], cu, rotary, None, 0, None, *new, k, v)
+    fg.fg_paged_append_rotated(pool, tab, cu, rotary, None, 0, None, *new, k2, v2)
+    fg.fg_sync_status()
+    assert torch.equal(k, k2) and torch.equal(v, v2) and torch.equal(pool.k_codes[big - F.pages:], small[0].k_codes)
