@@ -414,7 +414,6 @@ def test_one_row_listed_twice_and_groups_that_overlap_stay_in_bounds(fg):
     _hold(_run(fg, F, s), *ref)
     s = fg.PageShare(*[getattr(good, f).clone() for f in FIELDS])
     s.begin[1] = 0                                           # group 0 has no rows, group 1 everyone's
-    s.first[:3] += 0
     _hold(_run(fg, F, s)[3:], ref[0][3:], ref[1][3:])
     fg.fg_sync_status()
 
