@@ -17,7 +17,8 @@
 // registers an SM, 15 warps of which every second instruction waits for the one
 // before or for its load.  Eight slices a warp for many rows (four 155, two 168: a
 // run's angles are worked out again for each); blocks that stay, two an SM, 149;
-// three blocks an SM 190; four of four warps 155; half the queries' loads at once 149.
+// three blocks an SM 190; four of four warps 155; half the queries' loads at once 149;
+// the next head's loads under the one before 169 (spills), pieces found without divisions 140.
 #include "paged_codec.cuh"
 #include "rotary.cuh"
 
