@@ -434,6 +434,24 @@ def test_a_gap_between_groups_ends_them(fg):
     assert torch.equal(every, alone)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_many_groups_of_both_kinds(fg, d):
+    """40 groups, of few rows and of more than 128 in turn, and more sequences than a CTA plans for itself."""
+    which = np.concatenate((np.repeat(np.arange(40), 2), np.full(60, -1)))
+    few = np.concatenate((np.repeat(np.arange(40) % 3 > 0, 2), np.arange(60) % 2 > 0))
+    F = Forked(fg, (which, [3 + g % 7 for g in range(40)]), np.where(few, 9, 50), np.where(few, 1 + np.arange(140) % 3, 41 + np.arange(140) % 9),
+               2, 2, d, 16, 30)
+    ref = F.expect()
+    out = _run(fg, F)
+    assert torch.equal(out, _run(fg, F))
+    fg.fg_sync_status()
+    _hold(out, *ref)
+    alone = torch.empty_like(out)
+    fg.fg_paged_attention(F.pool, F.tab, _i32(F.cu), torch.as_tensor(F.q, device="cuda"), 4, alone, int(F.n.max()))
+    assert torch.equal(_run(fg, F, min_saved=-1), alone)
+    fg.fg_sync_status()
+
+
 @pytest.mark.parametrize("n, pages, shares", [(1, 20, False), (1, 90, True), (7, 10, False), (20, 24, True), (150, 24, False)])
 def test_sharing_where_it_saves(fg, n, pages, shares):
     """The library's own bound: 16 sequences over one prefix go by themselves, bit for bit, where that is cheaper."""
