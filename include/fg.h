@@ -491,9 +491,11 @@ fg_status fg_paged_read(const fg_page_pool* pool, const fg_page_table* t, const 
  * rounded one by one in fp32 (nothing is contracted), then once to the
  * activations' type.  Only the first `rot` dims of a head are rotated:
  *   FG_ROTARY_HALF:  pairs (i, i + rot/2);   FG_ROTARY_PAIRS: (2i, 2i + 1).
- * turns: device uint64 [rot/2], theta_i / 2 pi as a fraction of 2^64: a position
- * times it wraps exactly, so far positions lose nothing.  The rotation by -p is
- * the gradient of the one by p: negative positions are allowed in fg_rotate. */
+ * turns: device uint64 [rot/2], theta_i / 2 pi as a fraction of 2^64, to the
+ * nearest one: a position times it wraps exactly, so an angle is off by at most
+ * |p| 2^-65 turns, 2^-34 at the farthest (and those 36 bits are of that angle).
+ * The rotation by -p is the gradient of the one by p: negative positions are
+ * allowed in fg_rotate. */
 typedef enum { FG_ROTARY_HALF = 0, FG_ROTARY_PAIRS = 1 } fg_rotary_layout;
 typedef struct {
   const uint64_t* turns;
@@ -513,7 +515,9 @@ typedef struct {
  *           a share clamp((i - a)/max(z - a, 0.001), 0, 1) of theta_i / factor,
  *           the rest theta_i, and scale 0.1 ln(factor) + 1 (factor >= 1).
  * The other kinds have scale 1 and read only the numbers they name (BANDS and
- * RAMP: 0 < low < high).  rot even, 2 .. 65536; base > 1.  Host only. */
+ * RAMP: 0 < low < high).  rot even, 2 .. 65536; base > 1.  Numbers whose
+ * frequencies reach 2^32 turns, or whose stretched base is past the largest
+ * double, are FG_ERR_ARG.  Host only. */
 typedef enum {
   FG_ROTARY_PLAIN = 0, FG_ROTARY_LINEAR = 1, FG_ROTARY_BASE = 2, FG_ROTARY_BANDS = 3, FG_ROTARY_RAMP = 4
 } fg_rotary_scaling;

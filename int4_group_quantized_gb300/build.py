@@ -25,8 +25,8 @@ LIB = os.path.join(PKG, "libfg.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 COMMON = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-O2", "-I", INCLUDE,
           "-I", CSRC, "--expt-relaxed-constexpr"]
-# the codec must never contract a multiply and an add into one rounding
-PER_UNIT = {"codec.cu": ["-fmad=false"]}
+# the codec must never contract a multiply and an add into one rounding, the rotation's frequencies on the host neither
+PER_UNIT = {"codec.cu": ["-fmad=false"], "rotary.cu": ["-Xcompiler", "-ffp-contract=off"]}
 
 
 def nvcc() -> str:

@@ -224,11 +224,72 @@ fg_status check_apart(const void* x, int64_t ldx, const void* out, int64_t ldo, 
 
 using namespace fg;
 
+namespace {
+
+// Frequencies as sums of two doubles (Knuth's and Dekker's error-free sums and products): a position multiplies what the
+// last bits of a turn are off, so all 64 have to be right.  About 100 bits; built without contraction.
+struct Wide {
+  double hi, lo;
+};
+constexpr Wide kTau = {6.283185307179586232, 2.4492935982947064e-16}, kLn2 = {0.6931471805599453094, 2.3190468138462996e-17};
+constexpr double kMostTurns = 4294967296.0;   // of a position: 64 bits of the fraction are left
+
+Wide joined(double a, double b) {   // |a| >= |b|
+  const double s = a + b;
+  return {s, b - (s - a)};
+}
+Wide wide(double a, double b = 0.0) {   // a + b
+  const double s = a + b, t = s - a;
+  return {s, (a - (s - t)) + (b - t)};
+}
+Wide operator+(Wide a, Wide b) {
+  const Wide s = wide(a.hi, b.hi), t = wide(a.lo, b.lo), u = joined(s.hi, s.lo + t.hi);
+  return joined(u.hi, u.lo + t.lo);
+}
+Wide operator-(Wide a) { return {-a.hi, -a.lo}; }
+Wide operator*(Wide a, Wide b) {
+  const double p = a.hi * b.hi;
+  return joined(p, fma(a.hi, b.lo, fma(a.lo, b.hi, fma(a.hi, b.hi, -p))));
+}
+Wide operator/(Wide a, Wide b) {
+  const double q = a.hi / b.hi;
+  Wide r = a + -(b * wide(q));
+  const double q2 = r.hi / b.hi;
+  r = r + -(b * wide(q2));
+  return wide(q) + wide(q2, r.hi / b.hi);
+}
+// 2^k (1 + y)^256, y the series of a 256th of what is left of x
+Wide exp_wide(Wide x) {
+  const double k = rint(x.hi / kLn2.hi);
+  const Wide r = x + -(kLn2 * wide(k)), s = {ldexp(r.hi, -8), ldexp(r.lo, -8)};
+  Wide y = wide(0.0);
+  for (int n = 12; n > 0; --n) y = (wide(1.0) + y) * s / wide(n);
+  for (int i = 0; i < 8; ++i) y = y * (wide(2.0) + y);
+  y = wide(1.0) + y;
+  return {ldexp(y.hi, static_cast<int>(k)), ldexp(y.lo, static_cast<int>(k))};
+}
+Wide log_wide(double x) {
+  int k;
+  const Wide m = wide(frexp(x, &k));
+  Wide y = wide(log(m.hi));
+  for (int i = 0; i < 2; ++i) y = y + (m * exp_wide(-y) + wide(-1.0));   // Newton
+  return y + kLn2 * wide(k);
+}
+Wide share_of(Wide x) { return x.hi < 0.0 ? wide(0.0) : x.hi < 1.0 ? x : wide(1.0); }
+// The fraction of a turn, in units of 2^-64, rounded.
+uint64_t fraction(Wide t) {
+  const Wide f = t + wide(-floor(t.hi));   // in (-2^-52, 1]
+  const double h = ldexp(f.hi, 64), whole = floor(h);
+  const uint64_t top = whole < 0.0 || whole >= 18446744073709551616.0 ? 0 : static_cast<uint64_t>(whole);   // (2^64 is a whole turn)
+  return top + static_cast<uint64_t>(static_cast<int64_t>(rint((whole < 0.0 ? h : h - whole) + ldexp(f.lo, 64))));
+}
+
+}  // namespace
+
 extern "C" {
 
 fg_status fg_rotary_turns(int32_t rot, int32_t scaling, double base, double factor, double context, double low, double high,
                           uint64_t* turns, float* scale) {
-  constexpr double kTau = 6.28318530717958647692;
   if (!turns || !scale) return fail(FG_ERR_ARG, "null pointer");
   if (scaling < FG_ROTARY_PLAIN || scaling > FG_ROTARY_RAMP) return fail(FG_ERR_ARG, "scaling %d", scaling);
   if (rot < 2 || rot % 2 || rot > kMostRot) return fail(FG_ERR_SHAPE, "rotation of %d dims", rot);
@@ -239,23 +300,31 @@ fg_status fg_rotary_turns(int32_t rot, int32_t scaling, double base, double fact
   if (scaling == FG_ROTARY_BASE && rot < 4) return fail(FG_ERR_SHAPE, "a rotation of two dims has no other base");
   if (banded && !(context > 0.0 && context < INFINITY && low > 0.0 && low < high && high < INFINITY))
     return fail(FG_ERR_ARG, "context %g, low %g, high %g", context, low, high);
+  Wide ln_base = log_wide(base);
+  if (scaling == FG_ROTARY_BASE) {
+    ln_base = ln_base + log_wide(factor) * wide(rot) / wide(rot - 2);
+    if (!(ln_base.hi < 709.0)) return fail(FG_ERR_ARG, "base %g stretched by %g", base, factor);   // near the largest double
+  }
   double from = 0.0, to = 0.0;
-  if (scaling == FG_ROTARY_BASE) base *= pow(factor, static_cast<double>(rot) / (rot - 2));
   if (scaling == FG_ROTARY_RAMP) {
-    auto pair_of = [&](double t) { return rot * log(context / (kTau * t)) / (2.0 * log(base)); };
+    auto pair_of = [&](double t) { return rot * log(context / (kTau.hi * t)) / (2.0 * log(base)); };
     from = std::max(0.0, floor(pair_of(high)));
     to = std::min(rot - 1.0, ceil(pair_of(low)));
   }
-  for (int i = 0; i < rot / 2; ++i) {
-    double f = pow(base, -2.0 * i / rot);
-    double share = 1.0;   // of f, the rest of f / factor
-    if (scaling == FG_ROTARY_LINEAR) share = 0.0;
-    if (scaling == FG_ROTARY_BANDS) share = std::min(1.0, std::max(0.0, (context * f / kTau - low) / (high - low)));
-    if (scaling == FG_ROTARY_RAMP) share = 1.0 - std::min(1.0, std::max(0.0, (i - from) / std::max(to - from, 0.001)));
-    if (share < 1.0) f = share * f + (1.0 - share) * (f / factor);
-    const double t = f / kTau, part = rint(ldexp(t - floor(t), 64));
-    turns[i] = part >= 18446744073709551616.0 ? 0 : static_cast<uint64_t>(part);
-  }
+  for (int pass = 0; pass < 2; ++pass)   // looked at, then written
+    for (int i = 0; i < rot / 2; ++i) {
+      const Wide y = ln_base * wide(-2.0 * i) / wide(rot);
+      if (!(y.hi < 709.0)) return fail(FG_ERR_ARG, "frequency %d", i);
+      Wide f = exp_wide(y);
+      Wide share = wide(1.0);   // of f, the rest of f / factor
+      if (scaling == FG_ROTARY_LINEAR) share = wide(0.0);
+      if (scaling == FG_ROTARY_BANDS) share = share_of((wide(context) * f / kTau + wide(-low)) / wide(high, -low));
+      if (scaling == FG_ROTARY_RAMP) share = wide(1.0) + -share_of(wide(i, -from) / wide(std::max(to - from, 0.001)));
+      if (share.hi < 1.0) f = share * f + (wide(1.0) + -share) * (f / wide(factor));
+      const Wide t = f / kTau;
+      if (!(t.hi < kMostTurns)) return fail(FG_ERR_ARG, "frequency %d of %g", i, f.hi);
+      if (pass == 1) turns[i] = fraction(t);
+    }
   *scale = scaling == FG_ROTARY_RAMP ? static_cast<float>(0.1 * log(factor) + 1.0) : 1.0f;
   return FG_OK;
 }

@@ -1,8 +1,9 @@
 // Rotary positions, device side: cosine and sine of a position's angle to more
 // than fp32, and the rotation of a pair.
 //
-// An angle is a 64-bit fraction of a turn (position times turns, wrapping), so
-// it is exact however far the position.  Its top 8 bits, rounded, name one of
+// An angle is a 64-bit fraction of a turn (position times turns, wrapping): the
+// turns' own rounding, 2^-65 a step, is all that a far position adds up (2^-34
+// turns at 2^31).  Its top 8 bits, rounded, name one of
 // 256 angles whose cosine and sine stand in a table as sums of two fp32; the
 // rest, at most 1/512 turn (0.0123), goes through the addition theorem,
 //   cos(a + d) = C + C (cos d - 1) - S sin d,   sin(a + d) = S + S (cos d - 1) + C sin d,
