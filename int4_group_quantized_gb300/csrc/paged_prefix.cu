@@ -8,28 +8,32 @@
 //     the subnormal fp16 c * 2^-24, exact in the MMA) as the A operand in tensor
 //     memory; score = sum_g scale_g (C q)_g + min_g (sum q)_g, by the thread that
 //     owns the key, which holds its scales and minima: no rounding of K;
-//   O^T[dim][row] += V^T P^T, V restored to fp16 (its 128-byte-swizzled rows are
-//     the A operand, MN-major) and P as two fp16, value and remainder, side by
-//     side as 2 N columns, added when the sums leave: no rounding of P that counts.
-// What is left is V's rounding to fp16 and the result's.
+//   O^T[dim][row] += V^T P^T, V and P as two fp16 each, value and remainder. V's
+//     128-byte-swizzled rows are the A operand, MN-major; P's remainders lie beside
+//     the values as columns N .. 2 N - 1, added when the sums leave. V's remainders
+//     at 64 dims are the operand's rows 64 .. 127; at 128 they are operands of their
+//     own against P's values. The remainders' product is left out: it is 2^-22 of
+//     the whole, as what a remainder rounds away is.
+// What is left is the result's rounding (2.1e-4 of its size, as a step by itself; with
+// V rounded to fp16, as the chunks' kernel does, 2.7e-4 to 2.9e-4).
 //
 // One CTA an SM walks its share of the line of tiles (paged_prefix.cuh), 128 keys a
 // tile.  Warps 0..7: softmax, a key a thread, half of the rows each group of four
 // warps; 8..11: K's codes into tensor memory, a key a thread, a segment's Q, and in
 // turn a group of V's last 32 keys; 12..14: V's others; 15: the MMAs.  Two stages of
-// everything.  A row's maximum is known to all threads of its half: the segment's
+// everything but Q.  A row's maximum is known to all threads of its half: the segment's
 // first tile finds it, a later tile takes it as it is and looks only whether a weight
 // has left fp16 (a vote of the half); then the tile finds its maximum, the sums are
 // rescaled and the weights formed again.  The normaliser stays with the threads (a
 // key's share of every row's) until the segment ends.
 //
-// Not bound by the bytes (6 to 11% of the memory's rate) nor by the MMAs (16% of
-// the pipe's cycles) but by a tile's latencies: some 3,100 cycles, of which the 16
-// MMAs of d 128 take the issuing thread 1,800, its waits the rest, the weights of 64
-// rows 1,700 and the vote 300, restoring V as long; issue slots are 46% used.  64 rows
-// over 4,096 tokens, 32 heads of 128: 38 us; ten sequences' 80 rows a head each over
-// 12,928 to 31,104, 8 heads of 128: 114.  Measured and not kept, for the latter's
-// call, 161 us then: 17 warps at 96 registers 170, 16 softmax warps at 72 193, S two
+// Not bound by the bytes (5 to 10% of the memory's rate) nor by the MMAs but by a
+// tile's latencies: some 4,000 cycles, of which the 24 MMAs of d 128 take the issuing
+// thread most (some 110 each), its waits the rest; the weights of 64 rows take 1,700,
+// the vote 300, restoring V about as long as the products.  64 rows over 4,096 tokens,
+// 32 heads of 128: 40 us; ten sequences' 80 rows a head each over 12,928 to 31,104, 8
+// heads of 128: 133 (38 and 114 without V's remainders).  Measured and not kept without
+// these, for the latter's call, 161 us then: 17 warps at 96 registers 170, 16 softmax warps at 72 193, S two
 // tiles ahead 180, three copies of the restoring code 241 (instruction fetches).
 //
 // Every wait is bounded.  A half of the softmax warps decides everything by a
@@ -58,13 +62,16 @@ constexpr uint32_t kMostHalf = 0x7800u;   // 2^15 as fp16: weights up to it stan
 template <int D>
 struct Smem {
   static constexpr int kPanel = kKeys * 128;            // 128 rows of 128 bytes
-  static constexpr int kV = D / 64 * kPanel;
+  static constexpr int kV = (D == 128 ? 4 : 2) * kPanel;   // values, then remainders
+  static constexpr int kLow = D / 64 * kPanel;          // where the remainders begin
   static constexpr int kP = 2 * kPanel;                 // 2 N <= 128 columns
   static constexpr int kQPanel = kPrefixRows * 128;
   static constexpr int kQ = D / 64 * kQPanel;
   static constexpr int kSums = kPrefixRows * 8;         // (sum q of group 0, 1) of two rows side by side
   static constexpr int kMeta = kKeys * 16;              // K's scales and minima in units of the exponent
-  static constexpr int kBytes = 1024 + 2 * (kV + kP + kQ + kMeta) + 2 * kSums + 4 * kPrefixRows * 2 + 4 * kPrefixRows * 4 + 256;
+  static constexpr int kTurn = D == 128 ? 0 : kPrefixRows * 64 * 4;   // D = 64: a segment's sums of V's remainders, [row][64]
+  // one Q (a second would leave no room for V's remainders)
+  static constexpr int kBytes = 1024 + 2 * (kV + kP + kMeta) + kQ + kTurn + 2 * kSums + 4 * kPrefixRows * 2 + 4 * kPrefixRows * 4 + 256;
 };
 
 // A share's walk over its segments: parts of one unit's key tiles.
@@ -194,17 +201,34 @@ __device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_lo, uint32_t a_hi,
       "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(acc ? 1u : 0u)
       : "memory");
 }
-// 32 codes of a group through fp16(fmaf(q, scale, min)) into row r of a swizzled panel, from its 16-byte piece c0 on; every 8
-// dims in the order (0, 4), (1, 5), (2, 6), (3, 7).
-__device__ __forceinline__ void restore_half(const uint4& code, float scale, float mn, uint8_t* prow, int r, int c0) {
+// 32 codes of a group through fmaf(q, scale, min) into row r of two swizzled panels, `low` bytes apart, from the row's 16-byte
+// piece c0 on: the value cut to fp16's 11 bits, and what that leaves (below fp16's normal numbers, in steps of 2^-24).  Every 8
+// dims in the order (0, 4), (1, 5), (2, 6), (3, 7).  Two pieces a round, and a round for each half of a group, as instruction
+// fetches are what it costs (ten sequences each over 12,928 to 31,104 tokens, the call: 167 us; four pieces 172; rounding
+// and converting back in place of cutting 177 and 182, and 220 with no loop at all).
+__device__ __forceinline__ void restore_half(const uint4& code, float scale, float mn, uint8_t* prow, int low, int r, int c0) {
   const float2 lo2 = both(scale * 16777216.0f), hi2 = both(scale * 1048576.0f), m2 = both(mn);
-  const uint32_t words[4] = {code.x, code.y, code.z, code.w};
+  uint32_t w0 = code.x, w1 = code.y;
+#pragma unroll 1
+  for (int c = 0; c < 4; c += 2) {
 #pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    const uint32_t x = words[c], y = x >> 8;
-    const uint4 o = make_uint4(q4::cvt_f16x2(q4::fma_f32x2(halves(x & 0x000F000Fu), lo2, m2)), q4::cvt_f16x2(q4::fma_f32x2(halves(x & 0x00F000F0u), hi2, m2)),
-                               q4::cvt_f16x2(q4::fma_f32x2(halves(y & 0x000F000Fu), lo2, m2)), q4::cvt_f16x2(q4::fma_f32x2(halves(y & 0x00F000F0u), hi2, m2)));
-    *reinterpret_cast<uint4*>(prow + (((c0 + c) ^ (r & 7)) << 4)) = o;
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t x = i ? w1 : w0, y = x >> 8;
+      const float2 v[4] = {q4::fma_f32x2(halves(x & 0x000F000Fu), lo2, m2), q4::fma_f32x2(halves(x & 0x00F000F0u), hi2, m2),
+                           q4::fma_f32x2(halves(y & 0x000F000Fu), lo2, m2), q4::fma_f32x2(halves(y & 0x00F000F0u), hi2, m2)};
+      uint32_t hi[4], lo[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float2 cut = make_float2(__uint_as_float(__float_as_uint(v[e].x) & 0xffffe000u), __uint_as_float(__float_as_uint(v[e].y) & 0xffffe000u));
+        hi[e] = q4::cvt_f16x2(cut);
+        lo[e] = q4::cvt_f16x2(q4::fma_f32x2(cut, both(-1.0f), v[e]));
+      }
+      uint8_t* const to = prow + (((c0 + c + i) ^ (r & 7)) << 4);
+      *reinterpret_cast<uint4*>(to) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+      *reinterpret_cast<uint4*>(to + low) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    }
+    w0 = code.z;
+    w1 = code.w;
   }
 }
 template <int NG>
@@ -230,7 +254,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const PrefixArgs p,
   uint8_t* const sV = sm;
   uint8_t* const sP = sV + 2 * S::kV;
   uint8_t* const sQ = sP + 2 * S::kP;
-  float4* const sMeta = reinterpret_cast<float4*>(sQ + 2 * S::kQ);         // [stage][key] (scale, scale of group 1, minimum, minimum)
+  float* const sTurn = reinterpret_cast<float*>(sQ + S::kQ);
+  float4* const sMeta = reinterpret_cast<float4*>(sQ + S::kQ + S::kTurn);         // [stage][key] (scale, scale of group 1, minimum, minimum)
   float* const sSum = reinterpret_cast<float*>(sMeta + 2 * kKeys);         // [segment % 2][row / 2][group][row % 2]
   float* const sNeg = sSum + 2 * S::kSums / 4;                             // [row] minus the maximum
   float* const sShrink = sNeg + kPrefixRows;                               // [row] what a new maximum makes of sums
@@ -241,7 +266,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const PrefixArgs p,
   uint64_t* const vfull = bars + 6;    // [stage] V of the tile is in shared memory
   uint64_t* const pfull = bars + 8;    // [stage] P is, and S^T and the rows' sums have been read
   uint64_t* const pvdone = bars + 10;  // [stage] P V of the tile has completed
-  uint64_t* const qfull = bars + 12;   // [segment % 2] Q of the segment is in shared memory
+  uint64_t* const qfull = bars + 12;   // [segment % 2] Q of the segment is in shared memory, and its sums
   uint64_t* const drained = bars + 14; // O of the segment has been read
   uint64_t* const done = bars + 15;    // every MMA has completed
   uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(bars + 16);
@@ -365,10 +390,12 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const PrefixArgs p,
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         uint8_t* const to = sV + (n & 1) * S::kV + r * 128;
+#pragma unroll 1
+        for (int e = 0; e < 2 * NG; ++e) {
+          const int g = e >> 1;
+          restore_half(code[0], finite(g ? scale[NG - 1] : scale[0]), g ? mn[NG - 1] : mn[0], to + g * S::kPanel, S::kLow, r, 4 * (e & 1));
 #pragma unroll
-        for (int g = 0; g < NG; ++g) {
-          restore_half(code[2 * g], finite(scale[g]), mn[g], to + g * S::kPanel, r, 0);
-          restore_half(code[2 * g + 1], finite(scale[g]), mn[g], to + g * S::kPanel, r, 4);
+          for (int i = 0; i + 1 < 2 * NG; ++i) code[i] = code[i + 1];
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -377,13 +404,14 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const PrefixArgs p,
         look_up();
         continue;
       }
-      // P of the tile two before is there: S has read its codes, the softmax its scales.  (And Q and the sums of the segment
-      // two before, whose place a new one takes: its last tile is no later.)
+      // P of the tile two before is there: S has read its codes, the softmax its scales (and the sums of the segment two
+      // before, whose place a new segment's take: its last tile is no later).  A new segment's Q waits for S of the tile before.
       ok = n < 2 || mbar_wait(&pfull[n & 1], ((n >> 1) - 1) & 1, wait_limit, abort_flag);
+      if (ok && x == k.x && n > 0) ok = mbar_wait(&sfull[(n - 1) & 1], ((n - 1) >> 1) & 1, wait_limit, abort_flag);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       if (x == k.x) {
-        uint8_t* const q = sQ + (seg & 1) * S::kQ;
+        uint8_t* const q = sQ;
         float* const sum = sSum + (seg & 1) * (S::kSums / 4);
         constexpr int kPieces = D / 8;                    // 16 bytes each, a lane a piece
         const int pc = lane % kPieces, all = k.s.list * a.shape.group, r0 = k.u * k.at.rows;
@@ -437,7 +465,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const PrefixArgs p,
         uint8_t* const vto = sV + (n & 1) * S::kV + xg * S::kPanel + (96 + lane) * 128;
 #pragma unroll 1
         for (int e = 0; e < 2; ++e) {
-          restore_half(xcode[0], finite(xscale), xmn, vto, lane, 4 * e);   // (row 96 + lane: the same swizzle)
+          restore_half(xcode[0], finite(xscale), xmn, vto, S::kLow, lane, 4 * e);   // (row 96 + lane: the same swizzle)
           xcode[0] = xcode[1];
         }
         fence_proxy_async_smem();
@@ -456,7 +484,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const PrefixArgs p,
     // ---- MMA issuer --------------------------------------------------------------------
     if (lane == 0) {
       const uint32_t q_lo = static_cast<uint32_t>(smem_desc_sw128(smem_u32(sQ), 16, 1024));
-      const uint32_t v_lo = static_cast<uint32_t>(smem_desc_sw128(smem_u32(sV), D == 128 ? S::kPanel : 0, 1024));   // 64 dims: twice the same
+      const uint32_t v_lo = static_cast<uint32_t>(smem_desc_sw128(smem_u32(sV), S::kPanel, 1024));
       const uint32_t p_lo = static_cast<uint32_t>(smem_desc_sw128(smem_u32(sP), S::kPanel, 1024));
       int n = 0, seg = 0;
       bool ok = true, pending = false;
@@ -475,11 +503,14 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const PrefixArgs p,
         if (!p_in && !wait(&pfull[g & 1], g >> 1)) return;
         tc_fence_after();
         const uint32_t idesc = idesc_f16(128, 0, 1, 1) + (static_cast<uint32_t>(rows >> 2) << 17);   // 2 rows columns
+        const uint32_t idesc_low = idesc_f16(128, 0, 1, 1) + (static_cast<uint32_t>(rows >> 3) << 17);
 #pragma unroll
         for (int kk = 0; kk < kKeys / 16; ++kk) {
           if (kk == kKeys / 16 - 2) k_in = look(&kfull[g & 1], (g + 2) >> 1);   // of tile g + 2, late in the batch
-          mma_ss(tmem + kOut, v_lo + (g & 1) * (S::kV >> 4) + kk * (2048 >> 4), kDescHi, p_lo + (g & 1) * (S::kP >> 4) + kk * (2048 >> 4), kDescHi, idesc,
-                 !first || kk > 0);
+          const uint32_t weights = p_lo + (g & 1) * (S::kP >> 4) + kk * (2048 >> 4);
+          const uint32_t values = v_lo + (g & 1) * (S::kV >> 4) + kk * (2048 >> 4);
+          mma_ss(tmem + kOut, values, kDescHi, weights, kDescHi, idesc, !first || kk > 0);
+          if (D == 128) mma_ss(tmem + kOut, values + (S::kLow >> 4), kDescHi, weights, kDescHi, idesc_low, true);
         }
         mma_commit(&pvdone[g & 1]);
       };
@@ -498,7 +529,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const PrefixArgs p,
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
               mma_ts(tmem + kScore + 128 * (n & 1) + 64 * g, tmem + kCodes + 64 * (n & 1) + 32 * g + 8 * kk,
-                     q_lo + (((seg & 1) * S::kQ + g * S::kQPanel + 32 * kk) >> 4), kDescHi, idesc, kk > 0);
+                     q_lo + ((g * S::kQPanel + 32 * kk) >> 4), kDescHi, idesc, kk > 0);
           mbar_arrive(&sfull[n & 1]);
           mma_commit(&sfull[n & 1]);
           k_in = 0;
@@ -715,6 +746,19 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const PrefixArgs p,
             make_float2(-sNeg[first + lane], (c[0] + c[kPrefixRows]) + (c[2 * kPrefixRows] + c[3 * kPrefixRows]));
       }
       const uint32_t reals = __ballot_sync(0xffffffffu, real);
+      // D = 64: the sums of V's remainders, tensor memory's lanes 64 .. 127, to the threads of its values
+      float* const turn = sTurn + first * 64 + 32 * (quarter & 1) + lane;
+      if (D == 64 && quarter >= 2)
+#pragma unroll 1
+        for (int c = 0; c < chunks; ++c) {
+          uint32_t u[8], v[8];
+          tmem_ld8(tmem + kOut + lanes + first + 8 * c, u);
+          tmem_ld8(tmem + kOut + lanes + k.at.rows + first + 8 * c, v);
+          arrived(u, v);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) turn[(8 * c + e) * 64] = __uint_as_float(u[e]) + __uint_as_float(v[e]);
+        }
+      if (D == 64) bar_any(bar, false);
       if (D == 128 || quarter < 2) {
         float* const parts = (home ? a.prefix.home : a.prefix.extra) + 32 * quarter + (lane & 24) + ((lane & 1) << 2) + ((lane & 7) >> 1);   // the lane's dim
 #pragma unroll 1
@@ -726,7 +770,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const PrefixArgs p,
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             const int64_t to = __shfl_sync(0xffffffffu, place, 8 * c + e);
-            if ((reals >> (8 * c + e)) & 1u) parts[to * D] = __uint_as_float(u[e]) + __uint_as_float(v[e]);
+            const float low = D == 64 ? turn[(8 * c + e) * 64] : 0.0f;
+            if ((reals >> (8 * c + e)) & 1u) parts[to * D] = __uint_as_float(u[e]) + (__uint_as_float(v[e]) + low);
           }
         }
       }

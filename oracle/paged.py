@@ -213,6 +213,15 @@ def off_by_too_much(got, ref, tol, rms=None):
     return None
 
 
+def not_nearest(got, ref):
+    """The share of elements that are not the 64-bit result rounded to fp16: what arithmetic adds to that rounding shows
+    here and hardly in a bound (a result off by e steps before it is rounded is another fp16 in a share e of the cases).
+    Results of fp16's subnormals, and NaN, are left out."""
+    f = np.isfinite(ref) & (np.abs(ref) > 2.0 ** -13)
+    want = ref[f].astype(np.float16)
+    return float(np.mean(got[f].astype(np.float16) != want)) if f.any() else 0.0
+
+
 # ---- shared prefixes ---------------------------------------------------------------
 
 def share(table, lens, cu, pages, ps, min_tokens):
