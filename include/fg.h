@@ -592,7 +592,8 @@ fg_status fg_pages_share(const fg_page_table* t, const int32_t* cu, int64_t min_
  * their cost).
  * Sharing has launches of its own: where the groups save less than min_saved bytes
  * of cache reads (0: share all the same; negative: 64 MB) every sequence goes by
- * itself.  Counted are a sequence's reads of its group's tokens, once for up to 16
+ * itself.  Counted are the reads of its group's tokens of every sequence that would
+ * leave them to the group (see above: none that goes by itself anyway), once for up to 16
  * rows of a K/V head, four times for each 256 of more (they take as long), less
  * the group's own, once for each 64 of its rows (four times for each 256 in calls
  * of more than 16 where they are more than 128), and 8 tokens for the parts of

@@ -60,12 +60,12 @@ __device__ __forceinline__ int shared_tokens(const AttnArgs<__half>& a, int grou
   return rows[0] == q.row0 && rows[q.n - 1] == q.row0 + q.n - 1 ? s.tokens : 0;
 }
 
-// What sequence i reads of its group's tokens when it goes by itself.
-__device__ __forceinline__ int64_t read_alone(const PrefixArgs& p, int i) {
+// What sequence i reads of its group's tokens when it goes by itself; nothing where it does so in any case.
+__device__ __forceinline__ int64_t read_alone(const PrefixArgs& p, int groups, int i) {
   const AttnArgs<__half>& a = p.a;
-  const int g = a.prefix.group[i], tokens = a.prefix.tokens[i];
+  const int64_t tokens = shared_tokens(a, groups, i);
+  if (tokens == 0) return 0;
   const int64_t rows = (static_cast<int64_t>(a.batch.cu[i + 1]) - a.batch.cu[i]) * a.shape.group;
-  if (g < 0 || tokens <= 0 || rows <= 0) return 0;
   return tokens * (p.tile.workers == 0 || rows <= kStepRows ? 1 : kChunkRead * ((rows + kTileRows - 1) / kTileRows));
 }
 // What every CTA works out first, by all its threads: the whole line's length and share, what the launches after it read
@@ -82,8 +82,15 @@ __device__ __forceinline__ void prefix_line(const PrefixArgs& p, PrefixLine& lin
   const Table& t = a.tab;
   const int group = a.shape.group, heads = a.pool.heads, lane = threadIdx.x & 31;
   if (p.min_saved > 0) {
+    if (threadIdx.x < 32) {
+      int groups = 0;
+      bool last = false;
+      for (; !last && groups < t.seqs; groups += 32) last = __any_sync(0xffffffffu, groups + lane < t.seqs && a.prefix.leader[groups + lane] < 0);
+      if (lane == 0) line.groups = min(groups, t.seqs);
+    }
+    __syncthreads();
     int64_t sum = 0;
-    for (int i = threadIdx.x; i < t.seqs; i += blockDim.x) sum += read_alone(p, i);
+    for (int i = threadIdx.x; i < t.seqs; i += blockDim.x) sum += read_alone(p, line.groups, i);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     if (lane == 0 && sum > 0) atomicAdd(&line.alone, static_cast<unsigned long long>(sum));

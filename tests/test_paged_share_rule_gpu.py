@@ -1,0 +1,63 @@
+"""When a call shares: what is counted, where a share is older than the batch it is used for.  A call that does not share
+gives the bits of fg_paged_attention, one that does gives others."""
+import numpy as np
+import pytest
+import torch
+
+from test_paged_share_gpu import FIELDS, Forked, _hold, _i32, _run
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def fg():
+    import int4_group_quantized_gb300 as fg
+    return fg
+
+
+def _alone(fg, F):
+    out = torch.full(F.q.shape, 7.0, dtype=F.dtype, device="cuda")
+    fg.fg_paged_attention(F.pool, F.tab, _i32(F.cu), torch.as_tensor(F.q, device="cuda"), F.heads * F.r, out, int(F.n.max()))
+    return out
+
+
+def _decides(fg, F, share, saved):
+    """Shares up to `saved` bytes and no further."""
+    ref, alone, both = F.expect(), _alone(fg, F), _run(fg, F, share)
+    assert not torch.equal(alone, both)
+    for least, want in ((1, both), (saved, both), (saved + 1, alone), (2 * saved, alone)):
+        got = _run(fg, F, share, min_saved=least)
+        assert torch.equal(got, want), least
+        _hold(got, *ref)
+    fg.fg_sync_status()
+
+
+def test_sequences_cut_back_save_nothing(fg):
+    """Three of six sequences now end inside the prefix: their rows go by themselves, and what they read is not saved."""
+    F = Forked(fg, ([0] * 6, [30]), [40, 20, 50, 33, 25, 60], [1] * 6, 2, 2, 128, 16, 51)
+    share = F.find(fg)
+    assert share.tokens.tolist() == [480] * 6
+    F.lens[[1, 3, 4]] = [480, 400, 5]
+    F.upload(fg)
+    # three read 480 tokens each, the group them once, and six rows of two query heads leave their parts
+    _decides(fg, F, share, 2 * 128 * 5 // 4 * (480 * (3 - 1) - 8 * 2 * 6))
+
+
+def test_groups_behind_a_gap_save_nothing(fg):
+    """Groups are looked at 32 at a time up to the first gap: what others would save is not counted."""
+    n = 40
+    F = Forked(fg, (np.repeat(np.arange(n), 2), [8] * n), [3] * (2 * n), [1] * (2 * n), 1, 2, 64, 16, 52)
+    good = F.find(fg)
+    share = fg.PageShare(*[getattr(good, f).clone() for f in FIELDS])
+    share.leader[3] = -1
+    groups = 31                                              # 0 .. 31 but the gap
+    _decides(fg, F, share, 64 * 5 // 4 * (groups * (2 - 1) * 128 - 8 * 2 * 2 * groups))
+
+
+def test_rows_that_the_share_lists_elsewhere_save_nothing(fg):
+    """Sequences whose place in the list names other rows go by themselves."""
+    F = Forked(fg, ([0] * 8, [25]), [9] * 8, [1] * 8, 2, 1, 64, 16, 53)
+    good = F.find(fg)
+    share = fg.PageShare(*[getattr(good, f).clone() for f in FIELDS])
+    share.rows[5:8] = share.rows[0]
+    _decides(fg, F, share, 2 * 64 * 5 // 4 * (400 * (5 - 1) - 8 * 8))
