@@ -592,12 +592,16 @@ fg_status fg_pages_share(const fg_page_table* t, const int32_t* cu, int64_t min_
  * their cost).
  * Sharing has launches of its own: where the groups save less than min_saved bytes
  * of cache reads (0: share all the same; negative: 64 MB) every sequence goes by
- * itself.  Counted are the reads of its group's tokens of every sequence that would
+ * itself; in calls of more than 16 rows of a K/V head that is decided for chunks (of
+ * groups that have more than 128 rows of them) and for all others apart.  Counted
+ * are the reads of its group's tokens of every sequence that would
  * leave them to the group (see above: none that goes by itself anyway), once for up to 16
  * rows of a K/V head, four times for each 256 of more (they take as long), less
- * the group's own, once for each 64 of its rows (four times for each 256 in calls
- * of more than 16 where they are more than 128), and 8 tokens for the parts of
- * each of its rows.  (A row here: a row of the batch and a query head.)
+ * the group's own, once for each 64 of its rows (four times for each 256 of such
+ * chunks), and 8 tokens for the parts of each of its rows.  (A row here: a row of
+ * the batch and a query head; a chunk: a sequence of more than 16 of a K/V head.)
+ * Nothing is rounded to fewer bits than fg_paged_attention rounds the same row to:
+ * steps are not rounded to fp16 before the result is, chunks as they are there.
  * ws: 256-byte aligned, >= fg_paged_attention_shared_workspace_bytes. */
 size_t fg_paged_attention_shared_workspace_bytes(const fg_page_pool* pool, const fg_page_table* t, int32_t q_heads,
                                                  int64_t ntok, int64_t max_q);

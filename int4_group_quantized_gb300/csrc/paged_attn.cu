@@ -309,7 +309,7 @@ inline size_t up(size_t x) { return (x + 255) / 256 * 256; }
 struct Layout {
   ClassPlan step, tile;
   Prefix prefix;     // of a call beside shared prefixes
-  ClassPlan tall;    // its groups of many rows
+  ClassPlan tall;    // its groups of many rows of chunks
   int32_t* skip;
   size_t bytes;
 };
@@ -353,7 +353,7 @@ Layout layout_of(const fg_page_pool& pool, const fg_page_table& t, int32_t q_hea
       p += up(bytes);
     };
     take(l.skip, 4 * static_cast<size_t>(t.seqs));
-    take(l.prefix.info, sizeof(PrefixGroup) * static_cast<size_t>(t.seqs));
+    take(l.prefix.info, sizeof(PrefixGroup) * static_cast<size_t>(t.seqs) * (l.tile.workers ? 2 : 1));
     take(l.prefix.home_row, 4 * static_cast<size_t>(t.seqs));
     take(l.prefix.planned, 4);
     const size_t extra = static_cast<size_t>(kMaxSms) * (kPrefixRows + (l.tile.workers ? kTileRows : 0));
@@ -362,6 +362,8 @@ Layout layout_of(const fg_page_pool& pool, const fg_page_table& t, int32_t q_hea
       l.tall.rows = kTileRows;
       take(l.tall.head, 256);
       take(l.tall.pre, 8 * static_cast<size_t>(t.seqs + 1));
+      take(l.prefix.steps, 4 * static_cast<size_t>(t.seqs));
+      take(l.prefix.order, 4 * static_cast<size_t>(shared_rows));
     }
     take(l.prefix.home_stat, 8 * pairs);
     take(l.prefix.extra_stat, 8 * extra);
@@ -375,7 +377,7 @@ Layout layout_of(const fg_page_pool& pool, const fg_page_table& t, int32_t q_hea
 template <typename T>
 fg_status launch_attn(const fg_page_pool& pool, const fg_page_table& t, const int32_t* cu, const void* q, int64_t ldq,
                       int32_t q_heads, int64_t ntok, int64_t max_q, int64_t window, int64_t sinks, void* out,
-                      int64_t ldo, void* ws, unsigned int* err, cudaStream_t st, const fg_page_share* share = nullptr, int64_t min_saved = 0) {
+                      int64_t ldo, void* ws, unsigned int* err, cudaStream_t st, const fg_page_share* share = nullptr, int64_t min_saved = 0) {   // tokens' reads
   AttnArgs<T> a;
   a.pool = pool_of(pool);
   a.tab = table_of(t);
@@ -404,7 +406,8 @@ fg_status launch_attn(const fg_page_pool& pool, const fg_page_table& t, const in
       a.prefix.leader = share->leader;
       a.prefix.begin = share->begin;
       a.prefix.rows = share->rows;
-      const PrefixArgs p{a, l.skip, l.tall, std::min(num_sms(), kMaxSms), min_saved};
+      const PrefixArgs p{a, l.skip, l.tall, std::min(num_sms(), kMaxSms), {min_saved, min_saved}};
+      if (l.tall.workers > 0) FG_TRY(paged_prefix_order(p, st));
       FG_TRY(paged_prefix(p, pool.head_dim, st));
       if (l.tall.workers > 0) FG_TRY(paged_prefix_tile(a, l.tall, pool.head_dim, st));
       FG_TRY(paged_prefix_join(p, pool.head_dim, st));

@@ -17,7 +17,9 @@ struct PrefixGroup {
 };
 struct Prefix {
   const int32_t *group, *tokens, *first, *leader, *begin, *rows;   // fg_page_share
-  PrefixGroup* info;              // [*planned], groups that are none with no units among them
+  int32_t* steps;                 // [seqs] calls with chunks: of a group whose chunks are the chunks' kernel's the rows of its steps, else -1
+  int32_t* order;                 // [ntok] and of such a group's places in the list its steps' first, then its chunks'
+  PrefixGroup* info;              // [*planned], groups that are none with no units among them; [seqs + *planned] of their chunks
   int32_t* planned;
   int32_t* home_row;              // [seqs] the home of a sequence's first row
   float* home;                    // [ntok][q_heads][D], rows in the share's order
@@ -46,6 +48,26 @@ __device__ __forceinline__ SharedGroup shared_group(const Prefix& p, const Table
   s.list = ok ? end - s.first : 0;
   return s;
 }
+// The rows of group g that go to the chunks' kernel (tall), or to the other, as a part of the list, by `order` where the group
+// is split: a step is not to be rounded as chunks are because a chunk shares its prefix.
+struct ClassRows : SharedGroup {
+  bool split;
+};
+__device__ __forceinline__ ClassRows class_rows(const Prefix& p, const Table& t, const Batch& b, int g, bool tall) {
+  ClassRows s{shared_group(p, t, b, g), false};
+  const int steps = p.steps != nullptr && s.list > 0 ? p.steps[g] : -1;
+  s.split = steps >= 0;
+  if (!s.split) {
+    if (tall) s.list = 0;
+  } else if (tall) {
+    s.first += steps;
+    s.list -= steps;
+  } else {
+    s.list = steps;
+  }
+  return s;
+}
+__device__ __forceinline__ int place_of(const Prefix& p, const ClassRows& s, int x) { return s.split ? p.order[x] : x; }
 // Row x of the share's list as a row of the batch (row 0 in place of what is none: nobody reads its parts).
 __device__ __forceinline__ int listed_row(const Prefix& p, const Batch& b, int x) {
   const int r = p.rows[x];

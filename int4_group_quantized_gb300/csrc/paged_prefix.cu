@@ -41,6 +41,8 @@
 // that gave up.
 #include <math.h>
 
+#include <algorithm>
+
 #include "paged_prefix.cuh"
 #include "q4_dev.cuh"
 #include "tc_ptx.cuh"
@@ -78,7 +80,7 @@ struct Smem {
 struct Walk {
   int64_t left;
   int g, h, u, x, x1;
-  SharedGroup s;
+  ClassRows s;
   PrefixGroup at;
 };
 __device__ __forceinline__ void walk_begin(Walk& k, const PrefixArgs& p, const PrefixLine& line) {
@@ -88,7 +90,7 @@ __device__ __forceinline__ void walk_begin(Walk& k, const PrefixArgs& p, const P
   k.left = line.per < line.total - o0 ? line.per : line.total - o0;
   k.g = line.g;
   k.at = line.at;
-  k.s = shared_group(p.a.prefix, p.a.tab, p.a.batch, k.g);
+  k.s = class_rows(p.a.prefix, p.a.tab, p.a.batch, k.g, false);
   const int64_t in = o0 - k.at.base, unit = in / k.at.tiles;
   k.h = static_cast<int>(unit / k.at.units);
   k.u = static_cast<int>(unit - static_cast<int64_t>(k.h) * k.at.units);
@@ -102,8 +104,8 @@ __device__ __forceinline__ void walk_next(Walk& k, const PrefixArgs& p) {
     k.u = 0;
     if (++k.h == p.a.pool.heads) {
       k.h = 0;
-      do k.s = shared_group(p.a.prefix, p.a.tab, p.a.batch, ++k.g);
-      while (k.s.list == 0 || (p.tile.workers > 0 && static_cast<int64_t>(k.s.list) * p.a.shape.group > kPrefixFew));
+      do k.s = class_rows(p.a.prefix, p.a.tab, p.a.batch, ++k.g, false);
+      while (k.s.list == 0);
       k.at = prefix_group(k.s, p.a.shape.group, false);
     }
   }
@@ -288,7 +290,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const PrefixArgs p,
     mbar_init(drained, kSoftWarps);
     mbar_init(done, 1);
     *abort_flag = 0;
-    line.alone = 0;
+    line.alone[0] = line.alone[1] = 0;
     mbar_fence_init();
   }
   if (warp == kMmaWarp) tmem_alloc(tmem_slot, kTmemCols);
@@ -418,7 +420,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const PrefixArgs p,
         for (int m = quarter * (32 / kPieces) + lane / kPieces; m < k.at.rows; m += kKeyWarps * (32 / kPieces)) {
           const int row = r0 + m, lx = row / a.shape.group;
           const bool on = row < all;
-          const __half* from = a.q + static_cast<int64_t>(on ? listed_row(a.prefix, a.batch, k.s.first + lx) : 0) * a.ldq +
+          const __half* from = a.q + static_cast<int64_t>(on ? listed_row(a.prefix, a.batch, place_of(a.prefix, k.s, k.s.first + lx)) : 0) * a.ldq +
                                static_cast<int64_t>(k.h * a.shape.group + (on ? row - lx * a.shape.group : 0)) * D + 8 * pc;
           const uint4 u = on ? *reinterpret_cast<const uint4*>(from) : make_uint4(0u, 0u, 0u, 0u);
           // every 8 dims in the codes' order
@@ -738,7 +740,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const PrefixArgs p,
       const int row = k.u * k.at.rows + first + lane;
       const bool real = lane < rows && row < k.s.list * a.shape.group, home = k.x == 0;
       const int lx = real ? row / a.shape.group : 0;
-      const int64_t place = home ? static_cast<int64_t>(k.s.first + lx) * a.q_heads + k.h * a.shape.group + (real ? row - lx * a.shape.group : 0)
+      const int64_t place = home ? static_cast<int64_t>(place_of(a.prefix, k.s, k.s.first + lx)) * a.q_heads + k.h * a.shape.group + (real ? row - lx * a.shape.group : 0)
                                  : static_cast<int64_t>(blockIdx.x) * kPrefixRows + first + lane;
       if (quarter == 0 && real) {
         const float* const c = sNorm + first + lane;
@@ -812,27 +814,29 @@ __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const PrefixA
   const int planned = *a.prefix.planned;
   // the class's last group that begins before the worker's share does, found by every warp
   const bool tall = blockIdx.z > 0;
+  const PrefixGroup* const info = a.prefix.info + (tall ? a.tab.seqs : 0);
   int g = -1;
   for (int g0 = 0; g0 < planned; g0 += 32) {
     bool before = false;
     if (g0 + lane < planned) {
-      const PrefixGroup& x = a.prefix.info[g0 + lane];
-      before = x.units > 0 && (x.extra > 0) == tall && x.base < worker * x.per;
+      const PrefixGroup& x = info[g0 + lane];
+      before = x.units > 0 && x.base < worker * x.per;
     }
     const uint32_t found = __ballot_sync(0xffffffffu, before);
     if (found) g = g0 + 31 - __clz(found);
   }
   if (g < 0) return;
-  const PrefixGroup at = a.prefix.info[g];
+  const PrefixGroup at = info[g];
   const int64_t in = worker * at.per - at.base, unit = (in - 1) / at.tiles, start = at.base + unit * at.tiles;   // of the tile before the share
   const int h = static_cast<int>(unit / at.units), u = static_cast<int>(unit - static_cast<int64_t>(h) * at.units);
   if (h >= a.pool.heads || start / at.per + 1 != worker) return;   // past the group, or not the first
   const int count = static_cast<int>((start + at.tiles - 1) / at.per) - (worker - 1);
   if (count == 0) return;            // the share begins with the next unit
-  const int rows = min(at.rows, shared_group(a.prefix, a.tab, a.batch, g).list * group - u * at.rows);
+  const ClassRows list = class_rows(a.prefix, a.tab, a.batch, g, tall);
+  const int rows = min(at.rows, list.list * group - u * at.rows);
   for (int rr = blockIdx.y * kAtOnce + threadIdx.x / kCols; rr < rows; rr += kSplit * kAtOnce) {
     const int r = u * at.rows + rr, x = r / group;
-    const int64_t i = static_cast<int64_t>(at.first_row + x) * a.q_heads + h * group + r - x * group;
+    const int64_t i = static_cast<int64_t>(place_of(a.prefix, list, at.first_row + x)) * a.q_heads + h * group + r - x * group;
     float* const home = a.prefix.home + i * D + 4 * col;
     const int64_t extra = at.extra + static_cast<int64_t>(worker) * at.stride + rr;
     float2 s = a.prefix.home_stat[i];
@@ -869,6 +873,52 @@ __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const PrefixA
   }
 }
 
+// ---- steps and chunks of a group ---------------------------------------------------------------------
+// A block a group: the rows of its chunks are counted, and where they are many the list's places put in order, steps first
+// (a row's kind is its sequence's, found from the offsets), in two passes over the list.
+constexpr int kOrderThreads = 512;
+__global__ void __launch_bounds__(kOrderThreads) prefix_order_kernel(const PrefixArgs p) {
+  __shared__ int counts[2][kOrderThreads / 32];
+  griddep_launch();
+  griddep_wait();
+  const AttnArgs<__half>& a = p.a;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  for (int g = blockIdx.x; g < a.tab.seqs; g += gridDim.x) {
+    const SharedGroup s = shared_group(a.prefix, a.tab, a.batch, g);
+    auto chunk = [&](int x) {   // place x of the group
+      const int r = a.prefix.rows[s.first + x], i = seq_of_row(a.batch.cu, a.tab.seqs, r);
+      return i < a.tab.seqs && (static_cast<int64_t>(a.batch.cu[i + 1]) - a.batch.cu[i]) * a.shape.group > kStepRows;
+    };
+    int chunks = 0;
+    for (int x0 = 0; x0 < s.list; x0 += kOrderThreads) {
+      const int x = x0 + threadIdx.x;
+      chunks += __syncthreads_count(x < s.list && chunk(x));
+    }
+    const bool split = static_cast<int64_t>(chunks) * a.shape.group > kPrefixFew;
+    const int steps = s.list - chunks;
+    if (threadIdx.x == 0) a.prefix.steps[g] = split ? steps : -1;
+    if (s.leader < 0) break;   // past the last group
+    if (!split) continue;
+    int before = 0;            // chunks' rows
+    for (int x0 = 0, turn = 0; x0 < s.list; x0 += kOrderThreads, turn ^= 1) {
+      const int x = x0 + threadIdx.x;
+      const bool is = x < s.list && chunk(x);
+      const uint32_t mates = __ballot_sync(0xffffffffu, is);
+      if (lane == 0) counts[turn][warp] = __popc(mates);
+      __syncthreads();         // (the other turn's counts have been read by all when they are written again)
+      int at = before + __popc(mates & ((1u << lane) - 1));
+#pragma unroll
+      for (int w = 0; w < kOrderThreads / 32; ++w) {
+        const int c = counts[turn][w];
+        if (w < warp) at += c;
+        before += c;
+      }
+      if (x < s.list) a.prefix.order[s.first + (is ? steps + at : x - at)] = s.first + x;
+    }
+    __syncthreads();
+  }
+}
+
 template <int D>
 fg_status launch(const PrefixArgs& p, cudaStream_t st) {
   using S = Smem<D>;
@@ -885,6 +935,13 @@ fg_status launch(const PrefixArgs& p, cudaStream_t st) {
 }
 
 }  // namespace
+
+fg_status paged_prefix_order(const PrefixArgs& p, cudaStream_t st) {
+  Trace tr(KC_ATTN_PAGED_PLAN, st);
+  // (no fewer blocks than the groups that are looked at together, so that all of those before the first gap are counted)
+  const int grid = std::min(p.a.tab.seqs, std::max(32, 2 * p.workers));
+  return paged::launch("prefix_order_kernel", true, prefix_order_kernel, static_cast<unsigned>(grid), kOrderThreads, 0, st, p);
+}
 
 fg_status paged_prefix_join(const PrefixArgs& p, int head_dim, cudaStream_t st) {
   Trace tr(KC_ATTN_COMBINE, st);

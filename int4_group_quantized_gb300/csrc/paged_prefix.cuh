@@ -7,9 +7,9 @@
 // it.  The first part of a unit goes to the rows' home, that of a worker that goes
 // on with a unit to the worker's own place: a worker begins inside at most one.
 //
-// Two classes: groups of many rows in calls that allow chunks go to the chunks'
-// kernel (units of kTileRows rows), all others to this file's (units of at most
-// kPrefixRows).
+// Two classes: in calls that allow chunks, the chunks of groups that have many
+// rows of them go to the chunks' kernel (units of kTileRows rows), all other rows
+// to this file's (units of at most kPrefixRows).
 #pragma once
 
 #include "paged_attn.cuh"
@@ -22,11 +22,11 @@ struct PrefixArgs {
   int32_t* skip;          // [seqs] out: the tokens of a sequence that its group attends to
   ClassPlan tile;         // head and pre by group, out; no workers: one class
   int workers;
-  int64_t min_saved;      // tokens' reads that groups have to save; 0: groups whatever they save
+  int64_t min_saved[2];   // tokens' reads that a class's groups have to save; 0: groups whatever they save
 };
 
 constexpr int kPrefixKeysLog2 = 7;
-// Rows of a group up to which it is not the chunks' kernel's.
+// Rows of a group's chunks up to which they are not the chunks' kernel's.
 constexpr int kPrefixFew = 128;
 // What a read of a tile costs a unit of the chunks' kernel, in reads of a step's (some 14.5 ns over all SMs against 3 to 6), and
 // what a row's parts, written and read again, cost its query heads, in tokens of their K/V head (6400 rows of 32 heads some 70 us
@@ -47,8 +47,9 @@ __device__ __forceinline__ PrefixGroup prefix_group(const SharedGroup& s, int gr
   return g;
 }
 // The tokens that sequence i leaves to its group: those of its group if all of its rows stand behind them and are the
-// group's, as the share lists them, and the group is one of the line's (the first `groups`).
-__device__ __forceinline__ int shared_tokens(const AttnArgs<__half>& a, int groups, int i) {
+// group's, as the share lists them, and the group is one of the line's (the first `groups`).  tall: its rows' class.
+__device__ __forceinline__ int shared_tokens(const AttnArgs<__half>& a, int groups, int i, int& tall) {
+  tall = 0;
   const Prefix& p = a.prefix;
   const int g = p.group[i];
   if (g < 0 || g >= groups) return 0;
@@ -56,14 +57,15 @@ __device__ __forceinline__ int shared_tokens(const AttnArgs<__half>& a, int grou
   const Seq q = seq_of(a.tab, a.batch, i);
   const int x = p.first[i];
   if (s.list == 0 || q.n == 0 || p.tokens[i] != s.tokens || q.len - q.n < s.tokens || x < 0 || x > s.list - q.n) return 0;
+  tall = p.steps != nullptr && p.steps[g] >= 0 && static_cast<int64_t>(q.n) * a.shape.group > kStepRows ? 1 : 0;
   const int32_t* rows = p.rows + s.first + x;
   return rows[0] == q.row0 && rows[q.n - 1] == q.row0 + q.n - 1 ? s.tokens : 0;
 }
 
 // What sequence i reads of its group's tokens when it goes by itself; nothing where it does so in any case.
-__device__ __forceinline__ int64_t read_alone(const PrefixArgs& p, int groups, int i) {
+__device__ __forceinline__ int64_t read_alone(const PrefixArgs& p, int groups, int i, int& tall) {
   const AttnArgs<__half>& a = p.a;
-  const int64_t tokens = shared_tokens(a, groups, i);
+  const int64_t tokens = shared_tokens(a, groups, i, tall);
   if (tokens == 0) return 0;
   const int64_t rows = (static_cast<int64_t>(a.batch.cu[i + 1]) - a.batch.cu[i]) * a.shape.group;
   return tokens * (p.tile.workers == 0 || rows <= kStepRows ? 1 : kChunkRead * ((rows + kTileRows - 1) / kTileRows));
@@ -72,8 +74,9 @@ __device__ __forceinline__ int64_t read_alone(const PrefixArgs& p, int groups, i
 // (written by the CTAs together), and where its own share begins.
 struct PrefixLine {
   int64_t total, per;
-  unsigned long long alone;   // reads of the groups' sequences by themselves; 0 before
-  int groups;            // that are looked at, 0 where they do not save enough
+  unsigned long long alone[2];   // reads of the groups' sequences by themselves, by class; 0 before
+  bool worth[2];         // whether a class's groups save enough
+  int groups;            // that are looked at
   int g;                 // the group that the share begins in
   PrefixGroup at;
 };
@@ -81,7 +84,7 @@ __device__ __forceinline__ void prefix_line(const PrefixArgs& p, PrefixLine& lin
   const AttnArgs<__half>& a = p.a;
   const Table& t = a.tab;
   const int group = a.shape.group, heads = a.pool.heads, lane = threadIdx.x & 31;
-  if (p.min_saved > 0) {
+  if (p.min_saved[0] > 0 || p.min_saved[1] > 0) {
     if (threadIdx.x < 32) {
       int groups = 0;
       bool last = false;
@@ -89,30 +92,44 @@ __device__ __forceinline__ void prefix_line(const PrefixArgs& p, PrefixLine& lin
       if (lane == 0) line.groups = min(groups, t.seqs);
     }
     __syncthreads();
-    int64_t sum = 0;
-    for (int i = threadIdx.x; i < t.seqs; i += blockDim.x) sum += read_alone(p, line.groups, i);
+    int64_t sum[2] = {0, 0};
+    for (int i = threadIdx.x; i < t.seqs; i += blockDim.x) {
+      int tall;
+      const int64_t reads = read_alone(p, line.groups, i, tall);
+      sum[0] += tall ? 0 : reads;
+      sum[1] += tall ? reads : 0;
+    }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (lane == 0 && sum > 0) atomicAdd(&line.alone, static_cast<unsigned long long>(sum));
+    for (int c = 0; c < 2; ++c) {
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) sum[c] += __shfl_xor_sync(0xffffffffu, sum[c], o);
+      if (lane == 0 && sum[c] > 0) atomicAdd(&line.alone[c], static_cast<unsigned long long>(sum[c]));
+    }
     __syncthreads();
   }
   if (threadIdx.x < 32) {
-    bool worth = true;
+    bool worth[2] = {true, true};
     int64_t per[2] = {1, 1};
     for (int pass = 0; pass < 2; ++pass) {
-      int64_t spent = 0;                      // reads of the groups, and their parts
+      int64_t spent[2] = {0, 0};              // reads of the groups, and their parts
       int64_t at[2] = {0, 0};                 // of the two classes' lines
       const int64_t o0 = blockIdx.x * per[0];
       for (int g0 = 0; g0 < t.seqs; g0 += 32) {
         const int g = g0 + lane;
-        SharedGroup s{-1, 0, 0, 0};
-        if (g < t.seqs) s = shared_group(a.prefix, t, a.batch, g);
-        if (!worth) s.list = 0;
-        const bool tall = p.tile.workers > 0 && static_cast<int64_t>(s.list) * group > kPrefixFew;
-        PrefixGroup x = prefix_group(s, group, tall);
-        spent += static_cast<int64_t>(s.tokens) * x.units * (tall ? kChunkRead : 1) + static_cast<int64_t>(s.list) * group * kRowParts;
-        const int64_t n = s.list > 0 ? static_cast<int64_t>(heads) * x.units * x.tiles : 0;
-        int64_t inc[2] = {tall ? 0 : n, tall ? n : 0};
+        ClassRows s[2] = {{{-1, 0, 0, 0}, false}, {{-1, 0, 0, 0}, false}};
+        if (g < t.seqs) {
+          s[0] = class_rows(a.prefix, t, a.batch, g, false);
+          if (p.tile.workers > 0) s[1] = class_rows(a.prefix, t, a.batch, g, true);
+        }
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+          if (!worth[c]) s[c].list = 0;
+        PrefixGroup x[2] = {prefix_group(s[0], group, false), prefix_group(s[1], group, true)};
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+          spent[c] += static_cast<int64_t>(s[c].tokens) * x[c].units * (c ? kChunkRead : 1) + static_cast<int64_t>(s[c].list) * group * kRowParts;
+        const int64_t n[2] = {static_cast<int64_t>(heads) * x[0].units * x[0].tiles, static_cast<int64_t>(heads) * x[1].units * x[1].tiles};
+        int64_t inc[2] = {n[0], n[1]};
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1)
 #pragma unroll
@@ -121,39 +138,50 @@ __device__ __forceinline__ void prefix_line(const PrefixArgs& p, PrefixLine& lin
             if (lane >= o) inc[c] += up;
           }
         if (pass == 1) {
-          x.base = tall ? at[1] + inc[1] - n : at[0] + inc[0] - n;
-          x.per = tall ? per[1] : per[0];
-          x.extra = tall ? p.workers * kPrefixRows : 0;
-          if (blockIdx.x == 0 && g < t.seqs) {
-            a.prefix.info[g] = x;
-            if (p.tile.workers > 0) p.tile.pre[g] = at[1] + inc[1] - (tall ? n : 0);
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            x[c].base = at[c] + inc[c] - n[c];
+            x[c].per = per[c];
+            x[c].extra = c ? p.workers * kPrefixRows : 0;
           }
-          if (!tall && n > 0 && o0 >= x.base && o0 < x.base + n) {
+          if (blockIdx.x == 0 && g < t.seqs) {
+            a.prefix.info[g] = x[0];
+            if (p.tile.workers > 0) {
+              a.prefix.info[t.seqs + g] = x[1];
+              p.tile.pre[g] = x[1].base;
+            }
+          }
+          if (n[0] > 0 && o0 >= x[0].base && o0 < x[0].base + n[0]) {
             line.g = g;
-            line.at = x;
+            line.at = x[0];
           }
         }
 #pragma unroll
         for (int c = 0; c < 2; ++c) at[c] += __shfl_sync(0xffffffffu, inc[c], 31);
-        const bool last = __any_sync(0xffffffffu, s.leader < 0) || g0 + 32 >= t.seqs;   // past the last group
+        const bool last = __any_sync(0xffffffffu, s[0].leader < 0) || g0 + 32 >= t.seqs;   // past the last group
         if (!last) continue;
         const int groups = min(g0 + 32, t.seqs);
-        if (pass == 1 && lane == 0) line.groups = worth ? groups : 0;
-        if (pass == 1 && blockIdx.x == 0 && lane == 0) *a.prefix.planned = worth ? groups : 0;
+        if (pass == 1 && lane == 0) line.groups = groups;
+        if (pass == 1 && blockIdx.x == 0 && lane == 0) *a.prefix.planned = worth[0] || worth[1] ? groups : 0;
         if (pass == 1 && blockIdx.x == 0 && p.tile.workers > 0)
           for (int i = groups + lane; i <= t.seqs; i += 32) p.tile.pre[i] = at[1];
         break;
       }
       if (pass == 0) {
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) spent += __shfl_xor_sync(0xffffffffu, spent, o);
-        worth = p.min_saved == 0 || static_cast<int64_t>(line.alone) - spent >= p.min_saved;
-        if (!worth) at[0] = at[1] = 0;
+        for (int c = 0; c < 2; ++c) {
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) spent[c] += __shfl_xor_sync(0xffffffffu, spent[c], o);
+          worth[c] = p.min_saved[c] == 0 || static_cast<int64_t>(line.alone[c]) - spent[c] >= p.min_saved[c];
+          if (!worth[c]) at[c] = 0;
+        }
         per[0] = at[0] > p.workers ? (at[0] + p.workers - 1) / p.workers : 1;
         per[1] = p.tile.workers > 0 && at[1] > p.tile.workers ? (at[1] + p.tile.workers - 1) / p.tile.workers : 1;
         if (lane == 0) {
           line.total = at[0];
           line.per = per[0];
+          line.worth[0] = worth[0];
+          line.worth[1] = worth[1];
           if (blockIdx.x == 0 && p.tile.workers > 0) {
             p.tile.head[0] = at[1];
             p.tile.head[1] = per[1];
@@ -166,12 +194,15 @@ __device__ __forceinline__ void prefix_line(const PrefixArgs& p, PrefixLine& lin
   // the sequences one a CTA in turn, by warps that are not in a hurry
   if (threadIdx.x >= 128 && threadIdx.x < 256)
     for (int64_t i = blockIdx.x + static_cast<int64_t>(gridDim.x) * (threadIdx.x - 128); i < t.seqs; i += static_cast<int64_t>(gridDim.x) * 128) {
-      const int skip = shared_tokens(a, line.groups, static_cast<int>(i));
+      int tall, skip = shared_tokens(a, line.groups, static_cast<int>(i), tall);
+      if (!line.worth[tall]) skip = 0;
       p.skip[i] = skip;
       if (skip > 0) a.prefix.home_row[i] = a.prefix.begin[a.prefix.group[i]] + a.prefix.first[i];
     }
 }
 
+// In calls that allow chunks, first: Prefix::steps and order.
+fg_status paged_prefix_order(const PrefixArgs& p, cudaStream_t st);
 fg_status paged_prefix(const PrefixArgs& p, int head_dim, cudaStream_t st);
 // Behind it, and behind the chunks' kernel where that has groups: the parts of every row joined in its home.
 fg_status paged_prefix_join(const PrefixArgs& p, int head_dim, cudaStream_t st);

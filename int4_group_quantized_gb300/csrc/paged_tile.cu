@@ -106,7 +106,7 @@ __device__ __forceinline__ void walk_unit(Walk& k, const AttnArgs<__half>& a) {
 template <int MODE>
 __device__ __forceinline__ void walk_seq(Walk& k, const AttnArgs<__half>& a) {
   if (MODE == kPrefix) {
-    const SharedGroup g = shared_group(a.prefix, a.tab, a.batch, k.i);
+    const ClassRows g = class_rows(a.prefix, a.tab, a.batch, k.i, true);   // of a split group: rows by Prefix::order
     k.s = Seq{g.first, g.list, g.tokens + g.list, g.tokens, 0};
   } else {
     k.s = seq_of<MODE == kBehind>(a.tab, a.batch, k.i);
@@ -384,7 +384,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const AttnArgs<__half
       const int base = nx.h * a.shape.group;
       for (int r = lane; r < nx.un.rows; r += 32) {
         const int row_ = nx.un.r0 + r, t = row_ / a.shape.group;
-        const __half* p = a.q + static_cast<int64_t>(MODE == kPrefix ? listed_row(a.prefix, a.batch, nx.s.row0 + t) : nx.s.row0 + t) * a.ldq + static_cast<int64_t>(base + row_ - t * a.shape.group) * D;
+        const __half* p = a.q + static_cast<int64_t>(MODE == kPrefix ? listed_row(a.prefix, a.batch, a.prefix.order[nx.s.row0 + t]) : nx.s.row0 + t) * a.ldq + static_cast<int64_t>(base + row_ - t * a.shape.group) * D;
         asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
         if (D == 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(p + 64));
       }
@@ -572,7 +572,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const AttnArgs<__half
     // where the lane's row begins in rows ld apart
     auto place = [&](int64_t ld) {
       const int row = k.un.r0 + (r < k.un.rows ? r : 0), tok = row / a.shape.group;
-      return (MODE == kPrefix ? listed_row(a.prefix, a.batch, k.s.row0 + tok) : k.s.row0 + tok) * ld + static_cast<int64_t>(k.h * a.shape.group + row - tok * a.shape.group) * D;
+      return (MODE == kPrefix ? listed_row(a.prefix, a.batch, a.prefix.order[k.s.row0 + tok]) : k.s.row0 + tok) * ld + static_cast<int64_t>(k.h * a.shape.group + row - tok * a.shape.group) * D;
     };
     uint8_t* const stage = sOut + warp * S::kOut;
     bool ok = true;
@@ -824,8 +824,8 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const AttnArgs<__half
       rows = k.un.rows;
       if (MODE == kPrefix) {
         const int row = k.un.r0 + (r < rows ? r : 0), t = row / a.shape.group;
-        dst = from_start ? static_cast<int64_t>(k.s.row0 + t) * a.q_heads + k.h * a.shape.group + row - t * a.shape.group
-                         : a.prefix.info[k.i].extra + static_cast<int64_t>(w) * kRows + r;
+        dst = from_start ? static_cast<int64_t>(a.prefix.order[k.s.row0 + t]) * a.q_heads + k.h * a.shape.group + row - t * a.shape.group
+                         : a.prefix.info[a.tab.seqs + k.i].extra + static_cast<int64_t>(w) * kRows + r;
       } else {
         dst = place(a.ldo);
       }

@@ -107,3 +107,32 @@ def test_steps(fg, name):
             v = op.restore(*(x[F.table[i, j // ps], h, j % ps] for x in F.arr["v"]))
             mag[sl] = np.abs(v).max()                        # no less than the weighted mean
     _hold(out, ref, mag)
+
+
+MIXED = {   # groups, tails, rows, heads, query heads a head, d, page size: steps of at most 4 rows a K/V head, and chunks of their group
+    "steps first": (([0] * 36, [24]), np.r_[_sizes(30, 1, 60, 1), _sizes(6, 100, 160, 2)], [1] * 30 + [40, 100, 64, 9, 77, 90], 2, 2, 128, 64),
+    "in turn": (([0, 1] * 20, [50, 33]), np.resize([7, 9, 90, 130], 40), np.resize([1, 1, 70, 33], 40), 2, 2, 64, 16),
+    "one among many": (([0] * 7 + [-1], [30]), [80, 70, 60, 5, 99, 64, 40, 50], [50, 60, 41, 2, 64, 64, 40, 1], 3, 1, 128, 32),
+    "few rows of chunks": (([0] * 50, [30]), np.r_[_sizes(49, 1, 60, 3), 70], [1] * 49 + [60], 2, 1, 64, 32),
+    "two kinds of groups": (([0] * 20 + [1] * 20 + [2] * 5, [40, 11, 20]), np.r_[np.full(20, 9), _sizes(25, 60, 90, 4)],
+                            [1] * 20 + [1, 2] * 5 + [50] * 10 + [55] * 5, 2, 1, 64, 32),
+    "more than a CTA plans": (([0, 1, 2] * 60, [40, 3, 20]), np.resize([3, 66, 5, 40], 180), np.resize([1, 50, 2, 40], 180), 1, 2, 64, 16),
+}
+
+
+@pytest.mark.parametrize("name", MIXED)
+def test_steps_beside_chunks_of_their_group(fg, name):
+    """A step is as exact beside chunks as without them; the chunks keep their bounds."""
+    groups, tails, n, heads, r, d, ps = MIXED[name]
+    F = Forked(fg, groups, tails, n, heads, r, d, ps, 43)
+    out = _run(fg, F)
+    assert torch.equal(out, _run(fg, F))
+    fg.fg_sync_status()
+    ref, tol = F.expect()
+    got = out.double().cpu().numpy()
+    why = op.off_by_too_much(got, ref, tol, 3 * op.HALF)
+    assert why is None, why
+    steps = np.repeat(np.asarray(n) * r <= 4, n)
+    assert (np.asarray(n) * r <= 16).sum() == (np.asarray(n) * r <= 4).sum() > 0
+    share = op.not_nearest(got[steps], ref[steps])
+    assert share <= MOST, share

@@ -61,3 +61,21 @@ def test_rows_that_the_share_lists_elsewhere_save_nothing(fg):
     share = fg.PageShare(*[getattr(good, f).clone() for f in FIELDS])
     share.rows[5:8] = share.rows[0]
     _decides(fg, F, share, 2 * 64 * 5 // 4 * (400 * (5 - 1) - 8 * 8))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_steps_and_chunks_of_a_group_decide_apart(fg, d):
+    """A prefix over two steps and twelve chunks of 20 rows: the chunks save much, the steps little."""
+    F = Forked(fg, ([0] * 14, [30]), [9] + [30] * 12 + [12], [1] + [20] * 12 + [1], 2, 1, d, 16, 54)
+    share, ref, alone = F.find(fg), F.expect(), _alone(fg, F)
+    both = _run(fg, F, share)
+    token = 2 * d * 5 // 4
+    steps = token * (480 * (2 - 1) - 8 * 2)
+    chunks = token * (480 * 4 * (12 - 1) - 8 * 240)          # 240 rows: one unit of 256
+    row = torch.as_tensor(np.repeat(F.n == 1, F.n), device="cuda")
+    for least, s, c in ((0, both, both), (steps, both, both), (steps + 1, alone, both), (chunks, alone, both), (chunks + 1, alone, alone)):
+        out = _run(fg, F, share, min_saved=least)
+        fg.fg_sync_status()
+        assert torch.equal(out[row], s[row]) and torch.equal(out[~row], c[~row]), least
+        _hold(out, *ref)
+    assert not torch.equal(alone[row], both[row]) and not torch.equal(alone[~row], both[~row])
