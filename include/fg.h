@@ -591,8 +591,8 @@ fg_status fg_pages_share(const fg_page_table* t, const int32_t* cu, int64_t min_
  * (fp32 sums on the CUDA cores: the rows' arithmetic, not the cache's bytes, is
  * their cost).
  * Sharing has launches of its own: where the groups save less than min_saved bytes
- * of cache reads (0: share all the same; negative: 64 MB) every sequence goes by
- * itself; in calls of more than 16 rows of a K/V head that is decided for chunks (of
+ * of cache reads (0: share all the same; negative: the library's own rule, by what
+ * either way takes) every sequence goes by itself; in calls of more than 16 rows of a K/V head that is decided for chunks (of
  * groups that have more than 128 rows of them) and for all others apart.  Counted
  * are the reads of its group's tokens of every sequence that would
  * leave them to the group (see above: none that goes by itself anyway), once for up to 16

@@ -293,14 +293,22 @@ fg_status join(const AttnArgs<T>& a, const ClassPlan& step, const ClassPlan& til
                       32 * kJoinWarps, 0, st, a, step, tile);
 }
 
-// Bytes of cache reads that groups have to save before a call shares, as paged_prefix.cuh counts them.  Both sides in us, alone
-// (the launches that find it out among them: 8 for steps, 13 for chunks) and shared.  Steps over one prefix: 64 sequences, 32
-// heads of 128, 75 MB saved: 50 and 52, 157 MB: 65 and 52, 1.3 GB: 266 and 71; 16 sequences, 32 heads on 8, 39 MB: 32 and 39, 77
-// MB: 40 and 40, 157 MB: 54 and 43, 629 MB: 142 and 67.  Chunks, 16 sequences of 32 heads: 32 rows over 512 tokens, 126 MB: 99
-// and 105, over 2,048, 566 MB: 172 and 125; 128 rows over 2,048, 250 MB: 186 and 195, over 8,192, 1.3 GB: 479 and 360; 400 rows
-// over 2,048, 31 MB: 354 and 410 (their units of 256 rows are as full by themselves as in a group), over 8,192, 910 MB: 990 and
-// 917; ragged ones of 2 to 139 rows, 32 heads on 8, over two prefixes of 1,920 and 4,160, 69 MB: 194 and 163.
-constexpr int64_t kSharedSaves = int64_t(64) << 20;
+// ---- when a call shares ------------------------------------------------------------------
+// By min_saved, the reads that the header counts: a chunk's four times a step's, a group's unit once or four times, 8 tokens for
+// a row's parts.  By the library's own rule, what the launches cost, from 880 calls of 2 to 256 sequences of 1 to 400 rows over
+// one prefix of 128 to 32,768 tokens, with 32 heads of 128, 32 on 8, 64 on 8, 16 and 12 of 64, each timed alone
+// (fg_paged_attention) and shared (inputs larger than L2, or L2 flushed: the same rule):
+//   class 0: a chunk's 256 rows read as two steps do, a group's unit as two and a 24th of one for each row, a row's parts as 32
+//     tokens, and the launches as 100 MB.  Of 290 calls of steps four are more than 5% slower than the faster way, in all 0.5%, and of
+//     102 of a few chunks two.  Alone and
+//     shared, us: 16 sequences, 32 heads, 1,024 tokens 33 and 38 (goes alone), 2,048 60 and 41; 64 sequences 512 tokens 66 and 65,
+//     1,024 94 and 66; 4 sequences 8,192 tokens 44 and 55 (alone), 32,768 160 and 133.
+//   class 1: a chunk's 256 rows as four, a group's as five, parts as 32 tokens, the launches as 150 MB.  Of 492 calls 16, in all
+//     0.3%.  16 sequences, 32 heads, 20 rows over 1,024 tokens 102 and 108 (alone), 1,536 126 and 112; 128 rows over 2,048 161 and
+//     203 (alone), 8,192 458 and 371; 48 of 32 rows over 512 186 and 221 (alone), 1,024 262 and 241.
+// (One limit of 64 MB by the header's count for both took calls that are up to 1.7 times as slow.)
+constexpr SharePrices kCounted = {{4 * kStepPrice, 4 * kStepPrice}, {kStepPrice, 4 * kStepPrice}, 0, 8 * kStepPrice, {0, 0}};
+constexpr SharePrices kMeasured = {{2 * kStepPrice, 4 * kStepPrice}, {2 * kStepPrice, 5 * kStepPrice}, 1, 32 * kStepPrice, {100000000, 150000000}};
 
 // ---- workspace ------------------------------------------------------------------------
 constexpr int kMaxSms = 160;   // a workspace fits this many SMs; launches use no more
@@ -377,7 +385,7 @@ Layout layout_of(const fg_page_pool& pool, const fg_page_table& t, int32_t q_hea
 template <typename T>
 fg_status launch_attn(const fg_page_pool& pool, const fg_page_table& t, const int32_t* cu, const void* q, int64_t ldq,
                       int32_t q_heads, int64_t ntok, int64_t max_q, int64_t window, int64_t sinks, void* out,
-                      int64_t ldo, void* ws, unsigned int* err, cudaStream_t st, const fg_page_share* share = nullptr, int64_t min_saved = 0) {   // tokens' reads
+                      int64_t ldo, void* ws, unsigned int* err, cudaStream_t st, const fg_page_share* share = nullptr, const SharePrices& price = kCounted) {
   AttnArgs<T> a;
   a.pool = pool_of(pool);
   a.tab = table_of(t);
@@ -406,7 +414,7 @@ fg_status launch_attn(const fg_page_pool& pool, const fg_page_table& t, const in
       a.prefix.leader = share->leader;
       a.prefix.begin = share->begin;
       a.prefix.rows = share->rows;
-      const PrefixArgs p{a, l.skip, l.tall, std::min(num_sms(), kMaxSms), {min_saved, min_saved}};
+      const PrefixArgs p{a, l.skip, l.tall, std::min(num_sms(), kMaxSms), price};
       if (l.tall.workers > 0) FG_TRY(paged_prefix_order(p, st));
       FG_TRY(paged_prefix(p, pool.head_dim, st));
       if (l.tall.workers > 0) FG_TRY(paged_prefix_tile(a, l.tall, pool.head_dim, st));
@@ -517,12 +525,17 @@ fg_status fg_paged_attention_shared(const fg_page_pool* pool, const fg_page_tabl
   if (!err) return fail(FG_ERR_CUDA, "device error word");
   // in tokens; K and V of one are 1.25 bytes an element
   const int64_t token = static_cast<int64_t>(pool->heads) * pool->head_dim * 5 / 4;
-  const int64_t bytes = min_saved < 0 ? kSharedSaves : min_saved, least = bytes / token + (bytes % token != 0);
+  SharePrices price = min_saved < 0 ? kMeasured : kCounted;
+  for (int64_t& least : price.least) {
+    const int64_t bytes = min_saved < 0 ? least : min_saved, tokens = bytes / token + (bytes % token != 0);
+    least = std::min(tokens, INT64_MAX / kStepPrice) * kStepPrice;
+  }
   // all sequences' reads of all that a table row can name are no less than what groups can save
   const double group = static_cast<double>(q_heads / pool->heads), most = static_cast<double>(std::min<int64_t>(t->seqs, ntok));
-  const double reads = max_q * group <= kStepRows ? most : kChunkRead * (most + static_cast<double>(ntok) * group / kTileRows);
+  const double reads = max_q * group <= kStepRows ? kStepPrice * most : 4 * kStepPrice * (most + static_cast<double>(ntok) * group / kTileRows);
+  const int64_t least = std::min(price.least[0], price.least[1]);
   const bool never = least > 0 && static_cast<double>(t->stride) * t->page_size * reads < static_cast<double>(least);
-  return launch_attn<__half>(*pool, *t, cu, q, ldq, q_heads, ntok, max_q, 0, 0, out, ldo, ws, err, stream, never ? nullptr : s, least);
+  return launch_attn<__half>(*pool, *t, cu, q, ldq, q_heads, ntok, max_q, 0, 0, out, ldo, ws, err, stream, never ? nullptr : s, price);
 }
 
 }  // extern "C"

@@ -17,21 +17,27 @@
 namespace fg {
 namespace paged {
 
+// What a call counts to find whether it shares, by class (0: paged_prefix.cu's rows, 1: the chunks' kernel's), in 24ths of one
+// read of a token's K and V of a K/V head: a step's read of a token by itself is 24.
+struct SharePrices {
+  int chunk[2];           // a chunk's by itself, for each kTileRows of its rows
+  int unit[2];            // a group's unit
+  int unit_row;           // and each row of a unit of class 0
+  int row;                // a row's parts, written and read again
+  int64_t least[2];       // what a class's groups have to save; 0: groups whatever they save
+};
 struct PrefixArgs {
   AttnArgs<__half> a;
   int32_t* skip;          // [seqs] out: the tokens of a sequence that its group attends to
   ClassPlan tile;         // head and pre by group, out; no workers: one class
   int workers;
-  int64_t min_saved[2];   // tokens' reads that a class's groups have to save; 0: groups whatever they save
+  SharePrices price;
 };
 
 constexpr int kPrefixKeysLog2 = 7;
 // Rows of a group's chunks up to which they are not the chunks' kernel's.
 constexpr int kPrefixFew = 128;
-// What a read of a tile costs a unit of the chunks' kernel, in reads of a step's (some 14.5 ns over all SMs against 3 to 6), and
-// what a row's parts, written and read again, cost its query heads, in tokens of their K/V head (6400 rows of 32 heads some 70 us
-// where the heads have a K/V head each, as many where four share one: 5 to 20).
-constexpr int kChunkRead = 4, kRowParts = 8;
+constexpr int kStepPrice = 24;
 
 __device__ __forceinline__ PrefixGroup prefix_group(const SharedGroup& s, int group, bool tall) {
   PrefixGroup g;
@@ -62,13 +68,13 @@ __device__ __forceinline__ int shared_tokens(const AttnArgs<__half>& a, int grou
   return rows[0] == q.row0 && rows[q.n - 1] == q.row0 + q.n - 1 ? s.tokens : 0;
 }
 
-// What sequence i reads of its group's tokens when it goes by itself; nothing where it does so in any case.
+// What sequence i's reads of its group's tokens count when it goes by itself; nothing where it does so in any case.
 __device__ __forceinline__ int64_t read_alone(const PrefixArgs& p, int groups, int i, int& tall) {
   const AttnArgs<__half>& a = p.a;
   const int64_t tokens = shared_tokens(a, groups, i, tall);
   if (tokens == 0) return 0;
   const int64_t rows = (static_cast<int64_t>(a.batch.cu[i + 1]) - a.batch.cu[i]) * a.shape.group;
-  return tokens * (p.tile.workers == 0 || rows <= kStepRows ? 1 : kChunkRead * ((rows + kTileRows - 1) / kTileRows));
+  return tokens * (p.tile.workers == 0 || rows <= kStepRows ? kStepPrice : p.price.chunk[tall] * ((rows + kTileRows - 1) / kTileRows));
 }
 // What every CTA works out first, by all its threads: the whole line's length and share, what the launches after it read
 // (written by the CTAs together), and where its own share begins.
@@ -84,7 +90,7 @@ __device__ __forceinline__ void prefix_line(const PrefixArgs& p, PrefixLine& lin
   const AttnArgs<__half>& a = p.a;
   const Table& t = a.tab;
   const int group = a.shape.group, heads = a.pool.heads, lane = threadIdx.x & 31;
-  if (p.min_saved[0] > 0 || p.min_saved[1] > 0) {
+  if (p.price.least[0] > 0 || p.price.least[1] > 0) {
     if (threadIdx.x < 32) {
       int groups = 0;
       bool last = false;
@@ -127,7 +133,8 @@ __device__ __forceinline__ void prefix_line(const PrefixArgs& p, PrefixLine& lin
         PrefixGroup x[2] = {prefix_group(s[0], group, false), prefix_group(s[1], group, true)};
 #pragma unroll
         for (int c = 0; c < 2; ++c)
-          spent[c] += static_cast<int64_t>(s[c].tokens) * x[c].units * (c ? kChunkRead : 1) + static_cast<int64_t>(s[c].list) * group * kRowParts;
+          spent[c] += static_cast<int64_t>(s[c].tokens) * x[c].units * (p.price.unit[c] + (c ? 0 : p.price.unit_row * x[c].rows)) +
+                      static_cast<int64_t>(s[c].list) * group * p.price.row;
         const int64_t n[2] = {static_cast<int64_t>(heads) * x[0].units * x[0].tiles, static_cast<int64_t>(heads) * x[1].units * x[1].tiles};
         int64_t inc[2] = {n[0], n[1]};
 #pragma unroll
@@ -172,7 +179,7 @@ __device__ __forceinline__ void prefix_line(const PrefixArgs& p, PrefixLine& lin
         for (int c = 0; c < 2; ++c) {
 #pragma unroll
           for (int o = 16; o > 0; o >>= 1) spent[c] += __shfl_xor_sync(0xffffffffu, spent[c], o);
-          worth[c] = p.min_saved[c] == 0 || static_cast<int64_t>(line.alone[c]) - spent[c] >= p.min_saved[c];
+          worth[c] = p.price.least[c] == 0 || static_cast<int64_t>(line.alone[c]) - spent[c] >= p.price.least[c];
           if (!worth[c]) at[c] = 0;
         }
         per[0] = at[0] > p.workers ? (at[0] + p.workers - 1) / p.workers : 1;

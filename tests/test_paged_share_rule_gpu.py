@@ -79,3 +79,25 @@ def test_steps_and_chunks_of_a_group_decide_apart(fg, d):
         assert torch.equal(out[row], s[row]) and torch.equal(out[~row], c[~row]), least
         _hold(out, *ref)
     assert not torch.equal(alone[row], both[row]) and not torch.equal(alone[~row], both[~row])
+
+
+BY_ITSELF = {   # 32 heads of 128, one prefix: sequences, rows of each, tokens, and whether sharing is faster (us alone, shared)
+    "4 steps over 8,192": (4, 1, 8192, False),               # 44, 55
+    "8 steps over 2,048": (8, 1, 2048, False),               # 33, 37
+    "16 chunks of 32 over 512": (16, 32, 512, False),        # 78, 107 (they save 126 MB by the count that min_saved has)
+    "4 chunks of 128 over 4,096": (4, 128, 4096, False),     # 84, 99 (147 MB)
+    "16 steps over 2,048": (16, 1, 2048, True),              # 60, 41
+    "16 chunks of 20 over 2,048": (16, 20, 2048, True),      # 150, 122
+}
+
+
+@pytest.mark.parametrize("name", BY_ITSELF)
+def test_the_librarys_own_rule(fg, name):
+    """Calls that measured slower when they shared go by themselves."""
+    b, n, tokens, shares = BY_ITSELF[name]
+    F = Forked(fg, ([0] * b, [tokens // 64]), [300] * b, [n] * b, 32, 1, 128, 64, 55)
+    share = F.find(fg)
+    alone, both = _alone(fg, F), _run(fg, F, share)
+    assert not torch.equal(alone, both)
+    assert torch.equal(_run(fg, F, share, min_saved=-1), both if shares else alone)
+    fg.fg_sync_status()
