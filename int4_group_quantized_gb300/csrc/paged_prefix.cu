@@ -293,14 +293,16 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const PrefixArgs p,
     line.alone[0] = line.alone[1] = 0;
     mbar_fence_init();
   }
+  griddep_launch();
+  griddep_wait();
+  __syncthreads();
+  prefix_line(p, line);
+  if (line.total == 0) return;   // a call that does not share: no tensor memory is taken
   if (warp == kMmaWarp) tmem_alloc(tmem_slot, kTmemCols);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  griddep_launch();
-  griddep_wait();
-  prefix_line(p, line);
   Walk k = {};
   walk_begin(k, p, line);
 
@@ -875,24 +877,34 @@ __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const PrefixA
 
 // ---- steps and chunks of a group ---------------------------------------------------------------------
 // A block a group: the rows of its chunks are counted, and where they are many the list's places put in order, steps first
-// (a row's kind is its sequence's, found from the offsets), in two passes over the list.
+// (a row's kind is its sequence's, found from the offsets, which are looked up in shared memory while they fit there), in two
+// passes over the list, the second by the first's bits.
 constexpr int kOrderThreads = 512;
 __global__ void __launch_bounds__(kOrderThreads) prefix_order_kernel(const PrefixArgs p) {
+  constexpr int kNear = 1024, kKept = 32;
   __shared__ int counts[2][kOrderThreads / 32];
+  __shared__ int near[kNear + 1];
   griddep_launch();
   griddep_wait();
   const AttnArgs<__half>& a = p.a;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (a.tab.seqs <= kNear)
+    for (int i = threadIdx.x; i <= a.tab.seqs; i += kOrderThreads) near[i] = a.batch.cu[i];
+  const int32_t* const cu = a.tab.seqs <= kNear ? near : a.batch.cu;
   for (int g = blockIdx.x; g < a.tab.seqs; g += gridDim.x) {
     const SharedGroup s = shared_group(a.prefix, a.tab, a.batch, g);
+    if (g == static_cast<int>(blockIdx.x)) __syncthreads();   // the offsets are here
     auto chunk = [&](int x) {   // place x of the group
-      const int r = a.prefix.rows[s.first + x], i = seq_of_row(a.batch.cu, a.tab.seqs, r);
-      return i < a.tab.seqs && (static_cast<int64_t>(a.batch.cu[i + 1]) - a.batch.cu[i]) * a.shape.group > kStepRows;
+      const int r = a.prefix.rows[s.first + x], i = seq_of_row(cu, a.tab.seqs, r);
+      return i < a.tab.seqs && (static_cast<int64_t>(cu[i + 1]) - cu[i]) * a.shape.group > kStepRows;
     };
     int chunks = 0;
-    for (int x0 = 0; x0 < s.list; x0 += kOrderThreads) {
+    uint32_t kept = 0;          // the thread's first places
+    for (int x0 = 0, n = 0; x0 < s.list; x0 += kOrderThreads, ++n) {
       const int x = x0 + threadIdx.x;
-      chunks += __syncthreads_count(x < s.list && chunk(x));
+      const bool is = x < s.list && chunk(x);
+      if (n < kKept) kept |= (is ? 1u : 0u) << n;
+      chunks += __syncthreads_count(is);
     }
     const bool split = static_cast<int64_t>(chunks) * a.shape.group > kPrefixFew;
     const int steps = s.list - chunks;
@@ -900,9 +912,9 @@ __global__ void __launch_bounds__(kOrderThreads) prefix_order_kernel(const Prefi
     if (s.leader < 0) break;   // past the last group
     if (!split) continue;
     int before = 0;            // chunks' rows
-    for (int x0 = 0, turn = 0; x0 < s.list; x0 += kOrderThreads, turn ^= 1) {
+    for (int x0 = 0, turn = 0, n = 0; x0 < s.list; x0 += kOrderThreads, turn ^= 1, ++n) {
       const int x = x0 + threadIdx.x;
-      const bool is = x < s.list && chunk(x);
+      const bool is = n < kKept ? (kept >> n) & 1u : x < s.list && chunk(x);
       const uint32_t mates = __ballot_sync(0xffffffffu, is);
       if (lane == 0) counts[turn][warp] = __popc(mates);
       __syncthreads();         // (the other turn's counts have been read by all when they are written again)

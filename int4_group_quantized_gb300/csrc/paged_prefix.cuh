@@ -90,18 +90,80 @@ __device__ __forceinline__ void prefix_line(const PrefixArgs& p, PrefixLine& lin
   const AttnArgs<__half>& a = p.a;
   const Table& t = a.tab;
   const int group = a.shape.group, heads = a.pool.heads, lane = threadIdx.x & 31;
-  if (p.price.least[0] > 0 || p.price.least[1] > 0) {
-    if (threadIdx.x < 32) {
-      int groups = 0;
-      bool last = false;
-      for (; !last && groups < t.seqs; groups += 32) last = __any_sync(0xffffffffu, groups + lane < t.seqs && a.prefix.leader[groups + lane] < 0);
-      if (lane == 0) line.groups = min(groups, t.seqs);
+  bool worth[2] = {true, true};
+  int64_t per[2] = {1, 1}, spent[2], all[2];   // (warp 0) reads of the groups and their parts, and the classes' lines
+  // Groups up to the first gap, 32 at a time: what the classes' lines hold and cost, and (write) where each lies in them.
+  auto walk = [&](bool write) {
+    int64_t at[2] = {0, 0};
+    spent[0] = spent[1] = 0;
+    const int64_t o0 = blockIdx.x * per[0];
+    int groups = 0;
+    for (bool last = false; !last; groups += 32) {
+      const int g = groups + lane;
+      ClassRows s[2] = {{{-1, 0, 0, 0}, false}, {{-1, 0, 0, 0}, false}};
+      if (g < t.seqs) {
+        s[0] = class_rows(a.prefix, t, a.batch, g, false);
+        if (p.tile.workers > 0) s[1] = class_rows(a.prefix, t, a.batch, g, true);
+      }
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+        if (!worth[c]) s[c].list = 0;
+      PrefixGroup x[2] = {prefix_group(s[0], group, false), prefix_group(s[1], group, true)};
+      int64_t inc[2];
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        spent[c] += static_cast<int64_t>(s[c].tokens) * x[c].units * (p.price.unit[c] + (c ? 0 : p.price.unit_row * x[c].rows)) +
+                    static_cast<int64_t>(s[c].list) * group * p.price.row;
+        x[c].base = inc[c] = static_cast<int64_t>(heads) * x[c].units * x[c].tiles;
+      }
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const int64_t up = __shfl_up_sync(0xffffffffu, inc[c], o);
+          if (lane >= o) inc[c] += up;
+        }
+      if (write) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          x[c].base = at[c] + inc[c] - x[c].base;
+          x[c].per = per[c];
+          x[c].extra = c ? p.workers * kPrefixRows : 0;
+        }
+        if (blockIdx.x == 0 && g < t.seqs) {
+          a.prefix.info[g] = x[0];
+          if (p.tile.workers > 0) {
+            a.prefix.info[t.seqs + g] = x[1];
+            p.tile.pre[g] = x[1].base;
+          }
+        }
+        if (o0 >= x[0].base && o0 < at[0] + inc[0]) {
+          line.g = g;
+          line.at = x[0];
+        }
+      }
+#pragma unroll
+      for (int c = 0; c < 2; ++c) at[c] += __shfl_sync(0xffffffffu, inc[c], 31);
+      last = __any_sync(0xffffffffu, s[0].leader < 0) || groups + 32 >= t.seqs;
     }
-    __syncthreads();
+    all[0] = at[0];
+    all[1] = at[1];
+    groups = min(groups, t.seqs);
+    if (write && blockIdx.x == 0 && p.tile.workers > 0)
+      for (int i = groups + lane; i <= t.seqs; i += 32) p.tile.pre[i] = at[1];
+    return groups;
+  };
+  if (threadIdx.x < 32) {
+    const int groups = walk(false);
+    if (lane == 0) line.groups = groups;
+  } else if (p.price.least[0] > 0 || p.price.least[1] > 0) {   // meanwhile, by the other warps
+    int groups = 0;
+    for (bool last = false; !last && groups < t.seqs; groups += 32) last = __any_sync(0xffffffffu, groups + lane < t.seqs && a.prefix.leader[groups + lane] < 0);
+    groups = min(groups, t.seqs);
     int64_t sum[2] = {0, 0};
-    for (int i = threadIdx.x; i < t.seqs; i += blockDim.x) {
+    for (int i = threadIdx.x - 32; i < t.seqs; i += blockDim.x - 32) {
       int tall;
-      const int64_t reads = read_alone(p, line.groups, i, tall);
+      const int64_t reads = read_alone(p, groups, i, tall);
       sum[0] += tall ? 0 : reads;
       sum[1] += tall ? reads : 0;
     }
@@ -111,98 +173,42 @@ __device__ __forceinline__ void prefix_line(const PrefixArgs& p, PrefixLine& lin
       for (int o = 16; o > 0; o >>= 1) sum[c] += __shfl_xor_sync(0xffffffffu, sum[c], o);
       if (lane == 0 && sum[c] > 0) atomicAdd(&line.alone[c], static_cast<unsigned long long>(sum[c]));
     }
-    __syncthreads();
   }
+  __syncthreads();
   if (threadIdx.x < 32) {
-    bool worth[2] = {true, true};
-    int64_t per[2] = {1, 1};
-    for (int pass = 0; pass < 2; ++pass) {
-      int64_t spent[2] = {0, 0};              // reads of the groups, and their parts
-      int64_t at[2] = {0, 0};                 // of the two classes' lines
-      const int64_t o0 = blockIdx.x * per[0];
-      for (int g0 = 0; g0 < t.seqs; g0 += 32) {
-        const int g = g0 + lane;
-        ClassRows s[2] = {{{-1, 0, 0, 0}, false}, {{-1, 0, 0, 0}, false}};
-        if (g < t.seqs) {
-          s[0] = class_rows(a.prefix, t, a.batch, g, false);
-          if (p.tile.workers > 0) s[1] = class_rows(a.prefix, t, a.batch, g, true);
-        }
 #pragma unroll
-        for (int c = 0; c < 2; ++c)
-          if (!worth[c]) s[c].list = 0;
-        PrefixGroup x[2] = {prefix_group(s[0], group, false), prefix_group(s[1], group, true)};
+    for (int c = 0; c < 2; ++c) {
 #pragma unroll
-        for (int c = 0; c < 2; ++c)
-          spent[c] += static_cast<int64_t>(s[c].tokens) * x[c].units * (p.price.unit[c] + (c ? 0 : p.price.unit_row * x[c].rows)) +
-                      static_cast<int64_t>(s[c].list) * group * p.price.row;
-        const int64_t n[2] = {static_cast<int64_t>(heads) * x[0].units * x[0].tiles, static_cast<int64_t>(heads) * x[1].units * x[1].tiles};
-        int64_t inc[2] = {n[0], n[1]};
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1)
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const int64_t up = __shfl_up_sync(0xffffffffu, inc[c], o);
-            if (lane >= o) inc[c] += up;
-          }
-        if (pass == 1) {
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            x[c].base = at[c] + inc[c] - n[c];
-            x[c].per = per[c];
-            x[c].extra = c ? p.workers * kPrefixRows : 0;
-          }
-          if (blockIdx.x == 0 && g < t.seqs) {
-            a.prefix.info[g] = x[0];
-            if (p.tile.workers > 0) {
-              a.prefix.info[t.seqs + g] = x[1];
-              p.tile.pre[g] = x[1].base;
-            }
-          }
-          if (n[0] > 0 && o0 >= x[0].base && o0 < x[0].base + n[0]) {
-            line.g = g;
-            line.at = x[0];
-          }
-        }
-#pragma unroll
-        for (int c = 0; c < 2; ++c) at[c] += __shfl_sync(0xffffffffu, inc[c], 31);
-        const bool last = __any_sync(0xffffffffu, s[0].leader < 0) || g0 + 32 >= t.seqs;   // past the last group
-        if (!last) continue;
-        const int groups = min(g0 + 32, t.seqs);
-        if (pass == 1 && lane == 0) line.groups = groups;
-        if (pass == 1 && blockIdx.x == 0 && lane == 0) *a.prefix.planned = worth[0] || worth[1] ? groups : 0;
-        if (pass == 1 && blockIdx.x == 0 && p.tile.workers > 0)
-          for (int i = groups + lane; i <= t.seqs; i += 32) p.tile.pre[i] = at[1];
-        break;
-      }
-      if (pass == 0) {
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-#pragma unroll
-          for (int o = 16; o > 0; o >>= 1) spent[c] += __shfl_xor_sync(0xffffffffu, spent[c], o);
-          worth[c] = p.price.least[c] == 0 || static_cast<int64_t>(line.alone[c]) - spent[c] >= p.price.least[c];
-          if (!worth[c]) at[c] = 0;
-        }
-        per[0] = at[0] > p.workers ? (at[0] + p.workers - 1) / p.workers : 1;
-        per[1] = p.tile.workers > 0 && at[1] > p.tile.workers ? (at[1] + p.tile.workers - 1) / p.tile.workers : 1;
-        if (lane == 0) {
-          line.total = at[0];
-          line.per = per[0];
-          line.worth[0] = worth[0];
-          line.worth[1] = worth[1];
-          if (blockIdx.x == 0 && p.tile.workers > 0) {
-            p.tile.head[0] = at[1];
-            p.tile.head[1] = per[1];
-          }
+      for (int o = 16; o > 0; o >>= 1) spent[c] += __shfl_xor_sync(0xffffffffu, spent[c], o);
+      worth[c] = p.price.least[c] == 0 || static_cast<int64_t>(line.alone[c]) - spent[c] >= p.price.least[c];
+      if (!worth[c]) all[c] = 0;
+    }
+    per[0] = all[0] > p.workers ? (all[0] + p.workers - 1) / p.workers : 1;
+    per[1] = p.tile.workers > 0 && all[1] > p.tile.workers ? (all[1] + p.tile.workers - 1) / p.tile.workers : 1;
+    if (lane == 0) {
+      line.total = all[0];
+      line.per = per[0];
+      line.worth[0] = worth[0];
+      line.worth[1] = worth[1];
+      if (blockIdx.x == 0) {
+        *a.prefix.planned = worth[0] || worth[1] ? line.groups : 0;
+        if (p.tile.workers > 0) {
+          p.tile.head[0] = all[1];
+          p.tile.head[1] = per[1];
         }
       }
     }
+    if (worth[0] || worth[1]) walk(true);
   }
   __syncthreads();
   // the sequences one a CTA in turn, by warps that are not in a hurry
   if (threadIdx.x >= 128 && threadIdx.x < 256)
     for (int64_t i = blockIdx.x + static_cast<int64_t>(gridDim.x) * (threadIdx.x - 128); i < t.seqs; i += static_cast<int64_t>(gridDim.x) * 128) {
-      int tall, skip = shared_tokens(a, line.groups, static_cast<int>(i), tall);
-      if (!line.worth[tall]) skip = 0;
+      int tall, skip = 0;
+      if (line.worth[0] || line.worth[1]) {
+        skip = shared_tokens(a, line.groups, static_cast<int>(i), tall);
+        if (!line.worth[tall]) skip = 0;
+      }
       p.skip[i] = skip;
       if (skip > 0) a.prefix.home_row[i] = a.prefix.begin[a.prefix.group[i]] + a.prefix.first[i];
     }

@@ -327,6 +327,11 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const AttnArgs<__half
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int w = blockIdx.x;
 
+  if (MODE == kPrefix) {   // often there is nothing: then it ends before it takes tensor memory
+    griddep_launch();
+    griddep_wait();
+    if (pl.head[0] == 0) return;
+  }
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&qfull[i], 4);
@@ -346,8 +351,10 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const AttnArgs<__half
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  griddep_launch();
-  griddep_wait();
+  if (MODE != kPrefix) {
+    griddep_launch();
+    griddep_wait();
+  }
   __shared__ OwnPlan own;
   __shared__ Line line;   // not in registers: it is read between segments only
   {
