@@ -54,10 +54,10 @@ template <bool SKIP = false>
 __device__ __forceinline__ Seq seq_of(const Table& t, const Batch& b, int i) {
   Seq s;
   const int a = b.cu[i], e = b.cu[i + 1];
-  const int len = t.lens[i];
+  const int len = t.lens[i], left = SKIP ? t.skip[i] : 0;   // loaded together
   const bool ok = a >= 0 && e >= a && e <= b.ntok && len >= 0;
   if (!ok) atomicOr(b.err, DEV_ERR_BATCH);
-  const int skip = SKIP && ok ? t.skip[i] : 0;
+  const int skip = ok ? left : 0;
   s.row0 = ok ? a : 0;
   s.n = ok ? e - a : 0;
   s.len = ok ? len - skip : 0;

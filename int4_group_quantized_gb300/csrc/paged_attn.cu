@@ -370,8 +370,9 @@ Layout layout_of(const fg_page_pool& pool, const fg_page_table& t, int32_t q_hea
       l.tall.rows = kTileRows;
       take(l.tall.head, 256);
       take(l.tall.pre, 8 * static_cast<size_t>(t.seqs + 1));
-      take(l.prefix.steps, 4 * static_cast<size_t>(t.seqs));
+      for (int32_t** x : {&l.prefix.steps, &l.prefix.chunks, &l.prefix.member, &l.prefix.before}) take(*x, 4 * static_cast<size_t>(t.seqs));
       take(l.prefix.order, 4 * static_cast<size_t>(shared_rows));
+      take(l.prefix.head, 16);
     }
     take(l.prefix.home_stat, 8 * pairs);
     take(l.prefix.extra_stat, 8 * extra);
@@ -415,7 +416,7 @@ fg_status launch_attn(const fg_page_pool& pool, const fg_page_table& t, const in
       a.prefix.begin = share->begin;
       a.prefix.rows = share->rows;
       const PrefixArgs p{a, l.skip, l.tall, std::min(num_sms(), kMaxSms), price};
-      if (l.tall.workers > 0) FG_TRY(paged_prefix_order(p, st));
+      if (l.tall.workers > 0) FG_TRY(paged_prefix_plan(p, st));
       FG_TRY(paged_prefix(p, pool.head_dim, st));
       if (l.tall.workers > 0) FG_TRY(paged_prefix_tile(a, l.tall, pool.head_dim, st));
       FG_TRY(paged_prefix_join(p, pool.head_dim, st));

@@ -17,8 +17,11 @@ struct PrefixGroup {
 };
 struct Prefix {
   const int32_t *group, *tokens, *first, *leader, *begin, *rows;   // fg_page_share
-  int32_t* steps;                 // [seqs] calls with chunks: of a group whose chunks are the chunks' kernel's the rows of its steps, else -1
-  int32_t* order;                 // [ntok] and of such a group's places in the list its steps' first, then its chunks'
+  // calls with chunks (else null): of a group whose chunks are the chunks' kernel's the rows of its steps and of its chunks,
+  // [seqs] each, steps -1 where it is not split so; and its places in the list, its steps' first, then its chunks'
+  int32_t *steps, *chunks, *order;
+  int32_t *member, *before;       // [seqs] the group that a sequence leaves tokens to, -1: none; rows of its kind and group before its own
+  int64_t* head;                  // tiles of paged_prefix.cu's line, and of a share of it
   PrefixGroup* info;              // [*planned], groups that are none with no units among them; [seqs + *planned] of their chunks
   int32_t* planned;
   int32_t* home_row;              // [seqs] the home of a sequence's first row
@@ -59,11 +62,9 @@ __device__ __forceinline__ ClassRows class_rows(const Prefix& p, const Table& t,
   s.split = steps >= 0;
   if (!s.split) {
     if (tall) s.list = 0;
-  } else if (tall) {
-    s.first += steps;
-    s.list -= steps;
   } else {
-    s.list = steps;
+    s.first += tall ? steps : 0;
+    s.list = tall ? p.chunks[g] : steps;
   }
   return s;
 }

@@ -41,8 +41,6 @@
 // that gave up.
 #include <math.h>
 
-#include <algorithm>
-
 #include "paged_prefix.cuh"
 #include "q4_dev.cuh"
 #include "tc_ptx.cuh"
@@ -296,7 +294,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const PrefixArgs p,
   griddep_launch();
   griddep_wait();
   __syncthreads();
-  prefix_line(p, line);
+  if (p.tile.workers > 0) planned_line(p, line);
+  else prefix_line<false>(p, line);
   if (line.total == 0) return;   // a call that does not share: no tensor memory is taken
   if (warp == kMmaWarp) tmem_alloc(tmem_slot, kTmemCols);
   tc_fence_before();
@@ -875,59 +874,73 @@ __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const PrefixA
   }
 }
 
-// ---- steps and chunks of a group ---------------------------------------------------------------------
-// A block a group: the rows of its chunks are counted, and where they are many the list's places put in order, steps first
-// (a row's kind is its sequence's, found from the offsets, which are looked up in shared memory while they fit there), in two
-// passes over the list, the second by the first's bits.
-constexpr int kOrderThreads = 512;
-__global__ void __launch_bounds__(kOrderThreads) prefix_order_kernel(const PrefixArgs p) {
-  constexpr int kNear = 1024, kKept = 32;
-  __shared__ int counts[2][kOrderThreads / 32];
-  __shared__ int near[kNear + 1];
+// ---- the plan of a call with chunks ------------------------------------------------------------------
+// One CTA: who takes part, how many rows of steps and of chunks each group has and where a sequence's rows begin among those
+// of its kind (a warp adds them up, 32 sequences at a time), the line, and where a call shares the list's places in order,
+// steps first.  20 chunks over two prefixes: 7 us.
+constexpr int kPlanThreads = 1024, kNear = 1024;
+__global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixArgs p) {
+  __shared__ PrefixLine line;
+  __shared__ int32_t near_member[kNear], near_rows[kNear], near_count[2][kNear];
   griddep_launch();
   griddep_wait();
   const AttnArgs<__half>& a = p.a;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  if (a.tab.seqs <= kNear)
-    for (int i = threadIdx.x; i <= a.tab.seqs; i += kOrderThreads) near[i] = a.batch.cu[i];
-  const int32_t* const cu = a.tab.seqs <= kNear ? near : a.batch.cu;
-  for (int g = blockIdx.x; g < a.tab.seqs; g += gridDim.x) {
-    const SharedGroup s = shared_group(a.prefix, a.tab, a.batch, g);
-    if (g == static_cast<int>(blockIdx.x)) __syncthreads();   // the offsets are here
-    auto chunk = [&](int x) {   // place x of the group
-      const int r = a.prefix.rows[s.first + x], i = seq_of_row(cu, a.tab.seqs, r);
-      return i < a.tab.seqs && (static_cast<int64_t>(cu[i + 1]) - cu[i]) * a.shape.group > kStepRows;
-    };
-    int chunks = 0;
-    uint32_t kept = 0;          // the thread's first places
-    for (int x0 = 0, n = 0; x0 < s.list; x0 += kOrderThreads, ++n) {
-      const int x = x0 + threadIdx.x;
-      const bool is = x < s.list && chunk(x);
-      if (n < kKept) kept |= (is ? 1u : 0u) << n;
-      chunks += __syncthreads_count(is);
+  const Prefix& x = a.prefix;
+  const int seqs = a.tab.seqs, lane = threadIdx.x & 31, groups = groups_of(x, seqs);
+  int32_t* const count[2] = {groups <= kNear ? near_count[0] : x.steps, groups <= kNear ? near_count[1] : x.chunks};
+  if (threadIdx.x == 0) line.alone[0] = line.alone[1] = 0;
+  for (int g = threadIdx.x; g < groups; g += kPlanThreads) count[0][g] = count[1][g] = 0;
+  for (int i = threadIdx.x; i < seqs; i += kPlanThreads) {
+    const int g = shared_tokens(a, groups, i) > 0 ? x.group[i] : -1;
+    x.member[i] = g;
+    if (i < kNear) {
+      near_member[i] = g;
+      near_rows[i] = a.batch.cu[i + 1] - a.batch.cu[i];
     }
-    const bool split = static_cast<int64_t>(chunks) * a.shape.group > kPrefixFew;
-    const int steps = s.list - chunks;
-    if (threadIdx.x == 0) a.prefix.steps[g] = split ? steps : -1;
-    if (s.leader < 0) break;   // past the last group
-    if (!split) continue;
-    int before = 0;            // chunks' rows
-    for (int x0 = 0, turn = 0, n = 0; x0 < s.list; x0 += kOrderThreads, turn ^= 1, ++n) {
-      const int x = x0 + threadIdx.x;
-      const bool is = n < kKept ? (kept >> n) & 1u : x < s.list && chunk(x);
-      const uint32_t mates = __ballot_sync(0xffffffffu, is);
-      if (lane == 0) counts[turn][warp] = __popc(mates);
-      __syncthreads();         // (the other turn's counts have been read by all when they are written again)
-      int at = before + __popc(mates & ((1u << lane) - 1));
+  }
+  __syncthreads();
+  if (threadIdx.x < 32)
+    for (int i0 = 0; i0 < seqs; i0 += 32) {
+      const int i = i0 + lane;
+      const int g = i >= seqs ? -1 : i < kNear ? near_member[i] : x.member[i];
+      if (!__any_sync(0xffffffffu, g >= 0)) continue;
+      const int n = g < 0 ? 0 : i < kNear ? near_rows[i] : a.batch.cu[i + 1] - a.batch.cu[i];
+      const bool chunk = static_cast<int64_t>(n) * a.shape.group > kStepRows;
+      const uint32_t mates = __match_any_sync(0xffffffffu, g < 0 ? -1 : 2 * g + (chunk ? 1 : 0));   // the same kind of one group
+      int mine = 0, all = 0;
 #pragma unroll
-      for (int w = 0; w < kOrderThreads / 32; ++w) {
-        const int c = counts[turn][w];
-        if (w < warp) at += c;
-        before += c;
+      for (int l = 0; l < 32; ++l) {
+        const int m = __shfl_sync(0xffffffffu, n, l);
+        if ((mates >> l) & 1u) {
+          all += m;
+          if (l < lane) mine += m;
+        }
       }
-      if (x < s.list) a.prefix.order[s.first + (is ? steps + at : x - at)] = s.first + x;
+      if (g >= 0) mine += count[chunk][g];
+      __syncwarp();
+      if (g >= 0) {
+        x.before[i] = mine;
+        if (lane == __ffs(mates) - 1) count[chunk][g] += all;
+      }
+      __syncwarp();
     }
-    __syncthreads();
+  __syncthreads();
+  for (int g = threadIdx.x; g < groups; g += kPlanThreads) {
+    const int list = shared_group(x, a.tab, a.batch, g).list, steps = min(count[0][g], list), chunks = min(count[1][g], list - steps);   // (lists that contradict themselves)
+    const bool split = static_cast<int64_t>(chunks) * a.shape.group > kPrefixFew;
+    x.chunks[g] = chunks;
+    x.steps[g] = split ? steps : -1;
+  }
+  __syncthreads();
+  prefix_line<true>(p, line);
+  if (!line.worth[0] && !line.worth[1]) return;
+  for (int i = threadIdx.x >> 5; i < seqs; i += kPlanThreads / 32) {   // a warp a sequence
+    const int g = x.member[i];
+    if (g < 0 || x.steps[g] < 0) continue;
+    const int n = a.batch.cu[i + 1] - a.batch.cu[i];
+    const SharedGroup s = shared_group(x, a.tab, a.batch, g);
+    const int to = (static_cast<int64_t>(n) * a.shape.group > kStepRows ? x.steps[g] : 0) + x.before[i], from = s.first + x.first[i];
+    for (int r = lane; r < n && to + r < s.list; r += 32) x.order[s.first + to + r] = from + r;
   }
 }
 
@@ -948,11 +961,9 @@ fg_status launch(const PrefixArgs& p, cudaStream_t st) {
 
 }  // namespace
 
-fg_status paged_prefix_order(const PrefixArgs& p, cudaStream_t st) {
+fg_status paged_prefix_plan(const PrefixArgs& p, cudaStream_t st) {
   Trace tr(KC_ATTN_PAGED_PLAN, st);
-  // (no fewer blocks than the groups that are looked at together, so that all of those before the first gap are counted)
-  const int grid = std::min(p.a.tab.seqs, std::max(32, 2 * p.workers));
-  return paged::launch("prefix_order_kernel", true, prefix_order_kernel, static_cast<unsigned>(grid), kOrderThreads, 0, st, p);
+  return paged::launch("prefix_plan_kernel", true, prefix_plan_kernel, 1, kPlanThreads, 0, st, p);
 }
 
 fg_status paged_prefix_join(const PrefixArgs& p, int head_dim, cudaStream_t st) {

@@ -52,10 +52,9 @@ __device__ __forceinline__ PrefixGroup prefix_group(const SharedGroup& s, int gr
   g.stride = most;
   return g;
 }
-// The tokens that sequence i leaves to its group: those of its group if all of its rows stand behind them and are the
-// group's, as the share lists them, and the group is one of the line's (the first `groups`).  tall: its rows' class.
-__device__ __forceinline__ int shared_tokens(const AttnArgs<__half>& a, int groups, int i, int& tall) {
-  tall = 0;
+// The tokens that sequence i leaves to its group g: those of its group if all of its rows stand behind them and are the
+// group's, as the share lists them, and the group is one of the line's (the first `groups`).
+__device__ __forceinline__ int shared_tokens(const AttnArgs<__half>& a, int groups, int i) {
   const Prefix& p = a.prefix;
   const int g = p.group[i];
   if (g < 0 || g >= groups) return 0;
@@ -63,21 +62,43 @@ __device__ __forceinline__ int shared_tokens(const AttnArgs<__half>& a, int grou
   const Seq q = seq_of(a.tab, a.batch, i);
   const int x = p.first[i];
   if (s.list == 0 || q.n == 0 || p.tokens[i] != s.tokens || q.len - q.n < s.tokens || x < 0 || x > s.list - q.n) return 0;
-  tall = p.steps != nullptr && p.steps[g] >= 0 && static_cast<int64_t>(q.n) * a.shape.group > kStepRows ? 1 : 0;
   const int32_t* rows = p.rows + s.first + x;
   return rows[0] == q.row0 && rows[q.n - 1] == q.row0 + q.n - 1 ? s.tokens : 0;
 }
+// Rows of a K/V head that sequence i has.
+__device__ __forceinline__ int64_t rows_of(const AttnArgs<__half>& a, int i) {
+  return (static_cast<int64_t>(a.batch.cu[i + 1]) - a.batch.cu[i]) * a.shape.group;
+}
+// The same and its rows' class.  PLANNED: of a sequence whose group is known (calls with chunks).
+template <bool PLANNED>
+__device__ __forceinline__ int shared_class(const AttnArgs<__half>& a, int groups, int i, int& tall) {
+  tall = 0;
+  if (!PLANNED) return shared_tokens(a, groups, i);
+  const int g = a.prefix.member[i];
+  if (g < 0) return 0;
+  tall = a.prefix.steps[g] >= 0 && rows_of(a, i) > kStepRows ? 1 : 0;
+  return a.prefix.tokens[i];
+}
 
 // What sequence i's reads of its group's tokens count when it goes by itself; nothing where it does so in any case.
+template <bool PLANNED>
 __device__ __forceinline__ int64_t read_alone(const PrefixArgs& p, int groups, int i, int& tall) {
   const AttnArgs<__half>& a = p.a;
-  const int64_t tokens = shared_tokens(a, groups, i, tall);
+  const int64_t tokens = shared_class<PLANNED>(a, groups, i, tall);
   if (tokens == 0) return 0;
-  const int64_t rows = (static_cast<int64_t>(a.batch.cu[i + 1]) - a.batch.cu[i]) * a.shape.group;
-  return tokens * (p.tile.workers == 0 || rows <= kStepRows ? kStepPrice : p.price.chunk[tall] * ((rows + kTileRows - 1) / kTileRows));
+  const int64_t rows = rows_of(a, i);
+  return tokens * (!PLANNED || rows <= kStepRows ? kStepPrice : p.price.chunk[tall] * ((rows + kTileRows - 1) / kTileRows));
 }
-// What every CTA works out first, by all its threads: the whole line's length and share, what the launches after it read
-// (written by the CTAs together), and where its own share begins.
+// Groups that are looked at: up to the first gap, 32 at a time (by a warp).
+__device__ __forceinline__ int groups_of(const Prefix& p, int seqs) {
+  const int lane = threadIdx.x & 31;
+  int groups = 0;
+  for (bool last = false; !last && groups < seqs; groups += 32) last = __any_sync(0xffffffffu, groups + lane < seqs && p.leader[groups + lane] < 0);
+  return min(groups, seqs);
+}
+// The whole line's length and share, what the launches after it read, and where the CTA's own share begins.  Worked out by all
+// threads of every CTA of paged_prefix.cu's kernel, which write what the others read together; in calls with chunks
+// (PLANNED) by one CTA before them.
 struct PrefixLine {
   int64_t total, per;
   unsigned long long alone[2];   // reads of the groups' sequences by themselves, by class; 0 before
@@ -86,6 +107,7 @@ struct PrefixLine {
   int g;                 // the group that the share begins in
   PrefixGroup at;
 };
+template <bool PLANNED>
 __device__ __forceinline__ void prefix_line(const PrefixArgs& p, PrefixLine& line) {   // line: in shared memory
   const AttnArgs<__half>& a = p.a;
   const Table& t = a.tab;
@@ -103,7 +125,7 @@ __device__ __forceinline__ void prefix_line(const PrefixArgs& p, PrefixLine& lin
       ClassRows s[2] = {{{-1, 0, 0, 0}, false}, {{-1, 0, 0, 0}, false}};
       if (g < t.seqs) {
         s[0] = class_rows(a.prefix, t, a.batch, g, false);
-        if (p.tile.workers > 0) s[1] = class_rows(a.prefix, t, a.batch, g, true);
+        if (PLANNED) s[1] = class_rows(a.prefix, t, a.batch, g, true);
       }
 #pragma unroll
       for (int c = 0; c < 2; ++c)
@@ -132,7 +154,7 @@ __device__ __forceinline__ void prefix_line(const PrefixArgs& p, PrefixLine& lin
         }
         if (blockIdx.x == 0 && g < t.seqs) {
           a.prefix.info[g] = x[0];
-          if (p.tile.workers > 0) {
+          if (PLANNED) {
             a.prefix.info[t.seqs + g] = x[1];
             p.tile.pre[g] = x[1].base;
           }
@@ -149,7 +171,7 @@ __device__ __forceinline__ void prefix_line(const PrefixArgs& p, PrefixLine& lin
     all[0] = at[0];
     all[1] = at[1];
     groups = min(groups, t.seqs);
-    if (write && blockIdx.x == 0 && p.tile.workers > 0)
+    if (PLANNED && write)
       for (int i = groups + lane; i <= t.seqs; i += 32) p.tile.pre[i] = at[1];
     return groups;
   };
@@ -157,13 +179,11 @@ __device__ __forceinline__ void prefix_line(const PrefixArgs& p, PrefixLine& lin
     const int groups = walk(false);
     if (lane == 0) line.groups = groups;
   } else if (p.price.least[0] > 0 || p.price.least[1] > 0) {   // meanwhile, by the other warps
-    int groups = 0;
-    for (bool last = false; !last && groups < t.seqs; groups += 32) last = __any_sync(0xffffffffu, groups + lane < t.seqs && a.prefix.leader[groups + lane] < 0);
-    groups = min(groups, t.seqs);
+    const int groups = PLANNED ? 0 : groups_of(a.prefix, t.seqs);
     int64_t sum[2] = {0, 0};
     for (int i = threadIdx.x - 32; i < t.seqs; i += blockDim.x - 32) {
       int tall;
-      const int64_t reads = read_alone(p, groups, i, tall);
+      const int64_t reads = read_alone<PLANNED>(p, groups, i, tall);
       sum[0] += tall ? 0 : reads;
       sum[1] += tall ? reads : 0;
     }
@@ -184,7 +204,7 @@ __device__ __forceinline__ void prefix_line(const PrefixArgs& p, PrefixLine& lin
       if (!worth[c]) all[c] = 0;
     }
     per[0] = all[0] > p.workers ? (all[0] + p.workers - 1) / p.workers : 1;
-    per[1] = p.tile.workers > 0 && all[1] > p.tile.workers ? (all[1] + p.tile.workers - 1) / p.tile.workers : 1;
+    if (PLANNED) per[1] = all[1] > p.tile.workers ? (all[1] + p.tile.workers - 1) / p.tile.workers : 1;
     if (lane == 0) {
       line.total = all[0];
       line.per = per[0];
@@ -192,7 +212,9 @@ __device__ __forceinline__ void prefix_line(const PrefixArgs& p, PrefixLine& lin
       line.worth[1] = worth[1];
       if (blockIdx.x == 0) {
         *a.prefix.planned = worth[0] || worth[1] ? line.groups : 0;
-        if (p.tile.workers > 0) {
+        if (PLANNED) {
+          a.prefix.head[0] = all[0];
+          a.prefix.head[1] = per[0];
           p.tile.head[0] = all[1];
           p.tile.head[1] = per[1];
         }
@@ -202,20 +224,42 @@ __device__ __forceinline__ void prefix_line(const PrefixArgs& p, PrefixLine& lin
   }
   __syncthreads();
   // the sequences one a CTA in turn, by warps that are not in a hurry
-  if (threadIdx.x >= 128 && threadIdx.x < 256)
-    for (int64_t i = blockIdx.x + static_cast<int64_t>(gridDim.x) * (threadIdx.x - 128); i < t.seqs; i += static_cast<int64_t>(gridDim.x) * 128) {
+  const int from = PLANNED ? 0 : 128, width = PLANNED ? static_cast<int>(blockDim.x) : 128;
+  if (threadIdx.x >= from && threadIdx.x < from + width)
+    for (int64_t i = blockIdx.x + static_cast<int64_t>(gridDim.x) * (threadIdx.x - from); i < t.seqs; i += static_cast<int64_t>(gridDim.x) * width) {
       int tall, skip = 0;
       if (line.worth[0] || line.worth[1]) {
-        skip = shared_tokens(a, line.groups, static_cast<int>(i), tall);
+        skip = shared_class<PLANNED>(a, line.groups, static_cast<int>(i), tall);
         if (!line.worth[tall]) skip = 0;
       }
       p.skip[i] = skip;
       if (skip > 0) a.prefix.home_row[i] = a.prefix.begin[a.prefix.group[i]] + a.prefix.first[i];
     }
 }
+// Where the CTA's share begins, by every warp, of a line that was worked out before.
+__device__ __forceinline__ void planned_line(const PrefixArgs& p, PrefixLine& line) {
+  const AttnArgs<__half>& a = p.a;
+  const int lane = threadIdx.x & 31, planned = *a.prefix.planned;
+  const int64_t total = a.prefix.head[0], per = a.prefix.head[1], o0 = blockIdx.x * per;
+  if (threadIdx.x == 0) {
+    line.total = total;
+    line.per = per;
+  }
+  if (o0 < total && threadIdx.x < 32)
+    for (int g0 = 0; g0 < planned; g0 += 32) {
+      if (g0 + lane >= planned) continue;
+      const PrefixGroup x = a.prefix.info[g0 + lane];
+      const int64_t n = static_cast<int64_t>(a.pool.heads) * x.units * x.tiles;
+      if (o0 >= x.base && o0 < x.base + n) {
+        line.g = g0 + lane;
+        line.at = x;
+      }
+    }
+  __syncthreads();
+}
 
-// In calls that allow chunks, first: Prefix::steps and order.
-fg_status paged_prefix_order(const PrefixArgs& p, cudaStream_t st);
+// In calls that allow chunks, first: the line, groups' steps and chunks apart.
+fg_status paged_prefix_plan(const PrefixArgs& p, cudaStream_t st);
 fg_status paged_prefix(const PrefixArgs& p, int head_dim, cudaStream_t st);
 // Behind it, and behind the chunks' kernel where that has groups: the parts of every row joined in its home.
 fg_status paged_prefix_join(const PrefixArgs& p, int head_dim, cudaStream_t st);

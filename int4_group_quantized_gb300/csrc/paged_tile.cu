@@ -593,7 +593,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const AttnArgs<__half
     float m = -INFINITY;
     float2 l2 = make_float2(0.0f, 0.0f);
     uint32_t nans = 0;
-    int64_t home = -1;     // kBehind: where the row's shared prefix left its sums
+    int home = -1;         // kBehind: where the row's shared prefix left its sums (rows times heads are below 2^31)
     while (true) {
       // A round ends one segment and works on the next.  S of the last tile is complete, so Q's place is free: the next Q is
       // on its way while the last P V runs, and its first S runs while O is written.
@@ -660,7 +660,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const AttnArgs<__half
           for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(u[(e & 24) + ((e & 7) < 4 ? 2 * (e & 7) : 2 * (e & 7) - 7)]) * (MODE == kBehind ? fc * own : fc);
           if (MODE == kBehind) {
             if (home >= 0) {
-              const float* x = a.prefix.home + home * D + 32 * c;
+              const float* x = a.prefix.home + static_cast<int64_t>(home) * D + 32 * c;
 #pragma unroll
               for (int e = 0; e < 32; e += 4) {
                 const float4 y = *reinterpret_cast<const float4*>(x + e);
@@ -840,7 +840,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const AttnArgs<__half
         home = -1;
         if (from_start && r < rows && a.tab.skip[k.i] > 0) {
           const int row = k.un.r0 + r, t = row / a.shape.group;
-          home = prefix_home(a.prefix, k.i, t, k.h * a.shape.group + row - t * a.shape.group, a.q_heads);
+          home = static_cast<int>(prefix_home(a.prefix, k.i, t, k.h * a.shape.group + row - t * a.shape.group, a.q_heads));
         }
         __syncwarp();
       }
