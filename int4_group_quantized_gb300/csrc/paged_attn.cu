@@ -295,20 +295,21 @@ fg_status join(const AttnArgs<T>& a, const ClassPlan& step, const ClassPlan& til
 
 // ---- when a call shares ------------------------------------------------------------------
 // By min_saved, the reads that the header counts: a chunk's four times a step's, a group's unit once or four times, 8 tokens for
-// a row's parts.  By the library's own rule, what the launches cost, from 880 calls of 2 to 256 sequences of 1 to 400 rows over
-// one prefix of 128 to 32,768 tokens, with 32 heads of 128, 32 on 8, 64 on 8, 16 and 12 of 64, each timed alone
-// (fg_paged_attention) and shared (inputs larger than L2, or L2 flushed: the same rule):
-//   class 0: a chunk's 256 rows read as two steps do, a group's unit as two and a 24th of one for each row, a row's parts as 32
-//     tokens, and the launches as 100 MB.  Of 290 calls of steps four are more than 5% slower than the faster way, in all 0.5%, and of
-//     102 of a few chunks two.  Alone and
-//     shared, us: 16 sequences, 32 heads, 1,024 tokens 33 and 38 (goes alone), 2,048 60 and 41; 64 sequences 512 tokens 66 and 65,
-//     1,024 94 and 66; 4 sequences 8,192 tokens 44 and 55 (alone), 32,768 160 and 133.
-//   class 1: a chunk's 256 rows as four, a group's as five, parts as 32 tokens, the launches as 150 MB.  Of 492 calls 16, in all
-//     0.3%.  16 sequences, 32 heads, 20 rows over 1,024 tokens 102 and 108 (alone), 1,536 126 and 112; 128 rows over 2,048 161 and
-//     203 (alone), 8,192 458 and 371; 48 of 32 rows over 512 186 and 221 (alone), 1,024 262 and 241.
+// a row's parts.  By the library's own rule, what the launches take, in reads of one token of one K/V head (64 dims take as long
+// as 128), from 880 calls of 2 to 256 sequences of 1 to 400 rows over one prefix of 128 to 32,768 tokens, with 32 heads of 128,
+// 32 on 8, 64 on 8, 16, and 12 of 64, over inputs larger than L2, each timed by fg_paged_attention and shared:
+//   class 0: 256 rows of a chunk as three steps, a group's unit as two and a 24th of one for each row, a row's parts as 32 tokens,
+//     the launches as 500 thousand reads.  Of 290 calls of steps 7 are more than 5% slower than the faster way, in all 0.5%, of 102
+//     with a few chunks none.  By fg_paged_attention and shared, us: 16 sequences, 32 heads, 1,024 tokens 33 and 38 (goes alone),
+//     2,048 60 and 41; 64 sequences 512 tokens 66 and 65, 1,024 94 and 66; 4 sequences 8,192 tokens 44 and 55 (alone), 32,768 160
+//     and 133.
+//   class 1: 256 rows of a chunk as four, of a group as five, parts as 32 tokens, the launches as 900 thousand.  Of 492 calls 13, in
+//     all 0.5%.  16 sequences, 32 heads, 20 rows over 1,024 tokens 102 and 108 (alone), 1,536 126 and 112; 128 rows over 2,048 161
+//     and 203 (alone), 8,192 458 and 371; 48 of 32 rows over 512 186 and 221 (alone), 1,024 262 and 241.
+// A call that goes alone by it takes 6 us (steps) or 7 to 19 (chunks) more than fg_paged_attention: the launches that find it out.
 // (One limit of 64 MB by the header's count for both took calls that are up to 1.7 times as slow.)
 constexpr SharePrices kCounted = {{4 * kStepPrice, 4 * kStepPrice}, {kStepPrice, 4 * kStepPrice}, 0, 8 * kStepPrice, {0, 0}};
-constexpr SharePrices kMeasured = {{2 * kStepPrice, 4 * kStepPrice}, {2 * kStepPrice, 5 * kStepPrice}, 1, 32 * kStepPrice, {100000000, 150000000}};
+constexpr SharePrices kMeasured = {{3 * kStepPrice, 4 * kStepPrice}, {2 * kStepPrice, 5 * kStepPrice}, 1, 32 * kStepPrice, {500000, 900000}};
 
 // ---- workspace ------------------------------------------------------------------------
 constexpr int kMaxSms = 160;   // a workspace fits this many SMs; launches use no more
@@ -528,7 +529,7 @@ fg_status fg_paged_attention_shared(const fg_page_pool* pool, const fg_page_tabl
   const int64_t token = static_cast<int64_t>(pool->heads) * pool->head_dim * 5 / 4;
   SharePrices price = min_saved < 0 ? kMeasured : kCounted;
   for (int64_t& least : price.least) {
-    const int64_t bytes = min_saved < 0 ? least : min_saved, tokens = bytes / token + (bytes % token != 0);
+    const int64_t of = min_saved < 0 ? least : min_saved, one = min_saved < 0 ? pool->heads : token, tokens = of / one + (of % one != 0);
     least = std::min(tokens, INT64_MAX / kStepPrice) * kStepPrice;
   }
   // all sequences' reads of all that a table row can name are no less than what groups can save
