@@ -295,7 +295,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const PrefixArgs p,
   griddep_wait();
   __syncthreads();
   if (p.tile.workers > 0) planned_line(p, line);
-  else prefix_line<false>(p, line);
+  else prefix_line<false>(p, line, [&](int groups, int i, int& n, int& tall) { return tall = 0, shared_tokens(a, groups, i, n); });
   if (line.total == 0) return;   // a call that does not share: no tensor memory is taken
   if (warp == kMmaWarp) tmem_alloc(tmem_slot, kTmemCols);
   tc_fence_before();
@@ -882,6 +882,7 @@ constexpr int kPlanThreads = 1024, kNear = 1024;
 __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixArgs p) {
   __shared__ PrefixLine line;
   __shared__ int32_t near_member[kNear], near_rows[kNear], near_count[2][kNear];
+  __shared__ bool near_split[kNear];
   griddep_launch();
   griddep_wait();
   const AttnArgs<__half>& a = p.a;
@@ -889,22 +890,26 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixA
   const int seqs = a.tab.seqs, lane = threadIdx.x & 31, groups = groups_of(x, seqs);
   int32_t* const count[2] = {groups <= kNear ? near_count[0] : x.steps, groups <= kNear ? near_count[1] : x.chunks};
   if (threadIdx.x == 0) line.alone[0] = line.alone[1] = 0;
-  for (int g = threadIdx.x; g < groups; g += kPlanThreads) count[0][g] = count[1][g] = 0;
-  for (int i = threadIdx.x; i < seqs; i += kPlanThreads) {
-    const int g = shared_tokens(a, groups, i) > 0 ? x.group[i] : -1;
-    x.member[i] = g;
+  for (int g = threadIdx.x; g < groups; g += blockDim.x) count[0][g] = count[1][g] = 0;
+  for (int i = threadIdx.x; i < seqs; i += blockDim.x) {
+    int n;
+    const int g = shared_tokens(a, groups, i, n) > 0 ? x.group[i] : -1;
     if (i < kNear) {
       near_member[i] = g;
-      near_rows[i] = a.batch.cu[i + 1] - a.batch.cu[i];
+      near_rows[i] = n;
+    } else {
+      x.member[i] = g;
     }
   }
+  auto member = [&](int i) { return i < kNear ? near_member[i] : x.member[i]; };
+  auto rows_of = [&](int i) { return i < kNear ? near_rows[i] : a.batch.cu[i + 1] - a.batch.cu[i]; };
   __syncthreads();
   if (threadIdx.x < 32)
     for (int i0 = 0; i0 < seqs; i0 += 32) {
       const int i = i0 + lane;
-      const int g = i >= seqs ? -1 : i < kNear ? near_member[i] : x.member[i];
+      const int g = i < seqs ? member(i) : -1;
       if (!__any_sync(0xffffffffu, g >= 0)) continue;
-      const int n = g < 0 ? 0 : i < kNear ? near_rows[i] : a.batch.cu[i + 1] - a.batch.cu[i];
+      const int n = g < 0 ? 0 : rows_of(i);
       const bool chunk = static_cast<int64_t>(n) * a.shape.group > kStepRows;
       const uint32_t mates = __match_any_sync(0xffffffffu, g < 0 ? -1 : 2 * g + (chunk ? 1 : 0));   // the same kind of one group
       int mine = 0, all = 0;
@@ -925,19 +930,26 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixA
       __syncwarp();
     }
   __syncthreads();
-  for (int g = threadIdx.x; g < groups; g += kPlanThreads) {
+  for (int g = threadIdx.x; g < groups; g += blockDim.x) {
     const int list = shared_group(x, a.tab, a.batch, g).list, steps = min(count[0][g], list), chunks = min(count[1][g], list - steps);   // (lists that contradict themselves)
     const bool split = static_cast<int64_t>(chunks) * a.shape.group > kPrefixFew;
     x.chunks[g] = chunks;
     x.steps[g] = split ? steps : -1;
+    if (g < kNear) near_split[g] = split;
   }
   __syncthreads();
-  prefix_line<true>(p, line);
+  auto split = [&](int g) { return g < kNear ? near_split[g] : x.steps[g] >= 0; };
+  prefix_line<true>(p, line, [&](int, int i, int& n, int& tall) {
+    const int g = member(i);
+    n = rows_of(i);
+    tall = g >= 0 && split(g) && static_cast<int64_t>(n) * a.shape.group > kStepRows ? 1 : 0;
+    return g < 0 ? 0 : x.tokens[i];
+  });
   if (!line.worth[0] && !line.worth[1]) return;
-  for (int i = threadIdx.x >> 5; i < seqs; i += kPlanThreads / 32) {   // a warp a sequence
-    const int g = x.member[i];
-    if (g < 0 || x.steps[g] < 0) continue;
-    const int n = a.batch.cu[i + 1] - a.batch.cu[i];
+  for (int i = threadIdx.x >> 5; i < seqs; i += blockDim.x / 32) {   // a warp a sequence
+    const int g = member(i);
+    if (g < 0 || !split(g)) continue;
+    const int n = rows_of(i);
     const SharedGroup s = shared_group(x, a.tab, a.batch, g);
     const int to = (static_cast<int64_t>(n) * a.shape.group > kStepRows ? x.steps[g] : 0) + x.before[i], from = s.first + x.first[i];
     for (int r = lane; r < n && to + r < s.list; r += 32) x.order[s.first + to + r] = from + r;
@@ -963,7 +975,8 @@ fg_status launch(const PrefixArgs& p, cudaStream_t st) {
 
 fg_status paged_prefix_plan(const PrefixArgs& p, cudaStream_t st) {
   Trace tr(KC_ATTN_PAGED_PLAN, st);
-  return paged::launch("prefix_plan_kernel", true, prefix_plan_kernel, 1, kPlanThreads, 0, st, p);
+  const unsigned threads = p.a.tab.seqs <= 224 ? 256 : kPlanThreads;   // a thread a sequence, and a warp
+  return paged::launch("prefix_plan_kernel", true, prefix_plan_kernel, 1, threads, 0, st, p);
 }
 
 fg_status paged_prefix_join(const PrefixArgs& p, int head_dim, cudaStream_t st) {

@@ -52,42 +52,20 @@ __device__ __forceinline__ PrefixGroup prefix_group(const SharedGroup& s, int gr
   g.stride = most;
   return g;
 }
-// The tokens that sequence i leaves to its group g: those of its group if all of its rows stand behind them and are the
-// group's, as the share lists them, and the group is one of the line's (the first `groups`).
-__device__ __forceinline__ int shared_tokens(const AttnArgs<__half>& a, int groups, int i) {
+// The tokens that sequence i leaves to its group: those of its group if all of its rows stand behind them and are the
+// group's, as the share lists them, and the group is one of the line's (the first `groups`).  n: its rows.  (Loads that do not
+// need one another come first.)
+__device__ __forceinline__ int shared_tokens(const AttnArgs<__half>& a, int groups, int i, int& n) {
   const Prefix& p = a.prefix;
-  const int g = p.group[i];
-  if (g < 0 || g >= groups) return 0;
-  const SharedGroup s = shared_group(p, a.tab, a.batch, g);
+  const int g = p.group[i], x = p.first[i], tokens = p.tokens[i];
   const Seq q = seq_of(a.tab, a.batch, i);
-  const int x = p.first[i];
-  if (s.list == 0 || q.n == 0 || p.tokens[i] != s.tokens || q.len - q.n < s.tokens || x < 0 || x > s.list - q.n) return 0;
-  const int32_t* rows = p.rows + s.first + x;
-  return rows[0] == q.row0 && rows[q.n - 1] == q.row0 + q.n - 1 ? s.tokens : 0;
-}
-// Rows of a K/V head that sequence i has.
-__device__ __forceinline__ int64_t rows_of(const AttnArgs<__half>& a, int i) {
-  return (static_cast<int64_t>(a.batch.cu[i + 1]) - a.batch.cu[i]) * a.shape.group;
-}
-// The same and its rows' class.  PLANNED: of a sequence whose group is known (calls with chunks).
-template <bool PLANNED>
-__device__ __forceinline__ int shared_class(const AttnArgs<__half>& a, int groups, int i, int& tall) {
-  tall = 0;
-  if (!PLANNED) return shared_tokens(a, groups, i);
-  const int g = a.prefix.member[i];
-  if (g < 0) return 0;
-  tall = a.prefix.steps[g] >= 0 && rows_of(a, i) > kStepRows ? 1 : 0;
-  return a.prefix.tokens[i];
-}
-
-// What sequence i's reads of its group's tokens count when it goes by itself; nothing where it does so in any case.
-template <bool PLANNED>
-__device__ __forceinline__ int64_t read_alone(const PrefixArgs& p, int groups, int i, int& tall) {
-  const AttnArgs<__half>& a = p.a;
-  const int64_t tokens = shared_class<PLANNED>(a, groups, i, tall);
-  if (tokens == 0) return 0;
-  const int64_t rows = rows_of(a, i);
-  return tokens * (!PLANNED || rows <= kStepRows ? kStepPrice : p.price.chunk[tall] * ((rows + kTileRows - 1) / kTileRows));
+  n = q.n;
+  if (g < 0 || g >= groups || q.n == 0 || x < 0 || x > a.batch.ntok) return 0;
+  const int64_t at = static_cast<int64_t>(p.begin[g]) + x;
+  const bool inside = at >= 0 && at + q.n <= a.batch.ntok;
+  const int row0 = inside ? p.rows[at] : -1, row1 = inside ? p.rows[at + q.n - 1] : -1;
+  const SharedGroup s = shared_group(p, a.tab, a.batch, g);
+  return s.list > 0 && tokens == s.tokens && q.len - q.n >= s.tokens && x <= s.list - q.n && row0 == q.row0 && row1 == q.row0 + q.n - 1 ? s.tokens : 0;
 }
 // Groups that are looked at: up to the first gap, 32 at a time (by a warp).
 __device__ __forceinline__ int groups_of(const Prefix& p, int seqs) {
@@ -107,8 +85,9 @@ struct PrefixLine {
   int g;                 // the group that the share begins in
   PrefixGroup at;
 };
-template <bool PLANNED>
-__device__ __forceinline__ void prefix_line(const PrefixArgs& p, PrefixLine& line) {   // line: in shared memory
+// shared(groups, i, n, tall): the tokens that sequence i leaves to its group, its rows and their class.
+template <bool PLANNED, class F>
+__device__ __forceinline__ void prefix_line(const PrefixArgs& p, PrefixLine& line, F shared) {   // line: in shared memory
   const AttnArgs<__half>& a = p.a;
   const Table& t = a.tab;
   const int group = a.shape.group, heads = a.pool.heads, lane = threadIdx.x & 31;
@@ -181,9 +160,10 @@ __device__ __forceinline__ void prefix_line(const PrefixArgs& p, PrefixLine& lin
   } else if (p.price.least[0] > 0 || p.price.least[1] > 0) {   // meanwhile, by the other warps
     const int groups = PLANNED ? 0 : groups_of(a.prefix, t.seqs);
     int64_t sum[2] = {0, 0};
-    for (int i = threadIdx.x - 32; i < t.seqs; i += blockDim.x - 32) {
-      int tall;
-      const int64_t reads = read_alone<PLANNED>(p, groups, i, tall);
+    for (int i = threadIdx.x - 32; i < t.seqs; i += blockDim.x - 32) {   // what a sequence's reads count when it goes by itself
+      int n, tall;
+      const int64_t tokens = shared(groups, i, n, tall), rows = static_cast<int64_t>(n) * group;
+      const int64_t reads = tokens * (!PLANNED || rows <= kStepRows ? kStepPrice : p.price.chunk[tall] * ((rows + kTileRows - 1) / kTileRows));
       sum[0] += tall ? 0 : reads;
       sum[1] += tall ? reads : 0;
     }
@@ -227,9 +207,9 @@ __device__ __forceinline__ void prefix_line(const PrefixArgs& p, PrefixLine& lin
   const int from = PLANNED ? 0 : 128, width = PLANNED ? static_cast<int>(blockDim.x) : 128;
   if (threadIdx.x >= from && threadIdx.x < from + width)
     for (int64_t i = blockIdx.x + static_cast<int64_t>(gridDim.x) * (threadIdx.x - from); i < t.seqs; i += static_cast<int64_t>(gridDim.x) * width) {
-      int tall, skip = 0;
+      int n, tall, skip = 0;
       if (line.worth[0] || line.worth[1]) {
-        skip = shared_class<PLANNED>(a, line.groups, static_cast<int>(i), tall);
+        skip = shared(line.groups, static_cast<int>(i), n, tall);
         if (!line.worth[tall]) skip = 0;
       }
       p.skip[i] = skip;
