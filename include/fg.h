@@ -535,7 +535,9 @@ fg_status fg_rotate(const fg_rotary* r, const void* x, fg_dtype dt, int64_t rows
 
 /* The append of a model with rotary positions, in one launch: q's rows (device
  * [ntok][ldq], q_heads heads) are rotated to their positions lens[i] - n + t into
- * q_out (device [ntok][ldqo]: q itself with ldqo = ldq, or memory apart from it), k's rows are rotated, rounded to the
+ * q_out (device [ntok][ldqo]: q itself with ldqo = ldq, or memory apart from it; apart
+ * from k, v and the restored rows, which stay apart from q too: columns of one
+ * buffer's rows may lie side by side), k's rows are rotated, rounded to the
  * activations' type and stored as fg_paged_append stores them, v's as they are:
  * the same bits as fg_rotate of q and k and fg_paged_append of the result.
  * rot a multiple of 16, at most head_dim.  q may be NULL (then q_out is not

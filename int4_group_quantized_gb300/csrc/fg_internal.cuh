@@ -196,6 +196,8 @@ fg_status prefill_attention_simt(const fg_kv& kv, const void* q, int64_t ldq, in
 
 // ---- rotary positions ------------------------------------------------------
 fg_status check_rotary(const fg_rotary* r, int32_t head_dim);
+// Whether two sets of rows have memory in common.
+bool rows_meet(const void* x, int64_t ldx, int64_t xcols, const void* y, int64_t ldy, int64_t ycols, int64_t rows, fg_dtype dt);
 // Rotated rows (cols columns) go to the rows themselves or to memory apart from them.
 fg_status check_apart(const void* x, int64_t ldx, const void* out, int64_t ldo, int64_t rows, int64_t cols, fg_dtype dt);
 

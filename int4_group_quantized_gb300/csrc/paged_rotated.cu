@@ -19,6 +19,8 @@
 // run's angles are worked out again for each); blocks that stay, two an SM, 149;
 // three blocks an SM 190; four of four warps 155; half the queries' loads at once 149;
 // the next head's loads under the one before 169 (spills), pieces found without divisions 140.
+#include <initializer_list>
+
 #include "paged_codec.cuh"
 #include "rotary.cuh"
 
@@ -386,7 +388,16 @@ extern "C" fg_status fg_paged_append_rotated(const fg_page_pool* pool, const fg_
   if (!aligned(cu, 4) || !aligned(k, 16) || !aligned(v, 16) || ld % 8 || !aligned(k_restored, 16) || !aligned(v_restored, 16) ||
       (k_restored && ldr % 8) || (hq > 0 && (!aligned(q, 16) || !aligned(q_out, 16) || ldq % 8 || ldqo % 8)))
     return fail(FG_ERR_ALIGN, "rows need 16-byte alignment and strides that are multiples of 8");
-  if (hq > 0) FG_TRY(check_apart(q, ldq, q_out, ldqo, ntok, hq, static_cast<fg_dtype>(pool->dtype)));
+  if (hq > 0) {
+    const fg_dtype dt = static_cast<fg_dtype>(pool->dtype);
+    FG_TRY(check_apart(q, ldq, q_out, ldqo, ntok, hq, dt));
+    // blocks read k and v, and write restored rows, while others move queries
+    for (const void* x : {k, v})
+      if (rows_meet(x, ld, h1, q_out, ldqo, hq, ntok, dt)) return fail(FG_ERR_ARG, "rotated queries over keys or values");
+    for (const void* x : {k_restored, v_restored})
+      if (x && (rows_meet(x, ldr, h1, q_out, ldqo, hq, ntok, dt) || rows_meet(x, ldr, h1, q, ldq, hq, ntok, dt)))
+        return fail(FG_ERR_ARG, "restored rows over queries");
+  }
   unsigned int* err = device_error_word();
   if (!err) return fail(FG_ERR_CUDA, "device error word");
   if (pool->dtype == FG_F16)

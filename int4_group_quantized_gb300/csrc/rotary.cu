@@ -209,13 +209,17 @@ fg_status check_rotary(const fg_rotary* r, int32_t head_dim) {
   return FG_OK;
 }
 
-fg_status check_apart(const void* x, int64_t ldx, const void* out, int64_t ldo, int64_t rows, int64_t cols, fg_dtype dt) {
-  const char *xb = static_cast<const char*>(x), *ob = static_cast<const char*>(out);
-  const int64_t e = static_cast<int64_t>(dtype_bytes(dt)), xn = ((rows - 1) * ldx + cols) * e, on = ((rows - 1) * ldo + cols) * e;
+bool rows_meet(const void* x, int64_t ldx, int64_t xcols, const void* y, int64_t ldy, int64_t ycols, int64_t rows, fg_dtype dt) {
+  const char *xb = static_cast<const char*>(x), *yb = static_cast<const char*>(y);
+  const int64_t e = static_cast<int64_t>(dtype_bytes(dt)), xn = ((rows - 1) * ldx + xcols) * e, yn = ((rows - 1) * ldy + ycols) * e;
+  if (xb >= yb + yn || yb >= xb + xn) return false;
   // columns of one buffer's rows may lie side by side
-  const int64_t row = ldx * e, off = rows > 1 && ldx == ldo ? ((ob - xb) % row + row) % row : 0;
-  const bool beside = off >= cols * e && row - off >= cols * e;
-  if (x == out ? (rows > 1 && ldx != ldo) : (xb < ob + on && ob < xb + xn && !beside))
+  const int64_t row = ldx * e, off = rows > 1 && ldx == ldy ? ((yb - xb) % row + row) % row : 0;
+  return off < xcols * e || off + ycols * e > row;
+}
+
+fg_status check_apart(const void* x, int64_t ldx, const void* out, int64_t ldo, int64_t rows, int64_t cols, fg_dtype dt) {
+  if (x == out ? (rows > 1 && ldx != ldo) : rows_meet(x, ldx, cols, out, ldo, cols, rows, dt))
     return fail(FG_ERR_ARG, "rotated rows go to the rows themselves, with their stride, or to memory apart from them");
   return FG_OK;
 }
