@@ -576,10 +576,15 @@ typedef struct {
  * leader and those that have at least P leading entries in common with it form a
  * group: P is the number that saves the most page reads, P times the followers
  * that have so many, among numbers of at least min_tokens (>= 1) tokens; the larger
- * of two that save the same.  Entries that name no page end a prefix.
+ * of two that save the same.  Entries that name no page end a prefix.  One first page
+ * makes one group at most: where all sequences begin with the same page and only some
+ * with the same document after it, those that share the leader's longer part form it
+ * and the others none (64 sequences over 4 documents of 8,000 tokens behind 64 common
+ * ones: 16 share; without the common page all 64, in 4 groups).
  * A share holds until the table's leading entries, the offsets cu or the set of
- * sequences change: lengths may grow and pages be compacted meanwhile, so steps of an unchanged batch and
- * all layers use one.  Up to 16384 sequences. */
+ * sequences change: lengths may grow and pages be compacted meanwhile, so steps of an
+ * unchanged batch and all layers use one.  Up to 16384 sequences (17 us for 256, 72
+ * for 1,024, 14 ms for 16,384: it grows with the square). */
 size_t fg_pages_share_workspace_bytes(const fg_page_table* t);
 fg_status fg_pages_share(const fg_page_table* t, const int32_t* cu, int64_t min_tokens, const fg_page_share* s, void* ws,
                          size_t ws_bytes, cudaStream_t stream);
@@ -588,20 +593,23 @@ fg_status fg_pages_share(const fg_page_table* t, const int32_t* cu, int64_t min_
  * as s says: every group's shared tokens are read once for all its rows, each
  * sequence's others as before, and the two are joined in fp32.  Results differ from
  * fg_paged_attention's by roundings only and are the same bits every time for one
- * max_q class and share.  A sequence whose rows do not all stand behind its
+ * max_q class and share (the workspace holds ntok * q_heads * (head_dim + 2) floats
+ * for fp16 pools, whether rows share or not).  A sequence whose rows do not all stand behind its
  * group's tokens is computed by itself, and so is every sequence of an fp32 pool
- * (fp32 sums on the CUDA cores: the rows' arithmetic, not the cache's bytes, is
- * their cost).
+ * (the share is checked and not used).
  * Sharing has launches of its own: where the groups save less than min_saved bytes
  * of cache reads (0: share all the same; negative: the library's own rule, by what
- * either way takes) every sequence goes by itself; in calls of more than 16 rows of a K/V head that is decided for chunks (of
- * groups that have more than 128 rows of them) and for all others apart.  Counted
- * are the reads of its group's tokens of every sequence that would
- * leave them to the group (see above: none that goes by itself anyway), once for up to 16
- * rows of a K/V head, four times for each 256 of more (they take as long), less
- * the group's own, once for each 64 of its rows (four times for each 256 of such
- * chunks), and 8 tokens for the parts of each of its rows.  (A row here: a row of
- * the batch and a query head; a chunk: a sequence of more than 16 of a K/V head.)
+ * either way takes) every sequence goes by itself.  In calls of more than 16 rows of
+ * a K/V head that is decided for chunks (of groups that have more than 128 rows of
+ * them) and for all others apart.  A min_saved of bytes counts the reads of its
+ * group's tokens of every sequence that would leave them to the group, once for up to
+ * 16 rows of a K/V head and four times for each 256 of more, less the group's own,
+ * once for each 64 of its rows (four times for each 256 of such chunks), and 8 tokens
+ * for the parts of each of its rows.  (A row here: a row of the batch and a query
+ * head; a chunk: a sequence of more than 16 of a K/V head.)
+ * A call that asks and goes by itself takes 6 us longer than fg_paged_attention, with
+ * chunks 7 to 19: where groups are known to be few or short, call that, or give a
+ * min_saved that the table's rows cannot reach, for which nothing is asked.
  * Nothing is rounded to fewer bits than fg_paged_attention rounds the same row to:
  * steps are not rounded to fp16 before the result is, chunks as they are there.
  * ws: 256-byte aligned, >= fg_paged_attention_shared_workspace_bytes. */

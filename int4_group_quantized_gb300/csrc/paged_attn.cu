@@ -517,7 +517,7 @@ fg_status fg_paged_attention_shared(const fg_page_pool* pool, const fg_page_tabl
   if (!s) return fail(FG_ERR_ARG, "null share");
   if (ntok == 0 || max_q == 0 || t->seqs == 0) return FG_OK;
   FG_TRY(check_share(s, t, ntok));
-  if (pool->dtype == FG_F32)   // the rows' arithmetic is the cost: every sequence by itself
+  if (pool->dtype == FG_F32)   // every sequence by itself: no kernel here takes a group's fp32 rows together
     return fg_paged_attention(pool, t, cu, q, ldq, q_heads, ntok, max_q, 0, 0, out, ldo, ws, ws_bytes, stream);
   FG_TRY(check_rows(pool, cu, q, ldq, q_heads, out, ldo));
   const size_t need = fg_paged_attention_shared_workspace_bytes(pool, t, q_heads, ntok, max_q);

@@ -28,12 +28,13 @@
 // key's share of every row's) until the segment ends.
 //
 // Not bound by the bytes (5 to 10% of the memory's rate) nor by the MMAs but by a
-// tile's latencies: some 4,000 cycles, of which the 24 MMAs of d 128 take the issuing
+// tile's latencies: some 3,700 cycles, of which the 24 MMAs of d 128 take the issuing
 // thread most (some 110 each), its waits the rest; the weights of 64 rows take 1,700,
-// the vote 300, restoring V about as long as the products.  64 rows over 4,096 tokens,
-// 32 heads of 128: 40 us; ten sequences' 80 rows a head each over 12,928 to 31,104, 8
-// heads of 128: 133 (38 and 114 without V's remainders).  Measured and not kept without
-// these, for the latter's call, 161 us then: 17 warps at 96 registers 170, 16 softmax warps at 72 193, S two
+// the vote 300, restoring V longer than that.  A launch has some 15 to 20 us besides
+// that no tile accounts for (first fetches and loads, a segment's beginning and end).
+// 64 rows over 4,096 tokens, 32 heads of 128: 39 us; ten sequences' 80 rows a head each
+// over 12,928 to 31,104, 8 heads of 128: 131 (38 and 114 without V's remainders).
+// Measured and not kept without these, for the latter's call, 161 us then: 17 warps at 96 registers 170, 16 softmax warps at 72 193, S two
 // tiles ahead 180, three copies of the restoring code 241 (instruction fetches).
 //
 // Every wait is bounded.  A half of the softmax warps decides everything by a

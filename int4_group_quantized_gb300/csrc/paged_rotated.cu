@@ -19,6 +19,8 @@
 // run's angles are worked out again for each); blocks that stay, two an SM, 149;
 // three blocks an SM 190; four of four warps 155; half the queries' loads at once 149;
 // the next head's loads under the one before 169 (spills), pieces found without divisions 140.
+// The same as two calls, fg_rotate of the queries and this without them: 156 (69 and 85).
+// fp32: 225 us for 1,039 MB, 68% of a copy's rate.
 #include <initializer_list>
 
 #include "paged_codec.cuh"

@@ -8,8 +8,10 @@
 // leader's number of shared pages, numbers the groups and lists their rows.
 // Bound by launch latency and two chains of dependent reads; the rows' entries are
 // read once and compared with the leader's, which stay in L2.  256 sequences over
-// seven prefixes of 100 to 1,500 pages: 17 us, comparing 6, picking 8 (17 with its
-// numbers in global memory); 12 sequences 7.
+// seven prefixes of 100 to 1,500 pages: 17 us (each launch by itself, cold: comparing
+// 11, picking 13); 12 sequences 7.  Picking counts followers pair by pair in one CTA,
+// so it grows with the square: 1,024 sequences over one prefix 72 us, 4,096 0.96 ms,
+// 16,384 14 ms, made once when a batch changes.
 #include <algorithm>
 
 #include "paged.cuh"
@@ -122,7 +124,7 @@ __device__ __forceinline__ int cta_prefix(int v, int* slots, int& total) {
   return inc - v + (warp > 0 ? before : 0);
 }
 
-// SMALL: up to kSmall sequences, whose numbers then stay in shared memory (256 sequences: 9 us for 17).
+// SMALL: up to kSmall sequences, whose numbers then stay in shared memory (256 sequences: the call 17 us for 22).
 constexpr int kSmall = 1024;
 template <bool SMALL>
 __global__ void __launch_bounds__(kPickThreads) pick_kernel(const ShareArgs a) {
