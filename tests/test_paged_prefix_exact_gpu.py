@@ -136,3 +136,37 @@ def test_steps_beside_chunks_of_their_group(fg, name):
     assert (np.asarray(n) * r <= 16).sum() == (np.asarray(n) * r <= 4).sum() > 0
     share = op.not_nearest(got[steps], ref[steps])
     assert share <= MOST, share
+
+
+def test_more_sequences_and_groups_than_a_plan_keeps_near(fg):
+    """1,060 groups of two: two chunks, two steps, a chunk and a step in turn, past what the plan's shared memory holds."""
+    g = 1060
+    kind = np.arange(g) % 3
+    n = np.stack((np.where(kind == 0, 70, np.where(kind == 1, 1, 131)), np.where(kind == 0, 66, 1)), 1).reshape(-1)
+    F = Forked(fg, (np.repeat(np.arange(g), 2), np.ones(g, int)), n + np.arange(2 * g) % 5, n, 1, 1, 64, 16, 44)
+    share = F.find(fg)
+    assert int(share.group.max()) == g - 1
+    out = _run(fg, F, share)
+    assert torch.equal(out, _run(fg, F, share))
+    fg.fg_sync_status()
+    ref, tol = F.expect()
+    got = out.double().cpu().numpy()
+    why = op.off_by_too_much(got, ref, tol, 3 * op.HALF)
+    assert why is None, why
+    steps = np.repeat(n == 1, n)
+    assert op.not_nearest(got[steps], ref[steps]) <= MOST
+
+
+@pytest.mark.parametrize("seqs", [1023, 1024, 1025, 1100])
+def test_one_group_of_many_sequences(fg, seqs):
+    """Steps and chunks of one prefix in turn, around the number of sequences that the plan keeps near."""
+    n = np.where(np.arange(seqs) % 7 == 3, 18, 1)
+    F = Forked(fg, (np.where(np.arange(seqs) % 11 == 5, -1, 0), [9]), n + np.arange(seqs) % 3, n, 1, 1, 64, 16, 45)
+    out = _run(fg, F)
+    fg.fg_sync_status()
+    ref, tol = F.expect()
+    got = out.double().cpu().numpy()
+    why = op.off_by_too_much(got, ref, tol, 3 * op.HALF)
+    assert why is None, why
+    steps = np.repeat(n == 1, n)
+    assert op.not_nearest(got[steps], ref[steps]) <= MOST
